@@ -2,11 +2,12 @@
 
 The binding only marshals arguments: every step of the GEMM runs in the
 CUDA library ``libdense_gemm.so`` (built in-tree by ``_build.build()``),
-whose C ABI is declared in ``include/dense_gemm.h``.  The functions of the
-same names as the C entry points take integers (device addresses, sizes,
-a ``cudaStream_t`` value); ``matmul`` is a convenience wrapper for torch
-tensors on the current device and stream.  There is no fallback: if the
-library is missing the calls raise.
+whose C ABI is declared in ``include/dense_gemm.h`` and (microscaled
+operands) ``include/dense_gemm_mx.h``.  The functions of the same names as
+the C entry points take integers (device addresses, sizes, a
+``cudaStream_t`` value); ``matmul`` and the ``mx_*`` functions are
+convenience wrappers for torch tensors on the current device and stream.
+There is no fallback: if the library is missing the calls raise.
 """
 from __future__ import annotations
 
@@ -27,7 +28,7 @@ GEMM_ERR_SCRATCH_LIMIT = 6
 PATH_NOOP, PATH_ZERO_FILL, PATH_SIMT_TMA, PATH_SIMT_CPASYNC, PATH_TC_TMA, PATH_SIMT_MIXED = range(6)
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 
-# Every symbol include/dense_gemm.h declares.
+# Every symbol the headers under include/ declare.
 EXPORTED = ("gemm_f32", "gemm_f16", "gemm_bf16", "gemm_status_string", "gemm_device_check",
             "gemm_plan", "gemm_smem_layout_offset", "gemm_selftest_timeout", "gemm_f32_noalloc",
             "gemm_f32_ex", "gemm_f16_ex", "gemm_bf16_ex", "gemm_plan_ex",
@@ -35,7 +36,13 @@ EXPORTED = ("gemm_f32", "gemm_f16", "gemm_bf16", "gemm_status_string", "gemm_dev
             "gemm_host_blocks", "gemm_host_k_blocks", "gemm_selftest_flag_timeout",
             "gemm_plan_resident", "gemm_pair_clusters", "gemm_sgemm_clusters", "gemm_pair_units",
             "gemm_probe_ffma",
-            "gemm_probe_ffma_threads")
+            "gemm_probe_ffma_threads",
+            "gemm_mx_code_ld", "gemm_mx_scale_bytes", "gemm_mx_quantize", "gemm_mx_dequantize",
+            "gemm_mx4", "gemm_mx4_linear", "gemm_mx_grad")
+
+# Microscaled formats (gemm_mx_format_t).
+MXFP4, MXINT8 = 0, 1
+_MX_CODES = {"mxfp4": MXFP4, "mxint8": MXINT8, MXFP4: MXFP4, MXINT8: MXINT8}
 
 # Operand storage (gemm_op_t): N = as stored row-major, T = stored transposed
 # (A as K x M, B as N x K).
@@ -125,6 +132,20 @@ def load() -> ctypes.CDLL:
     lib.gemm_selftest_timeout.argtypes = [ctypes.c_uint, vp]
     lib.gemm_selftest_flag_timeout.restype = i
     lib.gemm_selftest_flag_timeout.argtypes = [ctypes.c_uint, vp]
+    lib.gemm_mx_code_ld.restype = i
+    lib.gemm_mx_code_ld.argtypes = [i, i]
+    lib.gemm_mx_scale_bytes.restype = ctypes.c_longlong
+    lib.gemm_mx_scale_bytes.argtypes = [i, i]
+    lib.gemm_mx_quantize.restype = i
+    lib.gemm_mx_quantize.argtypes = [i, i, i, i, i, vp, i, vp, i, vp, vp]
+    lib.gemm_mx_dequantize.restype = i
+    lib.gemm_mx_dequantize.argtypes = [i, i, i, i, vp, i, vp, vp, i, vp]
+    lib.gemm_mx4.restype = i
+    lib.gemm_mx4.argtypes = [i, i, i, i, f, vp, i, vp, vp, i, vp, f, vp, i, vp]
+    lib.gemm_mx4_linear.restype = i
+    lib.gemm_mx4_linear.argtypes = [i, i, i, i, vp, i, vp, i, vp, vp, i, vp]
+    lib.gemm_mx_grad.restype = i
+    lib.gemm_mx_grad.argtypes = [i, i, i, i, i, i, i, f, vp, i, vp, i, vp, f, vp, i, vp]
     _lib = lib
     return lib
 
@@ -307,6 +328,46 @@ def gemm_host_k_blocks(dtype, M, N, K) -> int:
     return load().gemm_host_k_blocks(code, M, N, K)
 
 
+def gemm_mx_code_ld(fmt, K) -> int:
+    return load().gemm_mx_code_ld(_MX_CODES.get(fmt, -1), K)
+
+
+def gemm_mx_scale_bytes(R, K) -> int:
+    return load().gemm_mx_scale_bytes(R, K)
+
+
+def gemm_mx_quantize(fmt, dtype, op, R, K, X, ldx, codes, ldq, scales, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    return load().gemm_mx_quantize(_MX_CODES.get(fmt, -1), code, _OP_CODES.get(op, -1), R, K, X,
+                                   ldx, codes, ldq, scales, stream)
+
+
+def gemm_mx_dequantize(fmt, dtype, R, K, codes, ldq, scales, Y, ldy, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    return load().gemm_mx_dequantize(_MX_CODES.get(fmt, -1), code, R, K, codes, ldq, scales, Y,
+                                     ldy, stream)
+
+
+def gemm_mx4(dtype, M, N, K, alpha, a_codes, lda, a_scales, b_codes, ldb, b_scales, beta, C, ldc,
+             stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    return load().gemm_mx4(code, M, N, K, alpha, a_codes, lda, a_scales, b_codes, ldb, b_scales,
+                           beta, C, ldc, stream)
+
+
+def gemm_mx4_linear(dtype, M, N, K, X, ldx, w_codes, ldw, w_scales, Y, ldy, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    return load().gemm_mx4_linear(code, M, N, K, X, ldx, w_codes, ldw, w_scales, Y, ldy, stream)
+
+
+def gemm_mx_grad(fmt, dtype, op_a, dtype_c, M, N, K, alpha, A, lda, b_codes, ldb, b_scales, beta,
+                 C, ldc, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    code_c = DTYPE_CODES[dtype_c] if isinstance(dtype_c, str) else int(dtype_c)
+    return load().gemm_mx_grad(_MX_CODES.get(fmt, -1), code, _OP_CODES.get(op_a, -1), code_c, M,
+                               N, K, alpha, A, lda, b_codes, ldb, b_scales, beta, C, ldc, stream)
+
+
 # ------------------------------------------------------------ torch wrapper
 
 def _torch_dtype_code(t):
@@ -385,3 +446,202 @@ def matmul(A, B, out=None, stream=None, alpha=1.0, beta=0.0):
     if st != GEMM_OK:
         raise GemmError(st, f"gemm_{code}")
     return out
+
+
+# ------------------------------------------------------------ microscaled operands
+
+class MXTensor:
+    """A quantised rows x cols array on the GPU: ``codes`` (uint8, rows x
+    pitch) and ``scales`` (uint8) in the layout that include/dense_gemm_mx.h
+    describes; ``fmt`` is "mxfp4" or "mxint8"."""
+    __slots__ = ("codes", "scales", "cols", "fmt")
+
+    def __init__(self, codes, scales, cols, fmt="mxfp4"):
+        if fmt not in ("mxfp4", "mxint8"):
+            raise ValueError("fmt must be 'mxfp4' or 'mxint8'")
+        rows, pitch = codes.shape
+        width = (cols + 1) // 2 if fmt == "mxfp4" else cols
+        if pitch < width or codes.stride(1) != 1 or codes.element_size() != 1:
+            raise ValueError("codes must be rows of at least the format's bytes for cols")
+        tiles = ((rows + 127) // 128) * ((cols + 127) // 128)
+        if scales.numel() < 512 * tiles or scales.element_size() != 1 \
+                or not scales.is_contiguous():
+            raise ValueError("scales must be contiguous, 512 bytes for each 128 x 128 tile")
+        self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, fmt
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _ld(self):
+        """Row pitch of the codes; a single row's may be its padded width."""
+        rows, pitch = self.codes.shape
+        return self.codes.stride(0) if rows > 1 else (pitch + 15) // 16 * 16
+
+
+_TORCH_CODES = {}
+
+
+def _dtype_code(dtype):
+    if not _TORCH_CODES:
+        import torch
+        _TORCH_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    try:
+        return _TORCH_CODES[dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {dtype}: float32, float16 or bfloat16") from None
+
+
+def _raw_stream(stream, device):
+    import torch
+    if stream is not None:
+        return stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t.device.type != "cuda":
+            raise ValueError("operands must be CUDA tensors")
+
+
+def _result(out, shape, dtype, device, beta):
+    import torch
+    if out is None:
+        if beta != 0:
+            raise ValueError("beta != 0 needs an existing out")
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        raise ValueError("out has the wrong shape, dtype or device")
+    return out
+
+
+def mx_quantize(X, fmt="mxfp4", stream=None):
+    """X (rows x cols; float32, float16 or bfloat16; row-major or a
+    transposed view, read in place) in format ``fmt``: blocks of 32 along
+    the columns.  Returns an MXTensor."""
+    import torch
+    _on_gpu(X)
+    code = _dtype_code(X.dtype)
+    if fmt not in ("mxfp4", "mxint8"):
+        raise ValueError("fmt must be 'mxfp4' or 'mxint8'")
+    R, K = X.shape
+    op, ldx = _operand(X, R, K)
+    lib = load()
+    f = _MX_CODES[fmt]
+    ldq = lib.gemm_mx_code_ld(f, K)
+    codes = torch.empty((R, ldq), dtype=torch.uint8, device=X.device)
+    scales = torch.empty(lib.gemm_mx_scale_bytes(R, K), dtype=torch.uint8, device=X.device)
+    st = lib.gemm_mx_quantize(f, code, op, R, K, X.data_ptr(), ldx, codes.data_ptr(), ldq,
+                              scales.data_ptr(), _raw_stream(stream, X.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_mx_quantize")
+    return MXTensor(codes, scales, K, fmt)
+
+
+def mx_dequantize(q, dtype=None, out=None, stream=None):
+    """The values of MXTensor ``q`` as a rows x cols tensor of ``dtype``
+    (default bfloat16, or that of ``out``)."""
+    import torch
+    _on_gpu(q)
+    R, K = q.shape
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    code = _dtype_code(dtype)
+    Y = _result(out, (R, K), dtype, q.device, 0)
+    st = load().gemm_mx_dequantize(_MX_CODES[q.fmt], code, R, K, q.codes.data_ptr(), q._ld(),
+                                   q.scales.data_ptr(), Y.data_ptr(), _ld(Y, R, K),
+                                   _raw_stream(stream, q.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_mx_dequantize")
+    return Y
+
+
+def mx_matmul(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
+    """alpha * (A @ B.T) + beta * out for MXFP4 operands A (M x K) and B
+    (N x K); the result is of ``dtype`` (default bfloat16, or that of
+    ``out``)."""
+    import torch
+    _on_gpu(A, B)
+    if A.fmt != "mxfp4" or B.fmt != "mxfp4":
+        raise ValueError("mx_matmul takes mxfp4 operands")
+    M, K = A.shape
+    N, K2 = B.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    code = _dtype_code(dtype)
+    C = _result(out, (M, N), dtype, A.device, beta)
+    st = load().gemm_mx4(code, M, N, K, float(alpha), A.codes.data_ptr(), A._ld(),
+                         A.scales.data_ptr(), B.codes.data_ptr(), B._ld(), B.scales.data_ptr(),
+                         float(beta), C.data_ptr(), _ld(C, M, N), _raw_stream(stream, A.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_mx4")
+    return C
+
+
+def mx_linear(x, W, out=None, stream=None):
+    """x @ W.T with x (M x K) quantised to MXFP4 on the way and W (N x K) an
+    MXFP4 MXTensor; the result has x's dtype."""
+    _on_gpu(x, W)
+    code = _dtype_code(x.dtype)
+    if W.fmt != "mxfp4":
+        raise ValueError("mx_linear takes mxfp4 weights")
+    M, K = x.shape
+    N, K2 = W.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    Y = _result(out, (M, N), x.dtype, x.device, 0)
+    st = load().gemm_mx4_linear(code, M, N, K, x.data_ptr(), _ld(x, M, K), W.codes.data_ptr(),
+                                W._ld(), W.scales.data_ptr(), Y.data_ptr(), _ld(Y, M, N),
+                                _raw_stream(stream, x.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_mx4_linear")
+    return Y
+
+
+def _operand_rows16(A, M, K):
+    """_operand for a 16-bit operand whose leading dimension must be a
+    multiple of 8: that of a single stored row is free, so it is rounded up,
+    and a single column with unit stride is a single row stored transposed."""
+    if K == 1 and M > 1 and A.stride(0) == 1:
+        return OP_T, (M + 7) // 8 * 8
+    op, ld = _operand(A, M, K)
+    if (M if op == OP_N else K) <= 1:
+        ld = ((K if op == OP_N else M) + 7) // 8 * 8
+    return op, ld
+
+
+def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
+    """alpha * (A @ B) + beta * out with A (M x K, float16 or bfloat16,
+    row-major or a transposed view) and B a K x N MXTensor: ``mx_grad(dY, W)``
+    is the gradient of a layer's input, ``mx_grad(dY.t(), kept_x)`` that of
+    its weights.  The result is of A's dtype or float32 (``dtype``, or that
+    of ``out``)."""
+    import torch
+    _on_gpu(A, B)
+    code = _dtype_code(A.dtype)
+    if code == 0:
+        raise ValueError("mx_grad takes a float16 or bfloat16 A")
+    M, K = A.shape
+    K2, N = B.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if dtype is None:
+        dtype = A.dtype if out is None else out.dtype
+    if dtype != A.dtype and dtype != torch.float32:
+        raise ValueError("the result is of A's dtype or float32")
+    op, lda = _operand_rows16(A, M, K)
+    C = _result(out, (M, N), dtype, A.device, beta)
+    st = load().gemm_mx_grad(_MX_CODES[B.fmt], code, op, _dtype_code(dtype), M, N, K,
+                             float(alpha), A.data_ptr(), lda, B.codes.data_ptr(), B._ld(),
+                             B.scales.data_ptr(), float(beta), C.data_ptr(), _ld(C, M, N),
+                             _raw_stream(stream, A.device))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_mx_grad")
+    return C

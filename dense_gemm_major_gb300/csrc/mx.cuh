@@ -1,0 +1,215 @@
+// Device helpers of the microscaled (MX) kernels: element conversions, block
+// scales, tcgen05 block-scaled MMA and scale copies, bounded role waits.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mx.h"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace dgemm {
+
+// Byte offset of the scale of (row, block) in an array whose rows have
+// `tiles` tiles of scales.
+__host__ __device__ __forceinline__ long long mx_scale_offset(int row, int block, int tiles) {
+  return ((long long)(row >> 7) * tiles + (block >> 2)) * kMxTileBytes + (row & 31) * 16 +
+         ((row >> 5) & 3) * 4 + (block & 3);
+}
+
+// Scale byte of a block whose largest |x| has the FP32 bits `amax`:
+// floor(log2) - emax + 127, clamped to [0, 254]; 255 for an infinity or NaN.
+// (The exponent field of a subnormal is 0, which clamps to 0 as well.)
+template <int kFmt>
+__device__ __forceinline__ unsigned mx_scale_byte(unsigned amax) {
+  const int e = (int)(amax >> 23);
+  if (e == 255) return 255u;
+  constexpr int emax = kFmt == GEMM_MXFP4 ? 2 : 0;
+  return (unsigned)(e > emax ? e - emax : 0);
+}
+
+// 2^(127 - s), the exact reciprocal of the scale s (0 .. 254; for 255, whose
+// codes are zeros, 0).
+__device__ __forceinline__ float mx_inverse_scale(unsigned s) {
+  const unsigned bits = s < 254u ? (254u - s) << 23 : (s == 254u ? 0x00400000u : 0u);
+  return __uint_as_float(bits);
+}
+
+// 2^(s - 127); NaN for 255.
+__device__ __forceinline__ float mx_scale_value(unsigned s) {
+  const unsigned bits = s == 0u ? 0x00400000u : (s == 255u ? 0x7FC00000u : s << 23);
+  return __uint_as_float(bits);
+}
+
+// Eight values, already divided by their scale, as E2M1 codes (value j in
+// bits 4j .. 4j + 3), rounded to nearest even and saturated to +-6.
+__device__ __forceinline__ unsigned e2m1x8(const float (&v)[8]) {
+  unsigned r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// v * 64 rounded to nearest even, clamped to +-127, in the low byte.  Adding
+// 1.5 * 2^23 leaves the integer in the low mantissa bits.
+__device__ __forceinline__ unsigned int8_bits(float v) {
+  const float y = fminf(fmaxf(v * 64.f, -127.f), 127.f);
+  return __float_as_uint(y + 12582912.f);
+}
+__device__ __forceinline__ uint2 int8x8(const float (&v)[8]) {
+  unsigned b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = int8_bits(v[i]);
+  uint2 r;
+  r.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  r.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return r;
+}
+
+// Eight E2M1 codes as FP32 values (without their scale).
+__device__ __forceinline__ void e2m1x8_to_f32(unsigned codes, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    unsigned h;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+        : "=r"(h)
+        : "r"(codes >> (8 * j)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
+}
+// Four MXINT8 codes (one word) as FP32 values (without their scale).
+__device__ __forceinline__ void int8x4_to_f32(unsigned w, float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = (float)(int)(signed char)(w >> (8 * j)) * 0.015625f;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32_any(T v) {
+  if constexpr (sizeof(T) == 4)
+    return v;
+  else
+    return elem_to_f32<T>(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32_any(float v) {
+  if constexpr (sizeof(T) == 4)
+    return v;
+  else if constexpr (__is_same(T, __half))
+    return __float2half_rn(v);
+  else
+    return __float2bfloat16_rn(v);
+}
+
+// ------------------------------------------------------------ tcgen05, block scaled
+
+// Shared-memory matrix descriptor without swizzle (8-row groups of 16-byte
+// rows, sbo bytes apart), as the copy of scales to tensor memory reads it.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 operands (K-major), E8M0
+// scales; M = m, N = n, and the byte (0 or 2) of the scale words at which
+// the step's two scales start.
+__host__ __device__ constexpr uint32_t instr_desc_mx4(uint32_t m, uint32_t n, uint32_t sf) {
+  return (sf << 4)                 // B scale byte
+         | (1u << 7)               // A format: E2M1
+         | (1u << 10)              // B format: E2M1
+         | ((n >> 3) << 17)
+         | (1u << 23)              // scale format: E8M0
+         | ((m >> 4) << 24)
+         | (sf << 29);             // A scale byte
+}
+
+// 64-deep block-scaled MMA step.
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// One 512-byte tile of scales (32 rows of 16 bytes) to 4 TMEM columns, in
+// all four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+// Untiled bulk copy global -> shared; addresses and size multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// ------------------------------------------------------------ role waits
+
+// A role's bounded wait by one thread; on giving up records the fault (once
+// per CTA) and raises the CTA's abort flag.  `spin`: no suspend hint.
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, unsigned* fault,
+                                          unsigned long long timeout_ns, int* abort,
+                                          unsigned code, bool spin) {
+  const bool ok = spin ? mbar_wait_spin_bounded(bar, parity, timeout_ns, abort)
+                       : mbar_wait_bounded(bar, parity, timeout_ns, abort);
+  if (ok) return true;
+  if (!*(volatile int*)abort) raise_fault(fault, code);
+  *(volatile int*)abort = 1;
+  return false;
+}
+// The same by a warp: lane 0 waits, the result is broadcast.
+__device__ __forceinline__ bool role_wait_warp(uint32_t bar, uint32_t parity, unsigned* fault,
+                                               unsigned long long timeout_ns, int* abort,
+                                               unsigned code, bool spin) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0)
+    ok = role_wait(bar, parity, fault, timeout_ns, abort, code, spin) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// ------------------------------------------------------------ epilogue
+
+// One thread's 32 accumulator values (FP32 bits) to C: value j belongs to
+// row row0 + j and column col of C, so that a warp writes 32 consecutive
+// columns of one row at a time, whatever C's alignment.
+template <typename T>
+__device__ __forceinline__ void store_column32(const uint32_t (&r)[32], T* C, long long ldc,
+                                               int M, int N, int row0, int col, float alpha,
+                                               float beta) {
+  if (col >= N) return;
+  T* c = C + (long long)row0 * ldc + col;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (row0 + j < M) {
+      float v = alpha * __uint_as_float(r[j]);
+      if (beta != 0.f) v = fmaf(beta, to_f32_any<T>(c[j * ldc]), v);
+      c[j * ldc] = from_f32_any<T>(v);
+    }
+  }
+}
+
+}  // namespace dgemm

@@ -1,0 +1,358 @@
+// C-ABI entry points of the microscaled (MX) operators: argument checks,
+// tensor maps, workspaces and launch.  See include/dense_gemm_mx.h.
+#include <cstdint>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "dense_gemm_mx.h"
+#include "launch.h"
+#include "mx.h"
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_sms[kMaxDevices];   // SM counts, 0 until asked for; guarded by g_mu
+
+// The quantised X of gemm_mx4_linear, one per (device, stream).
+struct Workspace {
+  unsigned char* ptr = nullptr;
+  size_t bytes = 0;
+};
+std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;   // guarded by g_mu
+
+gemm_status_t get_workspace(cudaStream_t stream, size_t bytes, unsigned char** out) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_UNSUPPORTED_DEVICE;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  Workspace& w = g_workspaces[std::make_pair(dev, stream)];
+  if (w.bytes < bytes) {
+    if (w.ptr != nullptr) {
+      // Earlier work queued on this stream may still use the old buffer.
+      if (cudaStreamSynchronize(stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+      }
+      cudaFree(w.ptr);
+      w.ptr = nullptr;
+      w.bytes = 0;
+    }
+    if (cudaMalloc(&w.ptr, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      w.ptr = nullptr;
+      return GEMM_ERR_LAUNCH;
+    }
+    w.bytes = bytes;
+  }
+  *out = w.ptr;
+  return GEMM_OK;
+}
+
+// The current device's fault word and SM count.
+gemm_status_t device(unsigned** fault, int* sms) {
+  unsigned* f = dgemm::current_fault_word();
+  int dev = -1;
+  if (f == nullptr || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return GEMM_ERR_UNSUPPORTED_DEVICE;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (g_sms[dev] == 0 &&
+      cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    g_sms[dev] = 0;
+    return GEMM_ERR_UNSUPPORTED_DEVICE;
+  }
+  *fault = f;
+  *sms = g_sms[dev];
+  return GEMM_OK;
+}
+
+// cuTensorMapEncodeTiled, fetched from the driver once.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// 2-D row-major array {inner, outer}, 128-byte swizzled boxes.
+bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
+               uint64_t outer, uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {pitch_bytes};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline bool aligned(const void* p, int n) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0;
+}
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }
+inline bool good_format(int fmt) { return fmt == GEMM_MXFP4 || fmt == GEMM_MXINT8; }
+inline bool good_dtype(int d) { return d >= 0 && d <= 2; }
+inline bool good_op(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
+
+inline uint64_t span(long long rows, long long width, long long pitch) {
+  return rows > 0 && width > 0 ? (uint64_t)((rows - 1) * pitch + width) : 0;
+}
+inline bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
+  if (an == 0 || bn == 0 || a == nullptr || b == nullptr) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + bn && b0 < a0 + an;
+}
+
+inline int code_bytes(int fmt, int K) { return fmt == GEMM_MXFP4 ? K / 2 + (K & 1) : K; }
+inline int code_ld(int fmt, int K) {
+  return (int)(((long long)code_bytes(fmt, K) + 15) / 16 * 16);
+}
+inline long long scale_bytes(int R, int K) {
+  return (long long)((R + 127ll) / 128) * dgemm::mx_scale_tiles(K) * dgemm::kMxTileBytes;
+}
+
+// A quantised R x K operand (R, K > 0) that a kernel reads or writes.
+gemm_status_t check_quantized(int fmt, int K, const void* codes, int ldq, const void* scales) {
+  if (codes == nullptr || scales == nullptr || ldq < code_ld(fmt, K)) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || ldq % 16 != 0) return GEMM_ERR_MISALIGNED;
+  return GEMM_OK;
+}
+inline bool overlaps_quantized(const void* p, uint64_t n, int fmt, int R, int K,
+                               const void* codes, int ldq, const void* scales) {
+  return overlap(p, n, codes, span(R, code_bytes(fmt, K), ldq)) ||
+         overlap(p, n, scales, (uint64_t)scale_bytes(R, K));
+}
+
+gemm_status_t status_of(cudaError_t e) {
+  if (e == cudaSuccess) return GEMM_OK;
+  cudaGetLastError();
+  return GEMM_ERR_LAUNCH;
+}
+
+// C := beta * C, the product with no terms.
+gemm_status_t scale_only(int dtype, int M, int N, float beta, void* C, int ldc,
+                         cudaStream_t stream) {
+  if (beta == 1.f) return GEMM_OK;
+  return status_of(dgemm::launch_scale_c(C, M, N, ldc, dtype, beta, stream));
+}
+
+// The product of checked operands, M, N, K > 0.
+gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a, long long lda,
+                      const void* sa, const void* b, long long ldb, const void* sb, float beta,
+                      void* C, int ldc, unsigned* fault, int sms, cudaStream_t stream) {
+  alignas(64) CUtensorMap tmA, tmB;
+  const uint64_t width = (uint64_t)code_bytes(GEMM_MXFP4, K);
+  if (!encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, width, (uint64_t)M, (uint64_t)lda, 128,
+                 dgemm::kMx4BM) ||
+      !encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, b, width, (uint64_t)N, (uint64_t)ldb, 128,
+                 dgemm::kMx4BN))
+    return GEMM_ERR_LAUNCH;
+  dgemm::Mx4Params p;
+  p.M = M, p.N = N, p.K = K;
+  p.sa = static_cast<const unsigned char*>(sa);
+  p.sb = static_cast<const unsigned char*>(sb);
+  p.tiles_m = ceil_div(M, dgemm::kMx4BM);
+  p.tiles_n = ceil_div(N, dgemm::kMx4BN);
+  p.group = 8;
+  p.alpha = alpha, p.beta = beta;
+  p.C = C, p.ldc = ldc, p.dtype = dtype;
+  p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
+  const long long tiles = (long long)p.tiles_m * p.tiles_n;
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  return status_of(dgemm::launch_mx4(p, &tmA, &tmB, grid, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_mx_code_ld(gemm_mx_format_t fmt, int K) {
+  if (!good_format(fmt) || K < 0) return -1;
+  return code_ld(fmt, K);
+}
+
+long long gemm_mx_scale_bytes(int R, int K) {
+  if (R < 0 || K < 0) return -1;
+  return scale_bytes(R, K);
+}
+
+gemm_status_t gemm_mx_quantize(gemm_mx_format_t fmt, int dtype, gemm_op_t op, int R, int K,
+                               const void* X, int ldx, void* codes, int ldq, void* scales,
+                               cudaStream_t stream) {
+  if (!good_format(fmt) || !good_dtype(dtype) || !good_op(op) || R < 0 || K < 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (R == 0 || K == 0) return GEMM_OK;
+  const int es = elem_size(dtype);
+  if (X == nullptr || ldx < (op == GEMM_OP_N ? K : R)) return GEMM_ERR_INVALID_ARG;
+  gemm_status_t st = check_quantized(fmt, K, codes, ldq, scales);
+  if (st != GEMM_OK) return st;
+  if (!aligned(X, es)) return GEMM_ERR_MISALIGNED;
+  const uint64_t xs = op == GEMM_OP_N ? span(R, (long long)K * es, (long long)ldx * es)
+                                      : span(K, (long long)R * es, (long long)ldx * es);
+  if (overlaps_quantized(X, xs, fmt, R, K, codes, ldq, scales) ||
+      overlap(codes, span(R, code_bytes(fmt, K), ldq), scales, (uint64_t)scale_bytes(R, K)))
+    return GEMM_ERR_INVALID_ARG;
+  unsigned* fault;
+  int sms;
+  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  return status_of(
+      dgemm::launch_mx_quantize(fmt, dtype, op, R, K, X, ldx, codes, ldq, scales, stream));
+}
+
+gemm_status_t gemm_mx_dequantize(gemm_mx_format_t fmt, int dtype, int R, int K,
+                                 const void* codes, int ldq, const void* scales, void* Y, int ldy,
+                                 cudaStream_t stream) {
+  if (!good_format(fmt) || !good_dtype(dtype) || R < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (R == 0 || K == 0) return GEMM_OK;
+  const int es = elem_size(dtype);
+  if (Y == nullptr || ldy < K) return GEMM_ERR_INVALID_ARG;
+  gemm_status_t st = check_quantized(fmt, K, codes, ldq, scales);
+  if (st != GEMM_OK) return st;
+  if (!aligned(Y, es)) return GEMM_ERR_MISALIGNED;
+  if (overlaps_quantized(Y, span(R, (long long)K * es, (long long)ldy * es), fmt, R, K, codes,
+                         ldq, scales))
+    return GEMM_ERR_INVALID_ARG;
+  unsigned* fault;
+  int sms;
+  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  return status_of(
+      dgemm::launch_mx_dequantize(fmt, dtype, R, K, codes, ldq, scales, Y, ldy, stream));
+}
+
+gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha, const void* a_codes, int lda,
+                       const void* a_scales, const void* b_codes, int ldb, const void* b_scales,
+                       float beta, void* C, int ldc, cudaStream_t stream) {
+  if (!good_dtype(dtype) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return GEMM_OK;
+  const int es = elem_size(dtype);
+  if (C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(C, es)) return GEMM_ERR_MISALIGNED;
+  const bool empty = K == 0 || alpha == 0.f;
+  gemm_status_t st;
+  if (!empty) {
+    const uint64_t cs = span(M, (long long)N * es, (long long)ldc * es);
+    if ((st = check_quantized(GEMM_MXFP4, K, a_codes, lda, a_scales)) != GEMM_OK ||
+        (st = check_quantized(GEMM_MXFP4, K, b_codes, ldb, b_scales)) != GEMM_OK)
+      return st;
+    if (overlaps_quantized(C, cs, GEMM_MXFP4, M, K, a_codes, lda, a_scales) ||
+        overlaps_quantized(C, cs, GEMM_MXFP4, N, K, b_codes, ldb, b_scales))
+      return GEMM_ERR_INVALID_ARG;
+  }
+  unsigned* fault;
+  int sms;
+  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  if (empty) return scale_only(dtype, M, N, beta, C, ldc, stream);
+  return run_mx4(dtype, M, N, K, alpha, a_codes, lda, a_scales, b_codes, ldb, b_scales, beta, C,
+                 ldc, fault, sms, stream);
+}
+
+gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int ldx,
+                              const void* w_codes, int ldw, const void* w_scales, void* Y,
+                              int ldy, cudaStream_t stream) {
+  if (!good_dtype(dtype) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return GEMM_OK;
+  const int es = elem_size(dtype);
+  if (Y == nullptr || ldy < N) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(Y, es)) return GEMM_ERR_MISALIGNED;
+  gemm_status_t st;
+  if (K > 0) {
+    if (X == nullptr || ldx < K) return GEMM_ERR_INVALID_ARG;
+    if ((st = check_quantized(GEMM_MXFP4, K, w_codes, ldw, w_scales)) != GEMM_OK) return st;
+    if (!aligned(X, es)) return GEMM_ERR_MISALIGNED;
+    const uint64_t ys = span(M, (long long)N * es, (long long)ldy * es);
+    if (overlap(Y, ys, X, span(M, (long long)K * es, (long long)ldx * es)) ||
+        overlaps_quantized(Y, ys, GEMM_MXFP4, N, K, w_codes, ldw, w_scales))
+      return GEMM_ERR_INVALID_ARG;
+  }
+  unsigned* fault;
+  int sms;
+  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  if (K == 0) return scale_only(dtype, M, N, 0.f, Y, ldy, stream);
+  const int ldq = code_ld(GEMM_MXFP4, K);
+  const size_t code_size = ((size_t)M * ldq + 255) / 256 * 256;
+  unsigned char* ws = nullptr;
+  st = get_workspace(stream, code_size + (size_t)scale_bytes(M, K), &ws);
+  if (st != GEMM_OK) return st;
+  st = status_of(dgemm::launch_mx_quantize(GEMM_MXFP4, dtype, GEMM_OP_N, M, K, X, ldx, ws, ldq,
+                                           ws + code_size, stream));
+  if (st != GEMM_OK) return st;
+  return run_mx4(dtype, M, N, K, 1.f, ws, ldq, ws + code_size, w_codes, ldw, w_scales, 0.f, Y,
+                 ldy, fault, sms, stream);
+}
+
+gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int dtype_c, int M,
+                           int N, int K, float alpha, const void* A, int lda,
+                           const void* b_codes, int ldb, const void* b_scales, float beta,
+                           void* C, int ldc, cudaStream_t stream) {
+  if (!good_format(fmt) || (dtype != 1 && dtype != 2) || !good_op(op_a) ||
+      (dtype_c != 0 && dtype_c != dtype) || M < 0 || N < 0 || K < 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return GEMM_OK;
+  const int es = elem_size(dtype_c);
+  if (C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(C, es)) return GEMM_ERR_MISALIGNED;
+  const bool empty = K == 0 || alpha == 0.f;
+  gemm_status_t st;
+  if (!empty) {
+    if (A == nullptr || lda < (op_a == GEMM_OP_N ? K : M)) return GEMM_ERR_INVALID_ARG;
+    if ((st = check_quantized(fmt, N, b_codes, ldb, b_scales)) != GEMM_OK) return st;
+    if (!aligned(A, 16) || lda % 8 != 0) return GEMM_ERR_MISALIGNED;
+    const uint64_t cs = span(M, (long long)N * es, (long long)ldc * es);
+    const uint64_t as = op_a == GEMM_OP_N ? span(M, (long long)K * 2, (long long)lda * 2)
+                                          : span(K, (long long)M * 2, (long long)lda * 2);
+    if (overlap(C, cs, A, as) || overlaps_quantized(C, cs, fmt, K, N, b_codes, ldb, b_scales))
+      return GEMM_ERR_INVALID_ARG;
+  }
+  unsigned* fault;
+  int sms;
+  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  if (empty) return scale_only(dtype_c, M, N, beta, C, ldc, stream);
+  alignas(64) CUtensorMap tmA;
+  const CUtensorMapDataType dt =
+      dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const bool enc = op_a == GEMM_OP_T
+                       ? encode_2d(&tmA, dt, A, (uint64_t)M, (uint64_t)K, (uint64_t)lda * 2, 64,
+                                   dgemm::kMxGradBK)
+                       : encode_2d(&tmA, dt, A, (uint64_t)K, (uint64_t)M, (uint64_t)lda * 2,
+                                   dgemm::kMxGradBK, dgemm::kMxGradBM);
+  if (!enc) return GEMM_ERR_LAUNCH;
+  dgemm::MxGradParams p;
+  p.M = M, p.N = N, p.K = K;
+  p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
+  p.codes = static_cast<const unsigned char*>(b_codes);
+  p.ldb = ldb;
+  p.sb = static_cast<const unsigned char*>(b_scales);
+  p.tiles_m = ceil_div(M, dgemm::kMxGradBM);
+  p.tiles_n = ceil_div(N, dgemm::kMxGradBN);
+  p.group = 16;
+  p.alpha = alpha, p.beta = beta;
+  p.C = C, p.ldc = ldc;
+  p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
+  const long long tiles = (long long)p.tiles_m * p.tiles_n;
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  return status_of(dgemm::launch_mx_grad(p, &tmA, grid, stream));
+}
+
+}  // extern "C"

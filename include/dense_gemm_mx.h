@@ -1,0 +1,117 @@
+/*
+ * dense_gemm_mx.h -- microscaled (MX) operands for the GB300 dense GEMM
+ * library: quantisation to 4 and 8 bits, the 4-bit product, and the products
+ * of a 16-bit array with a quantised one that a layer's backward pass needs.
+ *
+ * Formats (OCP Microscaling Formats v1.0).  A row is cut into blocks of 32
+ * consecutive values; the values of a block share one scale 2^(s - 127), s an
+ * E8M0 byte, and s = 255 makes the whole block NaN.
+ *   GEMM_MXFP4   elements are E2M1 codes: sign bit, then 0 .. 7 for
+ *                0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   GEMM_MXINT8  elements are two's complement integers -127 .. 127 that
+ *                stand for integer / 64.
+ *
+ * A quantised array of R rows and K columns is two device arrays:
+ *   codes   R rows with a pitch of ldq bytes (a multiple of 16, at least
+ *           gemm_mx_code_ld(fmt, K)).  MXFP4: columns 2j and 2j + 1 in the
+ *           low and high half of byte j (the high half of the last byte of
+ *           an odd row is 0).  MXINT8: column j in byte j.
+ *   scales  gemm_mx_scale_bytes(R, K) bytes: tiles of 128 rows x 4 blocks of
+ *           512 bytes each.  The scale of row r, block b is byte
+ *             (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4
+ *           of tile (r / 128) * T + b / 4, T = ceil(ceil(K / 32) / 4): the
+ *           order in which the tensor cores read the scales.  Within a row
+ *           that exists, the bytes of blocks past the last one must not be
+ *           255 (gemm_mx_quantize writes 0).
+ * Both bases are 16-byte aligned, else GEMM_ERR_MISALIGNED.
+ *
+ * dtype codes are those of gemm_plan: 0 = FP32, 1 = FP16, 2 = BF16.  Pointers,
+ * streams, errors and the device fault word follow dense_gemm.h: argument
+ * problems are reported synchronously before anything is queued, work is
+ * queued on `stream`, and every device-side wait is bounded.  Inputs must not
+ * overlap outputs.
+ */
+#ifndef DENSE_GEMM_MX_H_
+#define DENSE_GEMM_MX_H_
+
+#include "dense_gemm.h"
+
+#if defined(__cplusplus)
+extern "C" {
+#endif
+
+typedef enum gemm_mx_format_t { GEMM_MXFP4 = 0, GEMM_MXINT8 = 1 } gemm_mx_format_t;
+
+/* Smallest row pitch of the codes in bytes, a multiple of 16; -1 for a bad
+ * format or K < 0. */
+int gemm_mx_code_ld(gemm_mx_format_t fmt, int K);
+/* Bytes of the scales of an R x K array; -1 for a negative size. */
+long long gemm_mx_scale_bytes(int R, int K);
+
+/*
+ * Q := X in format fmt, X an R x K array of dtype (op == GEMM_OP_N: element
+ * (r,k) at X[r*ldx + k], ldx >= K; op == GEMM_OP_T: stored K x R, element
+ * (r,k) at X[k*ldx + r], ldx >= R; any alignment of dtype's size).
+ *  - Scale of a block: s = floor(log2(max |x|)) - emax + 127, clamped to
+ *    [0, 254], emax = 2 (MXFP4) or 0 (MXINT8); a block of zeros gets s = 0.
+ *    A block that holds an infinity or a NaN gets s = 255 and zero codes.
+ *  - Elements: x / 2^(s - 127) rounded to nearest even, saturated to +-6 or
+ *    +-127/64.
+ *  - The last block of a row is filled up with zeros.  Bytes of a code row
+ *    past the last 8-column group, and scales of rows past R, are not
+ *    written.
+ */
+gemm_status_t gemm_mx_quantize(gemm_mx_format_t fmt, int dtype, gemm_op_t op, int R, int K,
+                               const void *X, int ldx, void *codes, int ldq, void *scales,
+                               cudaStream_t stream);
+
+/* Y[r*ldy + k] := the value of element (r,k), rounded once to dtype (exact
+ * in FP32 and BF16; FP16 rounds to nearest even, past its range to
+ * infinity).  Any alignment of Y. */
+gemm_status_t gemm_mx_dequantize(gemm_mx_format_t fmt, int dtype, int R, int K,
+                                 const void *codes, int ldq, const void *scales, void *Y, int ldy,
+                                 cudaStream_t stream);
+
+/*
+ * C := alpha * A . B^T + beta * C, A (M x K) and B (N x K) in MXFP4, C of
+ * dtype row-major with any alignment.  FP32 accumulation; one rounding to
+ * dtype.  K == 0 or alpha == 0: C := beta * C; beta == 0: C is not read.
+ */
+gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha,
+                       const void *a_codes, int lda, const void *a_scales,
+                       const void *b_codes, int ldb, const void *b_scales, float beta,
+                       void *C, int ldc, cudaStream_t stream);
+
+/*
+ * A linear layer in 4 bits: Y := q(X) . W^T, X (M x K) and Y (M x N) of
+ * dtype, q(X) the MXFP4 quantisation of X, W (N x K) in MXFP4.  The same
+ * values as gemm_mx_quantize followed by gemm_mx4 up to the order of the
+ * sums.  q(X) lives in a workspace of the library (one per device and
+ * stream, grown on demand after synchronising that stream, kept until the
+ * process exits).
+ */
+gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void *X, int ldx,
+                              const void *w_codes, int ldw, const void *w_scales, void *Y,
+                              int ldy, cudaStream_t stream);
+
+/*
+ * C := alpha * op(A) . B + beta * C, the products of a backward pass: A of
+ * dtype (FP16 or BF16), B (K x N, blocks along N) in fmt, its values taken in
+ * A's type (exact in BF16; FP16 rounds them).  FP32 accumulation; C is
+ * row-major, of dtype_c (A's type or FP32), with any alignment.
+ *   gradient of a layer's input:    A = dY (op N), B = W
+ *   gradient of a layer's weights:  A = dY (op T, stored K x M), B = the
+ *                                   layer's kept input
+ * op_a as in gemm_*_op; A is 16-byte aligned and lda a multiple of 8, else
+ * GEMM_ERR_MISALIGNED.  K == 0 or alpha == 0: C := beta * C.
+ */
+gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int dtype_c, int M,
+                           int N, int K, float alpha, const void *A, int lda,
+                           const void *b_codes, int ldb, const void *b_scales, float beta,
+                           void *C, int ldc, cudaStream_t stream);
+
+#if defined(__cplusplus)
+}
+#endif
+
+#endif /* DENSE_GEMM_MX_H_ */

@@ -1,0 +1,506 @@
+"""GPU tests of the microscaled operators against the plain 64-bit
+implementation in mx_reference: quantisation and its inverse bit for bit,
+the 4-bit product, the linear layer and the products of the backward pass
+within a bound derived from FP32 accumulation and one rounding."""
+import numpy as np
+import pytest
+import torch
+
+import mx_reference as ref
+from parity import check_device, gpu_lib
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+FMTS = ["mxfp4", "mxint8"]
+
+
+@pytest.fixture(scope="module")
+def dg():
+    return gpu_lib()
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _rand(rng, rows, cols, dtype="f32", spread=3.0):
+    """Values over many binades, as a float32 array cast to dtype."""
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.uniform(-spread, spread, (rows, 1)))
+    return torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype])
+
+
+def _dev(t, op="N", pad=0, offset=0):
+    """t on the GPU, row-major or stored transposed, rows `pad` elements
+    wider than t's and the base `offset` elements into its buffer; the
+    padding holds NaN."""
+    s = t.t() if op == "T" else t
+    rows, cols = s.shape
+    buf = torch.full((rows * (cols + pad) + offset + 8,), float("nan"), dtype=t.dtype,
+                     device="cuda")
+    v = buf[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    v.copy_(s)
+    return v.t() if op == "T" else v
+
+
+def _operand(dg, x, fmt, pad=0):
+    """MXTensor of x by the plain implementation, the codes' rows `pad` bytes
+    wider, all padding bytes (codes 0xFF past a row's 8-column groups,
+    scales 0xFF of rows that do not exist) as a caller may leave them."""
+    codes, scales = ref.quantize(x, fmt)
+    cb, sb = ref.pack(codes, scales, fmt)
+    R, K = x.shape
+    wide = np.full((R, cb.shape[1] + pad), 0xFF, dtype=np.uint8)
+    width = (K + 1) // 2 if fmt == "mxfp4" else K
+    wide[:, :width] = cb[:, :width]
+    T = -(-K // 128)
+    rows = np.arange(-(-R // 128) * 128).reshape(-1, 4, 32).transpose(0, 2, 1)   # tile, r%32, quad
+    gone = np.broadcast_to((rows >= R)[:, None, :, :, None], (rows.shape[0], T, 32, 4, 4))
+    sb = np.where(gone.reshape(-1), 0xFF, sb).astype(np.uint8)
+    q = dg.MXTensor(torch.from_numpy(wide).cuda(), torch.from_numpy(sb).cuda(), K, fmt)
+    return q, ref.values(codes, scales, fmt)
+
+
+def _check(got, want, total, K, dtype):
+    """got within the bound of `want`; NaN exactly where want has it."""
+    assert got.dtype == TYPES[dtype] and tuple(got.shape) == want.shape
+    got = _np(got)
+    nan = np.isnan(want)
+    assert (np.isnan(got) == nan).all()
+    err = np.abs(np.where(nan, 0, got) - np.where(nan, 0, want))
+    lim = ref.bound(np.where(nan, 0, want), np.where(nan, 0, total), K, dtype)
+    worst = np.unravel_index(np.argmax(err - lim), err.shape)
+    assert (err <= lim).all(), (worst, got[worst], want[worst], lim[worst])
+
+
+# ------------------------------------------------------------ quantisation
+
+SHAPES = [(1, 1), (1, 32), (3, 33), (1, 4096), (130, 333), (33, 128), (257, 1000), (64, 2080)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_quantize_bytes(dg, fmt, dtype, op, shape):
+    rng = np.random.default_rng(sum(shape))
+    x = _rand(rng, *shape, dtype)
+    want_c, want_s = ref.quantize(_np(x), fmt)
+    for pad, offset in [(0, 0), (3, 0), (8, 1)]:
+        q = dg.mx_quantize(_dev(x, op, pad, offset), fmt)
+        check_device(dg)
+        c, s = ref.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(), shape[1], fmt)
+        assert (s == want_s).all()
+        same = (c == want_c) if fmt == "mxint8" else \
+            (c == want_c) | (((c & 7) == 0) & ((want_c & 7) == 0))   # -0 and 0 stand for 0
+        assert same.all()
+        if fmt == "mxfp4" and shape[1] % 2:
+            assert not (q.codes[:, shape[1] // 2] >> 4).any()
+        # The bytes of blocks past a row's last are finite scales.
+        full = ref.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(),
+                          min(-(-shape[1] // 128) * 128, q.codes.shape[1] * 2), "mxfp4")[1]
+        assert (full[:, want_s.shape[1]:] != 255).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("op", ["N", "T"])
+def test_quantize_special_values(dg, fmt, op):
+    x = np.zeros((40, 256), dtype=np.float32)
+    x[0, 5] = np.inf
+    x[1, 70] = -np.inf
+    x[2, 100] = np.nan
+    x[3, :] = np.float32(2.0 ** -149)                     # the smallest subnormal
+    x[4, :] = np.finfo(np.float32).max
+    x[5, :32] = -np.finfo(np.float32).max
+    x[6, :] = np.float32(2.0 ** -126)
+    x[7, ::2], x[7, 1::2] = 2.0 ** 100, 2.0 ** -100       # far apart in one block
+    x[8, :] = -0.0
+    grid = np.arange(256) / 32.0                           # every tie of both formats
+    x[9, :], x[10, :] = grid, -grid
+    x[11, :] = np.linspace(-127.75, 127.75, 256) / 64
+    x[12, :32] = np.float32(2.0 ** -127) * 1.5             # subnormal block
+    t = torch.from_numpy(x)
+    want_c, want_s = ref.quantize(x, fmt)
+    q = dg.mx_quantize(_dev(t, op), fmt)
+    c, s = ref.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(), 256, fmt)
+    assert (s == want_s).all()
+    want_v = ref.values(want_c, want_s, fmt)
+    got_v = ref.values(c, s, fmt)
+    np.testing.assert_array_equal(got_v, want_v)
+    back = dg.mx_dequantize(q, torch.float32)
+    np.testing.assert_array_equal(_np(back), want_v)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", SHAPES)
+def test_dequantize_values(dg, fmt, dtype, shape):
+    rng = np.random.default_rng(7 + sum(shape))
+    q, v = _operand(dg, _np(_rand(rng, *shape)), fmt, pad=16)
+    want = torch.from_numpy(v).to(TYPES[dtype])
+    buf = torch.full((shape[0], shape[1] + 5), -1.0, dtype=TYPES[dtype], device="cuda")
+    for out in [None, buf[:, :shape[1]]]:
+        y = dg.mx_dequantize(q, TYPES[dtype], out=out)
+        check_device(dg)
+        assert torch.equal(y.cpu(), want)
+    assert (buf[:, shape[1]:] == -1).all()
+
+
+def test_dequantize_every_scale(dg):
+    """All 256 scales, all codes of both formats; FP16 rounds and overflows."""
+    for fmt in FMTS:
+        codes = np.tile(np.arange(32) % 16 if fmt == "mxfp4" else np.arange(32) * 8 - 124, (256, 1))
+        scales = np.arange(256, dtype=np.uint8)[:, None]
+        cb, sb = ref.pack(codes, scales, fmt)
+        q = dg.MXTensor(torch.from_numpy(cb).cuda(), torch.from_numpy(sb).cuda(), 32, fmt)
+        v = ref.values(codes, scales, fmt)
+        for dtype in (torch.float32, torch.bfloat16, torch.float16):
+            got = dg.mx_dequantize(q, dtype).cpu()
+            want = torch.from_numpy(v).to(torch.float32).to(dtype)
+            assert torch.equal(torch.nan_to_num(got, 7.0), torch.nan_to_num(want, 7.0))
+            assert (got.isnan() == want.isnan()).all()
+
+
+# ------------------------------------------------------------ 4-bit product
+
+PRODUCTS = [(1, 1, 1), (1, 128, 32), (2, 3, 31), (128, 128, 256), (33, 77, 130), (129, 130, 333),
+            (300, 520, 1024), (1, 1000, 4096), (257, 64, 2000), (1000, 1030, 777),
+            (512, 256, 8192), (7, 4097, 160), (640, 2305, 385)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", PRODUCTS)
+def test_product(dg, dtype, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + 3 * N + 7 * K)
+    a, av = _operand(dg, _np(_rand(rng, M, K)), "mxfp4", pad=16)
+    b, bv = _operand(dg, _np(_rand(rng, N, K, spread=1.0)), "mxfp4")
+    got = dg.mx_matmul(a, b, dtype=TYPES[dtype])
+    check_device(dg)
+    _check(got, av @ bv.T, np.abs(av) @ np.abs(bv).T, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(5, 9, 70), (200, 300, 500), (700, 513, 256)])
+def test_product_scaled_into_a_padded_view(dg, dtype, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(5)
+    a, av = _operand(dg, _np(_rand(rng, M, K)), "mxfp4")
+    b, bv = _operand(dg, _np(_rand(rng, N, K, spread=1.0)), "mxfp4")
+    c0 = _rand(rng, M, N, dtype, spread=0.0)
+    out = _dev(c0, pad=3, offset=1)
+    dg.mx_matmul(a, b, out=out, alpha=0.5, beta=-2.0)
+    check_device(dg)
+    want = 0.5 * (av @ bv.T) - 2.0 * _np(c0)
+    total = 0.5 * (np.abs(av) @ np.abs(bv).T) + 2.0 * np.abs(_np(c0))
+    _check(out, want, total, K, dtype)
+    whole = out._base if out._base is not None else out
+    assert int(whole.isnan().sum()) == whole.numel() - M * N     # padding untouched
+    out.fill_(float("nan"))                                      # beta = 0: not read
+    dg.mx_matmul(a, b, out=out, alpha=0.5)
+    _check(out, 0.5 * (av @ bv.T), total, K, dtype)
+
+
+def test_products_without_terms(dg):
+    e = dg.MXTensor(torch.empty((3, 0), dtype=torch.uint8, device="cuda"),
+                    torch.empty(0, dtype=torch.uint8, device="cuda"), 0)
+    assert dg.gemm_mx4("f32", 3, 3, 0, 1.0, 0, 0, 0, 0, 0, 0, 0.0, 0, 3) == dg.GEMM_ERR_INVALID_ARG
+    out = torch.ones((3, 3), device="cuda")
+    dg.mx_matmul(e, e, out=out, beta=2.0)
+    assert (out == 2).all()
+    dg.mx_matmul(e, e, out=out)
+    assert (out == 0).all()
+    a, av = _operand(dg, np.ones((3, 40)), "mxfp4")
+    out = torch.ones((3, 3), device="cuda")
+    dg.mx_matmul(a, a, out=out, alpha=0.0, beta=3.0)
+    assert (out == 3).all()
+    assert dg.mx_linear(torch.empty((3, 0), dtype=torch.float16, device="cuda"), e).eq(0).all()
+    dy = torch.ones((2, 3), dtype=torch.bfloat16, device="cuda")
+    out = torch.ones((2, 40), device="cuda")
+    dg.mx_grad(dy[:, :0].contiguous(), dg.MXTensor(a.codes[:0], a.scales[:0], 40), out=out)
+    assert (out == 0).all()
+    assert dg.mx_matmul(a, dg.MXTensor(a.codes[:0], a.scales[:0], 40)).shape == (3, 0)
+
+
+def test_product_exact_on_integers(dg):
+    """Integer values whose sums stay below 2^24: the same bits in FP32."""
+    rng = np.random.default_rng(9)
+    a = rng.choice([-6, -4, -3, -2, -1, 0, 1, 2, 3, 4, 6], (384, 1100)).astype(np.float64)
+    b = rng.choice([-6, -4, -3, -2, -1, 0, 1, 2, 3, 4, 6], (260, 1100)).astype(np.float64)
+    a[:, ::32], b[:, ::32] = 4, 6      # every block's scale is 1
+    qa, av = _operand(dg, a, "mxfp4")
+    qb, bv = _operand(dg, b, "mxfp4")
+    assert (av == a).all() and (bv == b).all()
+    got = dg.mx_matmul(qa, qb, dtype=torch.float32)
+    assert (_np(got) == a @ b.T).all()
+
+
+def test_product_nan_blocks_stay_in_their_rows(dg):
+    rng = np.random.default_rng(11)
+    x = rng.standard_normal((200, 300))
+    x[17, 40] = np.inf
+    w = rng.standard_normal((150, 300))
+    w[149, 299] = np.nan
+    a, av = _operand(dg, x, "mxfp4")
+    b, bv = _operand(dg, w, "mxfp4")
+    got = dg.mx_matmul(a, b, dtype=torch.float32)
+    total = np.nan_to_num(np.abs(av)) @ np.nan_to_num(np.abs(bv)).T
+    _check(got, av @ bv.T, total, 300, "f32")
+
+
+# ------------------------------------------------------------ linear layer
+
+LINEAR = [(1, 1, 1), (1, 4096, 4096), (1, 1000, 333), (2, 128, 64), (7, 515, 1000),
+          (8, 2048, 512), (9, 300, 4096), (16, 256, 8192), (17, 1111, 999), (33, 4096, 4096),
+          (64, 640, 2048), (65, 200, 777), (128, 1024, 1024), (300, 1030, 512), (1000, 257, 130)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", LINEAR)
+def test_linear(dg, dtype, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + N + K)
+    x = _rand(rng, M, K, dtype, spread=2.0)
+    w, wv = _operand(dg, _np(_rand(rng, N, K, spread=1.0)), "mxfp4", pad=16)
+    xv = ref.values(*ref.quantize(_np(x), "mxfp4"), "mxfp4")
+    want, total = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    for pad, offset in [(0, 0), (5, 1)]:
+        got = dg.mx_linear(_dev(x, "N", pad, offset), w)
+        check_device(dg)
+        _check(got, want, total, K, dtype)
+    out = torch.full((M, N + 3), -1.0, dtype=TYPES[dtype], device="cuda")
+    dg.mx_linear(_dev(x), w, out=out[:, :N])
+    _check(out[:, :N], want, total, K, dtype)
+    assert (out[:, N:] == -1).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 200])
+def test_linear_special_rows(dg, M):
+    """A token with an infinity or a NaN spoils its own row only; a row of
+    zeros gives zeros; scales at both ends of their range."""
+    rng = np.random.default_rng(M)
+    x = rng.standard_normal((M, 500)).astype(np.float32)
+    if M > 1:
+        x[1, 499] = np.nan
+        x[2:3] = 0
+        x[3:4, 64:96] = 2.0 ** -149
+        x[4:5] *= 2.0 ** 60
+    t = torch.from_numpy(x)
+    w, wv = _operand(dg, rng.standard_normal((300, 500)), "mxfp4")
+    xv = ref.values(*ref.quantize(x, "mxfp4"), "mxfp4")
+    got = dg.mx_linear(t.cuda(), w)
+    _check(got, xv @ wv.T, np.nan_to_num(np.abs(xv)) @ np.abs(wv).T, 500, "f32")
+    if M == 1:
+        t[0, 3] = float("inf")
+        assert dg.mx_linear(t.cuda(), w).isnan().all()
+
+
+# ------------------------------------------------------------ backward products
+
+GRADS = [(1, 1, 1), (1, 40, 7), (16, 128, 64), (33, 77, 130), (256, 128, 64), (129, 300, 257),
+         (1000, 1030, 777), (40, 2048, 1000), (640, 512, 96), (300, 264, 4096), (515, 1284, 65)]
+
+
+def _grad_a(dg, rng, M, K, dtype, op, pad=0):
+    a = _rand(rng, M, K, dtype, spread=1.0)
+    s = a.t() if op == "T" else a
+    rows, cols = s.shape
+    buf = torch.full((rows, -(-cols // 8) * 8 + pad), float("nan"), dtype=a.dtype, device="cuda")
+    buf[:, :cols] = s.cuda()
+    v = buf[:, :cols]
+    return a, (v.t() if op == "T" else v)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("shape", GRADS)
+def test_grad(dg, fmt, dtype, op, out, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + 3 * N + 5 * K)
+    a, av = _grad_a(dg, rng, M, K, dtype, op, pad=8)
+    b, bv = _operand(dg, _np(_rand(rng, K, N, spread=1.0)), fmt, pad=16)
+    bv = _np(torch.from_numpy(bv).to(TYPES[dtype]))
+    dc = dtype if out == "same" else "f32"
+    got = dg.mx_grad(av, b, dtype=TYPES[dc])
+    check_device(dg)
+    _check(got, _np(a) @ bv, np.abs(_np(a)) @ np.abs(bv), K, dc)
+
+
+@pytest.mark.parametrize("fmt,op,dc", [("mxint8", "T", "f32"), ("mxfp4", "N", "bf16"),
+                                       ("mxint8", "N", "bf16")])
+def test_grad_accumulates_into_a_padded_view(dg, fmt, op, dc):
+    M, N, K = 300, 397, 500
+    rng = np.random.default_rng(3)
+    a, av = _grad_a(dg, rng, M, K, "bf16", op)
+    b, bv = _operand(dg, _np(_rand(rng, K, N)), fmt)
+    c0 = _rand(rng, M, N, dc, spread=0.0)
+    out = _dev(c0, pad=3, offset=1)
+    dg.mx_grad(av, b, out=out, alpha=0.25, beta=1.0)
+    check_device(dg)
+    total = 0.25 * (np.abs(_np(a)) @ np.abs(bv)) + np.abs(_np(c0))
+    _check(out, 0.25 * (_np(a) @ bv) + _np(c0), total, K, dc)
+    out.fill_(float("nan"))
+    dg.mx_grad(av, b, out=out)
+    _check(out, _np(a) @ bv, 4 * total, K, dc)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grad_every_scale(dg, fmt):
+    """Exact in BF16 over the whole range of scales whose values BF16 and
+    FP32 hold, one row of B for each scale; NaN blocks; FP16 as rounded."""
+    K = 256
+    codes = np.tile(np.arange(64) % 16 if fmt == "mxfp4" else np.arange(64) * 4 - 127, (K, 1))
+    scales = np.stack([np.arange(K), np.arange(K)[::-1]], axis=1).astype(np.uint8)
+    cb, sb = ref.pack(codes, scales, fmt)
+    b = dg.MXTensor(torch.from_numpy(cb).cuda(), torch.from_numpy(sb).cuda(), 64, fmt)
+    v = ref.values(codes, scales, fmt)
+    for dtype in ("bf16", "f16"):
+        # One-hot rows pick one row of B each; NaN rows (scale 255) spoil every sum, so
+        # they are left out of the contraction here.
+        keep = slice(1, 255)
+        bk = dg.MXTensor(torch.from_numpy(cb[keep]).cuda(), _scales_of(sb, keep, K).cuda(), 64, fmt)
+        a = torch.eye(254, dtype=TYPES[dtype], device="cuda")
+        buf = torch.zeros((254, 256), dtype=TYPES[dtype], device="cuda")
+        buf[:, :254] = a
+        got = dg.mx_grad(buf[:, :254], bk, dtype=torch.float32).cpu()
+        want = torch.from_numpy(v[keep]).float().to(TYPES[dtype]).float()
+        finite = torch.isfinite(want).all(dim=0)   # (inf * 0 of the other rows is NaN)
+        assert torch.equal(got[:, finite], want[:, finite])
+        assert got[:, ~finite].isnan().sum() >= (~finite).sum() * 253 if (~finite).any() else True
+    eye = torch.eye(256, dtype=torch.bfloat16, device="cuda")
+    assert dg.mx_grad(eye, b).isnan().all()
+
+
+def _scales_of(sb, keep, K):
+    """Tiles of the rows `keep` of a K-row, two-block array."""
+    r = np.arange(K)
+    rows = np.stack([sb[(r // 128) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + b]
+                     for b in range(2)], axis=1)[keep]
+    out = np.zeros(1024, dtype=np.uint8)
+    r = np.arange(rows.shape[0])
+    for b in range(2):
+        out[(r // 128) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + b] = rows[:, b]
+    return torch.from_numpy(out)
+
+
+def test_gradients_are_those_of_the_layer(dg):
+    """f(x, W) = sum(dY * (x W^T)) with the quantised x and W: mx_grad gives
+    its derivatives, by the formula and by differences (f is linear in each,
+    so a difference quotient is exact up to rounding)."""
+    rng = np.random.default_rng(21)
+    T, I, O = 96, 160, 72
+    x, w = rng.standard_normal((T, I)), rng.standard_normal((O, I)) / 13
+    qx, xv = _operand(dg, x, "mxint8")
+    qw, wv = _operand(dg, w, "mxfp4")
+    dy = _rand(rng, T, O, "bf16", spread=0.0)
+    d = _np(dy)
+    dyg = dy.cuda()
+    dx = dg.mx_grad(dyg, qw, dtype=torch.float32)
+    dw = dg.mx_grad(dyg.t(), qx, dtype=torch.float32)
+    _check(dx, d @ wv, np.abs(d) @ np.abs(wv), O, "f32")
+    _check(dw, d.T @ xv, np.abs(d).T @ np.abs(xv), T, "f32")
+
+    def f(xx, ww):
+        return float((d * (xx @ ww.T)).sum())
+    h = 0.5
+    for _ in range(4):
+        ux, uw = rng.standard_normal((T, I)), rng.standard_normal((O, I))
+        num = (f(xv + h * ux, wv) - f(xv - h * ux, wv)) / (2 * h)
+        assert abs(num - float((_np(dx) * ux).sum())) <= 1e-5 * np.abs(_np(dx) * ux).sum()
+        num = (f(xv, wv + h * uw) - f(xv, wv - h * uw)) / (2 * h)
+        assert abs(num - float((_np(dw) * uw).sum())) <= 1e-5 * np.abs(_np(dw) * uw).sum()
+
+
+# ------------------------------------------------------------ streams, graphs, sizes
+
+def test_other_stream_and_repeated_calls(dg):
+    """Calls on a side stream, back to back without waiting, and the same
+    bits again on another stream."""
+    rng = np.random.default_rng(31)
+    x = _rand(rng, 48, 1024, "bf16").cuda()
+    w, _ = _operand(dg, rng.standard_normal((512, 1024)), "mxfp4")
+    dy = _rand(rng, 48, 512, "bf16", spread=0.0).cuda()
+    first = (dg.mx_linear(x, w), dg.mx_grad(dy, w), dg.mx_dequantize(dg.mx_quantize(x, "mxint8")))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            again = (dg.mx_linear(x, w), dg.mx_grad(dy, w),
+                     dg.mx_dequantize(dg.mx_quantize(x, "mxint8")))
+    s.synchronize()
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+    # Different rows on two streams at once do not share a workspace.
+    x2 = (x * 3).contiguous()
+    want2 = dg.mx_linear(x2, w)
+    torch.cuda.synchronize()
+    t = torch.cuda.Stream()
+    outs = []
+    for _ in range(10):
+        with torch.cuda.stream(s):
+            a = dg.mx_linear(x, w)
+        with torch.cuda.stream(t):
+            b = dg.mx_linear(x2, w)
+        outs.append((a, b))
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, first[0]) and torch.equal(b, want2)
+    check_device(dg)
+
+
+def test_graph_replay(dg):
+    """A captured layer step replays on new inputs with the eager bits."""
+    rng = np.random.default_rng(41)
+    w, _ = _operand(dg, rng.standard_normal((640, 768)), "mxfp4")
+    x = _rand(rng, 200, 768, "bf16").cuda()
+    dy = _rand(rng, 200, 640, "bf16", spread=0.0).cuda()
+
+    def step():
+        kept = dg.mx_quantize(x, "mxint8")
+        return dg.mx_linear(x, w), dg.mx_grad(dy, w), dg.mx_grad(dy.t(), kept, dtype=torch.float32)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()          # grows the workspace of this stream
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = step()
+    for seed in (1, 2):
+        x.copy_(_rand(np.random.default_rng(seed), 200, 768, "bf16"))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, step()):
+            assert torch.equal(a, b)
+    check_device(dg)
+
+
+def test_arrays_past_32_bit_offsets(dg):
+    """More than 2^32 elements: sampled rows of the round trip, and a product
+    and a gradient whose operands cross the boundary."""
+    R, K = 140000, 32768
+    x = torch.empty((R, K), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(5)
+    for lo in range(0, R, 10000):
+        x[lo:lo + 10000] = torch.randn((10000, K), generator=gen, device="cuda")
+    rows = [0, 1, 65535, 65536, 131071, 131072, R - 1]
+    for fmt in FMTS:
+        q = dg.mx_quantize(x, fmt)
+        y = dg.mx_dequantize(q)
+        xs = _np(x[rows])
+        want = ref.values(*ref.quantize(xs, fmt), fmt)
+        assert (_np(y[rows]) == want).all()
+        if fmt == "mxfp4":
+            small, sv = _operand(dg, np.random.default_rng(1).standard_normal((8, K)), "mxfp4")
+            got = dg.mx_matmul(q, small, dtype=torch.float32)
+            _check(got[rows], want @ sv.T, np.abs(want) @ np.abs(sv).T, K, "f32")
+        else:
+            # One-hot rows of A pick rows of q: exact.
+            a = torch.zeros((len(rows), R), dtype=torch.bfloat16, device="cuda")
+            for i, r in enumerate(rows):
+                a[i, r] = 1
+            got = dg.mx_grad(a, q)
+            assert (_np(got) == want).all()
+        del q, y
+    check_device(dg)
