@@ -137,23 +137,24 @@ __host__ __device__ constexpr uint32_t instr_desc_mx4(uint32_t m, uint32_t n, ui
          | (sf << 29);             // A scale byte
 }
 
-// 64-deep block-scaled MMA step.
-__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
+// 64-deep block-scaled MMA step of a CTA pair (see mma_f16_pair); each CTA's
+// tensor memory holds the scales of its own rows of A and of all of B.
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                             uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
       "[%5], p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
 
 // One 512-byte tile of scales (32 rows of 16 bytes) to 4 TMEM columns, in
-// all four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+// all four lane quarters, in both CTAs of the pair from their own memories.
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
                : "memory");
 }
 
@@ -170,16 +171,32 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // ------------------------------------------------------------ role waits
 
 // A role's bounded wait by one thread; on giving up records the fault (once
-// per CTA) and raises the CTA's abort flag.  `spin`: no suspend hint.
+// per CTA) and raises the CTA's abort flag.  `spin`: no suspend hint.  The
+// clock is first read after a number of tries, because reading %globaltimer
+// takes longer than most of these waits last.
 __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, unsigned* fault,
                                           unsigned long long timeout_ns, int* abort,
                                           unsigned code, bool spin) {
-  const bool ok = spin ? mbar_wait_spin_bounded(bar, parity, timeout_ns, abort)
-                       : mbar_wait_bounded(bar, parity, timeout_ns, abort);
-  if (ok) return true;
-  if (!*(volatile int*)abort) raise_fault(fault, code);
-  *(volatile int*)abort = 1;
-  return false;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (spin ? mbar_try_wait(bar, parity) : mbar_try_wait_suspend(bar, parity, 10000u)) return true;
+    if ((it & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*(volatile int*)abort || now - t0 > timeout_ns) {
+        if (!*(volatile int*)abort) raise_fault(fault, code);
+        *(volatile int*)abort = 1;
+        return false;
+      }
+    }
+  }
+}
+// The same by a warp, each lane polling: quicker than a broadcast of one
+// lane's result (220 cycles) where the barrier is mostly complete already.
+__device__ __forceinline__ bool role_wait_lanes(uint32_t bar, uint32_t parity, unsigned* fault,
+                                                unsigned long long timeout_ns, int* abort,
+                                                unsigned code) {
+  return __all_sync(0xffffffffu, role_wait(bar, parity, fault, timeout_ns, abort, code, true));
 }
 // The same by a warp: lane 0 waits, the result is broadcast.
 __device__ __forceinline__ bool role_wait_warp(uint32_t bar, uint32_t parity, unsigned* fault,
@@ -191,25 +208,84 @@ __device__ __forceinline__ bool role_wait_warp(uint32_t bar, uint32_t parity, un
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Arrives on an mbarrier of any CTA of the cluster (shared::cluster address)
+// with the default release at CTA scope.  What the arrivals here hand over
+// is read by the asynchronous proxy (after fence.proxy.async by the writer)
+// or is tensor memory (after tcgen05 fences); a release at cluster scope
+// would wait some 1000 cycles for every earlier access of the thread.
+__device__ __forceinline__ void mbar_arrive_any_cta(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// ------------------------------------------------------------ pair schedule
+
+// Work unit u of a grid of CTA pairs (MxSchedule): tile column tn (256
+// columns of C), rows [row0, row0 + rows) of C (rows = 256 or 128), k-tiles
+// [kb, ke).
+struct MxUnit {
+  int tn, row0, rows, kb, ke, slice;
+};
+__device__ __forceinline__ MxUnit mx_unit(int u, const MxSchedule& sc, int nk) {
+  MxUnit w;
+  const int v = u / sc.slices;
+  w.slice = u - v * sc.slices;
+  w.kb = (int)((long long)w.slice * nk / sc.slices);
+  w.ke = (int)((long long)(w.slice + 1) * nk / sc.slices);
+  int tile = v, off = 0;
+  w.rows = kMxPairTile;
+  if (v >= sc.full_tiles) {
+    const int j = v - sc.full_tiles;
+    tile = sc.full_tiles + (j >> 1);
+    off = (j & 1) * (kMxPairTile / 2);
+    w.rows = kMxPairTile / 2;
+  }
+  int tm;
+  grouped_tile(tile, sc.tiles_n, sc.tiles_m, sc.group, w.tn, tm);
+  w.row0 = tm * kMxPairTile + off;
+  return w;
+}
+
 // ------------------------------------------------------------ epilogue
 
-// One thread's 32 accumulator values (FP32 bits) to C: value j belongs to
-// row row0 + j and column col of C, so that a warp writes 32 consecutive
-// columns of one row at a time, whatever C's alignment.
+// One thread's 32 FP32 sums to 32 rows of one column of C (c: the first
+// row's element; rows_left may be below 32 or even negative):
+// C := alpha * sum + beta * C.  A warp's lanes hold 32 consecutive columns,
+// so that each store writes one contiguous piece of a row, whatever C's
+// alignment.
 template <typename T>
-__device__ __forceinline__ void store_column32(const uint32_t (&r)[32], T* C, long long ldc,
-                                               int M, int N, int row0, int col, float alpha,
-                                               float beta) {
-  if (col >= N) return;
-  T* c = C + (long long)row0 * ldc + col;
+__device__ __forceinline__ void store_rows32(const float* v, T* c, long long ldc, int rows_left,
+                                             float alpha, float beta) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (row0 + j < M) {
-      float v = alpha * __uint_as_float(r[j]);
-      if (beta != 0.f) v = fmaf(beta, to_f32_any<T>(c[j * ldc]), v);
-      c[j * ldc] = from_f32_any<T>(v);
+  for (int g = 0; g < 4; ++g) {
+    if (beta == 0.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * g + j < rows_left) c[j * ldc] = from_f32_any<T>(alpha * v[8 * g + j]);
+    } else {
+      float old[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        old[j] = 8 * g + j < rows_left ? to_f32_any<T>(c[j * ldc]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * g + j < rows_left)
+          c[j * ldc] = from_f32_any<T>(fmaf(beta, old[j], alpha * v[8 * g + j]));
     }
+    c += 8 * ldc;
   }
+}
+
+// Waits for this thread's tcgen05.ld loads into r (see tmem_ld_wait).
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+        "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
 }
 
 }  // namespace dgemm

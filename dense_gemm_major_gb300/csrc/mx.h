@@ -30,15 +30,24 @@ cudaError_t launch_mx_dequantize(int fmt, int dtype, int R, int K, const void* c
                                  long long ldq, const void* scales, void* Y, long long ldy,
                                  cudaStream_t stream);
 
-// C := alpha * A . B^T + beta * C on tcgen05 block-scaled FP4.  The kernel
-// puts B's rows (C's columns) on the MMA's M side, so that a warp's 32 TMEM
-// lanes are 32 consecutive columns of a row of C.
+// Schedule of the kernels that compute 256 x 256 tiles of C on CTA pairs:
+// tiles [0, full_tiles) whole, the rest as two halves of 128 rows of C, each
+// over `slices` ranges of K (slices > 1: FP32 partial results at
+// ws + slice * M * ldw, summed by launch_splitk_reduce).
+struct MxSchedule {
+  int tiles_m, tiles_n;     // tiles of C along its rows and columns
+  int full_tiles, units;    // units: all halves and tiles, times slices
+  int slices;
+  int group;                // tile columns per rasterisation group
+};
+constexpr int kMxPairTile = 256;
+
+// C := alpha * A . B^T + beta * C on tcgen05 block-scaled FP4.
 struct Mx4Params {
   int M, N, K;                        // C is M x N
-  const unsigned char* sa;            // scales of A and B
-  const unsigned char* sb;
-  int tiles_m, tiles_n;               // tiles of C
-  int group;                          // tile columns of C per rasterisation group
+  MxSchedule sched;
+  float* ws;
+  long long ldw;
   float alpha, beta;
   void* C;
   long long ldc;
@@ -46,31 +55,33 @@ struct Mx4Params {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-constexpr int kMx4BN = 128;           // rows of B (columns of C) per tile
-constexpr int kMx4BM = 128;           // rows of A (rows of C) per tile
 constexpr int kMx4BK = 256;           // 128 bytes of codes
+// tmA, tmB: codes as bytes, boxes of 128 bytes x 64 and 128 rows; tmSA, tmSB:
+// scales as 32-bit words, one row per 128 rows of the operand, boxes of two
+// tiles.
 cudaError_t launch_mx4(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
-                       int grid, cudaStream_t stream);
+                       const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
+                       cudaStream_t stream);
 
 // C := alpha * op(A) . B + beta * C, B quantised (K x N).
 struct MxGradParams {
   int M, N, K;
   int fmt, dtype, op_a, dtype_c;
-  const unsigned char* codes;
-  long long ldb;
   const unsigned char* sb;
-  int tiles_m, tiles_n;
-  int group;
+  MxSchedule sched;
+  int seg;                  // k-tiles summed in tensor memory at a time
+  float* ws;
+  long long ldw;
   float alpha, beta;
   void* C;
   long long ldc;
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-constexpr int kMxGradBN = 128;        // columns of B (and C) per tile: the MMA's M side
-constexpr int kMxGradBM = 256;        // rows of C per tile: the MMA's N side
 constexpr int kMxGradBK = 64;
-cudaError_t launch_mx_grad(const MxGradParams& p, const CUtensorMap* tmA, int grid,
-                           cudaStream_t stream);
+// tmA: op(A), boxes of 64 x 64; tmB: the codes as bytes, boxes of 64 rows x
+// 128 columns.
+cudaError_t launch_mx_grad(const MxGradParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                           int pairs, cudaStream_t stream);
 
 }  // namespace dgemm

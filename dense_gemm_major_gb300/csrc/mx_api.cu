@@ -3,7 +3,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -15,25 +15,26 @@
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
-int g_sms[kMaxDevices];   // SM counts, 0 until asked for; guarded by g_mu
 
-// The quantised X of gemm_mx4_linear, one per (device, stream).
+// Device workspaces, one per (device, stream, use): the quantised X of
+// gemm_mx4_linear, and the FP32 partial results of products split along K
+// (one call can need both).
 struct Workspace {
   unsigned char* ptr = nullptr;
   size_t bytes = 0;
 };
-std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;   // guarded by g_mu
+constexpr int kWsQuantized = 0, kWsPartials = 1;
+std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_workspaces;   // guarded by g_mu
 
-gemm_status_t get_workspace(cudaStream_t stream, size_t bytes, unsigned char** out) {
+gemm_status_t get_workspace(cudaStream_t stream, int use, size_t bytes, unsigned char** out) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_UNSUPPORTED_DEVICE;
   }
   std::lock_guard<std::mutex> lock(g_mu);
-  Workspace& w = g_workspaces[std::make_pair(dev, stream)];
+  Workspace& w = g_workspaces[std::make_tuple(dev, stream, use)];
   if (w.bytes < bytes) {
     if (w.ptr != nullptr) {
       // Earlier work queued on this stream may still use the old buffer.
@@ -56,24 +57,14 @@ gemm_status_t get_workspace(cudaStream_t stream, size_t bytes, unsigned char** o
   return GEMM_OK;
 }
 
-// The current device's fault word and SM count.
-gemm_status_t device(unsigned** fault, int* sms) {
-  unsigned* f = dgemm::current_fault_word();
-  int dev = -1;
-  if (f == nullptr || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return GEMM_ERR_UNSUPPORTED_DEVICE;
-  }
-  std::lock_guard<std::mutex> lock(g_mu);
-  if (g_sms[dev] == 0 &&
-      cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    g_sms[dev] = 0;
-    return GEMM_ERR_UNSUPPORTED_DEVICE;
-  }
-  *fault = f;
-  *sms = g_sms[dev];
-  return GEMM_OK;
+// The current device's fault word, and the CTA pairs that it can hold at
+// once with one CTA per SM (fewer than half of its SMs: a cluster's CTAs
+// share a GPC; a pair too many would run after all others).
+gemm_status_t device(unsigned** fault, int* pairs) {
+  *fault = dgemm::current_fault_word();
+  if (*fault == nullptr) return GEMM_ERR_UNSUPPORTED_DEVICE;
+  *pairs = gemm_pair_clusters();
+  return *pairs > 0 ? GEMM_OK : GEMM_ERR_UNSUPPORTED_DEVICE;
 }
 
 // cuTensorMapEncodeTiled, fetched from the driver once.
@@ -92,9 +83,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D row-major array {inner, outer}, 128-byte swizzled boxes.
+// 2-D row-major array {inner, outer}.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
-               uint64_t outer, uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer) {
+               uint64_t outer, uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer,
+               bool swizzle = true) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, outer};
@@ -102,7 +94,8 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -158,30 +151,79 @@ gemm_status_t scale_only(int dtype, int M, int N, float beta, void* C, int ldc,
   return status_of(dgemm::launch_scale_c(C, M, N, ldc, dtype, beta, stream));
 }
 
+// Schedule of an M x N product of nk k-tiles on `pairs` CTA pairs.
+//  * Enough tiles for a round: whole 256 x 256 tiles; those of a last
+//    partial round run as halves when the halves fit one round.
+//  * Fewer tiles than pairs: halves if they still fit one round (or if C has
+//    no second half), and the remaining pairs share out K: as many slices as
+//    fit, of at least kMinSlice k-tiles each, because a slice costs a pass
+//    over an FP32 copy of C.
+constexpr long long kWorkspaceCap = 256ll << 20;   // bytes of partial results
+dgemm::MxSchedule schedule(int M, int N, int nk, int pairs, int group, int min_slice) {
+  dgemm::MxSchedule sc;
+  sc.tiles_m = ceil_div(M, dgemm::kMxPairTile);
+  sc.tiles_n = ceil_div(N, dgemm::kMxPairTile);
+  sc.group = group;
+  sc.slices = 1;
+  const int tiles = sc.tiles_m * sc.tiles_n;
+  if (tiles >= pairs) {
+    const int rem = tiles % pairs;
+    sc.full_tiles = 2 * rem <= pairs ? tiles - rem : tiles;
+  } else {
+    sc.full_tiles = M <= dgemm::kMxPairTile / 2 || 2 * tiles <= pairs ? 0 : tiles;
+    const int used = sc.full_tiles > 0 ? tiles : tiles * (M <= dgemm::kMxPairTile / 2 ? 1 : 2);
+    const long long slice_bytes = (long long)M * (((long long)N + 3) / 4 * 4) * 4;
+    int s = pairs / used;
+    if (s > nk / min_slice) s = nk / min_slice;
+    while (s > 1 && s * slice_bytes > kWorkspaceCap) --s;
+    if (s > 1) sc.slices = s;
+  }
+  sc.units = (sc.full_tiles + 2 * (tiles - sc.full_tiles)) * sc.slices;
+  return sc;
+}
+
+// The workspace of a schedule with slices.
+gemm_status_t partials(const dgemm::MxSchedule& sc, int M, int N, cudaStream_t stream, float** ws,
+                       long long* ldw) {
+  *ws = nullptr;
+  *ldw = ((long long)N + 3) / 4 * 4;
+  if (sc.slices == 1) return GEMM_OK;
+  unsigned char* p = nullptr;
+  const gemm_status_t st =
+      get_workspace(stream, kWsPartials, (size_t)sc.slices * M * *ldw * 4, &p);
+  *ws = reinterpret_cast<float*>(p);
+  return st;
+}
+
 // The product of checked operands, M, N, K > 0.
 gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a, long long lda,
                       const void* sa, const void* b, long long ldb, const void* sb, float beta,
-                      void* C, int ldc, unsigned* fault, int sms, cudaStream_t stream) {
-  alignas(64) CUtensorMap tmA, tmB;
+                      void* C, int ldc, unsigned* fault, int max_pairs, cudaStream_t stream) {
+  alignas(64) CUtensorMap tmA, tmB, tmSA, tmSB;
   const uint64_t width = (uint64_t)code_bytes(GEMM_MXFP4, K);
-  if (!encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, width, (uint64_t)M, (uint64_t)lda, 128,
-                 dgemm::kMx4BM) ||
-      !encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, b, width, (uint64_t)N, (uint64_t)ldb, 128,
-                 dgemm::kMx4BN))
+  const uint64_t srow = (uint64_t)dgemm::mx_scale_tiles(K) * dgemm::kMxTileBytes;
+  constexpr uint32_t sbox = dgemm::kMx4BK / 128 * dgemm::kMxTileBytes / 4;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapDataType u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  if (!encode_2d(&tmA, u8, a, width, (uint64_t)M, (uint64_t)lda, 128, 64) ||
+      !encode_2d(&tmB, u8, b, width, (uint64_t)N, (uint64_t)ldb, 128, 128) ||
+      !encode_2d(&tmSA, u32, sa, srow / 4, (uint64_t)ceil_div(M, 128), srow, sbox, 1, false) ||
+      !encode_2d(&tmSB, u32, sb, srow / 4, (uint64_t)ceil_div(N, 128), srow, sbox, 1, false))
     return GEMM_ERR_LAUNCH;
   dgemm::Mx4Params p;
   p.M = M, p.N = N, p.K = K;
-  p.sa = static_cast<const unsigned char*>(sa);
-  p.sb = static_cast<const unsigned char*>(sb);
-  p.tiles_m = ceil_div(M, dgemm::kMx4BM);
-  p.tiles_n = ceil_div(N, dgemm::kMx4BN);
-  p.group = 8;
+  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, 4);
+  gemm_status_t st = partials(p.sched, M, N, stream, &p.ws, &p.ldw);
+  if (st != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc, p.dtype = dtype;
   p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
-  const long long tiles = (long long)p.tiles_m * p.tiles_n;
-  const int grid = (int)(tiles < sms ? tiles : sms);
-  return status_of(dgemm::launch_mx4(p, &tmA, &tmB, grid, stream));
+  const int pairs = p.sched.units < max_pairs ? p.sched.units : max_pairs;
+  cudaError_t e = dgemm::launch_mx4(p, &tmA, &tmB, &tmSA, &tmSB, pairs, stream);
+  if (e == cudaSuccess && p.sched.slices > 1)
+    e = dgemm::launch_splitk_reduce(p.ws, p.sched.slices, M, N, p.ldw, C, ldc, dtype, alpha, beta,
+                                    stream);
+  return status_of(e);
 }
 
 }  // namespace
@@ -215,8 +257,8 @@ gemm_status_t gemm_mx_quantize(gemm_mx_format_t fmt, int dtype, gemm_op_t op, in
       overlap(codes, span(R, code_bytes(fmt, K), ldq), scales, (uint64_t)scale_bytes(R, K)))
     return GEMM_ERR_INVALID_ARG;
   unsigned* fault;
-  int sms;
-  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  int max_pairs;
+  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   return status_of(
       dgemm::launch_mx_quantize(fmt, dtype, op, R, K, X, ldx, codes, ldq, scales, stream));
 }
@@ -235,8 +277,8 @@ gemm_status_t gemm_mx_dequantize(gemm_mx_format_t fmt, int dtype, int R, int K,
                          ldq, scales))
     return GEMM_ERR_INVALID_ARG;
   unsigned* fault;
-  int sms;
-  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  int max_pairs;
+  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   return status_of(
       dgemm::launch_mx_dequantize(fmt, dtype, R, K, codes, ldq, scales, Y, ldy, stream));
 }
@@ -261,11 +303,11 @@ gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha, const void* 
       return GEMM_ERR_INVALID_ARG;
   }
   unsigned* fault;
-  int sms;
-  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  int max_pairs;
+  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (empty) return scale_only(dtype, M, N, beta, C, ldc, stream);
   return run_mx4(dtype, M, N, K, alpha, a_codes, lda, a_scales, b_codes, ldb, b_scales, beta, C,
-                 ldc, fault, sms, stream);
+                 ldc, fault, max_pairs, stream);
 }
 
 gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int ldx,
@@ -287,19 +329,19 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int
       return GEMM_ERR_INVALID_ARG;
   }
   unsigned* fault;
-  int sms;
-  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  int max_pairs;
+  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (K == 0) return scale_only(dtype, M, N, 0.f, Y, ldy, stream);
   const int ldq = code_ld(GEMM_MXFP4, K);
   const size_t code_size = ((size_t)M * ldq + 255) / 256 * 256;
   unsigned char* ws = nullptr;
-  st = get_workspace(stream, code_size + (size_t)scale_bytes(M, K), &ws);
+  st = get_workspace(stream, kWsQuantized, code_size + (size_t)scale_bytes(M, K), &ws);
   if (st != GEMM_OK) return st;
   st = status_of(dgemm::launch_mx_quantize(GEMM_MXFP4, dtype, GEMM_OP_N, M, K, X, ldx, ws, ldq,
                                            ws + code_size, stream));
   if (st != GEMM_OK) return st;
   return run_mx4(dtype, M, N, K, 1.f, ws, ldq, ws + code_size, w_codes, ldw, w_scales, 0.f, Y,
-                 ldy, fault, sms, stream);
+                 ldy, fault, max_pairs, stream);
 }
 
 gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int dtype_c, int M,
@@ -326,33 +368,37 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
       return GEMM_ERR_INVALID_ARG;
   }
   unsigned* fault;
-  int sms;
-  if ((st = device(&fault, &sms)) != GEMM_OK) return st;
+  int max_pairs;
+  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (empty) return scale_only(dtype_c, M, N, beta, C, ldc, stream);
-  alignas(64) CUtensorMap tmA;
+  alignas(64) CUtensorMap tmA, tmB;
   const CUtensorMapDataType dt =
       dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const bool enc = op_a == GEMM_OP_T
-                       ? encode_2d(&tmA, dt, A, (uint64_t)M, (uint64_t)K, (uint64_t)lda * 2, 64,
-                                   dgemm::kMxGradBK)
-                       : encode_2d(&tmA, dt, A, (uint64_t)K, (uint64_t)M, (uint64_t)lda * 2,
-                                   dgemm::kMxGradBK, dgemm::kMxGradBM);
-  if (!enc) return GEMM_ERR_LAUNCH;
+  const uint64_t inner = (uint64_t)(op_a == GEMM_OP_T ? M : K);
+  const uint64_t outer = (uint64_t)(op_a == GEMM_OP_T ? K : M);
+  if (!encode_2d(&tmA, dt, A, inner, outer, (uint64_t)lda * 2, 64, 64) ||
+      !encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, (uint64_t)code_bytes(fmt, N),
+                 (uint64_t)K, (uint64_t)ldb, (uint32_t)code_bytes(fmt, 128), dgemm::kMxGradBK,
+                 false))
+    return GEMM_ERR_LAUNCH;
   dgemm::MxGradParams p;
   p.M = M, p.N = N, p.K = K;
   p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
-  p.codes = static_cast<const unsigned char*>(b_codes);
-  p.ldb = ldb;
   p.sb = static_cast<const unsigned char*>(b_scales);
-  p.tiles_m = ceil_div(M, dgemm::kMxGradBM);
-  p.tiles_n = ceil_div(N, dgemm::kMxGradBN);
-  p.group = 16;
+  const int nk = ceil_div(K, dgemm::kMxGradBK);
+  p.sched = schedule(M, N, nk, max_pairs, 8, 8);
+  // FP32 results: at most 1024 terms per sum in tensor memory.
+  p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
+  if ((st = partials(p.sched, M, N, stream, &p.ws, &p.ldw)) != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc;
   p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
-  const long long tiles = (long long)p.tiles_m * p.tiles_n;
-  const int grid = (int)(tiles < sms ? tiles : sms);
-  return status_of(dgemm::launch_mx_grad(p, &tmA, grid, stream));
+  const int pairs = p.sched.units < max_pairs ? p.sched.units : max_pairs;
+  cudaError_t e = dgemm::launch_mx_grad(p, &tmA, &tmB, pairs, stream);
+  if (e == cudaSuccess && p.sched.slices > 1)
+    e = dgemm::launch_splitk_reduce(p.ws, p.sched.slices, M, N, p.ldw, C, ldc, dtype_c, alpha,
+                                    beta, stream);
+  return status_of(e);
 }
 
 }  // extern "C"

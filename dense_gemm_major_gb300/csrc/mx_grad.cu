@@ -3,300 +3,552 @@
 // microscaled format, blocks of 32 along N.
 //
 // The scales vary along N, not along the contraction, so they cannot be left
-// to a block-scaled MMA: B's codes become 16-bit values on their way into
-// shared memory (exact in BF16: 8 significant bits and a power of two) and
-// tcgen05.mma.kind::f16 accumulates in FP32.  B is the MMA's M side: a TMEM
-// lane is a column of C, and a warp's stores are 32 consecutive columns.
+// to a block-scaled MMA: B's codes become 16-bit values inside the kernel
+// (exact in BF16: at most 8 significant bits and a power of two) and
+// tcgen05.mma.kind::f16 accumulates in FP32.
 //
-// Roles (320 threads): warp 0 loads op(A) by TMA, warp 1 issues the MMAs,
-// warps 2-5 drain the accumulators, warps 6-9 read codes and scales and
-// write the converted tile (MN-major, 128-byte swizzle).
+// A cluster of two CTAs computes 256 columns x 256 rows of C with
+// cta_group::2.  B is the MMA's M side (each CTA converts its own 128
+// columns), op(A) its N side (each CTA loads half of the rows): a TMEM lane
+// is a column of C, so that a warp stores 32 consecutive columns of a row,
+// whatever C's alignment, and B, which costs instructions, is the operand
+// that no CTA touches twice per tile.
+//
+// Roles (512 threads): warp 0 loads op(A) by TMA, warp 1 issues the MMAs
+// (even CTA), warp 2 loads the codes (TMA) and tiles of scales into a ring of
+// their own, ahead of the MMAs' ring, warps 4-7 convert, warps 8-15 drain the
+// accumulators.
+//
+// FP32 sums.  The MMA truncates the running sum at every 16-deep step: over
+// 8192 terms that was measured as a relative error of 6e-6.  For FP32
+// results a tile is therefore summed in segments (MxGradParams::seg), and
+// the draining warps add the segments in registers, rounding to nearest; the
+// two accumulators in tensor memory let that overlap the next segment.
 #include "mx.cuh"
 
 namespace dgemm {
 namespace {
 
-constexpr int BM = kMxGradBM, BN = kMxGradBN, BK = kMxGradBK;
-constexpr int S = 4;
-constexpr int kThreads = 320;
-constexpr int kEpiWarps = 4;
-constexpr int kConvThreads = 128;
-constexpr uint32_t kBlock = 64 * BK * 2;                  // 64 wide, BK deep: 8 KB
-constexpr uint32_t kBBytes = BN / 64 * kBlock;            // converted B
-constexpr uint32_t kABytes = BM / 64 * kBlock;            // op(A)
-constexpr uint32_t kStage = kABytes + kBBytes;
-constexpr uint32_t kSmem = S * kStage + 1024 + 256;
-constexpr uint32_t kTmemCols = 2 * BM;
-static_assert(kTmemCols == 512, "tensor memory holds two accumulators");
+constexpr int BK = kMxGradBK;
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 4, kConvWarps = 4;
+constexpr int kEpiWarp = 8, kEpiWarps = 8;
+// Registers per thread: 128 at launch; after the split, 128 threads of loads
+// and MMAs, 128 of conversion, 256 of draining (128 sums and 32 loaded
+// values each): 40 + 88 + 2 * 192 = 4 * 128.
+constexpr int kRegsLaunch = 128, kRegsIssue = 40, kRegsConv = 88, kRegsEpi = 192;
+static_assert(kRegsIssue + kRegsConv + 2 * kRegsEpi <= 4 * kRegsLaunch, "register split");
 
+constexpr uint32_t kBlock = 64 * BK * 2;                  // 64 wide, BK deep: 8 KB
+constexpr uint32_t kConvBytes = 2 * kBlock;               // 128 columns of B
+constexpr uint32_t kABytes = 2 * kBlock;                  // 128 rows of C
+constexpr uint32_t kStage = kConvBytes + kABytes;         // what an MMA step reads
+constexpr uint32_t kTmemCols = 512;                       // two accumulators
+
+template <int kFmt>
+struct Layout {
+  static constexpr uint32_t kRawRow = kFmt == GEMM_MXFP4 ? 64 : 128;   // 128 codes
+  static constexpr uint32_t kRaw = kRawRow * BK;
+  static constexpr uint32_t kRawStage = kRaw + kMxTileBytes;
+  static constexpr int kStages = kFmt == GEMM_MXFP4 ? 6 : 5;
+  static constexpr int kRawStages = 6;
+  static constexpr uint32_t kSmem = kStages * kStage + kRawStages * kRawStage + 1024 + 512;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <int S, int R>
 struct alignas(8) Barriers {
-  uint64_t full[S];
-  uint64_t empty[S];
+  uint64_t full[S];       // even CTA: op(A) of both CTAs loaded, both conversions done
+  uint64_t empty[S];      // the MMAs on stage s are done
+  uint64_t raw_full[R];   // codes and scales of this CTA loaded
+  uint64_t raw_empty[R];  // and read by the converting warps
   uint64_t acc_full[2];
-  uint64_t acc_empty[2];
+  uint64_t acc_empty[2];  // even CTA
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Barriers) <= 256, "barrier block must fit its reserved space");
 
-// 16 codes of one row: 16 bytes (MXINT8) or 8 (MXFP4).
-struct Codes16 {
-  uint4 w;
-  unsigned scale;
+// ------------------------------------------------------------ conversion
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t twice(uint32_t h) { return h | (h << 16); }
+
+// FP16 bits of 2^e, e in [-24, 15].
+__device__ __forceinline__ uint32_t f16_pow2(int e) {
+  return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
+}
+
+// A block's scale as multipliers of its values.  BF16: one, exact (2^-127 is
+// a subnormal).  s * 0x00800080 puts s into both exponent fields; bit 6 of the
+// fraction makes 2^-127 of s = 0 and NaN of s = 255.
+// FP16: two powers of two whose product is the scale.  The first is at least
+// 2^-14, so a value times it is exact (both formats' steps are 2^-6 or more)
+// and only the second product rounds; the exponents below -39 that the clamp
+// changes give zero either way, those above 30 infinity.
+template <typename T>
+struct Scale {
+  uint32_t a, b;
+  __device__ __forceinline__ explicit Scale(unsigned s) {
+    if constexpr (__is_same(T, __nv_bfloat16)) {
+      a = s * 0x00800080u;
+      if (((s + 1u) & 0xFEu) == 0u) a |= 0x00400040u;
+      b = 0;
+    } else {
+      const int e = (int)s - 127;
+      const int e1 = min(max(e, -14), 15);
+      const int e2 = min(max(e - e1, -25), 15);
+      a = twice(s == 255u ? 0x7E00u : f16_pow2(e1));
+      b = twice(e2 < -24 ? 0u : f16_pow2(e2));
+    }
+  }
+  __device__ __forceinline__ uint32_t times(uint32_t v) const {
+    if constexpr (__is_same(T, __nv_bfloat16)) return mul_bf16x2(v, a);
+    return mul_f16x2(mul_f16x2(v, a), b);
+  }
 };
 
+// Eight E2M1 codes as four pairs of 16-bit values, scaled.
+template <typename T>
+__device__ __forceinline__ uint4 convert_e2m1x8(uint32_t w, const Scale<T>& sc) {
+  uint32_t r[4];
+  if constexpr (__is_same(T, __nv_bfloat16)) {
+    // The magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 have the BF16 bytes
+    // (high) 00 3F 3F 3F 40 40 40 40, (low) 00 00 80 C0 00 40 80 C0: a byte
+    // permutation looks four of them up at a time.  The sign of the even
+    // code of a byte sits at bit 7 after a shift by 4, that of the odd one at
+    // bit 7 as it is.
+    const uint32_t mag = w & 0x77777777u;
+    const uint32_t even = w << 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sel = h == 0 ? mag : mag >> 16;
+      const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);
+      const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t v = __byte_perm(lo, hi, j == 0 ? 0x5140 : 0x7362);
+        const int byte = 2 * h + j;
+        const uint32_t sign = __byte_perm(even, w, (byte << 4) | ((byte + 4) << 12));
+        r[byte] = sc.times(v) ^ (sign & 0x80008000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h;
+      asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+          "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+          : "=r"(h)
+          : "r"(w >> (8 * j)));
+      r[j] = sc.times(h);
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Four MXINT8 codes as two pairs of 16-bit values, scaled.
+template <typename T>
+__device__ __forceinline__ uint2 convert_int8x4(uint32_t w, const Scale<T>& sc) {
+  uint32_t r[2];
+  if constexpr (__is_same(T, __nv_bfloat16)) {
+    // A code c = low7 - 128 sign.  0x4000 + low7 is 2 + low7 / 64 in BF16 and
+    // 0x4000 + (c & 0x80) is 2 (1 + sign): their difference is c / 64, exactly.
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t p = __byte_perm(w, 0x40404040u, j == 0 ? 0x4140 : 0x4342);
+      r[j] = sc.times(sub_bf16x2(p & 0x407F407Fu, p & 0x40804080u));
+    }
+  } else {
+    // 0x4C00 + u is 16 + u / 64 in FP16; u = c + 128.
+    const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t p = __byte_perm(u, 0x4C4C4C4Cu, j == 0 ? 0x4140 : 0x4342);
+      r[j] = sc.times(sub_f16x2(p, 0x4C804C80u));
+    }
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+// What a converting lane takes at a time: 16 columns of each of 4 rows.
+template <int kFmt>
+struct Raw {
+  uint32_t w[4][kFmt == GEMM_MXFP4 ? 2 : 4];
+  unsigned s[4];
+};
+
+// ------------------------------------------------------------ kernel
+
 template <int kFmt, typename T, typename TC, bool kAT>
-__global__ void __launch_bounds__(kThreads, 1)
-    mx_grad_kernel(const __grid_constant__ CUtensorMap tmA, const MxGradParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mx_grad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const MxGradParams p) {
+  using L = Layout<kFmt>;
+  constexpr int S = L::kStages, R = L::kRawStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
-  Barriers* bars = reinterpret_cast<Barriers*>(base + S * kStage);
+  unsigned char* const sraw = base + S * kStage;
+  auto* bars = reinterpret_cast<Barriers<S, R>*>(sraw + R * L::kRawStage);
+  static_assert(sizeof(Barriers<S, R>) <= 512, "barrier block must fit its reserved space");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int units = p.tiles_m * p.tiles_n;
+  const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
+  const int npairs = gridDim.x >> 1;
   const int nk = (p.K + BK - 1) / BK;
+  const MxSchedule& sc = p.sched;
   constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&bars->full[s]), 1 + kConvThreads / 32);
+      mbar_init(smem_u32(&bars->full[s]), 1 + 2);
       mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    for (int r = 0; r < R; ++r) {
+      mbar_init(smem_u32(&bars->raw_full[r]), 1);
+      mbar_init(smem_u32(&bars->raw_empty[r]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&bars->acc_full[b]), 1);
-      mbar_init(smem_u32(&bars->acc_empty[b]), kEpiWarps);
+      mbar_init(smem_u32(&bars->acc_empty[b]), 2 * kEpiWarps);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) tma_prefetch_desc(&tmA);
-  if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = bars->tmem_base;
   wait_prior_grids();
   allow_dependent_grids();
 
   uint32_t issued = 0;
-  if (warp == 0) {
-    // ------------------------------------------------ op(A)
-    if (lane == 0) {
+  if (warp < kConvWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------- op(A) (both CTAs)
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        int tn, tm;
-        grouped_tile(u, p.tiles_n, p.tiles_m, p.group, tn, tm);
-        for (int kt = 0; kt < nk; ++kt, ++it) {
+      for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
+        const MxUnit w = mx_unit(u, sc, nk);
+        if (w.row0 >= p.M) continue;
+        const int boxes = w.rows / 128;               // of 64 rows of C, per CTA
+        const int row = w.row0 + (int)rank * (w.rows / 2);
+        for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
           const uint32_t s = it % S;
           ok = role_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
                          &bars->abort, kFaultTcProducerWait, true);
           if (!ok) break;
-          const uint32_t fb = smem_u32(&bars->full[s]);
-          const uint32_t st = smem_u32(base + s * kStage) + kBBytes;
-          mbar_arrive_expect_tx(fb, kABytes);
-          if constexpr (kAT) {   // stored K x M: 64-wide blocks of m, one row per k
-            for (int j = 0; j < BM / 64; ++j)
-              tma_load_2d(st + j * kBlock, &tmA, fb, tm * BM + j * 64, kt * BK);
-          } else {               // rows of 64 k
-            tma_load_2d(st, &tmA, fb, kt * BK, tm * BM);
+          const uint32_t sa = smem_u32(base + s * kStage) + kConvBytes;
+          const uint32_t fb = mapa_shared(smem_u32(&bars->full[s]), 0);
+          if (rank == 0)
+            mbar_arrive_expect_tx(smem_u32(&bars->full[s]), 2u * (uint32_t)boxes * kBlock);
+          for (int j = 0; j < boxes; ++j) {
+            if constexpr (kAT)   // stored K x M: rows of C contiguous
+              tma_load_2d_pair(sa + j * kBlock, &tmA, fb, row + j * 64, kt * BK);
+            else
+              tma_load_2d_pair(sa + j * kBlock, &tmA, fb, kt * BK, row + j * 64);
           }
           issued = it + 1;
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc(kAb, BN, BM, 1u, kAT ? 1u : 0u);
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------- codes and scales (both CTAs)
+      const int ktiles = mx_scale_tiles(p.N);
       uint32_t it = 0;
-      int local = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++local) {
-        const uint32_t b = local & 1;
-        ok = role_wait(smem_u32(&bars->acc_empty[b]), ((local >> 1) & 1u) ^ 1u, p.fault,
-                       p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
-        if (!ok) break;
-        tc_fence_after();
-        for (int kt = 0; kt < nk; ++kt, ++it) {
-          const uint32_t s = it % S;
-          ok = role_wait(smem_u32(&bars->full[s]), (it / S) & 1u, p.fault, p.timeout_ns,
-                         &bars->abort, kFaultTcMmaWait, true);
+      for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
+        const MxUnit w = mx_unit(u, sc, nk);
+        if (w.row0 >= p.M) continue;
+        const int ct = w.tn * 2 + (int)rank;          // this CTA's 128 columns
+        const uint32_t sbytes = ct < ktiles ? (uint32_t)kMxTileBytes : 0u;
+        for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
+          const uint32_t r = it % R;
+          ok = role_wait(smem_u32(&bars->raw_empty[r]), ((it / R) & 1u) ^ 1u, p.fault,
+                         p.timeout_ns, &bars->abort, kFaultTcProducerWait, true);
+          if (!ok) break;
+          const uint32_t raw = smem_u32(sraw + r * L::kRawStage);
+          const uint32_t rb = smem_u32(&bars->raw_full[r]);
+          mbar_arrive_expect_tx(rb, L::kRaw + sbytes);
+          tma_load_2d(raw, &tmB, rb, ct * (int)L::kRawRow, kt * BK);
+          if (sbytes != 0)
+            bulk_load(raw + L::kRaw,
+                      p.sb + ((long long)(kt * BK / 128) * ktiles + ct) * kMxTileBytes, sbytes, rb);
+          issued = it + 1;
+        }
+      }
+    } else if (warp == 1 && rank == 0 && lane == 0) {
+      // ---------------------------------------------- MMA issuer (even CTA)
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
+        const MxUnit w = mx_unit(u, sc, nk);
+        if (w.row0 >= p.M) continue;
+        const uint32_t idesc = instr_desc(kAb, 256, (uint32_t)w.rows, 1u, kAT ? 1u : 0u);
+        for (int k0 = w.kb; k0 < w.ke && ok; k0 += p.seg, ++seg) {
+          const int k1 = min(k0 + p.seg, w.ke);
+          const uint32_t b = seg & 1;
+          ok = role_wait(smem_u32(&bars->acc_empty[b]), ((seg >> 1) & 1u) ^ 1u, p.fault,
+                                 p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(base + s * kStage);
+          for (int kt = k0; kt < k1; ++kt, ++it) {
+            const uint32_t s = it % S;
+            ok = role_wait(smem_u32(&bars->full[s]), (it / S) & 1u, p.fault, p.timeout_ns,
+                                   &bars->abort, kFaultTcMmaWait, true);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(base + s * kStage);
+            const uint32_t sa = st + kConvBytes;
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            mma_f16(tmem_base + b * BM, mnmajor_desc(st, k, kBlock),
-                    kAT ? mnmajor_desc(st + kBBytes, k, kBlock) : kmajor_desc(st + kBBytes, k),
-                    idesc, (kt > 0 || k > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&bars->empty[s]));
+            for (int k = 0; k < BK / 16; ++k)
+              mma_f16_pair(tmem_base + b * 256, mnmajor_desc(st, k, kBlock),
+                           kAT ? mnmajor_desc(sa, k, kBlock) : kmajor_desc(sa, k), idesc,
+                           (kt > k0 || k > 0) ? 1u : 0u);
+            mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
+          }
+          if (!ok) break;
+          mma_commit_pair_multicast(smem_u32(&bars->acc_full[b]), 0x3);
         }
-        if (!ok) break;
-        mma_commit(smem_u32(&bars->acc_full[b]));
       }
     }
     __syncwarp();
-  } else if (warp < 2 + kEpiWarps) {
-    // ------------------------------------------------ epilogue
-    const int q = warp & 3;
-    int local = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++local) {
-      int tn, tm;
-      grouped_tile(u, p.tiles_n, p.tiles_m, p.group, tn, tm);
-      const uint32_t b = local & 1;
-      if (!role_wait_warp(smem_u32(&bars->acc_full[b]), (local >> 1) & 1u, p.fault, p.timeout_ns,
-                          &bars->abort, kFaultTcEpilogueWait, false))
-        break;
-      tc_fence_after();
-      const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * BM;
-      const int col = tn * BN + q * 32 + lane;
-#pragma unroll 1
-      for (int c = 0; c < BM / 64; ++c) {
-        uint32_t r0[32], r1[32];
-        tmem_ld32(t + c * 64, r0);
-        tmem_ld32(t + c * 64 + 32, r1);
-        tmem_ld_wait(r0, r1);
-        if (c == BM / 64 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty[b]));
-        }
-        const int row = tm * BM + c * 64;
-        store_column32<TC>(r0, static_cast<TC*>(p.C), p.ldc, p.M, p.N, row, col, p.alpha, p.beta);
-        store_column32<TC>(r1, static_cast<TC*>(p.C), p.ldc, p.M, p.N, row + 32, col, p.alpha,
-                           p.beta);
-      }
-    }
-  } else {
-    // ------------------------------------------------ conversion of B
-    // Thread t takes 16 columns (t % 8) of rows t / 8 + 16 i of a k-tile.
-    const int t = threadIdx.x - 32 * (2 + kEpiWarps);
-    const int chunk = t & 7;
-    const int row0 = t >> 3;
-    constexpr int kRowsPerPass = kConvThreads / 8;
-    constexpr int kPasses = BK / kRowsPerPass;
-    const int tiles = mx_scale_tiles(p.N);
-    uint32_t it = 0;
+  } else if (warp < kEpiWarp) {
+    // ------------------------------------------------ conversion of B (both CTAs)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+    // Each warp converts every fourth k-tile by itself, so that the four
+    // pay for their waits and fences at the same time: 0.63 us a tile with
+    // all four on one tile, most of it latency.
+    // Lane l takes the 16 columns 16 (l % 4) of the 64-column block
+    // (l / 8) % 2, rows (l / 4) % 2 + 2 (l / 16) + 4 j.  Eight lanes so store
+    // even chunks of one row and of the next, odd one, whose swizzle swaps
+    // even and odd: no bank conflicts.
+    const int v = warp - kConvWarp;
+    const int unit = lane & 3, blk = (lane >> 3) & 1;
+    const int row0 = ((lane >> 2) & 1) + 2 * (lane >> 4);
+    const int column = blk * 64 + unit * 16;
+    uint32_t first = 0;      // ring index of the unit's first k-tile
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      int tn, tm;
-      grouped_tile(u, p.tiles_n, p.tiles_m, p.group, tn, tm);
-      const int col = tn * BN + chunk * 16;
-      for (int kt = 0; kt < nk; ++kt, ++it) {
-        Codes16 c[kPasses];
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int k = kt * BK + row0 + i * kRowsPerPass;
-          c[i].w = make_uint4(0u, 0u, 0u, 0u);
-          c[i].scale = 0u;
-          if (k < p.K && col < p.N) {   // (a row of codes holds whole groups of 16 columns)
-            const unsigned char* src = p.codes + (long long)k * p.ldb;
-            if constexpr (kFmt == GEMM_MXFP4) {
-              const uint2 w = *reinterpret_cast<const uint2*>(src + col / 2);
-              c[i].w.x = w.x;
-              c[i].w.y = w.y;
-            } else {
-              c[i].w = *reinterpret_cast<const uint4*>(src + col);
-            }
-            c[i].scale = p.sb[mx_scale_offset(k, col >> 5, tiles)];
-          }
-        }
-        const uint32_t s = it % S;
-        ok = role_wait_warp(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault,
-                            p.timeout_ns, &bars->abort, kFaultTcProducerWait, true);
+    for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
+      const MxUnit w = mx_unit(u, sc, nk);
+      if (w.row0 >= p.M) continue;
+      for (int kt = w.kb + (int)((v - first) & 3u); kt < w.ke; kt += kConvWarps) {
+        const uint32_t it = first + (uint32_t)(kt - w.kb);
+        const uint32_t r = it % R, s = it % S;
+        ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), (it / R) & 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait);
         if (!ok) break;
-        unsigned char* dst = base + s * kStage + (chunk >> 2) * kBlock;
+        const unsigned char* raw = sraw + r * L::kRawStage;
+        const unsigned char* scales = raw + L::kRaw + ((kt * BK) & 64) / 32 * 4 + (column >> 5);
+        const int rows_left = p.K - kt * BK;
+        auto load = [&](int q, Raw<kFmt>& c) {   // rows 16 q .. 16 q + 15 of the tile
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int r = row0 + i * kRowsPerPass;
-          const float scale = mx_scale_value(c[i].scale);
-          float v[16];
-          if constexpr (kFmt == GEMM_MXFP4) {
-            float lo[8], hi[8];
-            e2m1x8_to_f32(c[i].w.x, lo);
-            e2m1x8_to_f32(c[i].w.y, hi);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = lo[j], v[8 + j] = hi[j];
-          } else {
-            int8x4_to_f32(c[i].w.x, v);
-            int8x4_to_f32(c[i].w.y, v + 4);
-            int8x4_to_f32(c[i].w.z, v + 8);
-            int8x4_to_f32(c[i].w.w, v + 12);
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 16 * q + 4 * i;
+            if constexpr (kFmt == GEMM_MXFP4) {
+              const uint2 x = *reinterpret_cast<const uint2*>(raw + row * L::kRawRow + column / 2);
+              c.w[i][0] = x.x, c.w[i][1] = x.y;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4*>(raw + row * L::kRawRow + column);
+              c.w[i][0] = x.x, c.w[i][1] = x.y, c.w[i][2] = x.z, c.w[i][3] = x.w;
+            }
+            c.s[i] = scales[(row & 31) * 16 + (row >> 5) * 4];
+            // Rows past K: zero codes, and any finite scale.
+            if (row >= rows_left) c.s[i] = 0;
           }
-          uint32_t h[8];
+        };
+        Raw<kFmt> c;
+        load(0, c);
+        ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault,
+                             p.timeout_ns, &bars->abort, kFaultTcProducerWait);
+        if (!ok) break;
+        unsigned char* st = base + s * kStage + blk * kBlock;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = pack2<T>(v[2 * j] * scale, v[2 * j + 1] * scale);
-          const int c0 = (chunk & 3) * 2;
-          *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) =
-              make_uint4(h[4], h[5], h[6], h[7]);
+        for (int q = 0; q < 4; ++q) {
+          Raw<kFmt> next;
+          if (q < 3) load(q + 1, next);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 16 * q + 4 * i;
+            const Scale<T> f(c.s[i]);
+            uint4 lo, hi;
+            if constexpr (kFmt == GEMM_MXFP4) {
+              lo = convert_e2m1x8<T>(c.w[i][0], f);
+              hi = convert_e2m1x8<T>(c.w[i][1], f);
+            } else {
+              const uint2 a = convert_int8x4<T>(c.w[i][0], f), b = convert_int8x4<T>(c.w[i][1], f);
+              const uint2 d = convert_int8x4<T>(c.w[i][2], f), e = convert_int8x4<T>(c.w[i][3], f);
+              lo = make_uint4(a.x, a.y, b.x, b.y);
+              hi = make_uint4(d.x, d.y, e.x, e.y);
+            }
+            unsigned char* dst = st + row * 128;
+            *reinterpret_cast<uint4*>(dst + (((2 * unit) ^ (row & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4*>(dst + (((2 * unit + 1) ^ (row & 7)) << 4)) = hi;
+          }
+          if (q < 3) c = next;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->full[s]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->raw_empty[r]));
+          mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
+        }
+      }
+      first += (uint32_t)(w.ke - w.kb);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (both CTAs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    // Warp: TMEM lanes 32 q .. 32 q + 31 (columns of C), half of the rows.
+    const int q = warp & 3;
+    const int half = (warp - kEpiWarp) >> 2;
+    uint32_t seg = 0;
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
+      const MxUnit w = mx_unit(u, sc, nk);
+      if (w.row0 >= p.M) continue;
+      const int chunks = w.rows / 64;      // of 32 rows, this warp's share
+      const int first = half * (w.rows / 2);
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int k0 = w.kb; k0 < w.ke; k0 += p.seg, ++seg) {
+        const uint32_t b = seg & 1;
+        ok = role_wait_warp(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
+                            &bars->abort, kFaultTcEpilogueWait, false);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256 + first;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < chunks) {
+            uint32_t r[32];
+            tmem_ld32(t + c * 32, r);
+            tmem_ld_wait32(r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c * 32 + j] = acc[c * 32 + j] + __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), 0));
+      }
+      if (!ok) break;
+      const int col = w.tn * 256 + (int)rank * 128 + q * 32 + lane;
+      if (col < p.N) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < chunks) {
+            const int row = w.row0 + first + c * 32;
+            if (sc.slices == 1)
+              store_rows32<TC>(acc + c * 32, static_cast<TC*>(p.C) + (long long)row * p.ldc + col,
+                               p.ldc, p.M - row, p.alpha, p.beta);
+            else
+              store_rows32<float>(acc + c * 32,
+                                  p.ws + ((long long)w.slice * p.M + row) * p.ldw + col, p.ldw,
+                                  p.M - row, 1.f, 0.f);
+          }
+        }
       }
     }
   }
 
   // ------------------------------------------------ teardown
-  tc_fence_before();
+  if (warp == 1 && rank == 0 && lane == 0) {
+    // Every MMA of the pair has completed before TMEM is freed.
+    mma_commit_pair_multicast(smem_u32(&bars->drain), 0x1);
+    if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
+      raise_fault(p.fault, kFaultDrainWait);
+  }
   __syncthreads();
-  if (warp == 0 && lane == 0 && bars->abort) {
-    // Let this CTA's copies in flight land before it exits.  (A stage that
-    // the converting warps left out never completes: the wait then gives up.)
-    const uint32_t first = issued > (uint32_t)S ? issued - S : 0;
+  if ((warp == 2 || (warp == 0 && rank == 0)) && lane == 0 && bars->abort) {
+    // Let the copies in flight land: those of codes on raw_full[], and those
+    // of op(A), both CTAs', on the even one's full[], whose arrivals by
+    // converting warps may be missing; the wait then gives up.
+    const uint32_t n = warp == 2 ? R : S;
+    const uint32_t first = issued > n ? issued - n : 0;
     for (uint32_t it = first; it < issued; ++it) {
-      if (!mbar_wait_bounded(smem_u32(&bars->full[it % S]), (it / S) & 1u, p.timeout_ns,
-                             nullptr)) {
+      const uint64_t* bar = warp == 2 ? &bars->raw_full[it % R] : &bars->full[it % S];
+      if (!mbar_wait_bounded(smem_u32(bar), (it / n) & 1u, p.timeout_ns, nullptr)) {
         raise_fault(p.fault, kFaultDrainWait);
         break;
       }
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves while the pair may still touch its memory
   if (warp == 1) {
     tc_fence_after();
-    if (lane == 0) {
-      mma_commit(smem_u32(&bars->drain));
-      if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
-        raise_fault(p.fault, kFaultDrainWait);
-    }
-    __syncwarp();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, kTmemCols);
   }
 }
 
 template <int kFmt, typename T, typename TC, bool kAT>
-cudaError_t launch_typed(const MxGradParams& p, const CUtensorMap* tmA, int grid,
-                         cudaStream_t stream) {
+cudaError_t launch_typed(const MxGradParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                         int pairs, cudaStream_t stream) {
   auto kernel = mx_grad_kernel<kFmt, T, TC, kAT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // The register split needs kRegsLaunch registers a thread at launch: with
+  // fewer, its setmaxnreg.inc would wait for ever.
+  static const bool fits = [&] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == kRegsLaunch;
+  }();
+  if (!fits) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Layout<kFmt>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_gemm_kernel(kernel, dim3(grid), dim3(kThreads), kSmem, stream, *tmA, p);
+  return launch_gemm_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Layout<kFmt>::kSmem, stream,
+                            *tmA, *tmB, p);
 }
 
 template <int kFmt, typename T>
-cudaError_t launch_fmt(const MxGradParams& p, const CUtensorMap* tmA, int grid, cudaStream_t s) {
+cudaError_t launch_fmt(const MxGradParams& p, const CUtensorMap* a, const CUtensorMap* b,
+                       int pairs, cudaStream_t s) {
   if (p.dtype_c == 0)
-    return p.op_a ? launch_typed<kFmt, T, float, true>(p, tmA, grid, s)
-                  : launch_typed<kFmt, T, float, false>(p, tmA, grid, s);
-  return p.op_a ? launch_typed<kFmt, T, T, true>(p, tmA, grid, s)
-                : launch_typed<kFmt, T, T, false>(p, tmA, grid, s);
+    return p.op_a ? launch_typed<kFmt, T, float, true>(p, a, b, pairs, s)
+                  : launch_typed<kFmt, T, float, false>(p, a, b, pairs, s);
+  return p.op_a ? launch_typed<kFmt, T, T, true>(p, a, b, pairs, s)
+                : launch_typed<kFmt, T, T, false>(p, a, b, pairs, s);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_grad(const MxGradParams& p, const CUtensorMap* tmA, int grid,
-                           cudaStream_t s) {
+cudaError_t launch_mx_grad(const MxGradParams& p, const CUtensorMap* a, const CUtensorMap* b,
+                           int pairs, cudaStream_t s) {
   if (p.dtype == 1)
-    return p.fmt == GEMM_MXFP4 ? launch_fmt<GEMM_MXFP4, __half>(p, tmA, grid, s)
-                               : launch_fmt<GEMM_MXINT8, __half>(p, tmA, grid, s);
-  return p.fmt == GEMM_MXFP4 ? launch_fmt<GEMM_MXFP4, __nv_bfloat16>(p, tmA, grid, s)
-                             : launch_fmt<GEMM_MXINT8, __nv_bfloat16>(p, tmA, grid, s);
+    return p.fmt == GEMM_MXFP4 ? launch_fmt<GEMM_MXFP4, __half>(p, a, b, pairs, s)
+                               : launch_fmt<GEMM_MXINT8, __half>(p, a, b, pairs, s);
+  return p.fmt == GEMM_MXFP4 ? launch_fmt<GEMM_MXFP4, __nv_bfloat16>(p, a, b, pairs, s)
+                             : launch_fmt<GEMM_MXINT8, __nv_bfloat16>(p, a, b, pairs, s);
 }
 
 }  // namespace dgemm
