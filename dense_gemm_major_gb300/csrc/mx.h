@@ -78,8 +78,8 @@ struct MxGradParams {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-constexpr int kMxGradBK = 64;
-// tmA: op(A), boxes of 64 x 64; tmB: the codes as bytes, boxes of 64 rows x
+constexpr int kMxGradBK = 128;
+// tmA: op(A), boxes of 64 x 64; tmB: the codes as bytes, boxes of 128 rows x
 // 128 columns.
 cudaError_t launch_mx_grad(const MxGradParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                            int pairs, cudaStream_t stream);

@@ -386,7 +386,7 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
   p.sb = static_cast<const unsigned char*>(b_scales);
   const int nk = ceil_div(K, dgemm::kMxGradBK);
-  p.sched = schedule(M, N, nk, max_pairs, 8, 8);
+  p.sched = schedule(M, N, nk, max_pairs, 8, 4);
   // FP32 results: at most 1024 terms per sum in tensor memory.
   p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
   if ((st = partials(p.sched, M, N, stream, &p.ws, &p.ldw)) != GEMM_OK) return st;

@@ -14,10 +14,10 @@
 // whatever C's alignment, and B, which costs instructions, is the operand
 // that no CTA touches twice per tile.
 //
-// Roles (512 threads): warp 0 loads op(A) by TMA, warp 1 issues the MMAs
+// Roles (640 threads): warp 0 loads op(A) by TMA, warp 1 issues the MMAs
 // (even CTA), warp 2 loads the codes (TMA) and tiles of scales into a ring of
-// their own, ahead of the MMAs' ring, warps 4-7 convert, warps 8-15 drain the
-// accumulators.
+// their own, ahead of the MMAs' ring, warps 4-11 convert, warps 12-19 drain
+// the accumulators.
 //
 // FP32 sums.  The MMA truncates the running sum at every 16-deep step: over
 // 8192 terms that was measured as a relative error of 6e-6.  For FP32
@@ -30,33 +30,42 @@ namespace dgemm {
 namespace {
 
 constexpr int BK = kMxGradBK;
-constexpr int kThreads = 512;
-constexpr int kConvWarp = 4, kConvWarps = 4;
-constexpr int kEpiWarp = 8, kEpiWarps = 8;
-// Registers per thread: 128 at launch; after the split, 128 threads of loads
-// and MMAs, 128 of conversion, 256 of draining (128 sums and 32 loaded
-// values each): 40 + 88 + 2 * 192 = 4 * 128.
-constexpr int kRegsLaunch = 128, kRegsIssue = 40, kRegsConv = 88, kRegsEpi = 192;
-static_assert(kRegsIssue + kRegsConv + 2 * kRegsEpi <= 4 * kRegsLaunch, "register split");
+constexpr int kThreads = 640;
+constexpr int kConvWarp = 4, kConvGroup = 4;              // two groups of 4 warps
+constexpr int kEpiWarp = 12, kEpiWarps = 8;
+// Registers per thread: 96 at launch; after the split 128 threads of loads
+// and MMAs, 256 of conversion, 256 of draining (128 sums and 16 loaded
+// values each): 32 + 2 * 56 + 2 * 168 = 5 * 96.
+constexpr int kRegsLaunch = 96, kRegsIssue = 32, kRegsConv = 56, kRegsEpi = 168;
+static_assert(kRegsIssue + 2 * kRegsConv + 2 * kRegsEpi <= 5 * kRegsLaunch, "register split");
 
-constexpr uint32_t kBlock = 64 * BK * 2;                  // 64 wide, BK deep: 8 KB
-constexpr uint32_t kConvBytes = 2 * kBlock;               // 128 columns of B
-constexpr uint32_t kABytes = 2 * kBlock;                  // 128 rows of C
-constexpr uint32_t kStage = kConvBytes + kABytes;         // what an MMA step reads
+// A stage is two halves of 64 of K, each with its part of both operands as
+// 64-wide, 128-byte swizzled blocks; one barrier round trip of the MMA
+// issuer covers eight MMAs (with stages of 64 it spent as long on its
+// barriers as on the MMAs: 121 against 88 us at 4096^3).
+constexpr int kHalves = BK / 64;
+constexpr uint32_t kBlock = 64 * 64 * 2;                  // 64 wide, 64 deep: 8 KB
+constexpr uint32_t kConvHalf = 2 * kBlock;                // 128 columns of B
+constexpr uint32_t kAHalf = 2 * kBlock;                   // 128 rows of C
+constexpr uint32_t kConvBytes = kHalves * kConvHalf;
+constexpr uint32_t kABytes = kHalves * kAHalf;
+constexpr uint32_t kStage = kConvBytes + kABytes;         // 64 KB
+constexpr int S = 3;
 constexpr uint32_t kTmemCols = 512;                       // two accumulators
+static_assert(BK == kMxTileRows, "a stage needs one tile of scales per CTA");
+static_assert(kHalves * kConvGroup * 32 == 256, "a converting group per half");
 
 template <int kFmt>
 struct Layout {
   static constexpr uint32_t kRawRow = kFmt == GEMM_MXFP4 ? 64 : 128;   // 128 codes
   static constexpr uint32_t kRaw = kRawRow * BK;
   static constexpr uint32_t kRawStage = kRaw + kMxTileBytes;
-  static constexpr int kStages = kFmt == GEMM_MXFP4 ? 6 : 5;
-  static constexpr int kRawStages = 6;
-  static constexpr uint32_t kSmem = kStages * kStage + kRawStages * kRawStage + 1024 + 512;
+  static constexpr int kRawStages = kFmt == GEMM_MXFP4 ? 3 : 2;
+  static constexpr uint32_t kSmem = S * kStage + kRawStages * kRawStage + 1024 + 512;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-template <int S, int R>
+template <int R>
 struct alignas(8) Barriers {
   uint64_t full[S];       // even CTA: op(A) of both CTAs loaded, both conversions done
   uint64_t empty[S];      // the MMAs on stage s are done
@@ -89,6 +98,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Byte permutation; a selector digit with its top bit set gives the sign of
+// the byte that it selects, eight times.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
 __device__ __forceinline__ uint32_t twice(uint32_t h) { return h | (h << 16); }
@@ -132,25 +148,20 @@ template <typename T>
 __device__ __forceinline__ uint4 convert_e2m1x8(uint32_t w, const Scale<T>& sc) {
   uint32_t r[4];
   if constexpr (__is_same(T, __nv_bfloat16)) {
-    // The magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 have the BF16 bytes
-    // (high) 00 3F 3F 3F 40 40 40 40, (low) 00 00 80 C0 00 40 80 C0: a byte
-    // permutation looks four of them up at a time.  The sign of the even
-    // code of a byte sits at bit 7 after a shift by 4, that of the odd one at
-    // bit 7 as it is.
-    const uint32_t mag = w & 0x77777777u;
-    const uint32_t even = w << 4;
+    // prmt looks up four magnitudes 2 |x| = 0, 1, 2, 3, 4, 6, 8, 12 as bytes
+    // and gives 0 where the selector's (the code's) top bit is set: with the
+    // codes, and with their signs flipped, the positive and the negative
+    // ones.  0xC0 + 2 x is the low byte of 96 + x in BF16 (high byte 0x42).
+    const uint32_t flipped = w ^ 0x88888888u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t sel = h == 0 ? mag : mag >> 16;
-      const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);
-      const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+      const uint32_t pos = prmt(0x03020100u, 0x0C080604u, h == 0 ? w : w >> 16);
+      const uint32_t neg = prmt(0x03020100u, 0x0C080604u, h == 0 ? flipped : flipped >> 16);
+      const uint32_t sum = 0xC0C0C0C0u + pos - neg;   // (no byte carries)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t v = __byte_perm(lo, hi, j == 0 ? 0x5140 : 0x7362);
-        const int byte = 2 * h + j;
-        const uint32_t sign = __byte_perm(even, w, (byte << 4) | ((byte + 4) << 12));
-        r[byte] = sc.times(v) ^ (sign & 0x80008000u);
-      }
+      for (int j = 0; j < 2; ++j)
+        r[2 * h + j] = sc.times(
+            sub_bf16x2(prmt(sum, 0x42424242u, j == 0 ? 0x4140 : 0x4342), 0x42C042C0u));
     }
   } else {
 #pragma unroll
@@ -191,13 +202,6 @@ __device__ __forceinline__ uint2 convert_int8x4(uint32_t w, const Scale<T>& sc) 
   return make_uint2(r[0], r[1]);
 }
 
-// What a converting lane takes at a time: 16 columns of each of 4 rows.
-template <int kFmt>
-struct Raw {
-  uint32_t w[4][kFmt == GEMM_MXFP4 ? 2 : 4];
-  unsigned s[4];
-};
-
 // ------------------------------------------------------------ kernel
 
 template <int kFmt, typename T, typename TC, bool kAT>
@@ -205,12 +209,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx_grad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const MxGradParams p) {
   using L = Layout<kFmt>;
-  constexpr int S = L::kStages, R = L::kRawStages;
+  constexpr int R = L::kRawStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
   unsigned char* const sraw = base + S * kStage;
-  auto* bars = reinterpret_cast<Barriers<S, R>*>(sraw + R * L::kRawStage);
-  static_assert(sizeof(Barriers<S, R>) <= 512, "barrier block must fit its reserved space");
+  auto* bars = reinterpret_cast<Barriers<R>*>(sraw + R * L::kRawStage);
+  static_assert(sizeof(Barriers<R>) <= 512, "barrier block must fit its reserved space");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
@@ -221,12 +225,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&bars->full[s]), 1 + 2);
+      mbar_init(smem_u32(&bars->full[s]), 1 + 2 * kHalves * kConvGroup);
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     for (int r = 0; r < R; ++r) {
       mbar_init(smem_u32(&bars->raw_full[r]), 1);
-      mbar_init(smem_u32(&bars->raw_empty[r]), 1);
+      mbar_init(smem_u32(&bars->raw_empty[r]), kHalves * kConvGroup);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&bars->acc_full[b]), 1);
@@ -269,12 +273,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sa = smem_u32(base + s * kStage) + kConvBytes;
           const uint32_t fb = mapa_shared(smem_u32(&bars->full[s]), 0);
           if (rank == 0)
-            mbar_arrive_expect_tx(smem_u32(&bars->full[s]), 2u * (uint32_t)boxes * kBlock);
-          for (int j = 0; j < boxes; ++j) {
-            if constexpr (kAT)   // stored K x M: rows of C contiguous
-              tma_load_2d_pair(sa + j * kBlock, &tmA, fb, row + j * 64, kt * BK);
-            else
-              tma_load_2d_pair(sa + j * kBlock, &tmA, fb, kt * BK, row + j * 64);
+            mbar_arrive_expect_tx(smem_u32(&bars->full[s]),
+                                  2u * kHalves * (uint32_t)boxes * kBlock);
+          for (int h = 0; h < kHalves; ++h) {
+            const int k = kt * BK + h * 64;
+            for (int j = 0; j < boxes; ++j) {
+              const uint32_t dst = sa + h * kAHalf + j * kBlock;
+              if constexpr (kAT)   // stored K x M: rows of C contiguous
+                tma_load_2d_pair(dst, &tmA, fb, row + j * 64, k);
+              else
+                tma_load_2d_pair(dst, &tmA, fb, k, row + j * 64);
+            }
           }
           issued = it + 1;
         }
@@ -300,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d(raw, &tmB, rb, ct * (int)L::kRawRow, kt * BK);
           if (sbytes != 0)
             bulk_load(raw + L::kRaw,
-                      p.sb + ((long long)(kt * BK / 128) * ktiles + ct) * kMxTileBytes, sbytes, rb);
+                      p.sb + ((long long)kt * ktiles + ct) * kMxTileBytes, sbytes, rb);
           issued = it + 1;
         }
       }
@@ -328,10 +337,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t st = smem_u32(base + s * kStage);
             const uint32_t sa = st + kConvBytes;
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              mma_f16_pair(tmem_base + b * 256, mnmajor_desc(st, k, kBlock),
-                           kAT ? mnmajor_desc(sa, k, kBlock) : kmajor_desc(sa, k), idesc,
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint32_t bh = st + (k >> 2) * kConvHalf, ah = sa + (k >> 2) * kAHalf;
+              mma_f16_pair(tmem_base + b * 256, mnmajor_desc(bh, k & 3, kBlock),
+                           kAT ? mnmajor_desc(ah, k & 3, kBlock) : kmajor_desc(ah, k & 3), idesc,
                            (kt > k0 || k > 0) ? 1u : 0u);
+            }
             mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
           }
           if (!ok) break;
@@ -343,85 +354,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp < kEpiWarp) {
     // ------------------------------------------------ conversion of B (both CTAs)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-    // Each warp converts every fourth k-tile by itself, so that the four
-    // pay for their waits and fences at the same time: 0.63 us a tile with
-    // all four on one tile, most of it latency.
-    // Lane l takes the 16 columns 16 (l % 4) of the 64-column block
-    // (l / 8) % 2, rows (l / 4) % 2 + 2 (l / 16) + 4 j.  Eight lanes so store
-    // even chunks of one row and of the next, odd one, whose swizzle swaps
-    // even and odd: no bank conflicts.
-    const int v = warp - kConvWarp;
+    // A group of 4 warps converts each half of a stage.  Lane l of warp v of
+    // its group takes the 16 columns 16 (l % 4) of the 64-column block
+    // (l / 8) % 2, rows 4 v + (l / 4) % 2 + 2 (l / 16) + 16 i.  Eight lanes so
+    // store even chunks of one row and of the next, odd one, whose swizzle
+    // swaps even and odd: no bank conflicts.
+    const int half = (warp - kConvWarp) / kConvGroup;
+    const int v = (warp - kConvWarp) % kConvGroup;
     const int unit = lane & 3, blk = (lane >> 3) & 1;
-    const int row0 = ((lane >> 2) & 1) + 2 * (lane >> 4);
+    const int row0 = 4 * v + ((lane >> 2) & 1) + 2 * (lane >> 4);
     const int column = blk * 64 + unit * 16;
-    uint32_t first = 0;      // ring index of the unit's first k-tile
+    uint32_t it = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
       const MxUnit w = mx_unit(u, sc, nk);
       if (w.row0 >= p.M) continue;
-      for (int kt = w.kb + (int)((v - first) & 3u); kt < w.ke; kt += kConvWarps) {
-        const uint32_t it = first + (uint32_t)(kt - w.kb);
+      for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
         const uint32_t r = it % R, s = it % S;
         ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), (it / R) & 1u, p.fault, p.timeout_ns,
                              &bars->abort, kFaultTcProducerWait);
         if (!ok) break;
-        const unsigned char* raw = sraw + r * L::kRawStage;
-        const unsigned char* scales = raw + L::kRaw + ((kt * BK) & 64) / 32 * 4 + (column >> 5);
-        const int rows_left = p.K - kt * BK;
-        auto load = [&](int q, Raw<kFmt>& c) {   // rows 16 q .. 16 q + 15 of the tile
+        const unsigned char* raw = sraw + r * L::kRawStage + half * 64 * L::kRawRow;
+        const unsigned char* scales =
+            sraw + r * L::kRawStage + L::kRaw + half * 2 * 4 + (column >> 5);
+        const int rows_left = p.K - kt * BK - half * 64;
+        // All loads before the first store, which the compiler could not
+        // move a load across.
+        uint32_t c[4][kFmt == GEMM_MXFP4 ? 2 : 4];
+        unsigned sb[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = row0 + 16 * q + 4 * i;
-            if constexpr (kFmt == GEMM_MXFP4) {
-              const uint2 x = *reinterpret_cast<const uint2*>(raw + row * L::kRawRow + column / 2);
-              c.w[i][0] = x.x, c.w[i][1] = x.y;
-            } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(raw + row * L::kRawRow + column);
-              c.w[i][0] = x.x, c.w[i][1] = x.y, c.w[i][2] = x.z, c.w[i][3] = x.w;
-            }
-            c.s[i] = scales[(row & 31) * 16 + (row >> 5) * 4];
-            // Rows past K: zero codes, and any finite scale.
-            if (row >= rows_left) c.s[i] = 0;
+        for (int i = 0; i < 4; ++i) {
+          const int row = row0 + 16 * i;
+          if constexpr (kFmt == GEMM_MXFP4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(raw + row * L::kRawRow + column / 2);
+            c[i][0] = x.x, c[i][1] = x.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(raw + row * L::kRawRow + column);
+            c[i][0] = x.x, c[i][1] = x.y, c[i][2] = x.z, c[i][3] = x.w;
           }
-        };
-        Raw<kFmt> c;
-        load(0, c);
+          sb[i] = scales[(row & 31) * 16 + (row >> 5) * 4];
+          // Rows past K: zero codes, and any finite scale.
+          if (row >= rows_left) sb[i] = 0;
+        }
         ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault,
                              p.timeout_ns, &bars->abort, kFaultTcProducerWait);
         if (!ok) break;
-        unsigned char* st = base + s * kStage + blk * kBlock;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
+        unsigned char* st = base + s * kStage + half * kConvHalf + blk * kBlock;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          Raw<kFmt> next;
-          if (q < 3) load(q + 1, next);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = row0 + 16 * q + 4 * i;
-            const Scale<T> f(c.s[i]);
-            uint4 lo, hi;
-            if constexpr (kFmt == GEMM_MXFP4) {
-              lo = convert_e2m1x8<T>(c.w[i][0], f);
-              hi = convert_e2m1x8<T>(c.w[i][1], f);
-            } else {
-              const uint2 a = convert_int8x4<T>(c.w[i][0], f), b = convert_int8x4<T>(c.w[i][1], f);
-              const uint2 d = convert_int8x4<T>(c.w[i][2], f), e = convert_int8x4<T>(c.w[i][3], f);
-              lo = make_uint4(a.x, a.y, b.x, b.y);
-              hi = make_uint4(d.x, d.y, e.x, e.y);
-            }
-            unsigned char* dst = st + row * 128;
-            *reinterpret_cast<uint4*>(dst + (((2 * unit) ^ (row & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(dst + (((2 * unit + 1) ^ (row & 7)) << 4)) = hi;
+        for (int i = 0; i < 4; ++i) {
+          const int row = row0 + 16 * i;
+          const Scale<T> f(sb[i]);
+          uint4 lo, hi;
+          if constexpr (kFmt == GEMM_MXFP4) {
+            lo = convert_e2m1x8<T>(c[i][0], f);
+            hi = convert_e2m1x8<T>(c[i][1], f);
+          } else {
+            const uint2 a = convert_int8x4<T>(c[i][0], f), b = convert_int8x4<T>(c[i][1], f);
+            const uint2 d = convert_int8x4<T>(c[i][2], f), e = convert_int8x4<T>(c[i][3], f);
+            lo = make_uint4(a.x, a.y, b.x, b.y);
+            hi = make_uint4(d.x, d.y, e.x, e.y);
           }
-          if (q < 3) c = next;
+          unsigned char* dst = st + row * 128;
+          *reinterpret_cast<uint4*>(dst + (((2 * unit) ^ (row & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(dst + (((2 * unit + 1) ^ (row & 7)) << 4)) = hi;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars->raw_empty[r]));
-          mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
-        }
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
       }
-      first += (uint32_t)(w.ke - w.kb);
     }
     __syncwarp();
   } else {
@@ -448,13 +450,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256 + first;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < chunks) {
-            uint32_t r[32];
-            tmem_ld32(t + c * 32, r);
-            tmem_ld_wait32(r);
+        for (int c = 0; c < 8; ++c) {
+          if (c < 2 * chunks) {
+            uint32_t r[16];
+            tmem_ld16(t + c * 16, r);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c * 32 + j] = acc[c * 32 + j] + __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __uint_as_float(r[j]);
           }
         }
         tc_fence_before();
