@@ -449,113 +449,160 @@ def matmul(A, B, out=None, stream=None, alpha=1.0, beta=0.0):
 
 
 # ------------------------------------------------------------ microscaled operands
+#
+# A layer of a few tokens takes a few microseconds on the GPU, less than a
+# careless wrapper on the CPU: these look each tensor property up once, and
+# torch itself once per process.
+
+_torch = None
+_TORCH_CODES = {}    # torch dtype -> dtype code
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _TORCH_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+        load()
+        _torch = torch
+    return _torch
+
+
+def _dtype_code(dtype):
+    code = _TORCH_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}: float32, float16 or bfloat16")
+    return code
+
+
+def _stream_of(stream, device):
+    """The given cudaStream_t, or torch's current stream on `device`."""
+    return stream if stream is not None else _torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _not_cuda():
+    raise ValueError("operands must be CUDA tensors")
+
 
 class MXTensor:
     """A quantised rows x cols array on the GPU: ``codes`` (uint8, rows x
     pitch) and ``scales`` (uint8) in the layout that include/dense_gemm_mx.h
     describes; ``fmt`` is "mxfp4" or "mxint8"."""
-    __slots__ = ("codes", "scales", "cols", "fmt")
+    __slots__ = ("_codes", "_scales", "_buffer", "rows", "cols", "fmt", "_ld")
 
     def __init__(self, codes, scales, cols, fmt="mxfp4"):
-        if fmt not in ("mxfp4", "mxint8"):
+        if fmt == "mxfp4":
+            width = (cols + 1) >> 1
+        elif fmt == "mxint8":
+            width = cols
+        else:
             raise ValueError("fmt must be 'mxfp4' or 'mxint8'")
         rows, pitch = codes.shape
-        width = (cols + 1) // 2 if fmt == "mxfp4" else cols
-        if pitch < width or codes.stride(1) != 1 or codes.element_size() != 1:
+        ld, unit = codes.stride()
+        if pitch < width or (unit != 1 and pitch > 1) or codes.element_size() != 1:
             raise ValueError("codes must be rows of at least the format's bytes for cols")
-        tiles = ((rows + 127) // 128) * ((cols + 127) // 128)
-        if scales.numel() < 512 * tiles or scales.element_size() != 1 \
-                or not scales.is_contiguous():
+        if scales.numel() < 512 * ((rows + 127) >> 7) * ((cols + 127) >> 7) \
+                or scales.element_size() != 1 or not scales.is_contiguous():
             raise ValueError("scales must be contiguous, 512 bytes for each 128 x 128 tile")
-        self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, fmt
+        self._codes, self._scales, self._buffer = codes, scales, None
+        self.rows, self.cols, self.fmt = rows, cols, fmt
+        # (The pitch of a single row is free: its padded width.)
+        self._ld = ld if rows > 1 else (pitch + 15) & ~15
 
     @property
     def shape(self):
-        return (self.codes.shape[0], self.cols)
+        return (self.rows, self.cols)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buffer[:self.rows * self._ld].view(self.rows, self._ld)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buffer[self.rows * self._ld:]
+        return self._scales
 
     @property
     def device(self):
-        return self.codes.device
+        return (self._codes if self._buffer is None else self._buffer).device
 
-    def _ld(self):
-        """Row pitch of the codes; a single row's may be its padded width."""
-        rows, pitch = self.codes.shape
-        return self.codes.stride(0) if rows > 1 else (pitch + 15) // 16 * 16
-
-
-_TORCH_CODES = {}
-
-
-def _dtype_code(dtype):
-    if not _TORCH_CODES:
-        import torch
-        _TORCH_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    try:
-        return _TORCH_CODES[dtype]
-    except KeyError:
-        raise ValueError(f"unsupported dtype {dtype}: float32, float16 or bfloat16") from None
+    def _pointers(self):
+        """Device addresses of codes and scales."""
+        if self._buffer is not None:
+            p = self._buffer.data_ptr()
+            return p, p + self.rows * self._ld
+        if not self._codes.is_cuda:
+            _not_cuda()
+        return self._codes.data_ptr(), self._scales.data_ptr()
 
 
-def _raw_stream(stream, device):
-    import torch
-    if stream is not None:
-        return stream
-    return torch.cuda.current_stream(device).cuda_stream
+def _rows_ld(t, rows, cols):
+    """Leading dimension of a row-major rows x cols tensor."""
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError("operands must be 2-D row-major (unit column stride)")
+    return s0 if rows > 1 else max(cols, 1)
 
 
-def _on_gpu(*tensors):
-    for t in tensors:
-        if t.device.type != "cuda":
-            raise ValueError("operands must be CUDA tensors")
-
-
-def _result(out, shape, dtype, device, beta):
-    import torch
+def _result(out, M, N, dtype, device, beta=0.0):
     if out is None:
         if beta != 0:
             raise ValueError("beta != 0 needs an existing out")
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        return _torch.empty((M, N), dtype=dtype, device=device), (N if N > 0 else 1)
+    if tuple(out.shape) != (M, N) or out.dtype != dtype or out.device != device:
         raise ValueError("out has the wrong shape, dtype or device")
-    return out
+    return out, _rows_ld(out, M, N)
 
 
 def mx_quantize(X, fmt="mxfp4", stream=None):
     """X (rows x cols; float32, float16 or bfloat16; row-major or a
     transposed view, read in place) in format ``fmt``: blocks of 32 along
     the columns.  Returns an MXTensor."""
-    import torch
-    _on_gpu(X)
-    code = _dtype_code(X.dtype)
-    if fmt not in ("mxfp4", "mxint8"):
+    torch = _torch or _get_torch()
+    if fmt != "mxfp4" and fmt != "mxint8":
         raise ValueError("fmt must be 'mxfp4' or 'mxint8'")
+    if not X.is_cuda:
+        _not_cuda()
+    code = _dtype_code(X.dtype)
     R, K = X.shape
-    op, ldx = _operand(X, R, K)
-    lib = load()
-    f = _MX_CODES[fmt]
-    ldq = lib.gemm_mx_code_ld(f, K)
-    codes = torch.empty((R, ldq), dtype=torch.uint8, device=X.device)
-    scales = torch.empty(lib.gemm_mx_scale_bytes(R, K), dtype=torch.uint8, device=X.device)
-    st = lib.gemm_mx_quantize(f, code, op, R, K, X.data_ptr(), ldx, codes.data_ptr(), ldq,
-                              scales.data_ptr(), _raw_stream(stream, X.device))
+    s0, s1 = X.stride()
+    if s1 == 1 or K <= 1:
+        op, ldx = OP_N, (s0 if R > 1 else max(K, 1))
+    elif s0 == 1 or R <= 1:
+        op, ldx = OP_T, s1
+    else:
+        raise ValueError("operands must have a unit row or column stride")
+    q = MXTensor.__new__(MXTensor)
+    q._codes = q._scales = None
+    q.rows, q.cols, q.fmt = R, K, fmt
+    ldq = q._ld = ((K if fmt == "mxint8" else (K + 1) >> 1) + 15) & ~15
+    codes = R * ldq
+    device = X.device
+    q._buffer = torch.empty(codes + 512 * ((R + 127) >> 7) * ((K + 127) >> 7), dtype=torch.uint8,
+                            device=device)
+    p = q._buffer.data_ptr()
+    st = _lib.gemm_mx_quantize(_MX_CODES[fmt], code, op, R, K, X.data_ptr(), ldx, p, ldq, p + codes,
+                               _stream_of(stream, device))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mx_quantize")
-    return MXTensor(codes, scales, K, fmt)
+    return q
 
 
 def mx_dequantize(q, dtype=None, out=None, stream=None):
     """The values of MXTensor ``q`` as a rows x cols tensor of ``dtype``
     (default bfloat16, or that of ``out``)."""
-    import torch
-    _on_gpu(q)
-    R, K = q.shape
+    torch = _torch or _get_torch()
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     code = _dtype_code(dtype)
-    Y = _result(out, (R, K), dtype, q.device, 0)
-    st = load().gemm_mx_dequantize(_MX_CODES[q.fmt], code, R, K, q.codes.data_ptr(), q._ld(),
-                                   q.scales.data_ptr(), Y.data_ptr(), _ld(Y, R, K),
-                                   _raw_stream(stream, q.device))
+    codes, scales = q._pointers()
+    device = q.device
+    Y, ldy = _result(out, q.rows, q.cols, dtype, device)
+    st = _lib.gemm_mx_dequantize(_MX_CODES[q.fmt], code, q.rows, q.cols, codes, q._ld, scales,
+                                 Y.data_ptr(), ldy, _stream_of(stream, device))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mx_dequantize")
     return Y
@@ -565,21 +612,21 @@ def mx_matmul(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     """alpha * (A @ B.T) + beta * out for MXFP4 operands A (M x K) and B
     (N x K); the result is of ``dtype`` (default bfloat16, or that of
     ``out``)."""
-    import torch
-    _on_gpu(A, B)
+    torch = _torch or _get_torch()
     if A.fmt != "mxfp4" or B.fmt != "mxfp4":
         raise ValueError("mx_matmul takes mxfp4 operands")
-    M, K = A.shape
-    N, K2 = B.shape
-    if K != K2:
-        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if A.cols != B.cols:
+        raise ValueError(f"inner dimensions differ: {A.cols} vs {B.cols}")
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     code = _dtype_code(dtype)
-    C = _result(out, (M, N), dtype, A.device, beta)
-    st = load().gemm_mx4(code, M, N, K, float(alpha), A.codes.data_ptr(), A._ld(),
-                         A.scales.data_ptr(), B.codes.data_ptr(), B._ld(), B.scales.data_ptr(),
-                         float(beta), C.data_ptr(), _ld(C, M, N), _raw_stream(stream, A.device))
+    pa, sa = A._pointers()
+    pb, sb = B._pointers()
+    device = A.device
+    M, N = A.rows, B.rows
+    C, ldc = _result(out, M, N, dtype, device, beta)
+    st = _lib.gemm_mx4(code, M, N, A.cols, alpha, pa, A._ld, sa, pb, B._ld, sb, beta, C.data_ptr(),
+                       ldc, _stream_of(stream, device))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mx4")
     return C
@@ -588,33 +635,25 @@ def mx_matmul(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
 def mx_linear(x, W, out=None, stream=None):
     """x @ W.T with x (M x K) quantised to MXFP4 on the way and W (N x K) an
     MXFP4 MXTensor; the result has x's dtype."""
-    _on_gpu(x, W)
-    code = _dtype_code(x.dtype)
+    _torch or _get_torch()
+    if not x.is_cuda:
+        _not_cuda()
+    dtype = x.dtype
+    code = _dtype_code(dtype)
     if W.fmt != "mxfp4":
         raise ValueError("mx_linear takes mxfp4 weights")
     M, K = x.shape
-    N, K2 = W.shape
-    if K != K2:
-        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    Y = _result(out, (M, N), x.dtype, x.device, 0)
-    st = load().gemm_mx4_linear(code, M, N, K, x.data_ptr(), _ld(x, M, K), W.codes.data_ptr(),
-                                W._ld(), W.scales.data_ptr(), Y.data_ptr(), _ld(Y, M, N),
-                                _raw_stream(stream, x.device))
+    if K != W.cols:
+        raise ValueError(f"inner dimensions differ: {K} vs {W.cols}")
+    codes, scales = W._pointers()
+    device = x.device
+    N = W.rows
+    Y, ldy = _result(out, M, N, dtype, device)
+    st = _lib.gemm_mx4_linear(code, M, N, K, x.data_ptr(), _rows_ld(x, M, K), codes, W._ld, scales,
+                              Y.data_ptr(), ldy, _stream_of(stream, device))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mx4_linear")
     return Y
-
-
-def _operand_rows16(A, M, K):
-    """_operand for a 16-bit operand whose leading dimension must be a
-    multiple of 8: that of a single stored row is free, so it is rounded up,
-    and a single column with unit stride is a single row stored transposed."""
-    if K == 1 and M > 1 and A.stride(0) == 1:
-        return OP_T, (M + 7) // 8 * 8
-    op, ld = _operand(A, M, K)
-    if (M if op == OP_N else K) <= 1:
-        ld = ((K if op == OP_N else M) + 7) // 8 * 8
-    return op, ld
 
 
 def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
@@ -623,25 +662,37 @@ def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     is the gradient of a layer's input, ``mx_grad(dY.t(), kept_x)`` that of
     its weights.  The result is of A's dtype or float32 (``dtype``, or that
     of ``out``)."""
-    import torch
-    _on_gpu(A, B)
-    code = _dtype_code(A.dtype)
+    torch = _torch or _get_torch()
+    if not A.is_cuda:
+        _not_cuda()
+    ta = A.dtype
+    code = _dtype_code(ta)
     if code == 0:
         raise ValueError("mx_grad takes a float16 or bfloat16 A")
     M, K = A.shape
-    K2, N = B.shape
-    if K != K2:
-        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if K != B.rows:
+        raise ValueError(f"inner dimensions differ: {K} vs {B.rows}")
     if dtype is None:
-        dtype = A.dtype if out is None else out.dtype
-    if dtype != A.dtype and dtype != torch.float32:
+        dtype = ta if out is None else out.dtype
+    if dtype != ta and dtype != torch.float32:
         raise ValueError("the result is of A's dtype or float32")
-    op, lda = _operand_rows16(A, M, K)
-    C = _result(out, (M, N), dtype, A.device, beta)
-    st = load().gemm_mx_grad(_MX_CODES[B.fmt], code, op, _dtype_code(dtype), M, N, K,
-                             float(alpha), A.data_ptr(), lda, B.codes.data_ptr(), B._ld(),
-                             B.scales.data_ptr(), float(beta), C.data_ptr(), _ld(C, M, N),
-                             _raw_stream(stream, A.device))
+    # The leading dimension (a multiple of 8) of a single stored row is free,
+    # so it is rounded up; a single column with unit stride is a single row
+    # stored transposed.
+    s0, s1 = A.stride()
+    if (s1 == 1 or K <= 1) and not (K == 1 and M > 1 and s0 == 1):
+        op, lda = OP_N, (s0 if M > 1 else (K + 7) & ~7)
+    elif s0 == 1 or M <= 1:
+        op, lda = OP_T, (s1 if K > 1 else (M + 7) & ~7)
+    else:
+        raise ValueError("operands must have a unit row or column stride")
+    codes, scales = B._pointers()
+    device = A.device
+    N = B.cols
+    C, ldc = _result(out, M, N, dtype, device, beta)
+    st = _lib.gemm_mx_grad(_MX_CODES[B.fmt], code, op, _TORCH_CODES[dtype], M, N, K, alpha,
+                           A.data_ptr(), lda, codes, B._ld, scales, beta, C.data_ptr(), ldc,
+                           _stream_of(stream, device))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_mx_grad")
     return C

@@ -2,6 +2,7 @@
 // functions, called by mx_api.cu.  Callers use include/dense_gemm_mx.h.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -20,6 +21,20 @@ __host__ __device__ inline int mx_blocks(int K) { return (K + kMxBlock - 1) / kM
 // Tiles of scales along a row of K columns.
 __host__ __device__ inline int mx_scale_tiles(int K) {
   return (mx_blocks(K) + kMxTileBlocks - 1) / kMxTileBlocks;
+}
+
+// Dynamic shared memory of `kernel`, allowed once per device: `done` (a static
+// of the caller) has a bit per device.
+template <typename... Params>
+cudaError_t mx_allow_smem(void (*kernel)(Params...), int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit & done->load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Quantisation; the arguments of gemm_mx_quantize, checked.
@@ -62,6 +77,37 @@ constexpr int kMx4BK = 256;           // 128 bytes of codes
 cudaError_t launch_mx4(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                        const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
                        cudaStream_t stream);
+
+// C := alpha * A . B^T + beta * C for up to 128 rows of A, which are given in
+// MXFP4 (tmA, sa) or, up to 48, as an array X of dtype that the kernel
+// quantises.
+struct Mx4FewParams {
+  int M, N, K;
+  const void* X;              // null: A in MXFP4
+  long long ldx;
+  bool vec;                   // rows of X are 16-byte aligned
+  const unsigned char* sa;    // scales of A and B
+  const unsigned char* sb;
+  int split;                  // CTAs (a cluster) that share a tile's K
+  float alpha, beta;
+  void* C;
+  long long ldc;
+  int dtype;                  // of C (and X)
+  unsigned* fault;
+  unsigned long long timeout_ns;
+};
+constexpr int kMx4FewRows = 128;
+// Quantising inside the kernel saves a launch (2.7 us of a calling thread)
+// but is done anew by the CTAs of every 128 columns: on the GPU, N = K = 4096,
+// inside / before the kernel: 1 row 5.3 / 6.0 us, 16 7.6 / 6.8, 33 9.3 / 8.1,
+// 48 10.6 / 8.7, 64 12.5 / 9.5, against some 11 us of CPU for two launches.
+constexpr int kMx4FewRawRows = 48;
+// Rows of A that the kernel computes for M of them.
+inline int mx4_few_tile(int M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+// tmA: A's codes as bytes, boxes of 128 bytes x mx4_few_tile(M) rows; tmB:
+// B's, boxes of 128 bytes x 128 rows.
+cudaError_t launch_mx4_few(const Mx4FewParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                           cudaStream_t stream);
 
 // C := alpha * op(A) . B + beta * C, B quantised (K x N).
 struct MxGradParams {

@@ -195,10 +195,43 @@ gemm_status_t partials(const dgemm::MxSchedule& sc, int M, int N, cudaStream_t s
   return st;
 }
 
+// The product of checked operands, 0 < M <= kMx4FewRows, N, K > 0; A is X,
+// unquantised, or a.
+gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X, long long ldx,
+                      const void* a, long long lda, const void* sa, const void* b, long long ldb,
+                      const void* sb, float beta, void* C, int ldc, unsigned* fault,
+                      int max_pairs, cudaStream_t stream) {
+  alignas(64) CUtensorMap tmA{}, tmB;
+  const uint64_t width = (uint64_t)code_bytes(GEMM_MXFP4, K);
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!encode_2d(&tmB, u8, b, width, (uint64_t)N, (uint64_t)ldb, 128, 128) ||
+      (X == nullptr && !encode_2d(&tmA, u8, a, width, (uint64_t)M, (uint64_t)lda, 128,
+                                  (uint32_t)dgemm::mx4_few_tile(M))))
+    return GEMM_ERR_LAUNCH;
+  dgemm::Mx4FewParams p;
+  p.M = M, p.N = N, p.K = K;
+  p.X = X, p.ldx = ldx;
+  p.vec = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
+  p.sa = static_cast<const unsigned char*>(sa);
+  p.sb = static_cast<const unsigned char*>(sb);
+  // As many CTAs (2, 4 or 8 of a cluster) to a tile's K as keep one wave,
+  // each with a stage at least.
+  p.split = 1;
+  const int tiles = ceil_div(N, 128), nk = ceil_div(K, dgemm::kMx4BK);
+  while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= 2 * max_pairs) p.split *= 2;
+  p.alpha = alpha, p.beta = beta;
+  p.C = C, p.ldc = ldc, p.dtype = dtype;
+  p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
+  return status_of(dgemm::launch_mx4_few(p, &tmA, &tmB, stream));
+}
+
 // The product of checked operands, M, N, K > 0.
 gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a, long long lda,
                       const void* sa, const void* b, long long ldb, const void* sb, float beta,
                       void* C, int ldc, unsigned* fault, int max_pairs, cudaStream_t stream) {
+  if (M <= dgemm::kMx4FewRows)
+    return run_few(dtype, M, N, K, alpha, nullptr, 0, a, lda, sa, b, ldb, sb, beta, C, ldc, fault,
+                   max_pairs, stream);
   alignas(64) CUtensorMap tmA, tmB, tmSA, tmSB;
   const uint64_t width = (uint64_t)code_bytes(GEMM_MXFP4, K);
   const uint64_t srow = (uint64_t)dgemm::mx_scale_tiles(K) * dgemm::kMxTileBytes;
@@ -332,6 +365,9 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int
   int max_pairs;
   if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (K == 0) return scale_only(dtype, M, N, 0.f, Y, ldy, stream);
+  if (M <= dgemm::kMx4FewRawRows)
+    return run_few(dtype, M, N, K, 1.f, X, ldx, nullptr, 0, nullptr, w_codes, ldw, w_scales, 0.f,
+                   Y, ldy, fault, max_pairs, stream);
   const int ldq = code_ld(GEMM_MXFP4, K);
   const size_t code_size = ((size_t)M * ldq + 255) / 256 * 256;
   unsigned char* ws = nullptr;

@@ -1,0 +1,346 @@
+// C = alpha * A . B^T + beta * C for up to 128 rows of A (decoding, small
+// batches), B (N x K) in MXFP4; A either in MXFP4 or, up to 48 rows, a 16- or
+// 32-bit array that is quantised to MXFP4 on the way, in the same launch.
+//
+// What bounds it is reading B once (N K 17 / 32 bytes) and, for a few rows,
+// latency.  B's rows are the M side of tcgen05.mma.kind::mxf4 (128 columns of
+// C per CTA) and A's its N side (16 to 128), so that no tile is wasted on
+// rows that do not exist.  So that B's bytes travel to all SMs at once, the
+// CTAs of a cluster share a tile's K; they add their FP32 partial tiles
+// through distributed shared memory in rank order, so results are
+// reproducible and there is no workspace and no second launch.
+//
+// Roles (320 threads): warp 0 loads codes (TMA) and scales (bulk copies),
+// warp 1 issues scale copies and MMAs, warps 2-9 quantise A where it comes
+// unquantised, and warps 2-5 then drain the accumulator.
+#include "mx.cuh"
+
+namespace dgemm {
+namespace {
+
+constexpr int BN = 128, BK = 256;
+constexpr int kThreads = 320;
+constexpr int kWorkWarp = 2;
+constexpr int kChunks = BK / 128;                        // scale tiles along K per stage
+constexpr uint32_t kBBytes = BN * BK / 2;                // 16 KB
+constexpr uint32_t kSBytes = kChunks * kMxTileBytes;     // 1 KB
+
+// MT: rows of A that the MMA computes.
+template <int MT>
+struct Layout {
+  static constexpr int kStages = MT <= 64 ? 8 : 6;
+  // The quantising warps work in groups, each on stages of its own: with few
+  // rows a warp per stage, so that all stages' loads of A are in flight at
+  // once.  Stages are a multiple of groups: a slot's stages all fall to one
+  // group, which therefore never waits for a phase whose predecessor it has
+  // not seen.
+  static constexpr int kGroups = MT <= 16 ? 8 : 4;
+  static constexpr int kGroupWarps = 8 / kGroups;
+  static_assert(MT > 64 || kStages % kGroups == 0, "one group per slot");
+  static constexpr uint32_t kABytes = MT * BK / 2;
+  static constexpr uint32_t kStage = (kBBytes + kABytes + 2 * kSBytes + 1023) / 1024 * 1024;
+  static constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;
+  static constexpr uint32_t kScaleCol = MT;              // TMEM: accumulator, then scales of
+  static constexpr uint32_t kTmemCols = MT <= 32 ? 64 : (MT <= 64 ? 128 : 256);   // two stages
+  static_assert(kScaleCol + 4 * 4 * kChunks <= kTmemCols, "tensor memory");
+  static_assert(MT * BN * 4 <= kStages * kStage, "partial tiles reuse the ring");
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <int S>
+struct alignas(8) Barriers {
+  uint64_t full[S];     // loaded, and A quantised
+  uint64_t empty[S];
+  uint64_t acc_full;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// 64-deep block-scaled MMA step, and the copy of a 512-byte tile of scales
+// to 4 TMEM columns (all four lane quarters), on one CTA.
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// One element of C.
+template <typename T>
+__device__ __forceinline__ void store_scaled(T* c, float sum, float alpha, float beta) {
+  float v = alpha * sum;
+  if (beta != 0.f) v = fmaf(beta, to_f32_any<T>(*c), v);
+  *c = from_f32_any<T>(v);
+}
+
+// kRaw: A is p.X, an array of T.
+template <int MT, typename T, bool kRaw>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx4_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const Mx4FewParams p) {
+  using L = Layout<MT>;
+  constexpr int S = L::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const base = align_smem_1024(smem_raw);
+  auto* bars = reinterpret_cast<Barriers<S>*>(base + S * L::kStage);
+  static_assert(sizeof(Barriers<S>) <= 256, "barrier block must fit its reserved space");
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tn = blockIdx.x / p.split;
+  const int rank = blockIdx.x - tn * p.split;
+  const int nk = (p.K + BK - 1) / BK;
+  const int kb = (int)((long long)rank * nk / p.split);
+  const int ke = (int)((long long)(rank + 1) * nk / p.split);
+  const int ktiles = mx_scale_tiles(p.K);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), 1 + (kRaw ? L::kGroupWarps : 0));
+      mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&bars->acc_full), 1);
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    if (!kRaw) tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), L::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_base;
+  wait_prior_grids();
+  allow_dependent_grids();
+
+  uint32_t issued = 0;
+  if (warp == 0) {
+    // ------------------------------------------------ loads
+    if (lane == 0) {
+      for (int kt = kb; kt < ke; ++kt) {
+        const uint32_t it = (uint32_t)(kt - kb), s = it % S;
+        if (!role_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
+                       &bars->abort, kFaultTcProducerWait, true))
+          break;
+        const uint32_t fb = smem_u32(&bars->full[s]);
+        const uint32_t st = smem_u32(base + s * L::kStage);
+        const uint32_t sbytes = (uint32_t)min(kChunks, ktiles - kt * kChunks) * kMxTileBytes;
+        const uint32_t ss = st + kBBytes + L::kABytes;
+        mbar_arrive_expect_tx(fb, kBBytes + sbytes + (kRaw ? 0u : L::kABytes + sbytes));
+        tma_load_2d(st, &tmB, fb, kt * (BK / 2), tn * BN);
+        const long long col = (long long)kt * kChunks;
+        bulk_load(ss, p.sb + ((long long)tn * ktiles + col) * kMxTileBytes, sbytes, fb);
+        if constexpr (!kRaw) {
+          tma_load_2d(st + kBBytes, &tmA, fb, kt * (BK / 2), 0);
+          bulk_load(ss + kSBytes, p.sa + col * kMxTileBytes, sbytes, fb);
+        }
+        issued = it + 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      for (int kt = kb; kt < ke; ++kt) {
+        const uint32_t it = (uint32_t)(kt - kb), s = it % S;
+        ok = role_wait(smem_u32(&bars->full[s]), (it / S) & 1u, p.fault, p.timeout_ns,
+                       &bars->abort, kFaultTcMmaWait, true);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(base + s * L::kStage);
+        const uint32_t sx = st + kBBytes, ss = sx + L::kABytes;
+        const uint32_t sfw = tmem_base + L::kScaleCol + (it & 1u) * 8 * kChunks;
+        const uint32_t sfx = sfw + 4 * kChunks;
+        const int chunks = min(kChunks, ktiles - kt * kChunks);
+        for (int c = 0; c < chunks; ++c) {
+          copy_scales(sfw + 4 * c, smem_desc_plain(ss + c * kMxTileBytes, 128));
+          copy_scales(sfx + 4 * c, smem_desc_plain(ss + kSBytes + c * kMxTileBytes, 128));
+        }
+#pragma unroll
+        for (int k = 0; k < BK / 64; ++k)
+          if (k < 2 * chunks)
+            mma_mx4(tmem_base, kmajor_desc(st, k), kmajor_desc(sx, k),
+                    instr_desc_mx4(BN, MT, (k & 1) * 2), sfw + 4 * (k >> 1), sfx + 4 * (k >> 1),
+                    (kt > kb || k > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&bars->empty[s]));
+      }
+      if (ok) mma_commit(smem_u32(&bars->acc_full));
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ quantisation, then the epilogue
+    const int v = (warp - kWorkWarp) % L::kGroupWarps;
+    bool ok = true;
+    for (int kt = kb + (warp - kWorkWarp) / L::kGroupWarps; kRaw && kt < ke; kt += L::kGroups) {
+      const uint32_t it = (uint32_t)(kt - kb), s = it % S;
+      ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcProducerWait);
+      if (!ok) break;
+      unsigned char* sx = base + s * L::kStage + kBBytes;
+      unsigned char* ss = sx + L::kABytes + kSBytes;
+      // A lane takes whole blocks: 8 of a row per stage, 16 bytes of codes
+      // each, which is one chunk of the swizzled row.  (Four lanes to a block,
+      // as in the kernel that only quantises, took 4 to 8 % longer.  Rows past
+      // M stay as they are: they only reach columns of the accumulator that
+      // are not stored.)
+#pragma unroll 2
+      for (int i = v * 32 + lane; i < 8 * p.M; i += 32 * L::kGroupWarps) {
+        const int m = i >> 3, b = i & 7;
+        const int k0 = kt * BK + b * kMxBlock;
+        const T* src = static_cast<const T*>(p.X) + (long long)m * p.ldx + k0;
+        float x[4][8];
+        if (p.vec && k0 + kMxBlock <= p.K) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) load8<T>(src + 8 * g, x[g]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j >> 3][j & 7] = k0 + j < p.K ? to_f32_any<T>(src[j]) : 0.f;
+        }
+        unsigned amax = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) amax = max(amax, abs_bits(x[j >> 3][j & 7]));
+        const unsigned sb = mx_scale_byte<GEMM_MXFP4>(amax);
+        const float inv = mx_inverse_scale(sb);
+        unsigned q[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[g][j] = sb == 255u ? 0.f : x[g][j] * inv;
+          q[g] = e2m1x8(x[g]);
+        }
+        *reinterpret_cast<uint4*>(sx + m * 128 + ((b ^ (m & 7)) << 4)) =
+            make_uint4(q[0], q[1], q[2], q[3]);
+        ss[(b >> 2) * kMxTileBytes + (m & 31) * 16 + (m >> 5) * 4 + (b & 3)] = (unsigned char)sb;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->full[s]));
+    }
+    if (warp < kWorkWarp + 4) {
+      const int q = warp & 3;
+      if (ke > kb)
+        ok = ok && role_wait_warp(smem_u32(&bars->acc_full), 0, p.fault, p.timeout_ns,
+                                  &bars->abort, kFaultTcEpilogueWait, true);
+      tc_fence_after();
+      const int col = q * 32 + lane;           // within the tile
+#pragma unroll 1
+      for (int c = 0; c < MT / 16; ++c) {
+        if (c * 16 >= p.M) break;
+        uint32_t r[16];
+        tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c * 16, r);
+        if (p.split > 1) {
+            // The partial tile, row-major, where the ring was.
+          float* part = reinterpret_cast<float*>(base) + c * 16 * BN + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[j * BN] = ke > kb ? __uint_as_float(r[j]) : 0.f;
+        } else if (tn * BN + col < p.N) {
+          T* y = static_cast<T*>(p.C) + (long long)(c * 16) * p.ldc + tn * BN + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c * 16 + j < p.M)
+              store_scaled<T>(y + j * p.ldc, __uint_as_float(r[j]), p.alpha, p.beta);
+        }
+      }
+    }
+  }
+  if (p.split > 1) {
+    // ------------------------------------------------ sum of the cluster's partial tiles
+    cluster_sync_all();
+    const int share = BN / p.split;            // columns of C that this CTA adds up
+    for (int i = threadIdx.x; i < share * p.M; i += kThreads) {
+      const int m = i / share;
+      const int col = rank * share + (i - m * share);
+      const uint32_t at = smem_u32(base) + (uint32_t)(m * BN + col) * 4u;
+      float sum = ld_cluster_f32(mapa_shared(at, 0));
+      for (int r = 1; r < p.split; ++r) sum += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
+      if (tn * BN + col < p.N)
+        store_scaled<T>(static_cast<T*>(p.C) + (long long)m * p.ldc + tn * BN + col, sum, p.alpha,
+                        p.beta);
+    }
+    cluster_sync_all();   // no CTA leaves while others read its partial tile
+  }
+
+  // ------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0 && lane == 0 && bars->abort) {
+    // Let this CTA's copies in flight land before it exits.
+    const uint32_t first = issued > (uint32_t)S ? issued - S : 0;
+    for (uint32_t it = first; it < issued; ++it) {
+      if (!mbar_wait_bounded(smem_u32(&bars->full[it % S]), (it / S) & 1u, p.timeout_ns,
+                             nullptr)) {
+        raise_fault(p.fault, kFaultDrainWait);
+        break;
+      }
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    if (lane == 0 && bars->abort) {
+      // (Otherwise acc_full has shown every MMA to be done.)
+      mma_commit(smem_u32(&bars->drain));
+      if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
+        raise_fault(p.fault, kFaultDrainWait);
+    }
+    __syncwarp();
+    tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+}
+
+template <int MT, typename T, bool kRaw>
+cudaError_t launch_typed(const Mx4FewParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                         cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = mx_allow_smem(mx4_few_kernel<MT, T, kRaw>, Layout<MT>::kSmem, &done);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.N + BN - 1) / BN;
+  return launch_gemm_kernel_clusters((unsigned)p.split, mx4_few_kernel<MT, T, kRaw>,
+                                     dim3((unsigned)(tiles * p.split)), dim3(kThreads),
+                                     Layout<MT>::kSmem, stream, *tmA, *tmB, p);
+}
+
+template <typename T>
+cudaError_t launch_rows(const Mx4FewParams& p, const CUtensorMap* a, const CUtensorMap* b,
+                        cudaStream_t s) {
+  const bool raw = p.X != nullptr;
+  switch (mx4_few_tile(p.M)) {
+    case 16:
+      return raw ? launch_typed<16, T, true>(p, a, b, s) : launch_typed<16, T, false>(p, a, b, s);
+    case 32:
+      return raw ? launch_typed<32, T, true>(p, a, b, s) : launch_typed<32, T, false>(p, a, b, s);
+    case 64:
+      return raw ? launch_typed<64, T, true>(p, a, b, s) : launch_typed<64, T, false>(p, a, b, s);
+    default:
+      return raw ? cudaErrorInvalidValue : launch_typed<128, T, false>(p, a, b, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_few(const Mx4FewParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                           cudaStream_t stream) {
+  if (p.dtype == 0) return launch_rows<float>(p, tmA, tmB, stream);
+  if (p.dtype == 1) return launch_rows<__half>(p, tmA, tmB, stream);
+  return launch_rows<__nv_bfloat16>(p, tmA, tmB, stream);
+}
+
+}  // namespace dgemm

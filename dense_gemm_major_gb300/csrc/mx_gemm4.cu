@@ -252,8 +252,8 @@ template <typename T>
 cudaError_t launch_typed(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                          const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
                          cudaStream_t stream) {
-  cudaError_t e =
-      cudaFuncSetAttribute(mx4_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = mx_allow_smem(mx4_kernel<T>, kSmem, &done);
   if (e != cudaSuccess) return e;
   return launch_gemm_kernel(mx4_kernel<T>, dim3(2 * pairs), dim3(kThreads), kSmem, stream, *tmA,
                             *tmB, *tmSA, *tmSB, p);

@@ -524,8 +524,8 @@ cudaError_t launch_typed(const MxGradParams& p, const CUtensorMap* tmA, const CU
     return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == kRegsLaunch;
   }();
   if (!fits) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Layout<kFmt>::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = mx_allow_smem(kernel, Layout<kFmt>::kSmem, &done);
   if (e != cudaSuccess) return e;
   return launch_gemm_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Layout<kFmt>::kSmem, stream,
                             *tmA, *tmB, p);

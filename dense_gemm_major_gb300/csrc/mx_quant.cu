@@ -11,25 +11,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight consecutive elements of type T, 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(src);
-    const float4 b = *reinterpret_cast<const float4*>(src + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(src);
-    const unsigned w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = pair_to_f32<T>(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
 template <typename T>
 __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
   if constexpr (sizeof(T) == 4) {
@@ -41,8 +22,6 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
 // Row-major X.  A thread takes 8 columns, four threads a block; a warp 256
 // columns of one row.  Work item: (row, chunk of 256 columns), chunks
 // covering whole tiles of scales so that the padding blocks get theirs.
@@ -51,6 +30,8 @@ __global__ void __launch_bounds__(kThreads)
     mx_quantize_kernel(int R, int K, const T* __restrict__ X, long long ldx, bool vec,
                        unsigned char* __restrict__ codes, long long ldq,
                        unsigned char* __restrict__ scales) {
+  wait_prior_grids();
+  allow_dependent_grids();
   const int lane = threadIdx.x & 31;
   const int tiles = mx_scale_tiles(K);
   const int chunks = (tiles + 1) / 2;
@@ -97,6 +78,8 @@ __global__ void __launch_bounds__(kThreads)
     mx_quantize_t_kernel(int R, int K, const T* __restrict__ X, long long ldx,
                          unsigned char* __restrict__ codes, long long ldq,
                          unsigned char* __restrict__ scales) {
+  wait_prior_grids();
+  allow_dependent_grids();
   const int lane = threadIdx.x & 31;
   const int tiles = mx_scale_tiles(K);
   const int blocks = tiles * kMxTileBlocks;
@@ -142,6 +125,8 @@ __global__ void __launch_bounds__(kThreads)
     mx_dequantize_kernel(int R, int K, const unsigned char* __restrict__ codes, long long ldq,
                          const unsigned char* __restrict__ scales, T* __restrict__ Y,
                          long long ldy, bool vec) {
+  wait_prior_grids();
+  allow_dependent_grids();
   const int lane = threadIdx.x & 31;
   const int tiles = mx_scale_tiles(K);
   const int chunks = (K + 255) / 256;
@@ -191,14 +176,12 @@ cudaError_t quantize_typed(int op, int R, int K, const T* X, long long ldx, unsi
   const int tiles = mx_scale_tiles(K);
   if (op == GEMM_OP_N) {
     const long long items = (long long)R * ((tiles + 1) / 2);
-    mx_quantize_kernel<kFmt, T><<<grid_for(items), kThreads, 0, stream>>>(
-        R, K, X, ldx, rows16(X, ldx), codes, ldq, scales);
-  } else {
-    const long long items = (long long)((R + 31) / 32) * tiles * kMxTileBlocks;
-    mx_quantize_t_kernel<kFmt, T><<<grid_for(items), kThreads, 0, stream>>>(R, K, X, ldx, codes,
-                                                                           ldq, scales);
+    return launch_gemm_kernel(mx_quantize_kernel<kFmt, T>, dim3(grid_for(items)), dim3(kThreads), 0,
+                              stream, R, K, X, ldx, rows16(X, ldx), codes, ldq, scales);
   }
-  return cudaGetLastError();
+  const long long items = (long long)((R + 31) / 32) * tiles * kMxTileBlocks;
+  return launch_gemm_kernel(mx_quantize_t_kernel<kFmt, T>, dim3(grid_for(items)), dim3(kThreads),
+                            0, stream, R, K, X, ldx, codes, ldq, scales);
 }
 
 template <int kFmt, typename T>
@@ -206,9 +189,8 @@ cudaError_t dequantize_typed(int R, int K, const unsigned char* codes, long long
                              const unsigned char* scales, T* Y, long long ldy,
                              cudaStream_t stream) {
   const long long items = (long long)R * ((K + 255) / 256);
-  mx_dequantize_kernel<kFmt, T><<<grid_for(items), kThreads, 0, stream>>>(
-      R, K, codes, ldq, scales, Y, ldy, rows16(Y, ldy));
-  return cudaGetLastError();
+  return launch_gemm_kernel(mx_dequantize_kernel<kFmt, T>, dim3(grid_for(items)), dim3(kThreads), 0,
+                            stream, R, K, codes, ldq, scales, Y, ldy, rows16(Y, ldy));
 }
 
 template <int kFmt>
