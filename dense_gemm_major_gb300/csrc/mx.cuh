@@ -135,14 +135,16 @@ __device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v
 
 // ------------------------------------------------------------ tcgen05, block scaled
 
-// Shared-memory matrix descriptor without swizzle (8-row groups of 16-byte
-// rows, sbo bytes apart), as the copy of scales to tensor memory reads it.
-__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
+// Shared-memory matrix descriptors in two words.  The high word (stride
+// between 8-row groups, version, swizzle) is the same for all of a kernel's
+// tiles, and the low one (address, leading offset) of a tile further along
+// differs by a plain addition of its distance in 16-byte units: one
+// instruction per operand of an MMA, which the issuing thread, alone in its
+// warp, can afford.
+constexpr uint32_t kDescHi128B = (1024u >> 4) | (1u << 14) | (2u << 29);   // 128-byte swizzle
+constexpr uint32_t kDescHiPlain = (128u >> 4) | (1u << 14);                // 8 rows of 16 bytes
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
 }
 
 // Instruction descriptor of kind::mxf4: E2M1 operands (K-major), E8M0
@@ -158,25 +160,42 @@ __host__ __device__ constexpr uint32_t instr_desc_mx4(uint32_t m, uint32_t n, ui
          | (sf << 29);             // A scale byte
 }
 
-// 64-deep block-scaled MMA step of a CTA pair (see mma_f16_pair); each CTA's
-// tensor memory holds the scales of its own rows of A and of all of B.
-__device__ __forceinline__ void mma_mx4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+// 16-deep kind::f16 MMA step of a CTA pair (see mma_f16_pair), 128-byte
+// swizzled operands.
+__device__ __forceinline__ void mma_f16_pair_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(kDescHi128B), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 64-deep block-scaled MMA step of a CTA pair; each CTA's tensor memory holds
+// the scales of its own rows of A and of all of B.
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d_tmem, uint32_t alo, uint32_t blo,
                                              uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                              uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%5], "
+      "[%6], p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(kDescHi128B), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
 
 // One 512-byte tile of scales (32 rows of 16 bytes) to 4 TMEM columns, in
 // all four lane quarters, in both CTAs of the pair from their own memories.
-__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr),
+      "r"(lo), "r"(kDescHiPlain)
+      : "memory");
 }
 
 // Untiled bulk copy global -> shared; addresses and size multiples of 16.

@@ -70,9 +70,9 @@ struct Mx4Params {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-constexpr int kMx4BK = 256;           // 128 bytes of codes
+constexpr int kMx4BK = 512;
 // tmA, tmB: codes as bytes, boxes of 128 bytes x 64 and 128 rows; tmSA, tmSB:
-// scales as 32-bit words, one row per 128 rows of the operand, boxes of two
+// scales as 64-bit words, one row per 128 rows of the operand, boxes of four
 // tiles.
 cudaError_t launch_mx4(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                        const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
@@ -96,7 +96,7 @@ struct Mx4FewParams {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-constexpr int kMx4FewRows = 128;
+constexpr int kMx4FewRows = 128, kMx4FewBK = 256;
 // Quantising inside the kernel saves a launch (2.7 us of a calling thread)
 // but is done anew by the CTAs of every 128 columns: on the GPU, N = K = 4096,
 // inside / before the kernel: 1 row 5.3 / 6.0 us, 16 7.6 / 6.8, 33 9.3 / 8.1,

@@ -217,7 +217,7 @@ gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X
   // As many CTAs (2, 4 or 8 of a cluster) to a tile's K as keep one wave,
   // each with a stage at least.
   p.split = 1;
-  const int tiles = ceil_div(N, 128), nk = ceil_div(K, dgemm::kMx4BK);
+  const int tiles = ceil_div(N, 128), nk = ceil_div(K, dgemm::kMx4FewBK);
   while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= 2 * max_pairs) p.split *= 2;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc, p.dtype = dtype;
@@ -235,17 +235,17 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
   alignas(64) CUtensorMap tmA, tmB, tmSA, tmSB;
   const uint64_t width = (uint64_t)code_bytes(GEMM_MXFP4, K);
   const uint64_t srow = (uint64_t)dgemm::mx_scale_tiles(K) * dgemm::kMxTileBytes;
-  constexpr uint32_t sbox = dgemm::kMx4BK / 128 * dgemm::kMxTileBytes / 4;
+  constexpr uint32_t sbox = dgemm::kMx4BK / 128 * dgemm::kMxTileBytes / 8;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const CUtensorMapDataType u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const CUtensorMapDataType u64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
   if (!encode_2d(&tmA, u8, a, width, (uint64_t)M, (uint64_t)lda, 128, 64) ||
       !encode_2d(&tmB, u8, b, width, (uint64_t)N, (uint64_t)ldb, 128, 128) ||
-      !encode_2d(&tmSA, u32, sa, srow / 4, (uint64_t)ceil_div(M, 128), srow, sbox, 1, false) ||
-      !encode_2d(&tmSB, u32, sb, srow / 4, (uint64_t)ceil_div(N, 128), srow, sbox, 1, false))
+      !encode_2d(&tmSA, u64, sa, srow / 8, (uint64_t)ceil_div(M, 128), srow, sbox, 1, false) ||
+      !encode_2d(&tmSB, u64, sb, srow / 8, (uint64_t)ceil_div(N, 128), srow, sbox, 1, false))
     return GEMM_ERR_LAUNCH;
   dgemm::Mx4Params p;
   p.M = M, p.N = N, p.K = K;
-  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, 4);
+  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, 2);
   gemm_status_t st = partials(p.sched, M, N, stream, &p.ws, &p.ldw);
   if (st != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;

@@ -59,20 +59,24 @@ struct alignas(8) Barriers {
 
 // 64-deep block-scaled MMA step, and the copy of a 512-byte tile of scales
 // to 4 TMEM columns (all four lane quarters), on one CTA.
-__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint32_t alo, uint32_t blo,
                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%5], "
+      "[%6], p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(kDescHi128B), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr),
+      "r"(lo), "r"(kDescHiPlain)
+      : "memory");
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -170,15 +174,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sx = st + kBBytes, ss = sx + L::kABytes;
         const uint32_t sfw = tmem_base + L::kScaleCol + (it & 1u) * 8 * kChunks;
         const uint32_t sfx = sfw + 4 * kChunks;
+        const uint32_t blo = desc_lo(st, 16), alo = desc_lo(sx, 16);
         const int chunks = min(kChunks, ktiles - kt * kChunks);
         for (int c = 0; c < chunks; ++c) {
-          copy_scales(sfw + 4 * c, smem_desc_plain(ss + c * kMxTileBytes, 128));
-          copy_scales(sfx + 4 * c, smem_desc_plain(ss + kSBytes + c * kMxTileBytes, 128));
+          copy_scales(sfw + 4 * c, desc_lo(ss + c * kMxTileBytes, 0));
+          copy_scales(sfx + 4 * c, desc_lo(ss + kSBytes + c * kMxTileBytes, 0));
         }
 #pragma unroll
         for (int k = 0; k < BK / 64; ++k)
           if (k < 2 * chunks)
-            mma_mx4(tmem_base, kmajor_desc(st, k), kmajor_desc(sx, k),
+            mma_mx4(tmem_base, blo + 2 * k, alo + 2 * k,
                     instr_desc_mx4(BN, MT, (k & 1) * 2), sfw + 4 * (k >> 1), sfx + 4 * (k >> 1),
                     (kt > kb || k > 0) ? 1u : 0u);
         mma_commit(smem_u32(&bars->empty[s]));

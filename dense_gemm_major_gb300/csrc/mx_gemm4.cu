@@ -25,15 +25,20 @@ namespace dgemm {
 namespace {
 
 constexpr int BK = kMx4BK;
-constexpr int S = 6;
+constexpr int S = 3;
 constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4, kEpiWarps = 8;
-constexpr uint32_t kHalf = 64 * BK / 2;                  // 64 rows of codes: 8 KB
-constexpr uint32_t kBBytes = 2 * kHalf;                  // this CTA's 128 columns of C
+// A stage is two blocks of 256 of K (rows of 128 bytes), each with its part
+// of both operands: one barrier round trip of the MMA issuer covers eight
+// MMAs.
+constexpr int kBlocks = BK / 256;
+constexpr uint32_t kHalf = 64 * 128;                     // 64 rows of a block: 8 KB
+constexpr uint32_t kBBytes = 2 * kHalf;                  // this CTA's 128 columns of C, a block
 constexpr uint32_t kABytes = 2 * kHalf;                  // this CTA's half of the rows
+constexpr uint32_t kBlock = kBBytes + kABytes;
 constexpr int kChunks = BK / 128;                        // scale tiles along K per stage
-constexpr uint32_t kSBytes = kChunks * kMxTileBytes;     // scales of 128 rows: 1 KB
-constexpr uint32_t kStage = kBBytes + kABytes + 3 * kSBytes;
+constexpr uint32_t kSBytes = kChunks * kMxTileBytes;     // scales of 128 rows: 2 KB
+constexpr uint32_t kStage = kBlocks * kBlock + 3 * kSBytes;
 constexpr uint32_t kSmem = S * kStage + 1024 + 512;
 // Tensor memory columns: the accumulator, then the scales of two stages (4
 // columns per scale tile: B's, then A's two per 128 of K).
@@ -68,6 +73,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
   const int npairs = gridDim.x >> 1;
   const int nk = (p.K + BK - 1) / BK;
+  const int ktiles = mx_scale_tiles(p.K);
   const MxSchedule& sc = p.sched;
 
   if (threadIdx.x == 0) {
@@ -116,13 +122,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t fb = mapa_shared(smem_u32(&bars->full[s]), 0);
           if (rank == 0)
             mbar_arrive_expect_tx(smem_u32(&bars->full[s]),
-                                  2u * (kBBytes + halves * kHalf + (1 + halves) * kSBytes));
+                                  2u * (kBlocks * (kBBytes + halves * kHalf) +
+                                        (1 + halves) * kSBytes));
           const uint32_t st = smem_u32(base + s * kStage);
-          const uint32_t ss = st + kBBytes + kABytes;
-          tma_load_2d_pair(st, &tmB, fb, kt * (BK / 2), ct * 128);
-          for (int j = 0; j < halves; ++j)
-            tma_load_2d_pair(st + kBBytes + j * kHalf, &tmA, fb, kt * (BK / 2), row + j * 64);
-          const int x = kt * (int)(kSBytes / 4);
+          for (int b = 0; b < kBlocks; ++b) {
+            const int x = kt * (BK / 2) + b * 128;
+            tma_load_2d_pair(st + b * kBlock, &tmB, fb, x, ct * 128);
+            for (int j = 0; j < halves; ++j)
+              tma_load_2d_pair(st + b * kBlock + kBBytes + j * kHalf, &tmA, fb, x, row + j * 64);
+          }
+          const uint32_t ss = st + kBlocks * kBlock;
+          const int x = kt * (int)(kSBytes / 8);
           tma_load_2d_pair(ss, &tmSB, fb, x, ct);
           // The scales of all of the tile's rows of C, in both CTAs.
           for (int j = 0; j < halves; ++j)
@@ -154,21 +164,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t st = smem_u32(base + s * kStage);
-          const uint32_t ss = st + kBBytes + kABytes;
+          const uint32_t slo = desc_lo(st + kBlocks * kBlock, 0);
+          const uint32_t blo = desc_lo(st, 16), alo = desc_lo(st + kBBytes, 16);
           const uint32_t sfb = tmem_base + kScaleCol + (it & 1u) * kScaleStage;
           const uint32_t sfa = sfb + 4 * kChunks;
+          const int chunks = min(kChunks, ktiles - kt * kChunks);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            copy_scales_pair(sfb + 4 * c, smem_desc_plain(ss + c * kMxTileBytes, 128));
-            for (int j = 0; j < halves; ++j)
-              copy_scales_pair(sfa + 8 * c + 4 * j,
-                               smem_desc_plain(ss + (1 + j) * kSBytes + c * kMxTileBytes, 128));
-          }
+            if (c >= chunks) break;
+            const uint32_t lo = slo + c * (kMxTileBytes >> 4);
+            copy_scales_pair(sfb + 4 * c, lo);
+            copy_scales_pair(sfa + 8 * c, lo + (kSBytes >> 4));
+            if (halves == 2) copy_scales_pair(sfa + 8 * c + 4, lo + (2 * kSBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < BK / 64; ++k)
-            mma_mx4_pair(tmem_base, kmajor_desc(st, k), kmajor_desc(st + kBBytes, k),
-                         (k & 1) ? idesc2 : idesc, sfb + 4 * (k >> 1), sfa + 8 * (k >> 1),
-                         (kt > w.kb || k > 0) ? 1u : 0u);
+            for (int k = 2 * c; k < 2 * c + 2; ++k) {
+              const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+              mma_mx4_pair(tmem_base, blo + off, alo + off, (k & 1) ? idesc2 : idesc, sfb + 4 * c,
+                           sfa + 8 * c, (kt > w.kb || k > 0) ? 1u : 0u);
+            }
+          }
           mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
         }
         if (!ok) break;

@@ -335,14 +335,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t st = smem_u32(base + s * kStage);
-            const uint32_t sa = st + kConvBytes;
+            // MN-major tiles step by 16 rows of 128 bytes per 16 of K, K-major
+            // ones by 32 bytes.
+            const uint32_t blo = desc_lo(st, kBlock);
+            const uint32_t alo = desc_lo(st + kConvBytes, kAT ? kBlock : 16);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-              const uint32_t bh = st + (k >> 2) * kConvHalf, ah = sa + (k >> 2) * kAHalf;
-              mma_f16_pair(tmem_base + b * 256, mnmajor_desc(bh, k & 3, kBlock),
-                           kAT ? mnmajor_desc(ah, k & 3, kBlock) : kmajor_desc(ah, k & 3), idesc,
-                           (kt > k0 || k > 0) ? 1u : 0u);
-            }
+            for (int k = 0; k < BK / 16; ++k)
+              mma_f16_pair_lo(tmem_base + b * 256,
+                              blo + (((k >> 2) * kConvHalf + (k & 3) * 2048) >> 4),
+                              alo + (((k >> 2) * kAHalf + (k & 3) * (kAT ? 2048 : 32)) >> 4),
+                              idesc, (kt > k0 || k > 0) ? 1u : 0u);
             mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
           }
           if (!ok) break;
