@@ -13,12 +13,14 @@
 // warp's 32 lanes are 32 consecutive columns, which makes the stores of a
 // row contiguous for any alignment of C.
 //
-// Roles (384 threads): warp 0 loads codes and scales by TMA, warp 1 (even
-// CTA) issues the copies of scales to tensor memory and the MMAs, warps 4-11
-// drain the accumulator.  Tensor memory holds one accumulator of 256 columns
-// and the scales of two stages (two accumulators and the scales would need
-// 560 columns of 512): the draining warps take all of it to registers before
-// they scale and store, so that the next tile can start.
+// Roles (512 threads): warp 12 loads codes and scales by TMA, warp 13 (even
+// CTA) issues the MMAs, warps 0-3 write the scales to tensor memory, warps
+// 4-11 drain the accumulator.  The scales could go there by tcgen05.cp, but
+// its copies take turns with the MMAs in the tensor pipe: 208 against 153 us
+// without any at 8192^3.  Tensor memory holds one accumulator of 256 columns
+// and the scales of the ring's three stages (two accumulators and two stages
+// of scales would not fit): the draining warps take all of it to registers
+// before they scale and store, so that the next tile can start.
 #include "mx.cuh"
 
 namespace dgemm {
@@ -26,8 +28,13 @@ namespace {
 
 constexpr int BK = kMx4BK;
 constexpr int S = 3;
-constexpr int kThreads = 384;
-constexpr int kEpiWarp = 4, kEpiWarps = 8;
+constexpr int kThreads = 512;
+constexpr int kScaleWarps = 4, kEpiWarp = 4, kEpiWarps = 8, kLoadWarp = 12, kMmaWarp = 13;
+// Registers per thread: 128 at launch; after the split 128 threads of scales,
+// 128 of loads and MMAs, 256 of draining (128 sums each):
+// 72 + 72 + 2 * 184 = 4 * 128.
+constexpr int kRegsLaunch = 128, kRegsScale = 72, kRegsIssue = 72, kRegsEpi = 184;
+static_assert(kRegsScale + kRegsIssue + 2 * kRegsEpi <= 4 * kRegsLaunch, "register split");
 // A stage is two blocks of 256 of K (rows of 128 bytes), each with its part
 // of both operands: one barrier round trip of the MMA issuer covers eight
 // MMAs.
@@ -40,17 +47,19 @@ constexpr int kChunks = BK / 128;                        // scale tiles along K 
 constexpr uint32_t kSBytes = kChunks * kMxTileBytes;     // scales of 128 rows: 2 KB
 constexpr uint32_t kStage = kBlocks * kBlock + 3 * kSBytes;
 constexpr uint32_t kSmem = S * kStage + 1024 + 512;
-// Tensor memory columns: the accumulator, then the scales of two stages (4
-// columns per scale tile: B's, then A's two per 128 of K).
+// Tensor memory columns: the accumulator, then for each stage the scales of
+// its four tiles of B (4 columns each) and of A (two row tiles, 8 columns).
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 256;
 constexpr uint32_t kScaleStage = 4 * kChunks * 3;
-static_assert(kScaleCol + 2 * kScaleStage <= kTmemCols, "tensor memory");
+static_assert(kChunks == 4, "16 and 32 columns of scales");
+static_assert(kScaleCol + S * kScaleStage <= kTmemCols, "tensor memory");
 static_assert(kStage % 1024 == 0, "stages keep the swizzle's alignment");
 static_assert(kSmem <= 232448, "shared memory");
 
 struct alignas(8) Barriers {
-  uint64_t full[S];     // even CTA: the loads of both CTAs
+  uint64_t full[S];     // even CTA: codes of both CTAs loaded, scales of both in TMEM
+  uint64_t scales[S];   // scales of this CTA loaded
   uint64_t empty[S];
   uint64_t acc_full;
   uint64_t acc_empty;   // even CTA
@@ -78,7 +87,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&bars->full[s]), 1);
+      mbar_init(smem_u32(&bars->full[s]), 1 + 2 * kScaleWarps);
+      mbar_init(smem_u32(&bars->scales[s]), 1);
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     mbar_init(smem_u32(&bars->acc_full), 1);
@@ -87,13 +97,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
   }
-  if (warp == 1) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
@@ -103,9 +113,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   allow_dependent_grids();
 
   uint32_t issued = 0;
-  if (warp == 0) {
-    // ------------------------------------------------ loads (both CTAs)
-    if (lane == 0) {
+  if (warp < kScaleWarps) {
+    // ------------------------------------------------ scales to tensor memory (both CTAs)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScale));
+    // Lane l of warp q writes lane 32 q + l: row l of a tile, 16 bytes, is its
+    // four columns there, the same in all four quarters.
+    const uint32_t t = tmem_base + ((uint32_t)(warp * 32) << 16) + kScaleCol;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
+      const MxUnit w = mx_unit(u, sc, nk);
+      if (w.row0 >= p.M) continue;
+      for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
+        const uint32_t s = it % S;
+        // (The loads were issued after the MMAs on this stage had finished, so
+        // its columns may be overwritten.)
+        ok = role_wait_lanes(smem_u32(&bars->scales[s]), (it / S) & 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait);
+        if (!ok) break;
+        const uint4* tile =
+            reinterpret_cast<const uint4*>(base + s * kStage + kBlocks * kBlock) + lane;
+        constexpr int kTile = kMxTileBytes / 16;
+        uint32_t rb[16], ra[32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const uint4 x = tile[c * kTile];
+          const uint4 y = tile[(kChunks + c) * kTile], z = tile[(2 * kChunks + c) * kTile];
+          rb[4 * c] = x.x, rb[4 * c + 1] = x.y, rb[4 * c + 2] = x.z, rb[4 * c + 3] = x.w;
+          ra[8 * c] = y.x, ra[8 * c + 1] = y.y, ra[8 * c + 2] = y.z, ra[8 * c + 3] = y.w;
+          ra[8 * c + 4] = z.x, ra[8 * c + 5] = z.y, ra[8 * c + 6] = z.z, ra[8 * c + 7] = z.w;
+        }
+        tmem_st16(t + s * kScaleStage, rb);
+        tmem_st32(t + s * kScaleStage + 4 * kChunks, ra);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kLoadWarp && lane == 0) {
+      // ---------------------------------------------- loads (both CTAs)
       uint32_t it = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
@@ -122,8 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t fb = mapa_shared(smem_u32(&bars->full[s]), 0);
           if (rank == 0)
             mbar_arrive_expect_tx(smem_u32(&bars->full[s]),
-                                  2u * (kBlocks * (kBBytes + halves * kHalf) +
-                                        (1 + halves) * kSBytes));
+                                  2u * kBlocks * (kBBytes + halves * kHalf));
           const uint32_t st = smem_u32(base + s * kStage);
           for (int b = 0; b < kBlocks; ++b) {
             const int x = kt * (BK / 2) + b * 128;
@@ -133,18 +182,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const uint32_t ss = st + kBlocks * kBlock;
           const int x = kt * (int)(kSBytes / 8);
-          tma_load_2d_pair(ss, &tmSB, fb, x, ct);
+          const uint32_t sb = smem_u32(&bars->scales[s]);
+          mbar_arrive_expect_tx(sb, (1 + halves) * kSBytes);
+          tma_load_2d(ss, &tmSB, sb, x, ct);
           // The scales of all of the tile's rows of C, in both CTAs.
           for (int j = 0; j < halves; ++j)
-            tma_load_2d_pair(ss + (1 + j) * kSBytes, &tmSA, fb, x, w.row0 / 128 + j);
+            tma_load_2d(ss + (1 + j) * kSBytes, &tmSA, sb, x, w.row0 / 128 + j);
           issued = it + 1;
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    } else if (warp == kMmaWarp && rank == 0 && lane == 0) {
+      // ---------------------------------------------- MMA issuer (even CTA)
       uint32_t it = 0, local = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
@@ -164,23 +212,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t st = smem_u32(base + s * kStage);
-          const uint32_t slo = desc_lo(st + kBlocks * kBlock, 0);
           const uint32_t blo = desc_lo(st, 16), alo = desc_lo(st + kBBytes, 16);
-          const uint32_t sfb = tmem_base + kScaleCol + (it & 1u) * kScaleStage;
+          const uint32_t sfb = tmem_base + kScaleCol + s * kScaleStage;
           const uint32_t sfa = sfb + 4 * kChunks;
           const int chunks = min(kChunks, ktiles - kt * kChunks);
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c >= chunks) break;
-            const uint32_t lo = slo + c * (kMxTileBytes >> 4);
-            copy_scales_pair(sfb + 4 * c, lo);
-            copy_scales_pair(sfa + 8 * c, lo + (kSBytes >> 4));
-            if (halves == 2) copy_scales_pair(sfa + 8 * c + 4, lo + (2 * kSBytes >> 4));
-#pragma unroll
-            for (int k = 2 * c; k < 2 * c + 2; ++k) {
+          for (int k = 0; k < BK / 64; ++k) {
+            if (k < 2 * chunks) {
               const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
-              mma_mx4_pair(tmem_base, blo + off, alo + off, (k & 1) ? idesc2 : idesc, sfb + 4 * c,
-                           sfa + 8 * c, (kt > w.kb || k > 0) ? 1u : 0u);
+              mma_mx4_pair(tmem_base, blo + off, alo + off, (k & 1) ? idesc2 : idesc,
+                           sfb + 4 * (k >> 1), sfa + 8 * (k >> 1),
+                           (kt > w.kb || k > 0) ? 1u : 0u);
             }
           }
           mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
@@ -191,8 +233,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= kEpiWarp) {
+  } else {
     // ------------------------------------------------ epilogue (both CTAs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     // Warp: TMEM lanes 32 q .. 32 q + 31 (columns of C), half of the rows.
     const int q = warp & 3;
     const int half = (warp - kEpiWarp) >> 2;
@@ -237,17 +280,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------ teardown
-  if (warp == 1 && rank == 0 && lane == 0) {
+  if (warp == kMmaWarp && rank == 0 && lane == 0) {
     mma_commit_pair_multicast(smem_u32(&bars->drain), 0x1);
     if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
       raise_fault(p.fault, kFaultDrainWait);
   }
-  if (warp == 0 && lane == 0 && rank == 0 && bars->abort) {
-    // Let the loads in flight (both CTAs count on the even one's) land.
+  if (warp == kLoadWarp && lane == 0 && bars->abort) {
+    // Let the loads in flight land: this CTA's scales, and (even CTA) both
+    // CTAs' codes on full[], whose arrivals by the warps of scales may be
+    // missing; the wait then gives up.
     const uint32_t first = issued > (uint32_t)S ? issued - S : 0;
     for (uint32_t it = first; it < issued; ++it) {
-      if (!mbar_wait_bounded(smem_u32(&bars->full[it % S]), (it / S) & 1u, p.timeout_ns,
-                             nullptr)) {
+      const uint32_t s = it % S, ph = (it / S) & 1u;
+      bool ok = mbar_wait_bounded(smem_u32(&bars->scales[s]), ph, p.timeout_ns, nullptr);
+      if (ok && rank == 0)
+        ok = mbar_wait_bounded(smem_u32(&bars->full[s]), ph, p.timeout_ns, nullptr);
+      if (!ok) {
         raise_fault(p.fault, kFaultDrainWait);
         break;
       }
@@ -256,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // neither CTA leaves while the pair may still touch its memory
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
@@ -266,6 +314,13 @@ template <typename T>
 cudaError_t launch_typed(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                          const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
                          cudaStream_t stream) {
+  // The register split needs kRegsLaunch registers a thread at launch: with
+  // fewer, its setmaxnreg.inc would wait for ever.
+  static const bool fits = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, mx4_kernel<T>) == cudaSuccess && a.numRegs == kRegsLaunch;
+  }();
+  if (!fits) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(mx4_kernel<T>, kSmem, &done);
   if (e != cudaSuccess) return e;
