@@ -58,20 +58,25 @@ __device__ __forceinline__ unsigned e2m1x8(const float (&v)[8]) {
   return r;
 }
 
-// v * 64 rounded to nearest even, clamped to +-127, in the low byte.  Adding
-// 1.5 * 2^23 leaves the integer in the low mantissa bits.
-__device__ __forceinline__ unsigned int8_bits(float v) {
-  const float y = fminf(fmaxf(v * 64.f, -127.f), 127.f);
-  return __float_as_uint(y + 12582912.f);
-}
-__device__ __forceinline__ uint2 int8x8(const float (&v)[8]) {
+// Eight values, already divided by their scale, as MXINT8 codes: v * 64
+// rounded to nearest even (adding 1.5 * 2^23 leaves the integer in the low
+// mantissa bits).  Only values of 127.5 / 64 or more would round past +-127;
+// `clamp` says whether the block has any (its largest shows that).
+__device__ __forceinline__ uint2 int8x8(float (&v)[8], bool clamp) {
+  if (clamp) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -1.984375f), 1.984375f);
+  }
   unsigned b[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = int8_bits(v[i]);
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(v[i], 64.f, 12582912.f));
   uint2 r;
   r.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   r.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
   return r;
+}
+__device__ __forceinline__ bool int8_clamps(unsigned amax, float inv) {
+  return __uint_as_float(amax) * inv >= 1.9921875f;
 }
 
 // Eight E2M1 codes as FP32 values (without their scale).
@@ -89,10 +94,13 @@ __device__ __forceinline__ void e2m1x8_to_f32(unsigned codes, float (&v)[8]) {
     v[2 * j + 1] = f.y;
   }
 }
-// Four MXINT8 codes (one word) as FP32 values (without their scale).
+// Four MXINT8 codes (one word) as FP32 values (without their scale):
+// 0x4B000000 + u is 2^23 + u; u = c + 128.
 __device__ __forceinline__ void int8x4_to_f32(unsigned w, float* v) {
+  const unsigned u = w ^ 0x80808080u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = (float)(int)(signed char)(w >> (8 * j)) * 0.015625f;
+  for (int j = 0; j < 4; ++j)
+    v[j] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + j)) - 8388736.f) * 0.015625f;
 }
 
 template <typename T>

@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[g][j] = sb == 255u ? 0.f : x[g][j] * inv;
-          q[g] = e2m1x8(x[g]);
+          for (int j = 0; j < 8; ++j) x[g][j] *= inv;
+          q[g] = sb == 255u ? 0u : e2m1x8(x[g]);
         }
         *reinterpret_cast<uint4*>(sx + m * 128 + ((b ^ (m & 7)) << 4)) =
             make_uint4(q[0], q[1], q[2], q[3]);

@@ -11,20 +11,27 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Two consecutive elements, 4-byte aligned, of a 16-bit type, and two values
+// as such a pair (never called for a 32-bit type).
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
-                                                pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-  }
+__device__ __forceinline__ float2 pair_to_f32_any(const T* src) {
+  if constexpr (sizeof(T) == 2) return pair_to_f32<T>(*reinterpret_cast<const unsigned*>(src));
+  return make_float2(0.f, 0.f);
+}
+template <typename T>
+__device__ __forceinline__ unsigned pack2_any(float lo, float hi) {
+  if constexpr (sizeof(T) == 2) return pack2<T>(lo, hi);
+  return 0u;
 }
 
-// Row-major X.  A thread takes 8 columns, four threads a block; a warp 256
-// columns of one row.  Work item: (row, chunk of 256 columns), chunks
-// covering whole tiles of scales so that the padding blocks get theirs.
+// Row-major X.  A thread takes 8 columns, four threads a block, a warp 256
+// columns of a row at a time and kStep such pieces in a row, their loads in
+// flight together: HBM's latency needs some 40 KB of them per SM.  A CTA has
+// kThreads / 32 rows; pieces cover whole tiles of scales, so that the padding
+// blocks get theirs.
+constexpr int kStep = 4;
+constexpr int kRowsPerCta = kThreads / 32;
+
 template <int kFmt, typename T>
 __global__ void __launch_bounds__(kThreads)
     mx_quantize_kernel(int R, int K, const T* __restrict__ X, long long ldx, bool vec,
@@ -33,136 +40,242 @@ __global__ void __launch_bounds__(kThreads)
   wait_prior_grids();
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kRowsPerCta + (threadIdx.x >> 5);
+  if (r >= R) return;
   const int tiles = mx_scale_tiles(K);
-  const int chunks = (tiles + 1) / 2;
-  const long long items = (long long)R * chunks;
-  const long long warps = (long long)gridDim.x * (kThreads / 32);
-  for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += warps) {
-    const int r = (int)(it / chunks);
-    const int col = (int)(it - (long long)r * chunks) * 256 + lane * 8;
-    float v[8];
-    const T* src = X + (long long)r * ldx + col;
-    if (vec && col + 8 <= K) {
-      load8<T>(src, v);
+  const int pieces = (tiles + 1) / 2;
+  const T* row = X + (long long)r * ldx;
+  unsigned char* q = codes + (long long)r * ldq;
+  unsigned char* srow = scales + mx_scale_offset(r, (lane >> 2) & 3, tiles);
+  for (int p0 = blockIdx.y * kStep; p0 < pieces; p0 += gridDim.y * kStep) {
+    float v[kStep][8];
+    // (The two ways apart, so that the compiler keeps all loads of the first
+    // in flight.)
+    if (vec && (p0 + kStep) * 256 <= K) {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) load8<T>(row + (p0 + i) * 256 + lane * 8, v[i]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col + j < K ? to_f32_any<T>(src[j]) : 0.f;
-    }
-    unsigned amax = 0;
+      for (int i = 0; i < kStep; ++i) {
+        const int col = (p0 + i) * 256 + lane * 8;
+        if (vec && col + 8 <= K) {
+          load8<T>(row + col, v[i]);
+        } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(v[j]));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const unsigned s = mx_scale_byte<kFmt>(amax);
-    const float inv = mx_inverse_scale(s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = s == 255u ? 0.f : v[j] * inv;
-    if (col < K) {
-      unsigned char* q = codes + (long long)r * ldq;
-      if constexpr (kFmt == GEMM_MXFP4)
-        *reinterpret_cast<unsigned*>(q + col / 2) = e2m1x8(v);
-      else
-        *reinterpret_cast<uint2*>(q + col) = int8x8(v);
+          for (int j = 0; j < 8; ++j) v[i][j] = col + j < K ? to_f32_any<T>(row[col + j]) : 0.f;
+        }
+      }
     }
-    const int block = col >> 5;
-    if ((lane & 3) == 0 && block < tiles * kMxTileBlocks)
-      scales[mx_scale_offset(r, block, tiles)] = (unsigned char)s;
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      if (p0 + i >= pieces) break;
+      const int col = (p0 + i) * 256 + lane * 8;
+      unsigned amax = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(v[i][j]));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const unsigned s = mx_scale_byte<kFmt>(amax);
+      const float inv = mx_inverse_scale(s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+      if (col < K) {
+        if constexpr (kFmt == GEMM_MXFP4) {
+          *reinterpret_cast<unsigned*>(q + col / 2) = s == 255u ? 0u : e2m1x8(v[i]);
+        } else {
+          const uint2 c = int8x8(v[i], int8_clamps(amax, inv));
+          *reinterpret_cast<uint2*>(q + col) = s == 255u ? make_uint2(0u, 0u) : c;
+        }
+      }
+      const int tile = (p0 + i) * 2 + (lane >> 4);
+      if ((lane & 3) == 0 && tile < tiles) srow[tile * kMxTileBytes] = (unsigned char)s;
+    }
   }
 }
 
-// X stored K x R: a thread takes a block of one row (32 values, ldx apart);
-// a warp 32 consecutive rows, so that each load is contiguous.
+// X stored K x R.  A CTA takes 32 V rows and 256 columns (V = 2 for 16-bit
+// types, whose two rows travel in one load), a warp one block of them: its
+// loads are contiguous along R.  The codes of the CTA meet in shared memory,
+// so that they leave as 128 (MXFP4) or 256 contiguous bytes of a row, and the
+// scales as words of four.
+template <int kFmt, typename T>
+struct TLayout {
+  static constexpr int V = sizeof(T) == 4 ? 1 : 2;
+  static constexpr int kRows = 32 * V;
+  static constexpr int kBlockBytes = kFmt == GEMM_MXFP4 ? 16 : 32;   // codes of a block
+  static constexpr int kRowBytes = 8 * kBlockBytes;
+  static constexpr int kPitch = kRowBytes + 16;                      // (bank conflicts)
+};
+
 template <int kFmt, typename T>
 __global__ void __launch_bounds__(kThreads)
-    mx_quantize_t_kernel(int R, int K, const T* __restrict__ X, long long ldx,
+    mx_quantize_t_kernel(int R, int K, const T* __restrict__ X, long long ldx, bool vec,
                          unsigned char* __restrict__ codes, long long ldq,
                          unsigned char* __restrict__ scales) {
+  using L = TLayout<kFmt, T>;
+  __shared__ __align__(16) unsigned char scode[L::kRows * L::kPitch];
+  __shared__ __align__(4) unsigned char sscale[L::kRows * 8];
   wait_prior_grids();
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int tiles = mx_scale_tiles(K);
-  const int blocks = tiles * kMxTileBlocks;
-  const long long items = (long long)((R + 31) / 32) * blocks;
-  const long long warps = (long long)gridDim.x * (kThreads / 32);
-  for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += warps) {
-    const int rg = (int)(it / blocks);
-    const int block = (int)(it - (long long)rg * blocks);
-    const int r = rg * 32 + lane;
-    if (r >= R) continue;
-    const int k0 = block * kMxBlock;
-    float v[32];
-    unsigned amax = 0;
+  const int r0 = blockIdx.x * L::kRows;
+  const int pieces = (tiles + 1) / 2;
+  for (int piece = blockIdx.y; piece < pieces; piece += gridDim.y) {
+    const int k0 = piece * 256 + warp * kMxBlock;
+    const int r = r0 + lane * L::V;
+    float v[L::V][32];
+    if (L::V == 2 && vec && r + 2 <= R && k0 + kMxBlock <= K) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j] = k0 + j < K ? to_f32_any<T>(X[(long long)(k0 + j) * ldx + r]) : 0.f;
-      amax = max(amax, abs_bits(v[j]));
-    }
-    const unsigned s = mx_scale_byte<kFmt>(amax);
-    const float inv = mx_inverse_scale(s);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = s == 255u ? 0.f : v[8 * g + j] * inv;
-      const int col = k0 + 8 * g;
-      if (col < K) {
-        unsigned char* q = codes + (long long)r * ldq;
-        if constexpr (kFmt == GEMM_MXFP4)
-          *reinterpret_cast<unsigned*>(q + col / 2) = e2m1x8(w);
-        else
-          *reinterpret_cast<uint2*>(q + col) = int8x8(w);
+      for (int j = 0; j < 32; ++j) {
+        const float2 f = pair_to_f32_any<T>(X + (long long)(k0 + j) * ldx + r);
+        v[0][j] = f.x;
+        v[L::V - 1][j] = f.y;
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+#pragma unroll
+        for (int i = 0; i < L::V; ++i)
+          v[i][j] = k0 + j < K && r + i < R ? to_f32_any<T>(X[(long long)(k0 + j) * ldx + r + i])
+                                            : 0.f;
     }
-    scales[mx_scale_offset(r, block, tiles)] = (unsigned char)s;
+#pragma unroll
+    for (int i = 0; i < L::V; ++i) {
+      unsigned amax = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) amax = max(amax, abs_bits(v[i][j]));
+      const unsigned s = mx_scale_byte<kFmt>(amax);
+      const float inv = mx_inverse_scale(s);
+      const bool clamp = kFmt == GEMM_MXINT8 && int8_clamps(amax, inv);
+      const int row = lane * L::V + i;
+      uint4* dst = reinterpret_cast<uint4*>(scode + row * L::kPitch + warp * L::kBlockBytes);
+      unsigned w[8];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = v[i][8 * g + j] * inv;
+        if constexpr (kFmt == GEMM_MXFP4) {
+          w[g] = s == 255u ? 0u : e2m1x8(x);
+        } else {
+          const uint2 c = int8x8(x, clamp);
+          w[2 * g] = s == 255u ? 0u : c.x;
+          w[2 * g + 1] = s == 255u ? 0u : c.y;
+        }
+      }
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (kFmt == GEMM_MXINT8) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      sscale[row * 8 + warp] = (unsigned char)s;
+    }
+    __syncthreads();
+    constexpr int kChunksPerRow = L::kRowBytes / 16;
+#pragma unroll
+    for (int i = threadIdx.x; i < L::kRows * kChunksPerRow; i += kThreads) {
+      const int row = i / kChunksPerRow, c = i % kChunksPerRow;
+      const long long at = (long long)piece * L::kRowBytes + c * 16;   // (a row's pitch has
+      if (r0 + row < R && at < ldq)                                    // whole 16-byte chunks)
+        if (at < (kFmt == GEMM_MXFP4 ? ((long long)K + 1) / 2 : (long long)K))
+          *reinterpret_cast<uint4*>(codes + (long long)(r0 + row) * ldq + at) =
+              *reinterpret_cast<const uint4*>(scode + row * L::kPitch + c * 16);
+    }
+    for (int i = threadIdx.x; i < L::kRows * 2; i += kThreads) {
+      const int row = i >> 1, tile = piece * 2 + (i & 1);
+      if (r0 + row < R && tile < tiles)
+        *reinterpret_cast<unsigned*>(scales + mx_scale_offset(r0 + row, tile * 4, tiles)) =
+            *reinterpret_cast<const unsigned*>(sscale + row * 8 + (i & 1) * 4);
+    }
+    __syncthreads();
   }
 }
 
-// The values of 8 columns per thread.
+// As mx_quantize_kernel, the other way.  A thread's 8 columns of a piece are
+// consecutive for 16-bit results and two groups of four, 128 apart, for FP32,
+// so that a warp's 16-byte stores are contiguous.
 template <int kFmt, typename T>
 __global__ void __launch_bounds__(kThreads)
     mx_dequantize_kernel(int R, int K, const unsigned char* __restrict__ codes, long long ldq,
                          const unsigned char* __restrict__ scales, T* __restrict__ Y,
                          long long ldy, bool vec) {
+  constexpr int G = sizeof(T) == 4 ? 2 : 1, W = 8 / G;    // groups of W columns
   wait_prior_grids();
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kRowsPerCta + (threadIdx.x >> 5);
+  if (r >= R) return;
   const int tiles = mx_scale_tiles(K);
-  const int chunks = (K + 255) / 256;
-  const long long items = (long long)R * chunks;
-  const long long warps = (long long)gridDim.x * (kThreads / 32);
-  for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += warps) {
-    const int r = (int)(it / chunks);
-    const int col = (int)(it - (long long)r * chunks) * 256 + lane * 8;
-    if (col >= K) continue;
-    const float scale = mx_scale_value(scales[mx_scale_offset(r, col >> 5, tiles)]);
-    const unsigned char* q = codes + (long long)r * ldq;
-    float v[8];
-    if constexpr (kFmt == GEMM_MXFP4) {
-      e2m1x8_to_f32(*reinterpret_cast<const unsigned*>(q + col / 2), v);
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(q + col);
-      int8x4_to_f32(w.x, v);
-      int8x4_to_f32(w.y, v + 4);
+  const int pieces = (K + 255) / 256;
+  const unsigned char* q = codes + (long long)r * ldq;
+  const unsigned char* srow = scales + mx_scale_offset(r, 0, tiles);
+  T* row = Y + (long long)r * ldy;
+  for (int p0 = blockIdx.y * kStep; p0 < pieces; p0 += gridDim.y * kStep) {
+    unsigned w[kStep][2];
+    unsigned s[kStep][G];
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int col = (p0 + i) * 256 + g * 128 + lane * W;
+        s[i][g] = 0u;
+        if constexpr (G == 1) w[i][1] = 0u;
+        w[i][g] = 0u;
+        if (col < K) {
+          if constexpr (kFmt == GEMM_MXFP4) {
+            if constexpr (G == 1)
+              w[i][0] = *reinterpret_cast<const unsigned*>(q + col / 2);
+            else
+              w[i][g] = *reinterpret_cast<const unsigned short*>(q + col / 2);
+          } else {
+            if constexpr (G == 1) {
+              const uint2 x = *reinterpret_cast<const uint2*>(q + col);
+              w[i][0] = x.x;
+              w[i][1] = x.y;
+            } else {
+              w[i][g] = *reinterpret_cast<const unsigned*>(q + col);
+            }
+          }
+          s[i][g] = srow[(col >> 7) * kMxTileBytes + ((col >> 5) & 3)];
+        }
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= scale;
-    T* dst = Y + (long long)r * ldy + col;
-    if (vec && col + 8 <= K) {
-      store8<T>(dst, v);
-    } else {
+    for (int i = 0; i < kStep; ++i) {
+      float v[8];
+      if constexpr (kFmt == GEMM_MXFP4) {
+        e2m1x8_to_f32(G == 1 ? w[i][0] : w[i][0] | (w[i][1] << 16), v);
+      } else {
+        int8x4_to_f32(w[i][0], v);
+        int8x4_to_f32(w[i][1], v + 4);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + j < K) dst[j] = from_f32_any<T>(v[j]);
+      for (int g = 0; g < G; ++g) {
+        const int col = (p0 + i) * 256 + g * 128 + lane * W;
+        const float scale = mx_scale_value(s[i][g]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[g * W + j] *= scale;
+        if (vec && col + W <= K) {
+          if constexpr (G == 1)
+            *reinterpret_cast<uint4*>(row + col) =
+                make_uint4(pack2_any<T>(v[0], v[1]), pack2_any<T>(v[2], v[3]),
+                           pack2_any<T>(v[4], v[5]), pack2_any<T>(v[6], v[7]));
+          else
+            *reinterpret_cast<float4*>(row + col) =
+                make_float4(v[g * W], v[g * W + 1], v[g * W + 2], v[g * W + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            if (col + j < K) row[col + j] = from_f32_any<T>(v[g * W + j]);
+        }
+      }
     }
   }
 }
 
-int grid_for(long long items) {
-  const long long ctas = (items + kThreads / 32 - 1) / (kThreads / 32);
-  return (int)(ctas < 65535 * 8 ? ctas : 65535 * 8);
+// CTAs of `rows` rows each, and along K of `step` pieces of 256 columns.
+dim3 grid_for(int R, int rows, int pieces, int step) {
+  const int y = (pieces + step - 1) / step;
+  return dim3((unsigned)((R + (long long)rows - 1) / rows), (unsigned)(y < 65535 ? y : 65535));
 }
 
 template <typename T>
@@ -173,23 +286,23 @@ bool rows16(const T* p, long long ld) {
 template <int kFmt, typename T>
 cudaError_t quantize_typed(int op, int R, int K, const T* X, long long ldx, unsigned char* codes,
                            long long ldq, unsigned char* scales, cudaStream_t stream) {
-  const int tiles = mx_scale_tiles(K);
-  if (op == GEMM_OP_N) {
-    const long long items = (long long)R * ((tiles + 1) / 2);
-    return launch_gemm_kernel(mx_quantize_kernel<kFmt, T>, dim3(grid_for(items)), dim3(kThreads), 0,
-                              stream, R, K, X, ldx, rows16(X, ldx), codes, ldq, scales);
-  }
-  const long long items = (long long)((R + 31) / 32) * tiles * kMxTileBlocks;
-  return launch_gemm_kernel(mx_quantize_t_kernel<kFmt, T>, dim3(grid_for(items)), dim3(kThreads),
-                            0, stream, R, K, X, ldx, codes, ldq, scales);
+  const int pieces = (mx_scale_tiles(K) + 1) / 2;
+  if (op == GEMM_OP_N)
+    return launch_gemm_kernel(mx_quantize_kernel<kFmt, T>, grid_for(R, kRowsPerCta, pieces, kStep),
+                              dim3(kThreads), 0, stream, R, K, X, ldx, rows16(X, ldx), codes, ldq,
+                              scales);
+  const bool vec = (reinterpret_cast<uintptr_t>(X) & 3u) == 0 && ldx % 2 == 0;
+  return launch_gemm_kernel(mx_quantize_t_kernel<kFmt, T>,
+                            grid_for(R, TLayout<kFmt, T>::kRows, pieces, 1), dim3(kThreads), 0,
+                            stream, R, K, X, ldx, vec, codes, ldq, scales);
 }
 
 template <int kFmt, typename T>
 cudaError_t dequantize_typed(int R, int K, const unsigned char* codes, long long ldq,
                              const unsigned char* scales, T* Y, long long ldy,
                              cudaStream_t stream) {
-  const long long items = (long long)R * ((K + 255) / 256);
-  return launch_gemm_kernel(mx_dequantize_kernel<kFmt, T>, dim3(grid_for(items)), dim3(kThreads), 0,
+  return launch_gemm_kernel(mx_dequantize_kernel<kFmt, T>,
+                            grid_for(R, kRowsPerCta, (K + 255) / 256, kStep), dim3(kThreads), 0,
                             stream, R, K, codes, ldq, scales, Y, ldy, rows16(Y, ldy));
 }
 
