@@ -295,15 +295,21 @@ __device__ __forceinline__ MxUnit mx_unit(int u, const MxSchedule& sc, int nk) {
   w.slice = u - v * sc.slices;
   w.kb = (int)((long long)w.slice * nk / sc.slices);
   w.ke = (int)((long long)(w.slice + 1) * nk / sc.slices);
+  int tm;
+  if (sc.by_halves) {
+    grouped_tile(v, sc.tiles_n, sc.halves_m, sc.group, w.tn, tm);
+    w.rows = kMxPairTile / 2;
+    w.row0 = tm * w.rows;
+    return w;
+  }
   int tile = v, off = 0;
   w.rows = kMxPairTile;
-  if (v >= sc.full_tiles) {
+  if (v >= sc.full_tiles) {   // (the second half can lie past M: the roles skip it)
     const int j = v - sc.full_tiles;
     tile = sc.full_tiles + (j >> 1);
     off = (j & 1) * (kMxPairTile / 2);
     w.rows = kMxPairTile / 2;
   }
-  int tm;
   grouped_tile(tile, sc.tiles_n, sc.tiles_m, sc.group, w.tn, tm);
   w.row0 = tm * kMxPairTile + off;
   return w;

@@ -46,16 +46,23 @@ cudaError_t launch_mx_dequantize(int fmt, int dtype, int R, int K, const void* c
                                  cudaStream_t stream);
 
 // Schedule of the kernels that compute 256 x 256 tiles of C on CTA pairs:
-// tiles [0, full_tiles) whole, the rest as two halves of 128 rows of C, each
-// over `slices` ranges of K (slices > 1: FP32 partial results at
-// ws + slice * M * ldw, summed by launch_splitk_reduce).
+// tiles [0, full_tiles) whole and the rest as two halves of 128 rows of C
+// (by_halves: all of C as halves), each over `slices` ranges of K (slices > 1:
+// FP32 partial results at ws + slice * M * ldw, summed by launch_mx_reduce).
 struct MxSchedule {
   int tiles_m, tiles_n;     // tiles of C along its rows and columns
+  int halves_m;             // halves along its rows
+  int by_halves;
   int full_tiles, units;    // units: all halves and tiles, times slices
   int slices;
   int group;                // tile columns per rasterisation group
 };
 constexpr int kMxPairTile = 256;
+
+// C := alpha * (the sum over s of ws[s * M * ldw + i * ldw + j], in slice
+// order) + beta * C; dtype of C.  ldw is a multiple of 4.
+cudaError_t launch_mx_reduce(const float* ws, int slices, int M, int N, long long ldw, float alpha,
+                             float beta, void* C, long long ldc, int dtype, cudaStream_t stream);
 
 // C := alpha * A . B^T + beta * C on tcgen05 block-scaled FP4.
 struct Mx4Params {

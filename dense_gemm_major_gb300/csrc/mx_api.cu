@@ -151,34 +151,56 @@ gemm_status_t scale_only(int dtype, int M, int N, float beta, void* C, int ldc,
   return status_of(dgemm::launch_scale_c(C, M, N, ldc, dtype, beta, stream));
 }
 
-// Schedule of an M x N product of nk k-tiles on `pairs` CTA pairs.
-//  * Enough tiles for a round: whole 256 x 256 tiles; those of a last
-//    partial round run as halves when the halves fit one round.
-//  * Fewer tiles than pairs: halves if they still fit one round (or if C has
-//    no second half), and the remaining pairs share out K: as many slices as
-//    fit, of at least kMinSlice k-tiles each, because a slice costs a pass
-//    over an FP32 copy of C.
+// Schedule of an M x N product of nk k-tiles on `pairs` CTA pairs: whole
+// 256 x 256 tiles (those of a last partial round as halves, when the halves
+// fit one round), or halves of 128 rows, each over 1 .. kMaxSlices ranges of
+// K; whichever the model below, in us, finds quickest.  Its constants are
+// measured on GB300 (per kernel: a k-tile of a whole tile and of a half; the
+// rest is common).
+struct StageCost {
+  double whole, half;
+};
+constexpr int kMaxSlices = 16;
 constexpr long long kWorkspaceCap = 256ll << 20;   // bytes of partial results
-dgemm::MxSchedule schedule(int M, int N, int nk, int pairs, int group, int min_slice) {
+constexpr double kUnitCost = 1.2;                  // pipeline fill, drain, store
+constexpr double kReduceCost = 2.0;                // the launch that sums the slices,
+constexpr double kReduceBytesPerUs = 6e6;          // and what it reads
+dgemm::MxSchedule schedule(int M, int N, int nk, int pairs, int group, StageCost cost) {
   dgemm::MxSchedule sc;
   sc.tiles_m = ceil_div(M, dgemm::kMxPairTile);
   sc.tiles_n = ceil_div(N, dgemm::kMxPairTile);
+  sc.halves_m = ceil_div(M, dgemm::kMxPairTile / 2);
   sc.group = group;
-  sc.slices = 1;
-  const int tiles = sc.tiles_m * sc.tiles_n;
-  if (tiles >= pairs) {
-    const int rem = tiles % pairs;
-    sc.full_tiles = 2 * rem <= pairs ? tiles - rem : tiles;
-  } else {
-    sc.full_tiles = M <= dgemm::kMxPairTile / 2 || 2 * tiles <= pairs ? 0 : tiles;
-    const int used = sc.full_tiles > 0 ? tiles : tiles * (M <= dgemm::kMxPairTile / 2 ? 1 : 2);
-    const long long slice_bytes = (long long)M * (((long long)N + 3) / 4 * 4) * 4;
-    int s = pairs / used;
-    if (s > nk / min_slice) s = nk / min_slice;
-    while (s > 1 && s * slice_bytes > kWorkspaceCap) --s;
-    if (s > 1) sc.slices = s;
+  const long long tiles = (long long)sc.tiles_m * sc.tiles_n;
+  const long long halves = (long long)sc.halves_m * sc.tiles_n;
+  const long long slice_bytes = (long long)M * (((long long)N + 3) / 4 * 4) * 4;
+  double best = -1.0;
+  auto take = [&](double us, bool by_halves, int slices) {
+    if (best >= 0.0 && us >= best - 1e-9) return;
+    best = us;
+    sc.by_halves = by_halves ? 1 : 0;
+    sc.slices = slices;
+  };
+  for (int s = 1; s <= kMaxSlices && s <= nk; ++s) {
+    if (s > 1 && s * slice_bytes > kWorkspaceCap) break;
+    const double k = (double)ceil_div(nk, s);
+    const double extra = s > 1 ? kReduceCost + (double)(s * slice_bytes) / kReduceBytesPerUs : 0.0;
+    const long long hr = (halves * s + pairs - 1) / pairs;
+    take((double)hr * (k * cost.half + kUnitCost) + extra, true, s);
+    const long long rem = tiles * s % pairs;
+    const bool split_rest = s == 1 && rem > 0 && 2 * rem <= pairs;
+    double us = (double)(tiles * s / pairs) * (k * cost.whole + kUnitCost);
+    if (rem > 0) us += (split_rest ? k * cost.half : k * cost.whole) + kUnitCost;
+    take(us + extra, false, s);
   }
-  sc.units = (sc.full_tiles + 2 * (tiles - sc.full_tiles)) * sc.slices;
+  if (sc.by_halves) {
+    sc.full_tiles = 0;
+    sc.units = (int)(halves * sc.slices);
+  } else {
+    const long long rem = tiles % pairs;
+    sc.full_tiles = (int)(sc.slices == 1 && 2 * rem <= pairs ? tiles - rem : tiles);
+    sc.units = (int)((sc.full_tiles + 2 * (tiles - sc.full_tiles)) * sc.slices);
+  }
   return sc;
 }
 
@@ -214,11 +236,11 @@ gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X
   p.vec = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
   p.sa = static_cast<const unsigned char*>(sa);
   p.sb = static_cast<const unsigned char*>(sb);
-  // As many CTAs (2, 4 or 8 of a cluster) to a tile's K as keep one wave,
-  // each with a stage at least.
+  // As many CTAs (2, 4 or 8 of a cluster) to a tile's K as keep one wave of
+  // two CTAs per SM, each with a stage at least.
   p.split = 1;
   const int tiles = ceil_div(N, 128), nk = ceil_div(K, dgemm::kMx4FewBK);
-  while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= 2 * max_pairs) p.split *= 2;
+  while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= 4 * max_pairs) p.split *= 2;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc, p.dtype = dtype;
   p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
@@ -245,7 +267,7 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
     return GEMM_ERR_LAUNCH;
   dgemm::Mx4Params p;
   p.M = M, p.N = N, p.K = K;
-  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, 2);
+  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, {0.76, 0.48});
   gemm_status_t st = partials(p.sched, M, N, stream, &p.ws, &p.ldw);
   if (st != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
@@ -254,8 +276,8 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
   const int pairs = p.sched.units < max_pairs ? p.sched.units : max_pairs;
   cudaError_t e = dgemm::launch_mx4(p, &tmA, &tmB, &tmSA, &tmSB, pairs, stream);
   if (e == cudaSuccess && p.sched.slices > 1)
-    e = dgemm::launch_splitk_reduce(p.ws, p.sched.slices, M, N, p.ldw, C, ldc, dtype, alpha, beta,
-                                    stream);
+    e = dgemm::launch_mx_reduce(p.ws, p.sched.slices, M, N, p.ldw, alpha, beta, C, ldc, dtype,
+                                stream);
   return status_of(e);
 }
 
@@ -422,7 +444,7 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
   p.sb = static_cast<const unsigned char*>(b_scales);
   const int nk = ceil_div(K, dgemm::kMxGradBK);
-  p.sched = schedule(M, N, nk, max_pairs, 8, 4);
+  p.sched = schedule(M, N, nk, max_pairs, 8, {0.86, 0.60});
   // FP32 results: at most 1024 terms per sum in tensor memory.
   p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
   if ((st = partials(p.sched, M, N, stream, &p.ws, &p.ldw)) != GEMM_OK) return st;
@@ -432,8 +454,8 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   const int pairs = p.sched.units < max_pairs ? p.sched.units : max_pairs;
   cudaError_t e = dgemm::launch_mx_grad(p, &tmA, &tmB, pairs, stream);
   if (e == cudaSuccess && p.sched.slices > 1)
-    e = dgemm::launch_splitk_reduce(p.ws, p.sched.slices, M, N, p.ldw, C, ldc, dtype_c, alpha,
-                                    beta, stream);
+    e = dgemm::launch_mx_reduce(p.ws, p.sched.slices, M, N, p.ldw, alpha, beta, C, ldc, dtype_c,
+                                stream);
   return status_of(e);
 }
 

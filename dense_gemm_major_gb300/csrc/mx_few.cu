@@ -28,13 +28,14 @@ constexpr uint32_t kSBytes = kChunks * kMxTileBytes;     // 1 KB
 // MT: rows of A that the MMA computes.
 template <int MT>
 struct Layout {
-  static constexpr int kStages = MT <= 64 ? 8 : 6;
-  // The quantising warps work in groups, each on stages of its own: with few
-  // rows a warp per stage, so that all stages' loads of A are in flight at
-  // once.  Stages are a multiple of groups: a slot's stages all fall to one
-  // group, which therefore never waits for a phase whose predecessor it has
-  // not seen.
-  static constexpr int kGroups = MT <= 16 ? 8 : 4;
+  // Two CTAs fit an SM, so that one's MMAs and scale copies run beside the
+  // other's: 64 x 8192 x 8192 took 14 us with one of twice the stages.
+  static constexpr int kStages = MT <= 64 ? 4 : 3;
+  // The quantising warps work in groups, each on stages of its own, so that
+  // several stages' loads of A are in flight at once.  Stages are a multiple
+  // of groups: a slot's stages all fall to one group, which therefore never
+  // waits for a phase whose predecessor it has not seen.
+  static constexpr int kGroups = 4;
   static constexpr int kGroupWarps = 8 / kGroups;
   static_assert(MT > 64 || kStages % kGroups == 0, "one group per slot");
   static constexpr uint32_t kABytes = MT * BK / 2;
@@ -44,7 +45,7 @@ struct Layout {
   static constexpr uint32_t kTmemCols = MT <= 32 ? 64 : (MT <= 64 ? 128 : 256);   // two stages
   static_assert(kScaleCol + 4 * 4 * kChunks <= kTmemCols, "tensor memory");
   static_assert(MT * BN * 4 <= kStages * kStage, "partial tiles reuse the ring");
-  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
 };
 
 template <int S>
@@ -95,7 +96,7 @@ __device__ __forceinline__ void store_scaled(T* c, float sum, float alpha, float
 
 // kRaw: A is p.X, an array of T.
 template <int MT, typename T, bool kRaw>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     mx4_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const Mx4FewParams p) {
   using L = Layout<MT>;
