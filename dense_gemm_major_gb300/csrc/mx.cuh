@@ -255,12 +255,14 @@ __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, unsigne
     }
   }
 }
-// The same by a warp, each lane polling: quicker than a broadcast of one
+// The same by a warp, each lane polling (`ready`: what an earlier try of the
+// lane gave): quicker than a broadcast of one
 // lane's result (220 cycles) where the barrier is mostly complete already.
 __device__ __forceinline__ bool role_wait_lanes(uint32_t bar, uint32_t parity, unsigned* fault,
                                                 unsigned long long timeout_ns, int* abort,
-                                                unsigned code) {
-  return __all_sync(0xffffffffu, role_wait(bar, parity, fault, timeout_ns, abort, code, true));
+                                                unsigned code, bool ready = false) {
+  return __all_sync(0xffffffffu,
+                    ready || role_wait(bar, parity, fault, timeout_ns, abort, code, true));
 }
 // The same by a warp: lane 0 waits, the result is broadcast.
 __device__ __forceinline__ bool role_wait_warp(uint32_t bar, uint32_t parity, unsigned* fault,
@@ -280,6 +282,18 @@ __device__ __forceinline__ bool role_wait_warp(uint32_t bar, uint32_t parity, un
 __device__ __forceinline__ void mbar_arrive_any_cta(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// Position in a ring of N slots: slot and the parity of its current use.
+template <int N>
+struct RingPos {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // ------------------------------------------------------------ pair schedule
 
@@ -343,6 +357,41 @@ __device__ __forceinline__ void store_rows32(const float* v, T* c, long long ldc
     }
     c += 8 * ldc;
   }
+}
+
+// The same by a whole warp (lanes with consecutive columns, the first even) for
+// a 16-bit C whose rows are 4-byte aligned and of even width, without beta:
+// lanes swap with their neighbour, so that each stores two columns of every
+// other row, in half as many stores.
+template <typename T>
+__device__ __forceinline__ void store_rows32_pairs(const float* v, T* c, long long ldc,
+                                                   int rows_left, bool inside, float alpha) {
+  const bool odd = threadIdx.x & 1;
+  T* p = c + (odd ? ldc - 1 : 0);
+  const int left = inside ? rows_left - (odd ? 1 : 0) : 0;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+    const uint32_t w = odd ? pack2<T>(alpha * got, alpha * v[j + 1]) : pack2<T>(alpha * v[j], alpha * got);
+    if (j < left) *reinterpret_cast<uint32_t*>(p) = w;
+    p += 2 * ldc;
+  }
+}
+
+// One warp's 32 x 32 piece of C by whichever of the two fits; `pairs`: C is
+// 4-byte aligned, ldc and N even.
+template <typename T>
+__device__ __forceinline__ void store_piece(const float* v, T* C, long long ldc, int M, int N,
+                                            int row, int col, bool pairs, float alpha,
+                                            float beta) {
+  T* c = C + (long long)row * ldc + col;
+  if constexpr (sizeof(T) == 2) {
+    if (pairs && beta == 0.f) {
+      store_rows32_pairs<T>(v, c, ldc, M - row, col < N, alpha);
+      return;
+    }
+  }
+  if (col < N) store_rows32<T>(v, c, ldc, M - row, alpha, beta);
 }
 
 // 16 consecutive FP32 columns of this thread's TMEM lane, waited for.

@@ -85,7 +85,7 @@ cudaError_t launch_mx4(const Mx4Params& p, const CUtensorMap* tmA, const CUtenso
                        const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
                        cudaStream_t stream);
 
-// C := alpha * A . B^T + beta * C for up to 128 rows of A, which are given in
+// C := alpha * A . B^T + beta * C for up to 64 rows of A, which are given in
 // MXFP4 (tmA, sa) or, up to 48, as an array X of dtype that the kernel
 // quantises.
 struct Mx4FewParams {
@@ -103,14 +103,16 @@ struct Mx4FewParams {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-constexpr int kMx4FewRows = 128, kMx4FewBK = 256;
+// (With a tile of 128 rows, CTA pairs and a reduction were quicker: 128 x 2048 x
+// 2048 7.7 against 9.7 us, 128 x 8192 x 8192 13.3 against 14.8.)
+constexpr int kMx4FewRows = 64, kMx4FewBK = 256;
 // Quantising inside the kernel saves a launch (2.7 us of a calling thread)
 // but is done anew by the CTAs of every 128 columns: on the GPU, N = K = 4096,
 // inside / before the kernel: 1 row 5.3 / 6.0 us, 16 7.6 / 6.8, 33 9.3 / 8.1,
 // 48 10.6 / 8.7, 64 12.5 / 9.5, against some 11 us of CPU for two launches.
 constexpr int kMx4FewRawRows = 48;
 // Rows of A that the kernel computes for M of them.
-inline int mx4_few_tile(int M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+inline int mx4_few_tile(int M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
 // tmA: A's codes as bytes, boxes of 128 bytes x mx4_few_tile(M) rows; tmB:
 // B's, boxes of 128 bytes x 128 rows.
 cudaError_t launch_mx4_few(const Mx4FewParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,

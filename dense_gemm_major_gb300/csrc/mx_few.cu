@@ -1,10 +1,10 @@
-// C = alpha * A . B^T + beta * C for up to 128 rows of A (decoding, small
+// C = alpha * A . B^T + beta * C for up to 64 rows of A (decoding, small
 // batches), B (N x K) in MXFP4; A either in MXFP4 or, up to 48 rows, a 16- or
 // 32-bit array that is quantised to MXFP4 on the way, in the same launch.
 //
 // What bounds it is reading B once (N K 17 / 32 bytes) and, for a few rows,
 // latency.  B's rows are the M side of tcgen05.mma.kind::mxf4 (128 columns of
-// C per CTA) and A's its N side (16 to 128), so that no tile is wasted on
+// C per CTA) and A's its N side (16 to 64), so that no tile is wasted on
 // rows that do not exist.  So that B's bytes travel to all SMs at once, the
 // CTAs of a cluster share a tile's K; they add their FP32 partial tiles
 // through distributed shared memory in rank order, so results are
@@ -30,19 +30,19 @@ template <int MT>
 struct Layout {
   // Two CTAs fit an SM, so that one's MMAs and scale copies run beside the
   // other's: 64 x 8192 x 8192 took 14 us with one of twice the stages.
-  static constexpr int kStages = MT <= 64 ? 4 : 3;
+  static constexpr int kStages = 4;
   // The quantising warps work in groups, each on stages of its own, so that
   // several stages' loads of A are in flight at once.  Stages are a multiple
   // of groups: a slot's stages all fall to one group, which therefore never
   // waits for a phase whose predecessor it has not seen.
   static constexpr int kGroups = 4;
   static constexpr int kGroupWarps = 8 / kGroups;
-  static_assert(MT > 64 || kStages % kGroups == 0, "one group per slot");
+  static_assert(kStages % kGroups == 0, "one group per slot");
   static constexpr uint32_t kABytes = MT * BK / 2;
   static constexpr uint32_t kStage = (kBBytes + kABytes + 2 * kSBytes + 1023) / 1024 * 1024;
   static constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;
   static constexpr uint32_t kScaleCol = MT;              // TMEM: accumulator, then scales of
-  static constexpr uint32_t kTmemCols = MT <= 32 ? 64 : (MT <= 64 ? 128 : 256);   // two stages
+  static constexpr uint32_t kTmemCols = MT <= 32 ? 64 : 128;   // two stages
   static_assert(kScaleCol + 4 * 4 * kChunks <= kTmemCols, "tensor memory");
   static_assert(MT * BN * 4 <= kStages * kStage, "partial tiles reuse the ring");
   static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
@@ -333,10 +333,8 @@ cudaError_t launch_rows(const Mx4FewParams& p, const CUtensorMap* a, const CUten
       return raw ? launch_typed<16, T, true>(p, a, b, s) : launch_typed<16, T, false>(p, a, b, s);
     case 32:
       return raw ? launch_typed<32, T, true>(p, a, b, s) : launch_typed<32, T, false>(p, a, b, s);
-    case 64:
-      return raw ? launch_typed<64, T, true>(p, a, b, s) : launch_typed<64, T, false>(p, a, b, s);
     default:
-      return raw ? cudaErrorInvalidValue : launch_typed<128, T, false>(p, a, b, s);
+      return raw ? launch_typed<64, T, true>(p, a, b, s) : launch_typed<64, T, false>(p, a, b, s);
   }
 }
 

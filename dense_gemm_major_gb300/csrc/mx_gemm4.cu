@@ -119,16 +119,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Lane l of warp q writes lane 32 q + l: row l of a tile, 16 bytes, is its
     // four columns there, the same in all four quarters.
     const uint32_t t = tmem_base + ((uint32_t)(warp * 32) << 16) + kScaleCol;
-    uint32_t it = 0;
+    RingPos<S> pos;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
       const MxUnit w = mx_unit(u, sc, nk);
       if (w.row0 >= p.M) continue;
-      for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
-        const uint32_t s = it % S;
+      for (int kt = w.kb; kt < w.ke; ++kt, pos.next()) {
+        const uint32_t s = pos.slot;
         // (The loads were issued after the MMAs on this stage had finished, so
         // its columns may be overwritten.)
-        ok = role_wait_lanes(smem_u32(&bars->scales[s]), (it / S) & 1u, p.fault, p.timeout_ns,
+        ok = role_wait_lanes(smem_u32(&bars->scales[s]), pos.parity, p.fault, p.timeout_ns,
                              &bars->abort, kFaultTcProducerWait);
         if (!ok) break;
         const uint4* tile =
@@ -156,6 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kLoadWarp && lane == 0) {
       // ---------------------------------------------- loads (both CTAs)
+      RingPos<S> pos;
       uint32_t it = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
@@ -164,9 +165,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int halves = w.rows / 128;            // 64-row boxes of A per CTA
         const int row = w.row0 + (int)rank * (w.rows / 2);
         const int ct = w.tn * 2 + (int)rank;
-        for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
-          const uint32_t s = it % S;
-          ok = role_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
+        for (int kt = w.kb; kt < w.ke; ++kt, ++it, pos.next()) {
+          const uint32_t s = pos.slot;
+          ok = role_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
                          &bars->abort, kFaultTcProducerWait, true);
           if (!ok) break;
           const uint32_t fb = mapa_shared(smem_u32(&bars->full[s]), 0);
@@ -193,25 +194,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp && rank == 0 && lane == 0) {
       // ---------------------------------------------- MMA issuer (even CTA)
-      uint32_t it = 0, local = 0;
+      // The barrier of the next stage is tried before this stage's MMAs are
+      // issued: a try takes over 100 cycles to answer.
+      RingPos<S> pos;
+      bool ready = false;
+      uint32_t local = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
         const MxUnit w = mx_unit(u, sc, nk);
         if (w.row0 >= p.M) continue;
-        const int halves = w.rows / 128;
         const uint32_t idesc = instr_desc_mx4(256, (uint32_t)w.rows, 0);
         const uint32_t idesc2 = instr_desc_mx4(256, (uint32_t)w.rows, 2);
         ok = role_wait(smem_u32(&bars->acc_empty), (local & 1u) ^ 1u, p.fault,
                                p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
         if (!ok) break;
         tc_fence_after();
-        for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
-          const uint32_t s = it % S;
-          ok = role_wait(smem_u32(&bars->full[s]), (it / S) & 1u, p.fault, p.timeout_ns,
-                                 &bars->abort, kFaultTcMmaWait, true);
+        for (int kt = w.kb; kt < w.ke; ++kt) {
+          const uint32_t s = pos.slot;
+          const uint32_t st = smem_u32(base + s * kStage);
+          ok = ready || role_wait(smem_u32(&bars->full[s]), pos.parity, p.fault, p.timeout_ns,
+                                  &bars->abort, kFaultTcMmaWait, true);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(base + s * kStage);
+          pos.next();
+          ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
           const uint32_t blo = desc_lo(st, 16), alo = desc_lo(st + kBBytes, 16);
           const uint32_t sfb = tmem_base + kScaleCol + s * kScaleStage;
           const uint32_t sfa = sfb + 4 * kChunks;
@@ -239,6 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Warp: TMEM lanes 32 q .. 32 q + 31 (columns of C), half of the rows.
     const int q = warp & 3;
     const int half = (warp - kEpiWarp) >> 2;
+    const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 && ((p.ldc | p.N) & 1) == 0;
     uint32_t local = 0;
     for (int u = blockIdx.x >> 1; u < sc.units; u += npairs) {
       const MxUnit w = mx_unit(u, sc, nk);
@@ -261,19 +268,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty), 0));
       const int col = w.tn * 256 + (int)rank * 128 + q * 32 + lane;
-      if (col < p.N) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < chunks) {
-            const int row = w.row0 + first + c * 32;
-            const float* v = reinterpret_cast<const float*>(r[c]);
-            if (sc.slices == 1)
-              store_rows32<T>(v, static_cast<T*>(p.C) + (long long)row * p.ldc + col, p.ldc,
-                              p.M - row, p.alpha, p.beta);
-            else
-              store_rows32<float>(v, p.ws + ((long long)w.slice * p.M + row) * p.ldw + col, p.ldw,
-                                  p.M - row, 1.f, 0.f);
-          }
+      for (int c = 0; c < 4; ++c) {
+        if (c < chunks) {
+          const int row = w.row0 + first + c * 32;
+          const float* v = reinterpret_cast<const float*>(r[c]);
+          if (sc.slices == 1)
+            store_piece<T>(v, static_cast<T*>(p.C), p.ldc, p.M, p.N, row, col, pairs, p.alpha,
+                           p.beta);
+          else if (col < p.N)
+            store_rows32<float>(v, p.ws + ((long long)w.slice * p.M + row) * p.ldw + col, p.ldw,
+                                p.M - row, 1.f, 0.f);
         }
       }
     }

@@ -258,6 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------- op(A) (both CTAs)
+      RingPos<S> pos;
       uint32_t it = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
@@ -265,9 +266,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (w.row0 >= p.M) continue;
         const int boxes = w.rows / 128;               // of 64 rows of C, per CTA
         const int row = w.row0 + (int)rank * (w.rows / 2);
-        for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
-          const uint32_t s = it % S;
-          ok = role_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
+        for (int kt = w.kb; kt < w.ke; ++kt, ++it, pos.next()) {
+          const uint32_t s = pos.slot;
+          ok = role_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
                          &bars->abort, kFaultTcProducerWait, true);
           if (!ok) break;
           const uint32_t sa = smem_u32(base + s * kStage) + kConvBytes;
@@ -291,6 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 2 && lane == 0) {
       // ---------------------------------------------- codes and scales (both CTAs)
       const int ktiles = mx_scale_tiles(p.N);
+      RingPos<R> pos;
       uint32_t it = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
@@ -298,10 +300,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (w.row0 >= p.M) continue;
         const int ct = w.tn * 2 + (int)rank;          // this CTA's 128 columns
         const uint32_t sbytes = ct < ktiles ? (uint32_t)kMxTileBytes : 0u;
-        for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
-          const uint32_t r = it % R;
-          ok = role_wait(smem_u32(&bars->raw_empty[r]), ((it / R) & 1u) ^ 1u, p.fault,
-                         p.timeout_ns, &bars->abort, kFaultTcProducerWait, true);
+        for (int kt = w.kb; kt < w.ke; ++kt, ++it, pos.next()) {
+          const uint32_t r = pos.slot;
+          ok = role_wait(smem_u32(&bars->raw_empty[r]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                         &bars->abort, kFaultTcProducerWait, true);
           if (!ok) break;
           const uint32_t raw = smem_u32(sraw + r * L::kRawStage);
           const uint32_t rb = smem_u32(&bars->raw_full[r]);
@@ -315,7 +317,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1 && rank == 0 && lane == 0) {
       // ---------------------------------------------- MMA issuer (even CTA)
-      uint32_t it = 0, seg = 0;
+      // The barrier of the next stage is tried before this stage's MMAs are
+      // issued: a try takes over 100 cycles to answer.
+      RingPos<S> pos;
+      bool ready = false;
+      uint32_t seg = 0;
       bool ok = true;
       for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
         const MxUnit w = mx_unit(u, sc, nk);
@@ -328,13 +334,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                  p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
           if (!ok) break;
           tc_fence_after();
-          for (int kt = k0; kt < k1; ++kt, ++it) {
-            const uint32_t s = it % S;
-            ok = role_wait(smem_u32(&bars->full[s]), (it / S) & 1u, p.fault, p.timeout_ns,
-                                   &bars->abort, kFaultTcMmaWait, true);
+          for (int kt = k0; kt < k1; ++kt) {
+            const uint32_t st = smem_u32(base + pos.slot * kStage);
+            const uint32_t freed = smem_u32(&bars->empty[pos.slot]);
+            ok = ready || role_wait(smem_u32(&bars->full[pos.slot]), pos.parity, p.fault,
+                                    p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t st = smem_u32(base + s * kStage);
+            pos.next();
+            ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
             // MN-major tiles step by 16 rows of 128 bytes per 16 of K, K-major
             // ones by 32 bytes.
             const uint32_t blo = desc_lo(st, kBlock);
@@ -345,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               blo + (((k >> 2) * kConvHalf + (k & 3) * 2048) >> 4),
                               alo + (((k >> 2) * kAHalf + (k & 3) * (kAT ? 2048 : 32)) >> 4),
                               idesc, (kt > k0 || k > 0) ? 1u : 0u);
-            mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
+            mma_commit_pair_multicast(freed, 0x3);
           }
           if (!ok) break;
           mma_commit_pair_multicast(smem_u32(&bars->acc_full[b]), 0x3);
@@ -366,15 +374,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int unit = lane & 3, blk = (lane >> 3) & 1;
     const int row0 = 4 * v + ((lane >> 2) & 1) + 2 * (lane >> 4);
     const int column = blk * 64 + unit * 16;
-    uint32_t it = 0;
+    RingPos<R> rpos;
+    RingPos<S> pos;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
       const MxUnit w = mx_unit(u, sc, nk);
       if (w.row0 >= p.M) continue;
-      for (int kt = w.kb; kt < w.ke; ++kt, ++it) {
-        const uint32_t r = it % R, s = it % S;
-        ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), (it / R) & 1u, p.fault, p.timeout_ns,
-                             &bars->abort, kFaultTcProducerWait);
+      for (int kt = w.kb; kt < w.ke; ++kt, rpos.next(), pos.next()) {
+        const uint32_t r = rpos.slot, s = pos.slot;
+        // (Both tries are on their way at once.)
+        const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), rpos.parity);
+        const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u);
+        ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), rpos.parity, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait, loaded);
         if (!ok) break;
         const unsigned char* raw = sraw + r * L::kRawStage + half * 64 * L::kRawRow;
         const unsigned char* scales =
@@ -398,8 +410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // Rows past K: zero codes, and any finite scale.
           if (row >= rows_left) sb[i] = 0;
         }
-        ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault,
-                             p.timeout_ns, &bars->abort, kFaultTcProducerWait);
+        ok = role_wait_lanes(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait, freed);
         if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
@@ -434,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Warp: TMEM lanes 32 q .. 32 q + 31 (columns of C), half of the rows.
     const int q = warp & 3;
     const int half = (warp - kEpiWarp) >> 2;
+    const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 && ((p.ldc | p.N) & 1) == 0;
     uint32_t seg = 0;
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
@@ -466,19 +479,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const int col = w.tn * 256 + (int)rank * 128 + q * 32 + lane;
-      if (col < p.N) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < chunks) {
-            const int row = w.row0 + first + c * 32;
-            if (sc.slices == 1)
-              store_rows32<TC>(acc + c * 32, static_cast<TC*>(p.C) + (long long)row * p.ldc + col,
-                               p.ldc, p.M - row, p.alpha, p.beta);
-            else
-              store_rows32<float>(acc + c * 32,
-                                  p.ws + ((long long)w.slice * p.M + row) * p.ldw + col, p.ldw,
-                                  p.M - row, 1.f, 0.f);
-          }
+      for (int c = 0; c < 4; ++c) {
+        if (c < chunks) {
+          const int row = w.row0 + first + c * 32;
+          const float* v = acc + c * 32;
+          if (sc.slices == 1)
+            store_piece<TC>(v, static_cast<TC*>(p.C), p.ldc, p.M, p.N, row, col, pairs, p.alpha,
+                            p.beta);
+          else if (col < p.N)
+            store_rows32<float>(v, p.ws + ((long long)w.slice * p.M + row) * p.ldw + col, p.ldw,
+                                p.M - row, 1.f, 0.f);
         }
       }
     }
