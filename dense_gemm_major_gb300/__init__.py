@@ -450,38 +450,23 @@ def matmul(A, B, out=None, stream=None, alpha=1.0, beta=0.0):
 
 # ------------------------------------------------------------ microscaled operands
 #
-# A layer of a few tokens takes a few microseconds on the GPU, less than a
-# careless wrapper on the CPU: these look each tensor property up once, and
-# torch itself once per process.
+# These functions are thin: the extension _mxcall (csrc/mx_python.cpp) reads the
+# tensors, allocates the result and calls the C ABI.  A layer of a few tokens
+# takes a few microseconds on the GPU, less than the same steps in Python.
 
-_torch = None
-_TORCH_CODES = {}    # torch dtype -> dtype code
+_mx = None
 
 
-def _get_torch():
-    global _torch
-    if _torch is None:
-        import torch
-        _TORCH_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+def _load_mx():
+    """The extension, given torch's objects at its first use."""
+    global _mx
+    if _mx is None:
         load()
-        _torch = torch
-    return _torch
-
-
-def _dtype_code(dtype):
-    code = _TORCH_CODES.get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}: float32, float16 or bfloat16")
-    return code
-
-
-def _stream_of(stream, device):
-    """The given cudaStream_t, or torch's current stream on `device`."""
-    return stream if stream is not None else _torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _not_cuda():
-    raise ValueError("operands must be CUDA tensors")
+        import torch
+        from . import _mxcall as ext
+        ext.setup(torch, MXTensor, GemmError)
+        _mx = ext
+    return _mx
 
 
 class MXTensor:
@@ -529,131 +514,35 @@ class MXTensor:
     def device(self):
         return (self._codes if self._buffer is None else self._buffer).device
 
-    def _pointers(self):
-        """Device addresses of codes and scales."""
-        if self._buffer is not None:
-            p = self._buffer.data_ptr()
-            return p, p + self.rows * self._ld
-        if not self._codes.is_cuda:
-            _not_cuda()
-        return self._codes.data_ptr(), self._scales.data_ptr()
-
-
-def _rows_ld(t, rows, cols):
-    """Leading dimension of a row-major rows x cols tensor."""
-    s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
-        raise ValueError("operands must be 2-D row-major (unit column stride)")
-    return s0 if rows > 1 else max(cols, 1)
-
-
-def _result(out, M, N, dtype, device, beta=0.0):
-    if out is None:
-        if beta != 0:
-            raise ValueError("beta != 0 needs an existing out")
-        return _torch.empty((M, N), dtype=dtype, device=device), (N if N > 0 else 1)
-    if tuple(out.shape) != (M, N) or out.dtype != dtype or out.device != device:
-        raise ValueError("out has the wrong shape, dtype or device")
-    return out, _rows_ld(out, M, N)
-
 
 def mx_quantize(X, fmt="mxfp4", stream=None):
     """X (rows x cols; float32, float16 or bfloat16; row-major or a
     transposed view, read in place) in format ``fmt``: blocks of 32 along
     the columns.  Returns an MXTensor."""
-    torch = _torch or _get_torch()
-    if fmt != "mxfp4" and fmt != "mxint8":
-        raise ValueError("fmt must be 'mxfp4' or 'mxint8'")
-    if not X.is_cuda:
-        _not_cuda()
-    code = _dtype_code(X.dtype)
-    R, K = X.shape
-    s0, s1 = X.stride()
-    if s1 == 1 or K <= 1:
-        op, ldx = OP_N, (s0 if R > 1 else max(K, 1))
-    elif s0 == 1 or R <= 1:
-        op, ldx = OP_T, s1
-    else:
-        raise ValueError("operands must have a unit row or column stride")
     q = MXTensor.__new__(MXTensor)
     q._codes = q._scales = None
-    q.rows, q.cols, q.fmt = R, K, fmt
-    ldq = q._ld = ((K if fmt == "mxint8" else (K + 1) >> 1) + 15) & ~15
-    codes = R * ldq
-    device = X.device
-    q._buffer = torch.empty(codes + 512 * ((R + 127) >> 7) * ((K + 127) >> 7), dtype=torch.uint8,
-                            device=device)
-    p = q._buffer.data_ptr()
-    st = _lib.gemm_mx_quantize(_MX_CODES[fmt], code, op, R, K, X.data_ptr(), ldx, p, ldq, p + codes,
-                               _stream_of(stream, device))
-    if st != GEMM_OK:
-        raise GemmError(st, "gemm_mx_quantize")
+    q._buffer, q.rows, q.cols, q._ld = (_mx or _load_mx()).quantize(X, fmt, stream)
+    q.fmt = fmt
     return q
 
 
 def mx_dequantize(q, dtype=None, out=None, stream=None):
     """The values of MXTensor ``q`` as a rows x cols tensor of ``dtype``
     (default bfloat16, or that of ``out``)."""
-    torch = _torch or _get_torch()
-    if dtype is None:
-        dtype = torch.bfloat16 if out is None else out.dtype
-    code = _dtype_code(dtype)
-    codes, scales = q._pointers()
-    device = q.device
-    Y, ldy = _result(out, q.rows, q.cols, dtype, device)
-    st = _lib.gemm_mx_dequantize(_MX_CODES[q.fmt], code, q.rows, q.cols, codes, q._ld, scales,
-                                 Y.data_ptr(), ldy, _stream_of(stream, device))
-    if st != GEMM_OK:
-        raise GemmError(st, "gemm_mx_dequantize")
-    return Y
+    return (_mx or _load_mx()).dequantize(q, dtype, out, stream)
 
 
 def mx_matmul(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     """alpha * (A @ B.T) + beta * out for MXFP4 operands A (M x K) and B
     (N x K); the result is of ``dtype`` (default bfloat16, or that of
     ``out``)."""
-    torch = _torch or _get_torch()
-    if A.fmt != "mxfp4" or B.fmt != "mxfp4":
-        raise ValueError("mx_matmul takes mxfp4 operands")
-    if A.cols != B.cols:
-        raise ValueError(f"inner dimensions differ: {A.cols} vs {B.cols}")
-    if dtype is None:
-        dtype = torch.bfloat16 if out is None else out.dtype
-    code = _dtype_code(dtype)
-    pa, sa = A._pointers()
-    pb, sb = B._pointers()
-    device = A.device
-    M, N = A.rows, B.rows
-    C, ldc = _result(out, M, N, dtype, device, beta)
-    st = _lib.gemm_mx4(code, M, N, A.cols, alpha, pa, A._ld, sa, pb, B._ld, sb, beta, C.data_ptr(),
-                       ldc, _stream_of(stream, device))
-    if st != GEMM_OK:
-        raise GemmError(st, "gemm_mx4")
-    return C
+    return (_mx or _load_mx()).matmul(A, B, out, dtype, alpha, beta, stream)
 
 
 def mx_linear(x, W, out=None, stream=None):
     """x @ W.T with x (M x K) quantised to MXFP4 on the way and W (N x K) an
     MXFP4 MXTensor; the result has x's dtype."""
-    _torch or _get_torch()
-    if not x.is_cuda:
-        _not_cuda()
-    dtype = x.dtype
-    code = _dtype_code(dtype)
-    if W.fmt != "mxfp4":
-        raise ValueError("mx_linear takes mxfp4 weights")
-    M, K = x.shape
-    if K != W.cols:
-        raise ValueError(f"inner dimensions differ: {K} vs {W.cols}")
-    codes, scales = W._pointers()
-    device = x.device
-    N = W.rows
-    Y, ldy = _result(out, M, N, dtype, device)
-    st = _lib.gemm_mx4_linear(code, M, N, K, x.data_ptr(), _rows_ld(x, M, K), codes, W._ld, scales,
-                              Y.data_ptr(), ldy, _stream_of(stream, device))
-    if st != GEMM_OK:
-        raise GemmError(st, "gemm_mx4_linear")
-    return Y
+    return (_mx or _load_mx()).linear(x, W, out, stream)
 
 
 def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
@@ -662,37 +551,4 @@ def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     is the gradient of a layer's input, ``mx_grad(dY.t(), kept_x)`` that of
     its weights.  The result is of A's dtype or float32 (``dtype``, or that
     of ``out``)."""
-    torch = _torch or _get_torch()
-    if not A.is_cuda:
-        _not_cuda()
-    ta = A.dtype
-    code = _dtype_code(ta)
-    if code == 0:
-        raise ValueError("mx_grad takes a float16 or bfloat16 A")
-    M, K = A.shape
-    if K != B.rows:
-        raise ValueError(f"inner dimensions differ: {K} vs {B.rows}")
-    if dtype is None:
-        dtype = ta if out is None else out.dtype
-    if dtype != ta and dtype != torch.float32:
-        raise ValueError("the result is of A's dtype or float32")
-    # The leading dimension (a multiple of 8) of a single stored row is free,
-    # so it is rounded up; a single column with unit stride is a single row
-    # stored transposed.
-    s0, s1 = A.stride()
-    if (s1 == 1 or K <= 1) and not (K == 1 and M > 1 and s0 == 1):
-        op, lda = OP_N, (s0 if M > 1 else (K + 7) & ~7)
-    elif s0 == 1 or M <= 1:
-        op, lda = OP_T, (s1 if K > 1 else (M + 7) & ~7)
-    else:
-        raise ValueError("operands must have a unit row or column stride")
-    codes, scales = B._pointers()
-    device = A.device
-    N = B.cols
-    C, ldc = _result(out, M, N, dtype, device, beta)
-    st = _lib.gemm_mx_grad(_MX_CODES[B.fmt], code, op, _TORCH_CODES[dtype], M, N, K, alpha,
-                           A.data_ptr(), lda, codes, B._ld, scales, beta, C.data_ptr(), ldc,
-                           _stream_of(stream, device))
-    if st != GEMM_OK:
-        raise GemmError(st, "gemm_mx_grad")
-    return C
+    return (_mx or _load_mx()).grad(A, B, out, dtype, alpha, beta, stream)

@@ -1,4 +1,5 @@
-"""In-tree build of the CUDA library (libdense_gemm.so) for sm_103a.
+"""In-tree build of the CUDA library (libdense_gemm.so) for sm_103a, and of
+the CPython extension (_mxcall.so) that calls its microscaled entry points.
 
 Each translation unit under csrc/ is compiled by its own nvcc process, in
 parallel, then linked into one shared library next to this file.  A unit is
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libdense_gemm.so")
+# The CPython extension around the microscaled entry points.
+EXT_SOURCE = os.path.join(CSRC, "mx_python.cpp")
+EXT = os.path.join(PKG, "_mxcall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -80,7 +85,23 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.check_call(cmd)
+    build_extension(verbose)
     return LIB
+
+
+def build_extension(verbose: bool = False) -> None:
+    """_mxcall.so, linked to libdense_gemm.so beside it."""
+    newest = max([os.path.getmtime(EXT_SOURCE)] + [os.path.getmtime(h) for h in _headers()])
+    if os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
+        return
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") \
+        if os.path.dirname(nvcc()) else "/usr/local/cuda/include"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", EXT_SOURCE, "-o", EXT,
+           "-I", INCLUDE, "-I", cuda, "-I", sysconfig.get_paths()["include"],
+           "-L", PKG, "-ldense_gemm", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
 
 
 if __name__ == "__main__":
