@@ -53,14 +53,16 @@ constexpr uint32_t kStage = kConvBytes + kABytes;         // 64 KB
 constexpr int S = 3;
 constexpr uint32_t kTmemCols = 512;                       // two accumulators
 static_assert(BK == kMxTileRows, "a stage needs one tile of scales per CTA");
-static_assert(kHalves * kConvGroup * 32 == 256, "a converting group per half");
 
 template <int kFmt>
 struct Layout {
   static constexpr uint32_t kRawRow = kFmt == GEMM_MXFP4 ? 64 : 128;   // 128 codes
   static constexpr uint32_t kRaw = kRawRow * BK;
   static constexpr uint32_t kRawStage = kRaw + kMxTileBytes;
-  static constexpr int kRawStages = kFmt == GEMM_MXFP4 ? 3 : 2;
+  // (Even: a slot's stages all fall to one group of converting warps, which
+  // therefore never waits for a phase whose predecessor it has not seen.)
+  static constexpr int kRawStages = 2;
+  static_assert(kRawStages % 2 == 0, "one group per slot");
   static constexpr uint32_t kSmem = S * kStage + kRawStages * kRawStage + 1024 + 512;
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -225,12 +227,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&bars->full[s]), 1 + 2 * kHalves * kConvGroup);
+      mbar_init(smem_u32(&bars->full[s]), 1 + 2 * kConvGroup);
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     for (int r = 0; r < R; ++r) {
       mbar_init(smem_u32(&bars->raw_full[r]), 1);
-      mbar_init(smem_u32(&bars->raw_empty[r]), kHalves * kConvGroup);
+      mbar_init(smem_u32(&bars->raw_empty[r]), kConvGroup);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&bars->acc_full[b]), 1);
@@ -364,80 +366,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp < kEpiWarp) {
     // ------------------------------------------------ conversion of B (both CTAs)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-    // A group of 4 warps converts each half of a stage.  Lane l of warp v of
-    // its group takes the 16 columns 16 (l % 4) of the 64-column block
-    // (l / 8) % 2, rows 4 v + (l / 4) % 2 + 2 (l / 16) + 16 i.  Eight lanes so
-    // store even chunks of one row and of the next, odd one, whose swizzle
-    // swaps even and odd: no bank conflicts.
-    const int half = (warp - kConvWarp) / kConvGroup;
+    // The two groups of 4 warps take turns at the stages, so that one's waits
+    // and fences pass while the other converts: half a stage each, in step,
+    // left the ALUs idle for half of the time.
+    // Lane l of warp v of its group takes the 16 columns 16 (l % 4) of the
+    // 64-column block (l / 8) % 2, rows 4 v + (l / 4) % 2 + 2 (l / 16) + 16 i.
+    // Eight lanes so store even chunks of one row and of the next, odd one,
+    // whose swizzle swaps even and odd: no bank conflicts.
+    const int group = (warp - kConvWarp) / kConvGroup;
     const int v = (warp - kConvWarp) % kConvGroup;
     const int unit = lane & 3, blk = (lane >> 3) & 1;
     const int row0 = 4 * v + ((lane >> 2) & 1) + 2 * (lane >> 4);
     const int column = blk * 64 + unit * 16;
-    RingPos<R> rpos;
-    RingPos<S> pos;
+    uint32_t first = 0;      // ring index of the unit's first stage
     bool ok = true;
     for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
       const MxUnit w = mx_unit(u, sc, nk);
       if (w.row0 >= p.M) continue;
-      for (int kt = w.kb; kt < w.ke; ++kt, rpos.next(), pos.next()) {
-        const uint32_t r = rpos.slot, s = pos.slot;
+      for (int kt = w.kb + (int)((group ^ first) & 1u); kt < w.ke; kt += 2) {
+        const uint32_t it = first + (uint32_t)(kt - w.kb);
+        const uint32_t r = it % R, s = it % S;
         // (Both tries are on their way at once.)
-        const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), rpos.parity);
-        const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u);
-        ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), rpos.parity, p.fault, p.timeout_ns,
+        const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), (it / R) & 1u);
+        const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u);
+        ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), (it / R) & 1u, p.fault, p.timeout_ns,
                              &bars->abort, kFaultTcProducerWait, loaded);
         if (!ok) break;
-        const unsigned char* raw = sraw + r * L::kRawStage + half * 64 * L::kRawRow;
-        const unsigned char* scales =
-            sraw + r * L::kRawStage + L::kRaw + half * 2 * 4 + (column >> 5);
-        const int rows_left = p.K - kt * BK - half * 64;
-        // All loads before the first store, which the compiler could not
-        // move a load across.
-        uint32_t c[4][kFmt == GEMM_MXFP4 ? 2 : 4];
-        unsigned sb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = row0 + 16 * i;
-          if constexpr (kFmt == GEMM_MXFP4) {
-            const uint2 x = *reinterpret_cast<const uint2*>(raw + row * L::kRawRow + column / 2);
-            c[i][0] = x.x, c[i][1] = x.y;
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(raw + row * L::kRawRow + column);
-            c[i][0] = x.x, c[i][1] = x.y, c[i][2] = x.z, c[i][3] = x.w;
+        for (int half = 0; half < kHalves; ++half) {
+          const unsigned char* raw = sraw + r * L::kRawStage + half * 64 * L::kRawRow;
+          const unsigned char* scales =
+              sraw + r * L::kRawStage + L::kRaw + half * 2 * 4 + (column >> 5);
+          const int rows_left = p.K - kt * BK - half * 64;
+          // All loads before the first store, which the compiler could not
+          // move a load across.
+          uint32_t c[4][kFmt == GEMM_MXFP4 ? 2 : 4];
+          unsigned sb[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 16 * i;
+            if constexpr (kFmt == GEMM_MXFP4) {
+              const uint2 x = *reinterpret_cast<const uint2*>(raw + row * L::kRawRow + column / 2);
+              c[i][0] = x.x, c[i][1] = x.y;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4*>(raw + row * L::kRawRow + column);
+              c[i][0] = x.x, c[i][1] = x.y, c[i][2] = x.z, c[i][3] = x.w;
+            }
+            sb[i] = scales[(row & 31) * 16 + (row >> 5) * 4];
+            // Rows past K: zero codes, and any finite scale.
+            if (row >= rows_left) sb[i] = 0;
           }
-          sb[i] = scales[(row & 31) * 16 + (row >> 5) * 4];
-          // Rows past K: zero codes, and any finite scale.
-          if (row >= rows_left) sb[i] = 0;
+          if (half == 0)
+            ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault,
+                                 p.timeout_ns, &bars->abort, kFaultTcProducerWait, freed);
+          if (!ok) break;
+          if (half == kHalves - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
+          }
+          unsigned char* st = base + s * kStage + half * kConvHalf + blk * kBlock;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 16 * i;
+            const Scale<T> f(sb[i]);
+            uint4 lo, hi;
+            if constexpr (kFmt == GEMM_MXFP4) {
+              lo = convert_e2m1x8<T>(c[i][0], f);
+              hi = convert_e2m1x8<T>(c[i][1], f);
+            } else {
+              const uint2 a = convert_int8x4<T>(c[i][0], f), b = convert_int8x4<T>(c[i][1], f);
+              const uint2 d = convert_int8x4<T>(c[i][2], f), e = convert_int8x4<T>(c[i][3], f);
+              lo = make_uint4(a.x, a.y, b.x, b.y);
+              hi = make_uint4(d.x, d.y, e.x, e.y);
+            }
+            unsigned char* dst = st + row * 128;
+            *reinterpret_cast<uint4*>(dst + (((2 * unit) ^ (row & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4*>(dst + (((2 * unit + 1) ^ (row & 7)) << 4)) = hi;
+          }
         }
-        ok = role_wait_lanes(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
-                             &bars->abort, kFaultTcProducerWait, freed);
         if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
-        unsigned char* st = base + s * kStage + half * kConvHalf + blk * kBlock;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = row0 + 16 * i;
-          const Scale<T> f(sb[i]);
-          uint4 lo, hi;
-          if constexpr (kFmt == GEMM_MXFP4) {
-            lo = convert_e2m1x8<T>(c[i][0], f);
-            hi = convert_e2m1x8<T>(c[i][1], f);
-          } else {
-            const uint2 a = convert_int8x4<T>(c[i][0], f), b = convert_int8x4<T>(c[i][1], f);
-            const uint2 d = convert_int8x4<T>(c[i][2], f), e = convert_int8x4<T>(c[i][3], f);
-            lo = make_uint4(a.x, a.y, b.x, b.y);
-            hi = make_uint4(d.x, d.y, e.x, e.y);
-          }
-          unsigned char* dst = st + row * 128;
-          *reinterpret_cast<uint4*>(dst + (((2 * unit) ^ (row & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + (((2 * unit + 1) ^ (row & 7)) << 4)) = hi;
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
       }
+      first += (uint32_t)(w.ke - w.kb);
     }
     __syncwarp();
   } else {
