@@ -164,7 +164,7 @@ constexpr int kMaxSlices = 16;
 constexpr long long kWorkspaceCap = 256ll << 20;   // bytes of partial results
 constexpr double kUnitCost = 1.2;                  // pipeline fill, drain, store
 constexpr double kReduceCost = 2.0;                // the launch that sums the slices,
-constexpr double kReduceBytesPerUs = 6e6;          // and what it reads
+constexpr double kReduceBytesPerUs = 3e6;          // and what is written and read for it
 dgemm::MxSchedule schedule(int M, int N, int nk, int pairs, int group, StageCost cost) {
   dgemm::MxSchedule sc;
   sc.tiles_m = ceil_div(M, dgemm::kMxPairTile);
@@ -444,7 +444,7 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
   p.sb = static_cast<const unsigned char*>(b_scales);
   const int nk = ceil_div(K, dgemm::kMxGradBK);
-  p.sched = schedule(M, N, nk, max_pairs, 8, {0.86, 0.60});
+  p.sched = schedule(M, N, nk, max_pairs, 8, {0.74, 0.56});
   // FP32 results: at most 1024 terms per sum in tensor memory.
   p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
   if ((st = partials(p.sched, M, N, stream, &p.ws, &p.ldw)) != GEMM_OK) return st;

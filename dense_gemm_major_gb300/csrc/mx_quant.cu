@@ -11,13 +11,17 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Two consecutive elements, 4-byte aligned, of a 16-bit type, and two values
-// as such a pair (never called for a 32-bit type).
+// The value in a word as loaded: half i of a pair of 16-bit ones, or FP32.
 template <typename T>
-__device__ __forceinline__ float2 pair_to_f32_any(const T* src) {
-  if constexpr (sizeof(T) == 2) return pair_to_f32<T>(*reinterpret_cast<const unsigned*>(src));
-  return make_float2(0.f, 0.f);
+__device__ __forceinline__ float value_of(unsigned w, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(w);
+  } else {
+    const float2 f = pair_to_f32<T>(w);
+    return i == 0 ? f.x : f.y;
+  }
 }
+// Two values as a pair of a 16-bit type (never called for FP32).
 template <typename T>
 __device__ __forceinline__ unsigned pack2_any(float lo, float hi) {
   if constexpr (sizeof(T) == 2) return pack2<T>(lo, hi);
@@ -125,27 +129,32 @@ __global__ void __launch_bounds__(kThreads)
   for (int piece = blockIdx.y; piece < pieces; piece += gridDim.y) {
     const int k0 = piece * 256 + warp * kMxBlock;
     const int r = r0 + lane * L::V;
-    float v[L::V][32];
-    if (L::V == 2 && vec && r + 2 <= R && k0 + kMxBlock <= K) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float2 f = pair_to_f32_any<T>(X + (long long)(k0 + j) * ldx + r);
-        v[0][j] = f.x;
-        v[L::V - 1][j] = f.y;
-      }
-    } else {
+    // The block's values as loaded (pairs of 16-bit ones stay packed: half the
+    // registers, twice the CTAs per SM).
+    unsigned raw[32];
+    if (L::V == 1 || (vec && r + 2 <= R && k0 + kMxBlock <= K)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
+        raw[j] = L::V == 2 || (k0 + j < K && r < R)
+                     ? *reinterpret_cast<const unsigned*>(X + (long long)(k0 + j) * ldx + r)
+                     : 0u;
+    } else {
 #pragma unroll
-        for (int i = 0; i < L::V; ++i)
-          v[i][j] = k0 + j < K && r + i < R ? to_f32_any<T>(X[(long long)(k0 + j) * ldx + r + i])
-                                            : 0.f;
+      for (int j = 0; j < 32; ++j) {
+        unsigned h[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          h[i] = k0 + j < K && r + i < R
+                     ? reinterpret_cast<const unsigned short*>(X)[(long long)(k0 + j) * ldx + r + i]
+                     : 0u;
+        raw[j] = h[0] | (h[1] << 16);
+      }
     }
 #pragma unroll
     for (int i = 0; i < L::V; ++i) {
       unsigned amax = 0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) amax = max(amax, abs_bits(v[i][j]));
+      for (int j = 0; j < 32; ++j) amax = max(amax, abs_bits(value_of<T>(raw[j], i)));
       const unsigned s = mx_scale_byte<kFmt>(amax);
       const float inv = mx_inverse_scale(s);
       const bool clamp = kFmt == GEMM_MXINT8 && int8_clamps(amax, inv);
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int g = 0; g < 4; ++g) {
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = v[i][8 * g + j] * inv;
+        for (int j = 0; j < 8; ++j) x[j] = value_of<T>(raw[8 * g + j], i) * inv;
         if constexpr (kFmt == GEMM_MXFP4) {
           w[g] = s == 255u ? 0u : e2m1x8(x);
         } else {
