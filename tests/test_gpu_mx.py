@@ -504,3 +504,93 @@ def test_arrays_past_32_bit_offsets(dg):
             assert (_np(got) == want).all()
         del q, y
     check_device(dg)
+
+
+# ------------------------------------------------------------ schedules
+
+@pytest.mark.parametrize("shape", [(2100, 2500, 300), (130, 200, 6000), (64, 3000, 2500),
+                                   (400, 100, 3000), (4200, 1030, 520)])
+def test_product_schedules(dg, shape):
+    """Whole tiles with a last round of halves (one of them past M), ranges of
+    K summed afterwards, few rows over a cluster; scaled, with an old C."""
+    M, N, K = shape
+    rng = np.random.default_rng(M)
+    a, av = _operand(dg, _np(_rand(rng, M, K, spread=1.0)), "mxfp4")
+    b, bv = _operand(dg, _np(_rand(rng, N, K, spread=1.0)), "mxfp4")
+    want, total = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    for dtype in ("bf16", "f32"):
+        _check(dg.mx_matmul(a, b, dtype=TYPES[dtype]), want, total, K, dtype)
+        c0 = _rand(rng, M, N, dtype, spread=0.0)
+        out = _dev(c0, pad=2)
+        dg.mx_matmul(a, b, out=out, alpha=-1.5, beta=0.5)
+        check_device(dg)
+        _check(out, -1.5 * want + 0.5 * _np(c0), 1.5 * total + 0.5 * np.abs(_np(c0)), K, dtype)
+
+
+@pytest.mark.parametrize("fmt,op", [("mxint8", "T"), ("mxfp4", "N")])
+@pytest.mark.parametrize("shape", [(2100, 2500, 300), (130, 200, 6000), (400, 100, 3000)])
+def test_grad_schedules(dg, fmt, op, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + 1)
+    a, av = _grad_a(dg, rng, M, K, "bf16", op)
+    b, bv = _operand(dg, _np(_rand(rng, K, N, spread=1.0)), fmt)
+    want, total = _np(a) @ bv, np.abs(_np(a)) @ np.abs(bv)
+    for dtype in ("bf16", "f32"):
+        _check(dg.mx_grad(av, b, dtype=TYPES[dtype]), want, total, K, dtype)
+        c0 = _rand(rng, M, N, dtype, spread=0.0)
+        out = _dev(c0, pad=2)
+        dg.mx_grad(av, b, out=out, alpha=-1.5, beta=0.5)
+        check_device(dg)
+        _check(out, -1.5 * want + 0.5 * _np(c0), 1.5 * total + 0.5 * np.abs(_np(c0)), K, dtype)
+
+
+def test_long_float32_sums_round_to_nearest(dg):
+    """Over 32768 terms the FP32 result keeps the error of sums of 1024 terms
+    each, which the tensor cores truncate (a relative error that grows with
+    the number of 16-term steps, 64 here), added with rounding: 64 * 2^-23
+    of the largest partial sum and 32 * 2^-24 of the running one, over a
+    random walk of like terms well under 4e-6 of the result's norm.  Summed
+    in one piece it was above 2e-5."""
+    rng = np.random.default_rng(77)
+    K = 32768
+    a = _rand(rng, K, 128, "bf16", spread=0.0)
+    b, bv = _operand(dg, rng.standard_normal((K, 96)), "mxint8")
+    got = _np(dg.mx_grad(a.cuda().t(), b, dtype=torch.float32))
+    want = _np(a).T @ bv
+    assert np.linalg.norm(got - want) <= 4e-6 * np.linalg.norm(want)
+
+
+def test_refusals_of_the_wrappers(dg):
+    x = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    q4, q8 = dg.mx_quantize(x), dg.mx_quantize(x, "mxint8")
+    wide = torch.zeros((8, 8, 4), dtype=torch.bfloat16, device="cuda")
+    bad = [
+        lambda: dg.mx_quantize(x, "mxfp6"), lambda: dg.mx_quantize(x.cpu()),
+        lambda: dg.mx_quantize(x.double()), lambda: dg.mx_quantize(wide),
+        lambda: dg.mx_quantize(wide[:, :, 1]),                      # no unit stride
+        lambda: dg.mx_dequantize(x), lambda: dg.mx_dequantize(q4, torch.int8),
+        lambda: dg.mx_dequantize(q4, out=torch.zeros((8, 63), device="cuda")),
+        lambda: dg.mx_dequantize(q4, torch.float16, out=torch.zeros((8, 64), device="cuda")),
+        lambda: dg.mx_matmul(q4, q8), lambda: dg.mx_matmul(q4, q4, beta=1.0),
+        lambda: dg.mx_matmul(q4, dg.mx_quantize(x[:, :32])),
+        lambda: dg.mx_matmul(q4, q4, out=torch.zeros((8, 8))),
+        lambda: dg.mx_linear(x, q8), lambda: dg.mx_linear(x[:, :32], q4),
+        lambda: dg.mx_linear(x.t(), dg.mx_quantize(torch.zeros((5, 8), device="cuda"))),
+        lambda: dg.mx_linear(x, q4, out=torch.zeros((8, 8), device="cuda")),
+        lambda: dg.mx_grad(x.float(), q4), lambda: dg.mx_grad(x, q4),
+        lambda: dg.mx_grad(x[:, :8], q4, dtype=torch.float16),
+        lambda: dg.mx_grad(x[:, :8], q4, beta=1.0), lambda: dg.mx_grad(wide[:, :, 1], q4),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    shifted = torch.zeros(8 * 64 + 8, dtype=torch.bfloat16, device="cuda")[1:513].view(8, 64)
+    for f, status in [(lambda: dg.mx_grad(shifted[:, :8], q4), dg.GEMM_ERR_MISALIGNED),
+                      (lambda: dg.mx_grad(torch.zeros((8, 17), dtype=torch.bfloat16,
+                                                      device="cuda")[:, :8], q4),
+                       dg.GEMM_ERR_MISALIGNED),
+                      (lambda: dg.mx_quantize(x[:1].expand(8, 64)), dg.GEMM_ERR_INVALID_ARG)]:
+        with pytest.raises(dg.GemmError) as e:
+            f()
+        assert e.value.status == status
+    check_device(dg)
