@@ -256,8 +256,9 @@ __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, unsigne
   }
 }
 // The same by a warp, each lane polling (`ready`: what an earlier try of the
-// lane gave): quicker than a broadcast of one
-// lane's result (220 cycles) where the barrier is mostly complete already.
+// lane gave).  Where a warp waits for every stage, that is quicker than one
+// lane polling while the others wait for its answer: dX 4096^3 89 against
+// 152 us.
 __device__ __forceinline__ bool role_wait_lanes(uint32_t bar, uint32_t parity, unsigned* fault,
                                                 unsigned long long timeout_ns, int* abort,
                                                 unsigned code, bool ready = false) {

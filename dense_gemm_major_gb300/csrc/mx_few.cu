@@ -10,6 +10,10 @@
 // through distributed shared memory in rank order, so results are
 // reproducible and there is no workspace and no second launch.
 //
+// Measured at N = K = 4096, back to back: 1 row 4.9 us, 8 5.3, 33 8.6 (a cold
+// read of B's 8.9 MB alone takes 1.3 us; launch, tensor memory, barriers and
+// the two cluster barriers are the most of the rest).
+//
 // Roles (320 threads): warp 0 loads codes (TMA) and scales (bulk copies),
 // warp 1 issues scale copies and MMAs, warps 2-9 quantise A where it comes
 // unquantised, and warps 2-5 then drain the accumulator.
@@ -80,9 +84,11 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
       : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
   return v;
 }
 
@@ -271,16 +277,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.split > 1) {
     // ------------------------------------------------ sum of the cluster's partial tiles
     cluster_sync_all();
-    const int share = BN / p.split;            // columns of C that this CTA adds up
+    // This CTA adds up BN / split of the columns, four of a row per thread, all
+    // partial tiles' values on their way at once (33 x 4096 x 4096 8.6 us, one
+    // value after the other 8.9).
+    constexpr int kMaxSplit = 8;
+    const int share = BN / p.split / 4;
     for (int i = threadIdx.x; i < share * p.M; i += kThreads) {
       const int m = i / share;
-      const int col = rank * share + (i - m * share);
+      const int col = (rank * share + (i - m * share)) * 4;
       const uint32_t at = smem_u32(base) + (uint32_t)(m * BN + col) * 4u;
-      float sum = ld_cluster_f32(mapa_shared(at, 0));
-      for (int r = 1; r < p.split; ++r) sum += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
-      if (tn * BN + col < p.N)
-        store_scaled<T>(static_cast<T*>(p.C) + (long long)m * p.ldc + tn * BN + col, sum, p.alpha,
-                        p.beta);
+      float4 v[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        v[r] = r < p.split ? ld_cluster_v4(mapa_shared(at, (uint32_t)r))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r) {
+        sum[0] += v[r].x;
+        sum[1] += v[r].y;
+        sum[2] += v[r].z;
+        sum[3] += v[r].w;
+      }
+      T* c = static_cast<T*>(p.C) + (long long)m * p.ldc + tn * BN + col;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (tn * BN + col + j < p.N) store_scaled<T>(c + j, sum[j], p.alpha, p.beta);
     }
     cluster_sync_all();   // no CTA leaves while others read its partial tile
   }
