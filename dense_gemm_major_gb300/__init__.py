@@ -476,23 +476,9 @@ class MXTensor:
     __slots__ = ("_codes", "_scales", "_buffer", "rows", "cols", "fmt", "_ld")
 
     def __init__(self, codes, scales, cols, fmt="mxfp4"):
-        if fmt == "mxfp4":
-            width = (cols + 1) >> 1
-        elif fmt == "mxint8":
-            width = cols
-        else:
-            raise ValueError("fmt must be 'mxfp4' or 'mxint8'")
-        rows, pitch = codes.shape
-        ld, unit = codes.stride()
-        if pitch < width or (unit != 1 and pitch > 1) or codes.element_size() != 1:
-            raise ValueError("codes must be rows of at least the format's bytes for cols")
-        if scales.numel() < 512 * ((rows + 127) >> 7) * ((cols + 127) >> 7) \
-                or scales.element_size() != 1 or not scales.is_contiguous():
-            raise ValueError("scales must be contiguous, 512 bytes for each 128 x 128 tile")
+        self.rows, self._ld = (_mx or _load_mx()).describe(codes, scales, cols, fmt)
         self._codes, self._scales, self._buffer = codes, scales, None
-        self.rows, self.cols, self.fmt = rows, cols, fmt
-        # (The pitch of a single row is free: its padded width.)
-        self._ld = ld if rows > 1 else (pitch + 15) & ~15
+        self.cols, self.fmt = cols, fmt
 
     @property
     def shape(self):

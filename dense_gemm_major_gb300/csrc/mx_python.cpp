@@ -20,7 +20,7 @@ PyObject *g_empty, *g_raw_stream, *g_error, *g_tensor_type;   // set by setup()
 PyObject *g_dtype[3], *g_uint8;                               // float32, float16, bfloat16
 PyObject *g_empty_names;                                      // ("dtype", "device")
 PyObject *n_is_cuda, *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_device, *n_index, *n_codes,
-    *n_scales, *n_buffer, *n_rows, *n_cols, *n_fmt, *n_ld, *n_mxfp4, *n_mxint8;
+    *n_scales, *n_buffer, *n_rows, *n_cols, *n_fmt, *n_ld, *n_mxfp4, *n_numel, *n_is_contiguous;
 
 // An owned reference.
 struct Ref {
@@ -366,6 +366,40 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return c.tensor.release();
 }
 
+// describe(codes, scales, cols, fmt) -> (rows, pitch of the codes): the checks
+// of an MXTensor's arrays.
+PyObject* describe(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 4)) return nullptr;
+  int cols, rows, width, ld, unit;
+  if (!to_int(a[2], &cols)) return nullptr;
+  gemm_mx_format_t fmt = GEMM_MXFP4;
+  if (!PyUnicode_Check(a[3])) return value_error("fmt must be 'mxfp4' or 'mxint8'"), nullptr;
+  if (PyUnicode_CompareWithASCIIString(a[3], "mxfp4") != 0) {
+    if (PyUnicode_CompareWithASCIIString(a[3], "mxint8") != 0)
+      return value_error("fmt must be 'mxfp4' or 'mxint8'"), nullptr;
+    fmt = GEMM_MXINT8;
+  }
+  Ref type(PyObject_GetAttr(a[0], n_dtype)), shape(PyObject_GetAttr(a[0], n_shape));
+  if (!type || !shape || !pair_of(shape.p, &rows, &width)) return nullptr;
+  Ref stride(PyObject_CallMethodNoArgs(a[0], n_stride));
+  if (!stride || !pair_of(stride.p, &ld, &unit)) return nullptr;
+  if (type.p != g_uint8 || (long long)width * (fmt == GEMM_MXFP4 ? 2 : 1) < cols ||
+      (unit != 1 && width > 1))
+    return value_error("codes must be uint8 rows of at least the format's bytes for cols"),
+           nullptr;
+  Ref stype(PyObject_GetAttr(a[1], n_dtype));
+  Ref contiguous(PyObject_CallMethodNoArgs(a[1], n_is_contiguous));
+  Ref count(PyObject_CallMethodNoArgs(a[1], n_numel));
+  if (!stype || !contiguous || !count) return nullptr;
+  const long long have = PyLong_AsLongLong(count.p);
+  if (have == -1 && PyErr_Occurred()) return nullptr;
+  if (stype.p != g_uint8 || contiguous.p != Py_True || have < gemm_mx_scale_bytes(rows, cols))
+    return value_error("scales must be contiguous uint8, 512 bytes for each 128 x 128 tile"),
+           nullptr;
+  // (The pitch of a single row is free: its padded width.)
+  return Py_BuildValue("ii", rows, rows > 1 ? ld : (int)(((long long)width + 15) / 16 * 16));
+}
+
 // setup(torch, MXTensor, GemmError)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 3) {
@@ -380,7 +414,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
                {&n_index, "index"},     {&n_codes, "_codes"},  {&n_scales, "_scales"},
                {&n_buffer, "_buffer"},  {&n_rows, "rows"},     {&n_cols, "cols"},
                {&n_fmt, "fmt"},         {&n_ld, "_ld"},        {&n_mxfp4, "mxfp4"},
-               {&n_mxint8, "mxint8"}};
+               {&n_numel, "numel"},     {&n_is_contiguous, "is_contiguous"}};
   for (auto& x : names)
     if (*x.to == nullptr && (*x.to = PyUnicode_InternFromString(x.name)) == nullptr)
       return nullptr;
@@ -402,7 +436,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(setup), METHOD(quantize), METHOD(dequantize), METHOD(matmul),
-                           METHOD(linear), METHOD(grad), {nullptr, nullptr, 0, nullptr}};
+                           METHOD(linear), METHOD(grad),
+                           METHOD(describe), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_mxcall", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
