@@ -30,6 +30,12 @@
  * problems are reported synchronously before anything is queued, work is
  * queued on `stream`, and every device-side wait is bounded.  Inputs must not
  * overlap outputs.
+ *
+ * Device memory: products that share out K (few tiles, long K) keep FP32
+ * partial results in a workspace of the library, and gemm_mx4_linear with more
+ * than a few rows its quantised X in another: one each per (device, stream),
+ * grown after synchronising that stream and kept until the process exits.
+ * Before a stream capture, make one call of the same sizes on that stream.
  */
 #ifndef DENSE_GEMM_MX_H_
 #define DENSE_GEMM_MX_H_
@@ -86,9 +92,7 @@ gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha,
  * A linear layer in 4 bits: Y := q(X) . W^T, X (M x K) and Y (M x N) of
  * dtype, q(X) the MXFP4 quantisation of X, W (N x K) in MXFP4.  The same
  * values as gemm_mx_quantize followed by gemm_mx4 up to the order of the
- * sums.  q(X) lives in a workspace of the library (one per device and
- * stream, grown on demand after synchronising that stream, kept until the
- * process exits).
+ * sums.
  */
 gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void *X, int ldx,
                               const void *w_codes, int ldw, const void *w_scales, void *Y,
