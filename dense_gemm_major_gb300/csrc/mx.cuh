@@ -232,6 +232,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// True in one lane of a converged warp, always the same one (so that a later
+// tcgen05.commit covers what the role issued).  Roles of a single thread branch on
+// this rather than on the lane's number: the compiler then knows that one
+// thread runs them and keeps addresses and descriptors in uniform registers,
+// where TMA and tcgen05 instructions want them (dX 4096^3 86.6 -> 80.5 us, the
+// 4-bit product 28.4 -> 27.0).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ------------------------------------------------------------ role waits
 
 // A role's bounded wait by one thread; on giving up records the fault (once
@@ -256,23 +270,15 @@ __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, unsigne
   }
 }
 // The same by a warp, each lane polling (`ready`: what an earlier try of the
-// lane gave).  Where a warp waits for every stage, that is quicker than one
-// lane polling while the others wait for its answer: dX 4096^3 89 against
-// 152 us.
+// lane gave).  One lane polling while the others wait for its answer is much
+// slower where a warp waits for every stage (dX 4096^3 152 against 89 us) and
+// still shows where it waits once per tile (89.2 against 86.5 us).
 __device__ __forceinline__ bool role_wait_lanes(uint32_t bar, uint32_t parity, unsigned* fault,
                                                 unsigned long long timeout_ns, int* abort,
-                                                unsigned code, bool ready = false) {
+                                                unsigned code, bool ready = false,
+                                                bool spin = true) {
   return __all_sync(0xffffffffu,
-                    ready || role_wait(bar, parity, fault, timeout_ns, abort, code, true));
-}
-// The same by a warp: lane 0 waits, the result is broadcast.
-__device__ __forceinline__ bool role_wait_warp(uint32_t bar, uint32_t parity, unsigned* fault,
-                                               unsigned long long timeout_ns, int* abort,
-                                               unsigned code, bool spin) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0)
-    ok = role_wait(bar, parity, fault, timeout_ns, abort, code, spin) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+                    ready || role_wait(bar, parity, fault, timeout_ns, abort, code, spin));
 }
 
 // Arrives on an mbarrier of any CTA of the cluster (shared::cluster address)

@@ -39,7 +39,7 @@ struct Layout {
   // several stages' loads of A are in flight at once.  Stages are a multiple
   // of groups: a slot's stages all fall to one group, which therefore never
   // waits for a phase whose predecessor it has not seen.
-  static constexpr int kGroups = 4;
+  static constexpr int kGroups = 2;
   static constexpr int kGroupWarps = 8 / kGroups;
   static_assert(kStages % kGroups == 0, "one group per slot");
   static constexpr uint32_t kABytes = MT * BK / 2;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t issued = 0;
   if (warp == 0) {
     // ------------------------------------------------ loads
-    if (lane == 0) {
+    if (elect_one()) {
       for (int kt = kb; kt < ke; ++kt) {
         const uint32_t it = (uint32_t)(kt - kb), s = it % S;
         if (!role_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       for (int kt = kb; kt < ke; ++kt) {
         const uint32_t it = (uint32_t)(kt - kb), s = it % S;
@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp < kWorkWarp + 4) {
       const int q = warp & 3;
       if (ke > kb)
-        ok = ok && role_wait_warp(smem_u32(&bars->acc_full), 0, p.fault, p.timeout_ns,
-                                  &bars->abort, kFaultTcEpilogueWait, true);
+        ok = ok && role_wait_lanes(smem_u32(&bars->acc_full), 0, p.fault, p.timeout_ns,
+                                   &bars->abort, kFaultTcEpilogueWait);
       tc_fence_after();
       const int col = q * 32 + lane;           // within the tile
 #pragma unroll 1
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 0 && lane == 0 && bars->abort) {
+  if (warp == 0 && elect_one() && bars->abort) {
     // Let this CTA's copies in flight land before it exits.
     const uint32_t first = issued > (uint32_t)S ? issued - S : 0;
     for (uint32_t it = first; it < issued; ++it) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (warp == 1) {
     tc_fence_after();
-    if (lane == 0 && bars->abort) {
+    if (elect_one() && bars->abort) {
       // (Otherwise acc_full has shown every MMA to be done.)
       mma_commit(smem_u32(&bars->drain));
       if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))

@@ -154,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kLoadWarp && lane == 0) {
+    if (warp == kLoadWarp && elect_one()) {
       // ---------------------------------------------- loads (both CTAs)
       RingPos<S> pos;
       uint32_t it = 0;
@@ -192,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           issued = it + 1;
         }
       }
-    } else if (warp == kMmaWarp && rank == 0 && lane == 0) {
+    } else if (warp == kMmaWarp && rank == 0 && elect_one()) {
       // ---------------------------------------------- MMA issuer (even CTA)
       // The barrier of the next stage is tried before this stage's MMAs are
       // issued: a try takes over 100 cycles to answer.
@@ -252,8 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (w.row0 >= p.M) continue;
       const int chunks = w.rows / 64;      // of 32 rows, this warp's share
       const int first = half * (w.rows / 2);
-      if (!role_wait_warp(smem_u32(&bars->acc_full), local & 1u, p.fault, p.timeout_ns,
-                          &bars->abort, kFaultTcEpilogueWait, false))
+      if (!role_wait_lanes(smem_u32(&bars->acc_full), local & 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcEpilogueWait, false, false))
         break;
       ++local;
       tc_fence_after();
@@ -285,12 +285,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------ teardown
-  if (warp == kMmaWarp && rank == 0 && lane == 0) {
+  if (warp == kMmaWarp && rank == 0 && elect_one()) {
     mma_commit_pair_multicast(smem_u32(&bars->drain), 0x1);
     if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
       raise_fault(p.fault, kFaultDrainWait);
   }
-  if (warp == kLoadWarp && lane == 0 && bars->abort) {
+  if (warp == kLoadWarp && elect_one() && bars->abort) {
     // Let the loads in flight land: this CTA's scales, and (even CTA) both
     // CTAs' codes on full[], whose arrivals by the warps of scales may be
     // missing; the wait then gives up.

@@ -258,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t issued = 0;
   if (warp < kConvWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
       // ---------------------------------------------- op(A) (both CTAs)
       RingPos<S> pos;
       uint32_t it = 0;
@@ -291,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           issued = it + 1;
         }
       }
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2 && elect_one()) {
       // ---------------------------------------------- codes and scales (both CTAs)
       const int ktiles = mx_scale_tiles(p.N);
       RingPos<R> pos;
@@ -317,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           issued = it + 1;
         }
       }
-    } else if (warp == 1 && rank == 0 && lane == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
       // ---------------------------------------------- MMA issuer (even CTA)
       // The barrier of the next stage is tried before this stage's MMAs are
       // issued: a try takes over 100 cycles to answer.
@@ -333,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int k1 = min(k0 + p.seg, w.ke);
           const uint32_t b = seg & 1;
           ok = role_wait(smem_u32(&bars->acc_empty[b]), ((seg >> 1) & 1u) ^ 1u, p.fault,
-                                 p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
+                         p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
           if (!ok) break;
           tc_fence_after();
           for (int kt = k0; kt < k1; ++kt) {
@@ -471,8 +471,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 128; ++j) acc[j] = 0.f;
       for (int k0 = w.kb; k0 < w.ke; k0 += p.seg, ++seg) {
         const uint32_t b = seg & 1;
-        ok = role_wait_warp(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
-                            &bars->abort, kFaultTcEpilogueWait, false);
+        ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcEpilogueWait, false, false);
         if (!ok) break;
         tc_fence_after();
         const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256 + first;
@@ -508,14 +508,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------ teardown
-  if (warp == 1 && rank == 0 && lane == 0) {
+  if (warp == 1 && rank == 0 && elect_one()) {
     // Every MMA of the pair has completed before TMEM is freed.
     mma_commit_pair_multicast(smem_u32(&bars->drain), 0x1);
     if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
       raise_fault(p.fault, kFaultDrainWait);
   }
   __syncthreads();
-  if ((warp == 2 || (warp == 0 && rank == 0)) && lane == 0 && bars->abort) {
+  if ((warp == 2 || (warp == 0 && rank == 0)) && elect_one() && bars->abort) {
     // Let the copies in flight land: those of codes on raw_full[], and those
     // of op(A), both CTAs', on the even one's full[], whose arrivals by
     // converting warps may be missing; the wait then gives up.
