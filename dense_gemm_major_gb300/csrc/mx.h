@@ -103,14 +103,19 @@ struct Mx4FewParams {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-// (With a tile of 128 rows, CTA pairs and a reduction were quicker: 128 x 2048 x
-// 2048 7.7 against 9.7 us, 128 x 8192 x 8192 13.3 against 14.8.)
+// The pair kernel against this one at 64 rows, N x K: 2048 x 2048 5.6 / 6.0 us,
+// 4096 x 4096 7.1 / 7.7, 512 x 512 4.4 / 4.2, 4096 x 14336 11.1 / 9.5, 8192 x
+// 8192 11.3 / 8.1, 1024 x 8192 7.5 / 5.6; at 32 rows this one is quicker in all.
+// (With a tile of 128 rows the pairs were: 128 x 2048 x 2048 7.7 / 9.7 us.)
 constexpr int kMx4FewRows = 64, kMx4FewBK = 256;
-// Quantising inside the kernel saves a launch (2.7 us of a calling thread)
-// but is done anew by the CTAs of every 128 columns: on the GPU, N = K = 4096,
-// inside / before the kernel: 1 row 5.3 / 6.0 us, 16 7.6 / 6.8, 33 9.3 / 8.1,
-// 48 10.6 / 8.7, 64 12.5 / 9.5, against some 11 us of CPU for two launches.
-constexpr int kMx4FewRawRows = 48;
+// Quantising A inside the kernel saves a launch (1.2 us of the GPU and 2.7 us
+// of a calling thread), but each CTA then quantises the rows' part that it
+// multiplies: M times its share of K values, done anew for every 128 columns.
+// Inside / before, us: 16384 values 1024 x 8192 (N x K), 16 rows 4.8 / 5.6;
+// 24576 values 4096 x 4096, 48 rows 8.8 / 8.7, 1024 x 8192, 24 rows 6.3 / 6.1,
+// and 8192 x 8192, 12 rows 8.0 / 8.2; 33792 values 1024 x 8192, 33 rows 7.3 /
+// 6.4; 49152 values 8192 x 8192, 24 rows 11.1 / 8.8.
+constexpr int kMx4FewRawRows = 48, kMx4FewRawValues = 24 * 1024;
 // Rows of A that the kernel computes for M of them.
 inline int mx4_few_tile(int M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
 // tmA: A's codes as bytes, boxes of 128 bytes x mx4_few_tile(M) rows; tmB:

@@ -217,6 +217,22 @@ gemm_status_t partials(const dgemm::MxSchedule& sc, int M, int N, cudaStream_t s
   return st;
 }
 
+// CTAs of the few-row kernel that share a tile's K: as many (2, 4 or 8 of a
+// cluster) as keep one wave of two CTAs per SM, each with a stage at least.
+int few_split(int N, int K, int max_pairs) {
+  const int tiles = ceil_div(N, 128), nk = ceil_div(K, dgemm::kMx4FewBK);
+  int split = 1;
+  while (split < 8 && 2 * split <= nk && 2 * split * tiles <= 4 * max_pairs) split *= 2;
+  return split;
+}
+
+// Whether the few-row kernel quantises A itself: see kMx4FewRawRows.
+bool few_raw(int M, int N, int K, int max_pairs) {
+  const int stages = ceil_div(ceil_div(K, dgemm::kMx4FewBK), few_split(N, K, max_pairs));
+  return M <= dgemm::kMx4FewRawRows &&
+         (long long)M * stages * dgemm::kMx4FewBK <= dgemm::kMx4FewRawValues;
+}
+
 // The product of checked operands, 0 < M <= kMx4FewRows, N, K > 0; A is X,
 // unquantised, or a.
 gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X, long long ldx,
@@ -236,11 +252,7 @@ gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X
   p.vec = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
   p.sa = static_cast<const unsigned char*>(sa);
   p.sb = static_cast<const unsigned char*>(sb);
-  // As many CTAs (2, 4 or 8 of a cluster) to a tile's K as keep one wave of
-  // two CTAs per SM, each with a stage at least.
-  p.split = 1;
-  const int tiles = ceil_div(N, 128), nk = ceil_div(K, dgemm::kMx4FewBK);
-  while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= 4 * max_pairs) p.split *= 2;
+  p.split = few_split(N, K, max_pairs);
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc, p.dtype = dtype;
   p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();
@@ -267,7 +279,7 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
     return GEMM_ERR_LAUNCH;
   dgemm::Mx4Params p;
   p.M = M, p.N = N, p.K = K;
-  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, {0.76, 0.48});
+  p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, {0.70, 0.44});
   gemm_status_t st = partials(p.sched, M, N, stream, &p.ws, &p.ldw);
   if (st != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
@@ -387,7 +399,7 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int
   int max_pairs;
   if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (K == 0) return scale_only(dtype, M, N, 0.f, Y, ldy, stream);
-  if (M <= dgemm::kMx4FewRawRows)
+  if (few_raw(M, N, K, max_pairs))
     return run_few(dtype, M, N, K, 1.f, X, ldx, nullptr, 0, nullptr, w_codes, ldw, w_scales, 0.f,
                    Y, ldy, fault, max_pairs, stream);
   const int ldq = code_ld(GEMM_MXFP4, K);
@@ -444,7 +456,7 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
   p.sb = static_cast<const unsigned char*>(b_scales);
   const int nk = ceil_div(K, dgemm::kMxGradBK);
-  p.sched = schedule(M, N, nk, max_pairs, 8, {0.74, 0.56});
+  p.sched = schedule(M, N, nk, max_pairs, 8, {0.66, 0.50});
   // FP32 results: at most 1024 terms per sum in tensor memory.
   p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
   if ((st = partials(p.sched, M, N, stream, &p.ws, &p.ldw)) != GEMM_OK) return st;

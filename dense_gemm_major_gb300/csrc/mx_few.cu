@@ -1,6 +1,7 @@
 // C = alpha * A . B^T + beta * C for up to 64 rows of A (decoding, small
-// batches), B (N x K) in MXFP4; A either in MXFP4 or, up to 48 rows, a 16- or
-// 32-bit array that is quantised to MXFP4 on the way, in the same launch.
+// batches), B (N x K) in MXFP4; A either in MXFP4 or, up to kMx4FewRawRows
+// rows of moderate length, a 16- or 32-bit array that is quantised to MXFP4 on
+// the way, in the same launch.
 //
 // What bounds it is reading B once (N K 17 / 32 bytes) and, for a few rows,
 // latency.  B's rows are the M side of tcgen05.mma.kind::mxf4 (128 columns of
@@ -10,7 +11,7 @@
 // through distributed shared memory in rank order, so results are
 // reproducible and there is no workspace and no second launch.
 //
-// Measured at N = K = 4096, back to back: 1 row 4.9 us, 8 5.3, 33 8.6 (a cold
+// Measured at N = K = 4096, back to back: 1 row 4.5 us, 8 4.9, 33 7.6 (a cold
 // read of B's 8.9 MB alone takes 1.3 us; launch, tensor memory, barriers and
 // the two cluster barriers are the most of the rest).
 //
@@ -278,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------ sum of the cluster's partial tiles
     cluster_sync_all();
     // This CTA adds up BN / split of the columns, four of a row per thread, all
-    // partial tiles' values on their way at once (33 x 4096 x 4096 8.6 us, one
-    // value after the other 8.9).
+    // partial tiles' values on their way at once (33 x 4096 x 4096 8.9 -> 8.6 us
+    // against one value after the other).
     constexpr int kMaxSplit = 8;
     const int share = BN / p.split / 4;
     for (int i = threadIdx.x; i < share * p.M; i += kThreads) {

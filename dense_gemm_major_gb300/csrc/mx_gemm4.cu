@@ -21,6 +21,11 @@
 // and the scales of the ring's three stages (two accumulators and two stages
 // of scales would not fit): the draining warps take all of it to registers
 // before they scale and store, so that the next tile can start.
+//
+// Measured: 8192^3 155 us (7.1 PFLOP/s), 4096^3 26.  At 8192^3 the loads alone
+// take 136 us; with all stores going to one row of C it takes 139: what is
+// left over is the write traffic of C, not its instructions (streaming and
+// write-through stores change nothing).
 #include "mx.cuh"
 
 namespace dgemm {

@@ -33,7 +33,7 @@
  *
  * Device memory: products that share out K (few tiles, long K) keep FP32
  * partial results in a workspace of the library, and gemm_mx4_linear with more
- * than a few rows its quantised X in another: one each per (device, stream),
+ * than a few rows, or long ones, its quantised X in another: one each per (device, stream),
  * grown after synchronising that stream and kept until the process exits.
  * Before a stream capture, make one call of the same sizes on that stream.
  */

@@ -274,6 +274,25 @@ def test_linear(dg, dtype, shape):
     assert (out[:, N:] == -1).all()
 
 
+# Few rows: the last size that the product's kernel quantises itself and the
+# first that is quantised before it, by rows and by length.
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(24, 300, 8192), (25, 300, 8192), (33, 129, 7999),
+                                   (48, 400, 4096), (49, 400, 4096), (4, 140, 40000),
+                                   (5, 140, 40000), (1, 20, 70000)])
+def test_linear_few_long_rows(dg, dtype, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + N + K)
+    x = _rand(rng, M, K, dtype, spread=2.0)
+    w, wv = _operand(dg, _np(_rand(rng, N, K, spread=1.0)), "mxfp4", pad=16)
+    xv = ref.values(*ref.quantize(_np(x), "mxfp4"), "mxfp4")
+    want, total = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    for pad, offset in [(0, 0), (5, 1)]:
+        got = dg.mx_linear(_dev(x, "N", pad, offset), w)
+        check_device(dg)
+        _check(got, want, total, K, dtype)
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 200])
 def test_linear_special_rows(dg, M):
     """A token with an infinity or a NaN spoils its own row only; a row of
