@@ -22,10 +22,12 @@
 // of scales would not fit): the draining warps take all of it to registers
 // before they scale and store, so that the next tile can start.
 //
-// Measured: 8192^3 155 us (7.1 PFLOP/s), 4096^3 26.  At 8192^3 the loads alone
-// take 136 us; with all stores going to one row of C it takes 139: what is
-// left over is the write traffic of C, not its instructions (streaming and
-// write-through stores change nothing).
+// Measured: 8192^3 156 us (7.0 PFLOP/s), 4096^3 26.  16384^3 1095 (8.0
+// PFLOP/s).  At 8192^3 it takes 114 us without its MMAs, 137 without its stores
+// and 139 with all of them to one row of C: what stores cost is C's write
+// traffic beside the loads, not instructions.  Streaming and write-through
+// stores change nothing, whole 128-byte lines per warp 1 to 3 %, stores paced
+// over the next tile -2 to -5 % at the largest sizes and +5 % at smaller ones.
 #include "mx.cuh"
 
 namespace dgemm {
