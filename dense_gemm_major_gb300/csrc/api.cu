@@ -10,9 +10,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
-#include <map>
 #include <mutex>
-#include <tuple>
 #include <utility>
 
 #include <cuda.h>
@@ -22,6 +20,7 @@
 #include "dense_gemm.h"
 #include "launch.h"
 #include "ptx.cuh"
+#include "workspace.h"
 
 namespace {
 
@@ -46,64 +45,13 @@ struct DeviceInfo {
 std::mutex g_mu;
 DeviceInfo g_devices[kMaxDevices];
 
-// Device workspaces: one per (device, stream, use), grown on demand, never
-// shrunk, freed at process exit by the driver.  Use kWsPartials holds
-// split-K slices or stream-K partial tiles, kWsPack a packed operand; one
-// call can need both.
-struct Workspace {
-  float* ptr = nullptr;
-  size_t bytes = 0;
-  unsigned epoch = 0;   // kWsFlags: the last epoch handed to a launch
-};
-// kWsFlags holds the hand-over flags of cut tiles (the pair kernel's K
-// split, the SGEMM's stream-K pieces): zeroed when (re)allocated, then only
-// ever set to a launch's epoch (or cleared).
-constexpr int kWsPartials = 0, kWsPack = 1, kWsFlags = 2;
-std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_workspaces;   // guarded by g_mu
-
+// A workspace of FP32 words (workspace.h).
 gemm_status_t get_workspace(cudaStream_t stream, size_t bytes, float** out,
-                            int use = kWsPartials) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_UNSUPPORTED_DEVICE;
-  }
-  std::lock_guard<std::mutex> lock(g_mu);
-  Workspace& w = g_workspaces[std::make_tuple(dev, stream, use)];
-  if (w.bytes < bytes) {
-    // Earlier work queued on this stream may still use the old buffer.
-    if (w.ptr != nullptr) {
-      if (cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_LAUNCH;
-      }
-      cudaFree(w.ptr);
-      w.ptr = nullptr;
-      w.bytes = 0;
-    }
-    if (cudaMalloc(&w.ptr, bytes) != cudaSuccess) {
-      cudaGetLastError();
-      w.ptr = nullptr;
-      return GEMM_ERR_LAUNCH;
-    }
-    w.bytes = bytes;
-    if (use == kWsFlags && cudaMemsetAsync(w.ptr, 0, bytes, stream) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_LAUNCH;
-    }
-  }
-  *out = w.ptr;
-  return GEMM_OK;
-}
-
-// The next epoch of the K-split flags of (current device, stream); never 0.
-unsigned next_epoch(cudaStream_t stream) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
-  std::lock_guard<std::mutex> lock(g_mu);
-  Workspace& w = g_workspaces[std::make_tuple(dev, stream, kWsFlags)];
-  if (++w.epoch == 0) w.epoch = 1;
-  return w.epoch;
+                            dgemm::WorkspaceUse use = dgemm::kWsPartials) {
+  void* p = nullptr;
+  const gemm_status_t st = dgemm::get_workspace(stream, use, bytes, &p);
+  if (st == GEMM_OK) *out = static_cast<float*>(p);
+  return st;
 }
 
 constexpr long long kSplitkWorkspaceCap = 64ll << 20;   // bytes
@@ -795,7 +743,7 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
       // row-major operands are re-pitched, both in one launch.  A's copy
       // comes first.
       float* packed = nullptr;
-      st = get_workspace(stream, (size_t)plan.pack_bytes, &packed, kWsPack);
+      st = get_workspace(stream, (size_t)plan.pack_bytes, &packed, dgemm::kWsPack);
       if (st != GEMM_OK) return st;
       float* dst = packed;
       dgemm::RepitchJob jobs[2];
@@ -879,10 +827,10 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
         p.epoch = fixed->epoch;
       } else {
         float* flags = nullptr;
-        st = get_workspace(stream, (size_t)words * 4, &flags, kWsFlags);
+        st = get_workspace(stream, (size_t)words * 4, &flags, dgemm::kWsFlags);
         if (st != GEMM_OK) return st;
         p.sk_flags = reinterpret_cast<unsigned*>(flags);
-        p.epoch = next_epoch(stream);
+        p.epoch = dgemm::next_epoch(stream);
       }
     }
     p.alpha = alpha;
@@ -959,10 +907,10 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
       st = get_workspace(stream, (size_t)plan.workspace_bytes, &p.kpart);
       if (st != GEMM_OK) return st;
       float* flags = nullptr;
-      st = get_workspace(stream, (size_t)(plan.ctas / 2) * 8 * 4, &flags, kWsFlags);
+      st = get_workspace(stream, (size_t)(plan.ctas / 2) * 8 * 4, &flags, dgemm::kWsFlags);
       if (st != GEMM_OK) return st;
       p.kflag = reinterpret_cast<unsigned*>(flags);
-      p.epoch = next_epoch(stream);
+      p.epoch = dgemm::next_epoch(stream);
     }
     if (plan.cluster_ctas == 2)
       e = dgemm::launch_gemm_tc_pair(dtype, p, &tmA, &tmB, &tmC, plan.ctas / 2, stream);

@@ -1,9 +1,6 @@
 // C-ABI entry points of the microscaled (MX) operators: argument checks,
 // tensor maps, workspaces and launch.  See include/dense_gemm_mx.h.
 #include <cstdint>
-#include <map>
-#include <mutex>
-#include <tuple>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -12,50 +9,9 @@
 #include "dense_gemm_mx.h"
 #include "launch.h"
 #include "mx.h"
+#include "workspace.h"
 
 namespace {
-
-std::mutex g_mu;
-
-// Device workspaces, one per (device, stream, use): the quantised X of
-// gemm_mx4_linear, and the FP32 partial results of products split along K
-// (one call can need both).
-struct Workspace {
-  unsigned char* ptr = nullptr;
-  size_t bytes = 0;
-};
-constexpr int kWsQuantized = 0, kWsPartials = 1;
-std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_workspaces;   // guarded by g_mu
-
-gemm_status_t get_workspace(cudaStream_t stream, int use, size_t bytes, unsigned char** out) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_UNSUPPORTED_DEVICE;
-  }
-  std::lock_guard<std::mutex> lock(g_mu);
-  Workspace& w = g_workspaces[std::make_tuple(dev, stream, use)];
-  if (w.bytes < bytes) {
-    if (w.ptr != nullptr) {
-      // Earlier work queued on this stream may still use the old buffer.
-      if (cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_LAUNCH;
-      }
-      cudaFree(w.ptr);
-      w.ptr = nullptr;
-      w.bytes = 0;
-    }
-    if (cudaMalloc(&w.ptr, bytes) != cudaSuccess) {
-      cudaGetLastError();
-      w.ptr = nullptr;
-      return GEMM_ERR_LAUNCH;
-    }
-    w.bytes = bytes;
-  }
-  *out = w.ptr;
-  return GEMM_OK;
-}
 
 // The current device's fault word, and the CTA pairs that it can hold at
 // once with one CTA per SM (fewer than half of its SMs: a cluster's CTAs
@@ -210,10 +166,10 @@ gemm_status_t partials(const dgemm::MxSchedule& sc, int M, int N, cudaStream_t s
   *ws = nullptr;
   *ldw = ((long long)N + 3) / 4 * 4;
   if (sc.slices == 1) return GEMM_OK;
-  unsigned char* p = nullptr;
+  void* p = nullptr;
   const gemm_status_t st =
-      get_workspace(stream, kWsPartials, (size_t)sc.slices * M * *ldw * 4, &p);
-  *ws = reinterpret_cast<float*>(p);
+      dgemm::get_workspace(stream, dgemm::kWsPartials, (size_t)sc.slices * M * *ldw * 4, &p);
+  *ws = static_cast<float*>(p);
   return st;
 }
 
@@ -406,9 +362,10 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int
                    Y, ldy, fault, max_pairs, stream);
   const int ldq = code_ld(GEMM_MXFP4, K);
   const size_t code_size = ((size_t)M * ldq + 255) / 256 * 256;
-  unsigned char* ws = nullptr;
-  st = get_workspace(stream, kWsQuantized, code_size + (size_t)scale_bytes(M, K), &ws);
+  void* p = nullptr;
+  st = dgemm::get_workspace(stream, dgemm::kWsQuantized, code_size + (size_t)scale_bytes(M, K), &p);
   if (st != GEMM_OK) return st;
+  unsigned char* const ws = static_cast<unsigned char*>(p);
   st = status_of(dgemm::launch_mx_quantize(GEMM_MXFP4, dtype, GEMM_OP_N, M, K, X, ldx, ws, ldq,
                                            ws + code_size, stream));
   if (st != GEMM_OK) return st;

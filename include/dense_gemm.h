@@ -27,10 +27,13 @@
  *  - Every pointer is caller-owned DEVICE memory of the current device.  The
  *    work is queued on `stream` and the call returns without synchronising.
  *  - Device memory: the library owns up to three arrays per (device,
- *    stream), each allocated by the first call that needs it and grown,
- *    after synchronising that stream, when a later call needs more; they
- *    live until the process exits and calls on different streams never
- *    share one.  (1) An FP32 workspace (gemm_plan_t.workspace_bytes, at most
+ *    stream), each allocated by the first call that needs it and replaced
+ *    by a larger one (at least twice its size) when a later call needs
+ *    more; calls on different streams never share one.  All of them,
+ *    outgrown ones too, live until the process exits: a graph captured on a
+ *    stream holds the addresses of that time, and stays valid whatever is
+ *    called there later.  Graphs captured on one stream share its arrays:
+ *    their replays, and other work on that stream, must not overlap.  (1) An FP32 workspace (gemm_plan_t.workspace_bytes, at most
  *    64 MiB): split-K slices, the FP16/BF16 pair kernel's stream-K partial
  *    tiles, and the FP32 stream-K partial tiles of scaled calls with
  *    beta != 0.  (2) An operand copy (gemm_plan_t.pack_bytes, at most

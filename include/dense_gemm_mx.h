@@ -33,9 +33,11 @@
  *
  * Device memory: products that share out K (few tiles, long K) keep FP32
  * partial results in a workspace of the library, and gemm_mx4_linear with more
- * than a few rows, or long ones, its quantised X in another: one each per (device, stream),
- * grown after synchronising that stream and kept until the process exits.
- * Before a stream capture, make one call of the same sizes on that stream.
+ * than a few rows, or long ones, its quantised X in another: one each per
+ * (device, stream), under the rules of dense_gemm.h (replaced by a larger one
+ * when a call needs more, never freed, shared by the graphs captured on the
+ * stream, whose replays must not overlap).  Before a stream capture, make one
+ * call of the same sizes on that stream.
  */
 #ifndef DENSE_GEMM_MX_H_
 #define DENSE_GEMM_MX_H_

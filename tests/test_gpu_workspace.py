@@ -1,0 +1,91 @@
+"""GPU tests of the library's per-stream workspaces: captured graphs keep
+working after a later call on their stream has needed a larger one."""
+import numpy as np
+import pytest
+import torch
+
+from parity import check_device, gpu_lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dg():
+    return gpu_lib()
+
+
+def _capture(step, s):
+    """step() as a graph on stream s, after a call that allocates what it needs."""
+    with torch.cuda.stream(s):
+        step()
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = step()
+    return g, outs
+
+
+def _replays_like_eager(dg, g, outs, step, fills):
+    for fill in fills:
+        fill()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    check_device(dg)
+
+
+def test_mx_graph_replays_after_a_larger_call(dg):
+    """A layer step whose forward product has its own quantised X and whose
+    gradient sums ranges of K, captured; then a larger step on the stream."""
+    gen = torch.Generator("cuda").manual_seed(3)
+
+    def rand(rows, cols, dtype=torch.bfloat16):
+        return torch.randn((rows, cols), generator=gen, device="cuda").to(dtype)
+    w = dg.mx_quantize(rand(640, 768))
+    x, dy, wide = rand(80, 768), rand(3000, 256), dg.mx_quantize(rand(3000, 128), "mxint8")
+
+    def step():
+        return dg.mx_linear(x, w), dg.mx_grad(dy.t(), wide, dtype=torch.float32)
+    s = torch.cuda.Stream()
+    g, outs = _capture(step, s)
+    big = rand(5000, 768)
+    big_dy, big_kept = rand(8192, 512), dg.mx_quantize(rand(8192, 512), "mxint8")
+    held = []
+    with torch.cuda.stream(s):
+        held.append(dg.mx_linear(big, w))
+        held.append(dg.mx_grad(big_dy.t(), big_kept, dtype=torch.float32))
+    torch.cuda.synchronize()
+    # (Whatever the library freed would come back here.)
+    held += [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(64)]
+    _replays_like_eager(dg, g, outs, step,
+                        [lambda: None, lambda: (x.normal_(generator=gen), dy.normal_(generator=gen))])
+
+
+@pytest.mark.parametrize("shape,larger", [((256, 256, 256), (512, 512, 1024)),    # slices of K
+                                          ((2048, 2048, 512), (2048, 4096, 512)),  # cut tiles
+                                          ((1000, 1030, 777), (2000, 2062, 1555))])  # re-pitched
+def test_sgemm_graph_replays_after_a_larger_call(dg, shape, larger):
+    gen = torch.Generator("cuda").manual_seed(4)
+
+    def operands(M, N, K):
+        return (torch.randint(-4, 5, (M, K), generator=gen, device="cuda").float(),
+                torch.randint(-4, 5, (K, N), generator=gen, device="cuda").float())
+    A, B = operands(*shape)
+    LA, LB = operands(*larger)
+    s = torch.cuda.Stream()
+    g, outs = _capture(lambda: (dg.matmul(A, B),), s)
+    with torch.cuda.stream(s):
+        held = [dg.matmul(LA, LB) for _ in range(2)]
+    torch.cuda.synchronize()
+    held += [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(64)]
+    for seed in range(2):
+        A.random_(-4, 5, generator=gen)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        # Sums of small integers: exact in any order.
+        assert np.array_equal(outs[0].cpu().numpy(), (A.double() @ B.double()).cpu().numpy())
+    check_device(dg)
