@@ -46,10 +46,10 @@ std::mutex g_mu;
 DeviceInfo g_devices[kMaxDevices];
 
 // A workspace of FP32 words (workspace.h).
-gemm_status_t get_workspace(cudaStream_t stream, size_t bytes, float** out,
+gemm_status_t get_workspace(dgemm::StreamWorkspaces& workspaces, size_t bytes, float** out,
                             dgemm::WorkspaceUse use = dgemm::kWsPartials) {
   void* p = nullptr;
-  const gemm_status_t st = dgemm::get_workspace(stream, use, bytes, &p);
+  const gemm_status_t st = workspaces.get(use, bytes, &p);
   if (st == GEMM_OK) *out = static_cast<float*>(p);
   return st;
 }
@@ -724,6 +724,7 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
   st = plan_impl(dtype, op_a, op_b, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, dev->sms,
                  dev->pair_clusters, &plan, allow_copy, &dev->sgemm_caps);
   if (st != GEMM_OK) return st;
+  dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
   cudaError_t e = cudaSuccess;
 
   if (plan.path == GEMM_PATH_ZERO_FILL) {
@@ -743,7 +744,7 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
       // row-major operands are re-pitched, both in one launch.  A's copy
       // comes first.
       float* packed = nullptr;
-      st = get_workspace(stream, (size_t)plan.pack_bytes, &packed, dgemm::kWsPack);
+      st = get_workspace(workspaces, (size_t)plan.pack_bytes, &packed, dgemm::kWsPack);
       if (st != GEMM_OK) return st;
       float* dst = packed;
       dgemm::RepitchJob jobs[2];
@@ -810,14 +811,14 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
         if (plan.workspace_bytes > fixed->ws_bytes) return GEMM_ERR_SCRATCH_LIMIT;
         p.ws = fixed->ws;
       } else {
-        st = get_workspace(stream, (size_t)plan.workspace_bytes, &p.ws);
+        st = get_workspace(workspaces, (size_t)plan.workspace_bytes, &p.ws);
         if (st != GEMM_OK) return st;
       }
     }
     if (p.slices == 1 && plan.split_tiles > 0) {
       if (plan.workspace_bytes > 0) {
         if (fixed != nullptr) return GEMM_ERR_SCRATCH_LIMIT;   // (beta != 0: never planned)
-        st = get_workspace(stream, (size_t)plan.workspace_bytes, &p.tail_ws);
+        st = get_workspace(workspaces, (size_t)plan.workspace_bytes, &p.tail_ws);
         if (st != GEMM_OK) return st;
       }
       const long long words = 2ll * (plan.ctas - 1);
@@ -827,10 +828,10 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
         p.epoch = fixed->epoch;
       } else {
         float* flags = nullptr;
-        st = get_workspace(stream, (size_t)words * 4, &flags, dgemm::kWsFlags);
+        st = get_workspace(workspaces, (size_t)words * 4, &flags, dgemm::kWsFlags);
         if (st != GEMM_OK) return st;
         p.sk_flags = reinterpret_cast<unsigned*>(flags);
-        p.epoch = dgemm::next_epoch(stream);
+        p.epoch = workspaces.next_epoch();
       }
     }
     p.alpha = alpha;
@@ -890,7 +891,7 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
     p.ws = nullptr;
     p.ldw = ((long long)N + 3) / 4 * 4;
     if (p.slices > 1) {
-      st = get_workspace(stream, (size_t)plan.workspace_bytes, &p.ws);
+      st = get_workspace(workspaces, (size_t)plan.workspace_bytes, &p.ws);
       if (st != GEMM_OK) return st;
     }
     p.alpha = alpha;
@@ -904,13 +905,13 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
     if (plan.cluster_ctas == 2 && plan.split_in_k) {
       // Stream-K share: head partials and their flags, one per range
       // boundary (boundary 0 is unused).
-      st = get_workspace(stream, (size_t)plan.workspace_bytes, &p.kpart);
+      st = get_workspace(workspaces, (size_t)plan.workspace_bytes, &p.kpart);
       if (st != GEMM_OK) return st;
       float* flags = nullptr;
-      st = get_workspace(stream, (size_t)(plan.ctas / 2) * 8 * 4, &flags, dgemm::kWsFlags);
+      st = get_workspace(workspaces, (size_t)(plan.ctas / 2) * 8 * 4, &flags, dgemm::kWsFlags);
       if (st != GEMM_OK) return st;
       p.kflag = reinterpret_cast<unsigned*>(flags);
-      p.epoch = dgemm::next_epoch(stream);
+      p.epoch = workspaces.next_epoch();
     }
     if (plan.cluster_ctas == 2)
       e = dgemm::launch_gemm_tc_pair(dtype, p, &tmA, &tmB, &tmC, plan.ctas / 2, stream);

@@ -161,14 +161,14 @@ dgemm::MxSchedule schedule(int M, int N, int nk, int pairs, int group, StageCost
 }
 
 // The workspace of a schedule with slices.
-gemm_status_t partials(const dgemm::MxSchedule& sc, int M, int N, cudaStream_t stream, float** ws,
-                       long long* ldw) {
+gemm_status_t partials(const dgemm::MxSchedule& sc, int M, int N,
+                       dgemm::StreamWorkspaces& workspaces, float** ws, long long* ldw) {
   *ws = nullptr;
   *ldw = ((long long)N + 3) / 4 * 4;
   if (sc.slices == 1) return GEMM_OK;
   void* p = nullptr;
   const gemm_status_t st =
-      dgemm::get_workspace(stream, dgemm::kWsPartials, (size_t)sc.slices * M * *ldw * 4, &p);
+      workspaces.get(dgemm::kWsPartials, (size_t)sc.slices * M * *ldw * 4, &p);
   *ws = static_cast<float*>(p);
   return st;
 }
@@ -218,7 +218,8 @@ gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X
 // The product of checked operands, M, N, K > 0.
 gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a, long long lda,
                       const void* sa, const void* b, long long ldb, const void* sb, float beta,
-                      void* C, int ldc, unsigned* fault, int max_pairs, cudaStream_t stream) {
+                      void* C, int ldc, unsigned* fault, int max_pairs,
+                      dgemm::StreamWorkspaces& workspaces, cudaStream_t stream) {
   if (M <= dgemm::kMx4FewRows)
     return run_few(dtype, M, N, K, alpha, nullptr, 0, a, lda, sa, b, ldb, sb, beta, C, ldc, fault,
                    max_pairs, stream);
@@ -238,7 +239,7 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
   // (Groups of 2 / 8 / 64 tile columns: 8192^3 150 / 156 / 152 us, but 16384^3,
   // whose operands L2 does not hold, 1199 / 1095 / 1330.)
   p.sched = schedule(M, N, ceil_div(K, dgemm::kMx4BK), max_pairs, 8, {0.70, 0.44});
-  gemm_status_t st = partials(p.sched, M, N, stream, &p.ws, &p.ldw);
+  gemm_status_t st = partials(p.sched, M, N, workspaces, &p.ws, &p.ldw);
   if (st != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc, p.dtype = dtype;
@@ -331,8 +332,9 @@ gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha, const void* 
   int max_pairs;
   if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (empty) return scale_only(dtype, M, N, beta, C, ldc, stream);
+  dgemm::StreamWorkspaces workspaces(stream);
   return run_mx4(dtype, M, N, K, alpha, a_codes, lda, a_scales, b_codes, ldb, b_scales, beta, C,
-                 ldc, fault, max_pairs, stream);
+                 ldc, fault, max_pairs, workspaces, stream);
 }
 
 gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int ldx,
@@ -362,15 +364,16 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int
                    Y, ldy, fault, max_pairs, stream);
   const int ldq = code_ld(GEMM_MXFP4, K);
   const size_t code_size = ((size_t)M * ldq + 255) / 256 * 256;
+  dgemm::StreamWorkspaces workspaces(stream);   // held until the product is queued
   void* p = nullptr;
-  st = dgemm::get_workspace(stream, dgemm::kWsQuantized, code_size + (size_t)scale_bytes(M, K), &p);
+  st = workspaces.get(dgemm::kWsQuantized, code_size + (size_t)scale_bytes(M, K), &p);
   if (st != GEMM_OK) return st;
   unsigned char* const ws = static_cast<unsigned char*>(p);
   st = status_of(dgemm::launch_mx_quantize(GEMM_MXFP4, dtype, GEMM_OP_N, M, K, X, ldx, ws, ldq,
                                            ws + code_size, stream));
   if (st != GEMM_OK) return st;
   return run_mx4(dtype, M, N, K, 1.f, ws, ldq, ws + code_size, w_codes, ldw, w_scales, 0.f, Y,
-                 ldy, fault, max_pairs, stream);
+                 ldy, fault, max_pairs, workspaces, stream);
 }
 
 gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int dtype_c, int M,
@@ -420,7 +423,8 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   p.sched = schedule(M, N, nk, max_pairs, 16, {0.66, 0.50});
   // FP32 results: at most 1024 terms per sum in tensor memory.
   p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
-  if ((st = partials(p.sched, M, N, stream, &p.ws, &p.ldw)) != GEMM_OK) return st;
+  dgemm::StreamWorkspaces workspaces(stream);
+  if ((st = partials(p.sched, M, N, workspaces, &p.ws, &p.ldw)) != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc;
   p.fault = fault, p.timeout_ns = dgemm::wait_bound_ns();

@@ -33,7 +33,10 @@
  *    outgrown ones too, live until the process exits: a graph captured on a
  *    stream holds the addresses of that time, and stays valid whatever is
  *    called there later.  Graphs captured on one stream share its arrays:
- *    their replays, and other work on that stream, must not overlap.  (1) An FP32 workspace (gemm_plan_t.workspace_bytes, at most
+ *    their replays, and other work on that stream, must not overlap.
+ *    Host threads may call on one stream at the same time: each call's
+ *    kernels that use an array are queued together.  (cudaStreamPerThread
+ *    has arrays for each host thread that uses it.)  (1) An FP32 workspace (gemm_plan_t.workspace_bytes, at most
  *    64 MiB): split-K slices, the FP16/BF16 pair kernel's stream-K partial
  *    tiles, and the FP32 stream-K partial tiles of scaled calls with
  *    beta != 0.  (2) An operand copy (gemm_plan_t.pack_bytes, at most

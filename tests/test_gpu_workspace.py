@@ -1,5 +1,8 @@
 """GPU tests of the library's per-stream workspaces: captured graphs keep
-working after a later call on their stream has needed a larger one."""
+working after a later call on their stream has needed a larger one, and host
+threads may share a stream."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -89,3 +92,41 @@ def test_sgemm_graph_replays_after_a_larger_call(dg, shape, larger):
         # Sums of small integers: exact in any order.
         assert np.array_equal(outs[0].cpu().numpy(), (A.double() @ B.double()).cpu().numpy())
     check_device(dg)
+
+
+@pytest.mark.parametrize("per_thread", [False, True])
+def test_two_threads_call_on_one_stream(dg, per_thread):
+    """Layers of two threads through the C ABI (ctypes lets both run), one of
+    them larger at each call: each gets the product of its own rows."""
+    gen = torch.Generator("cuda").manual_seed(6)
+    w = dg.mx_quantize(torch.randn((256, 512), generator=gen, device="cuda"))
+    stream = 2 if per_thread else torch.cuda.Stream().cuda_stream   # 2: cudaStreamPerThread
+    calls = 60
+    jobs = []
+    for t in range(2):
+        xs = [torch.randn((70 + (37 * i if t else 0), 512), generator=gen, device="cuda").bfloat16()
+              for i in range(calls)]
+        ys = [torch.full((x.shape[0], 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+              for x in xs]
+        jobs.append((xs, ys, [dg.mx_linear(x, w) for x in xs]))
+    torch.cuda.synchronize()
+    go = threading.Barrier(2)
+    status = [None, None]
+
+    def work(t):
+        xs, ys, _ = jobs[t]
+        go.wait()
+        status[t] = [dg.gemm_mx4_linear("bf16", x.shape[0], 256, 512, x.data_ptr(), 512,
+                                        w.codes.data_ptr(), w.codes.stride(0), w.scales.data_ptr(),
+                                        y.data_ptr(), 256, stream) for x, y in zip(xs, ys)]
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    check_device(dg)
+    for t, (_, ys, want) in enumerate(jobs):
+        assert status[t] == [dg.GEMM_OK] * calls
+        for a, b in zip(ys, want):
+            assert torch.equal(a, b)

@@ -4,6 +4,7 @@ which hands out addresses and records what is freed."""
 import ctypes
 import os
 import subprocess
+import threading
 
 import pytest
 
@@ -41,10 +42,18 @@ int t_freed() { return (int)g_freed.size(); }
 int t_allocations() { return (int)g_sizes.size(); }
 size_t t_size(int i) { return g_sizes[i]; }
 size_t t_cleared() { size_t s = 0; for (size_t n : g_cleared) s += n; return s; }
-void* t_get(uintptr_t stream, int use, size_t bytes) {
+void* t_open(uintptr_t stream) { return new dgemm::StreamWorkspaces((cudaStream_t)stream); }
+void* t_use(void* w, int use, size_t bytes) {
   void* p = nullptr;
-  return dgemm::get_workspace((cudaStream_t)stream, (dgemm::WorkspaceUse)use, bytes, &p) == GEMM_OK
+  return ((dgemm::StreamWorkspaces*)w)->get((dgemm::WorkspaceUse)use, bytes, &p) == GEMM_OK
              ? p : nullptr;
+}
+unsigned t_epoch(void* w) { return ((dgemm::StreamWorkspaces*)w)->next_epoch(); }
+void t_close(void* w) { delete (dgemm::StreamWorkspaces*)w; }
+void* t_get(uintptr_t stream, int use, size_t bytes) {   // a call that needs one workspace
+  dgemm::StreamWorkspaces w((cudaStream_t)stream);
+  void* p = nullptr;
+  return w.get((dgemm::WorkspaceUse)use, bytes, &p) == GEMM_OK ? p : nullptr;
 }
 }
 """
@@ -63,6 +72,10 @@ def ws(tmp_path):
     h.t_get.restype = ctypes.c_void_p
     h.t_get.argtypes = [ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t]
     h.t_size.restype = h.t_cleared.restype = ctypes.c_size_t
+    h.t_open.restype = h.t_use.restype = ctypes.c_void_p
+    h.t_open.argtypes = [ctypes.c_size_t]
+    h.t_use.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t]
+    h.t_close.argtypes = h.t_epoch.argtypes = [ctypes.c_void_p]
     h.t_limit.argtypes = [ctypes.c_size_t]
     return h
 
@@ -103,3 +116,50 @@ def test_little_memory(ws):
     assert second not in (None, first) and ws.t_size(1) == 1200
     assert ws.t_get(16, PACK, 1600) is None
     assert ws.t_get(16, PACK, 1200) == second
+
+
+def _in_thread(f):
+    """f() started in a thread of its own; (thread, its results)."""
+    out = []
+    t = threading.Thread(target=lambda: out.append(f()), daemon=True)
+    t.start()
+    return t, out
+
+
+@pytest.mark.parametrize("first,second", [(QUANTIZED, QUANTIZED), (QUANTIZED, PARTIALS)])
+def test_a_call_keeps_others_on_its_stream_waiting(ws, first, second):
+    """From a call's first workspace until its last kernel is queued no other
+    thread gets one of the stream, be it to write it or to replace it."""
+    call = ws.t_open(16)
+    mine = ws.t_use(call, first, 1000)
+    t, out = _in_thread(lambda: ws.t_get(16, second, 5000))
+    t.join(0.2)
+    assert t.is_alive() and ws.t_allocations() == 1
+    assert ws.t_use(call, first, 500) == mine
+    # Another stream, and a call that needs no workspace, go on.
+    other, got = _in_thread(lambda: ws.t_get(32, first, 1000))
+    other.join(20)
+    assert got and got[0] is not None
+    ws.t_close(ws.t_open(16))
+    ws.t_close(call)
+    t.join(20)
+    assert out and out[0] not in (None, mine)
+
+
+def test_epochs_are_never_repeated(ws):
+    seen = []
+    for _ in range(3):
+        call = ws.t_open(16)
+        ws.t_use(call, FLAGS, 64)
+        seen += [ws.t_epoch(call), ws.t_epoch(call)]
+        ws.t_close(call)
+    assert seen == [1, 2, 3, 4, 5, 6]
+
+
+def test_the_per_thread_stream_is_another_one_in_each_thread(ws):
+    per_thread = 2   # cudaStreamPerThread
+    here = ws.t_get(per_thread, QUANTIZED, 1000)
+    t, out = _in_thread(lambda: ws.t_get(per_thread, QUANTIZED, 1000))
+    t.join(20)
+    assert out[0] not in (None, here)
+    assert ws.t_get(per_thread, QUANTIZED, 1000) == here
