@@ -16,7 +16,7 @@
 
 namespace {
 
-PyObject *g_empty, *g_raw_stream, *g_error, *g_tensor_type;   // set by setup()
+PyObject *g_empty, *g_raw_stream, *g_current_device, *g_error, *g_tensor_type;   // set by setup()
 PyObject *g_dtype[3], *g_uint8;                               // float32, float16, bfloat16
 PyObject *g_empty_names;                                      // ("dtype", "device")
 PyObject *n_is_cuda, *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_device, *n_index, *n_codes,
@@ -154,12 +154,25 @@ struct Quantized {
   }
 };
 
-// The given cudaStream_t, or torch's current stream on `device`.
+// Whether two operands' devices are the same.
+bool one_device(PyObject* a, PyObject* b) {
+  const int same = PyObject_RichCompareBool(a, b, Py_EQ);
+  if (same == 0) return value_error("operands must be on one device");
+  return same == 1;
+}
+
+// The given cudaStream_t, or torch's current stream on `device`, which must be
+// the current one: the library's kernels run there.
 bool stream_of(PyObject* stream, PyObject* device, cudaStream_t* out) {
   Ref s;
+  Ref index(PyObject_GetAttr(device, n_index));
+  if (!index) return false;
+  Ref current(PyObject_CallNoArgs(g_current_device));
+  if (!current) return false;
+  const int same = PyObject_RichCompareBool(index.p, current.p, Py_EQ);
+  if (same < 0) return false;
+  if (!same) return value_error("operands must be on the current CUDA device");
   if (stream == Py_None) {
-    Ref index(PyObject_GetAttr(device, n_index));
-    if (!index) return false;
     s.set(PyObject_CallOneArg(g_raw_stream, index.p));
     if (!s) return false;
   } else {
@@ -289,7 +302,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!x.read(a[0]) || !w.read(a[1])) return nullptr;
   if (x.fmt != GEMM_MXFP4 || w.fmt != GEMM_MXFP4)
     return value_error("mx_matmul takes mxfp4 operands"), nullptr;
-  if (!same_inner(x.cols, w.cols)) return nullptr;
+  if (!one_device(x.device.p, w.device.p) || !same_inner(x.cols, w.cols)) return nullptr;
   Ref dtype(result_dtype(a[3], a[2], g_dtype[2]));
   int code;
   double alpha, beta;
@@ -316,7 +329,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int ldx;
   Result y;
   cudaStream_t stream;
-  if (!same_inner(x.cols, w.cols) || !x.row_major(&ldx) ||
+  if (!one_device(x.device.p, w.device.p) || !same_inner(x.cols, w.cols) || !x.row_major(&ldx) ||
       !stream_of(a[3], x.device.p, &stream) ||
       !y.make(a[2], x.rows, w.rows, x.dtype.p, x.device.p, 0.0))
     return nullptr;
@@ -333,7 +346,7 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Quantized b;
   if (!x.read(a[0]) || !b.read(a[1])) return nullptr;
   if (x.code == 0) return value_error("mx_grad takes a float16 or bfloat16 A"), nullptr;
-  if (!same_inner(x.cols, b.rows)) return nullptr;
+  if (!one_device(x.device.p, b.device.p) || !same_inner(x.cols, b.rows)) return nullptr;
   // The leading dimension (a multiple of 8) of a single stored row is free, so
   // it is rounded up; a single column with unit stride is a single row stored
   // transposed.
@@ -396,6 +409,8 @@ PyObject* describe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (stype.p != g_uint8 || contiguous.p != Py_True || have < gemm_mx_scale_bytes(rows, cols))
     return value_error("scales must be contiguous uint8, 512 bytes for each 128 x 128 tile"),
            nullptr;
+  Ref device(PyObject_GetAttr(a[0], n_device)), sdevice(PyObject_GetAttr(a[1], n_device));
+  if (!device || !sdevice || !one_device(device.p, sdevice.p)) return nullptr;
   // (The pitch of a single row is free: its padded width.)
   return Py_BuildValue("ii", rows, rows > 1 ? ld : (int)(((long long)width + 15) / 16 * 16));
 }
@@ -423,7 +438,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if ((g_dtype[i] = PyObject_GetAttrString(a[0], types[i])) == nullptr) return nullptr;
   if ((g_uint8 = PyObject_GetAttrString(a[0], "uint8")) == nullptr) return nullptr;
   Ref c(PyObject_GetAttrString(a[0], "_C"));
-  if (!c || (g_raw_stream = PyObject_GetAttrString(c.p, "_cuda_getCurrentRawStream")) == nullptr)
+  if (!c || (g_raw_stream = PyObject_GetAttrString(c.p, "_cuda_getCurrentRawStream")) == nullptr ||
+      (g_current_device = PyObject_GetAttrString(c.p, "_cuda_getDevice")) == nullptr)
     return nullptr;
   if ((g_empty_names = Py_BuildValue("(OO)", n_dtype, n_device)) == nullptr) return nullptr;
   Py_INCREF(a[1]);

@@ -189,3 +189,79 @@ def test_reference_pack_round_trip(fmt):
     v = ref.values(c, s, fmt)
     again = ref.quantize(v, fmt)
     assert (ref.values(*again, fmt) == v).all()
+
+
+class FakeTensor:
+    """What the wrappers read of a tensor that claims to be on a GPU."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device, address=FAKE):
+        import torch
+        self.shape, self.dtype, self.device = shape, dtype, torch.device(device)
+        self.address = address
+
+    def stride(self):
+        return (self.shape[-1], 1)[-len(self.shape):]
+
+    def data_ptr(self):
+        return self.address
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+
+def _fake_quantized(device, rows=8, cols=64, fmt="mxfp4"):
+    import torch
+    width = cols // 2 if fmt == "mxfp4" else cols
+    return dg.MXTensor(FakeTensor((rows, width), torch.uint8, device, Q),
+                       FakeTensor((512,), torch.uint8, device, S), cols, fmt)
+
+
+def test_scales_must_be_where_the_codes_are():
+    import torch
+    codes = torch.zeros(4, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="one device"):
+        dg.MXTensor(codes, torch.zeros(512, dtype=torch.uint8, device="meta"), 64)
+    with pytest.raises(ValueError, match="one device"):
+        dg.MXTensor(FakeTensor((4, 32), torch.uint8, "cuda:0"),
+                    torch.zeros(512, dtype=torch.uint8), 64)
+
+
+def test_operands_must_be_on_one_device():
+    import torch
+    q0, q1 = _fake_quantized("cuda:0"), _fake_quantized("cuda:1")
+    x = FakeTensor((5, 64), torch.bfloat16, "cuda:0", X)
+    dy = FakeTensor((5, 8), torch.bfloat16, "cuda:0", X)
+    for f in [lambda: dg.mx_matmul(q0, q1), lambda: dg.mx_linear(x, q1),
+              lambda: dg.mx_grad(dy, q1)]:
+        with pytest.raises(ValueError, match="one device"):
+            f()
+
+
+def test_operands_must_be_on_the_current_device():
+    """With a stand-in for torch, whose current device is another one."""
+    import types
+
+    import torch
+    ext = dg._load_mx()
+    names = ("float32", "float16", "bfloat16", "uint8", "empty")
+    c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: 0, _cuda_getDevice=lambda: 0)
+    fake = types.SimpleNamespace(_C=c, **{n: getattr(torch, n) for n in names})
+    q1 = _fake_quantized("cuda:1")
+    x = FakeTensor((5, 64), torch.bfloat16, "cuda:1", X)
+    y = FakeTensor((5, 8), torch.bfloat16, "cuda:1", Y)
+    ext.setup(fake, dg.MXTensor, dg.GemmError)
+    try:
+        for stream in (None, 0, 16):
+            for f in [lambda: dg.mx_quantize(x, stream=stream),
+                      lambda: dg.mx_dequantize(q1, stream=stream),
+                      lambda: dg.mx_matmul(q1, q1, stream=stream),
+                      lambda: dg.mx_linear(x, q1, out=y, stream=stream),
+                      lambda: dg.mx_grad(y, q1, stream=stream)]:
+                with pytest.raises(ValueError, match="current CUDA device"):
+                    f()
+    finally:
+        ext.setup(torch, dg.MXTensor, dg.GemmError)
