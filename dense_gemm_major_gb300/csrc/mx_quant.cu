@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       const int tile = (p0 + i) * 2 + (lane >> 4);
-      if ((lane & 3) == 0 && tile < tiles) srow[tile * kMxTileBytes] = (unsigned char)s;
+      if ((lane & 3) == 0 && tile < tiles)
+        srow[(long long)tile * kMxTileBytes] = (unsigned char)s;
     }
   }
 }
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads)
               w[i][g] = *reinterpret_cast<const unsigned*>(q + col);
             }
           }
-          s[i][g] = srow[(col >> 7) * kMxTileBytes + ((col >> 5) & 3)];
+          s[i][g] = srow[(long long)(col >> 7) * kMxTileBytes + ((col >> 5) & 3)];
         }
       }
     }

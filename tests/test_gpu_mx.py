@@ -525,6 +525,37 @@ def test_arrays_past_32_bit_offsets(dg):
     check_device(dg)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_row_past_32_bit_scale_offsets(dg, fmt):
+    """A row of over 2^29 columns, whose scales lie further than 2^31 bytes
+    apart: the codes, scales and values of its pieces as short rows."""
+    W = 32768
+    K = 2 ** 29 + 5 * W + 1037
+    gen = torch.Generator("cuda").manual_seed(8)
+    x = torch.empty((1, K), dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, K, 1 << 27):
+        n = min(1 << 27, K - lo)
+        x[0, lo:lo + n] = torch.randn(n, generator=gen, device="cuda")
+    q = dg.mx_quantize(x, fmt)
+    y = dg.mx_dequantize(q)
+    check_device(dg)
+    body = K // W * W
+    per_byte = 2 if fmt == "mxfp4" else 1
+    scales = q.scales.view(-1, 512)[:, :4].reshape(-1)      # of row 0, block by block
+    for lo, piece in [(0, x[:, :body].view(-1, W)), (body, x[:, body:])]:
+        p = dg.mx_quantize(piece, fmt)
+        R, C = piece.shape
+        n = R * C
+        assert torch.equal(y[0, lo:lo + n].view(R, C), dg.mx_dequantize(p))
+        width = -(-C // per_byte)
+        assert torch.equal(q.codes[0, lo // per_byte:lo // per_byte + R * width],
+                           p.codes[:, :width].reshape(-1))
+        nb = -(-C // 32)
+        s = p.scales.view(-1, -(-nb // 4), 32, 4, 4).permute(0, 3, 2, 1, 4)
+        s = s.reshape(s.shape[0] * 128, -1)[:R, :nb].reshape(-1)
+        assert torch.equal(scales[lo // 32:lo // 32 + R * nb], s)
+
+
 # ------------------------------------------------------------ schedules
 
 @pytest.mark.parametrize("shape", [(2100, 2500, 300), (130, 200, 6000), (64, 3000, 2500),
