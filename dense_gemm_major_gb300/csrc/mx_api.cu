@@ -63,6 +63,7 @@ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 inline int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }
 inline bool good_format(int fmt) { return fmt == GEMM_MXFP4 || fmt == GEMM_MXINT8; }
 inline bool good_dtype(int d) { return d >= 0 && d <= 2; }
+inline bool good_size(int n) { return n >= 0 && n <= GEMM_MX_MAX_SIZE; }
 inline bool good_op(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 
 inline uint64_t span(long long rows, long long width, long long pitch) {
@@ -257,19 +258,20 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
 extern "C" {
 
 int gemm_mx_code_ld(gemm_mx_format_t fmt, int K) {
-  if (!good_format(fmt) || K < 0) return -1;
+  if (!good_format(fmt) || !good_size(K)) return -1;
   return code_ld(fmt, K);
 }
 
 long long gemm_mx_scale_bytes(int R, int K) {
-  if (R < 0 || K < 0) return -1;
+  if (!good_size(R) || !good_size(K)) return -1;
   return scale_bytes(R, K);
 }
 
 gemm_status_t gemm_mx_quantize(gemm_mx_format_t fmt, int dtype, gemm_op_t op, int R, int K,
                                const void* X, int ldx, void* codes, int ldq, void* scales,
                                cudaStream_t stream) {
-  if (!good_format(fmt) || !good_dtype(dtype) || !good_op(op) || R < 0 || K < 0)
+  if (!good_format(fmt) || !good_dtype(dtype) || !good_op(op) || !good_size(R) ||
+      !good_size(K))
     return GEMM_ERR_INVALID_ARG;
   if (R == 0 || K == 0) return GEMM_OK;
   const int es = elem_size(dtype);
@@ -292,7 +294,8 @@ gemm_status_t gemm_mx_quantize(gemm_mx_format_t fmt, int dtype, gemm_op_t op, in
 gemm_status_t gemm_mx_dequantize(gemm_mx_format_t fmt, int dtype, int R, int K,
                                  const void* codes, int ldq, const void* scales, void* Y, int ldy,
                                  cudaStream_t stream) {
-  if (!good_format(fmt) || !good_dtype(dtype) || R < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (!good_format(fmt) || !good_dtype(dtype) || !good_size(R) || !good_size(K))
+    return GEMM_ERR_INVALID_ARG;
   if (R == 0 || K == 0) return GEMM_OK;
   const int es = elem_size(dtype);
   if (Y == nullptr || ldy < K) return GEMM_ERR_INVALID_ARG;
@@ -312,7 +315,8 @@ gemm_status_t gemm_mx_dequantize(gemm_mx_format_t fmt, int dtype, int R, int K,
 gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha, const void* a_codes, int lda,
                        const void* a_scales, const void* b_codes, int ldb, const void* b_scales,
                        float beta, void* C, int ldc, cudaStream_t stream) {
-  if (!good_dtype(dtype) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (!good_dtype(dtype) || !good_size(M) || !good_size(N) || !good_size(K))
+    return GEMM_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return GEMM_OK;
   const int es = elem_size(dtype);
   if (C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
@@ -340,7 +344,8 @@ gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha, const void* 
 gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int ldx,
                               const void* w_codes, int ldw, const void* w_scales, void* Y,
                               int ldy, cudaStream_t stream) {
-  if (!good_dtype(dtype) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (!good_dtype(dtype) || !good_size(M) || !good_size(N) || !good_size(K))
+    return GEMM_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return GEMM_OK;
   const int es = elem_size(dtype);
   if (Y == nullptr || ldy < N) return GEMM_ERR_INVALID_ARG;
@@ -381,7 +386,7 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
                            const void* b_codes, int ldb, const void* b_scales, float beta,
                            void* C, int ldc, cudaStream_t stream) {
   if (!good_format(fmt) || (dtype != 1 && dtype != 2) || !good_op(op_a) ||
-      (dtype_c != 0 && dtype_c != dtype) || M < 0 || N < 0 || K < 0)
+      (dtype_c != 0 && dtype_c != dtype) || !good_size(M) || !good_size(N) || !good_size(K))
     return GEMM_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return GEMM_OK;
   const int es = elem_size(dtype_c);

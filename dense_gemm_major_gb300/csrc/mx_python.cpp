@@ -46,6 +46,8 @@ bool value_error(const char* text) {
   return false;
 }
 
+bool too_large() { return value_error("a size is above the formats' limit, 2^31 - 1024"); }
+
 PyObject* failed(gemm_status_t st, const char* what) {
   Ref e(PyObject_CallFunction(g_error, "is", (int)st, what));
   if (e) PyErr_SetObject(g_error, e.p);
@@ -264,6 +266,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   cudaStream_t stream;
   if (!stream_of(a[2], x.device.p, &stream)) return nullptr;
+  if (x.rows > GEMM_MX_MAX_SIZE || x.cols > GEMM_MX_MAX_SIZE) return too_large(), nullptr;
   const int ldq = gemm_mx_code_ld(fmt, x.cols);
   const long long codes = (long long)x.rows * ldq;
   Ref size(PyLong_FromLongLong(codes + gemm_mx_scale_bytes(x.rows, x.cols)));
@@ -400,6 +403,7 @@ PyObject* describe(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (unit != 1 && width > 1))
     return value_error("codes must be uint8 rows of at least the format's bytes for cols"),
            nullptr;
+  if (rows > GEMM_MX_MAX_SIZE || cols > GEMM_MX_MAX_SIZE) return too_large(), nullptr;
   Ref stype(PyObject_GetAttr(a[1], n_dtype));
   Ref contiguous(PyObject_CallMethodNoArgs(a[1], n_is_contiguous));
   Ref count(PyObject_CallMethodNoArgs(a[1], n_numel));

@@ -25,6 +25,9 @@
  *           255 (gemm_mx_quantize writes 0).
  * Both bases are 16-byte aligned, else GEMM_ERR_MISALIGNED.
  *
+ * Sizes (M, N, K and R) are at most GEMM_MX_MAX_SIZE, so that the tiles which
+ * cover an array end below 2^31; larger ones are GEMM_ERR_INVALID_ARG.
+ *
  * dtype codes are those of gemm_plan: 0 = FP32, 1 = FP16, 2 = BF16.  Pointers,
  * streams, errors and the device fault word follow dense_gemm.h: argument
  * problems are reported synchronously before anything is queued, work is
@@ -50,10 +53,13 @@ extern "C" {
 
 typedef enum gemm_mx_format_t { GEMM_MXFP4 = 0, GEMM_MXINT8 = 1 } gemm_mx_format_t;
 
+#define GEMM_MX_MAX_SIZE (2147483647 - 1023)
+
 /* Smallest row pitch of the codes in bytes, a multiple of 16; -1 for a bad
- * format or K < 0. */
+ * format, K < 0 or K > GEMM_MX_MAX_SIZE. */
 int gemm_mx_code_ld(gemm_mx_format_t fmt, int K);
-/* Bytes of the scales of an R x K array; -1 for a negative size. */
+/* Bytes of the scales of an R x K array; -1 for a size that is negative or
+ * above GEMM_MX_MAX_SIZE. */
 long long gemm_mx_scale_bytes(int R, int K);
 
 /*

@@ -241,27 +241,71 @@ def test_operands_must_be_on_one_device():
             f()
 
 
-def test_operands_must_be_on_the_current_device():
-    """With a stand-in for torch, whose current device is another one."""
+@pytest.fixture
+def current_device_0():
+    """A stand-in for torch that has a current CUDA device, number 0."""
     import types
 
     import torch
     ext = dg._load_mx()
     names = ("float32", "float16", "bfloat16", "uint8", "empty")
     c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: 0, _cuda_getDevice=lambda: 0)
-    fake = types.SimpleNamespace(_C=c, **{n: getattr(torch, n) for n in names})
+    ext.setup(types.SimpleNamespace(_C=c, **{n: getattr(torch, n) for n in names}), dg.MXTensor,
+              dg.GemmError)
+    yield
+    ext.setup(torch, dg.MXTensor, dg.GemmError)
+
+
+def test_operands_must_be_on_the_current_device(current_device_0):
+    import torch
     q1 = _fake_quantized("cuda:1")
     x = FakeTensor((5, 64), torch.bfloat16, "cuda:1", X)
     y = FakeTensor((5, 8), torch.bfloat16, "cuda:1", Y)
-    ext.setup(fake, dg.MXTensor, dg.GemmError)
-    try:
-        for stream in (None, 0, 16):
-            for f in [lambda: dg.mx_quantize(x, stream=stream),
-                      lambda: dg.mx_dequantize(q1, stream=stream),
-                      lambda: dg.mx_matmul(q1, q1, stream=stream),
-                      lambda: dg.mx_linear(x, q1, out=y, stream=stream),
-                      lambda: dg.mx_grad(y, q1, stream=stream)]:
-                with pytest.raises(ValueError, match="current CUDA device"):
-                    f()
-    finally:
-        ext.setup(torch, dg.MXTensor, dg.GemmError)
+    for stream in (None, 0, 16):
+        for f in [lambda: dg.mx_quantize(x, stream=stream),
+                  lambda: dg.mx_dequantize(q1, stream=stream),
+                  lambda: dg.mx_matmul(q1, q1, stream=stream),
+                  lambda: dg.mx_linear(x, q1, out=y, stream=stream),
+                  lambda: dg.mx_grad(y, q1, stream=stream)]:
+            with pytest.raises(ValueError, match="current CUDA device"):
+                f()
+
+
+# ------------------------------------------------------------ the largest sizes
+
+LIMIT = 2 ** 31 - 1024
+
+
+@pytest.mark.parametrize("K", [LIMIT - 33, LIMIT - 1, LIMIT])
+def test_sizes_up_to_the_limit(K):
+    assert dg.gemm_mx_code_ld("mxfp4", K) == -(-((K + 1) // 2) // 16) * 16
+    assert dg.gemm_mx_code_ld("mxint8", K) == -(-K // 16) * 16
+    assert dg.gemm_mx_scale_bytes(1, K) == -(-K // 128) * 512
+    assert dg.gemm_mx_scale_bytes(K, 1) == -(-K // 128) * 512
+
+
+@pytest.mark.parametrize("K", [LIMIT + 1, 2 ** 31 - 16, 2 ** 31 - 1])
+def test_sizes_past_the_limit_are_refused(K):
+    for fmt in ("mxfp4", "mxint8"):
+        assert dg.gemm_mx_code_ld(fmt, K) == -1
+        for R, C in [(K, 64), (1, K)]:
+            assert _quantize(fmt=fmt, R=R, K=C, ldx=2 ** 31 - 1, ldq=2 ** 31 - 16) == INVALID
+            assert dg.gemm_mx_dequantize(fmt, "bf16", R, C, Q, 2 ** 31 - 16, S, Y,
+                                         2 ** 31 - 1) == INVALID
+    assert dg.gemm_mx_scale_bytes(1, K) == -1 and dg.gemm_mx_scale_bytes(K, 1) == -1
+    ld = 2 ** 31 - 16
+    for M, N, C in [(K, 8, 64), (4, K, 64), (4, 8, K)]:
+        assert dg.gemm_mx4("bf16", M, N, C, 1.0, Q, ld, S, Q2, ld, S2, 0.0, Y, ld) == INVALID
+        assert dg.gemm_mx4_linear("bf16", M, N, C, X, ld, Q, ld, S, Y, ld) == INVALID
+        assert dg.gemm_mx_grad("mxint8", "bf16", "N", "bf16", M, N, C, 1.0, X, ld, Q, ld, S, 0.0,
+                               Y, ld) == INVALID
+
+
+def test_wrappers_refuse_sizes_past_the_limit(current_device_0):
+    import torch
+    with pytest.raises(ValueError, match="limit"):
+        dg.mx_quantize(FakeTensor((1, 2 ** 31 - 1), torch.bfloat16, "cuda:0", X), stream=16)
+    for shape, cols in [((1, 2 ** 31 - 16), 2 ** 31 - 1), ((2 ** 31 - 1, 16), 16)]:
+        with pytest.raises(ValueError, match="limit"):
+            dg.MXTensor(FakeTensor(shape, torch.uint8, "cuda:0", Q),
+                        FakeTensor((2 ** 40,), torch.uint8, "cuda:0", S), cols)
