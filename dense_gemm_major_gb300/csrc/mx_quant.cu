@@ -133,10 +133,14 @@ __global__ void __launch_bounds__(kThreads)
     // The block's values as loaded (pairs of 16-bit ones stay packed: half the
     // registers, twice the CTAs per SM).
     unsigned raw[32];
-    if (L::V == 1 || (vec && r + 2 <= R && k0 + kMxBlock <= K)) {
+    if ((L::V == 1 || vec) && r + L::V <= R && k0 + kMxBlock <= K) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        raw[j] = L::V == 2 || (k0 + j < K && r < R)
+        raw[j] = *reinterpret_cast<const unsigned*>(X + (long long)(k0 + j) * ldx + r);
+    } else if constexpr (L::V == 1) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        raw[j] = k0 + j < K && r < R
                      ? *reinterpret_cast<const unsigned*>(X + (long long)(k0 + j) * ldx + r)
                      : 0u;
     } else {
@@ -180,15 +184,28 @@ __global__ void __launch_bounds__(kThreads)
       sscale[row * 8 + warp] = (unsigned char)s;
     }
     __syncthreads();
-    constexpr int kChunksPerRow = L::kRowBytes / 16;
+    // In 16-byte chunks; a ragged piece up to the end of its last group of 8
+    // columns in words.
+    unsigned char* const q = codes + (long long)r0 * ldq + (long long)piece * L::kRowBytes;
+    if (K - piece * 256 > 248) {
+      constexpr int kChunks = L::kRowBytes / 16;
 #pragma unroll
-    for (int i = threadIdx.x; i < L::kRows * kChunksPerRow; i += kThreads) {
-      const int row = i / kChunksPerRow, c = i % kChunksPerRow;
-      const long long at = (long long)piece * L::kRowBytes + c * 16;   // (a row's pitch has
-      if (r0 + row < R && at < ldq)                                    // whole 16-byte chunks)
-        if (at < (kFmt == GEMM_MXFP4 ? ((long long)K + 1) / 2 : (long long)K))
-          *reinterpret_cast<uint4*>(codes + (long long)(r0 + row) * ldq + at) =
-              *reinterpret_cast<const uint4*>(scode + row * L::kPitch + c * 16);
+      for (int i = threadIdx.x; i < L::kRows * kChunks; i += kThreads) {
+        const int row = i / kChunks, at = i % kChunks * 16;
+        if (r0 + row < R)
+          *reinterpret_cast<uint4*>(q + row * ldq + at) =
+              *reinterpret_cast<const uint4*>(scode + row * L::kPitch + at);
+      }
+    } else {
+      constexpr int kWords = L::kRowBytes / 4;
+      const int left = (K - piece * 256 + 7) / 8 * (L::kBlockBytes / 4);
+#pragma unroll 1
+      for (int i = threadIdx.x; i < L::kRows * kWords; i += kThreads) {
+        const int row = i / kWords, at = i % kWords * 4;
+        if (r0 + row < R && at < left)
+          *reinterpret_cast<unsigned*>(q + row * ldq + at) =
+              *reinterpret_cast<const unsigned*>(scode + row * L::kPitch + at);
+      }
     }
     for (int i = threadIdx.x; i < L::kRows * 2; i += kThreads) {
       const int row = i >> 1, tile = piece * 2 + (i & 1);

@@ -103,6 +103,33 @@ def test_quantize_bytes(dg, fmt, dtype, op, shape):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("shape", [(1, 1), (3, 9), (130, 40), (70, 250), (33, 273), (64, 517)])
+def test_quantize_writes_only_its_bytes(dg, fmt, dtype, op, shape):
+    """Whole groups of 8 columns of a code row, and the scales of rows that
+    exist; what lies between rows belongs to the caller."""
+    R, K = shape
+    x = _dev(_rand(np.random.default_rng(R), R, K, dtype), op)
+    ldq = dg.gemm_mx_code_ld(fmt, K) + 32
+    codes = torch.full((R, ldq), 0xA5, dtype=torch.uint8, device="cuda")
+    scales = torch.full((dg.gemm_mx_scale_bytes(R, K),), 0xA5, dtype=torch.uint8, device="cuda")
+    assert dg.gemm_mx_quantize(fmt, dtype, op, R, K, x.data_ptr(), x.stride(1 if op == "T" else 0),
+                               codes.data_ptr(), ldq, scales.data_ptr(),
+                               torch.cuda.current_stream().cuda_stream) == dg.GEMM_OK
+    check_device(dg)
+    width = -(-K // 8) * (4 if fmt == "mxfp4" else 8)
+    assert (codes[:, width:] == 0xA5).all()
+    rows = scales.cpu().numpy().reshape(-(-R // 128), -(-K // 128), 32, 4, 4)
+    rows = rows.transpose(0, 3, 2, 1, 4).reshape(-(-R // 128) * 128, -1)
+    assert (rows[R:] == 0xA5).all()
+    want_c, want_s = ref.quantize(_np(x), fmt)
+    c, s = ref.unpack(codes[:, :ldq - 32].cpu().numpy(), scales.cpu().numpy(), K, fmt)
+    assert (s == want_s).all()
+    np.testing.assert_array_equal(ref.values(c, s, fmt), ref.values(want_c, want_s, fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("op", ["N", "T"])
 def test_quantize_special_values(dg, fmt, op):
     x = np.zeros((40, 256), dtype=np.float32)
