@@ -217,6 +217,20 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// 2, 4 or 8 bytes of codes, aligned to as many, as one or two words.
+template <int kBytes>
+__device__ __forceinline__ void load_codes(const unsigned char* c, unsigned* w) {
+  if constexpr (kBytes == 2) {
+    w[0] = *reinterpret_cast<const unsigned short*>(c);
+  } else if constexpr (kBytes == 4) {
+    w[0] = *reinterpret_cast<const unsigned*>(c);
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(c);
+    w[0] = x.x;
+    w[1] = x.y;
+  }
+}
+
 // As mx_quantize_kernel, the other way.  A thread's 8 columns of a piece are
 // consecutive for 16-bit results and two groups of four, 128 apart, for FP32,
 // so that a warp's 16-byte stores are contiguous.
@@ -225,7 +239,8 @@ __global__ void __launch_bounds__(kThreads)
     mx_dequantize_kernel(int R, int K, const unsigned char* __restrict__ codes, long long ldq,
                          const unsigned char* __restrict__ scales, T* __restrict__ Y,
                          long long ldy, bool vec) {
-  constexpr int G = sizeof(T) == 4 ? 2 : 1, W = 8 / G;    // groups of W columns
+  constexpr int G = sizeof(T) == 4 ? 2 : 1, W = 8 / G;    // groups of W columns,
+  constexpr int kBytes = kFmt == GEMM_MXFP4 ? W / 2 : W;   // of this many bytes
   wait_prior_grids();
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
@@ -239,30 +254,37 @@ __global__ void __launch_bounds__(kThreads)
   for (int p0 = blockIdx.y * kStep; p0 < pieces; p0 += gridDim.y * kStep) {
     unsigned w[kStep][2];
     unsigned s[kStep][G];
+    // (The two ways apart, as above.)
+    if ((p0 + kStep) * 256 <= K) {
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
+      for (int i = 0; i < kStep; ++i) {
+        w[i][1] = 0u;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int col = (p0 + i) * 256 + g * 128 + lane * W;
-        s[i][g] = 0u;
-        if constexpr (G == 1) w[i][1] = 0u;
-        w[i][g] = 0u;
-        if (col < K) {
-          if constexpr (kFmt == GEMM_MXFP4) {
-            if constexpr (G == 1)
-              w[i][0] = *reinterpret_cast<const unsigned*>(q + col / 2);
-            else
-              w[i][g] = *reinterpret_cast<const unsigned short*>(q + col / 2);
-          } else {
-            if constexpr (G == 1) {
-              const uint2 x = *reinterpret_cast<const uint2*>(q + col);
-              w[i][0] = x.x;
-              w[i][1] = x.y;
-            } else {
-              w[i][g] = *reinterpret_cast<const unsigned*>(q + col);
-            }
-          }
+        for (int g = 0; g < G; ++g) {
+          const int col = (p0 + i) * 256 + g * 128 + lane * W;
+          load_codes<kBytes>(q + (kFmt == GEMM_MXFP4 ? col / 2 : col), &w[i][g]);
           s[i][g] = srow[(long long)(col >> 7) * kMxTileBytes + ((col >> 5) & 3)];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        w[i][0] = w[i][1] = 0u;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int col = (p0 + i) * 256 + g * 128 + lane * W;
+          const unsigned char* c = q + (kFmt == GEMM_MXFP4 ? col / 2 : col);
+          s[i][g] = 0u;
+          if (col >= K) continue;
+          s[i][g] = srow[(long long)(col >> 7) * kMxTileBytes + ((col >> 5) & 3)];
+          if (col + W <= K) {
+            load_codes<kBytes>(c, &w[i][g]);
+          } else {   // nothing past a row's last code is read
+            const int bytes = kFmt == GEMM_MXFP4 ? (K - col + 1) / 2 : K - col;
+#pragma unroll
+            for (int j = 0; j < kBytes; ++j)
+              if (j < bytes) w[i][g + j / 4] |= (unsigned)c[j] << (8 * (j % 4));
+          }
         }
       }
     }

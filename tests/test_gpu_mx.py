@@ -173,6 +173,34 @@ def test_dequantize_values(dg, fmt, dtype, shape):
     assert (buf[:, shape[1]:] == -1).all()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(1, 1), (1, 5), (1, 33), (3, 7), (2, 250), (5, 1001)])
+def test_arrays_whose_last_row_ends_with_its_codes(dg, fmt, dtype, shape):
+    """The tensor of the codes has no byte past the last row's last code; what
+    follows in memory (0xFF here, finite scales' codes) is no part of it."""
+    R, K = shape
+    x = _np(_rand(np.random.default_rng(K), R, K))
+    codes, scales = ref.quantize(x, fmt)
+    cb, sb = ref.pack(codes, scales, fmt)
+    width = (K + 1) // 2 if fmt == "mxfp4" else K
+    pitch = cb.shape[1]
+    flat = np.full((R, pitch), 0xFF, dtype=np.uint8)
+    flat[:, :width] = cb[:, :width]
+    buf = torch.full((R * pitch + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    buf[:R * pitch] = torch.from_numpy(flat.reshape(-1)).cuda()
+    tight = buf[:(R - 1) * pitch + width].as_strided((R, width), (pitch, 1))
+    q = dg.MXTensor(tight, torch.from_numpy(sb).cuda(), K, fmt)
+    want = ref.values(codes, scales, fmt)
+    y = dg.mx_dequantize(q, TYPES[dtype])
+    check_device(dg)
+    assert torch.equal(y.cpu(), torch.from_numpy(want).to(TYPES[dtype]))
+    if fmt == "mxfp4" and dtype != "f32":
+        a = _rand(np.random.default_rng(1), 3, K, dtype)
+        av = ref.values(*ref.quantize(_np(a), fmt), fmt)
+        _check(dg.mx_linear(a.cuda(), q), av @ want.T, np.abs(av) @ np.abs(want).T, K, dtype)
+
+
 def test_dequantize_every_scale(dg):
     """All 256 scales, all codes of both formats; FP16 rounds and overflows."""
     for fmt in FMTS:
