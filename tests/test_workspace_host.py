@@ -66,8 +66,9 @@ def ws(tmp_path):
     src.write_text(HARNESS)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_build.nvcc())) or "/usr/local/cuda",
                         "include")
-    subprocess.check_call(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-pthread", str(src),
-                           "-o", str(lib), "-I", _build.CSRC, "-I", _build.INCLUDE, "-I", cuda])
+    # (-Bsymbolic: the stand-in's calls, even where torch has loaded the real ones.)
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-pthread",
+                           "-Wl,-Bsymbolic", str(src), "-o", str(lib), "-I", _build.CSRC, "-I", _build.INCLUDE, "-I", cuda])
     h = ctypes.CDLL(str(lib))
     h.t_get.restype = ctypes.c_void_p
     h.t_get.argtypes = [ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t]
