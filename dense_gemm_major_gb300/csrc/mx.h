@@ -78,6 +78,8 @@ struct Mx4Params {
   unsigned long long timeout_ns;
 };
 constexpr int kMx4BK = 512;
+// Terms of an FP32 result that the 4-bit products sum in tensor memory at a time.
+constexpr int kMx4SegTerms = 4096;
 // tmA, tmB: codes as bytes, boxes of 128 bytes x 64 and 128 rows; tmSA, tmSB:
 // scales as 64-bit words, one row per 128 rows of the operand, boxes of four
 // tiles.

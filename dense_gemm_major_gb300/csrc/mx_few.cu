@@ -30,8 +30,17 @@ constexpr int kChunks = BK / 128;                        // scale tiles along K 
 constexpr uint32_t kBBytes = BN * BK / 2;                // 16 KB
 constexpr uint32_t kSBytes = kChunks * kMxTileBytes;     // 1 KB
 
-// MT: rows of A that the MMA computes.
-template <int MT>
+// FP32 results: the tensor cores truncate the running sum at each step, and
+// where block scales lie so far apart that sums no longer fit 24 bits the
+// error grows with their number (over 32768 terms 1e-5 of the result's norm with
+// scales over 24 binades; see mx_gemm4.cu).  So a sum of
+// at most kMx4SegTerms terms is formed in the accumulator, and such sums are
+// added with rounding in other columns of tensor memory.
+constexpr int kSegTiles = kMx4SegTerms / BK;
+
+// MT: rows of A that the MMA computes; kSums: with columns for the sums of
+// segments.
+template <int MT, bool kSums>
 struct Layout {
   // Two CTAs fit an SM, so that one's MMAs and scale copies run beside the
   // other's: 64 x 8192 x 8192 took 14 us with one of twice the stages.
@@ -46,9 +55,12 @@ struct Layout {
   static constexpr uint32_t kABytes = MT * BK / 2;
   static constexpr uint32_t kStage = (kBBytes + kABytes + 2 * kSBytes + 1023) / 1024 * 1024;
   static constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;
-  static constexpr uint32_t kScaleCol = MT;              // TMEM: accumulator, then scales of
-  static constexpr uint32_t kTmemCols = MT <= 32 ? 64 : 128;   // two stages
-  static_assert(kScaleCol + 4 * 4 * kChunks <= kTmemCols, "tensor memory");
+  // Tensor memory: the accumulator, the scales of two stages, the sums.
+  static constexpr uint32_t kScaleCol = MT;
+  static constexpr uint32_t kSumCol = kScaleCol + 4 * 4 * kChunks;
+  static constexpr uint32_t kUsedCols = kSumCol + (kSums ? MT : 0);
+  static constexpr uint32_t kTmemCols = kUsedCols <= 64 ? 64 : (kUsedCols <= 128 ? 128 : 256);
+  static_assert(2 * kTmemCols <= 512, "tensor memory of two CTAs");
   static_assert(MT * BN * 4 <= kStages * kStage, "partial tiles reuse the ring");
   static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
 };
@@ -58,6 +70,7 @@ struct alignas(8) Barriers {
   uint64_t full[S];     // loaded, and A quantised
   uint64_t empty[S];
   uint64_t acc_full;
+  uint64_t acc_empty;   // a segment's sum has been taken
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -101,12 +114,13 @@ __device__ __forceinline__ void store_scaled(T* c, float sum, float alpha, float
   *c = from_f32_any<T>(v);
 }
 
-// kRaw: A is p.X, an array of T.
-template <int MT, typename T, bool kRaw>
+// kRaw: A is p.X, an array of T.  kSegments: sums of more than kSegTiles stages
+// in segments.
+template <int MT, typename T, bool kRaw, bool kSegments>
 __global__ void __launch_bounds__(kThreads, 2)
     mx4_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const Mx4FewParams p) {
-  using L = Layout<MT>;
+  using L = Layout<MT, kSegments>;
   constexpr int S = L::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
@@ -127,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     mbar_init(smem_u32(&bars->acc_full), 1);
+    mbar_init(smem_u32(&bars->acc_empty), 4);
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -174,6 +189,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool ok = true;
       for (int kt = kb; kt < ke; ++kt) {
         const uint32_t it = (uint32_t)(kt - kb), s = it % S;
+        const bool starts = kSegments ? it % kSegTiles == 0 : it == 0;   // a segment
+        if (kSegments && starts && it > 0) {
+          mma_commit(smem_u32(&bars->acc_full));
+          ok = role_wait(smem_u32(&bars->acc_empty), (it / kSegTiles - 1) & 1u, p.fault,
+                         p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
+          if (!ok) break;
+        }
         ok = role_wait(smem_u32(&bars->full[s]), (it / S) & 1u, p.fault, p.timeout_ns,
                        &bars->abort, kFaultTcMmaWait, true);
         if (!ok) break;
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (k < 2 * chunks)
             mma_mx4(tmem_base, blo + 2 * k, alo + 2 * k,
                     instr_desc_mx4(BN, MT, (k & 1) * 2), sfw + 4 * (k >> 1), sfx + 4 * (k >> 1),
-                    (kt > kb || k > 0) ? 1u : 0u);
+                    (!starts || k > 0) ? 1u : 0u);
         mma_commit(smem_u32(&bars->empty[s]));
       }
       if (ok) mma_commit(smem_u32(&bars->acc_full));
@@ -203,8 +225,40 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------ quantisation, then the epilogue
     const int v = (warp - kWorkWarp) % L::kGroupWarps;
     bool ok = true;
+    // Takes the accumulator of segment `taken`, not the last one, by warps 2-5.
+    uint32_t taken = 0;
+    const uint32_t lanes = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
+    auto take_segment = [&] {
+      ok = role_wait_lanes(smem_u32(&bars->acc_full), taken & 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcEpilogueWait);
+      if (!ok) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < MT / 16 && c * 16 < p.M; ++c) {
+        uint32_t r[16];
+        tmem_ld16(lanes + c * 16, r);
+        if (taken > 0) {
+          uint32_t sum[16];
+          tmem_ld16(lanes + L::kSumCol + c * 16, sum);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(sum[j]));
+        }
+        tmem_st16(lanes + L::kSumCol + c * 16, r);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty));
+      ++taken;
+    };
     for (int kt = kb + (warp - kWorkWarp) / L::kGroupWarps; kRaw && kt < ke; kt += L::kGroups) {
       const uint32_t it = (uint32_t)(kt - kb), s = it % S;
+      // (Every stage before this segment is, or will be, quantised without
+      // waiting for this warp.)
+      if (kSegments && warp < kWorkWarp + 4)
+        while (ok && (taken + 1) * kSegTiles <= it) take_segment();
+      if (!ok) break;
       ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
                            &bars->abort, kFaultTcProducerWait);
       if (!ok) break;
@@ -250,8 +304,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (warp < kWorkWarp + 4) {
       const int q = warp & 3;
+      if (kSegments)
+        while (ok && (int)(taken + 1) * kSegTiles < ke - kb) take_segment();
       if (ke > kb)
-        ok = ok && role_wait_lanes(smem_u32(&bars->acc_full), 0, p.fault, p.timeout_ns,
+        ok = ok && role_wait_lanes(smem_u32(&bars->acc_full), taken & 1u, p.fault, p.timeout_ns,
                                    &bars->abort, kFaultTcEpilogueWait);
       tc_fence_after();
       const int col = q * 32 + lane;           // within the tile
@@ -259,9 +315,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int c = 0; c < MT / 16; ++c) {
         if (c * 16 >= p.M) break;
         uint32_t r[16];
-        tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c * 16, r);
+        tmem_ld16(lanes + c * 16, r);
+        if (kSegments && taken > 0) {
+          uint32_t sum[16];
+          tmem_ld16(lanes + L::kSumCol + c * 16, sum);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            r[j] = __float_as_uint(__uint_as_float(sum[j]) + __uint_as_float(r[j]));
+        }
         if (p.split > 1) {
-            // The partial tile, row-major, where the ring was.
+          // The partial tile, row-major, where the ring was.
           float* part = reinterpret_cast<float*>(base) + c * 16 * BN + col;
 #pragma unroll
           for (int j = 0; j < 16; ++j) part[j * BN] = ke > kb ? __uint_as_float(r[j]) : 0.f;
@@ -335,16 +398,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+template <int MT, typename T, bool kRaw, bool kSegments>
+cudaError_t launch_kernel(const Mx4FewParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                          cudaStream_t stream) {
+  auto kernel = mx4_few_kernel<MT, T, kRaw, kSegments>;
+  constexpr int smem = Layout<MT, kSegments>::kSmem;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = mx_allow_smem(kernel, smem, &done);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.N + BN - 1) / BN;
+  return launch_gemm_kernel_clusters((unsigned)p.split, kernel, dim3((unsigned)(tiles * p.split)),
+                                     dim3(kThreads), smem, stream, *tmA, *tmB, p);
+}
+
 template <int MT, typename T, bool kRaw>
 cudaError_t launch_typed(const Mx4FewParams& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                          cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = mx_allow_smem(mx4_few_kernel<MT, T, kRaw>, Layout<MT>::kSmem, &done);
-  if (e != cudaSuccess) return e;
-  const int tiles = (p.N + BN - 1) / BN;
-  return launch_gemm_kernel_clusters((unsigned)p.split, mx4_few_kernel<MT, T, kRaw>,
-                                     dim3((unsigned)(tiles * p.split)), dim3(kThreads),
-                                     Layout<MT>::kSmem, stream, *tmA, *tmB, p);
+  if constexpr (sizeof(T) == 4) {
+    const int nk = (p.K + BK - 1) / BK;
+    if ((nk + p.split - 1) / p.split > kSegTiles)
+      return launch_kernel<MT, T, kRaw, true>(p, tmA, tmB, stream);
+  }
+  return launch_kernel<MT, T, kRaw, false>(p, tmA, tmB, stream);
 }
 
 template <typename T>

@@ -22,6 +22,17 @@
 // of scales would not fit): the draining warps take all of it to registers
 // before they scale and store, so that the next tile can start.
 //
+// FP32 results are summed in segments of kMx4SegTerms terms, which the draining
+// warps add with rounding: the tensor cores truncate the running sum at each
+// step, and where block scales lie so far apart that sums no longer fit 24 bits
+// the error grows with their number.  K = 32768, scales over 12 / 16 / 24
+// binades: 4.6e-6 / 8.7e-6 / 1.0e-5 of the result's norm in one piece, 5e-7 /
+// 1.0e-6 / 1.3e-6 in segments (a plain FP32 product 3e-7); over 8 binades 6e-8,
+// over 4, or with a few columns 20 times as large as the others, exact.
+// Segments of 1024 / 2048 / 4096 / 8192 terms take 239 / 199 / 180 / 175 us at
+// 8192^3, 4096 x 4096 x 16384 119 / 102 / 93 / 89 (in one piece 87).  16-bit
+// results round far coarser than either.
+//
 // Measured: 8192^3 156 us (7.0 PFLOP/s), 4096^3 26.  16384^3 1095 (8.0
 // PFLOP/s).  At 8192^3 it takes 114 us without its MMAs, 137 without its stores
 // and 139 with all of them to one row of C: what stores cost is C's write
@@ -34,6 +45,7 @@ namespace dgemm {
 namespace {
 
 constexpr int BK = kMx4BK;
+constexpr int kSegTiles = kMx4SegTerms / BK;
 constexpr int S = 3;
 constexpr int kThreads = 512;
 constexpr int kScaleWarps = 4, kEpiWarp = 4, kEpiWarps = 8, kLoadWarp = 12, kMmaWarp = 13;
@@ -76,7 +88,10 @@ struct alignas(8) Barriers {
 };
 static_assert(sizeof(Barriers) <= 512, "barrier block must fit its reserved space");
 
-template <typename T>
+// kSegments: sums of more than kSegTiles k-tiles in segments.  (Draining a
+// segment to add it takes longer than draining all columns at once: 7.5
+// against 7.0 us at 1000 x 1030 x 777.)
+template <typename T, bool kSegments>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -212,37 +227,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (w.row0 >= p.M) continue;
         const uint32_t idesc = instr_desc_mx4(256, (uint32_t)w.rows, 0);
         const uint32_t idesc2 = instr_desc_mx4(256, (uint32_t)w.rows, 2);
-        ok = role_wait(smem_u32(&bars->acc_empty), (local & 1u) ^ 1u, p.fault,
-                               p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
-        if (!ok) break;
-        tc_fence_after();
-        for (int kt = w.kb; kt < w.ke; ++kt) {
-          const uint32_t s = pos.slot;
-          const uint32_t st = smem_u32(base + s * kStage);
-          ok = ready || role_wait(smem_u32(&bars->full[s]), pos.parity, p.fault, p.timeout_ns,
-                                  &bars->abort, kFaultTcMmaWait, true);
+        int k0 = w.kb;
+        do {
+          const int k1 = kSegments ? min(k0 + kSegTiles, w.ke) : w.ke;
+          ok = role_wait(smem_u32(&bars->acc_empty), (local & 1u) ^ 1u, p.fault, p.timeout_ns,
+                         &bars->abort, kFaultTcMmaWait, true);
           if (!ok) break;
           tc_fence_after();
-          pos.next();
-          ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
-          const uint32_t blo = desc_lo(st, 16), alo = desc_lo(st + kBBytes, 16);
-          const uint32_t sfb = tmem_base + kScaleCol + s * kScaleStage;
-          const uint32_t sfa = sfb + 4 * kChunks;
-          const int chunks = min(kChunks, ktiles - kt * kChunks);
+          for (int kt = k0; kt < k1; ++kt) {
+            const uint32_t s = pos.slot;
+            const uint32_t st = smem_u32(base + s * kStage);
+            ok = ready || role_wait(smem_u32(&bars->full[s]), pos.parity, p.fault, p.timeout_ns,
+                                    &bars->abort, kFaultTcMmaWait, true);
+            if (!ok) break;
+            tc_fence_after();
+            pos.next();
+            ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
+            const uint32_t blo = desc_lo(st, 16), alo = desc_lo(st + kBBytes, 16);
+            const uint32_t sfb = tmem_base + kScaleCol + s * kScaleStage;
+            const uint32_t sfa = sfb + 4 * kChunks;
+            const int chunks = min(kChunks, ktiles - kt * kChunks);
 #pragma unroll
-          for (int k = 0; k < BK / 64; ++k) {
-            if (k < 2 * chunks) {
-              const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
-              mma_mx4_pair(tmem_base, blo + off, alo + off, (k & 1) ? idesc2 : idesc,
-                           sfb + 4 * (k >> 1), sfa + 8 * (k >> 1),
-                           (kt > w.kb || k > 0) ? 1u : 0u);
+            for (int k = 0; k < BK / 64; ++k) {
+              if (k < 2 * chunks) {
+                const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                mma_mx4_pair(tmem_base, blo + off, alo + off, (k & 1) ? idesc2 : idesc,
+                             sfb + 4 * (k >> 1), sfa + 8 * (k >> 1),
+                             (kt > k0 || k > 0) ? 1u : 0u);
+              }
             }
+            mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
           }
-          mma_commit_pair_multicast(smem_u32(&bars->empty[s]), 0x3);
-        }
-        if (!ok) break;
-        mma_commit_pair_multicast(smem_u32(&bars->acc_full), 0x3);
-        ++local;
+          if (!ok) break;
+          mma_commit_pair_multicast(smem_u32(&bars->acc_full), 0x3);
+          ++local;
+          k0 = k1;
+        } while (kSegments && k0 < w.ke);
       }
     }
     __syncwarp();
@@ -254,26 +274,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int half = (warp - kEpiWarp) >> 2;
     const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 && ((p.ldc | p.N) & 1) == 0;
     uint32_t local = 0;
-    for (int u = blockIdx.x >> 1; u < sc.units; u += npairs) {
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; u < sc.units && ok; u += npairs) {
       const MxUnit w = mx_unit(u, sc, nk);
       if (w.row0 >= p.M) continue;
       const int chunks = w.rows / 64;      // of 32 rows, this warp's share
       const int first = half * (w.rows / 2);
-      if (!role_wait_lanes(smem_u32(&bars->acc_full), local & 1u, p.fault, p.timeout_ns,
-                           &bars->abort, kFaultTcEpilogueWait, false, false))
-        break;
-      ++local;
-      tc_fence_after();
       const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + first;
       uint32_t r[4][32];
+      if constexpr (kSegments) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) tmem_ld32(t + c * 32, r[c]);
+        for (int c = 0; c < 4; ++c) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty), 0));
+          for (int j = 0; j < 32; ++j) r[c][j] = 0x80000000u;   // -0
+        }
+      }
+      int k0 = w.kb;
+      do {
+        ok = role_wait_lanes(smem_u32(&bars->acc_full), local & 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcEpilogueWait, false, false);
+        if (!ok) break;
+        tc_fence_after();
+        if constexpr (!kSegments) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < chunks) tmem_ld32(t + c * 32, r[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c < 2 * chunks) {
+              uint32_t x[16];
+              tmem_ld16(t + c * 16, x);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                uint32_t& sum = r[c / 2][(c & 1) * 16 + j];
+                sum = __float_as_uint(__uint_as_float(sum) + __uint_as_float(x[j]));
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty), 0));
+        ++local;
+        k0 += kSegTiles;
+      } while (kSegments && k0 < w.ke);
+      if (!ok) break;
       const int col = w.tn * 256 + (int)rank * 128 + q * 32 + lane;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -322,22 +370,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T>
-cudaError_t launch_typed(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+template <typename T, bool kSegments>
+cudaError_t launch_kernel(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
                          const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
                          cudaStream_t stream) {
   // The register split needs kRegsLaunch registers a thread at launch: with
   // fewer, its setmaxnreg.inc would wait for ever.
   static const bool fits = [] {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, mx4_kernel<T>) == cudaSuccess && a.numRegs == kRegsLaunch;
+    return cudaFuncGetAttributes(&a, mx4_kernel<T, kSegments>) == cudaSuccess && a.numRegs == kRegsLaunch;
   }();
   if (!fits) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = mx_allow_smem(mx4_kernel<T>, kSmem, &done);
+  cudaError_t e = mx_allow_smem(mx4_kernel<T, kSegments>, kSmem, &done);
   if (e != cudaSuccess) return e;
-  return launch_gemm_kernel(mx4_kernel<T>, dim3(2 * pairs), dim3(kThreads), kSmem, stream, *tmA,
+  return launch_gemm_kernel(mx4_kernel<T, kSegments>, dim3(2 * pairs), dim3(kThreads), kSmem, stream, *tmA,
                             *tmB, *tmSA, *tmSB, p);
+}
+
+template <typename T>
+cudaError_t launch_typed(const Mx4Params& p, const CUtensorMap* tmA, const CUtensorMap* tmB,
+                         const CUtensorMap* tmSA, const CUtensorMap* tmSB, int pairs,
+                         cudaStream_t stream) {
+  if constexpr (sizeof(T) == 4) {
+    const int nk = (p.K + BK - 1) / BK;
+    if ((nk + p.sched.slices - 1) / p.sched.slices > kSegTiles)
+      return launch_kernel<T, true>(p, tmA, tmB, tmSA, tmSB, pairs, stream);
+  }
+  return launch_kernel<T, false>(p, tmA, tmB, tmSA, tmSB, pairs, stream);
 }
 
 }  // namespace

@@ -665,6 +665,34 @@ def test_long_float32_sums_round_to_nearest(dg):
     assert np.linalg.norm(got - want) <= 4e-6 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("M,N,linear", [(2048, 2048, False), (8, 19600, False), (2, 19600, True),
+                                        (40, 260, False), (1, 260, True)])
+def test_long_float32_products_of_far_scales(dg, M, N, linear):
+    """Blocks whose scales lie up to 24 binades apart, so that no sum fits the
+    24 bits of FP32, over 32768 terms.  The tensor cores drop up to 2^-23 of
+    the running sum at each 64-deep step, on average half of that; a result
+    keeps at most 64 such steps (the sum of 4096 terms) and adds its at most
+    eight parts with 2^-24 each: 64 * 2^-24 + 8 * 2^-24 = 4.3e-6 of the
+    largest partial sums, which are below the result's norm in a random walk.
+    (In one piece, as with the first two shapes, it was 1e-5.)"""
+    K = 32768
+    gen = torch.Generator("cuda").manual_seed(12)
+
+    def rand(rows):
+        x = torch.randn((rows, K), generator=gen, device="cuda")
+        e = torch.randint(-12, 13, (rows, K // 32), generator=gen, device="cuda")
+        return (x.view(rows, -1, 32) * torch.exp2(e.float()).unsqueeze(-1)).view(rows, K)
+    x = rand(M)
+    b = dg.mx_quantize(rand(N))
+    a = dg.mx_quantize(x)
+    got = dg.mx_linear(x, b) if linear else dg.mx_matmul(a, b, dtype=torch.float32)
+    check_device(dg)
+    rows, cols = slice(0, 64), slice(0, N, max(N // 512, 1))
+    av = dg.mx_dequantize(a, torch.float32)[rows].double()
+    want = av @ dg.mx_dequantize(b, torch.float32)[cols].double().t()
+    assert (got[rows, cols].double() - want).norm() <= 4.3e-6 * want.norm()
+
+
 def test_refusals_of_the_wrappers(dg):
     x = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
     q4, q8 = dg.mx_quantize(x), dg.mx_quantize(x, "mxint8")
