@@ -422,12 +422,15 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   p.M = M, p.N = N, p.K = K;
   p.fmt = fmt, p.dtype = dtype, p.op_a = op_a, p.dtype_c = dtype_c;
   p.sb = static_cast<const unsigned char*>(b_scales);
-  const int nk = ceil_div(K, dgemm::kMxGradBK);
   // (Groups of 8 / 16 tile columns: dX 8192^3 569 / 556 us, 16384 x 4096 x 4096
   // 311 / 304, dW and 4096^3 alike.)
-  p.sched = schedule(M, N, nk, max_pairs, 16, {0.66, 0.50});
-  // FP32 results: at most 1024 terms per sum in tensor memory.
-  p.seg = dtype_c == 0 ? 1024 / dgemm::kMxGradBK : nk;
+  p.sched = schedule(M, N, ceil_div(K, dgemm::kMxGradBK), max_pairs, 16, {0.66, 0.50});
+  // Terms per sum in tensor memory, which truncates at each step of 16: sums of
+  // like terms come out too small, the more the longer they are (FP16, positive
+  // terms: 1.4e-6 over 1024, 8.5e-5 over 16384, 3e-3 over 2^19).  FP32 results:
+  // 1024 (512 / 256 leave a third / a sixth of the error and take 1.5 to 2.4 % /
+  // 7 to 13 % longer).  16-bit ones: 16384, a fifth of FP16's rounding.
+  p.seg = (dtype_c == 0 ? 1024 : 16384) / dgemm::kMxGradBK;
   dgemm::StreamWorkspaces workspaces(stream);
   if ((st = partials(p.sched, M, N, workspaces, &p.ws, &p.ldw)) != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;

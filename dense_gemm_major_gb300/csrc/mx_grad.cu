@@ -20,10 +20,10 @@
 // the accumulators.
 //
 // FP32 sums.  The MMA truncates the running sum at every 16-deep step: over
-// 8192 terms that was measured as a relative error of 6e-6.  For FP32
-// results a tile is therefore summed in segments (MxGradParams::seg), and
-// the draining warps add the segments in registers, rounding to nearest; the
-// two accumulators in tensor memory let that overlap the next segment.
+// 8192 terms that was measured as a relative error of 6e-6.  A tile is
+// therefore summed in segments (MxGradParams::seg), and the draining warps
+// add the segments in registers, rounding to nearest; the two accumulators in
+// tensor memory let that overlap the next segment.
 #include "mx.cuh"
 
 namespace dgemm {

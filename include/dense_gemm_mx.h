@@ -114,7 +114,12 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void *X, int
  * C := alpha * op(A) . B + beta * C, the products of a backward pass: A of
  * dtype (FP16 or BF16), B (K x N, blocks along N) in fmt, its values taken in
  * A's type (exact in BF16; FP16 rounds them).  FP32 accumulation; C is
- * row-major, of dtype_c (A's type or FP32), with any alignment.
+ * row-major, of dtype_c (A's type or FP32), with any alignment.  (The tensor
+ * cores truncate the running sum at each step of 16 terms.  FP32 results are
+ * sums, rounded to nearest, of parts of at most 1024 terms: an error of 2e-7
+ * of the result's norm with terms of random signs and up to 1.4e-6 with like
+ * ones, against 1e-7 to 4e-7 of a plain FP32 product; 16-bit results of parts
+ * of 16384 terms.)
  *   gradient of a layer's input:    A = dY (op N), B = W
  *   gradient of a layer's weights:  A = dY (op T, stored K x M), B = the
  *                                   layer's kept input

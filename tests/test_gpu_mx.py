@@ -665,6 +665,30 @@ def test_long_float32_sums_round_to_nearest(dg):
     assert np.linalg.norm(got - want) <= 4e-6 * np.linalg.norm(want)
 
 
+def test_long_16_bit_sums_keep_their_size(dg):
+    """A gradient over 2^19 tokens of like terms, too large for ranges of K:
+    what the truncation of each step in tensor memory takes off the results
+    stays below 2^-11 * 0.27 = 1.3e-4, a quarter of what FP16 rounds.  (Parts
+    of 16384 terms lose 1.0e-4; in one piece it was 3e-3.)"""
+    K, M, N = 1 << 19, 8192, 4224
+    gen = torch.Generator("cuda").manual_seed(15)
+    dy = torch.empty((K, M), dtype=torch.float16, device="cuda")
+    x = torch.empty((K, N), dtype=torch.float16, device="cuda")
+    step = 1 << 16
+    for lo in range(0, K, step):
+        dy[lo:lo + step] = torch.rand((step, M), generator=gen, device="cuda") + 0.5
+        x[lo:lo + step] = torch.rand((step, N), generator=gen, device="cuda") + 0.5
+    kept = dg.mx_quantize(x, "mxint8")
+    values = dg.mx_dequantize(kept, torch.float16)
+    got = dg.mx_grad(dy.t(), kept, alpha=2.0 ** -19)[:16].double()
+    check_device(dg)
+    want = torch.zeros((16, N), dtype=torch.float64, device="cuda")
+    for lo in range(0, K, step):
+        want += dy[lo:lo + step, :16].double().t() @ values[lo:lo + step].double()
+    want *= 2.0 ** -19
+    assert abs(float(((got - want) / want).mean())) <= 1.3e-4
+
+
 @pytest.mark.parametrize("M,N,linear", [(2048, 2048, False), (8, 19600, False), (2, 19600, True),
                                         (40, 260, False), (1, 260, True)])
 def test_long_float32_products_of_far_scales(dg, M, N, linear):
