@@ -535,6 +535,7 @@ def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     """alpha * (A @ B) + beta * out with A (M x K, float16 or bfloat16,
     row-major or a transposed view) and B a K x N MXTensor: ``mx_grad(dY, W)``
     is the gradient of a layer's input, ``mx_grad(dY.t(), kept_x)`` that of
-    its weights.  The result is of A's dtype or float32 (``dtype``, or that
+    its weights.  A has rows of a multiple of 16 bytes, or is contiguous (rows
+    of other widths are then copied to aligned ones first).  The result is of A's dtype or float32 (``dtype``, or that
     of ``out``)."""
     return (_mx or _load_mx()).grad(A, B, out, dtype, alpha, beta, stream)

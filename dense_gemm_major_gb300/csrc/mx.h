@@ -59,6 +59,11 @@ struct MxSchedule {
 };
 constexpr int kMxPairTile = 256;
 
+// D (16-byte aligned rows of ldd elements, a multiple of 8) := S, rows x cols
+// packed 16-bit elements.
+cudaError_t launch_mx_align(const void* S, long long rows, int cols, void* D, long long ldd,
+                            cudaStream_t stream);
+
 // C := alpha * (the sum over s of ws[s * M * ldw + i * ldw + j], in slice
 // order) + beta * C; dtype of C.  ldw is a multiple of 4.
 cudaError_t launch_mx_reduce(const float* ws, int slices, int M, int N, long long ldw, float alpha,

@@ -393,11 +393,14 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   if (C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
   if (!aligned(C, es)) return GEMM_ERR_MISALIGNED;
   const bool empty = K == 0 || alpha == 0.f;
+  // A as stored: `outer` rows of `inner` elements.
+  const int inner = op_a == GEMM_OP_T ? M : K, outer = op_a == GEMM_OP_T ? K : M;
+  const bool packed = lda == inner && lda % 8 != 0;
   gemm_status_t st;
   if (!empty) {
     if (A == nullptr || lda < (op_a == GEMM_OP_N ? K : M)) return GEMM_ERR_INVALID_ARG;
     if ((st = check_quantized(fmt, N, b_codes, ldb, b_scales)) != GEMM_OK) return st;
-    if (!aligned(A, 16) || lda % 8 != 0) return GEMM_ERR_MISALIGNED;
+    if (packed ? !aligned(A, 2) : (!aligned(A, 16) || lda % 8 != 0)) return GEMM_ERR_MISALIGNED;
     const uint64_t cs = span(M, (long long)N * es, (long long)ldc * es);
     const uint64_t as = op_a == GEMM_OP_N ? span(M, (long long)K * 2, (long long)lda * 2)
                                           : span(K, (long long)M * 2, (long long)lda * 2);
@@ -408,12 +411,21 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   int max_pairs;
   if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
   if (empty) return scale_only(dtype_c, M, N, beta, C, ldc, stream);
+  dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
+  const void* rows = A;
+  long long ldr = lda;
+  if (packed) {
+    ldr = ((long long)lda + 7) / 8 * 8;
+    void* p = nullptr;
+    if ((st = workspaces.get(dgemm::kWsPack, (size_t)outer * ldr * 2, &p)) != GEMM_OK) return st;
+    if ((st = status_of(dgemm::launch_mx_align(A, outer, inner, p, ldr, stream))) != GEMM_OK)
+      return st;
+    rows = p;
+  }
   alignas(64) CUtensorMap tmA, tmB;
   const CUtensorMapDataType dt =
       dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint64_t inner = (uint64_t)(op_a == GEMM_OP_T ? M : K);
-  const uint64_t outer = (uint64_t)(op_a == GEMM_OP_T ? K : M);
-  if (!encode_2d(&tmA, dt, A, inner, outer, (uint64_t)lda * 2, 64, 64) ||
+  if (!encode_2d(&tmA, dt, rows, (uint64_t)inner, (uint64_t)outer, (uint64_t)ldr * 2, 64, 64) ||
       !encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, b_codes, (uint64_t)code_bytes(fmt, N),
                  (uint64_t)K, (uint64_t)ldb, (uint32_t)code_bytes(fmt, 128), dgemm::kMxGradBK,
                  false))
@@ -431,7 +443,6 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   // 1024 (512 / 256 leave a third / a sixth of the error and take 1.5 to 2.4 % /
   // 7 to 13 % longer).  16-bit ones: 16384, a fifth of FP16's rounding.
   p.seg = (dtype_c == 0 ? 1024 : 16384) / dgemm::kMxGradBK;
-  dgemm::StreamWorkspaces workspaces(stream);
   if ((st = partials(p.sched, M, N, workspaces, &p.ws, &p.ldw)) != GEMM_OK) return st;
   p.alpha = alpha, p.beta = beta;
   p.C = C, p.ldc = ldc;

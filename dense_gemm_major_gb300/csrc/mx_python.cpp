@@ -350,16 +350,18 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!x.read(a[0]) || !b.read(a[1])) return nullptr;
   if (x.code == 0) return value_error("mx_grad takes a float16 or bfloat16 A"), nullptr;
   if (!one_device(x.device.p, b.device.p) || !same_inner(x.cols, b.rows)) return nullptr;
-  // The leading dimension (a multiple of 8) of a single stored row is free, so
-  // it is rounded up; a single column with unit stride is a single row stored
-  // transposed.
+  // The leading dimension of a single stored row is free: rounded up to a
+  // multiple of 8, which is read where it is, or for an unaligned one its width.
+  // A single column with unit stride is a single row stored transposed.
+  const bool aligned = ((uintptr_t)x.ptr & 15u) == 0;
+  auto single = [&](int width) { return aligned ? (int)(((long long)width + 7) / 8 * 8) : width; };
   gemm_op_t op = GEMM_OP_N;
   int lda;
   if ((x.s1 == 1 || x.cols <= 1) && !(x.cols == 1 && x.rows > 1 && x.s0 == 1)) {
-    lda = x.rows > 1 ? x.s0 : (int)(((long long)x.cols + 7) / 8 * 8);
+    lda = x.rows > 1 ? x.s0 : single(x.cols);
   } else if (x.s0 == 1 || x.rows <= 1) {
     op = GEMM_OP_T;
-    lda = x.cols > 1 ? x.s1 : (int)(((long long)x.rows + 7) / 8 * 8);
+    lda = x.cols > 1 ? x.s1 : single(x.rows);
   } else {
     return value_error("operands must have a unit row or column stride"), nullptr;
   }

@@ -12,7 +12,7 @@ namespace dgemm {
 
 enum WorkspaceUse {
   kWsPartials,   // FP32 partial results: split-K slices, stream-K tiles, ranges of K
-  kWsPack,       // copies of FP32 operands (transposed, or with aligned rows)
+  kWsPack,       // copies of operands (transposed, or with aligned rows)
   kWsFlags,      // hand-over flags of cut tiles: zeroed when allocated, then only ever set
                  // to a launch's epoch (or cleared)
   kWsQuantized,  // the quantised X of gemm_mx4_linear

@@ -35,8 +35,9 @@
  * overlap outputs.
  *
  * Device memory: products that share out K (few tiles, long K) keep FP32
- * partial results in a workspace of the library, and gemm_mx4_linear with more
- * than a few rows, or long ones, its quantised X in another: one each per
+ * partial results in a workspace of the library, gemm_mx4_linear with more
+ * than a few rows, or long ones, its quantised X in another, and gemm_mx_grad
+ * the copy of a packed A in the one of operand copies: one each per
  * (device, stream), under the rules of dense_gemm.h (replaced by a larger one
  * when a call needs more, never freed, shared by the graphs captured on the
  * stream, whose replays must not overlap).  Before a stream capture, make one
@@ -123,8 +124,10 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void *X, int
  *   gradient of a layer's input:    A = dY (op N), B = W
  *   gradient of a layer's weights:  A = dY (op T, stored K x M), B = the
  *                                   layer's kept input
- * op_a as in gemm_*_op; A is 16-byte aligned and lda a multiple of 8, else
- * GEMM_ERR_MISALIGNED.  K == 0 or alpha == 0: C := beta * C.
+ * op_a as in gemm_*_op.  A is 16-byte aligned and lda a multiple of 8, or A is
+ * packed with another lda (its rows follow one another: lda is the stored
+ * width) at any alignment of its type, which takes a copy with aligned rows in a
+ * workspace first; else GEMM_ERR_MISALIGNED.  K == 0 or alpha == 0: C := beta * C.
  */
 gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int dtype_c, int M,
                            int N, int K, float alpha, const void *A, int lda,

@@ -420,6 +420,52 @@ def test_grad_accumulates_into_a_padded_view(dg, fmt, op, dc):
     _check(out, _np(a) @ bv, 4 * total, K, dc)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("shape", [(1, 9, 7), (7, 40, 1), (33, 77, 129), (130, 64, 517),
+                                   (515, 130, 1003), (300, 256, 20), (1001, 96, 1030)])
+def test_grad_of_contiguous_operands(dg, dtype, op, shape):
+    """Contiguous A whose rows are no multiple of 16 bytes, as autograd gives
+    them, and slices of it that begin at odd addresses: the bits of the
+    product with an aligned copy of A."""
+    M, N, K = shape
+    rng = np.random.default_rng(M + N + K)
+    b, bv = _operand(dg, _np(_rand(rng, K, N, spread=1.0)), "mxint8")
+    a, av = _grad_a(dg, rng, M, K, dtype, op)
+    bv = _np(torch.from_numpy(bv).to(TYPES[dtype]))
+    want = dg.mx_grad(av, b, dtype=torch.float32)
+    _check(want, _np(a) @ bv, np.abs(_np(a)) @ np.abs(bv), K, "f32")
+    rows, cols = (M, K) if op == "N" else (K, M)
+    stored = (a if op == "N" else a.t()).contiguous()
+    whole = torch.full((rows + 2, cols), float("nan"), dtype=a.dtype, device="cuda")
+    for lo in (0, 1, 2):
+        if (lo * cols * 2) % 16 and cols % 8 == 0:
+            continue
+        whole.fill_(float("nan"))
+        part = whole[lo:lo + rows]
+        part.copy_(stored)
+        got = dg.mx_grad(part if op == "N" else part.t(), b, dtype=torch.float32)
+        check_device(dg)
+        assert torch.equal(got, want)
+
+
+def test_a_layer_of_odd_width_runs_backward(dg):
+    """y of mx_linear, and a gradient of its layout, through autograd."""
+    gen = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn((70, 130), generator=gen, device="cuda").bfloat16()
+    w = dg.mx_quantize(torch.randn((77, 130), generator=gen, device="cuda"))
+    y = dg.mx_linear(x, w)
+    assert y.is_contiguous() and y.shape == (70, 77)
+    y.requires_grad_()
+    (y.float() ** 2).sum().backward()
+    dy, kept = y.grad, dg.mx_quantize(x, "mxint8")
+    wide = torch.zeros((70, 80), dtype=dy.dtype, device="cuda")
+    wide[:, :77] = dy
+    assert torch.equal(dg.mx_grad(dy, w), dg.mx_grad(wide[:, :77], w))
+    assert torch.equal(dg.mx_grad(dy.t(), kept, dtype=torch.float32),
+                       dg.mx_grad(wide[:, :77].t(), kept, dtype=torch.float32))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_grad_every_scale(dg, fmt):
     """Exact in BF16 over the whole range of scales whose values BF16 and

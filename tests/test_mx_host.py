@@ -136,6 +136,19 @@ def test_valid_calls_without_a_gpu_fail_loudly():
     assert dg.gemm_mx4("f32", 4, 8, 0, 1.0, 0, 0, 0, 0, 0, 0, 0.0, Y, 8) == st
 
 
+@pytest.mark.parametrize("op,M,K,lda,A,misaligned", [
+    ("N", 4, 63, 63, X, False), ("N", 4, 63, 63, X + 2, False), ("N", 4, 63, 63, X + 1, True),
+    ("T", 4, 64, 4, X + 2, False), ("T", 5, 64, 5, X, False), ("N", 4, 63, 65, X, True),
+    ("N", 4, 64, 64, X + 2, True), ("T", 8, 64, 8, X + 2, True), ("T", 4, 64, 5, X, True),
+])
+def test_grad_takes_packed_operands_of_any_width(op, M, K, lda, A, misaligned):
+    import torch
+    if not misaligned and torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    st = dg.gemm_mx_grad("mxint8", "bf16", op, "bf16", M, 8, K, 1.0, A, lda, Q, 16, S, 0.0, Y, 8)
+    assert st == (MISALIGNED if misaligned else dg.GEMM_ERR_UNSUPPORTED_DEVICE)
+
+
 def test_wrappers_refuse_wrong_tensors():
     import torch
     x = torch.zeros(4, 64)
