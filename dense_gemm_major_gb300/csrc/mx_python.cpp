@@ -41,6 +41,17 @@ struct Ref {
   explicit operator bool() const { return p != nullptr; }
 };
 
+// A call of the library, which may wait (for a workspace, or for room in a full
+// stream): other Python threads run meanwhile, the callbacks among them that the
+// stream may be waiting for.
+template <typename F>
+gemm_status_t without_gil(F call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const gemm_status_t st = call();
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 bool value_error(const char* text) {
   PyErr_SetString(PyExc_ValueError, text);
   return false;
@@ -117,12 +128,12 @@ struct Matrix {
   }
 };
 
-// An MXTensor's arrays.
+// An MXTensor's arrays, kept alive.
 struct Quantized {
   int rows, cols, ld;
   gemm_mx_format_t fmt;
   char *codes, *scales;
-  Ref device;
+  Ref device, owner, owner2;
   bool read(PyObject* q) {
     if (!PyObject_TypeCheck(q, (PyTypeObject*)g_tensor_type))
       return value_error("the operand must be an MXTensor");
@@ -140,6 +151,7 @@ struct Quantized {
       codes = (char*)p;
       scales = codes + (long long)rows * ld;
       device.set(PyObject_GetAttr(buffer.p, n_device));
+      owner.set(buffer.release());
       return (bool)device;
     }
     Ref c(PyObject_GetAttr(q, n_codes)), s(PyObject_GetAttr(q, n_scales));
@@ -152,6 +164,8 @@ struct Quantized {
     if (!address(s.p, &p)) return false;
     scales = (char*)p;
     device.set(PyObject_GetAttr(c.p, n_device));
+    owner.set(c.release());
+    owner2.set(s.release());
     return (bool)device;
   }
 };
@@ -274,8 +288,10 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Ref buffer(empty(size.p, g_uint8, x.device.p));
   void* p;
   if (!buffer || !address(buffer.p, &p)) return nullptr;
-  const gemm_status_t st = gemm_mx_quantize(fmt, x.code, op, x.rows, x.cols, x.ptr, ldx, p, ldq,
-                                            (char*)p + codes, stream);
+  const gemm_status_t st = without_gil([&] {
+    return gemm_mx_quantize(fmt, x.code, op, x.rows, x.cols, x.ptr, ldx, p, ldq, (char*)p + codes,
+                            stream);
+  });
   if (st != GEMM_OK) return failed(st, "gemm_mx_quantize");
   return Py_BuildValue("Niii", buffer.release(), x.rows, x.cols, ldq);
 }
@@ -292,8 +308,10 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!dtype || !dtype_code(dtype.p, &code) || !stream_of(a[3], q.device.p, &stream) ||
       !y.make(a[2], q.rows, q.cols, dtype.p, q.device.p, 0.0))
     return nullptr;
-  const gemm_status_t st = gemm_mx_dequantize(q.fmt, code, q.rows, q.cols, q.codes, q.ld, q.scales,
-                                              y.ptr, y.ld, stream);
+  const gemm_status_t st = without_gil([&] {
+    return gemm_mx_dequantize(q.fmt, code, q.rows, q.cols, q.codes, q.ld, q.scales, y.ptr, y.ld,
+                              stream);
+  });
   if (st != GEMM_OK) return failed(st, "gemm_mx_dequantize");
   return y.tensor.release();
 }
@@ -315,9 +333,10 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !stream_of(a[6], x.device.p, &stream) ||
       !c.make(a[2], x.rows, w.rows, dtype.p, x.device.p, beta))
     return nullptr;
-  const gemm_status_t st =
-      gemm_mx4(code, x.rows, w.rows, x.cols, (float)alpha, x.codes, x.ld, x.scales, w.codes, w.ld,
-               w.scales, (float)beta, c.ptr, c.ld, stream);
+  const gemm_status_t st = without_gil([&] {
+    return gemm_mx4(code, x.rows, w.rows, x.cols, (float)alpha, x.codes, x.ld, x.scales, w.codes,
+                    w.ld, w.scales, (float)beta, c.ptr, c.ld, stream);
+  });
   if (st != GEMM_OK) return failed(st, "gemm_mx4");
   return c.tensor.release();
 }
@@ -336,8 +355,10 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !stream_of(a[3], x.device.p, &stream) ||
       !y.make(a[2], x.rows, w.rows, x.dtype.p, x.device.p, 0.0))
     return nullptr;
-  const gemm_status_t st = gemm_mx4_linear(x.code, x.rows, w.rows, x.cols, x.ptr, ldx, w.codes,
-                                           w.ld, w.scales, y.ptr, y.ld, stream);
+  const gemm_status_t st = without_gil([&] {
+    return gemm_mx4_linear(x.code, x.rows, w.rows, x.cols, x.ptr, ldx, w.codes, w.ld, w.scales,
+                           y.ptr, y.ld, stream);
+  });
   if (st != GEMM_OK) return failed(st, "gemm_mx4_linear");
   return y.tensor.release();
 }
@@ -377,9 +398,10 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!stream_of(a[6], x.device.p, &stream) ||
       !c.make(a[2], x.rows, b.cols, dtype.p, x.device.p, beta))
     return nullptr;
-  const gemm_status_t st =
-      gemm_mx_grad(b.fmt, x.code, op, code, x.rows, b.cols, x.cols, (float)alpha, x.ptr, lda,
-                   b.codes, b.ld, b.scales, (float)beta, c.ptr, c.ld, stream);
+  const gemm_status_t st = without_gil([&] {
+    return gemm_mx_grad(b.fmt, x.code, op, code, x.rows, b.cols, x.cols, (float)alpha, x.ptr, lda,
+                        b.codes, b.ld, b.scales, (float)beta, c.ptr, c.ld, stream);
+  });
   if (st != GEMM_OK) return failed(st, "gemm_mx_grad");
   return c.tensor.release();
 }

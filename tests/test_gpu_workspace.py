@@ -130,3 +130,35 @@ def test_two_threads_call_on_one_stream(dg, per_thread):
         assert status[t] == [dg.GEMM_OK] * calls
         for a, b in zip(ys, want):
             assert torch.equal(a, b)
+
+
+def test_two_threads_call_the_wrappers_on_one_stream(dg):
+    """The same through mx_linear and mx_grad, which let other threads run."""
+    gen = torch.Generator("cuda").manual_seed(7)
+    w = dg.mx_quantize(torch.randn((264, 512), generator=gen, device="cuda"))
+    s = torch.cuda.Stream()
+    jobs = []
+    for t in range(2):
+        xs = [torch.randn((70 + 31 * i * (1 + t), 512), generator=gen, device="cuda").bfloat16()
+              for i in range(30)]
+        jobs.append([(x, dg.mx_linear(x, w)) for x in xs])
+        jobs[t] = [(x, y, dg.mx_grad(y, w), torch.empty_like(y), torch.empty_like(x))
+                   for x, y in jobs[t]]
+    torch.cuda.synchronize()
+    go = threading.Barrier(2)
+
+    def work(t):
+        go.wait()
+        for x, y, _, out, dx in jobs[t]:
+            dg.mx_linear(x, w, out=out, stream=s.cuda_stream)
+            dg.mx_grad(y, w, out=dx, stream=s.cuda_stream)
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    check_device(dg)
+    for job in jobs:
+        for _, y, want, out, dx in job:
+            assert torch.equal(out, y) and torch.equal(dx, want)
