@@ -453,6 +453,12 @@ def matmul(A, B, out=None, stream=None, alpha=1.0, beta=0.0):
 # These functions are thin: the extension _mxcall (csrc/mx_python.cpp) reads the
 # tensors, allocates the result and calls the C ABI.  A layer of a few tokens
 # takes a few microseconds on the GPU, less than the same steps in Python.
+#
+# ``stream`` is a cudaStream_t value (default: torch's current stream).  A result
+# allocated here belongs to the stream that it is written on, and may be used
+# on torch's current one as well once that waits for the work.  Operands that
+# are freed while work on another stream than their own may still read them
+# must be recorded there first (Tensor.record_stream, MXTensor.record_stream).
 
 _mx = None
 
@@ -467,6 +473,21 @@ def _load_mx():
         ext.setup(torch, MXTensor, GemmError)
         _mx = ext
     return _mx
+
+
+def _on_stream(stream, call):
+    """call(), whose result is newly allocated, with ``stream`` as torch's
+    current stream: memory of the caller's stream might still be in use there,
+    by work queued before it was freed."""
+    import torch
+    current = torch.cuda.current_stream()
+    if stream == current.cuda_stream:
+        return call()
+    # (1 is cudaStreamLegacy, another name of the default stream.)
+    with torch.cuda.stream(torch.cuda.ExternalStream(0 if stream == 1 else stream)):
+        result = call()
+    result.record_stream(current)
+    return result
 
 
 class MXTensor:
@@ -500,11 +521,18 @@ class MXTensor:
     def device(self):
         return (self._codes if self._buffer is None else self._buffer).device
 
+    def record_stream(self, stream):
+        """Tensor.record_stream of the codes and scales."""
+        for t in (self._codes, self._scales) if self._buffer is None else (self._buffer,):
+            t.record_stream(stream)
+
 
 def mx_quantize(X, fmt="mxfp4", stream=None):
     """X (rows x cols; float32, float16 or bfloat16; row-major or a
     transposed view, read in place) in format ``fmt``: blocks of 32 along
     the columns.  Returns an MXTensor."""
+    if stream is not None:
+        return _on_stream(stream, lambda: mx_quantize(X, fmt))
     q = MXTensor.__new__(MXTensor)
     q._codes = q._scales = None
     q._buffer, q.rows, q.cols, q._ld = (_mx or _load_mx()).quantize(X, fmt, stream)
@@ -515,6 +543,8 @@ def mx_quantize(X, fmt="mxfp4", stream=None):
 def mx_dequantize(q, dtype=None, out=None, stream=None):
     """The values of MXTensor ``q`` as a rows x cols tensor of ``dtype``
     (default bfloat16, or that of ``out``)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, lambda: mx_dequantize(q, dtype))
     return (_mx or _load_mx()).dequantize(q, dtype, out, stream)
 
 
@@ -522,12 +552,16 @@ def mx_matmul(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     """alpha * (A @ B.T) + beta * out for MXFP4 operands A (M x K) and B
     (N x K); the result is of ``dtype`` (default bfloat16, or that of
     ``out``)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, lambda: mx_matmul(A, B, None, dtype, alpha, beta))
     return (_mx or _load_mx()).matmul(A, B, out, dtype, alpha, beta, stream)
 
 
 def mx_linear(x, W, out=None, stream=None):
     """x @ W.T with x (M x K) quantised to MXFP4 on the way and W (N x K) an
     MXFP4 MXTensor; the result has x's dtype."""
+    if stream is not None and out is None:
+        return _on_stream(stream, lambda: mx_linear(x, W))
     return (_mx or _load_mx()).linear(x, W, out, stream)
 
 
@@ -538,4 +572,6 @@ def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     its weights.  A has rows of a multiple of 16 bytes, or is contiguous (rows
     of other widths are then copied to aligned ones first).  The result is of A's dtype or float32 (``dtype``, or that
     of ``out``)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, lambda: mx_grad(A, B, None, dtype, alpha, beta))
     return (_mx or _load_mx()).grad(A, B, out, dtype, alpha, beta, stream)

@@ -570,6 +570,39 @@ def test_other_stream_and_repeated_calls(dg):
     check_device(dg)
 
 
+def test_stream_argument_and_the_allocator(dg):
+    """Work on a side stream given as `stream` does not get memory that work of
+    the current stream still reads, and its results may be used there."""
+    gen = torch.Generator("cuda").manual_seed(9)
+    x = torch.randn((64, 4096), generator=gen, device="cuda").bfloat16()
+    w = dg.mx_quantize(torch.randn((4096, 4096), generator=gen, device="cuda"))
+    want = (dg.mx_quantize(x, "mxint8")._buffer.clone(), dg.mx_linear(x, w), dg.mx_grad(x, w),
+            dg.mx_dequantize(w), dg.mx_matmul(w, w))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        busy = [torch.ones_like(t) for t in want for _ in range(2)]
+        torch.cuda._sleep(20_000_000)          # the sums wait here for some milliseconds
+        sums = [t.sum(dtype=torch.float64) for t in busy]
+        sizes = [t.numel() for t in busy]
+        del busy                                # back to the current stream's pool
+        s = side.cuda_stream
+        q = dg.mx_quantize(x, "mxint8", stream=s)
+        got = (q, dg.mx_linear(x, w, stream=s), dg.mx_grad(x, w, stream=s),
+               dg.mx_dequantize(w, stream=s), dg.mx_matmul(w, w, stream=s))
+        torch.cuda.current_stream().wait_stream(side)
+        got = (q._buffer,) + got[1:]
+        copies = [t.clone() for t in got]
+        q.record_stream(torch.cuda.current_stream())
+        del q, got
+        assert [float(t) for t in sums] == [float(n) for n in sizes]
+        for a, b in zip(copies, want):
+            assert torch.equal(a, b)
+    for s in (0, 1):                            # the default stream by both its names
+        assert torch.equal(dg.mx_linear(x, w, stream=s), want[1])
+    check_device(dg)
+
+
 def test_graph_replay(dg):
     """A captured layer step replays on new inputs with the eager bits."""
     rng = np.random.default_rng(41)

@@ -274,14 +274,60 @@ def test_operands_must_be_on_the_current_device(current_device_0):
     q1 = _fake_quantized("cuda:1")
     x = FakeTensor((5, 64), torch.bfloat16, "cuda:1", X)
     y = FakeTensor((5, 8), torch.bfloat16, "cuda:1", Y)
-    for stream in (None, 0, 16):
-        for f in [lambda: dg.mx_quantize(x, stream=stream),
-                  lambda: dg.mx_dequantize(q1, stream=stream),
-                  lambda: dg.mx_matmul(q1, q1, stream=stream),
-                  lambda: dg.mx_linear(x, q1, out=y, stream=stream),
-                  lambda: dg.mx_grad(y, q1, stream=stream)]:
-            with pytest.raises(ValueError, match="current CUDA device"):
-                f()
+    for f in [lambda: dg.mx_quantize(x), lambda: dg.mx_dequantize(q1), lambda: dg.mx_matmul(q1, q1),
+              lambda: dg.mx_linear(x, q1), lambda: dg.mx_grad(y, q1),
+              lambda: dg.mx_dequantize(q1, out=x, stream=16),
+              lambda: dg.mx_matmul(q1, q1, out=y, stream=0),
+              lambda: dg.mx_linear(x, q1, out=y, stream=16),
+              lambda: dg.mx_grad(y, q1, out=x, stream=16)]:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f()
+
+
+@pytest.mark.parametrize("stream,current", [(16, 16), (0, 0), (1, 0), (7 << 20, 7 << 20)])
+def test_results_are_allocated_on_the_stream_that_writes_them(monkeypatch, stream, current):
+    """With stand-ins for torch's streams and allocation; the calls then fail
+    for want of a GPU."""
+    import contextlib
+    import types
+
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    ext, now, seen = dg._load_mx(), [8], []   # torch's current stream is number 8
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        try:
+            yield
+        finally:
+            now.pop()
+
+    def empty(size, dtype=None, device=None):
+        seen.append(now[-1])
+        return FakeTensor(size if isinstance(size, tuple) else (size,), dtype, device, Y)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=8))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: now[-1], _cuda_getDevice=lambda: 0)
+    names = ("float32", "float16", "bfloat16", "uint8")
+    ext.setup(types.SimpleNamespace(_C=c, empty=empty, **{n: getattr(torch, n) for n in names}),
+              dg.MXTensor, dg.GemmError)
+    try:
+        q = _fake_quantized("cuda:0")
+        x, dy = (FakeTensor((5, n), torch.bfloat16, "cuda:0", X) for n in (64, 8))
+        calls = [lambda s: dg.mx_quantize(x, stream=s), lambda s: dg.mx_dequantize(q, stream=s),
+                 lambda s: dg.mx_matmul(q, q, stream=s), lambda s: dg.mx_linear(x, q, stream=s),
+                 lambda s: dg.mx_grad(dy, q, stream=s)]
+        for s, want in [(stream, current), (8, 8), (None, 8)]:
+            for f in calls:
+                with pytest.raises(dg.GemmError):
+                    f(s)
+            assert seen == [want] * len(calls)
+            seen.clear()
+    finally:
+        ext.setup(torch, dg.MXTensor, dg.GemmError)
 
 
 # ------------------------------------------------------------ the largest sizes
@@ -317,7 +363,7 @@ def test_sizes_past_the_limit_are_refused(K):
 def test_wrappers_refuse_sizes_past_the_limit(current_device_0):
     import torch
     with pytest.raises(ValueError, match="limit"):
-        dg.mx_quantize(FakeTensor((1, 2 ** 31 - 1), torch.bfloat16, "cuda:0", X), stream=16)
+        dg.mx_quantize(FakeTensor((1, 2 ** 31 - 1), torch.bfloat16, "cuda:0", X))
     for shape, cols in [((1, 2 ** 31 - 16), 2 ** 31 - 1), ((2 ** 31 - 1, 16), 16)]:
         with pytest.raises(ValueError, match="limit"):
             dg.MXTensor(FakeTensor(shape, torch.uint8, "cuda:0", Q),
