@@ -1,5 +1,5 @@
 """In-tree build of the CUDA library (libdense_gemm.so) for sm_103a, and of
-the CPython extension (_mxcall.so) that calls its microscaled entry points.
+the CPython extension (_mxcall) that calls its microscaled entry points.
 
 Each translation unit under csrc/ is compiled by its own nvcc process, in
 parallel, then linked into one shared library next to this file.  A unit is
@@ -19,9 +19,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libdense_gemm.so")
-# The CPython extension around the microscaled entry points.
+# The CPython extension around the microscaled entry points (needs Python's
+# headers), named for the interpreter that it is built for: another one neither
+# loads it nor takes it for up to date.
 EXT_SOURCE = os.path.join(CSRC, "mx_python.cpp")
-EXT = os.path.join(PKG, "_mxcall.so")
+EXT = os.path.join(PKG, "_mxcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -90,7 +92,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
 
 
 def build_extension(verbose: bool = False) -> None:
-    """_mxcall.so, linked to libdense_gemm.so beside it."""
+    """_mxcall, linked to libdense_gemm.so beside it."""
     newest = max([os.path.getmtime(EXT_SOURCE)] + [os.path.getmtime(h) for h in _headers()])
     if os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
         return

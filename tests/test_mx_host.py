@@ -149,6 +149,14 @@ def test_grad_takes_packed_operands_of_any_width(op, M, K, lda, A, misaligned):
     assert st == (MISALIGNED if misaligned else dg.GEMM_ERR_UNSUPPORTED_DEVICE)
 
 
+def test_extension_is_named_for_its_interpreter():
+    import sysconfig
+
+    from dense_gemm_major_gb300 import _build
+    assert _build.EXT.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert dg._load_mx().__file__ == _build.EXT
+
+
 def test_wrappers_refuse_wrong_tensors():
     import torch
     x = torch.zeros(4, 64)
