@@ -459,6 +459,10 @@ def matmul(A, B, out=None, stream=None, alpha=1.0, beta=0.0):
 # on torch's current one as well once that waits for the work.  Operands that
 # are freed while work on another stream than their own may still read them
 # must be recorded there first (Tensor.record_stream, MXTensor.record_stream).
+#
+# Like matmul(), none of them takes part in autograd: results never require a
+# gradient.  MXLinear in examples/mx_layer.py is a torch.autograd.Function of a
+# layer's three products.
 
 _mx = None
 
@@ -558,8 +562,8 @@ def mx_matmul(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
 
 
 def mx_linear(x, W, out=None, stream=None):
-    """x @ W.T with x (M x K) quantised to MXFP4 on the way and W (N x K) an
-    MXFP4 MXTensor; the result has x's dtype."""
+    """x @ W.T with x (M x K, row-major) quantised to MXFP4 on the way and W
+    (N x K) an MXFP4 MXTensor; the result has x's dtype and no gradient."""
     if stream is not None and out is None:
         return _on_stream(stream, lambda: mx_linear(x, W))
     return (_mx or _load_mx()).linear(x, W, out, stream)
