@@ -110,11 +110,17 @@ struct Mx4FewParams {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-// The pair kernel against this one at 64 rows, N x K: 2048 x 2048 5.6 / 6.0 us,
-// 4096 x 4096 7.1 / 7.7, 512 x 512 4.4 / 4.2, 4096 x 14336 11.1 / 9.5, 8192 x
-// 8192 11.3 / 8.1, 1024 x 8192 7.5 / 5.6; at 32 rows this one is quicker in all.
-// (With a tile of 128 rows the pairs were: 128 x 2048 x 2048 7.7 / 9.7 us.)
+// The pair kernel against this one at 64 rows, N x K, us: 512 x 512 4.6 / 4.4, 1024
+// x 1024 5.0 / 4.1, 2048 x 8192 9.2 / 7.4, 8192 x 8192 11.7 / 8.3, 4096 x 14336
+// 11.3 / 9.8, 65536 x 2048 14.9 / 14.2, but 2048 x 2048 5.8 / 6.4, 4096 x 4096 7.3 /
+// 7.8, 8192 x 1024 5.2 / 5.9, 16384 x 4096 8.2 / 8.5: short rows leave the cluster
+// little to share, and tiles of 256 columns few rounds.  At 56 rows those are 5.8 / 5.9, 7.3 / 7.2, 5.2 / 5.7 and 9.0 /
+// 8.3; at 32 this one is quicker in all.  (With a tile of 128 rows the pairs
+// were: 128 x 2048 x 2048 7.7 / 9.7 us.)
 constexpr int kMx4FewRows = 64, kMx4FewBK = 256;
+inline int mx4_few_rows(int N, int K) {
+  return N >= 2048 && N <= 16384 && K <= 4096 ? kMx4FewRows - 8 : kMx4FewRows;
+}
 // Quantising A inside the kernel saves a launch (1.2 us of the GPU and 2.7 us
 // of a calling thread), but each CTA then quantises the rows' part that it
 // multiplies: M times its share of K values, done anew for every 128 columns.

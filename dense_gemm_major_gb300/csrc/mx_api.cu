@@ -190,7 +190,7 @@ bool few_raw(int M, int N, int K, int max_pairs) {
          (long long)M * stages * dgemm::kMx4FewBK <= dgemm::kMx4FewRawValues;
 }
 
-// The product of checked operands, 0 < M <= kMx4FewRows, N, K > 0; A is X,
+// The product of checked operands, 0 < M <= mx4_few_rows(), N, K > 0; A is X,
 // unquantised, or a.
 gemm_status_t run_few(int dtype, int M, int N, int K, float alpha, const void* X, long long ldx,
                       const void* a, long long lda, const void* sa, const void* b, long long ldb,
@@ -221,7 +221,7 @@ gemm_status_t run_mx4(int dtype, int M, int N, int K, float alpha, const void* a
                       const void* sa, const void* b, long long ldb, const void* sb, float beta,
                       void* C, int ldc, unsigned* fault, int max_pairs,
                       dgemm::StreamWorkspaces& workspaces, cudaStream_t stream) {
-  if (M <= dgemm::kMx4FewRows)
+  if (M <= dgemm::mx4_few_rows(N, K))
     return run_few(dtype, M, N, K, alpha, nullptr, 0, a, lda, sa, b, ldb, sb, beta, C, ldc, fault,
                    max_pairs, stream);
   alignas(64) CUtensorMap tmA, tmB, tmSA, tmSB;

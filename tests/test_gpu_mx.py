@@ -329,6 +329,23 @@ def test_linear(dg, dtype, shape):
     assert (out[:, N:] == -1).all()
 
 
+# Wide products of short rows: the last size of the few-row kernel and the
+# first of the pair kernel, and long rows beside them.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(56, 2048, 1000), (57, 2048, 1000), (64, 2050, 4096),
+                                   (64, 2047, 4096), (64, 2050, 4097), (65, 2047, 300)])
+def test_products_around_the_few_row_limit(dg, dtype, shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + N + K)
+    x = _rand(rng, M, K, dtype, spread=2.0)
+    w, wv = _operand(dg, _np(_rand(rng, N, K, spread=1.0)), "mxfp4")
+    xv = ref.values(*ref.quantize(_np(x), "mxfp4"), "mxfp4")
+    want, total = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    _check(dg.mx_linear(_dev(x), w), want, total, K, dtype)
+    _check(dg.mx_matmul(dg.mx_quantize(_dev(x)), w, dtype=TYPES[dtype]), want, total, K, dtype)
+    check_device(dg)
+
+
 # Few rows: the last size that the product's kernel quantises itself and the
 # first that is quantised before it, by rows and by length.
 @pytest.mark.parametrize("dtype", list(TYPES))
