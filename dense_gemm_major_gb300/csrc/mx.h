@@ -124,11 +124,18 @@ inline int mx4_few_rows(int N, int K) {
 // Quantising A inside the kernel saves a launch (1.2 us of the GPU and 2.7 us
 // of a calling thread), but each CTA then quantises the rows' part that it
 // multiplies: M times its share of K values, done anew for every 128 columns.
-// Inside / before, us: 16384 values 1024 x 8192 (N x K), 16 rows 4.8 / 5.6;
-// 24576 values 4096 x 4096, 48 rows 8.8 / 8.7, 1024 x 8192, 24 rows 6.3 / 6.1,
-// and 8192 x 8192, 12 rows 8.0 / 8.2; 33792 values 1024 x 8192, 33 rows 7.3 /
-// 6.4; 49152 values 8192 x 8192, 24 rows 11.1 / 8.8.
+// Where the CTAs run in several waves that counts for each.  Inside / before, us,
+// up to 16 rows: 16384 values 1024 x 8192 (N x K), 16 rows 4.9 / 5.8, 4096 x 4096,
+// 16 rows (8192) 5.7 / 6.7, 16384 x 4096, 8 rows 7.4 / 8.4; 28672 values 4096 x
+// 14336, 16 rows 8.6 / 8.6; 32768 values 16384 x 4096, 16 rows 8.4 / 8.1, 65536 x
+// 2048, 8 rows (two waves) 12.4 / 11.7.  With more rows a stage's blocks are
+// three passes of its warps' lanes or more, which pays for one or two stages:
+// 4096 x 4096 (two), 17 / 24 / 33 / 48 rows 7.0 / 6.9 / 7.8 / 9.0 and 7.0 / 7.4 /
+// 8.0 / 8.8, 2048 x 2048 (one), 24 / 40 rows 5.4 / 6.5 and 6.0 / 6.8; but 1024 x
+// 8192 (four), 17 / 24 rows 7.2 / 6.5 and 6.2 / 6.3, 2048 x 8192 8.0 / 7.6 and
+// 7.0 / 7.1.
 constexpr int kMx4FewRawRows = 48, kMx4FewRawValues = 24 * 1024;
+constexpr int kMx4FewRawShort = 16, kMx4FewRawStages = 2;
 // Rows of A that the kernel computes for M of them.
 inline int mx4_few_tile(int M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
 // tmA: A's codes as bytes, boxes of 128 bytes x mx4_few_tile(M) rows; tmB:

@@ -185,9 +185,12 @@ int few_split(int N, int K, int max_pairs) {
 
 // Whether the few-row kernel quantises A itself: see kMx4FewRawRows.
 bool few_raw(int M, int N, int K, int max_pairs) {
-  const int stages = ceil_div(ceil_div(K, dgemm::kMx4FewBK), few_split(N, K, max_pairs));
+  const int split = few_split(N, K, max_pairs);
+  const long long waves = ((long long)ceil_div(N, 128) * split + 4 * max_pairs - 1) / (4 * max_pairs);
+  const long long stages = ceil_div(ceil_div(K, dgemm::kMx4FewBK), split) * waves;
   return M <= dgemm::kMx4FewRawRows &&
-         (long long)M * stages * dgemm::kMx4FewBK <= dgemm::kMx4FewRawValues;
+         M * stages * dgemm::kMx4FewBK <= dgemm::kMx4FewRawValues &&
+         (M <= dgemm::kMx4FewRawShort || stages <= dgemm::kMx4FewRawStages);
 }
 
 // The product of checked operands, 0 < M <= mx4_few_rows(), N, K > 0; A is X,
