@@ -11,7 +11,7 @@
 // through distributed shared memory in rank order, so results are
 // reproducible and there is no workspace and no second launch.
 //
-// Measured at N = K = 4096, back to back: 1 row 4.5 us, 8 4.9, 33 7.6 (a cold
+// Measured at N = K = 4096, back to back: 1 row 4.9 us, 8 5.1, 33 7.8 (a cold
 // read of B's 8.9 MB alone takes 1.3 us; launch, tensor memory, barriers and
 // the two cluster barriers are the most of the rest).
 //

@@ -33,8 +33,8 @@
 // 8192^3, 4096 x 4096 x 16384 119 / 102 / 93 / 89 (in one piece 87).  16-bit
 // results round far coarser than either.
 //
-// Measured: 8192^3 156 us (7.0 PFLOP/s), 4096^3 26.  16384^3 1095 (8.0
-// PFLOP/s).  At 8192^3 it takes 114 us without its MMAs, 137 without its stores
+// Measured: 8192^3 156 us (7.0 PFLOP/s), 4096^3 26.  16384^3 1095 to 1133 (8.0
+// to 7.8 PFLOP/s).  At 8192^3 it takes 114 us without its MMAs, 137 without its stores
 // and 139 with all of them to one row of C: what stores cost is C's write
 // traffic beside the loads, not instructions.  Streaming and write-through
 // stores change nothing, whole 128-byte lines per warp 1 to 3 %, stores paced
