@@ -15,7 +15,8 @@
  *   codes   R rows with a pitch of ldq bytes (a multiple of 16, at least
  *           gemm_mx_code_ld(fmt, K)).  MXFP4: columns 2j and 2j + 1 in the
  *           low and high half of byte j (the high half of the last byte of
- *           an odd row is 0).  MXINT8: column j in byte j.
+ *           an odd row is 0).  MXINT8: column j in byte j.  Nothing past a
+ *           row's last code is read, so the last row may end there.
  *   scales  gemm_mx_scale_bytes(R, K) bytes: tiles of 128 rows x 4 blocks of
  *           512 bytes each.  The scale of row r, block b is byte
  *             (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4
@@ -54,7 +55,7 @@ extern "C" {
 
 typedef enum gemm_mx_format_t { GEMM_MXFP4 = 0, GEMM_MXINT8 = 1 } gemm_mx_format_t;
 
-#define GEMM_MX_MAX_SIZE (2147483647 - 1023)
+#define GEMM_MX_MAX_SIZE (2147483647 - 1023)   /* 2^31 - 1024 */
 
 /* Smallest row pitch of the codes in bytes, a multiple of 16; -1 for a bad
  * format, K < 0 or K > GEMM_MX_MAX_SIZE. */

@@ -593,7 +593,7 @@ def test_stream_argument_and_the_allocator(dg):
     gen = torch.Generator("cuda").manual_seed(9)
     x = torch.randn((64, 4096), generator=gen, device="cuda").bfloat16()
     w = dg.mx_quantize(torch.randn((4096, 4096), generator=gen, device="cuda"))
-    want = (dg.mx_quantize(x, "mxint8")._buffer.clone(), dg.mx_linear(x, w), dg.mx_grad(x, w),
+    want = (dg.mx_quantize(x, "mxint8").codes.clone(), dg.mx_linear(x, w), dg.mx_grad(x, w),
             dg.mx_dequantize(w), dg.mx_matmul(w, w))
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -608,7 +608,7 @@ def test_stream_argument_and_the_allocator(dg):
         got = (q, dg.mx_linear(x, w, stream=s), dg.mx_grad(x, w, stream=s),
                dg.mx_dequantize(w, stream=s), dg.mx_matmul(w, w, stream=s))
         torch.cuda.current_stream().wait_stream(side)
-        got = (q._buffer,) + got[1:]
+        got = (q.codes,) + got[1:]
         copies = [t.clone() for t in got]
         q.record_stream(torch.cuda.current_stream())
         del q, got
