@@ -498,10 +498,10 @@ class MXTensor:
     """A quantised rows x cols array on the GPU: ``codes`` (uint8, rows x
     pitch) and ``scales`` (uint8) in the layout that include/dense_gemm_mx.h
     describes; ``fmt`` is "mxfp4" or "mxint8"."""
-    __slots__ = ("_codes", "_scales", "_buffer", "rows", "cols", "fmt", "_ld")
+    __slots__ = ("_codes", "_scales", "_buffer", "_device", "rows", "cols", "fmt", "_ld")
 
     def __init__(self, codes, scales, cols, fmt="mxfp4"):
-        self.rows, self._ld = (_mx or _load_mx()).describe(codes, scales, cols, fmt)
+        self.rows, self._ld, self._device = (_mx or _load_mx()).describe(codes, scales, cols, fmt)
         self._codes, self._scales, self._buffer = codes, scales, None
         self.cols, self.fmt = cols, fmt
 
@@ -539,7 +539,7 @@ def mx_quantize(X, fmt="mxfp4", stream=None):
         return _on_stream(stream, lambda: mx_quantize(X, fmt))
     q = MXTensor.__new__(MXTensor)
     q._codes = q._scales = None
-    q._buffer, q.rows, q.cols, q._ld = (_mx or _load_mx()).quantize(X, fmt, stream)
+    q._buffer, q.rows, q.cols, q._ld, q._device = (_mx or _load_mx()).quantize(X, fmt, stream)
     q.fmt = fmt
     return q
 

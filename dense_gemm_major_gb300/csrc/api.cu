@@ -19,6 +19,7 @@
 
 #include "dense_gemm.h"
 #include "launch.h"
+#include "mx.h"
 #include "ptx.cuh"
 #include "workspace.h"
 
@@ -932,13 +933,17 @@ gemm_status_t run(int dtype, int op_a, int op_b, int M, int N, int K, float alph
 
 namespace dgemm {
 
-// For other translation units of the library: the current device's fault
-// word (nullptr if the device is unsupported) and the bound of every wait.
-unsigned* current_fault_word() {
-  DeviceInfo* dev = nullptr;
-  return current_device(&dev) == GEMM_OK ? dev->fault : nullptr;
-}
+// For other translation units of the library: the bound of every wait, and
+// what the current device offers.
 unsigned long long wait_bound_ns() { return wait_timeout_ns(); }
+gemm_status_t current_device_pairs(unsigned** fault, int* pairs) {
+  DeviceInfo* dev = nullptr;
+  const gemm_status_t st = current_device(&dev);
+  if (st != GEMM_OK) return st;
+  *fault = dev->fault;
+  *pairs = dev->pair_clusters;
+  return *fault != nullptr && *pairs > 0 ? GEMM_OK : GEMM_ERR_UNSUPPORTED_DEVICE;
+}
 
 gemm_status_t run_f32_no_copy(int M, int N, int K, const float* A, int lda, const float* B,
                               int ldb, float* C, int ldc, cudaStream_t stream,

@@ -473,9 +473,7 @@ inline int splitk_slices(int tiles, int slots, int nk) {
 
 // ---------------------------------------------------------------- shared state
 
-// The current device's fault word (nullptr if unsupported) and the bound of
-// every device-side wait, from the C-ABI translation unit.
-unsigned* current_fault_word();
+// The bound of every device-side wait, from the C-ABI translation unit.
 unsigned long long wait_bound_ns();
 
 // Caller-owned device scratch for an FP32 call that must not allocate:

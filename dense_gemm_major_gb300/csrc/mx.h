@@ -37,6 +37,11 @@ cudaError_t mx_allow_smem(void (*kernel)(Params...), int bytes, std::atomic<uint
   return e;
 }
 
+// The current device's fault word, and the CTA pairs that it can hold at once
+// with one CTA per SM (fewer than half of its SMs: a cluster's CTAs share a
+// GPC; a pair too many would run after all others).  In api.cu.
+gemm_status_t current_device_pairs(unsigned** fault, int* pairs);
+
 // Quantisation; the arguments of gemm_mx_quantize, checked.
 cudaError_t launch_mx_quantize(int fmt, int dtype, int op, int R, int K, const void* X,
                                long long ldx, void* codes, long long ldq, void* scales,

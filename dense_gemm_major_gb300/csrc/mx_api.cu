@@ -13,16 +13,6 @@
 
 namespace {
 
-// The current device's fault word, and the CTA pairs that it can hold at
-// once with one CTA per SM (fewer than half of its SMs: a cluster's CTAs
-// share a GPC; a pair too many would run after all others).
-gemm_status_t device(unsigned** fault, int* pairs) {
-  *fault = dgemm::current_fault_word();
-  if (*fault == nullptr) return GEMM_ERR_UNSUPPORTED_DEVICE;
-  *pairs = gemm_pair_clusters();
-  return *pairs > 0 ? GEMM_OK : GEMM_ERR_UNSUPPORTED_DEVICE;
-}
-
 // cuTensorMapEncodeTiled, fetched from the driver once.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -289,7 +279,7 @@ gemm_status_t gemm_mx_quantize(gemm_mx_format_t fmt, int dtype, gemm_op_t op, in
     return GEMM_ERR_INVALID_ARG;
   unsigned* fault;
   int max_pairs;
-  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
+  if ((st = dgemm::current_device_pairs(&fault, &max_pairs)) != GEMM_OK) return st;
   return status_of(
       dgemm::launch_mx_quantize(fmt, dtype, op, R, K, X, ldx, codes, ldq, scales, stream));
 }
@@ -310,7 +300,7 @@ gemm_status_t gemm_mx_dequantize(gemm_mx_format_t fmt, int dtype, int R, int K,
     return GEMM_ERR_INVALID_ARG;
   unsigned* fault;
   int max_pairs;
-  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
+  if ((st = dgemm::current_device_pairs(&fault, &max_pairs)) != GEMM_OK) return st;
   return status_of(
       dgemm::launch_mx_dequantize(fmt, dtype, R, K, codes, ldq, scales, Y, ldy, stream));
 }
@@ -337,7 +327,7 @@ gemm_status_t gemm_mx4(int dtype, int M, int N, int K, float alpha, const void* 
   }
   unsigned* fault;
   int max_pairs;
-  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
+  if ((st = dgemm::current_device_pairs(&fault, &max_pairs)) != GEMM_OK) return st;
   if (empty) return scale_only(dtype, M, N, beta, C, ldc, stream);
   dgemm::StreamWorkspaces workspaces(stream);
   return run_mx4(dtype, M, N, K, alpha, a_codes, lda, a_scales, b_codes, ldb, b_scales, beta, C,
@@ -365,7 +355,7 @@ gemm_status_t gemm_mx4_linear(int dtype, int M, int N, int K, const void* X, int
   }
   unsigned* fault;
   int max_pairs;
-  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
+  if ((st = dgemm::current_device_pairs(&fault, &max_pairs)) != GEMM_OK) return st;
   if (K == 0) return scale_only(dtype, M, N, 0.f, Y, ldy, stream);
   if (few_raw(M, N, K, max_pairs))
     return run_few(dtype, M, N, K, 1.f, X, ldx, nullptr, 0, nullptr, w_codes, ldw, w_scales, 0.f,
@@ -412,7 +402,7 @@ gemm_status_t gemm_mx_grad(gemm_mx_format_t fmt, int dtype, gemm_op_t op_a, int 
   }
   unsigned* fault;
   int max_pairs;
-  if ((st = device(&fault, &max_pairs)) != GEMM_OK) return st;
+  if ((st = dgemm::current_device_pairs(&fault, &max_pairs)) != GEMM_OK) return st;
   if (empty) return scale_only(dtype_c, M, N, beta, C, ldc, stream);
   dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
   const void* rows = A;

@@ -20,7 +20,8 @@ PyObject *g_empty, *g_raw_stream, *g_current_device, *g_error, *g_tensor_type;  
 PyObject *g_dtype[3], *g_uint8;                               // float32, float16, bfloat16
 PyObject *g_empty_names;                                      // ("dtype", "device")
 PyObject *n_is_cuda, *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_device, *n_index, *n_codes,
-    *n_scales, *n_buffer, *n_rows, *n_cols, *n_fmt, *n_ld, *n_mxfp4, *n_numel, *n_is_contiguous;
+    *n_scales, *n_buffer, *n_rows, *n_cols, *n_fmt, *n_ld, *n_mxfp4, *n_numel, *n_is_contiguous,
+    *n_mx_device;
 
 // An owned reference.
 struct Ref {
@@ -128,7 +129,8 @@ struct Matrix {
   }
 };
 
-// An MXTensor's arrays, kept alive.
+// An MXTensor's arrays, kept alive.  (Its _device is that of the arrays, None
+// where they are not on a GPU.)
 struct Quantized {
   int rows, cols, ld;
   gemm_mx_format_t fmt;
@@ -137,6 +139,9 @@ struct Quantized {
   bool read(PyObject* q) {
     if (!PyObject_TypeCheck(q, (PyTypeObject*)g_tensor_type))
       return value_error("the operand must be an MXTensor");
+    device.set(PyObject_GetAttr(q, n_mx_device));
+    if (!device) return false;
+    if (device.p == Py_None) return value_error("operands must be CUDA tensors");
     if (!attr_int(q, n_rows, &rows) || !attr_int(q, n_cols, &cols) || !attr_int(q, n_ld, &ld))
       return false;
     Ref f(PyObject_GetAttr(q, n_fmt));
@@ -150,23 +155,18 @@ struct Quantized {
       if (!address(buffer.p, &p)) return false;
       codes = (char*)p;
       scales = codes + (long long)rows * ld;
-      device.set(PyObject_GetAttr(buffer.p, n_device));
       owner.set(buffer.release());
-      return (bool)device;
+      return true;
     }
     Ref c(PyObject_GetAttr(q, n_codes)), s(PyObject_GetAttr(q, n_scales));
     if (!c || !s) return false;
-    Ref cuda(PyObject_GetAttr(c.p, n_is_cuda));
-    if (!cuda) return false;
-    if (cuda.p != Py_True) return value_error("operands must be CUDA tensors");
     if (!address(c.p, &p)) return false;
     codes = (char*)p;
     if (!address(s.p, &p)) return false;
     scales = (char*)p;
-    device.set(PyObject_GetAttr(c.p, n_device));
     owner.set(c.release());
     owner2.set(s.release());
-    return (bool)device;
+    return true;
   }
 };
 
@@ -258,7 +258,7 @@ bool arity(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
-// quantize(X, fmt, stream) -> (buffer, rows, cols, pitch of the codes)
+// quantize(X, fmt, stream) -> (buffer, rows, cols, pitch of the codes, device)
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 3)) return nullptr;
   if (!PyUnicode_Check(a[1])) return value_error("fmt must be 'mxfp4' or 'mxint8'"), nullptr;
@@ -293,7 +293,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             stream);
   });
   if (st != GEMM_OK) return failed(st, "gemm_mx_quantize");
-  return Py_BuildValue("Niii", buffer.release(), x.rows, x.cols, ldq);
+  return Py_BuildValue("NiiiN", buffer.release(), x.rows, x.cols, ldq, x.device.release());
 }
 
 // dequantize(q, dtype, out, stream)
@@ -406,8 +406,8 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return c.tensor.release();
 }
 
-// describe(codes, scales, cols, fmt) -> (rows, pitch of the codes): the checks
-// of an MXTensor's arrays.
+// describe(codes, scales, cols, fmt) -> (rows, pitch of the codes, device or
+// None): the checks of an MXTensor's arrays.
 PyObject* describe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 4)) return nullptr;
   int cols, rows, width, ld, unit;
@@ -440,7 +440,10 @@ PyObject* describe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Ref device(PyObject_GetAttr(a[0], n_device)), sdevice(PyObject_GetAttr(a[1], n_device));
   if (!device || !sdevice || !one_device(device.p, sdevice.p)) return nullptr;
   // (The pitch of a single row is free: its padded width.)
-  return Py_BuildValue("ii", rows, rows > 1 ? ld : (int)(((long long)width + 15) / 16 * 16));
+  Ref cuda(PyObject_GetAttr(a[0], n_is_cuda));
+  if (!cuda) return nullptr;
+  return Py_BuildValue("iiO", rows, rows > 1 ? ld : (int)(((long long)width + 15) / 16 * 16),
+                       cuda.p == Py_True ? device.p : Py_None);
 }
 
 // setup(torch, MXTensor, GemmError)
@@ -457,7 +460,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
                {&n_index, "index"},     {&n_codes, "_codes"},  {&n_scales, "_scales"},
                {&n_buffer, "_buffer"},  {&n_rows, "rows"},     {&n_cols, "cols"},
                {&n_fmt, "fmt"},         {&n_ld, "_ld"},        {&n_mxfp4, "mxfp4"},
-               {&n_numel, "numel"},     {&n_is_contiguous, "is_contiguous"}};
+               {&n_numel, "numel"},     {&n_is_contiguous, "is_contiguous"},
+               {&n_mx_device, "_device"}};
   for (auto& x : names)
     if (*x.to == nullptr && (*x.to = PyUnicode_InternFromString(x.name)) == nullptr)
       return nullptr;

@@ -50,6 +50,7 @@ class Quantized:
     def __init__(self, rows):
         self.rows, self.cols, self.fmt, self._ld, self._buffer = rows, 64, "mxfp4", 32, None
         self._codes, self._scales = Tensor((rows, 32), "uint8"), Tensor((512,), "uint8")
+        self._device = device
 
 def empty(size, dtype=None, device=None):
     return Tensor(size if isinstance(size, tuple) else (size,), dtype)
