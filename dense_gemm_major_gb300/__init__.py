@@ -2,11 +2,12 @@
 
 The binding only marshals arguments: every step of the GEMM runs in the
 CUDA library ``libdense_gemm.so`` (built in-tree by ``_build.build()``),
-whose C ABI is declared in ``include/dense_gemm.h`` and (microscaled
-operands) ``include/dense_gemm_mx.h``.  The functions of the same names as
+whose C ABI is declared in ``include/dense_gemm.h``, (microscaled
+operands) ``include/dense_gemm_mx.h`` and (products grouped by expert)
+``include/dense_gemm_group.h``.  The functions of the same names as
 the C entry points take integers (device addresses, sizes, a
-``cudaStream_t`` value); ``matmul`` and the ``mx_*`` functions are
-convenience wrappers for torch tensors on the current device and stream.
+``cudaStream_t`` value); ``matmul``, the ``mx_*`` and the ``grouped_*``
+functions are convenience wrappers for torch tensors on the current device and stream.
 There is no fallback: if the library is missing the calls raise.
 """
 from __future__ import annotations
@@ -38,7 +39,8 @@ EXPORTED = ("gemm_f32", "gemm_f16", "gemm_bf16", "gemm_status_string", "gemm_dev
             "gemm_probe_ffma",
             "gemm_probe_ffma_threads",
             "gemm_mx_code_ld", "gemm_mx_scale_bytes", "gemm_mx_quantize", "gemm_mx_dequantize",
-            "gemm_mx4", "gemm_mx4_linear", "gemm_mx_grad")
+            "gemm_mx4", "gemm_mx4_linear", "gemm_mx_grad",
+            "gemm_grouped", "gemm_grouped_grad")
 
 # Microscaled formats (gemm_mx_format_t).
 MXFP4, MXINT8 = 0, 1
@@ -146,6 +148,11 @@ def load() -> ctypes.CDLL:
     lib.gemm_mx4_linear.argtypes = [i, i, i, i, vp, i, vp, i, vp, vp, i, vp]
     lib.gemm_mx_grad.restype = i
     lib.gemm_mx_grad.argtypes = [i, i, i, i, i, i, i, f, vp, i, vp, i, vp, f, vp, i, vp]
+    ll = ctypes.c_longlong
+    lib.gemm_grouped.restype = i
+    lib.gemm_grouped.argtypes = [i, i, i, i, i, i, i, f, vp, i, vp, i, ll, vp, f, vp, i, vp]
+    lib.gemm_grouped_grad.restype = i
+    lib.gemm_grouped_grad.argtypes = [i, i, i, i, i, i, f, vp, i, vp, i, vp, f, vp, i, ll, vp]
     _lib = lib
     return lib
 
@@ -368,6 +375,22 @@ def gemm_mx_grad(fmt, dtype, op_a, dtype_c, M, N, K, alpha, A, lda, b_codes, ldb
                                N, K, alpha, A, lda, b_codes, ldb, b_scales, beta, C, ldc, stream)
 
 
+def gemm_grouped(dtype, op_b, dtype_c, rows, N, K, groups, alpha, A, lda, B, ldb, stride_b,
+                 offsets, beta, C, ldc, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    code_c = DTYPE_CODES[dtype_c] if isinstance(dtype_c, str) else int(dtype_c)
+    return load().gemm_grouped(code, _OP_CODES.get(op_b, -1), code_c, rows, N, K, groups, alpha, A,
+                               lda, B, ldb, stride_b, offsets, beta, C, ldc, stream)
+
+
+def gemm_grouped_grad(dtype, dtype_c, rows, M, N, groups, alpha, A, lda, X, ldx, offsets, beta, C,
+                      ldc, stride_c, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    code_c = DTYPE_CODES[dtype_c] if isinstance(dtype_c, str) else int(dtype_c)
+    return load().gemm_grouped_grad(code, code_c, rows, M, N, groups, alpha, A, lda, X, ldx,
+                                    offsets, beta, C, ldc, stride_c, stream)
+
+
 # ------------------------------------------------------------ torch wrapper
 
 def _torch_dtype_code(t):
@@ -579,3 +602,55 @@ def mx_grad(A, B, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
     if stream is not None and out is None:
         return _on_stream(stream, lambda: mx_grad(A, B, None, dtype, alpha, beta))
     return (_mx or _load_mx()).grad(A, B, out, dtype, alpha, beta, stream)
+
+
+# ------------------------------------------------------------ products grouped by expert
+#
+# Rows are sorted by group: group g's rows are offsets[g] .. offsets[g + 1] - 1,
+# ``offsets`` a contiguous int32 CUDA tensor of groups + 1 elements, which is read
+# when the work runs (include/dense_gemm_group.h has the rules).  Thin like the
+# mx_* functions (csrc/group_python.cpp); what is said there of streams and
+# autograd holds here.  ExpertLinear in examples/expert_layer.py is a
+# torch.autograd.Function of the three products.
+
+_group = None
+
+
+def _load_group():
+    """The extension, given torch's objects at its first use."""
+    global _group
+    if _group is None:
+        load()
+        import torch
+        from . import _groupcall as ext
+        ext.setup(torch, GemmError)
+        _group = ext
+    return _group
+
+
+def grouped_matmul(A, B, offsets, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
+    """out[i] = alpha * (A[i] @ B[g]) + beta * out[i] for the rows i of each
+    group g.  A (rows x K) and B (groups x K x N) are float16 or bfloat16, A
+    row-major, B's matrices row-major or transposed views, which are read in
+    place: with weights W stored groups x out x in, ``grouped_matmul(x,
+    W.transpose(1, 2), offsets)`` is a layer's forward product and
+    ``grouped_matmul(dy, W, offsets)`` the gradient of its input.  The result is
+    of the operands' dtype or float32 (``dtype``, or that of ``out``).  Rows of no
+    group are not written: a new result does not define them.  Operands have rows
+    (and matrices) of a multiple of 16 bytes, or are contiguous (those of other
+    widths are then copied to aligned ones first)."""
+    if stream is not None and out is None:
+        return _on_stream(stream,
+                          lambda: grouped_matmul(A, B, offsets, None, dtype, alpha, beta))
+    return (_group or _load_group()).grouped_matmul(A, B, offsets, out, dtype, alpha, beta, stream)
+
+
+def grouped_grad(A, X, offsets, out=None, dtype=None, alpha=1.0, beta=0.0, stream=None):
+    """out[g] = alpha * (A[rows of g].T @ X[rows of g]) + beta * out[g] for every
+    group g (an empty one's product is zero), groups x M x N from A (rows x M)
+    and X (rows x N), both row-major: ``grouped_grad(dy, x, offsets)`` is the
+    gradient of weights stored groups x out x in.  Types, alignment and
+    ``dtype`` as in grouped_matmul."""
+    if stream is not None and out is None:
+        return _on_stream(stream, lambda: grouped_grad(A, X, offsets, None, dtype, alpha, beta))
+    return (_group or _load_group()).grouped_grad(A, X, offsets, out, dtype, alpha, beta, stream)

@@ -1,5 +1,6 @@
 """In-tree build of the CUDA library (libdense_gemm.so) for sm_103a, and of
-the CPython extension (_mxcall) that calls its microscaled entry points.
+the CPython extensions (_mxcall, _groupcall) that call its microscaled and its
+grouped entry points.
 
 Each translation unit under csrc/ is compiled by its own nvcc process, in
 parallel, then linked into one shared library next to this file.  A unit is
@@ -19,11 +20,14 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libdense_gemm.so")
-# The CPython extension around the microscaled entry points (needs Python's
-# headers), named for the interpreter that it is built for: another one neither
-# loads it nor takes it for up to date.
+# The CPython extensions around the microscaled and the grouped entry points (they
+# need Python's headers), named for the interpreter that they are built for:
+# another one neither loads them nor takes them for up to date.
+_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX") or ".so"
 EXT_SOURCE = os.path.join(CSRC, "mx_python.cpp")
-EXT = os.path.join(PKG, "_mxcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+EXT = os.path.join(PKG, "_mxcall" + _SUFFIX)
+GROUP_EXT_SOURCE = os.path.join(CSRC, "group_python.cpp")
+GROUP_EXT = os.path.join(PKG, "_groupcall" + _SUFFIX)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -92,18 +96,23 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
 
 
 def build_extension(verbose: bool = False) -> None:
-    """_mxcall, linked to libdense_gemm.so beside it."""
-    newest = max([os.path.getmtime(EXT_SOURCE)] + [os.path.getmtime(h) for h in _headers()])
-    if os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
-        return
-    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") \
-        if os.path.dirname(nvcc()) else "/usr/local/cuda/include"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", EXT_SOURCE, "-o", EXT,
-           "-I", INCLUDE, "-I", cuda, "-I", sysconfig.get_paths()["include"],
-           "-L", PKG, "-ldense_gemm", "-Wl,-rpath,$ORIGIN"]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.check_call(cmd)
+    """The CPython extensions, linked to libdense_gemm.so beside them."""
+    procs = []
+    for source, ext in ((EXT_SOURCE, EXT), (GROUP_EXT_SOURCE, GROUP_EXT)):
+        newest = max([os.path.getmtime(source)] + [os.path.getmtime(h) for h in _headers()])
+        if os.path.exists(ext) and os.path.getmtime(ext) >= newest:
+            continue
+        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") \
+            if os.path.dirname(nvcc()) else "/usr/local/cuda/include"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", source, "-o", ext,
+               "-I", INCLUDE, "-I", cuda, "-I", sysconfig.get_paths()["include"],
+               "-L", PKG, "-ldense_gemm", "-Wl,-rpath,$ORIGIN"]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append((cmd, subprocess.Popen(cmd)))
+    for cmd, p in procs:
+        if p.wait() != 0:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,49 @@
+// Internal interface of the grouped products: the launch functions, called by
+// group_api.cu.  Callers use include/dense_gemm_group.h.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "dense_gemm_group.h"
+#include "launch.h"
+
+namespace dgemm {
+
+// The kernel's three forms, by what its MMAs' M side (256 columns of C) and N
+// side (up to 256 rows of C) read:
+//   forward  B stored N x K, K-major          X, K-major
+//   input    B stored K x N, MN-major         X, K-major
+//   weights  X, MN-major                      A, MN-major, both over a group's rows
+enum GroupKind { kGroupForward = 0, kGroupInput = 1, kGroupWeights = 2 };
+
+constexpr int kGroupTile = 256;       // columns of C, and rows at most, of a CTA pair's unit
+constexpr int kGroupBK = 128;
+constexpr int kGroupMaxGroups = GEMM_GROUP_MAX_GROUPS;
+
+struct GroupParams {
+  int kind;
+  int rows, groups;
+  // Products: C is rows x N, terms of the sums K.  Weights: C[g] is M x N (A's
+  // columns x X's), the sums run over the group's rows (K == 0: without terms).
+  int M, N, K;
+  int per_group;            // weights: tiles of a C[g]
+  const int* offsets;
+  int zmul;                 // 0: one B for all groups
+  int seg;                  // k-tiles summed in tensor memory at a time
+  float alpha, beta;
+  void* C;
+  long long ldc, stride_c;  // stride_c: weights
+  unsigned* fault;
+  unsigned long long timeout_ns;
+};
+
+// tmM: B as {K, N, groups} with boxes of 64 x 128 x 1 (forward), as {N, K,
+// groups} with boxes of 64 x 128 x 1 (input), or X as {N, rows} with boxes of
+// 64 x 64 (weights).  tmN, tmN16: X as {K, rows} with boxes of 64 x 128 and 64 x
+// 16, or A as {M, rows} with boxes of 64 x 64 (weights; both alike).
+cudaError_t launch_group(int dtype, int dtype_c, const GroupParams& p, const CUtensorMap* tmM,
+                         const CUtensorMap* tmN, const CUtensorMap* tmN16, int pairs,
+                         cudaStream_t stream);
+
+}  // namespace dgemm

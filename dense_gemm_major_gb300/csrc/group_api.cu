@@ -1,0 +1,202 @@
+// C-ABI entry points of the grouped products: argument checks, tensor maps,
+// operand copies and launch.  See include/dense_gemm_group.h.
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "group.h"
+#include "mx.h"
+#include "workspace.h"
+
+namespace {
+
+using namespace dgemm::api;
+
+inline bool good_size(int n) { return n >= 0 && n <= GEMM_GROUP_MAX_SIZE; }
+inline bool good_types(int dtype, int dtype_c) {
+  return (dtype == 1 || dtype == 2) && (dtype_c == 0 || dtype_c == dtype);
+}
+inline CUtensorMapDataType map_type(int dtype) {
+  return dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// A 16-bit operand: `count` matrices of `outer` rows of `inner` elements.
+struct Operand {
+  const void* p;
+  long long inner, outer, ld, count, stride;
+  bool packed;            // at any alignment: a copy with aligned rows is taken
+  // The matrices lie behind one another (or are one, stride 0).
+  gemm_status_t check() {
+    if (p == nullptr || ld < inner) return GEMM_ERR_INVALID_ARG;
+    const long long span1 = (outer - 1) * ld + inner;
+    if (count > 1 && stride != 0 && stride < span1) return GEMM_ERR_INVALID_ARG;
+    packed = false;
+    if (aligned(p, 16) && ld % 8 == 0 && (count == 1 || stride % 8 == 0)) return GEMM_OK;
+    packed = ld == inner && (count == 1 || stride == 0 || stride == outer * ld);
+    return packed && aligned(p, 2) ? GEMM_OK : GEMM_ERR_MISALIGNED;
+  }
+  long long matrices() const { return stride == 0 ? 1 : count; }
+  uint64_t bytes() const {
+    return (uint64_t)((matrices() - 1) * stride + (outer - 1) * ld + inner) * 2;
+  }
+  long long copy_ld() const { return (inner + 7) / 8 * 8; }
+  size_t copy_bytes() const {   // a multiple of 256
+    return packed ? ((size_t)(matrices() * outer * copy_ld()) * 2 + 255) / 256 * 256 : 0;
+  }
+  gemm_status_t copy_to(void* to, cudaStream_t stream) {
+    const long long ldd = copy_ld();
+    const gemm_status_t st = status_of(
+        dgemm::launch_mx_align(p, matrices() * outer, (int)inner, to, ldd, stream));
+    p = to;
+    ld = ldd;
+    stride = stride == 0 ? 0 : outer * ldd;
+    return st;
+  }
+};
+
+// Operands that TMA cannot address become copies in the workspace that `ws` holds.
+gemm_status_t align_operands(Operand& a, Operand& b, dgemm::StreamWorkspaces& ws,
+                             cudaStream_t stream) {
+  if (!a.packed && !b.packed) return GEMM_OK;
+  void* p = nullptr;
+  gemm_status_t st = ws.get(dgemm::kWsPack, a.copy_bytes() + b.copy_bytes(), &p);
+  if (st != GEMM_OK) return st;
+  char* const second = static_cast<char*>(p) + a.copy_bytes();
+  if (a.packed && (st = a.copy_to(p, stream)) != GEMM_OK) return st;
+  if (b.packed && (st = b.copy_to(second, stream)) != GEMM_OK) return st;
+  return GEMM_OK;
+}
+
+bool encode_rows(CUtensorMap* map, int dtype, const Operand& o, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer};
+  const cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  return encode_tiled(map, map_type(dtype), 2, o.p, dims, strides, box);
+}
+bool encode_matrices(CUtensorMap* map, int dtype, const Operand& o) {
+  const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer,
+                              (cuuint64_t)o.matrices()};
+  // (The distance of a single matrix's successor: never used, but checked.)
+  const cuuint64_t far = (cuuint64_t)(o.stride != 0 && o.count > 1 ? o.stride : o.outer * o.ld);
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, far * 2};
+  const cuuint32_t box[3] = {64, 128, 1};
+  return encode_tiled(map, map_type(dtype), 3, o.p, dims, strides, box);
+}
+
+// k-tiles per sum in tensor memory, which truncates at each step of 16: sums of
+// like terms come out too small, the more the longer they are.  FP32 results:
+// 1024 terms, 16-bit ones 16384 (a fifth of FP16's rounding).
+inline int segment(int dtype_c) { return (dtype_c == 0 ? 1024 : 16384) / dgemm::kGroupBK; }
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int N, int K,
+                           int groups, float alpha, const void* A, int lda, const void* B, int ldb,
+                           long long stride_b, const int* offsets, float beta, void* C, int ldc,
+                           cudaStream_t stream) {
+  if (!good_types(dtype, dtype_c) || (op_b != GEMM_OP_N && op_b != GEMM_OP_T) ||
+      !good_size(rows) || !good_size(N) || !good_size(K) || groups < 0 ||
+      groups > GEMM_GROUP_MAX_GROUPS)
+    return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 || N == 0 || groups == 0) return GEMM_OK;
+  const int es = dtype_c == 0 ? 4 : 2;
+  if (C == nullptr || ldc < N || offsets == nullptr) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(C, es) || !aligned(offsets, 4)) return GEMM_ERR_MISALIGNED;
+  const uint64_t c_bytes = span(rows, (long long)N * es, (long long)ldc * es);
+  if (overlap(C, c_bytes, offsets, (uint64_t)(groups + 1) * 4)) return GEMM_ERR_INVALID_ARG;
+  const bool empty = K == 0 || alpha == 0.f;
+  const bool t = op_b == GEMM_OP_T;
+  Operand a{A, K, rows, lda, 1, 0, false};
+  Operand b{B, t ? K : N, t ? N : K, ldb, groups, stride_b, false};
+  gemm_status_t st;
+  if (!empty) {
+    if (stride_b < 0) return GEMM_ERR_INVALID_ARG;
+    if ((st = a.check()) != GEMM_OK || (st = b.check()) != GEMM_OK) return st;
+    if (overlap(C, c_bytes, A, a.bytes()) || overlap(C, c_bytes, B, b.bytes()))
+      return GEMM_ERR_INVALID_ARG;
+  } else if (beta == 1.f) {
+    return GEMM_OK;
+  }
+  dgemm::GroupParams p;
+  int max_pairs;
+  if ((st = dgemm::current_device_pairs(&p.fault, &max_pairs)) != GEMM_OK) return st;
+  dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
+  alignas(64) CUtensorMap tmM{}, tmN{}, tmN16{};
+  if (!empty) {
+    if ((st = align_operands(a, b, workspaces, stream)) != GEMM_OK) return st;
+    if (!encode_matrices(&tmM, dtype, b) || !encode_rows(&tmN, dtype, a, 128) ||
+        !encode_rows(&tmN16, dtype, a, 16))
+      return GEMM_ERR_LAUNCH;
+  }
+  p.kind = t ? dgemm::kGroupForward : dgemm::kGroupInput;
+  p.rows = rows, p.groups = groups;
+  p.M = 0, p.N = N, p.K = empty ? 0 : K;
+  p.per_group = 0;
+  p.offsets = offsets;
+  p.zmul = stride_b == 0 ? 0 : 1;
+  p.seg = segment(dtype_c);
+  p.alpha = empty ? 0.f : alpha, p.beta = beta;
+  p.C = C, p.ldc = ldc, p.stride_c = 0;
+  p.timeout_ns = dgemm::wait_bound_ns();
+  // No more units than whole tiles of rows and a ragged one per group.
+  const long long most = ((long long)rows / dgemm::kGroupTile + (groups < rows ? groups : rows)) *
+                         ceil_div(N, dgemm::kGroupTile);
+  const int pairs = (int)(most < max_pairs ? most : max_pairs);
+  return status_of(dgemm::launch_group(dtype, dtype_c, p, &tmM, &tmN, &tmN16, pairs, stream));
+}
+
+gemm_status_t gemm_grouped_grad(int dtype, int dtype_c, int rows, int M, int N, int groups,
+                                float alpha, const void* A, int lda, const void* X, int ldx,
+                                const int* offsets, float beta, void* C, int ldc,
+                                long long stride_c, cudaStream_t stream) {
+  if (!good_types(dtype, dtype_c) || !good_size(rows) || !good_size(M) || !good_size(N) ||
+      groups < 0 || groups > GEMM_GROUP_MAX_GROUPS)
+    return GEMM_ERR_INVALID_ARG;
+  if (M == 0 || N == 0 || groups == 0) return GEMM_OK;
+  const int es = dtype_c == 0 ? 4 : 2;
+  const long long one = (long long)(M - 1) * ldc + N;   // elements that a C[g] spans
+  if (C == nullptr || ldc < N || offsets == nullptr || (groups > 1 && stride_c < one))
+    return GEMM_ERR_INVALID_ARG;
+  if (!aligned(C, es) || !aligned(offsets, 4)) return GEMM_ERR_MISALIGNED;
+  const uint64_t c_bytes = (uint64_t)((groups - 1) * (groups > 1 ? stride_c : 0) + one) * es;
+  if (overlap(C, c_bytes, offsets, (uint64_t)(groups + 1) * 4)) return GEMM_ERR_INVALID_ARG;
+  const bool empty = rows == 0 || alpha == 0.f;
+  Operand a{A, M, rows, lda, 1, 0, false}, x{X, N, rows, ldx, 1, 0, false};
+  gemm_status_t st;
+  if (!empty) {
+    if ((st = a.check()) != GEMM_OK || (st = x.check()) != GEMM_OK) return st;
+    if (overlap(C, c_bytes, A, a.bytes()) || overlap(C, c_bytes, X, x.bytes()))
+      return GEMM_ERR_INVALID_ARG;
+  } else if (beta == 1.f) {
+    return GEMM_OK;
+  }
+  dgemm::GroupParams p;
+  int max_pairs;
+  if ((st = dgemm::current_device_pairs(&p.fault, &max_pairs)) != GEMM_OK) return st;
+  dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
+  alignas(64) CUtensorMap tmM{}, tmN{};
+  if (!empty) {
+    if ((st = align_operands(a, x, workspaces, stream)) != GEMM_OK) return st;
+    if (!encode_rows(&tmM, dtype, x, 64) || !encode_rows(&tmN, dtype, a, 64))
+      return GEMM_ERR_LAUNCH;
+  }
+  p.kind = dgemm::kGroupWeights;
+  p.rows = rows, p.groups = groups;
+  p.M = M, p.N = N, p.K = empty ? 0 : 1;
+  p.per_group = ceil_div(M, dgemm::kGroupTile) * ceil_div(N, dgemm::kGroupTile);
+  p.offsets = offsets;
+  p.zmul = 0;
+  p.seg = segment(dtype_c);
+  p.alpha = empty ? 0.f : alpha, p.beta = beta;
+  p.C = C, p.ldc = ldc, p.stride_c = groups > 1 ? stride_c : 0;
+  p.timeout_ns = dgemm::wait_bound_ns();
+  const long long units = (long long)groups * p.per_group;
+  const int pairs = (int)(units < max_pairs ? units : max_pairs);
+  return status_of(dgemm::launch_group(dtype, dtype_c, p, &tmM, &tmN, &tmN, pairs, stream));
+}
+
+}  // extern "C"

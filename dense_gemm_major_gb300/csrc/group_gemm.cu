@@ -1,0 +1,472 @@
+// Products grouped by expert on sm_103a tensor cores: rows sorted by group, each
+// group with its own matrix (forward and input gradient), or each group with its
+// own result over the group's rows (weights' gradient).  The groups' bounds are
+// on the device only.
+//
+// A cluster of two CTAs computes units of 256 columns x up to 256 rows of C with
+// tcgen05.mma.cta_group::2.kind::f16.  The columns of C are the MMA's M side,
+// the rows its N side, which goes in steps of 32: a group's last, ragged unit
+// costs MMAs and loads for its rows only, where 256 rows on the M side would be
+// padded in full.  A TMEM lane is a column of C, so that a warp stores 32
+// consecutive columns of a row, whatever C's alignment, and the rows of the next
+// group are simply not stored.
+//
+// Roles (384 threads): warp 0 loads both operands by TMA, warp 1 issues the MMAs
+// (even CTA), warp 2 clears the rows past a group's end (weights' gradient),
+// warps 4-11 drain the accumulators and store.
+//
+// FP32 sums.  The MMA truncates the running sum at every 16-deep step, so a unit
+// is summed in segments (GroupParams::seg), which the draining warps add in
+// registers, rounding to nearest; the two accumulators in tensor memory let that
+// overlap the next segment.
+#include "group.h"
+#include "mx.cuh"
+
+namespace dgemm {
+namespace {
+
+constexpr int BK = kGroupBK;
+constexpr int kThreads = 384;
+constexpr int kEpiWarp = 4, kEpiWarps = 8;
+// A stage: the CTA's 128 columns of C and up to 128 rows, BK deep.  K-major
+// operands are two blocks of 64 k (128-byte swizzled rows), MN-major ones two
+// blocks 64 wide with a row for each k: 16 KB a block either way.
+constexpr uint32_t kBlock = 128 * 128;
+constexpr uint32_t kSide = 2 * kBlock;
+constexpr uint32_t kStage = 2 * kSide;
+constexpr int S = 3;
+constexpr uint32_t kTmemCols = 512;                       // two accumulators
+constexpr uint32_t kTableBytes = (kGroupMaxGroups + 1) * 2 * 4;
+constexpr uint32_t kSmemBytes = S * kStage + kTableBytes + 512 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+struct alignas(8) Barriers {
+  uint64_t full[S];       // even CTA: both CTAs' operands are there
+  uint64_t empty[S];      // the MMAs on stage s are done
+  uint64_t tail[S];       // weights: this CTA's part of a stage that ends its group
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];  // even CTA
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Barriers) <= 512, "barrier block must fit its reserved space");
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* desc,
+                                                 uint32_t cluster_bar, int32_t x, int32_t y,
+                                                 int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// A unit: rows [row, row_end) of C (at most 256; weights: of C[g]) by the 256
+// columns from col; the sum's k-tiles are nk, from row k0 of the operands and up
+// to k_end (weights; products: from column 0 up to K).
+struct Unit {
+  int g, row, row_end, col;
+  int nk, k0, k_end;
+  int mma_rows;             // rows rounded up to the MMA's steps of 32
+};
+
+// The units of a grid of CTA pairs, which each takes in increasing order.
+struct Walk {
+  int g = 0;
+  template <int kKind>
+  __device__ __forceinline__ Unit unit(int u, const GroupParams& p, const int* start,
+                                       const int* unit0) {
+    Unit w;
+    int tm, tn;
+    if constexpr (kKind == kGroupWeights) {
+      w.g = u / p.per_group;
+      // (Groups of 16 tiles along C's columns share the operands in L2.)
+      grouped_tile(u - w.g * p.per_group, (p.N + kGroupTile - 1) / kGroupTile,
+                   (p.M + kGroupTile - 1) / kGroupTile, 16, tn, tm);
+      w.row = tm * kGroupTile;
+      w.row_end = min(w.row + kGroupTile, p.M);
+      w.k0 = start[w.g];
+      w.k_end = start[w.g + 1];
+      w.nk = p.K == 0 ? 0 : (w.k_end - w.k0 + BK - 1) / BK;
+    } else {
+      while (unit0[g + 1] <= u) ++g;
+      w.g = g;
+      const int rows = start[g + 1] - start[g];
+      grouped_tile(u - unit0[g], (rows + kGroupTile - 1) / kGroupTile,
+                   (p.N + kGroupTile - 1) / kGroupTile, 16, tm, tn);
+      w.row = start[g] + tm * kGroupTile;
+      w.row_end = min(w.row + kGroupTile, start[g + 1]);
+      w.k0 = 0;
+      w.k_end = p.K;
+      w.nk = (p.K + BK - 1) / BK;
+    }
+    w.col = tn * kGroupTile;
+    w.mma_rows = (w.row_end - w.row + 31) & ~31;
+    return w;
+  }
+};
+
+// The groups' first rows, put in order, and (products) their first units; by
+// one warp.  Returns the number of units.
+__device__ __forceinline__ int group_table(const GroupParams& p, int* start, int* unit0) {
+  const int lane = threadIdx.x & 31;
+  const int tiles_n = (p.N + kGroupTile - 1) / kGroupTile;
+  int last = 0, units = 0;
+  bool bad = false;
+  for (int base = 0; base <= p.groups; base += 32) {
+    const int i = base + lane;
+    const int raw = i <= p.groups ? p.offsets[i] : p.rows;
+    int v = min(max(raw, 0), p.rows);
+    const int own = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, last);
+    bad |= own != raw || v != own;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = last;
+    // Units of group i - 1, whose end this lane has.
+    int n = i >= 1 && i <= p.groups
+                ? (int)((long long)((v - before + kGroupTile - 1) / kGroupTile) * tiles_n)
+                : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    if (i <= p.groups) {
+      start[i] = v;
+      unit0[i] = units + n;
+    }
+    units += __shfl_sync(0xffffffffu, n, 31);
+    last = __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
+    raise_fault(p.fault, kFaultGroupOffsets);
+  return p.kind == kGroupWeights ? p.groups * p.per_group : units;
+}
+
+template <typename T, typename TC, int kKind>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    group_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN,
+                 const __grid_constant__ CUtensorMap tmN16, const GroupParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const base = align_smem_1024(smem_raw);
+  int* const start = reinterpret_cast<int*>(base + S * kStage);
+  int* const unit0 = start + kGroupMaxGroups + 1;
+  auto* bars = reinterpret_cast<Barriers*>(base + S * kStage + kTableBytes);
+  __shared__ int s_units;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
+  const int npairs = gridDim.x >> 1;
+  constexpr bool kWeights = kKind == kGroupWeights;
+  constexpr bool kMK = kKind == kGroupForward;   // the M side is K-major
+  constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), kWeights ? 2 : 1);
+      mbar_init(smem_u32(&bars->empty[s]), 1);
+      mbar_init(smem_u32(&bars->tail[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&bars->acc_full[b]), 1);
+      mbar_init(smem_u32(&bars->acc_empty[b]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmM);
+    tma_prefetch_desc(&tmN);
+    if constexpr (!kWeights) tma_prefetch_desc(&tmN16);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
+  wait_prior_grids();
+  allow_dependent_grids();
+  if (warp == 2) {
+    const int n = group_table(p, start, unit0);
+    if (lane == 0) s_units = n;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_base;
+  const int units = s_units;
+
+  uint32_t issued = 0;
+  if (warp == 0) {
+    if (elect_one()) {
+      // ---------------------------------------------- loads (both CTAs)
+      RingPos<S> pos;
+      Walk walk;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
+        const Unit w = walk.unit<kKind>(u, p, start, unit0);
+        const int half = w.mma_rows / 2;                 // rows of C that this CTA loads
+        const int row = w.row + (int)rank * half;
+        const int col = w.col + (int)rank * 128;
+        const int z = w.g * p.zmul;
+        for (int kt = 0; kt < w.nk; ++kt, ++it, pos.next()) {
+          const uint32_t s = pos.slot;
+          ok = role_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                         &bars->abort, kFaultTcProducerWait, true);
+          if (!ok) break;
+          const uint32_t sm = smem_u32(base + s * kStage), sn = sm + kSide;
+          const uint32_t full = smem_u32(&bars->full[s]);
+          const uint32_t fb = mapa_shared(full, 0);
+          if constexpr (kWeights) {
+            const int k = w.k0 + kt * BK;
+            const int valid = w.k_end - k;               // rows of the group from k on
+            const int deep = valid > 64 ? 2 : 1, wide = half > 64 ? 2 : 1;
+            const uint32_t bytes = (uint32_t)(deep * (2 + wide)) * (kBlock / 2);
+            const bool ragged = valid < BK && (valid & 15) != 0;
+            const uint32_t tail = smem_u32(&bars->tail[s]);
+            if (ragged)
+              mbar_arrive_expect_tx(tail, bytes);
+            else if (rank == 0)
+              mbar_arrive_expect_tx(full, 2 * bytes);
+            else
+              mbar_arrive_any_cta(fb);
+            for (int d = 0; d < deep; ++d) {
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t to = sm + j * kBlock + d * (kBlock / 2);
+                if (ragged)
+                  tma_load_2d(to, &tmM, tail, col + j * 64, k + d * 64);
+                else
+                  tma_load_2d_pair(to, &tmM, fb, col + j * 64, k + d * 64);
+              }
+              for (int j = 0; j < wide; ++j) {
+                const uint32_t to = sn + j * kBlock + d * (kBlock / 2);
+                if (ragged)
+                  tma_load_2d(to, &tmN, tail, row + j * 64, k + d * 64);
+                else
+                  tma_load_2d_pair(to, &tmN, fb, row + j * 64, k + d * 64);
+              }
+            }
+          } else {
+            if (rank == 0)
+              mbar_arrive_expect_tx(full, 2 * (kSide + (uint32_t)half * 256));
+            const int k = kt * BK;
+            for (int j = 0; j < 2; ++j) {
+              if constexpr (kMK)
+                tma_load_3d_pair(sm + j * kBlock, &tmM, fb, k + j * 64, col, z);
+              else
+                tma_load_3d_pair(sm + j * kBlock, &tmM, fb, col + j * 64, k, z);
+            }
+            for (int j = 0; j < 2; ++j) {
+              if (half == 128) {
+                tma_load_2d_pair(sn + j * kBlock, &tmN, fb, k + j * 64, row);
+              } else {
+                for (int r = 0; r < half; r += 16)
+                  tma_load_2d_pair(sn + j * kBlock + r * 128, &tmN16, fb, k + j * 64, row + r);
+              }
+            }
+          }
+          issued = it + 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      // ---------------------------------------------- MMA issuer (even CTA)
+      RingPos<S> pos;
+      Walk walk;
+      bool ready = false;
+      uint32_t seg = 0;
+      bool ok = true;
+      for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
+        const Unit w = walk.unit<kKind>(u, p, start, unit0);
+        const uint32_t idesc = instr_desc(kAb, 256, (uint32_t)w.mma_rows, kMK ? 0u : 1u,
+                                          kWeights ? 1u : 0u);
+        for (int k0 = 0; k0 < w.nk && ok; k0 += p.seg, ++seg) {
+          const int k1 = min(k0 + p.seg, w.nk);
+          const uint32_t b = seg & 1;
+          ok = role_wait(smem_u32(&bars->acc_empty[b]), ((seg >> 1) & 1u) ^ 1u, p.fault,
+                         p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
+          if (!ok) break;
+          tc_fence_after();
+          for (int kt = k0; kt < k1; ++kt) {
+            const uint32_t st = smem_u32(base + pos.slot * kStage);
+            const uint32_t freed = smem_u32(&bars->empty[pos.slot]);
+            ok = ready || role_wait(smem_u32(&bars->full[pos.slot]), pos.parity, p.fault,
+                                    p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
+            if (!ok) break;
+            tc_fence_after();
+            pos.next();
+            ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
+            // MN-major blocks step by 16 rows of 128 bytes per 16 of K, K-major
+            // ones by 32 bytes, 64 to a block.
+            const uint32_t mlo = desc_lo(st, kMK ? 16 : kBlock);
+            const uint32_t nlo = desc_lo(st + kSide, kWeights ? kBlock : 16);
+            // (Whole steps past the group's end are left out, not only cleared:
+            // nothing has loaded them.)
+            const int steps = kWeights ? min((w.k_end - w.k0 - kt * BK + 15) / 16, BK / 16)
+                                       : BK / 16;
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              if (!kWeights || k < steps)
+                mma_f16_pair_lo(
+                    tmem_base + b * 256,
+                    mlo + ((kMK ? (k >> 2) * kBlock + (k & 3) * 32 : k * 2048) >> 4),
+                    nlo + ((kWeights ? k * 2048 : (k >> 2) * kBlock + (k & 3) * 32) >> 4), idesc,
+                    (kt > k0 || k > 0) ? 1u : 0u);
+            mma_commit_pair_multicast(freed, 0x3);
+          }
+          if (!ok) break;
+          mma_commit_pair_multicast(smem_u32(&bars->acc_full[b]), 0x3);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    if constexpr (kWeights) {
+      // ------------------------------------------------ ragged ends (both CTAs)
+      // The rows of the next group in a group's last 16 are cleared in both
+      // operands (zero times a NaN is not zero).
+      Walk walk;
+      uint32_t it = 0, uses = 0;   // a bit per slot: the parity of its next use
+      bool ok = true;
+      for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
+        const Unit w = walk.unit<kKind>(u, p, start, unit0);
+        it += (uint32_t)w.nk;
+        const int valid = w.k_end - w.k0 - (w.nk - 1) * BK;
+        if (w.nk == 0 || (valid & 15) == 0) continue;
+        const uint32_t s = (it - 1) % S;
+        ok = role_wait_lanes(smem_u32(&bars->tail[s]), (uses >> s) & 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait, false, false);
+        if (!ok) break;
+        uses ^= 1u << s;
+        const int blocks = w.mma_rows / 2 > 64 ? 4 : 3;
+        const int clear = 16 - (valid & 15);
+        for (int i = lane; i < blocks * clear * 8; i += 32) {
+          const int row = valid + (i >> 3) % clear, b = (i >> 3) / clear;
+          *reinterpret_cast<uint4*>(base + s * kStage + b * kBlock + row * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kEpiWarp) {
+    // ------------------------------------------------ epilogue (both CTAs)
+    // Warp: TMEM lanes 32 q .. 32 q + 31 (columns of C), every other 32 rows.
+    const int q = warp & 3;
+    const int half = (warp - kEpiWarp) >> 2;
+    const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 &&
+                       ((p.ldc | p.N) & 1) == 0 && (p.stride_c & 1) == 0;
+    Walk walk;
+    uint32_t seg = 0;
+    bool ok = true;
+    for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
+      const Unit w = walk.unit<kKind>(u, p, start, unit0);
+      const int chunks = w.mma_rows / 32;
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int k0 = 0; k0 < w.nk; k0 += p.seg, ++seg) {
+        const uint32_t b = seg & 1;
+        ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcEpilogueWait, false, false);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int chunk = 2 * (c >> 1) + half;
+          if (chunk < chunks) {
+            uint32_t r[16];
+            tmem_ld16(t + chunk * 32 + (c & 1) * 16, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), 0));
+      }
+      if (!ok) break;
+      const int col = w.col + (int)rank * 128 + q * 32 + lane;
+      TC* c_out = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int chunk = 2 * c + half;
+        if (chunk < chunks)
+          store_piece<TC>(acc + c * 32, c_out, p.ldc, w.row_end, p.N, w.row + chunk * 32, col,
+                          pairs, p.alpha, p.beta);
+      }
+    }
+  }
+
+  // ------------------------------------------------ teardown
+  if (warp == 1 && rank == 0 && elect_one()) {
+    // Every MMA of the pair has completed before TMEM is freed.
+    mma_commit_pair_multicast(smem_u32(&bars->drain), 0x1);
+    if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
+      raise_fault(p.fault, kFaultDrainWait);
+  }
+  __syncthreads();
+  if (warp == 0 && rank == 0 && elect_one() && bars->abort) {
+    // Let the copies in flight land; a stage whose other arrivals are missing
+    // makes the wait give up.
+    const uint32_t first = issued > (uint32_t)S ? issued - S : 0;
+    for (uint32_t it = first; it < issued; ++it) {
+      if (!mbar_wait_bounded(smem_u32(&bars->full[it % S]), (it / S) & 1u, p.timeout_ns,
+                             nullptr)) {
+        raise_fault(p.fault, kFaultDrainWait);
+        break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves while the pair may still touch its memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+template <typename T, typename TC, int kKind>
+cudaError_t launch_typed(const GroupParams& p, const CUtensorMap* tmM, const CUtensorMap* tmN,
+                         const CUtensorMap* tmN16, int pairs, cudaStream_t stream) {
+  auto kernel = group_kernel<T, TC, kKind>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = mx_allow_smem(kernel, kSmemBytes, &done);
+  if (e != cudaSuccess) return e;
+  return launch_gemm_kernel(kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, *tmM,
+                            *tmN, *tmN16, p);
+}
+
+template <typename T, typename TC>
+cudaError_t launch_kind(const GroupParams& p, const CUtensorMap* a, const CUtensorMap* b,
+                        const CUtensorMap* c, int pairs, cudaStream_t stream) {
+  if (p.kind == kGroupForward) return launch_typed<T, TC, kGroupForward>(p, a, b, c, pairs, stream);
+  if (p.kind == kGroupInput) return launch_typed<T, TC, kGroupInput>(p, a, b, c, pairs, stream);
+  return launch_typed<T, TC, kGroupWeights>(p, a, b, c, pairs, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_group(int dtype, int dtype_c, const GroupParams& p, const CUtensorMap* tmM,
+                         const CUtensorMap* tmN, const CUtensorMap* tmN16, int pairs,
+                         cudaStream_t stream) {
+  if (dtype == 1)
+    return dtype_c == 0 ? launch_kind<__half, float>(p, tmM, tmN, tmN16, pairs, stream)
+                        : launch_kind<__half, __half>(p, tmM, tmN, tmN16, pairs, stream);
+  return dtype_c == 0
+             ? launch_kind<__nv_bfloat16, float>(p, tmM, tmN, tmN16, pairs, stream)
+             : launch_kind<__nv_bfloat16, __nv_bfloat16>(p, tmM, tmN, tmN16, pairs, stream);
+}
+
+}  // namespace dgemm

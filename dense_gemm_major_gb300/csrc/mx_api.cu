@@ -3,9 +3,9 @@
 #include <cstdint>
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include "api_util.h"
 #include "dense_gemm_mx.h"
 #include "launch.h"
 #include "mx.h"
@@ -13,57 +13,23 @@
 
 namespace {
 
-// cuTensorMapEncodeTiled, fetched from the driver once.
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      p = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
+using namespace dgemm::api;
 
 // 2-D row-major array {inner, outer}.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
                uint64_t outer, uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer,
                bool swizzle = true) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {pitch_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, dt, 2, base, dims, strides, box, swizzle);
 }
 
-inline bool aligned(const void* p, int n) {
-  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0;
-}
-inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 inline int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }
 inline bool good_format(int fmt) { return fmt == GEMM_MXFP4 || fmt == GEMM_MXINT8; }
 inline bool good_dtype(int d) { return d >= 0 && d <= 2; }
 inline bool good_size(int n) { return n >= 0 && n <= GEMM_MX_MAX_SIZE; }
 inline bool good_op(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
-
-inline uint64_t span(long long rows, long long width, long long pitch) {
-  return rows > 0 && width > 0 ? (uint64_t)((rows - 1) * pitch + width) : 0;
-}
-inline bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
-  if (an == 0 || bn == 0 || a == nullptr || b == nullptr) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + bn && b0 < a0 + an;
-}
 
 inline int code_bytes(int fmt, int K) { return fmt == GEMM_MXFP4 ? K / 2 + (K & 1) : K; }
 inline int code_ld(int fmt, int K) {
@@ -83,12 +49,6 @@ inline bool overlaps_quantized(const void* p, uint64_t n, int fmt, int R, int K,
                                const void* codes, int ldq, const void* scales) {
   return overlap(p, n, codes, span(R, code_bytes(fmt, K), ldq)) ||
          overlap(p, n, scales, (uint64_t)scale_bytes(R, K));
-}
-
-gemm_status_t status_of(cudaError_t e) {
-  if (e == cudaSuccess) return GEMM_OK;
-  cudaGetLastError();
-  return GEMM_ERR_LAUNCH;
 }
 
 // C := beta * C, the product with no terms.

@@ -1,133 +1,17 @@
-// The torch wrappers of the microscaled operators as a CPython extension: it
-// reads the tensors' properties, allocates the result and calls the C ABI.
-// In Python, with ctypes, that took 3 to 4 us more per call, for a layer that
-// takes 5 us on the GPU.  dense_gemm_major_gb300/__init__.py documents the
+// The torch wrappers of the microscaled operators as a CPython extension around
+// the C ABI (see py_call.h).  dense_gemm_major_gb300/__init__.py documents the
 // functions and gives their defaults.
-//
-// torch itself is only used through its Python objects, handed over once by
-// setup(); nothing of it is linked or included.
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-
-#include <climits>
-#include <cstdint>
+#include "py_call.h"
 
 #include "dense_gemm_mx.h"
 
 namespace {
 
-PyObject *g_empty, *g_raw_stream, *g_current_device, *g_error, *g_tensor_type;   // set by setup()
-PyObject *g_dtype[3], *g_uint8;                               // float32, float16, bfloat16
-PyObject *g_empty_names;                                      // ("dtype", "device")
-PyObject *n_is_cuda, *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_device, *n_index, *n_codes,
-    *n_scales, *n_buffer, *n_rows, *n_cols, *n_fmt, *n_ld, *n_mxfp4, *n_numel, *n_is_contiguous,
-    *n_mx_device;
-
-// An owned reference.
-struct Ref {
-  PyObject* p;
-  explicit Ref(PyObject* o = nullptr) : p(o) {}
-  Ref(const Ref&) = delete;
-  Ref& operator=(const Ref&) = delete;
-  ~Ref() { Py_XDECREF(p); }
-  void set(PyObject* o) {
-    Py_XDECREF(p);
-    p = o;
-  }
-  PyObject* release() {
-    PyObject* o = p;
-    p = nullptr;
-    return o;
-  }
-  explicit operator bool() const { return p != nullptr; }
-};
-
-// A call of the library, which may wait (for a workspace, or for room in a full
-// stream): other Python threads run meanwhile, the callbacks among them that the
-// stream may be waiting for.
-template <typename F>
-gemm_status_t without_gil(F call) {
-  PyThreadState* state = PyEval_SaveThread();
-  const gemm_status_t st = call();
-  PyEval_RestoreThread(state);
-  return st;
-}
-
-bool value_error(const char* text) {
-  PyErr_SetString(PyExc_ValueError, text);
-  return false;
-}
+PyObject *g_tensor_type;   // set by setup()
+PyObject *n_codes, *n_scales, *n_buffer, *n_rows, *n_cols, *n_fmt, *n_ld, *n_mxfp4, *n_numel,
+    *n_is_contiguous, *n_mx_device;
 
 bool too_large() { return value_error("a size is above the formats' limit, 2^31 - 1024"); }
-
-PyObject* failed(gemm_status_t st, const char* what) {
-  Ref e(PyObject_CallFunction(g_error, "is", (int)st, what));
-  if (e) PyErr_SetObject(g_error, e.p);
-  return nullptr;
-}
-
-bool to_int(PyObject* o, int* out) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) return false;
-  if (v < 0 || v > INT_MAX) return value_error("a size or stride is negative or above 2^31 - 1");
-  *out = (int)v;
-  return true;
-}
-
-bool attr_int(PyObject* o, PyObject* name, int* out) {
-  Ref a(PyObject_GetAttr(o, name));
-  return a && to_int(a.p, out);
-}
-
-bool address(PyObject* t, void** out) {
-  Ref a(PyObject_CallMethodNoArgs(t, n_data_ptr));
-  if (!a) return false;
-  *out = PyLong_AsVoidPtr(a.p);
-  return *out != nullptr || !PyErr_Occurred();
-}
-
-bool dtype_code(PyObject* dtype, int* code) {
-  for (int i = 0; i < 3; ++i)
-    if (dtype == g_dtype[i]) {
-      *code = i;
-      return true;
-    }
-  PyErr_Format(PyExc_ValueError, "unsupported dtype %S: float32, float16 or bfloat16", dtype);
-  return false;
-}
-
-// Two ints of a tuple-like (torch.Size and strides are tuples).
-bool pair_of(PyObject* t, int* a, int* b) {
-  if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 2) return value_error("operands must be 2-D");
-  return to_int(PyTuple_GET_ITEM(t, 0), a) && to_int(PyTuple_GET_ITEM(t, 1), b);
-}
-
-// A 2-D CUDA tensor.
-struct Matrix {
-  int code, rows, cols, s0, s1;
-  void* ptr;
-  Ref dtype, device;
-  bool read(PyObject* t) {
-    Ref cuda(PyObject_GetAttr(t, n_is_cuda));
-    if (!cuda) return false;
-    if (cuda.p != Py_True) return value_error("operands must be CUDA tensors");
-    dtype.set(PyObject_GetAttr(t, n_dtype));
-    if (!dtype || !dtype_code(dtype.p, &code)) return false;
-    Ref shape(PyObject_GetAttr(t, n_shape));
-    if (!shape || !pair_of(shape.p, &rows, &cols)) return false;
-    Ref stride(PyObject_CallMethodNoArgs(t, n_stride));
-    if (!stride || !pair_of(stride.p, &s0, &s1)) return false;
-    device.set(PyObject_GetAttr(t, n_device));
-    return device && address(t, &ptr);
-  }
-  // Leading dimension as a row-major array.
-  bool row_major(int* ld) const {
-    if (s1 != 1 && cols > 1)
-      return value_error("operands must be 2-D row-major (unit column stride)");
-    *ld = rows > 1 ? s0 : (cols > 0 ? cols : 1);
-    return true;
-  }
-};
 
 // An MXTensor's arrays, kept alive.  (Its _device is that of the arrays, None
 // where they are not on a GPU.)
@@ -169,94 +53,6 @@ struct Quantized {
     return true;
   }
 };
-
-// Whether two operands' devices are the same.
-bool one_device(PyObject* a, PyObject* b) {
-  const int same = PyObject_RichCompareBool(a, b, Py_EQ);
-  if (same == 0) return value_error("operands must be on one device");
-  return same == 1;
-}
-
-// The given cudaStream_t, or torch's current stream on `device`, which must be
-// the current one: the library's kernels run there.
-bool stream_of(PyObject* stream, PyObject* device, cudaStream_t* out) {
-  Ref s;
-  Ref index(PyObject_GetAttr(device, n_index));
-  if (!index) return false;
-  Ref current(PyObject_CallNoArgs(g_current_device));
-  if (!current) return false;
-  const int same = PyObject_RichCompareBool(index.p, current.p, Py_EQ);
-  if (same < 0) return false;
-  if (!same) return value_error("operands must be on the current CUDA device");
-  if (stream == Py_None) {
-    s.set(PyObject_CallOneArg(g_raw_stream, index.p));
-    if (!s) return false;
-  } else {
-    Py_INCREF(stream);
-    s.set(stream);
-  }
-  *out = (cudaStream_t)PyLong_AsVoidPtr(s.p);
-  return *out != nullptr || !PyErr_Occurred();
-}
-
-PyObject* empty(PyObject* size, PyObject* dtype, PyObject* device) {
-  PyObject* args[3] = {size, dtype, device};
-  return PyObject_Vectorcall(g_empty, args, 1, g_empty_names);
-}
-
-// `out`, checked, or a new rows x cols tensor.
-struct Result {
-  Ref tensor;
-  int ld;
-  void* ptr;
-  bool make(PyObject* out, int rows, int cols, PyObject* dtype, PyObject* device, double beta) {
-    if (out == Py_None) {
-      if (beta != 0.0) return value_error("beta != 0 needs an existing out");
-      Ref size(Py_BuildValue("(ii)", rows, cols));
-      if (!size) return false;
-      tensor.set(empty(size.p, dtype, device));
-      ld = cols > 0 ? cols : 1;
-      return tensor && address(tensor.p, &ptr);
-    }
-    Matrix m;
-    if (!m.read(out)) return false;
-    const int same = PyObject_RichCompareBool(m.device.p, device, Py_EQ);
-    if (same < 0) return false;
-    if (m.rows != rows || m.cols != cols || m.dtype.p != dtype || !same)
-      return value_error("out has the wrong shape, dtype or device");
-    Py_INCREF(out);
-    tensor.set(out);
-    ptr = m.ptr;
-    return m.row_major(&ld);
-  }
-};
-
-// The dtype asked for, that of `out`, or `otherwise` (a new reference).
-PyObject* result_dtype(PyObject* dtype, PyObject* out, PyObject* otherwise) {
-  if (dtype == Py_None && out != Py_None) return PyObject_GetAttr(out, n_dtype);
-  PyObject* d = dtype == Py_None ? otherwise : dtype;
-  Py_INCREF(d);
-  return d;
-}
-
-bool same_inner(int a, int b) {
-  if (a == b) return true;
-  PyErr_Format(PyExc_ValueError, "inner dimensions differ: %d vs %d", a, b);
-  return false;
-}
-
-bool two_doubles(PyObject* a, PyObject* b, double* x, double* y) {
-  *x = PyFloat_AsDouble(a);
-  if (*x == -1.0 && PyErr_Occurred()) return false;
-  *y = PyFloat_AsDouble(b);
-  return *y != -1.0 || !PyErr_Occurred();
-}
-
-bool arity(Py_ssize_t n, Py_ssize_t want) {
-  if (n == want && g_empty != nullptr) return true;
-  PyErr_SetString(PyExc_TypeError, "wrong number of arguments, or setup() was not called");
-  return false;
-}
 
 // quantize(X, fmt, stream) -> (buffer, rows, cols, pitch of the codes, device)
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -452,33 +248,14 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "setup(torch, MXTensor, GemmError)");
     return nullptr;
   }
-  struct {
-    PyObject** to;
-    const char* name;
-  } names[] = {{&n_is_cuda, "is_cuda"}, {&n_dtype, "dtype"},   {&n_shape, "shape"},
-               {&n_stride, "stride"},   {&n_data_ptr, "data_ptr"}, {&n_device, "device"},
-               {&n_index, "index"},     {&n_codes, "_codes"},  {&n_scales, "_scales"},
-               {&n_buffer, "_buffer"},  {&n_rows, "rows"},     {&n_cols, "cols"},
-               {&n_fmt, "fmt"},         {&n_ld, "_ld"},        {&n_mxfp4, "mxfp4"},
-               {&n_numel, "numel"},     {&n_is_contiguous, "is_contiguous"},
-               {&n_mx_device, "_device"}};
-  for (auto& x : names)
-    if (*x.to == nullptr && (*x.to = PyUnicode_InternFromString(x.name)) == nullptr)
-      return nullptr;
-  const char* types[3] = {"float32", "float16", "bfloat16"};
-  for (int i = 0; i < 3; ++i)
-    if ((g_dtype[i] = PyObject_GetAttrString(a[0], types[i])) == nullptr) return nullptr;
-  if ((g_uint8 = PyObject_GetAttrString(a[0], "uint8")) == nullptr) return nullptr;
-  Ref c(PyObject_GetAttrString(a[0], "_C"));
-  if (!c || (g_raw_stream = PyObject_GetAttrString(c.p, "_cuda_getCurrentRawStream")) == nullptr ||
-      (g_current_device = PyObject_GetAttrString(c.p, "_cuda_getDevice")) == nullptr)
-    return nullptr;
-  if ((g_empty_names = Py_BuildValue("(OO)", n_dtype, n_device)) == nullptr) return nullptr;
+  const Name names[] = {{&n_codes, "_codes"}, {&n_scales, "_scales"}, {&n_buffer, "_buffer"},
+                        {&n_rows, "rows"},    {&n_cols, "cols"},      {&n_fmt, "fmt"},
+                        {&n_ld, "_ld"},       {&n_mxfp4, "mxfp4"},    {&n_numel, "numel"},
+                        {&n_is_contiguous, "is_contiguous"},
+                        {&n_mx_device, "_device"}, {nullptr, nullptr}};
   Py_INCREF(a[1]);
   g_tensor_type = a[1];
-  Py_INCREF(a[2]);
-  g_error = a[2];
-  if ((g_empty = PyObject_GetAttrString(a[0], "empty")) == nullptr) return nullptr;
+  if (!setup_common(a[0], a[2], names)) return nullptr;
   Py_RETURN_NONE;
 }
 

@@ -321,6 +321,7 @@ enum FaultCode : unsigned {
   kFaultTcPairTmem = 1u << 6,   // the two CTAs of a pair got different TMEM bases
   kFaultTcPartialWait = 1u << 7,   // a K-split piece's partial never arrived
   kFaultSgemmPieceWait = 1u << 8,  // an SGEMM stream-K piece's partner never published
+  kFaultGroupOffsets = 1u << 9,    // offsets of groups that decrease or leave 0 .. rows
 };
 
 __device__ __forceinline__ void raise_fault(unsigned* fault, unsigned code) {

@@ -1,0 +1,83 @@
+/*
+ * dense_gemm_group.h -- products grouped by expert for the GB300 dense GEMM
+ * library: the forward product, and both products of the backward pass, of
+ * layers whose rows go to one of several weight matrices each.
+ *
+ * Rows are sorted by group.  `offsets` is a device array of groups + 1 32-bit
+ * integers: group g's rows are offsets[g] .. offsets[g + 1] - 1, of `rows`
+ * rows in all.  It is read when the work runs, not when it is queued, so that a
+ * router's kernel may have written it and a captured graph may be replayed with
+ * other groups.  Groups may be empty; rows before offsets[0] and from
+ * offsets[groups] on belong to none, and nothing of them is read into a result or
+ * written.  Offsets that decrease or leave 0 .. rows are moved to the nearest
+ * that do not (an offset below an earlier one to that one), and set bit 9 of the
+ * device fault word (gemm_device_check).
+ *
+ * dtype codes are those of gemm_plan: 1 = FP16, 2 = BF16 (0 = FP32 for dtype_c).
+ * Operands are of dtype, results of dtype_c: that, or FP32.  FP32 accumulation; one
+ * rounding.  (The tensor cores truncate the running sum at each step of 16 terms.
+ * FP32 results are sums, rounded to nearest, of parts of at most 1024 terms, 16-bit
+ * ones of parts of 16384.)
+ *
+ * Pointers, streams, errors and the device fault word follow dense_gemm.h:
+ * argument problems are reported synchronously before anything is queued, work is
+ * queued on `stream`, and every device-side wait is bounded.  Inputs must not
+ * overlap outputs.  Sizes are at most GEMM_GROUP_MAX_SIZE, groups at most
+ * GEMM_GROUP_MAX_GROUPS.
+ *
+ * Alignment: an operand is 16-byte aligned with leading dimension (and distance
+ * between groups) a multiple of 8, or packed (the leading dimension its stored
+ * width, groups directly behind one another) at any alignment of its type, which
+ * takes a copy with aligned rows in a workspace first; else
+ * GEMM_ERR_MISALIGNED.  C has any alignment of its type.
+ *
+ * Device memory: only such copies take any, in the workspace of operand copies:
+ * one per (device, stream), under the rules of dense_gemm.h (replaced by a larger
+ * one when a call needs more, never freed, shared by the graphs captured on the
+ * stream, whose replays must not overlap).  Before a stream capture that needs
+ * it, make one call of the same sizes on that stream.
+ */
+#ifndef DENSE_GEMM_GROUP_H_
+#define DENSE_GEMM_GROUP_H_
+
+#include "dense_gemm.h"
+
+#if defined(__cplusplus)
+extern "C" {
+#endif
+
+#define GEMM_GROUP_MAX_GROUPS 1024
+#define GEMM_GROUP_MAX_SIZE (2147483647 - 1023)   /* 2^31 - 1024 */
+
+/*
+ * C[i] := alpha * A[i] . op(B[g]) + beta * C[i] for the rows i of each group g.
+ * A is rows x K, C rows x N.  B: groups matrices, stride_b elements apart, K x N
+ * (op_b == GEMM_OP_N, ldb >= N) or stored N x K (GEMM_OP_T, ldb >= K), one
+ * directly behind the other or with room between them; stride_b == 0: one matrix
+ * for all groups.
+ *   forward product:               A = X,  B = W (out x in) as GEMM_OP_T
+ *   gradient of a layer's input:   A = dY, B = W as GEMM_OP_N
+ * K == 0 or alpha == 0: C := beta * C on the groups' rows (A and B not read);
+ * beta == 0: C is not read.
+ */
+gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int N, int K,
+                           int groups, float alpha, const void *A, int lda, const void *B, int ldb,
+                           long long stride_b, const int *offsets, float beta, void *C, int ldc,
+                           cudaStream_t stream);
+
+/*
+ * C[g] := alpha * A[rows of g]^T . X[rows of g] + beta * C[g] for every group g: A
+ * is rows x M, X rows x N, C[g] (M x N, ldc >= N) at C + g * stride_c.  The
+ * gradient of a layer's weights (out x in): A = dY, X the layer's input.  An empty
+ * group's C[g] becomes beta * C[g]; beta == 0: C is not read.
+ */
+gemm_status_t gemm_grouped_grad(int dtype, int dtype_c, int rows, int M, int N, int groups,
+                                float alpha, const void *A, int lda, const void *X, int ldx,
+                                const int *offsets, float beta, void *C, int ldc,
+                                long long stride_c, cudaStream_t stream);
+
+#if defined(__cplusplus)
+}
+#endif
+
+#endif /* DENSE_GEMM_GROUP_H_ */
