@@ -4,10 +4,11 @@ The binding only marshals arguments: every step of the GEMM runs in the
 CUDA library ``libdense_gemm.so`` (built in-tree by ``_build.build()``),
 whose C ABI is declared in ``include/dense_gemm.h``, (microscaled
 operands) ``include/dense_gemm_mx.h`` and (products grouped by expert)
-``include/dense_gemm_group.h``.  The functions of the same names as
+``include/dense_gemm_group.h`` and (4-bit weights with group scales)
+``include/dense_gemm_q4.h``.  The functions of the same names as
 the C entry points take integers (device addresses, sizes, a
-``cudaStream_t`` value); ``matmul``, the ``mx_*`` and the ``grouped_*``
-functions are convenience wrappers for torch tensors on the current device and stream.
+``cudaStream_t`` value); ``matmul``, the ``mx_*``, the ``grouped_*`` functions
+and ``q4_linear`` are convenience wrappers for torch tensors on the current device and stream.
 There is no fallback: if the library is missing the calls raise.
 """
 from __future__ import annotations
@@ -40,7 +41,7 @@ EXPORTED = ("gemm_f32", "gemm_f16", "gemm_bf16", "gemm_status_string", "gemm_dev
             "gemm_probe_ffma_threads",
             "gemm_mx_code_ld", "gemm_mx_scale_bytes", "gemm_mx_quantize", "gemm_mx_dequantize",
             "gemm_mx4", "gemm_mx4_linear", "gemm_mx_grad",
-            "gemm_grouped", "gemm_grouped_grad")
+            "gemm_grouped", "gemm_grouped_grad", "gemm_q4_linear")
 
 # Microscaled formats (gemm_mx_format_t).
 MXFP4, MXINT8 = 0, 1
@@ -153,6 +154,8 @@ def load() -> ctypes.CDLL:
     lib.gemm_grouped.argtypes = [i, i, i, i, i, i, i, f, vp, i, vp, i, ll, vp, f, vp, i, vp]
     lib.gemm_grouped_grad.restype = i
     lib.gemm_grouped_grad.argtypes = [i, i, i, i, i, i, f, vp, i, vp, i, vp, f, vp, i, ll, vp]
+    lib.gemm_q4_linear.restype = i
+    lib.gemm_q4_linear.argtypes = [i, i, i, i, i, i, vp, i, vp, i, vp, vp, vp, vp, i, vp]
     _lib = lib
     return lib
 
@@ -391,6 +394,13 @@ def gemm_grouped_grad(dtype, dtype_c, rows, M, N, groups, alpha, A, lda, X, ldx,
                                     offsets, beta, C, ldc, stride_c, stream)
 
 
+def gemm_q4_linear(dtype, group, rows, N, K, experts, X, ldx, codes, ldq, scales, zeros, offsets,
+                   Y, ldy, stream=0) -> int:
+    code = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    return load().gemm_q4_linear(code, group, rows, N, K, experts, X, ldx, codes, ldq, scales,
+                                 zeros, offsets, Y, ldy, stream)
+
+
 # ------------------------------------------------------------ torch wrapper
 
 def _torch_dtype_code(t):
@@ -623,7 +633,7 @@ def _load_group():
         load()
         import torch
         from . import _groupcall as ext
-        ext.setup(torch, GemmError)
+        ext.setup(torch, Q4Tensor, GemmError)
         _group = ext
     return _group
 
@@ -654,3 +664,80 @@ def grouped_grad(A, X, offsets, out=None, dtype=None, alpha=1.0, beta=0.0, strea
     if stream is not None and out is None:
         return _on_stream(stream, lambda: grouped_grad(A, X, offsets, None, dtype, alpha, beta))
     return (_group or _load_group()).grouped_grad(A, X, offsets, out, dtype, alpha, beta, stream)
+
+
+# ------------------------------------------------------------ 4-bit weights with group scales
+
+class Q4Tensor:
+    """Weights (out x in, or experts x out x in) held in 4 bits with a scale for
+    each ``group`` of them along a row (a multiple of 32), as
+    include/dense_gemm_q4.h describes:  value = scale * (code - zero).
+
+    codes   uint8, (experts x) out x pitch, columns 2j and 2j + 1 in the low and
+            high half of byte j; the pitch a multiple of 16 bytes, experts one
+            behind the other
+    scales  float16 or bfloat16, contiguous (experts x) out x ceil(cols / group)
+    zeros   uint8 of the scales' shape, 0 .. 15, contiguous; None: 8 for all
+    cols    columns (default: two for each byte of codes)"""
+    __slots__ = ("codes", "scales", "zeros", "experts", "rows", "cols", "group", "_ld")
+
+    def __init__(self, codes, scales, zeros=None, cols=None, group=128):
+        import torch
+        if codes.dim() not in (2, 3) or codes.dtype != torch.uint8 or not codes.is_cuda:
+            raise ValueError("codes must be a 2-D or 3-D uint8 CUDA tensor")
+        lead, width = codes.shape[:-1], codes.shape[-1]
+        cols = 2 * width if cols is None else int(cols)
+        group = int(group)
+        if group < 32 or group % 32 or group > 2 ** 31 - 32:
+            raise ValueError("group must be a multiple of 32")
+        if cols < 0 or (cols + 1) // 2 > width:
+            raise ValueError("codes have fewer columns than cols")
+        if codes.dim() == 3 and not 1 <= lead[0] <= 1024:
+            raise ValueError("1 to 1024 experts")
+        rows = lead[-1]
+        ld = codes.stride(-2) if rows > 1 else -(-width // 16) * 16
+        if codes.dim() == 3 and lead[0] > 1:
+            if rows <= 1:
+                ld = codes.stride(0)
+            if codes.stride(0) != rows * ld:
+                raise ValueError("experts' codes must follow one another")
+        if (width > 1 and codes.stride(-1) != 1) or ld < (cols + 1) // 2:
+            raise ValueError("codes' rows must be contiguous and not overlap")
+        if ld % 16 or codes.data_ptr() % 16:
+            raise ValueError("codes need 16-byte aligned rows")
+        shape = (*lead, -(-cols // group))
+        if (scales.dtype not in (torch.float16, torch.bfloat16) or tuple(scales.shape) != shape
+                or not scales.is_contiguous() or scales.device != codes.device):
+            raise ValueError(f"scales must be contiguous float16 or bfloat16 of shape {shape} "
+                             "on the codes' device")
+        if zeros is not None and (zeros.dtype != torch.uint8 or tuple(zeros.shape) != shape
+                                  or not zeros.is_contiguous() or zeros.device != codes.device):
+            raise ValueError(f"zeros must be contiguous uint8 of shape {shape} on the codes' device")
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.experts = lead[0] if codes.dim() == 3 else 0
+        self.rows, self.cols, self.group, self._ld = rows, cols, group, ld
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def record_stream(self, stream):
+        """Tensor.record_stream of the codes, scales and zeros."""
+        for t in (self.codes, self.scales, self.zeros):
+            if t is not None:
+                t.record_stream(stream)
+
+
+def q4_linear(x, W, offsets=None, out=None, stream=None):
+    """x @ W.T with x (rows x in; float16 or bfloat16, row-major) and W a Q4Tensor
+    whose scales have x's dtype, which the result has too.  Weights of experts
+    take ``offsets``, as grouped_matmul does: the rows of expert g are multiplied
+    with its matrix, and rows of no expert are not written.  x has rows of a
+    multiple of 16 bytes, or is contiguous (copied to aligned rows first)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, lambda: q4_linear(x, W, offsets))
+    return (_group or _load_group()).q4_linear(x, W, offsets, out, stream)

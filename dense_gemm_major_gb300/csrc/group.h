@@ -24,11 +24,12 @@ constexpr int kGroupMaxGroups = GEMM_GROUP_MAX_GROUPS;
 struct GroupParams {
   int kind;
   int rows, groups;
+  int first_group = 0;      // of those that offsets has; C and B are from it on
   // Products: C is rows x N, terms of the sums K.  Weights: C[g] is M x N (A's
   // columns x X's), the sums run over the group's rows (K == 0: without terms).
   int M, N, K;
   int per_group;            // weights: tiles of a C[g]
-  const int* offsets;
+  const int* offsets;       // null (groups 1): all rows are one group's
   int zmul;                 // 0: one B for all groups
   int seg;                  // k-tiles summed in tensor memory at a time
   float alpha, beta;

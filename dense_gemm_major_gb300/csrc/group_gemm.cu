@@ -114,9 +114,11 @@ __device__ __forceinline__ int group_table(const GroupParams& p, int* start, int
   const int tiles_n = (p.N + kGroupTile - 1) / kGroupTile;
   int last = 0, units = 0;
   bool bad = false;
-  for (int base = 0; base <= p.groups; base += 32) {
+  const int end = p.first_group + p.groups;
+  for (int base = 0; base <= end; base += 32) {
     const int i = base + lane;
-    const int raw = i <= p.groups ? p.offsets[i] : p.rows;
+    const int raw = p.offsets == nullptr ? (i == 0 ? 0 : p.rows)
+                                         : (i <= end ? p.offsets[i] : p.rows);
     int v = min(max(raw, 0), p.rows);
     const int own = v;
 #pragma unroll
@@ -129,7 +131,7 @@ __device__ __forceinline__ int group_table(const GroupParams& p, int* start, int
     int before = __shfl_up_sync(0xffffffffu, v, 1);
     if (lane == 0) before = last;
     // Units of group i - 1, whose end this lane has.
-    int n = i >= 1 && i <= p.groups
+    int n = i > p.first_group && i <= end
                 ? (int)((long long)((v - before + kGroupTile - 1) / kGroupTile) * tiles_n)
                 : 0;
 #pragma unroll
@@ -137,9 +139,9 @@ __device__ __forceinline__ int group_table(const GroupParams& p, int* start, int
       const int o = __shfl_up_sync(0xffffffffu, n, d);
       if (lane >= d) n += o;
     }
-    if (i <= p.groups) {
-      start[i] = v;
-      unit0[i] = units + n;
+    if (i >= p.first_group && i <= end) {
+      start[i - p.first_group] = v;
+      unit0[i - p.first_group] = units + n;
     }
     units += __shfl_sync(0xffffffffu, n, 31);
     last = __shfl_sync(0xffffffffu, v, 31);

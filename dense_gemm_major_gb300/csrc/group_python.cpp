@@ -1,13 +1,15 @@
-// The torch wrappers of the grouped products as a CPython extension around the C
-// ABI (see py_call.h).  dense_gemm_major_gb300/__init__.py documents the
+// The torch wrappers of the grouped products and of those with 4-bit weights as a
+// CPython extension around the C ABI (see py_call.h).  dense_gemm_major_gb300/__init__.py documents the
 // functions and gives their defaults.
 #include "py_call.h"
 
 #include "dense_gemm_group.h"
+#include "dense_gemm_q4.h"
 
 namespace {
 
-PyObject* g_int32;   // set by setup()
+PyObject *g_int32, *g_q4_type;   // set by setup()
+PyObject *n_codes, *n_scales, *n_zeros, *n_experts, *n_rows, *n_cols, *n_group, *n_ld;
 
 // A 3-D CUDA tensor: matrices of rows x cols.
 struct Matrices {
@@ -187,21 +189,71 @@ PyObject* grouped_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return out.release();
 }
 
-// setup(torch, GemmError)
+// q4_linear(x, W, offsets, out, stream)
+PyObject* q4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 5)) return nullptr;
+  Matrix x;
+  int ldx, experts, rows, cols, group, ldq;
+  if (!x.read(a[0]) || !row_major16(x, &ldx)) return nullptr;
+  PyObject* const w = a[1];
+  if (!PyObject_TypeCheck(w, (PyTypeObject*)g_q4_type))
+    return value_error("the weights must be a Q4Tensor"), nullptr;
+  if (!attr_int(w, n_experts, &experts) || !attr_int(w, n_rows, &rows) ||
+      !attr_int(w, n_cols, &cols) || !attr_int(w, n_group, &group) || !attr_int(w, n_ld, &ldq))
+    return nullptr;
+  Ref codes(PyObject_GetAttr(w, n_codes)), scales(PyObject_GetAttr(w, n_scales)),
+      zeros(PyObject_GetAttr(w, n_zeros));
+  if (!codes || !scales || !zeros) return nullptr;
+  Ref device(PyObject_GetAttr(codes.p, n_device)), type(PyObject_GetAttr(scales.p, n_dtype));
+  if (!device || !type) return nullptr;
+  if (type.p != x.dtype.p) return value_error("x and the scales must have the same dtype"), nullptr;
+  if (!one_device(x.device.p, device.p) || !same_inner(x.cols, cols)) return nullptr;
+  Offsets off{0, nullptr};
+  if (experts > 0) {
+    if (a[2] == Py_None) return value_error("weights of experts need offsets"), nullptr;
+    if (!off.read(a[2], x.device.p)) return nullptr;
+    if (off.groups != experts)
+      return value_error("offsets must have one element more than there are experts"), nullptr;
+  } else if (a[2] != Py_None) {
+    return value_error("offsets are for weights of experts (3-D codes)"), nullptr;
+  }
+  void *qp, *sp, *zp = nullptr;
+  if (!address(codes.p, &qp) || !address(scales.p, &sp) ||
+      (zeros.p != Py_None && !address(zeros.p, &zp)))
+    return nullptr;
+  Result y;
+  cudaStream_t stream;
+  if (!stream_of(a[4], x.device.p, &stream) ||
+      !y.make(a[3], x.rows, rows, x.dtype.p, x.device.p, 0.0))
+    return nullptr;
+  const gemm_status_t st = without_gil([&] {
+    return gemm_q4_linear(x.code, group, x.rows, rows, x.cols, experts, x.ptr, ldx, qp, ldq, sp,
+                          zp, (const int*)off.ptr, y.ptr, y.ld, stream);
+  });
+  if (st != GEMM_OK) return failed(st, "gemm_q4_linear");
+  return y.tensor.release();
+}
+
+// setup(torch, Q4Tensor, GemmError)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 2) {
-    PyErr_SetString(PyExc_TypeError, "setup(torch, GemmError)");
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "setup(torch, Q4Tensor, GemmError)");
     return nullptr;
   }
-  const Name names[] = {{nullptr, nullptr}};
+  const Name names[] = {{&n_codes, "codes"}, {&n_scales, "scales"}, {&n_zeros, "zeros"},
+                        {&n_experts, "experts"}, {&n_rows, "rows"}, {&n_cols, "cols"},
+                        {&n_group, "group"}, {&n_ld, "_ld"}, {nullptr, nullptr}};
+  Py_INCREF(a[1]);
+  g_q4_type = a[1];
   if ((g_int32 = PyObject_GetAttrString(a[0], "int32")) == nullptr ||
-      !setup_common(a[0], a[1], names))
+      !setup_common(a[0], a[2], names))
     return nullptr;
   Py_RETURN_NONE;
 }
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(setup), METHOD(grouped_matmul), METHOD(grouped_grad),
+                           METHOD(q4_linear),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_groupcall", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

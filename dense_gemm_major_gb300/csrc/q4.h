@@ -1,0 +1,49 @@
+// Internal interface of the products with 4-bit weights and group scales: the
+// kernels' launch functions, called by q4_api.cu.  Callers use
+// include/dense_gemm_q4.h.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "dense_gemm_q4.h"
+#include "launch.h"
+
+namespace dgemm {
+
+// Few rows: a CTA computes 64 columns of Y (rows of W) for up to 64 rows of one
+// expert, over its share of K.
+constexpr int kQ4TileN = 64;
+constexpr int kQ4BK = 512;
+constexpr int kQ4MaxRows = 64;
+struct Q4FewParams {
+  int rows, N, K, group;
+  int experts;              // 0: one matrix for all rows
+  const int* offsets;
+  int tile_rows;            // rows of Y per CTA: a multiple of 8, at most 64
+  int slots;                // upper bound of tiles of rows
+  int split;                // CTAs (a cluster) that share a tile's K
+  const void* scales;
+  const unsigned char* zeros;
+  void* Y;
+  long long ldy;
+  unsigned* fault;
+  unsigned long long timeout_ns;
+};
+// Rows per CTA for the rows (of an expert) to expect.
+inline int q4_tile_rows(int rows) {
+  return rows <= 32 ? (rows + 7) / 8 * 8 : (rows <= 48 ? 48 : 64);
+}
+// tmQ: the codes as bytes {ceil(K / 2), N, experts} with boxes of 128 x 64 x 1; tmX: X
+// as {K, rows} with boxes of 64 x tile_rows.
+cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
+                          const CUtensorMap* tmX, cudaStream_t stream);
+
+// D (rows x K of dtype, pitch ldd, a multiple of 8) := the weights.  With offsets,
+// row r is of expert r / N, and those without rows are left out.
+cudaError_t launch_q4_values(int dtype, int group, long long rows, int N, int K,
+                             const unsigned char* codes, int ldq, const void* scales,
+                             const unsigned char* zeros, const int* offsets, void* D,
+                             long long ldd, cudaStream_t stream);
+
+}  // namespace dgemm

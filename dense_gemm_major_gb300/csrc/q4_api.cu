@@ -1,0 +1,160 @@
+// C-ABI entry point of the products with 4-bit weights and group scales: argument
+// checks, choice between the kernel for few rows and a product with the weights in
+// 16 bits, launch.  See include/dense_gemm_q4.h.
+#include <cstdint>
+#include <cstdlib>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "group.h"
+#include "group_operands.h"
+#include "q4.h"
+#include "workspace.h"
+
+namespace {
+
+using namespace dgemm::api;
+
+inline bool good_size(int n) { return n >= 0 && n <= GEMM_GROUP_MAX_SIZE; }
+
+struct Q4Call {
+  int dtype, group, rows, N, K, experts;
+  Operand x;
+  const unsigned char* codes;
+  int ldq;
+  const void* scales;
+  const unsigned char* zeros;
+  const int* offsets;
+  void* Y;
+  int ldy;
+  unsigned* fault;
+  int pairs;
+  int matrices() const { return experts == 0 ? 1 : experts; }
+};
+
+// The product by the kernel for few rows; `expect`: rows of an expert to expect.
+gemm_status_t run_few(const Q4Call& c, int expect, cudaStream_t stream) {
+  dgemm::Q4FewParams p;
+  p.rows = c.rows, p.N = c.N, p.K = c.K, p.group = c.group;
+  p.experts = c.experts, p.offsets = c.offsets;
+  p.tile_rows = dgemm::q4_tile_rows(expect);
+  p.slots = c.experts == 0 ? ceil_div(c.rows, p.tile_rows)
+                           : c.rows / p.tile_rows + (c.experts < c.rows ? c.experts : c.rows);
+  // CTAs that share a tile's K: as many (a cluster of at most 8) as keep one wave,
+  // each with a stage at least.
+  const long long tiles = (long long)ceil_div(c.N, dgemm::kQ4TileN) * p.slots;
+  const int nk = ceil_div(c.K, dgemm::kQ4BK);
+  const int room = 2 * c.pairs * (p.tile_rows <= 16 ? 2 : 1);
+  p.split = 1;
+  while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= room) p.split *= 2;
+  p.scales = c.scales, p.zeros = c.zeros;
+  p.Y = c.Y, p.ldy = c.ldy;
+  p.fault = c.fault, p.timeout_ns = dgemm::wait_bound_ns();
+  alignas(64) CUtensorMap tmQ, tmX;
+  const cuuint64_t dims[3] = {(cuuint64_t)((c.K + 1ll) / 2), (cuuint64_t)c.N,
+                              (cuuint64_t)c.matrices()};
+  const cuuint64_t strides[2] = {(cuuint64_t)c.ldq, (cuuint64_t)c.N * c.ldq};
+  const cuuint32_t box[3] = {128, dgemm::kQ4TileN, 1};
+  if (!encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, box) ||
+      !encode_rows(&tmX, c.dtype, c.x, (uint32_t)p.tile_rows))
+    return GEMM_ERR_LAUNCH;
+  return status_of(dgemm::launch_q4_few(c.dtype, p, &tmQ, &tmX, stream));
+}
+
+// The product with the weights in 16 bits, in parts of them that fit the workspace:
+// some experts, or some columns of Y.
+gemm_status_t run_values(const Q4Call& c, dgemm::StreamWorkspaces& workspaces,
+                         cudaStream_t stream) {
+  const long long ldd = ((long long)c.K + 7) / 8 * 8, groups = ceil_div(c.K, c.group);
+  long long fit = GEMM_Q4_WORKSPACE / (ldd * 2);       // rows of W
+  if (fit < 1) fit = 1;
+  const bool whole = fit >= c.N;                        // matrices at a time, or parts of one
+  const int part = whole ? c.N : (int)(fit >= 256 ? fit / 256 * 256 : fit);
+  int together = whole ? (int)(fit / c.N < c.matrices() ? fit / c.N : c.matrices()) : 1;
+  void* d = nullptr;
+  gemm_status_t st =
+      workspaces.get(dgemm::kWsValues, (size_t)together * part * ldd * 2, &d);
+  if (st != GEMM_OK) return st;
+  dgemm::GroupParams p;
+  p.kind = dgemm::kGroupForward;
+  p.rows = c.rows, p.M = 0, p.K = c.K, p.per_group = 0;
+  p.zmul = 1;
+  p.seg = segment(c.dtype);
+  p.alpha = 1.f, p.beta = 0.f;
+  p.ldc = c.ldy, p.stride_c = 0;
+  p.fault = c.fault, p.timeout_ns = dgemm::wait_bound_ns();
+  alignas(64) CUtensorMap tmM, tmN, tmN16;
+  if (!encode_rows(&tmN, c.dtype, c.x, 128) || !encode_rows(&tmN16, c.dtype, c.x, 16))
+    return GEMM_ERR_LAUNCH;
+  for (int e = 0; e < c.matrices(); e += together) {
+    const int n = c.matrices() - e < together ? c.matrices() - e : together;
+    for (int n0 = 0; n0 < c.N; n0 += part) {
+      const int cols = c.N - n0 < part ? c.N - n0 : part;
+      const long long row = (long long)e * c.N + n0;    // of all codes
+      st = status_of(dgemm::launch_q4_values(
+          c.dtype, c.group, (long long)n * cols, cols, c.K, c.codes + row * c.ldq, c.ldq,
+          static_cast<const char*>(c.scales) + row * groups * 2,
+          c.zeros == nullptr ? nullptr : c.zeros + row * groups,
+          c.offsets == nullptr ? nullptr : c.offsets + e, d, ldd, stream));
+      if (st != GEMM_OK) return st;
+      const Operand w{d, c.K, cols, ldd, n, (long long)cols * ldd, false};
+      if (!encode_matrices(&tmM, c.dtype, w)) return GEMM_ERR_LAUNCH;
+      p.groups = n, p.first_group = e, p.N = cols, p.offsets = c.offsets;
+      p.C = static_cast<char*>(c.Y) + (long long)n0 * 2;
+      const long long most = ((long long)c.rows / dgemm::kGroupTile + (n < c.rows ? n : c.rows)) *
+                             ceil_div(cols, dgemm::kGroupTile);
+      st = status_of(dgemm::launch_group(c.dtype, c.dtype, p, &tmM, &tmN, &tmN16,
+                                         (int)(most < c.pairs ? most : c.pairs), stream));
+      if (st != GEMM_OK) return st;
+    }
+  }
+  return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, int K, int experts,
+                                        const void* X, int ldx, const void* codes, int ldq,
+                                        const void* scales, const void* zeros,
+                                        const int* offsets, void* Y, int ldy,
+                                        cudaStream_t stream) {
+  if ((dtype != 1 && dtype != 2) || group < 32 || group % 32 != 0 || !good_size(rows) ||
+      !good_size(N) || !good_size(K) || experts < 0 || experts > GEMM_GROUP_MAX_GROUPS ||
+      (experts == 0) != (offsets == nullptr))
+    return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 || N == 0) return GEMM_OK;
+  if (Y == nullptr || ldy < N) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(Y, 2) || !aligned(offsets, 4)) return GEMM_ERR_MISALIGNED;
+  Q4Call c{dtype, group, rows, N, K, experts, Operand{X, K, rows, ldx, 1, 0, false},
+           static_cast<const unsigned char*>(codes), ldq, scales,
+           static_cast<const unsigned char*>(zeros), offsets, Y, ldy, nullptr, 0};
+  const uint64_t ys = span(rows, (long long)N * 2, (long long)ldy * 2);
+  gemm_status_t st;
+  if (overlap(Y, ys, offsets, offsets == nullptr ? 0 : (uint64_t)(experts + 1) * 4))
+    return GEMM_ERR_INVALID_ARG;
+  if (K > 0) {
+    if (codes == nullptr || scales == nullptr || ldq < (K + 1ll) / 2) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || ldq % 16 != 0 || !aligned(scales, 2)) return GEMM_ERR_MISALIGNED;
+    if ((st = c.x.check()) != GEMM_OK) return st;
+    const long long all = (long long)c.matrices() * N, g = ceil_div(K, group);
+    if (overlap(Y, ys, X, c.x.bytes()) ||
+        overlap(Y, ys, codes, span(all, (K + 1ll) / 2, ldq)) ||
+        overlap(Y, ys, scales, (uint64_t)(all * g * 2)) ||
+        overlap(Y, ys, zeros, (uint64_t)(all * g)))
+      return GEMM_ERR_INVALID_ARG;
+  } else {
+    // No terms: the groups' rows become zeros.
+    if (experts != 0)
+      return gemm_grouped(dtype, GEMM_OP_T, dtype, rows, N, 0, experts, 1.f, nullptr, 0, nullptr,
+                          0, 0, offsets, 0.f, Y, ldy, stream);
+  }
+  if ((st = dgemm::current_device_pairs(&c.fault, &c.pairs)) != GEMM_OK) return st;
+  if (K == 0) return status_of(dgemm::launch_scale_c(Y, rows, N, ldy, dtype, 0.f, stream));
+  dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
+  Operand none{nullptr, 0, 0, 0, 1, 0, false};
+  if ((st = align_operands(c.x, none, workspaces, stream)) != GEMM_OK) return st;
+  const int expect = experts == 0 ? rows : ceil_div(rows, experts);
+  static const int few_rows = [] { const char* s = getenv("Q4_FEW"); return s ? atoi(s) : 128; }();
+  return expect <= few_rows ? run_few(c, expect, stream) : run_values(c, workspaces, stream);
+}

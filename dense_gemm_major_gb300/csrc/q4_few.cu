@@ -1,0 +1,481 @@
+// Products of a few rows with 4-bit weights and group scales: Y = X . W^T,
+// W[n][k] = s[n][k / group] (q[n][k] - z[n][k / group]).
+//
+// Bound by reading the codes, half a byte a weight.  A CTA takes 64 rows of W and a
+// share of K; its 8 warps are 2 groups of 32 rows x 4 ranges of a stage's K, and
+// multiply with mma.sync.m16n8k16: W's rows on the 16-wide side, X's on the 8-wide
+// one.  The integers q - z are exact in 16 bits; each group's sum is kept apart in
+// FP32 and scaled once, so that no product is rounded.  (The tensor cores of
+// tcgen05 would want the 16-bit values in shared memory, four times the bytes that
+// came in, for rows that fill 1/16 of their tile.)
+//
+// Codes and X come by TMA into a ring.  The sum's order is free as long as both
+// operands have it: a thread's word of eight codes is taken apart as the pairs (0,
+// 4), (1, 5), (2, 6), (3, 7), one mask and shift each, and X's eight values are
+// permuted the same way.  The four ranges of K and then the CTAs of the cluster are
+// added in their order.
+#include "mx.cuh"
+#include "q4.h"
+
+namespace dgemm {
+namespace {
+
+constexpr int kWarpsN = 2, kWarpsK = 4, kWarps = kWarpsN * kWarpsK;
+constexpr int kThreads = 32 * (kWarps + 1);               // and one that loads
+constexpr int kSliceK = kQ4BK / kWarpsK;                   // of a stage, per warp: 128
+constexpr uint32_t kCodeBox = 128 * kQ4TileN;              // 256 codes of each row: 8 KB
+constexpr int kCodeBoxes = kQ4BK / 256, kXBoxes = kQ4BK / 64;
+static_assert(kWarpsN * 32 == kQ4TileN, "32 rows of W per warp");
+
+// kTiles: 8-row tiles of X.
+template <int kTiles>
+struct Layout {
+  static constexpr uint32_t kXBox = kTiles * 8 * 128;      // 64 values of each row
+  static constexpr uint32_t kStage = kCodeBoxes * kCodeBox + kXBoxes * kXBox;
+  // Two CTAs per SM up to 16 rows; as many stages as there is room for.
+  static constexpr int kCtas = kTiles <= 2 ? 2 : 1;
+  static constexpr int S = (232448 / kCtas - 2560) / kStage;
+  static constexpr uint32_t kSmem = S * kStage + 256 + 1024;
+  // The sums take the ring's place.
+  static_assert(kWarpsK * kQ4TileN * kTiles * 8 * 4 <= S * kStage, "shared memory");
+  static_assert(S >= 2 && kSmem <= 232448, "shared memory");
+};
+
+template <int S>
+struct alignas(8) Barriers {
+  uint64_t full[S];
+  uint64_t empty[S];
+  int abort;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* desc, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (__is_same(T, __half))
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A zero in the form that codes are reduced by: 128 + z in BF16; in FP16 1024 + z
+// and -(64 + z).
+template <typename T>
+struct Zero {
+  uint32_t a, b;
+  __device__ __forceinline__ explicit Zero(uint32_t z) {
+    if constexpr (__is_same(T, __half)) {
+      a = 0x64006400u | (z * 0x00010001u);
+      b = 0xD400D400u | (z * 0x00100010u);
+    } else {
+      a = 0x43004300u | (z * 0x00010001u);
+      b = 0;
+    }
+  }
+};
+
+// The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes, less their zero.  A code
+// in the low mantissa bits of 128 (BF16) or 1024 (FP16) is that plus the code; FP16 has
+// room for one four bits further up, 1024 + 16 q.
+template <typename T>
+__device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, uint32_t (&v)[4]) {
+  if constexpr (__is_same(T, __half)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = w >> (8 * i);
+      const uint32_t lo = (x & 0x000F000Fu) | 0x64006400u;
+      const uint32_t hi = (x & 0x00F000F0u) | 0x64006400u;
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2 * i]) : "r"(lo), "r"(z.a));
+      asm("fma.rn.f16x2 %0, %1, %2, %3;"
+          : "=r"(v[2 * i + 1])
+          : "r"(hi), "r"(0x2C002C00u), "r"(z.b));   // 1/16
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(x), "r"(z.a));
+    }
+  }
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Tile `slot` of the rows: its expert (-1: there is no such tile) and rows [lo, hi).
+// By one warp; offsets are put in order as group_gemm.cu does.
+struct Rows {
+  int expert, lo, hi;
+};
+__device__ __forceinline__ Rows rows_of_slot(int slot, const Q4FewParams& p) {
+  Rows r;
+  if (p.experts == 0) {
+    r.expert = 0;
+    r.lo = slot * p.tile_rows;
+    r.hi = min(r.lo + p.tile_rows, p.rows);
+    return r;
+  }
+  r.expert = -1, r.lo = r.hi = 0;
+  const int lane = threadIdx.x & 31;
+  int last = 0, tiles = 0;
+  bool bad = false;
+  for (int base = 0; base <= p.experts; base += 32) {
+    const int i = base + lane;
+    const int raw = i <= p.experts ? p.offsets[i] : p.rows;
+    const int own = min(max(raw, 0), p.rows);
+    int v = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, last);
+    bad |= own != raw || v != own;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = last;
+    const int mine = i >= 1 && i <= p.experts ? (v - before + p.tile_rows - 1) / p.tile_rows : 0;
+    int n = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    // (Lane i has the end of expert i - 1, whose tiles end at tiles + n.)
+    const unsigned here =
+        __ballot_sync(0xffffffffu, slot < tiles + n && slot >= tiles + n - mine);
+    if (here != 0 && r.expert < 0) {
+      const int src = __ffs(here) - 1;
+      r.expert = base + src - 1;
+      const int first = __shfl_sync(0xffffffffu, tiles + n - mine, src);
+      r.lo = __shfl_sync(0xffffffffu, before, src) + (slot - first) * p.tile_rows;
+      r.hi = min(r.lo + p.tile_rows, __shfl_sync(0xffffffffu, v, src));
+    }
+    tiles += __shfl_sync(0xffffffffu, n, 31);
+    last = __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0 && slot == 0)
+    raise_fault(p.fault, kFaultGroupOffsets);
+  return r;
+}
+
+template <typename T, int kTiles>
+__global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
+    q4_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
+                  const Q4FewParams p) {
+  using L = Layout<kTiles>;
+  constexpr int S = L::S;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const base = align_smem_1024(smem_raw);
+  float* const sums = reinterpret_cast<float*>(base);
+  auto* bars = reinterpret_cast<Barriers<S>*>(base + S * L::kStage);
+  static_assert(sizeof(Barriers<S>) <= 256, "barrier block must fit its reserved space");
+  __shared__ Rows s_rows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int n0 = (int)(blockIdx.x / (unsigned)p.split) * kQ4TileN;
+  const int nk = (p.K + kQ4BK - 1) / kQ4BK;
+  const int kb = (int)((long long)rank * nk / p.split);
+  const int ke = (int)((long long)(rank + 1) * nk / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), 1);
+      mbar_init(smem_u32(&bars->empty[s]), kWarps);
+    }
+    bars->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmX);
+  }
+  wait_prior_grids();
+  allow_dependent_grids();
+  if (warp == 0) {
+    const Rows r = rows_of_slot((int)blockIdx.y, p);
+    if (lane == 0) s_rows = r;
+  }
+  __syncthreads();
+  const Rows rows = s_rows;
+  if (rows.expert < 0) return;   // (the same in all of a cluster)
+
+  uint32_t issued = 0;
+  if (warp == kWarps) {
+    if (elect_one()) {
+      // ---------------------------------------------- loads
+      RingPos<S> pos;
+      for (int kt = kb; kt < ke; ++kt, pos.next()) {
+        if (!role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                       &bars->abort, kFaultTcProducerWait, true))
+          break;
+        const uint32_t st = smem_u32(base + pos.slot * L::kStage);
+        const uint32_t full = smem_u32(&bars->full[pos.slot]);
+        mbar_arrive_expect_tx(full, L::kStage);
+#pragma unroll
+        for (int j = 0; j < kCodeBoxes; ++j)
+          tma_load_3d(st + j * kCodeBox, &tmQ, full, (kt * kQ4BK + j * 256) / 2, n0, rows.expert);
+#pragma unroll
+        for (int j = 0; j < kXBoxes; ++j)
+          tma_load_2d(st + kCodeBoxes * kCodeBox + j * L::kXBox, &tmX, full, kt * kQ4BK + j * 64,
+                      rows.lo);
+        ++issued;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ products
+    const int wn = warp / kWarpsK, wk = warp % kWarpsK;
+    const int g = lane >> 2, t = lane & 3;
+    const int groups = (p.K + p.group - 1) / p.group;
+    // This lane's row of W, whose scales and zeros it reads for the warp.
+    const int row = n0 + wn * 32 + lane;
+    const long long srow = ((long long)rows.expert * p.N + row) * groups;
+    const T* const scales = static_cast<const T*>(p.scales) + srow;
+    const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + srow : nullptr;
+    const bool real = row < p.N;
+    constexpr int kSteps = kSliceK / 32;
+    float acc[2][kTiles][4], part[2][kTiles][4];
+#pragma unroll
+    for (int i = 0; i < 2 * kTiles * 4; ++i)
+      (&acc[0][0][0])[i] = 0.f, (&part[0][0][0])[i] = 0.f;
+
+    // Scale and zero of each 32-deep step of a stage's slice, read a stage ahead.
+    float sc[kSteps];
+    uint32_t zr[kSteps];
+    auto read_scales = [&](int kt) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int k = kt * kQ4BK + wk * kSliceK + i * 32;
+        const bool ok = real && kt < ke && k < p.K;
+        const int at = ok ? k / p.group : 0;
+        sc[i] = ok ? elem_to_f32<T>(scales[at]) : 0.f;
+        zr[i] = ok && zeros != nullptr ? zeros[at] & 15u : 8u;
+      }
+    };
+    read_scales(kb);
+    RingPos<S> pos;
+    bool ok = true;
+    for (int kt = kb; kt < ke; ++kt, pos.next()) {
+      float s[kSteps];
+      uint32_t z[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) s[i] = sc[i], z[i] = zr[i];
+      read_scales(kt + 1);
+      ok = role_wait_lanes(smem_u32(&bars->full[pos.slot]), pos.parity, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcMmaWait);
+      if (!ok) break;
+      const unsigned char* const st = base + pos.slot * L::kStage;
+      const int k0 = kt * kQ4BK + wk * kSliceK;
+      // Chunks of 16 bytes in 128-byte rows are swizzled by the row.
+      const unsigned char* const q =
+          st + (wk >> 1) * kCodeBox + (wn * 32 + g) * 128 + t * 4;
+      // (An 8-row tile's rows in the order 0, 4, 1, 5, 2, 6, 3, 7: eight lanes with two
+      // rows' four chunks then read 128 different bytes.)
+      const int xr = (g >> 1) | ((g & 1) << 2);
+      const unsigned char* const xs =
+          st + kCodeBoxes * kCodeBox + wk * 2 * L::kXBox + xr * 128;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        if (k0 + i * 32 >= p.K) break;
+        uint32_t w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          w[r] = *reinterpret_cast<const uint32_t*>(q + r * 8 * 128 +
+                                                    ((((wk & 1) * 4 + i) ^ g) << 4));
+        uint32_t v[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          codes_less_zero<T>(w[r], Zero<T>(__shfl_sync(0xffffffffu, z[i], r * 8 + g)), v[r]);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              xs + (i >> 1) * L::kXBox + m * 1024 + ((((i & 1) * 4 + t) ^ xr) << 4));
+          const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
+          const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0[4] = {v[2 * h][0], v[2 * h + 1][0], v[2 * h][1], v[2 * h + 1][1]};
+            const uint32_t a1[4] = {v[2 * h][2], v[2 * h + 1][2], v[2 * h][3], v[2 * h + 1][3]};
+            mma_16816<T>(part[h][m], a0, b0, b1);
+            mma_16816<T>(part[h][m], a1, b2, b3);
+          }
+        }
+        // The group's end, or this warp's last step before another range of K.
+        const int next = k0 + (i + 1) * 32;
+        if (i == kSteps - 1 || next >= p.K || next % p.group == 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float lo = __shfl_sync(0xffffffffu, s[i], h * 16 + g);
+            const float hi = __shfl_sync(0xffffffffu, s[i], h * 16 + 8 + g);
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                acc[h][m][e] = fmaf(e < 2 ? lo : hi, part[h][m][e], acc[h][m][e]);
+                part[h][m][e] = 0.f;
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->empty[pos.slot]));
+    }
+    // sums[wk][row of X][row of W], where the stages were.
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    float* const to = sums + wk * (kQ4TileN * kTiles * 8) + wn * 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          to[(m * 8 + t + 4 * (e & 1)) * kQ4TileN + h * 16 + (e >> 1) * 8 + g] = acc[h][m][e];
+  }
+  __syncthreads();
+  if (warp == kWarps && elect_one() && bars->abort) {
+    // Let the copies in flight land.
+    for (uint32_t it = issued > (uint32_t)S ? issued - S : 0; it < issued; ++it)
+      if (!mbar_wait_bounded(smem_u32(&bars->full[it % S]), (it / S) & 1u, p.timeout_ns,
+                             nullptr)) {
+        raise_fault(p.fault, kFaultDrainWait);
+        break;
+      }
+  }
+  // The ranges of K in order, into the first; then this CTA's part of the tile over
+  // the cluster.
+  const int values = (rows.hi - rows.lo) * kQ4TileN;
+  constexpr int kPlane = kQ4TileN * kTiles * 8;
+  T* const Y = static_cast<T*>(p.Y);
+  if (p.split == 1) {
+    for (int i = threadIdx.x; i < values; i += kThreads) {
+      float v = sums[i];
+#pragma unroll
+      for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
+      const int n = n0 + i % kQ4TileN;
+      if (n < p.N) Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v);
+    }
+  } else {
+    for (int i = threadIdx.x; i < values; i += kThreads) {
+      float v = sums[i];
+#pragma unroll
+      for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
+      sums[i] = v;
+    }
+    cluster_sync_all();
+    for (int i = rank * kThreads + threadIdx.x; i < values; i += p.split * kThreads) {
+      const uint32_t at = smem_u32(sums + i);
+      float v = 0.f;
+      for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
+      const int n = n0 + i % kQ4TileN;
+      if (n < p.N) Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v);
+    }
+    cluster_sync_all();   // nobody leaves while its sums may still be read
+  }
+}
+
+template <typename T, int kTiles>
+cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
+                         cudaStream_t stream) {
+  auto kernel = q4_few_kernel<T, kTiles>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = mx_allow_smem(kernel, Layout<kTiles>::kSmem, &done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = ((long long)p.N + kQ4TileN - 1) / kQ4TileN;
+  return launch_gemm_kernel_clusters((unsigned)p.split, kernel,
+                                     dim3((unsigned)(tiles * p.split), (unsigned)p.slots),
+                                     dim3(kThreads), Layout<kTiles>::kSmem, stream, *tmQ, *tmX, p);
+}
+
+template <typename T>
+cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
+                         cudaStream_t stream) {
+  switch (p.tile_rows / 8) {
+    case 1: return launch_tiles<T, 1>(p, q, x, stream);
+    case 2: return launch_tiles<T, 2>(p, q, x, stream);
+    case 3: return launch_tiles<T, 3>(p, q, x, stream);
+    case 4: return launch_tiles<T, 4>(p, q, x, stream);
+    case 6: return launch_tiles<T, 6>(p, q, x, stream);
+    case 8: return launch_tiles<T, 8>(p, q, x, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// ------------------------------------------------------------ weights in 16 bits
+
+// Each thread: the 32 codes of 16 bytes, which share a scale.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    q4_values_kernel(int group, long long rows, int N, int K, const unsigned char* codes, int ldq,
+                     const T* scales, const unsigned char* zeros, const int* offsets, T* D,
+                     long long ldd) {
+  wait_prior_grids();
+  allow_dependent_grids();
+  const int chunks = (K + 31) / 32, groups = (K + group - 1) / group;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < rows * chunks;
+       i += (long long)gridDim.x * blockDim.x) {
+    const long long r = i / chunks;
+    const int c = (int)(i - r * chunks);
+    if (offsets != nullptr) {
+      const int e = (int)(r / N);
+      if (offsets[e + 1] <= offsets[e]) continue;
+    }
+    const uint4 w = *reinterpret_cast<const uint4*>(codes + r * ldq + (long long)c * 16);
+    const long long at = r * groups + c * 32 / group;
+    const float s = elem_to_f32<T>(scales[at]);
+    const float z = zeros != nullptr ? (float)(zeros[at] & 15) : 8.f;
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+    T* const to = D + r * ldd + c * 32;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c * 32 + j * 8 >= K) break;       // (ldd has room for whole groups of 8)
+      uint32_t v[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        v[h] = pack2<T>(((float)((q[j] >> (8 * h)) & 15u) - z) * s,
+                        ((float)((q[j] >> (8 * h + 4)) & 15u) - z) * s);
+      *reinterpret_cast<uint4*>(to + j * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
+                          const CUtensorMap* tmX, cudaStream_t stream) {
+  return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)
+                    : launch_typed<__nv_bfloat16>(p, tmQ, tmX, stream);
+}
+
+cudaError_t launch_q4_values(int dtype, int group, long long rows, int N, int K,
+                             const unsigned char* codes, int ldq, const void* scales,
+                             const unsigned char* zeros, const int* offsets, void* D,
+                             long long ldd, cudaStream_t stream) {
+  const long long ctas = (rows * ((K + 31) / 32) + 255) / 256;
+  const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20));
+  if (dtype == 1)
+    return launch_gemm_kernel(q4_values_kernel<__half>, grid, dim3(256), 0, stream, group, rows, N,
+                              K, codes, ldq, static_cast<const __half*>(scales), zeros, offsets,
+                              static_cast<__half*>(D), ldd);
+  return launch_gemm_kernel(q4_values_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, group,
+                            rows, N, K, codes, ldq, static_cast<const __nv_bfloat16*>(scales),
+                            zeros, offsets, static_cast<__nv_bfloat16*>(D), ldd);
+}
+
+}  // namespace dgemm

@@ -16,6 +16,7 @@ enum WorkspaceUse {
   kWsFlags,      // hand-over flags of cut tiles: zeroed when allocated, then only ever set
                  // to a launch's epoch (or cleared)
   kWsQuantized,  // the quantised X of gemm_mx4_linear
+  kWsValues,     // 4-bit weights in 16 bits
   kWsUses
 };
 

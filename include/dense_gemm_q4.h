@@ -1,0 +1,61 @@
+/*
+ * dense_gemm_q4.h -- products with weights held in 4 bits with a scale for each
+ * group of them, for the GB300 dense GEMM library: a linear layer whose
+ * activations stay in 16 bits, for one weight matrix or one for each expert.
+ *
+ * Weights (out x in, N x K; `experts` of them, one behind the other, where rows
+ * are grouped by expert):
+ *   codes   N rows of ldq bytes (a multiple of 16, at least (K + 1) / 2), 16-byte
+ *           aligned: columns 2j and 2j + 1 in the low and high half of byte j.
+ *           Nothing past a row's last code counts.
+ *   scales  N rows of ceil(K / group) values of X's type, contiguous
+ *   zeros   N rows of ceil(K / group) bytes, contiguous, of which the low four bits
+ *           count; or NULL: 8 for all
+ *   W[n][k] = scales[n][k / group] * (code(n, k) - zeros[n][k / group])
+ * group is a multiple of 32 (one at least K: a scale for each row).
+ *
+ * dtype codes are those of gemm_plan: 1 = FP16, 2 = BF16.  Pointers, streams, errors
+ * and the device fault word follow dense_gemm.h, offsets of experts
+ * dense_gemm_group.h: argument problems are reported synchronously before anything
+ * is queued, work is queued on `stream`, and every device-side wait is bounded.
+ * Inputs must not overlap outputs.  Sizes are at most GEMM_GROUP_MAX_SIZE.
+ *
+ * Device memory: calls with many rows take a workspace for the weights in 16 bits,
+ * at most GEMM_Q4_WORKSPACE bytes (more only where one expert's single row of codes
+ * needs more): one per (device, stream), under the rules of dense_gemm.h (replaced
+ * by a larger one when a call needs more, never freed, shared by the graphs captured
+ * on the stream, whose replays must not overlap).  Before a stream capture, make one
+ * call of the same sizes on that stream.
+ */
+#ifndef DENSE_GEMM_Q4_H_
+#define DENSE_GEMM_Q4_H_
+
+#include "dense_gemm.h"
+#include "dense_gemm_group.h"
+
+#if defined(__cplusplus)
+extern "C" {
+#endif
+
+#define GEMM_Q4_WORKSPACE (256ll << 20)
+
+/*
+ * Y[i] := X[i] . W^T for X (rows x K) and Y (rows x N) of dtype: with experts == 0
+ * for all rows, W the only matrix (offsets is NULL); else for the rows i of each
+ * expert g, W its matrix, as gemm_grouped does.  X is 16-byte aligned and ldx a
+ * multiple of 8, or X is packed (ldx == K) at any alignment of its type, which takes
+ * a copy with aligned rows in a workspace first; else GEMM_ERR_MISALIGNED.  Y has any
+ * alignment of its type.  FP32 accumulation; one rounding.  (Few rows: the integers
+ * code - zero, exact in 16 bits, are multiplied and each group's FP32 sum scaled.
+ * Many: the weights are rounded to dtype first.)  K == 0: zeros.
+ */
+gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, int K, int experts,
+                             const void *X, int ldx, const void *codes, int ldq,
+                             const void *scales, const void *zeros, const int *offsets, void *Y,
+                             int ldy, cudaStream_t stream);
+
+#if defined(__cplusplus)
+}
+#endif
+
+#endif /* DENSE_GEMM_Q4_H_ */
