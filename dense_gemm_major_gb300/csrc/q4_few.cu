@@ -115,6 +115,21 @@ __device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, ui
   }
 }
 
+// Volatile, so that no load moves past the arrival that gives its stage back.
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -177,7 +192,9 @@ __device__ __forceinline__ Rows rows_of_slot(int slot, const Q4FewParams& p) {
   return r;
 }
 
-template <typename T, int kTiles>
+// kEach: a scale for each step of 32 terms; else for each warp's slice of a stage
+// (groups of a multiple of 128).
+template <typename T, int kTiles, bool kEach>
 __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     q4_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                   const Q4FewParams p) {
@@ -247,66 +264,85 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     // This lane's row of W, whose scales and zeros it reads for the warp.
     const int row = n0 + wn * 32 + lane;
     const long long srow = ((long long)rows.expert * p.N + row) * groups;
-    const T* const scales = static_cast<const T*>(p.scales) + srow;
+    const uint16_t* const scales = static_cast<const uint16_t*>(p.scales) + srow;
     const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + srow : nullptr;
     const bool real = row < p.N;
     constexpr int kSteps = kSliceK / 32;
-    float acc[2][kTiles][4], part[2][kTiles][4];
+    float acc[2][kTiles][4];
 #pragma unroll
-    for (int i = 0; i < 2 * kTiles * 4; ++i)
-      (&acc[0][0][0])[i] = 0.f, (&part[0][0][0])[i] = 0.f;
+    for (int i = 0; i < 2 * kTiles * 4; ++i) (&acc[0][0][0])[i] = 0.f;
 
-    // Scale and zero of each 32-deep step of a stage's slice, read a stage ahead.
-    float sc[kSteps];
-    uint32_t zr[kSteps];
-    auto read_scales = [&](int kt) {
+    // The scales and zeros of a stage's slice, read a stage ahead and left as they
+    // come: a conversion would wait for them at once.  `at`, `pos`: group of a
+    // slice's first step, and its place in it.
+    uint16_t sc[kEach ? kSteps : 1];
+    unsigned char zr[kEach ? kSteps : 1];
+    const int far_at = kQ4BK / p.group, far_pos = kQ4BK % p.group;
+    int at = (kb * kQ4BK + wk * kSliceK) / p.group;
+    int pos = (kb * kQ4BK + wk * kSliceK) % p.group;
+    auto read_scales = [&](int kt, int at, int pos) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int k = kt * kQ4BK + wk * kSliceK + i * 32;
-        const bool ok = real && kt < ke && k < p.K;
-        const int at = ok ? k / p.group : 0;
-        sc[i] = ok ? elem_to_f32<T>(scales[at]) : 0.f;
-        zr[i] = ok && zeros != nullptr ? zeros[at] & 15u : 8u;
+      for (int i = 0; i < (kEach ? kSteps : 1); ++i) {
+        const bool ok = real && kt < ke && kt * kQ4BK + wk * kSliceK + i * 32 < p.K;
+        sc[i] = ok ? scales[at] : (uint16_t)0;
+        zr[i] = ok && zeros != nullptr ? zeros[at] : (unsigned char)8;
+        if ((pos += 32) == p.group) pos = 0, ++at;
       }
     };
-    read_scales(kb);
-    RingPos<S> pos;
-    bool ok = true;
-    for (int kt = kb; kt < ke; ++kt, pos.next()) {
-      float s[kSteps];
-      uint32_t z[kSteps];
+    read_scales(kb, at, pos);
+    // Chunks of 16 bytes in 128-byte rows are swizzled by the row.  (An 8-row tile of
+    // X has its rows in the order 0, 4, 1, 5, 2, 6, 3, 7: eight lanes with two rows'
+    // four chunks then read 128 different bytes.)
+    const int xr = (g >> 1) | ((g & 1) << 2);
+    uint32_t q_at[kSteps], x_at[2];
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) s[i] = sc[i], z[i] = zr[i];
-      read_scales(kt + 1);
-      ok = role_wait_lanes(smem_u32(&bars->full[pos.slot]), pos.parity, p.fault, p.timeout_ns,
+    for (int i = 0; i < kSteps; ++i)
+      q_at[i] = (wk >> 1) * kCodeBox + (wn * 32 + g) * 128 + t * 4 +
+                ((((wk & 1) * 4 + i) ^ g) << 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      x_at[i] = kCodeBoxes * kCodeBox + wk * 2 * L::kXBox + xr * 128 + (((i * 4 + t) ^ xr) << 4);
+    RingPos<S> ring;
+    bool ok = true;
+    for (int kt = kb; kt < ke; ++kt, ring.next()) {
+      float s[kEach ? kSteps : 1];
+      uint32_t z[kEach ? kSteps : 1];
+#pragma unroll
+      for (int i = 0; i < (kEach ? kSteps : 1); ++i) {
+        s[i] = elem_to_f32<T>(__builtin_bit_cast(T, sc[i]));
+        z[i] = zr[i] & 15u;
+      }
+      at += far_at;
+      if ((pos += far_pos) >= p.group) pos -= p.group, ++at;
+      read_scales(kt + 1, at, pos);
+      ok = role_wait_lanes(smem_u32(&bars->full[ring.slot]), ring.parity, p.fault, p.timeout_ns,
                            &bars->abort, kFaultTcMmaWait);
       if (!ok) break;
-      const unsigned char* const st = base + pos.slot * L::kStage;
-      const int k0 = kt * kQ4BK + wk * kSliceK;
-      // Chunks of 16 bytes in 128-byte rows are swizzled by the row.
-      const unsigned char* const q =
-          st + (wk >> 1) * kCodeBox + (wn * 32 + g) * 128 + t * 4;
-      // (An 8-row tile's rows in the order 0, 4, 1, 5, 2, 6, 3, 7: eight lanes with two
-      // rows' four chunks then read 128 different bytes.)
-      const int xr = (g >> 1) | ((g & 1) << 2);
-      const unsigned char* const xs =
-          st + kCodeBoxes * kCodeBox + wk * 2 * L::kXBox + xr * 128;
+      const uint32_t st = smem_u32(base) + ring.slot * L::kStage;
+      // (Past K, X is zeros and the codes stand for finite values.)
+      uint32_t w[kSteps][4];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          w[i][r] = ld_shared_u32(st + q_at[i] + r * 8 * 128);
+      float part[2][kTiles][4];
+      Zero<T> zero[4] = {Zero<T>(0), Zero<T>(0), Zero<T>(0), Zero<T>(0)};
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        if (k0 + i * 32 >= p.K) break;
-        uint32_t w[4];
+        if (kEach || i == 0) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          w[r] = *reinterpret_cast<const uint32_t*>(q + r * 8 * 128 +
-                                                    ((((wk & 1) * 4 + i) ^ g) << 4));
+          for (int r = 0; r < 4; ++r)
+            zero[r] = Zero<T>(__shfl_sync(0xffffffffu, z[i], r * 8 + g));
+#pragma unroll
+          for (int e = 0; e < 2 * kTiles * 4; ++e) (&part[0][0][0])[e] = 0.f;
+        }
         uint32_t v[4][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          codes_less_zero<T>(w[r], Zero<T>(__shfl_sync(0xffffffffu, z[i], r * 8 + g)), v[r]);
+        for (int r = 0; r < 4; ++r) codes_less_zero<T>(w[i][r], zero[r], v[r]);
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-          const uint4 x = *reinterpret_cast<const uint4*>(
-              xs + (i >> 1) * L::kXBox + m * 1024 + ((((i & 1) * 4 + t) ^ xr) << 4));
+          const uint4 x = ld_shared_v4(st + x_at[i & 1] + (i >> 1) * L::kXBox + m * 1024);
           const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
           const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
 #pragma unroll
@@ -317,25 +353,24 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
             mma_16816<T>(part[h][m], a1, b2, b3);
           }
         }
-        // The group's end, or this warp's last step before another range of K.
-        const int next = k0 + (i + 1) * 32;
-        if (i == kSteps - 1 || next >= p.K || next % p.group == 0) {
+        if (kEach || i == kSteps - 1) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float lo = __shfl_sync(0xffffffffu, s[i], h * 16 + g);
-            const float hi = __shfl_sync(0xffffffffu, s[i], h * 16 + 8 + g);
+            const float lo = __shfl_sync(0xffffffffu, s[kEach ? i : 0], h * 16 + g);
+            const float hi = __shfl_sync(0xffffffffu, s[kEach ? i : 0], h * 16 + 8 + g);
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < 4; ++e)
                 acc[h][m][e] = fmaf(e < 2 ? lo : hi, part[h][m][e], acc[h][m][e]);
-                part[h][m][e] = 0.f;
-              }
           }
         }
       }
+      // The proxy fence waits for the loads above: without it TMA has been seen to
+      // refill the stage before the last of them had read it.
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->empty[pos.slot]));
+      if (lane == 0) mbar_arrive(smem_u32(&bars->empty[ring.slot]));
     }
     // sums[wk][row of X][row of W], where the stages were.
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
@@ -390,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
   }
 }
 
-template <typename T, int kTiles>
+template <typename T, int kTiles, bool kEach>
 cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
                          cudaStream_t stream) {
-  auto kernel = q4_few_kernel<T, kTiles>;
+  auto kernel = q4_few_kernel<T, kTiles, kEach>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(kernel, Layout<kTiles>::kSmem, &done);
   if (e != cudaSuccess) return e;
@@ -403,16 +438,16 @@ cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUt
                                      dim3(kThreads), Layout<kTiles>::kSmem, stream, *tmQ, *tmX, p);
 }
 
-template <typename T>
+template <typename T, bool kEach>
 cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                          cudaStream_t stream) {
   switch (p.tile_rows / 8) {
-    case 1: return launch_tiles<T, 1>(p, q, x, stream);
-    case 2: return launch_tiles<T, 2>(p, q, x, stream);
-    case 3: return launch_tiles<T, 3>(p, q, x, stream);
-    case 4: return launch_tiles<T, 4>(p, q, x, stream);
-    case 6: return launch_tiles<T, 6>(p, q, x, stream);
-    case 8: return launch_tiles<T, 8>(p, q, x, stream);
+    case 1: return launch_tiles<T, 1, kEach>(p, q, x, stream);
+    case 2: return launch_tiles<T, 2, kEach>(p, q, x, stream);
+    case 3: return launch_tiles<T, 3, kEach>(p, q, x, stream);
+    case 4: return launch_tiles<T, 4, kEach>(p, q, x, stream);
+    case 6: return launch_tiles<T, 6, kEach>(p, q, x, stream);
+    case 8: return launch_tiles<T, 8, kEach>(p, q, x, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -459,8 +494,11 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream) {
-  return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)
-                    : launch_typed<__nv_bfloat16>(p, tmQ, tmX, stream);
+  if (p.group % kSliceK == 0)
+    return dtype == 1 ? launch_typed<__half, false>(p, tmQ, tmX, stream)
+                      : launch_typed<__nv_bfloat16, false>(p, tmQ, tmX, stream);
+  return dtype == 1 ? launch_typed<__half, true>(p, tmQ, tmX, stream)
+                    : launch_typed<__nv_bfloat16, true>(p, tmQ, tmX, stream);
 }
 
 cudaError_t launch_q4_values(int dtype, int group, long long rows, int N, int K,

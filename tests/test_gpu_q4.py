@@ -95,6 +95,22 @@ def test_dense(dg, dtype, zeros, shape):
     assert torch.equal(dg.q4_linear(x, w), y)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows", [7, 16, 40])
+def test_long_rows(dg, dtype, group, rows):
+    """Rings that go round several times, on all SMs at once, over and over: every
+    pass has the same bits, within the bound."""
+    gen = torch.Generator("cuda").manual_seed(rows + group)
+    x = _x(gen, rows, 8192, dtype)
+    w, values = _weights(dg, gen, (8192,), 8192, dtype, group, True)
+    y = dg.q4_linear(x, w)
+    _check(y, x, values, 8192, dtype, False)
+    for _ in range(5):
+        assert torch.equal(dg.q4_linear(x, w), y)
+    check_device(dg)
+
+
 EXPERTS = [([1], 64, 64, 32), ([0, 1, 0, 2], 130, 520, 64), ([0, 0], 64, 64, 32),
            ([3, 0, 9, 1, 40], 65, 777, 32), ([1] * 33, 64, 300, 128), ([70, 0, 1, 200], 100, 512, 64),
            ([300, 0, 500, 7], 129, 777, 96), ([0, 1500], 64, 96, 32)]
