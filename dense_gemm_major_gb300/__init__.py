@@ -676,10 +676,14 @@ class Q4Tensor:
     codes   uint8, (experts x) out x pitch, columns 2j and 2j + 1 in the low and
             high half of byte j; the pitch a multiple of 16 bytes, experts one
             behind the other
-    scales  float16 or bfloat16, contiguous (experts x) out x ceil(cols / group)
-    zeros   uint8 of the scales' shape, 0 .. 15, contiguous; None: 8 for all
-    cols    columns (default: two for each byte of codes)"""
-    __slots__ = ("codes", "scales", "zeros", "experts", "rows", "cols", "group", "_ld")
+    scales  float16 or bfloat16, (experts x) out x ceil(cols / group)
+    zeros   uint8 of the scales' shape, 0 .. 15; None: 8 for all
+    cols    columns (default: two for each byte of codes)
+
+    codes are kept as they are.  Scales and zeros are kept with the values of a
+    group of columns together, as the kernels read them: copied once, here, unless
+    they are transposed views of such arrays."""
+    __slots__ = ("codes", "_scales", "_zeros", "experts", "rows", "cols", "group", "_ld")
 
     def __init__(self, codes, scales, zeros=None, cols=None, group=128):
         import torch
@@ -707,13 +711,14 @@ class Q4Tensor:
             raise ValueError("codes need 16-byte aligned rows")
         shape = (*lead, -(-cols // group))
         if (scales.dtype not in (torch.float16, torch.bfloat16) or tuple(scales.shape) != shape
-                or not scales.is_contiguous() or scales.device != codes.device):
-            raise ValueError(f"scales must be contiguous float16 or bfloat16 of shape {shape} "
-                             "on the codes' device")
+                or scales.device != codes.device):
+            raise ValueError(f"scales must be float16 or bfloat16 of shape {shape} on the codes' "
+                             "device")
         if zeros is not None and (zeros.dtype != torch.uint8 or tuple(zeros.shape) != shape
-                                  or not zeros.is_contiguous() or zeros.device != codes.device):
-            raise ValueError(f"zeros must be contiguous uint8 of shape {shape} on the codes' device")
-        self.codes, self.scales, self.zeros = codes, scales, zeros
+                                  or zeros.device != codes.device):
+            raise ValueError(f"zeros must be uint8 of shape {shape} on the codes' device")
+        self.codes, self._scales = codes, scales.transpose(-1, -2).contiguous()
+        self._zeros = None if zeros is None else zeros.transpose(-1, -2).contiguous()
         self.experts = lead[0] if codes.dim() == 3 else 0
         self.rows, self.cols, self.group, self._ld = rows, cols, group, ld
 
@@ -722,12 +727,20 @@ class Q4Tensor:
         return (*self.codes.shape[:-1], self.cols)
 
     @property
+    def scales(self):
+        return self._scales.transpose(-1, -2)
+
+    @property
+    def zeros(self):
+        return None if self._zeros is None else self._zeros.transpose(-1, -2)
+
+    @property
     def device(self):
         return self.codes.device
 
     def record_stream(self, stream):
         """Tensor.record_stream of the codes, scales and zeros."""
-        for t in (self.codes, self.scales, self.zeros):
+        for t in (self.codes, self._scales, self._zeros):
             if t is not None:
                 t.record_stream(stream)
 

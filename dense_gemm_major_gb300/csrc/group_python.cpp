@@ -240,7 +240,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "setup(torch, Q4Tensor, GemmError)");
     return nullptr;
   }
-  const Name names[] = {{&n_codes, "codes"}, {&n_scales, "scales"}, {&n_zeros, "zeros"},
+  const Name names[] = {{&n_codes, "codes"}, {&n_scales, "_scales"}, {&n_zeros, "_zeros"},
                         {&n_experts, "experts"}, {&n_rows, "rows"}, {&n_cols, "cols"},
                         {&n_group, "group"}, {&n_ld, "_ld"}, {nullptr, nullptr}};
   Py_INCREF(a[1]);

@@ -39,11 +39,13 @@ inline int q4_tile_rows(int rows) {
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream);
 
-// D (rows x K of dtype, pitch ldd, a multiple of 8) := the weights.  With offsets,
-// row r is of expert r / N, and those without rows are left out.
-cudaError_t launch_q4_values(int dtype, int group, long long rows, int N, int K,
-                             const unsigned char* codes, int ldq, const void* scales,
-                             const unsigned char* zeros, const int* offsets, void* D,
-                             long long ldd, cudaStream_t stream);
+// D (experts x N rows of K values of dtype, pitch ldd, a multiple of 8) := the
+// weights of `experts` matrices, or N rows of them: their codes stride_q bytes apart,
+// their scales and zeros scale_n to a group.  Experts without rows by `offsets`
+// (null: one without) are left out.
+cudaError_t launch_q4_values(int dtype, int group, int experts, int N, int K, int scale_n,
+                             const unsigned char* codes, int ldq, long long stride_q,
+                             const void* scales, const unsigned char* zeros, const int* offsets,
+                             void* D, long long ldd, cudaStream_t stream);
 
 }  // namespace dgemm

@@ -91,11 +91,11 @@ gemm_status_t run_values(const Q4Call& c, dgemm::StreamWorkspaces& workspaces,
     const int n = c.matrices() - e < together ? c.matrices() - e : together;
     for (int n0 = 0; n0 < c.N; n0 += part) {
       const int cols = c.N - n0 < part ? c.N - n0 : part;
-      const long long row = (long long)e * c.N + n0;    // of all codes
+      const long long first = (long long)e * groups * c.N + n0;   // scale
       st = status_of(dgemm::launch_q4_values(
-          c.dtype, c.group, (long long)n * cols, cols, c.K, c.codes + row * c.ldq, c.ldq,
-          static_cast<const char*>(c.scales) + row * groups * 2,
-          c.zeros == nullptr ? nullptr : c.zeros + row * groups,
+          c.dtype, c.group, n, cols, c.K, c.N, c.codes + ((long long)e * c.N + n0) * c.ldq, c.ldq,
+          (long long)c.N * c.ldq, static_cast<const char*>(c.scales) + first * 2,
+          c.zeros == nullptr ? nullptr : c.zeros + first,
           c.offsets == nullptr ? nullptr : c.offsets + e, d, ldd, stream));
       if (st != GEMM_OK) return st;
       const Operand w{d, c.K, cols, ldd, n, (long long)cols * ldd, false};

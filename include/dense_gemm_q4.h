@@ -8,10 +8,10 @@
  *   codes   N rows of ldq bytes (a multiple of 16, at least (K + 1) / 2), 16-byte
  *           aligned: columns 2j and 2j + 1 in the low and high half of byte j.
  *           Nothing past a row's last code counts.
- *   scales  N rows of ceil(K / group) values of X's type, contiguous
- *   zeros   N rows of ceil(K / group) bytes, contiguous, of which the low four bits
+ *   scales  ceil(K / group) rows of N values of X's type, contiguous
+ *   zeros   ceil(K / group) rows of N bytes, contiguous, of which the low four bits
  *           count; or NULL: 8 for all
- *   W[n][k] = scales[n][k / group] * (code(n, k) - zeros[n][k / group])
+ *   W[n][k] = scales[k / group][n] * (code(n, k) - zeros[k / group][n])
  * group is a multiple of 32 (one at least K: a scale for each row).
  *
  * dtype codes are those of gemm_plan: 1 = FP16, 2 = BF16.  Pointers, streams, errors
