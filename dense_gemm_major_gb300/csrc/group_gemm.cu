@@ -19,15 +19,15 @@
 // is summed in segments (GroupParams::seg), which the draining warps add in
 // registers, rounding to nearest; the two accumulators in tensor memory let that
 // overlap the next segment.
-#include "group.h"
-#include "mx.cuh"
+#include "group_sched.cuh"
 
 namespace dgemm {
 namespace {
 
 constexpr int BK = kGroupBK;
 constexpr int kThreads = 384;
-constexpr int kEpiWarp = 4, kEpiWarps = 8;
+constexpr int kEpiWarp = 4, kEpiWarps = kGroupEpiWarps;
+
 // A stage: the CTA's 128 columns of C and up to 128 rows, BK deep.  K-major
 // operands are two blocks of 64 k (128-byte swizzled rows), MN-major ones two
 // blocks 64 wide with a row for each k: 16 KB a block either way.
@@ -36,7 +36,7 @@ constexpr uint32_t kSide = 2 * kBlock;
 constexpr uint32_t kStage = 2 * kSide;
 constexpr int S = 3;
 constexpr uint32_t kTmemCols = 512;                       // two accumulators
-constexpr uint32_t kTableBytes = (kGroupMaxGroups + 1) * 2 * 4;
+constexpr uint32_t kTableBytes = (sizeof(GroupTables) + 15) / 16 * 16;
 constexpr uint32_t kSmemBytes = S * kStage + kTableBytes + 512 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 
@@ -62,109 +62,18 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// A unit: rows [row, row_end) of C (at most 256; weights: of C[g]) by the 256
-// columns from col; the sum's k-tiles are nk, from row k0 of the operands and up
-// to k_end (weights; products: from column 0 up to K).
-struct Unit {
-  int g, row, row_end, col;
-  int nk, k0, k_end;
-  int mma_rows;             // rows rounded up to the MMA's steps of 32
-};
-
-// The units of a grid of CTA pairs, which each takes in increasing order.
-struct Walk {
-  int g = 0;
-  template <int kKind>
-  __device__ __forceinline__ Unit unit(int u, const GroupParams& p, const int* start,
-                                       const int* unit0) {
-    Unit w;
-    int tm, tn;
-    if constexpr (kKind == kGroupWeights) {
-      w.g = u / p.per_group;
-      // (Groups of 16 tiles along C's columns share the operands in L2.)
-      grouped_tile(u - w.g * p.per_group, (p.N + kGroupTile - 1) / kGroupTile,
-                   (p.M + kGroupTile - 1) / kGroupTile, 16, tn, tm);
-      w.row = tm * kGroupTile;
-      w.row_end = min(w.row + kGroupTile, p.M);
-      w.k0 = start[w.g];
-      w.k_end = start[w.g + 1];
-      w.nk = p.K == 0 ? 0 : (w.k_end - w.k0 + BK - 1) / BK;
-    } else {
-      while (unit0[g + 1] <= u) ++g;
-      w.g = g;
-      const int rows = start[g + 1] - start[g];
-      grouped_tile(u - unit0[g], (rows + kGroupTile - 1) / kGroupTile,
-                   (p.N + kGroupTile - 1) / kGroupTile, 16, tm, tn);
-      w.row = start[g] + tm * kGroupTile;
-      w.row_end = min(w.row + kGroupTile, start[g + 1]);
-      w.k0 = 0;
-      w.k_end = p.K;
-      w.nk = (p.K + BK - 1) / BK;
-    }
-    w.col = tn * kGroupTile;
-    w.mma_rows = (w.row_end - w.row + 31) & ~31;
-    return w;
-  }
-};
-
-// The groups' first rows, put in order, and (products) their first units; by
-// one warp.  Returns the number of units.
-__device__ __forceinline__ int group_table(const GroupParams& p, int* start, int* unit0) {
-  const int lane = threadIdx.x & 31;
-  const int tiles_n = (p.N + kGroupTile - 1) / kGroupTile;
-  int last = 0, units = 0;
-  bool bad = false;
-  const int end = p.first_group + p.groups;
-  for (int base = 0; base <= end; base += 32) {
-    const int i = base + lane;
-    const int raw = p.offsets == nullptr ? (i == 0 ? 0 : p.rows)
-                                         : (i <= end ? p.offsets[i] : p.rows);
-    int v = min(max(raw, 0), p.rows);
-    const int own = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v = max(v, o);
-    }
-    v = max(v, last);
-    bad |= own != raw || v != own;
-    int before = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) before = last;
-    // Units of group i - 1, whose end this lane has.
-    int n = i > p.first_group && i <= end
-                ? (int)((long long)((v - before + kGroupTile - 1) / kGroupTile) * tiles_n)
-                : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, n, d);
-      if (lane >= d) n += o;
-    }
-    if (i >= p.first_group && i <= end) {
-      start[i - p.first_group] = v;
-      unit0[i - p.first_group] = units + n;
-    }
-    units += __shfl_sync(0xffffffffu, n, 31);
-    last = __shfl_sync(0xffffffffu, v, 31);
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
-    raise_fault(p.fault, kFaultGroupOffsets);
-  return p.kind == kGroupWeights ? p.groups * p.per_group : units;
-}
-
 template <typename T, typename TC, int kKind>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     group_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN,
                  const __grid_constant__ CUtensorMap tmN16, const GroupParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
-  int* const start = reinterpret_cast<int*>(base + S * kStage);
-  int* const unit0 = start + kGroupMaxGroups + 1;
+  GroupTables& tables = *reinterpret_cast<GroupTables*>(base + S * kStage);
   auto* bars = reinterpret_cast<Barriers*>(base + S * kStage + kTableBytes);
-  __shared__ int s_units;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
-  const int npairs = gridDim.x >> 1;
+  const int npairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
   constexpr bool kWeights = kKind == kGroupWeights;
   constexpr bool kMK = kKind == kGroupForward;   // the M side is K-major
   constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
@@ -191,27 +100,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
   wait_prior_grids();
   allow_dependent_grids();
-  if (warp == 2) {
-    const int n = group_table(p, start, unit0);
-    if (lane == 0) s_units = n;
-  }
+  if (warp == 2) group_tables<kKind>(p, tables);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = bars->tmem_base;
-  const int units = s_units;
+  const int units = tables.units;
 
   uint32_t issued = 0;
   if (warp == 0) {
     if (elect_one()) {
       // ---------------------------------------------- loads (both CTAs)
       RingPos<S> pos;
-      Walk walk;
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
-        const Unit w = walk.unit<kKind>(u, p, start, unit0);
+      for (int u = pair; u < units && ok; u += npairs) {
+        const GroupUnit w = group_unit<kKind>(u, p, tables);
         const int half = w.mma_rows / 2;                 // rows of C that this CTA loads
         const int row = w.row + (int)rank * half;
         const int col = w.col + (int)rank * 128;
@@ -281,12 +186,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0 && elect_one()) {
       // ---------------------------------------------- MMA issuer (even CTA)
       RingPos<S> pos;
-      Walk walk;
       bool ready = false;
       uint32_t seg = 0;
       bool ok = true;
-      for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
-        const Unit w = walk.unit<kKind>(u, p, start, unit0);
+      for (int u = pair; u < units && ok; u += npairs) {
+        const GroupUnit w = group_unit<kKind>(u, p, tables);
         const uint32_t idesc = instr_desc(kAb, 256, (uint32_t)w.mma_rows, kMK ? 0u : 1u,
                                           kWeights ? 1u : 0u);
         for (int k0 = 0; k0 < w.nk && ok; k0 += p.seg, ++seg) {
@@ -334,17 +238,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ ragged ends (both CTAs)
       // The rows of the next group in a group's last 16 are cleared in both
       // operands (zero times a NaN is not zero).
-      Walk walk;
       uint32_t it = 0, uses = 0;   // a bit per slot: the parity of its next use
       bool ok = true;
-      for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
-        const Unit w = walk.unit<kKind>(u, p, start, unit0);
+      for (int u = pair; u < units && ok; u += npairs) {
+        const GroupUnit w = group_unit<kKind>(u, p, tables);
         it += (uint32_t)w.nk;
         const int valid = w.k_end - w.k0 - (w.nk - 1) * BK;
         if (w.nk == 0 || (valid & 15) == 0) continue;
         const uint32_t s = (it - 1) % S;
         ok = role_wait_lanes(smem_u32(&bars->tail[s]), (uses >> s) & 1u, p.fault, p.timeout_ns,
-                             &bars->abort, kFaultTcProducerWait, false, false);
+                             &bars->abort, kFaultTcProducerWait);
         if (!ok) break;
         uses ^= 1u << s;
         const int blocks = w.mma_rows / 2 > 64 ? 4 : 3;
@@ -361,53 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp >= kEpiWarp) {
-    // ------------------------------------------------ epilogue (both CTAs)
-    // Warp: TMEM lanes 32 q .. 32 q + 31 (columns of C), every other 32 rows.
-    const int q = warp & 3;
-    const int half = (warp - kEpiWarp) >> 2;
-    const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 &&
-                       ((p.ldc | p.N) & 1) == 0 && (p.stride_c & 1) == 0;
-    Walk walk;
-    uint32_t seg = 0;
-    bool ok = true;
-    for (int u = blockIdx.x >> 1; u < units && ok; u += npairs) {
-      const Unit w = walk.unit<kKind>(u, p, start, unit0);
-      const int chunks = w.mma_rows / 32;
-      float acc[128];
-#pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-      for (int k0 = 0; k0 < w.nk; k0 += p.seg, ++seg) {
-        const uint32_t b = seg & 1;
-        ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
-                             &bars->abort, kFaultTcEpilogueWait, false, false);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int chunk = 2 * (c >> 1) + half;
-          if (chunk < chunks) {
-            uint32_t r[16];
-            tmem_ld16(t + chunk * 32 + (c & 1) * 16, r);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __uint_as_float(r[j]);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), 0));
-      }
-      if (!ok) break;
-      const int col = w.col + (int)rank * 128 + q * 32 + lane;
-      TC* c_out = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int chunk = 2 * c + half;
-        if (chunk < chunks)
-          store_piece<TC>(acc + c * 32, c_out, p.ldc, w.row_end, p.N, w.row + chunk * 32, col,
-                          pairs, p.alpha, p.beta);
-      }
-    }
+    group_epilogue<TC, kKind>(p, tables, bars, tmem_base, rank, warp - kEpiWarp, pair, npairs);
   }
 
   // ------------------------------------------------ teardown

@@ -1,0 +1,189 @@
+// The work of the grouped kernels' CTA pairs, from offsets that only the device
+// knows: units of C, which the pairs take in rounds, and their draining.
+//
+// A group's rows are cut into equal tiles of at most 256, a multiple of 32 (1342
+// rows: six of 224 rather than five of 256 and one of 62), so that the units of a round
+// end together: 8192 rows of 8 experts, 4096 x 4096, 167 -> 161 us.  (Ranges of units cut
+// along K, one for each pair, whose pieces meet through a workspace, were slower in
+// every case: storing and adding the pieces took 8 to 10 us at the end, the last round
+// that is not full 4 to 8.)
+#pragma once
+
+#include "group.h"
+#include "mx.cuh"
+
+namespace dgemm {
+
+constexpr int kGroupEpiWarps = 8;
+
+// A unit: rows [row, row_end) of C (at most 256; weights: of C[g]) by the 256
+// columns from col; the sum's k-tiles are nk, from row k0 of the operands and up
+// to k_end (weights; products: from column 0 up to K).
+struct GroupUnit {
+  int g, row, row_end, col;
+  int nk, k0, k_end;
+  int mma_rows;             // rows rounded up to the MMA's steps of 32
+};
+
+struct GroupTables {
+  int start[kGroupMaxGroups + 1];        // first rows of the groups, in order
+  int unit0[kGroupMaxGroups + 1];        // their first units
+  short tile[kGroupMaxGroups];           // rows of their tiles
+  int units;
+};
+
+// Rows of a group's tiles (m > 0).
+__device__ __forceinline__ int group_tile_rows(int m) {
+  const int tiles = (m + kGroupTile - 1) / kGroupTile;
+  return ((int)((unsigned)(m + tiles - 1) / (unsigned)tiles) + 31) & ~31;
+}
+__device__ __forceinline__ int group_k_tiles(int terms) { return (terms + kGroupBK - 1) / kGroupBK; }
+
+// The last group g in [0, groups) with first[g] <= x.
+template <typename V>
+__device__ __forceinline__ int group_find(const V* first, int groups, V x) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The tables, by one warp.
+template <int kKind>
+__device__ __forceinline__ void group_tables(const GroupParams& p, GroupTables& t) {
+  const int lane = threadIdx.x & 31;
+  const int tiles_n = (p.N + kGroupTile - 1) / kGroupTile;
+  int last = 0, units = 0;
+  bool bad = false;
+  const int end = p.first_group + p.groups;
+  for (int base = 0; base <= end; base += 32) {
+    const int i = base + lane;
+    const int raw = p.offsets == nullptr ? (i == 0 ? 0 : p.rows)
+                                         : (i <= end ? p.offsets[i] : p.rows);
+    const int own = min(max(raw, 0), p.rows);
+    int v = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, last);
+    bad |= own != raw || v != own;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = last;
+    // Group i - 1, whose end this lane has.
+    const int m = v - before;
+    const bool is = i > p.first_group && i <= end;
+    int n = 0;
+    if (is) n = kKind == kGroupWeights ? p.per_group : (m + kGroupTile - 1) / kGroupTile * tiles_n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    if (kKind != kGroupWeights && is && m > 0)
+      t.tile[i - 1 - p.first_group] = (short)group_tile_rows(m);
+    if (i >= p.first_group && i <= end) {
+      t.start[i - p.first_group] = v;
+      t.unit0[i - p.first_group] = units + n;
+    }
+    units += __shfl_sync(0xffffffffu, n, 31);
+    last = __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
+    raise_fault(p.fault, kFaultGroupOffsets);
+  if (lane == 0) t.units = units;
+}
+
+template <int kKind>
+__device__ __forceinline__ GroupUnit group_unit(int u, const GroupParams& p,
+                                                const GroupTables& t) {
+  GroupUnit w;
+  int tm, tn;
+  if constexpr (kKind == kGroupWeights) {
+    w.g = u / p.per_group;
+    // (Groups of 16 tiles along C's columns share the operands in L2.)
+    grouped_tile(u - w.g * p.per_group, (p.N + kGroupTile - 1) / kGroupTile,
+                 (p.M + kGroupTile - 1) / kGroupTile, 16, tn, tm);
+    w.row = tm * kGroupTile;
+    w.row_end = min(w.row + kGroupTile, p.M);
+    w.k0 = t.start[w.g];
+    w.k_end = t.start[w.g + 1];
+    w.nk = p.K == 0 ? 0 : group_k_tiles(w.k_end - w.k0);
+  } else {
+    w.g = group_find(t.unit0, p.groups, u);
+    const int first = t.start[w.g], rows = t.start[w.g + 1] - first;
+    grouped_tile(u - t.unit0[w.g], (rows + kGroupTile - 1) / kGroupTile,
+                 (p.N + kGroupTile - 1) / kGroupTile, 16, tm, tn);
+    w.row = first + tm * t.tile[w.g];
+    w.row_end = min(w.row + t.tile[w.g], first + rows);
+    w.k0 = 0;
+    w.k_end = p.K;
+    w.nk = group_k_tiles(p.K);
+  }
+  w.col = tn * kGroupTile;
+  w.mma_rows = (w.row_end - w.row + 31) & ~31;
+  return w;
+}
+
+// ------------------------------------------------------------ draining
+
+// Drains a pair's units (both CTAs, kGroupEpiWarps warps each): warp `ew` takes TMEM
+// lanes 32 (ew % 4) .. + 31 (columns of C) and every other 32 rows.
+template <typename TC, int kKind, typename Bars>
+__device__ __forceinline__ void group_epilogue(const GroupParams& p, const GroupTables& t,
+                                               Bars* bars, uint32_t tmem_base, uint32_t rank,
+                                               int ew, int pair, int npairs) {
+  const int lane = threadIdx.x & 31;
+  const int q = ew & 3, half = ew >> 2;
+  constexpr bool kWeights = kKind == kGroupWeights;
+  const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 && ((p.ldc | p.N) & 1) == 0 &&
+                     (p.stride_c & 1) == 0;
+  uint32_t seg = 0;
+  bool ok = true;
+  for (int u = pair; u < t.units; u += npairs) {
+    const GroupUnit w = group_unit<kKind>(u, p, t);
+    const int chunks = w.mma_rows / 32;
+    float acc[128];
+#pragma unroll
+    for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+    for (int k0 = 0; k0 < w.nk; k0 += p.seg, ++seg) {
+      const uint32_t b = seg & 1;
+      ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcEpilogueWait, false, false);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int chunk = 2 * (c >> 1) + half;
+        if (chunk < chunks) {
+          uint32_t r[16];
+          tmem_ld16(ta + chunk * 32 + (c & 1) * 16, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __uint_as_float(r[j]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), 0));
+    }
+    if (!ok) break;
+    const int col = w.col + (int)rank * 128 + q * 32 + lane;
+    TC* c_out = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int chunk = 2 * c + half;
+      if (chunk < chunks)
+        store_piece<TC>(acc + c * 32, c_out, p.ldc, w.row_end, p.N, w.row + chunk * 32, col, pairs,
+                        p.alpha, p.beta);
+    }
+  }
+}
+
+}  // namespace dgemm
