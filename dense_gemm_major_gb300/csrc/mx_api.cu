@@ -22,7 +22,8 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint6
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {pitch_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
-  return encode_tiled(map, dt, 2, base, dims, strides, box, swizzle);
+  return encode_tiled(map, dt, 2, base, dims, strides, box,
+                      swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 inline int elem_size(int dtype) { return dtype == 0 ? 4 : 2; }

@@ -1,0 +1,115 @@
+// Device helpers of the kernels with 4-bit weights: tiles of rows, and codes as 16-bit
+// integers.
+#pragma once
+
+#include "mx.cuh"
+#include "q4.h"
+
+namespace dgemm {
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* desc, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// (a & b) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t fma_x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  if constexpr (__is_same(T, __half))
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  else
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mul_x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (__is_same(T, __half))
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Volatile, so that no load moves past the arrival that gives its stage back.
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Tile `slot` of the rows, tile_rows each: its expert (-1: there is no such tile) and
+// rows [lo, hi).  By one warp; offsets are put in order as group_sched.cuh does.
+struct Q4Rows {
+  int expert, lo, hi;
+};
+__device__ __forceinline__ Q4Rows q4_rows_of_slot(int slot, const Q4FewParams& p) {
+  Q4Rows r;
+  if (p.experts == 0) {
+    r.expert = 0;
+    r.lo = slot * p.tile_rows;
+    r.hi = min(r.lo + p.tile_rows, p.rows);
+    return r;
+  }
+  r.expert = -1, r.lo = r.hi = 0;
+  const int lane = threadIdx.x & 31;
+  int last = 0, tiles = 0;
+  bool bad = false;
+  for (int base = 0; base <= p.experts; base += 32) {
+    const int i = base + lane;
+    const int raw = i <= p.experts ? p.offsets[i] : p.rows;
+    const int own = min(max(raw, 0), p.rows);
+    int v = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, last);
+    bad |= own != raw || v != own;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = last;
+    const int mine = i >= 1 && i <= p.experts ? (v - before + p.tile_rows - 1) / p.tile_rows : 0;
+    int n = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    // (Lane i has the end of expert i - 1, whose tiles end at tiles + n.)
+    const unsigned here =
+        __ballot_sync(0xffffffffu, slot < tiles + n && slot >= tiles + n - mine);
+    if (here != 0 && r.expert < 0) {
+      const int src = __ffs(here) - 1;
+      r.expert = base + src - 1;
+      const int first = __shfl_sync(0xffffffffu, tiles + n - mine, src);
+      r.lo = __shfl_sync(0xffffffffu, before, src) + (slot - first) * p.tile_rows;
+      r.hi = min(r.lo + p.tile_rows, __shfl_sync(0xffffffffu, v, src));
+    }
+    tiles += __shfl_sync(0xffffffffu, n, 31);
+    last = __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0 && slot == 0)
+    raise_fault(p.fault, kFaultGroupOffsets);
+  return r;
+}
+
+}  // namespace dgemm

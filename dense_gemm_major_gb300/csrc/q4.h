@@ -39,6 +39,15 @@ inline int q4_tile_rows(int rows) {
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream);
 
+// More rows: 128 columns of Y for up to 128 rows of one expert, over a share of K.
+constexpr int kQ4RowsTileN = 128;
+constexpr int kQ4RowsBK = 128;
+inline int q4_rows_tile(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+// tmQ: the codes with boxes of 64 x 128 x 1, 64-byte swizzled; tmX: boxes of 64 x
+// tile_rows.
+cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
+                           const CUtensorMap* tmX, cudaStream_t stream);
+
 // D (experts x N rows of K values of dtype, pitch ldd, a multiple of 8) := the
 // weights of `experts` matrices, or N rows of them: their codes stride_q bytes apart,
 // their scales and zeros scale_n to a group.  Experts without rows by `offsets`

@@ -33,19 +33,21 @@ struct Q4Call {
   int matrices() const { return experts == 0 ? 1 : experts; }
 };
 
-// The product by the kernel for few rows; `expect`: rows of an expert to expect.
-gemm_status_t run_few(const Q4Call& c, int expect, cudaStream_t stream) {
+// The product by one of the kernels that read the codes (few: the one for few rows);
+// `expect`: rows of an expert to expect.
+gemm_status_t run_codes(const Q4Call& c, bool few, int expect, cudaStream_t stream) {
   dgemm::Q4FewParams p;
   p.rows = c.rows, p.N = c.N, p.K = c.K, p.group = c.group;
   p.experts = c.experts, p.offsets = c.offsets;
-  p.tile_rows = dgemm::q4_tile_rows(expect);
+  p.tile_rows = few ? dgemm::q4_tile_rows(expect) : dgemm::q4_rows_tile(expect);
   p.slots = c.experts == 0 ? ceil_div(c.rows, p.tile_rows)
                            : c.rows / p.tile_rows + (c.experts < c.rows ? c.experts : c.rows);
   // CTAs that share a tile's K: as many (a cluster of at most 8) as keep one wave,
   // each with a stage at least.
-  const long long tiles = (long long)ceil_div(c.N, dgemm::kQ4TileN) * p.slots;
-  const int nk = ceil_div(c.K, dgemm::kQ4BK);
-  const int room = 2 * c.pairs * (p.tile_rows <= 16 ? 2 : 1);
+  const int tile_n = few ? dgemm::kQ4TileN : dgemm::kQ4RowsTileN;
+  const long long tiles = (long long)ceil_div(c.N, tile_n) * p.slots;
+  const int nk = ceil_div(c.K, few ? dgemm::kQ4BK : dgemm::kQ4RowsBK);
+  const int room = 2 * c.pairs * (few && p.tile_rows <= 16 ? 2 : 1);
   p.split = 1;
   while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= room) p.split *= 2;
   p.scales = c.scales, p.zeros = c.zeros;
@@ -55,11 +57,13 @@ gemm_status_t run_few(const Q4Call& c, int expect, cudaStream_t stream) {
   const cuuint64_t dims[3] = {(cuuint64_t)((c.K + 1ll) / 2), (cuuint64_t)c.N,
                               (cuuint64_t)c.matrices()};
   const cuuint64_t strides[2] = {(cuuint64_t)c.ldq, (cuuint64_t)c.N * c.ldq};
-  const cuuint32_t box[3] = {128, dgemm::kQ4TileN, 1};
-  if (!encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, box) ||
+  const cuuint32_t box[3] = {few ? 128u : 64u, (cuuint32_t)tile_n, 1};
+  if (!encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, box,
+                    few ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
       !encode_rows(&tmX, c.dtype, c.x, (uint32_t)p.tile_rows))
     return GEMM_ERR_LAUNCH;
-  return status_of(dgemm::launch_q4_few(c.dtype, p, &tmQ, &tmX, stream));
+  return status_of(few ? dgemm::launch_q4_few(c.dtype, p, &tmQ, &tmX, stream)
+                       : dgemm::launch_q4_rows(c.dtype, p, &tmQ, &tmX, stream));
 }
 
 // The product with the weights in 16 bits, in parts of them that fit the workspace:
@@ -155,6 +159,9 @@ extern "C" gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, i
   Operand none{nullptr, 0, 0, 0, 1, 0, false};
   if ((st = align_operands(c.x, none, workspaces, stream)) != GEMM_OK) return st;
   const int expect = experts == 0 ? rows : ceil_div(rows, experts);
-  static const int few_rows = [] { const char* s = getenv("Q4_FEW"); return s ? atoi(s) : 128; }();
-  return expect <= few_rows ? run_few(c, expect, stream) : run_values(c, workspaces, stream);
+  static const int few_rows = [] { const char* s = getenv("Q4_FEW"); return s ? atoi(s) : 8; }();
+  static const int mid_rows = [] { const char* s = getenv("Q4_MID"); return s ? atoi(s) : 128; }();
+  if (expect <= few_rows) return run_codes(c, true, expect, stream);
+  if (expect <= mid_rows) return run_codes(c, false, expect, stream);
+  return run_values(c, workspaces, stream);
 }

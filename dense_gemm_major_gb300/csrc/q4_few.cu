@@ -14,8 +14,7 @@
 // 4), (1, 5), (2, 6), (3, 7), one mask and shift each, and X's eight values are
 // permuted the same way.  The four ranges of K and then the CTAs of the cluster are
 // added in their order.
-#include "mx.cuh"
-#include "q4.h"
+#include "q4.cuh"
 
 namespace dgemm {
 namespace {
@@ -48,15 +47,6 @@ struct alignas(8) Barriers {
   int abort;
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* desc, uint32_t bar,
-                                            int32_t x, int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 template <typename T>
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
@@ -72,22 +62,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// (a & b) | c
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ uint32_t fma_x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  if constexpr (__is_same(T, __half))
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  else
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
 }
 
 // A zero as what is added to codes: -(128 + z) in BF16; in FP16 -(1024 + z) and
@@ -125,81 +99,10 @@ __device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, ui
   }
 }
 
-// Volatile, so that no load moves past the arrival that gives its stage back.
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
-}
-
-// Tile `slot` of the rows: its expert (-1: there is no such tile) and rows [lo, hi).
-// By one warp; offsets are put in order as group_gemm.cu does.
-struct Rows {
-  int expert, lo, hi;
-};
-__device__ __forceinline__ Rows rows_of_slot(int slot, const Q4FewParams& p) {
-  Rows r;
-  if (p.experts == 0) {
-    r.expert = 0;
-    r.lo = slot * p.tile_rows;
-    r.hi = min(r.lo + p.tile_rows, p.rows);
-    return r;
-  }
-  r.expert = -1, r.lo = r.hi = 0;
-  const int lane = threadIdx.x & 31;
-  int last = 0, tiles = 0;
-  bool bad = false;
-  for (int base = 0; base <= p.experts; base += 32) {
-    const int i = base + lane;
-    const int raw = i <= p.experts ? p.offsets[i] : p.rows;
-    const int own = min(max(raw, 0), p.rows);
-    int v = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v = max(v, o);
-    }
-    v = max(v, last);
-    bad |= own != raw || v != own;
-    int before = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) before = last;
-    const int mine = i >= 1 && i <= p.experts ? (v - before + p.tile_rows - 1) / p.tile_rows : 0;
-    int n = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, n, d);
-      if (lane >= d) n += o;
-    }
-    // (Lane i has the end of expert i - 1, whose tiles end at tiles + n.)
-    const unsigned here =
-        __ballot_sync(0xffffffffu, slot < tiles + n && slot >= tiles + n - mine);
-    if (here != 0 && r.expert < 0) {
-      const int src = __ffs(here) - 1;
-      r.expert = base + src - 1;
-      const int first = __shfl_sync(0xffffffffu, tiles + n - mine, src);
-      r.lo = __shfl_sync(0xffffffffu, before, src) + (slot - first) * p.tile_rows;
-      r.hi = min(r.lo + p.tile_rows, __shfl_sync(0xffffffffu, v, src));
-    }
-    tiles += __shfl_sync(0xffffffffu, n, 31);
-    last = __shfl_sync(0xffffffffu, v, 31);
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0 && slot == 0)
-    raise_fault(p.fault, kFaultGroupOffsets);
-  return r;
 }
 
 // kEach: a scale for each step of 32 terms; else for each warp's slice of a stage
@@ -215,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
   float* const sums = reinterpret_cast<float*>(base);
   auto* bars = reinterpret_cast<Barriers<S>*>(base + S * L::kStage);
   static_assert(sizeof(Barriers<S>) <= 256, "barrier block must fit its reserved space");
-  __shared__ Rows s_rows;
+  __shared__ Q4Rows s_rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
   const int n0 = (int)(blockIdx.x / (unsigned)p.split) * kQ4TileN;
@@ -236,11 +139,11 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
   wait_prior_grids();
   allow_dependent_grids();
   if (warp == 0) {
-    const Rows r = rows_of_slot((int)blockIdx.y, p);
+    const Q4Rows r = q4_rows_of_slot((int)blockIdx.y, p);
     if (lane == 0) s_rows = r;
   }
   __syncthreads();
-  const Rows rows = s_rows;
+  const Q4Rows rows = s_rows;
   if (rows.expert < 0) return;   // (the same in all of a cluster)
 
   uint32_t issued = 0;

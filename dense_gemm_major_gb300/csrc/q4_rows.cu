@@ -1,0 +1,395 @@
+// Products of up to 128 rows with 4-bit weights and group scales on tcgen05:
+// Y = X . W^T, the weights rounded to X's type on the way.
+//
+// Bound by reading the codes and by the instructions that make 16-bit values of them
+// (for eight codes 9 of the integer and 8 of the FMA pipe, each at half rate), which
+// do not depend on the number of rows; so W is the MMA's M side (128 rows per CTA), X
+// its N side (16 to 128).  The values go to tensor memory, from where the MMA reads its
+// A: through shared memory they would be written and read at four times the codes'
+// bytes, which is what bounded a first version (8192 x 8192, 16 rows: 19.8 us).  A
+// thread has a row of W, as a lane of tensor memory has.  So that W's bytes travel to all
+// SMs at once, the CTAs of a cluster share a tile's K; they add their FP32 partial
+// tiles through distributed shared memory in rank order, so results are reproducible and
+// there is no workspace.
+//
+// Roles (640 threads): warp 0 loads the codes (TMA) into a ring of their own, warp 1
+// issues the MMAs, warp 2 loads X, warps 4-19 convert: two groups of 8 warps take turns
+// at 128-deep stages, so that one's waits pass while the other converts.  Warps 4-7
+// then drain the accumulator.
+#include "q4.cuh"
+
+namespace dgemm {
+namespace {
+
+constexpr int BN = kQ4RowsTileN, BK = kQ4RowsBK;
+constexpr int kThreads = 640;
+constexpr int kConvWarp = 4, kGroups = 2, kGroupWarps = 8;
+constexpr uint32_t kRawBytes = BN * BK / 2;                 // 8 KB
+constexpr uint32_t kACols = BK / 2;                         // of tensor memory, a stage of W
+
+// MT: rows of X that the MMA computes.
+template <int MT>
+struct Layout {
+  static constexpr uint32_t kXBlock = MT * 128;             // 64 k of X
+  static constexpr uint32_t kStage = 2 * kXBlock;
+  // (Even numbers: a slot's stages all fall to one group of converting warps, which
+  // therefore never waits for a phase whose predecessor it has not seen.)
+  static constexpr int S = MT <= 64 ? 6 : 4, R = MT <= 64 ? 12 : 10;
+  static_assert(S % kGroups == 0 && R % kGroups == 0, "one group per slot");
+  static constexpr uint32_t kSmem = S * kStage + R * kRawBytes + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(MT * BN * 4 <= S * kStage + R * kRawBytes, "partial tiles reuse the rings");
+  // Tensor memory: the accumulator, then W's stages.
+  static constexpr uint32_t kACol = MT < 32 ? 32 : MT;
+  static_assert(kACol + S * kACols <= 512, "tensor memory");
+};
+
+template <int S, int R>
+struct alignas(8) Barriers {
+  uint64_t full[S];       // X loaded, W converted
+  uint64_t empty[S];
+  uint64_t raw_full[R];
+  uint64_t raw_empty[R];
+  uint64_t acc_full;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// 16-deep step with A in tensor memory: 128 lanes by 8 columns of pairs.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Eight codes as four pairs of weights, in the order of their columns: z -(128 + zero)
+// in BF16, -(1024 + zero) in FP16, twice; s the scale, twice.
+template <typename T>
+__device__ __forceinline__ void weights8(uint32_t w, uint32_t z, uint32_t s, uint32_t* v) {
+  constexpr uint32_t kOne = __is_same(T, __half) ? 0x3C003C00u : 0x3F803F80u;
+  constexpr uint32_t kBase = __is_same(T, __half) ? 0x64006400u : 0x43004300u;
+  const uint32_t h = w >> 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // Byte j of the low and of the high halves; the other bytes are masked away.
+    const uint32_t x = __byte_perm(w, h, (j + 4) * 0x1100 + j * 0x11);
+    v[j] = mul_x2<T>(fma_x2<T>(and_or(x, 0x000F000Fu, kBase), kOne, z), s);
+  }
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+    q4_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
+                   const Q4FewParams p) {
+  using L = Layout<MT>;
+  constexpr int S = L::S, R = L::R;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const base = align_smem_1024(smem_raw);
+  unsigned char* const raw_base = base + S * L::kStage;
+  auto* bars = reinterpret_cast<Barriers<S, R>*>(raw_base + R * kRawBytes);
+  static_assert(sizeof(Barriers<S, R>) <= 512, "barrier block must fit its reserved space");
+  __shared__ Q4Rows s_rows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int n0 = (int)(blockIdx.x / (unsigned)p.split) * BN;
+  const int nk = (p.K + BK - 1) / BK;
+  const int kb = (int)((long long)rank * nk / p.split);
+  const int ke = (int)((long long)(rank + 1) * nk / p.split);
+  constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bars->full[s]), 1 + kGroupWarps);
+      mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    for (int r = 0; r < R; ++r) {
+      mbar_init(smem_u32(&bars->raw_full[r]), 1);
+      mbar_init(smem_u32(&bars->raw_empty[r]), kGroupWarps);
+    }
+    mbar_init(smem_u32(&bars->acc_full), 1);
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), 512);
+  wait_prior_grids();
+  allow_dependent_grids();
+  if (warp == 2) {
+    const Q4Rows r = q4_rows_of_slot((int)blockIdx.y, p);
+    if (lane == 0) s_rows = r;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_base;
+  const Q4Rows rows = s_rows;
+  if (rows.expert < 0) {   // (the same in all of a cluster)
+    if (warp == 1) tmem_dealloc(tmem_base, 512);
+    return;
+  }
+
+  uint32_t issued = 0;
+  if (warp == 0) {
+    if (elect_one()) {
+      // ---------------------------------------------- codes
+      RingPos<R> pos;
+      for (int kt = kb; kt < ke; ++kt, pos.next()) {
+        if (!role_wait(smem_u32(&bars->raw_empty[pos.slot]), pos.parity ^ 1u, p.fault,
+                       p.timeout_ns, &bars->abort, kFaultTcProducerWait, true))
+          break;
+        const uint32_t full = smem_u32(&bars->raw_full[pos.slot]);
+        mbar_arrive_expect_tx(full, kRawBytes);
+        tma_load_3d(smem_u32(raw_base + pos.slot * kRawBytes), &tmQ, full, kt * (BK / 2), n0,
+                    rows.expert);
+        ++issued;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    if (elect_one()) {
+      // ---------------------------------------------- X
+      RingPos<S> pos;
+      for (int kt = kb; kt < ke; ++kt, pos.next()) {
+        if (!role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                       &bars->abort, kFaultTcProducerWait, true))
+          break;
+        const uint32_t full = smem_u32(&bars->full[pos.slot]);
+        const uint32_t to = smem_u32(base + pos.slot * L::kStage);
+        mbar_arrive_expect_tx(full, 2 * L::kXBlock);
+        tma_load_2d(to, &tmX, full, kt * BK, rows.lo);
+        tma_load_2d(to + L::kXBlock, &tmX, full, kt * BK + 64, rows.lo);
+        ++issued;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one()) {
+      // ---------------------------------------------- MMA issuer
+      RingPos<S> pos;
+      bool ok = true;
+      for (int kt = kb; kt < ke; ++kt, pos.next()) {
+        ok = role_wait(smem_u32(&bars->full[pos.slot]), pos.parity, p.fault, p.timeout_ns,
+                       &bars->abort, kFaultTcMmaWait, true);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(base + pos.slot * L::kStage);
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k)
+          mma_f16_ta(tmem_base, tmem_base + L::kACol + pos.slot * kACols + k * 8,
+                     kmajor_desc(st + (k >> 2) * L::kXBlock, k & 3),
+                     instr_desc(kAb, BN, MT, 0, 0), (kt > kb || k > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&bars->empty[pos.slot]));
+      }
+      if (ok) mma_commit(smem_u32(&bars->acc_full));
+    }
+    __syncwarp();
+  } else if (warp >= kConvWarp) {
+    // ------------------------------------------------ conversion
+    // A thread of its group: a row, and 64 of a stage's 128 columns.
+    const int group = (warp - kConvWarp) / kGroupWarps;
+    // (A warp reaches the lanes 32 (warp % 4) .. + 31.)
+    const int row = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
+    const int n = n0 + row;
+    const bool real = n < p.N;
+    const long long first =
+        (long long)rows.expert * ((p.K + p.group - 1) / p.group) * p.N + n;
+    const uint16_t* const scales = static_cast<const uint16_t*>(p.scales) + first;
+    const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + first : nullptr;
+    // The scales and zeros of its two runs of 32 columns, read a turn ahead.
+    uint16_t sc[2];
+    unsigned char zr[2];
+    const int far_at = kGroups * BK / p.group, far_pos = kGroups * BK % p.group;
+    int at = ((kb + group) * BK + half * 64) / p.group;
+    int pos_in = ((kb + group) * BK + half * 64) % p.group;
+    auto read_scales = [&](int kt) {
+      int a = at, q = pos_in;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool ok = real && kt < ke && kt * BK + half * 64 + i * 32 < p.K;
+        const long long to = (long long)a * p.N;
+        sc[i] = ok ? scales[to] : (uint16_t)0;
+        zr[i] = ok && zeros != nullptr ? zeros[to] : (unsigned char)8;
+        if ((q += 32) == p.group) q = 0, ++a;
+      }
+    };
+    // 64-byte rows, 16-byte chunks swizzled by the row's bits 1 and 2.
+    uint32_t from[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      from[i] = row * 64 + (((half * 2 + i) ^ ((row >> 1) & 3)) << 4);
+    const uint32_t to = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + L::kACol + half * 32;
+    read_scales(kb + group);
+    uint32_t it = (uint32_t)group;
+    bool ok = true;
+    for (int kt = kb + group; kt < ke; kt += kGroups, it += kGroups) {
+      const uint32_t r = it % R, s = it % S;
+      uint32_t sv[2], zv[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sv[i] = sc[i] * 0x00010001u;
+        zv[i] = (__is_same(T, __half) ? 0xE400E400u : 0xC300C300u) + (zr[i] & 15u) * 0x00010001u;
+      }
+      at += far_at;
+      if ((pos_in += far_pos) >= p.group) pos_in -= p.group, ++at;
+      read_scales(kt + kGroups);
+      // (Both tries are on their way at once.)
+      const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), (it / R) & 1u);
+      const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u);
+      ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), (it / R) & 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcProducerWait, loaded);
+      if (!ok) break;
+      const uint32_t raw = smem_u32(raw_base) + r * kRawBytes;
+      const uint4 q0 = ld_shared_v4(raw + from[0]), q1 = ld_shared_v4(raw + from[1]);
+      const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      uint32_t a[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) weights8<T>(w[j], zv[j >> 2], sv[j >> 2], a + 4 * j);
+      // (The fence waits for the loads, before TMA refills the slot.)
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
+      ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcProducerWait, freed);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_st32(to + s * kACols, a);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->full[s]));
+    }
+    // ------------------------------------------------ draining
+    if (warp < kConvWarp + 4) {
+      ok = ok && role_wait_lanes(smem_u32(&bars->acc_full), 0u, p.fault, p.timeout_ns,
+                                 &bars->abort, kFaultTcEpilogueWait);
+      tc_fence_after();
+      const int col = (warp & 3) * 32 + lane;
+      const uint32_t lanes = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
+      const int m_end = rows.hi - rows.lo;
+#pragma unroll 1
+      for (int c = 0; c < MT / 16 && c * 16 < m_end; ++c) {
+        uint32_t r[16];
+        tmem_ld16(lanes + c * 16, r);
+        if (p.split > 1) {
+          // The partial tile, row-major, where the ring was.
+          float* const part = reinterpret_cast<float*>(base) + c * 16 * BN + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[j * BN] = __uint_as_float(r[j]);
+        } else if (n0 + col < p.N) {
+          T* const y = static_cast<T*>(p.Y) + (long long)(rows.lo + c * 16) * p.ldy + n0 + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c * 16 + j < m_end) y[j * p.ldy] = from_f32_any<T>(__uint_as_float(r[j]));
+        }
+      }
+    }
+  }
+  if (p.split > 1) {
+    // ------------------------------------------------ sum of the cluster's partial tiles
+    cluster_sync_all();
+    // This CTA adds up BN / split of the columns, four of a row per thread, all partial
+    // tiles' values on their way at once.
+    constexpr int kMaxSplit = 8;
+    const int share = BN / p.split / 4;
+    for (int i = threadIdx.x; i < share * (rows.hi - rows.lo); i += kThreads) {
+      const int m = i / share;
+      const int col = (rank * share + (i - m * share)) * 4;
+      const uint32_t from = smem_u32(base) + (uint32_t)(m * BN + col) * 4u;
+      float4 v[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        v[r] = r < p.split ? ld_cluster_v4(mapa_shared(from, (uint32_t)r))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r) {
+        sum[0] += v[r].x;
+        sum[1] += v[r].y;
+        sum[2] += v[r].z;
+        sum[3] += v[r].w;
+      }
+      T* const y = static_cast<T*>(p.Y) + (long long)(rows.lo + m) * p.ldy + n0 + col;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n0 + col + j < p.N) y[j] = from_f32_any<T>(sum[j]);
+    }
+    cluster_sync_all();   // no CTA leaves while others read its partial tile
+  }
+
+  // ------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if ((warp == 0 || warp == 2) && elect_one() && bars->abort) {
+    // Let the copies in flight land; a stage of which conversions are missing makes
+    // the wait give up.
+    const uint32_t n = warp == 0 ? R : S;
+    for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i) {
+      const uint64_t* const bar = warp == 0 ? &bars->raw_full[i % R] : &bars->full[i % S];
+      if (!mbar_wait_bounded(smem_u32(bar), (i / n) & 1u, p.timeout_ns, nullptr)) {
+        raise_fault(p.fault, kFaultDrainWait);
+        break;
+      }
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    if (elect_one() && bars->abort) {
+      // (Otherwise acc_full has shown every MMA to be done.)
+      mma_commit(smem_u32(&bars->drain));
+      if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
+        raise_fault(p.fault, kFaultDrainWait);
+    }
+    __syncwarp();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <typename T, int MT>
+cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
+                        cudaStream_t stream) {
+  auto kernel = q4_rows_kernel<T, MT>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = mx_allow_smem(kernel, Layout<MT>::kSmem, &done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = ((long long)p.N + BN - 1) / BN;
+  return launch_gemm_kernel_clusters((unsigned)p.split, kernel,
+                                     dim3((unsigned)(tiles * p.split), (unsigned)p.slots),
+                                     dim3(kThreads), Layout<MT>::kSmem, stream, *tmQ, *tmX, p);
+}
+
+template <typename T>
+cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
+                         cudaStream_t stream) {
+  switch (p.tile_rows) {
+    case 16: return launch_rows<T, 16>(p, q, x, stream);
+    case 32: return launch_rows<T, 32>(p, q, x, stream);
+    case 64: return launch_rows<T, 64>(p, q, x, stream);
+    case 128: return launch_rows<T, 128>(p, q, x, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
+                           const CUtensorMap* tmX, cudaStream_t stream) {
+  return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)
+                    : launch_typed<__nv_bfloat16>(p, tmQ, tmX, stream);
+}
+
+}  // namespace dgemm

@@ -53,10 +53,11 @@ def _weights(dg, gen, lead, K, dtype, group, zeros, pad=0):
     return dg.Q4Tensor(codes, scales, z, cols=K, group=group), values
 
 
-def _check(got, x, values, K, dtype, rounded):
+def _check(got, x, values, K, dtype, rounded=True):
     """got within the bound of x . values^T.  rounded: the weights may have been
-    rounded to dtype (half a unit each).  A group's sum is multiplied by its scale and
-    added to a running sum: two more roundings of FP32 for every 32 terms."""
+    rounded to dtype (half a unit each), as they are for more than FEW rows.  A group's
+    sum is multiplied by its scale and added to a running sum: two more roundings of
+    FP32 for every 32 terms."""
     p, total = x.double() @ values.t(), x.double().abs() @ values.abs().t()
     lim = torch.from_numpy(ref.bound(p.cpu().numpy(), total.cpu().numpy(), 2 * K + 512, dtype))
     if rounded:
@@ -91,7 +92,7 @@ def test_dense(dg, dtype, zeros, shape):
     inside = torch.zeros_like(wide, dtype=torch.bool)
     inside[1:rows + 1, 2:2 + N] = True
     assert (wide[~inside] == 7.0).all()
-    _check(y, x, values, K, dtype, rows > 64)
+    _check(y, x, values, K, dtype, rows > 8)
     assert torch.equal(dg.q4_linear(x, w), y)
 
 
@@ -105,7 +106,7 @@ def test_long_rows(dg, dtype, group, rows):
     x = _x(gen, rows, 8192, dtype)
     w, values = _weights(dg, gen, (8192,), 8192, dtype, group, True)
     y = dg.q4_linear(x, w)
-    _check(y, x, values, 8192, dtype, False)
+    _check(y, x, values, 8192, dtype, rows > 8)
     for _ in range(5):
         assert torch.equal(dg.q4_linear(x, w), y)
     check_device(dg)
@@ -172,7 +173,7 @@ def test_special_values_stay_in_their_row_and_column(dg, rows):
     assert y[1].isnan().all() and y[:, 77].isnan().all()
     keep_r = torch.tensor([r for r in range(rows) if r != 1], device="cuda")
     keep_c = torch.tensor([c for c in range(130) if c != 77], device="cuda")
-    _check(y[keep_r][:, keep_c], x[keep_r], values[keep_c], 512, "bf16", rows > 64)
+    _check(y[keep_r][:, keep_c], x[keep_r], values[keep_c], 512, "bf16", rows > 8)
     check_device(dg)
 
 
@@ -181,11 +182,11 @@ def test_contiguous_x_of_any_width(dg, rows):
     gen = torch.Generator("cuda").manual_seed(5)
     x = torch.randn((rows, 333), generator=gen, device="cuda").half()
     w, values = _weights(dg, gen, (96,), 333, "f16", 64, True)
-    _check(dg.q4_linear(x, w), x, values, 333, "f16", rows > 64)
+    _check(dg.q4_linear(x, w), x, values, 333, "f16", rows > 8)
     buf = torch.randn(rows * 512 + 1, generator=gen, device="cuda").half()
     x = buf[1:].view(rows, 512)                       # packed, not 16-byte aligned
     w, values = _weights(dg, gen, (96,), 512, "f16", 64, False)
-    _check(dg.q4_linear(x, w), x, values, 512, "f16", rows > 64)
+    _check(dg.q4_linear(x, w), x, values, 512, "f16", rows > 8)
     check_device(dg)
 
 
