@@ -43,8 +43,7 @@ cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tm
 constexpr int kQ4RowsTileN = 128;
 constexpr int kQ4RowsBK = 128;
 inline int q4_rows_tile(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
-// tmQ: the codes with boxes of 64 x 128 x 1, 64-byte swizzled; tmX: boxes of 64 x
-// tile_rows.
+// tmQ: the codes with boxes of 128 x 128 x 1; tmX: boxes of 64 x tile_rows.
 cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                            const CUtensorMap* tmX, cudaStream_t stream);
 

@@ -46,7 +46,7 @@ gemm_status_t run_codes(const Q4Call& c, bool few, int expect, cudaStream_t stre
   // each with a stage at least.
   const int tile_n = few ? dgemm::kQ4TileN : dgemm::kQ4RowsTileN;
   const long long tiles = (long long)ceil_div(c.N, tile_n) * p.slots;
-  const int nk = ceil_div(c.K, few ? dgemm::kQ4BK : dgemm::kQ4RowsBK);
+  const int nk = ceil_div(c.K, few ? dgemm::kQ4BK : 2 * dgemm::kQ4RowsBK);
   const int room = 2 * c.pairs * (few && p.tile_rows <= 16 ? 2 : 1);
   p.split = 1;
   while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= room) p.split *= 2;
@@ -57,9 +57,8 @@ gemm_status_t run_codes(const Q4Call& c, bool few, int expect, cudaStream_t stre
   const cuuint64_t dims[3] = {(cuuint64_t)((c.K + 1ll) / 2), (cuuint64_t)c.N,
                               (cuuint64_t)c.matrices()};
   const cuuint64_t strides[2] = {(cuuint64_t)c.ldq, (cuuint64_t)c.N * c.ldq};
-  const cuuint32_t box[3] = {few ? 128u : 64u, (cuuint32_t)tile_n, 1};
-  if (!encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, box,
-                    few ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+  const cuuint32_t box[3] = {128, (cuuint32_t)tile_n, 1};
+  if (!encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, box) ||
       !encode_rows(&tmX, c.dtype, c.x, (uint32_t)p.tile_rows))
     return GEMM_ERR_LAUNCH;
   return status_of(few ? dgemm::launch_q4_few(c.dtype, p, &tmQ, &tmX, stream)

@@ -13,8 +13,8 @@
 // there is no workspace.
 //
 // Roles (640 threads): warp 0 loads the codes (TMA) into a ring of their own, warp 1
-// issues the MMAs, warp 2 loads X, warps 4-19 convert: two groups of 8 warps take turns
-// at 128-deep stages, so that one's waits pass while the other converts.  Warps 4-7
+// issues the MMAs, warp 2 loads X, warps 4-19 convert: four groups of 4 warps take turns
+// at 128-deep stages, so that one's waits pass while the others convert.  Warps 4-7
 // then drain the accumulator.
 #include "q4.cuh"
 
@@ -23,8 +23,10 @@ namespace {
 
 constexpr int BN = kQ4RowsTileN, BK = kQ4RowsBK;
 constexpr int kThreads = 640;
-constexpr int kConvWarp = 4, kGroups = 2, kGroupWarps = 8;
-constexpr uint32_t kRawBytes = BN * BK / 2;                 // 8 KB
+constexpr int kConvWarp = 4, kGroups = 4, kGroupWarps = 4;
+// A slot of codes is two stages deep: 128 bytes of each row.  (With one stage, 64
+// bytes, the loads were what took longest: 16.9 against ... us.)
+constexpr uint32_t kRawBytes = BN * BK;                     // 16 KB
 constexpr uint32_t kACols = BK / 2;                         // of tensor memory, a stage of W
 
 // MT: rows of X that the MMA computes.
@@ -32,10 +34,12 @@ template <int MT>
 struct Layout {
   static constexpr uint32_t kXBlock = MT * 128;             // 64 k of X
   static constexpr uint32_t kStage = 2 * kXBlock;
-  // (Even numbers: a slot's stages all fall to one group of converting warps, which
-  // therefore never waits for a phase whose predecessor it has not seen.)
-  static constexpr int S = MT <= 64 ? 6 : 4, R = MT <= 64 ? 12 : 10;
-  static_assert(S % kGroups == 0 && R % kGroups == 0, "one group per slot");
+  // A group may only wait for a phase whose predecessor is known to be over.  Slots of
+  // codes: their number is even, so that each is read by the same two groups every time.
+  // Stages: the MMAs free them in order, and a group has seen the one freed that it
+  // waited for kGroups stages ago, so that there need to be that many.
+  static constexpr int S = MT <= 64 ? 6 : 4, R = 6;
+  static_assert(S >= kGroups && R % 2 == 0, "phases");
   static constexpr uint32_t kSmem = S * kStage + R * kRawBytes + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(MT * BN * 4 <= S * kStage + R * kRawBytes, "partial tiles reuse the rings");
@@ -90,7 +94,9 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-template <typename T, int MT>
+// kEach: a scale for each run of 32 columns; else for each stage (groups of a multiple of
+// 128).
+template <typename T, int MT, bool kEach>
 __global__ void __launch_bounds__(kThreads, 1)
     q4_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                    const Q4FewParams p) {
@@ -105,9 +111,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
   const int n0 = (int)(blockIdx.x / (unsigned)p.split) * BN;
-  const int nk = (p.K + BK - 1) / BK;
-  const int kb = (int)((long long)rank * nk / p.split);
-  const int ke = (int)((long long)(rank + 1) * nk / p.split);
+  // k-tiles [kb, ke), from an even one on.
+  const int nk = (p.K + BK - 1) / BK, nk2 = (nk + 1) / 2;
+  const int kb = 2 * (int)((long long)rank * nk2 / p.split);
+  const int ke = min(2 * (int)((long long)(rank + 1) * nk2 / p.split), nk);
   constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
 
   if (threadIdx.x == 0) {
@@ -117,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int r = 0; r < R; ++r) {
       mbar_init(smem_u32(&bars->raw_full[r]), 1);
-      mbar_init(smem_u32(&bars->raw_empty[r]), kGroupWarps);
+      mbar_init(smem_u32(&bars->raw_empty[r]), 2 * kGroupWarps);
     }
     mbar_init(smem_u32(&bars->acc_full), 1);
     mbar_init(smem_u32(&bars->drain), 1);
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       // ---------------------------------------------- codes
       RingPos<R> pos;
-      for (int kt = kb; kt < ke; ++kt, pos.next()) {
+      for (int kt = kb; kt < ke; kt += 2, pos.next()) {
         if (!role_wait(smem_u32(&bars->raw_empty[pos.slot]), pos.parity ^ 1u, p.fault,
                        p.timeout_ns, &bars->abort, kFaultTcProducerWait, true))
           break;
@@ -200,78 +207,91 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------ conversion
-    // A thread of its group: a row, and 64 of a stage's 128 columns.
+    // A thread of its group has a row.  (A warp reaches the lanes 32 (warp % 4) .. + 31.)
+    constexpr int kRuns = kEach ? BK / 32 : 1;
     const int group = (warp - kConvWarp) / kGroupWarps;
-    // (A warp reaches the lanes 32 (warp % 4) .. + 31.)
-    const int row = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
+    const int row = (warp & 3) * 32 + lane;
     const int n = n0 + row;
     const bool real = n < p.N;
     const long long first =
         (long long)rows.expert * ((p.K + p.group - 1) / p.group) * p.N + n;
     const uint16_t* const scales = static_cast<const uint16_t*>(p.scales) + first;
     const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + first : nullptr;
-    // The scales and zeros of its two runs of 32 columns, read a turn ahead.
-    uint16_t sc[2];
-    unsigned char zr[2];
+    // The scales and zeros of its runs, read a turn ahead and left as they come.
+    uint16_t sc[kRuns];
+    unsigned char zr[kRuns];
     const int far_at = kGroups * BK / p.group, far_pos = kGroups * BK % p.group;
-    int at = ((kb + group) * BK + half * 64) / p.group;
-    int pos_in = ((kb + group) * BK + half * 64) % p.group;
+    int at = (kb + group) * BK / p.group;
+    int pos_in = (kb + group) * BK % p.group;
     auto read_scales = [&](int kt) {
       int a = at, q = pos_in;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool ok = real && kt < ke && kt * BK + half * 64 + i * 32 < p.K;
+      for (int i = 0; i < kRuns; ++i) {
+        const bool ok = real && kt < ke && kt * BK + i * 32 < p.K;
         const long long to = (long long)a * p.N;
         sc[i] = ok ? scales[to] : (uint16_t)0;
         zr[i] = ok && zeros != nullptr ? zeros[to] : (unsigned char)8;
         if ((q += 32) == p.group) q = 0, ++a;
       }
     };
-    // 64-byte rows, 16-byte chunks swizzled by the row's bits 1 and 2.
-    uint32_t from[2];
+    // 16-byte chunks in 128-byte rows are swizzled by the row; a stage has four.
+    uint32_t from[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      from[i] = row * 64 + (((half * 2 + i) ^ ((row >> 1) & 3)) << 4);
-    const uint32_t to = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + L::kACol + half * 32;
+    for (int i = 0; i < 4; ++i)
+      from[i] = row * 128 + ((((group & 1) * 4 + i) ^ (row & 7)) << 4);
+    const uint32_t to = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + L::kACol;
     read_scales(kb + group);
     uint32_t it = (uint32_t)group;
     bool ok = true;
     for (int kt = kb + group; kt < ke; kt += kGroups, it += kGroups) {
-      const uint32_t r = it % R, s = it % S;
-      uint32_t sv[2], zv[2];
+      const uint32_t r = (it / 2) % R, s = it % S;
+      const uint32_t raw_parity = (it / 2 / R) & 1u, parity = ((it / S) & 1u) ^ 1u;
+      // (Both tries are on their way at once.)
+      const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), raw_parity);
+      const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), parity);
+      uint32_t sv[kRuns], zv[kRuns];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kRuns; ++i) {
         sv[i] = sc[i] * 0x00010001u;
         zv[i] = (__is_same(T, __half) ? 0xE400E400u : 0xC300C300u) + (zr[i] & 15u) * 0x00010001u;
       }
       at += far_at;
       if ((pos_in += far_pos) >= p.group) pos_in -= p.group, ++at;
       read_scales(kt + kGroups);
-      // (Both tries are on their way at once.)
-      const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), (it / R) & 1u);
-      const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u);
-      ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), (it / R) & 1u, p.fault, p.timeout_ns,
+      ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), raw_parity, p.fault, p.timeout_ns,
                            &bars->abort, kFaultTcProducerWait, loaded);
       if (!ok) break;
       const uint32_t raw = smem_u32(raw_base) + r * kRawBytes;
-      const uint4 q0 = ld_shared_v4(raw + from[0]), q1 = ld_shared_v4(raw + from[1]);
-      const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-      uint32_t a[32];
+      uint4 q[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) weights8<T>(w[j], zv[j >> 2], sv[j >> 2], a + 4 * j);
-      // (The fence waits for the loads, before TMA refills the slot.)
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
-      ok = role_wait_lanes(smem_u32(&bars->empty[s]), ((it / S) & 1u) ^ 1u, p.fault, p.timeout_ns,
+      for (int i = 0; i < 4; ++i) q[i] = ld_shared_v4(raw + from[i]);
+      ok = role_wait_lanes(smem_u32(&bars->empty[s]), parity, p.fault, p.timeout_ns,
                            &bars->abort, kFaultTcProducerWait, freed);
       if (!ok) break;
       tc_fence_after();
-      tmem_st32(to + s * kACols, a);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = q[2 * h + i];
+          const uint32_t sr = sv[kEach ? 2 * h + i : 0], zz = zv[kEach ? 2 * h + i : 0];
+          weights8<T>(x.x, zz, sr, a + 16 * i);
+          weights8<T>(x.y, zz, sr, a + 16 * i + 4);
+          weights8<T>(x.z, zz, sr, a + 16 * i + 8);
+          weights8<T>(x.w, zz, sr, a + 16 * i + 12);
+        }
+        tmem_st32(to + s * kACols + h * 32, a);
+      }
+      // (The proxy fence waits for the loads, before TMA refills the slot.)
+      fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->full[s]));
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->full[s]));
+        mbar_arrive(smem_u32(&bars->raw_empty[r]));
+      }
     }
     // ------------------------------------------------ draining
     if (warp < kConvWarp + 4) {
@@ -359,10 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool kEach>
 cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
                         cudaStream_t stream) {
-  auto kernel = q4_rows_kernel<T, MT>;
+  auto kernel = q4_rows_kernel<T, MT, kEach>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(kernel, Layout<MT>::kSmem, &done);
   if (e != cudaSuccess) return e;
@@ -372,14 +392,14 @@ cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* tmQ, const CUte
                                      dim3(kThreads), Layout<MT>::kSmem, stream, *tmQ, *tmX, p);
 }
 
-template <typename T>
+template <typename T, bool kEach>
 cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                          cudaStream_t stream) {
   switch (p.tile_rows) {
-    case 16: return launch_rows<T, 16>(p, q, x, stream);
-    case 32: return launch_rows<T, 32>(p, q, x, stream);
-    case 64: return launch_rows<T, 64>(p, q, x, stream);
-    case 128: return launch_rows<T, 128>(p, q, x, stream);
+    case 16: return launch_rows<T, 16, kEach>(p, q, x, stream);
+    case 32: return launch_rows<T, 32, kEach>(p, q, x, stream);
+    case 64: return launch_rows<T, 64, kEach>(p, q, x, stream);
+    case 128: return launch_rows<T, 128, kEach>(p, q, x, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -388,8 +408,11 @@ cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUten
 
 cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                            const CUtensorMap* tmX, cudaStream_t stream) {
-  return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)
-                    : launch_typed<__nv_bfloat16>(p, tmQ, tmX, stream);
+  if (p.group % BK == 0)
+    return dtype == 1 ? launch_typed<__half, false>(p, tmQ, tmX, stream)
+                      : launch_typed<__nv_bfloat16, false>(p, tmQ, tmX, stream);
+  return dtype == 1 ? launch_typed<__half, true>(p, tmQ, tmX, stream)
+                    : launch_typed<__nv_bfloat16, true>(p, tmQ, tmX, stream);
 }
 
 }  // namespace dgemm
