@@ -11,16 +11,15 @@
 
 namespace dgemm {
 
-// Few rows: a CTA computes 64 columns of Y (rows of W) for up to 64 rows of one
-// expert, over its share of K.
+// Few rows: a CTA computes 64 columns of Y (rows of W) for 8 or 16 rows of one expert,
+// over its share of K.
 constexpr int kQ4TileN = 64;
 constexpr int kQ4BK = 512;
-constexpr int kQ4MaxRows = 64;
 struct Q4FewParams {
   int rows, N, K, group;
   int experts;              // 0: one matrix for all rows
   const int* offsets;
-  int tile_rows;            // rows of Y per CTA: a multiple of 8, at most 64
+  int tile_rows;            // rows of Y per CTA
   int slots;                // upper bound of tiles of rows
   int split;                // CTAs (a cluster) that share a tile's K
   const void* scales;
@@ -30,10 +29,6 @@ struct Q4FewParams {
   unsigned* fault;
   unsigned long long timeout_ns;
 };
-// Rows per CTA for the rows (of an expert) to expect.
-inline int q4_tile_rows(int rows) {
-  return rows <= 32 ? (rows + 7) / 8 * 8 : (rows <= 48 ? 48 : 64);
-}
 // tmQ: the codes as bytes {ceil(K / 2), N, experts} with boxes of 128 x 64 x 1; tmX: X
 // as {K, rows} with boxes of 64 x tile_rows.
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
@@ -42,7 +37,9 @@ cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tm
 // More rows: 128 columns of Y for up to 128 rows of one expert, over a share of K.
 constexpr int kQ4RowsTileN = 128;
 constexpr int kQ4RowsBK = 128;
-inline int q4_rows_tile(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+inline int q4_rows_tile(int rows) {
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+}
 // tmQ: the codes with boxes of 128 x 128 x 1; tmX: boxes of 64 x tile_rows.
 cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                            const CUtensorMap* tmX, cudaStream_t stream);

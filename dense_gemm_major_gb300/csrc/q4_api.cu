@@ -2,7 +2,6 @@
 // checks, choice between the kernel for few rows and a product with the weights in
 // 16 bits, launch.  See include/dense_gemm_q4.h.
 #include <cstdint>
-#include <cstdlib>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -33,23 +32,52 @@ struct Q4Call {
   int matrices() const { return experts == 0 ? 1 : experts; }
 };
 
-// The product by one of the kernels that read the codes (few: the one for few rows);
-// `expect`: rows of an expert to expect.
-gemm_status_t run_codes(const Q4Call& c, bool few, int expect, cudaStream_t stream) {
+// Which kernel, by the rows (of an expert) to expect.
+//
+// Few: mma.sync on registers.  Against the tcgen05 kernel, us, BF16 and groups of 128 /
+// FP16 and groups of 64: 8 rows 4096 x 4096 6.2 / 6.7 and 7.5 / 7.8, 8192 x 8192 12.8 /
+// 15.1 and 15.0 / 16.4; 16 rows 1024 x 1024 3.6 / 3.9 and 4.4 / 4.7, 4096 x 4096 7.2 / 8.4
+// and 7.8 / 8.1, but 8192 x 8192 15.5 / 19.4 and 15.2 / 16.7, 14336 x 4096 14.5 / 17.8
+// and 13.8 / 15.1; 24 rows 4096 x 4096 8.1 / 8.7 and 8.1 / 8.4.  Of experts, whose groups
+// are uneven: 16 rows to 32 experts, 2048 x 2048, 15.9 and 20.6, 64 25.0 and 26.2, but 64 to
+// 8 14.3 and 11.0.
+constexpr int kFewRows = 8, kFewRowsSmall = 16, kFewRowsExperts = 4;
+constexpr long long kFewSmall = 1ll << 24;         // weights
+bool few_rows(const Q4Call& c, int expect) {
+  if (c.experts != 0) return expect <= kFewRowsExperts;
+  return expect <= ((long long)c.N * c.K <= kFewSmall ? kFewRowsSmall : kFewRows);
+}
+// Rows: tcgen05, each 128 rows' CTAs converting the weights for themselves.  Against the
+// product with the weights in 16 bits, us: 512 rows 4096 x 4096 19.1 and 34.1, 8192 x 8192
+// 57 and 96; 768 36.5 and 34.6, 85 and 128; 14336 x 4096 93 and 104; but 1024 37.3 and
+// 35.1, 113 and 129, 14336 x 4096 113 and 103.  8 experts of 2048 x 2048: 256 rows each 37
+// and 46, 512 58 and 56.
+constexpr int kCodeRows = 768;
+
+// The product by one of the kernels that read the codes.  (Not done: terms beyond what a
+// sum in tensor memory, which truncates at each step, should have; see segment().  BF16
+// rounds eight times as coarsely.)
+bool run_codes(const Q4Call& c, int expect, cudaStream_t stream, gemm_status_t* st) {
+  const bool few = few_rows(c, expect);
   dgemm::Q4FewParams p;
   p.rows = c.rows, p.N = c.N, p.K = c.K, p.group = c.group;
   p.experts = c.experts, p.offsets = c.offsets;
-  p.tile_rows = few ? dgemm::q4_tile_rows(expect) : dgemm::q4_rows_tile(expect);
+  if (few)
+    p.tile_rows = expect <= 8 ? 8 : 16;
+  else   // (An expert with more rows than a tile has its weights converted again.)
+    p.tile_rows = dgemm::q4_rows_tile(c.experts == 0 ? expect : 2 * expect);
   p.slots = c.experts == 0 ? ceil_div(c.rows, p.tile_rows)
                            : c.rows / p.tile_rows + (c.experts < c.rows ? c.experts : c.rows);
   // CTAs that share a tile's K: as many (a cluster of at most 8) as keep one wave,
-  // each with a stage at least.
+  // each with a slot of codes at least.
   const int tile_n = few ? dgemm::kQ4TileN : dgemm::kQ4RowsTileN;
   const long long tiles = (long long)ceil_div(c.N, tile_n) * p.slots;
   const int nk = ceil_div(c.K, few ? dgemm::kQ4BK : 2 * dgemm::kQ4RowsBK);
-  const int room = 2 * c.pairs * (few && p.tile_rows <= 16 ? 2 : 1);
+  const int room = 2 * c.pairs * (few ? 2 : 1);
   p.split = 1;
   while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= room) p.split *= 2;
+  if (!few && (c.K - 1) / p.split >= segment(c.dtype) * dgemm::kGroupBK * (c.dtype == 2 ? 8 : 1))
+    return false;
   p.scales = c.scales, p.zeros = c.zeros;
   p.Y = c.Y, p.ldy = c.ldy;
   p.fault = c.fault, p.timeout_ns = dgemm::wait_bound_ns();
@@ -60,9 +88,11 @@ gemm_status_t run_codes(const Q4Call& c, bool few, int expect, cudaStream_t stre
   const cuuint32_t box[3] = {128, (cuuint32_t)tile_n, 1};
   if (!encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, box) ||
       !encode_rows(&tmX, c.dtype, c.x, (uint32_t)p.tile_rows))
-    return GEMM_ERR_LAUNCH;
-  return status_of(few ? dgemm::launch_q4_few(c.dtype, p, &tmQ, &tmX, stream)
-                       : dgemm::launch_q4_rows(c.dtype, p, &tmQ, &tmX, stream));
+    *st = GEMM_ERR_LAUNCH;
+  else
+    *st = status_of(few ? dgemm::launch_q4_few(c.dtype, p, &tmQ, &tmX, stream)
+                        : dgemm::launch_q4_rows(c.dtype, p, &tmQ, &tmX, stream));
+  return true;
 }
 
 // The product with the weights in 16 bits, in parts of them that fit the workspace:
@@ -158,9 +188,6 @@ extern "C" gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, i
   Operand none{nullptr, 0, 0, 0, 1, 0, false};
   if ((st = align_operands(c.x, none, workspaces, stream)) != GEMM_OK) return st;
   const int expect = experts == 0 ? rows : ceil_div(rows, experts);
-  static const int few_rows = [] { const char* s = getenv("Q4_FEW"); return s ? atoi(s) : 8; }();
-  static const int mid_rows = [] { const char* s = getenv("Q4_MID"); return s ? atoi(s) : 128; }();
-  if (expect <= few_rows) return run_codes(c, true, expect, stream);
-  if (expect <= mid_rows) return run_codes(c, false, expect, stream);
+  if (expect <= kCodeRows && run_codes(c, expect, stream, &st)) return st;
   return run_values(c, workspaces, stream);
 }

@@ -31,8 +31,8 @@ template <int kTiles>
 struct Layout {
   static constexpr uint32_t kXBox = kTiles * 8 * 128;      // 64 values of each row
   static constexpr uint32_t kStage = kCodeBoxes * kCodeBox + kXBoxes * kXBox;
-  // Two CTAs per SM up to 16 rows; as many stages as there is room for.
-  static constexpr int kCtas = kTiles <= 2 ? 2 : 1;
+  // Two CTAs per SM, with as many stages as there is room for.
+  static constexpr int kCtas = 2;
   static constexpr int S = (232448 / kCtas - 2560) / kStage;
   static constexpr uint32_t kSmem = S * kStage + 256 + 1024;
   // The sums take the ring's place.
@@ -357,15 +357,8 @@ cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUt
 template <typename T, bool kEach>
 cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                          cudaStream_t stream) {
-  switch (p.tile_rows / 8) {
-    case 1: return launch_tiles<T, 1, kEach>(p, q, x, stream);
-    case 2: return launch_tiles<T, 2, kEach>(p, q, x, stream);
-    case 3: return launch_tiles<T, 3, kEach>(p, q, x, stream);
-    case 4: return launch_tiles<T, 4, kEach>(p, q, x, stream);
-    case 6: return launch_tiles<T, 6, kEach>(p, q, x, stream);
-    case 8: return launch_tiles<T, 8, kEach>(p, q, x, stream);
-  }
-  return cudaErrorInvalidValue;
+  return p.tile_rows == 8 ? launch_tiles<T, 1, kEach>(p, q, x, stream)
+                          : launch_tiles<T, 2, kEach>(p, q, x, stream);
 }
 
 // ------------------------------------------------------------ weights in 16 bits

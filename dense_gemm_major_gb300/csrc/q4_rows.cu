@@ -60,14 +60,16 @@ struct alignas(8) Barriers {
   int abort;
 };
 
-// 16-deep step with A in tensor memory: 128 lanes by 8 columns of pairs.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+// 16-deep step with A in tensor memory: 128 lanes by 8 columns of pairs; B as in
+// mma_f16_pair_lo.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(kDescHi128B), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -187,20 +189,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (elect_one()) {
       // ---------------------------------------------- MMA issuer
+      // (The barrier of the next stage is tried before this stage's MMAs are issued: a
+      // try takes over 100 cycles to answer.)
       RingPos<S> pos;
-      bool ok = true;
-      for (int kt = kb; kt < ke; ++kt, pos.next()) {
-        ok = role_wait(smem_u32(&bars->full[pos.slot]), pos.parity, p.fault, p.timeout_ns,
-                       &bars->abort, kFaultTcMmaWait, true);
+      bool ok = true, ready = false;
+      for (int kt = kb; kt < ke; ++kt) {
+        const uint32_t slot = pos.slot;
+        ok = ready || role_wait(smem_u32(&bars->full[slot]), pos.parity, p.fault, p.timeout_ns,
+                                &bars->abort, kFaultTcMmaWait, true);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(base + pos.slot * L::kStage);
+        pos.next();
+        ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
+        const uint32_t blo = desc_lo(smem_u32(base + slot * L::kStage), 16);
+        const uint32_t a = tmem_base + L::kACol + slot * kACols;
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k)
-          mma_f16_ta(tmem_base, tmem_base + L::kACol + pos.slot * kACols + k * 8,
-                     kmajor_desc(st + (k >> 2) * L::kXBlock, k & 3),
+          mma_f16_ta(tmem_base, a + k * 8, blo + (((k >> 2) * L::kXBlock + (k & 3) * 32) >> 4),
                      instr_desc(kAb, BN, MT, 0, 0), (kt > kb || k > 0) ? 1u : 0u);
-        mma_commit(smem_u32(&bars->empty[pos.slot]));
+        mma_commit(smem_u32(&bars->empty[slot]));
       }
       if (ok) mma_commit(smem_u32(&bars->acc_full));
     }

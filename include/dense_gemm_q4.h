@@ -45,9 +45,9 @@ extern "C" {
  * expert g, W its matrix, as gemm_grouped does.  X is 16-byte aligned and ldx a
  * multiple of 8, or X is packed (ldx == K) at any alignment of its type, which takes
  * a copy with aligned rows in a workspace first; else GEMM_ERR_MISALIGNED.  Y has any
- * alignment of its type.  FP32 accumulation; one rounding.  (Few rows: the integers
- * code - zero, exact in 16 bits, are multiplied and each group's FP32 sum scaled.
- * Many: the weights are rounded to dtype first.)  K == 0: zeros.
+ * alignment of its type.  FP32 accumulation; one rounding.  (Up to 8 rows, or 16 of a
+ * small matrix: the integers code - zero, exact in 16 bits, are multiplied and each
+ * group's FP32 sum scaled.  More: the weights are rounded to dtype first.)  K == 0: zeros.
  */
 gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, int K, int experts,
                              const void *X, int ldx, const void *codes, int ldq,
