@@ -20,6 +20,18 @@ enum GroupKind { kGroupForward = 0, kGroupInput = 1, kGroupWeights = 2 };
 constexpr int kGroupTile = 256;       // columns of C, and rows at most, of a CTA pair's unit
 constexpr int kGroupBK = 128;
 constexpr int kGroupMaxGroups = GEMM_GROUP_MAX_GROUPS;
+// Most rows of a product's units, by the rows of a group to expect.  64 / 256, us: 32
+// experts of 2048 x 2048: 32 rows 29.6 / 30.9, 256 49.2 / 53.2, 1024 50.2 / 54.9, 2048 51.9 /
+// 56.2; 8 of 4096 x 4096: 8 rows 37.5 / 43.4, 512 51.3 / 52.2.  (Each unit reads its
+// weights, so that larger groups want larger ones.)
+inline int group_unit_rows(int rows, int groups) {
+  return rows <= 64ll * groups ? 64 : kGroupTile;
+}
+// No more units than whole tiles of rows and a ragged one for each group that can have any.
+inline long long group_units(int rows, int groups, int N, int tile_rows) {
+  return ((long long)rows / tile_rows + (groups < rows ? groups : rows)) *
+         ((N + kGroupTile - 1ll) / kGroupTile);
+}
 
 struct GroupParams {
   int kind;
@@ -28,6 +40,7 @@ struct GroupParams {
   // Products: C is rows x N, terms of the sums K.  Weights: C[g] is M x N (A's
   // columns x X's), the sums run over the group's rows (K == 0: without terms).
   int M, N, K;
+  int tile_rows;            // most rows of a unit: 256, or 64 (products)
   int per_group;            // weights: tiles of a C[g]
   const int* offsets;       // null (groups 1): all rows are one group's
   int zmul;                 // 0: one B for all groups
@@ -41,8 +54,8 @@ struct GroupParams {
 
 // tmM: B as {K, N, groups} with boxes of 64 x 128 x 1 (forward), as {N, K,
 // groups} with boxes of 64 x 128 x 1 (input), or X as {N, rows} with boxes of
-// 64 x 64 (weights).  tmN, tmN16: X as {K, rows} with boxes of 64 x 128 and 64 x
-// 16, or A as {M, rows} with boxes of 64 x 64 (weights; both alike).
+// 64 x 64 (weights).  tmN, tmN16: X as {K, rows} with boxes of 64 x tile_rows / 2 and
+// 64 x 16, or A as {M, rows} with boxes of 64 x 64 (weights; both alike).
 cudaError_t launch_group(int dtype, int dtype_c, const GroupParams& p, const CUtensorMap* tmM,
                          const CUtensorMap* tmN, const CUtensorMap* tmN16, int pairs,
                          cudaStream_t stream);

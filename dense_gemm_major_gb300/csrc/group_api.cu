@@ -53,9 +53,10 @@ gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int
   if ((st = dgemm::current_device_pairs(&p.fault, &max_pairs)) != GEMM_OK) return st;
   dgemm::StreamWorkspaces workspaces(stream);   // held until everything is queued
   alignas(64) CUtensorMap tmM{}, tmN{}, tmN16{};
+  p.tile_rows = dgemm::group_unit_rows(rows, groups);
   if (!empty) {
     if ((st = align_operands(a, b, workspaces, stream)) != GEMM_OK) return st;
-    if (!encode_matrices(&tmM, dtype, b) || !encode_rows(&tmN, dtype, a, 128) ||
+    if (!encode_matrices(&tmM, dtype, b) || !encode_rows(&tmN, dtype, a, (uint32_t)p.tile_rows / 2) ||
         !encode_rows(&tmN16, dtype, a, 16))
       return GEMM_ERR_LAUNCH;
   }
@@ -69,9 +70,7 @@ gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int
   p.alpha = empty ? 0.f : alpha, p.beta = beta;
   p.C = C, p.ldc = ldc, p.stride_c = 0;
   p.timeout_ns = dgemm::wait_bound_ns();
-  // No more units than whole tiles of rows and a ragged one per group.
-  const long long most = ((long long)rows / dgemm::kGroupTile + (groups < rows ? groups : rows)) *
-                         ceil_div(N, dgemm::kGroupTile);
+  const long long most = dgemm::group_units(rows, groups, N, p.tile_rows);
   const int pairs = (int)(most < max_pairs ? most : max_pairs);
   return status_of(dgemm::launch_group(dtype, dtype_c, p, &tmM, &tmN, &tmN16, pairs, stream));
 }
@@ -112,6 +111,7 @@ gemm_status_t gemm_grouped_grad(int dtype, int dtype_c, int rows, int M, int N, 
       return GEMM_ERR_LAUNCH;
   }
   p.kind = dgemm::kGroupWeights;
+  p.tile_rows = dgemm::kGroupTile;
   p.rows = rows, p.groups = groups;
   p.M = M, p.N = N, p.K = empty ? 0 : 1;
   p.per_group = ceil_div(M, dgemm::kGroupTile) * ceil_div(N, dgemm::kGroupTile);

@@ -1,12 +1,12 @@
 // The work of the grouped kernels' CTA pairs, from offsets that only the device
 // knows: units of C, which the pairs take in rounds, and their draining.
 //
-// A group's rows are cut into equal tiles of at most 256, a multiple of 32 (1342
-// rows: six of 224 rather than five of 256 and one of 62), so that the units of a round
-// end together: 8192 rows of 8 experts, 4096 x 4096, 167 -> 161 us.  (Ranges of units cut
-// along K, one for each pair, whose pieces meet through a workspace, were slower in
-// every case: storing and adding the pieces took 8 to 10 us at the end, the last round
-// that is not full 4 to 8.)
+// A group's rows are cut into equal tiles of at most 256 (few rows: 64), a multiple of 32
+// (1342 rows: six of 224 rather than five of 256 and one of 62), so that the units of a
+// round end together: 8192 rows of 8 experts, 4096 x 4096, 167 -> 161 us.  (Groups taken in
+// the order of their units' cost changed nothing.  Ranges of units cut along K, one for
+// each pair, whose pieces meet through a workspace, were slower in every case: storing
+// and adding the pieces took 8 to 10 us at the end, the last round that is not full 4 to 8.)
 #pragma once
 
 #include "group.h"
@@ -16,7 +16,7 @@ namespace dgemm {
 
 constexpr int kGroupEpiWarps = 8;
 
-// A unit: rows [row, row_end) of C (at most 256; weights: of C[g]) by the 256
+// A unit: rows [row, row_end) of C (at most a tile; weights: of C[g]) by the 256
 // columns from col; the sum's k-tiles are nk, from row k0 of the operands and up
 // to k_end (weights; products: from column 0 up to K).
 struct GroupUnit {
@@ -32,9 +32,10 @@ struct GroupTables {
   int units;
 };
 
-// Rows of a group's tiles (m > 0).
+// Rows of a group's tiles of at most kRows (m > 0).
+template <int kRows>
 __device__ __forceinline__ int group_tile_rows(int m) {
-  const int tiles = (m + kGroupTile - 1) / kGroupTile;
+  const int tiles = (m + kRows - 1) / kRows;
   return ((int)((unsigned)(m + tiles - 1) / (unsigned)tiles) + 31) & ~31;
 }
 __device__ __forceinline__ int group_k_tiles(int terms) { return (terms + kGroupBK - 1) / kGroupBK; }
@@ -53,8 +54,8 @@ __device__ __forceinline__ int group_find(const V* first, int groups, V x) {
   return lo;
 }
 
-// The tables, by one warp.
-template <int kKind>
+// The tables, by one warp.  kRows: most rows of a tile.
+template <int kKind, int kRows>
 __device__ __forceinline__ void group_tables(const GroupParams& p, GroupTables& t) {
   const int lane = threadIdx.x & 31;
   const int tiles_n = (p.N + kGroupTile - 1) / kGroupTile;
@@ -79,28 +80,26 @@ __device__ __forceinline__ void group_tables(const GroupParams& p, GroupTables& 
     // Group i - 1, whose end this lane has.
     const int m = v - before;
     const bool is = i > p.first_group && i <= end;
-    int n = 0;
-    if (is) n = kKind == kGroupWeights ? p.per_group : (m + kGroupTile - 1) / kGroupTile * tiles_n;
+    if (kKind != kGroupWeights) {
+      int n = is ? (m + kRows - 1) / kRows * tiles_n : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, n, d);
-      if (lane >= d) n += o;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n += o;
+      }
+      if (is && m > 0) t.tile[i - 1 - p.first_group] = (short)group_tile_rows<kRows>(m);
+      if (i >= p.first_group && i <= end) t.unit0[i - p.first_group] = units + n;
+      units += __shfl_sync(0xffffffffu, n, 31);
     }
-    if (kKind != kGroupWeights && is && m > 0)
-      t.tile[i - 1 - p.first_group] = (short)group_tile_rows(m);
-    if (i >= p.first_group && i <= end) {
-      t.start[i - p.first_group] = v;
-      t.unit0[i - p.first_group] = units + n;
-    }
-    units += __shfl_sync(0xffffffffu, n, 31);
+    if (i >= p.first_group && i <= end) t.start[i - p.first_group] = v;
     last = __shfl_sync(0xffffffffu, v, 31);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
     raise_fault(p.fault, kFaultGroupOffsets);
-  if (lane == 0) t.units = units;
+  if (lane == 0) t.units = kKind == kGroupWeights ? p.groups * p.per_group : units;
 }
 
-template <int kKind>
+template <int kKind, int kRows>
 __device__ __forceinline__ GroupUnit group_unit(int u, const GroupParams& p,
                                                 const GroupTables& t) {
   GroupUnit w;
@@ -109,19 +108,19 @@ __device__ __forceinline__ GroupUnit group_unit(int u, const GroupParams& p,
     w.g = u / p.per_group;
     // (Groups of 16 tiles along C's columns share the operands in L2.)
     grouped_tile(u - w.g * p.per_group, (p.N + kGroupTile - 1) / kGroupTile,
-                 (p.M + kGroupTile - 1) / kGroupTile, 16, tn, tm);
-    w.row = tm * kGroupTile;
-    w.row_end = min(w.row + kGroupTile, p.M);
+                 (p.M + kRows - 1) / kRows, 16, tn, tm);
+    w.row = tm * kRows;
+    w.row_end = min(w.row + kRows, p.M);
     w.k0 = t.start[w.g];
     w.k_end = t.start[w.g + 1];
     w.nk = p.K == 0 ? 0 : group_k_tiles(w.k_end - w.k0);
   } else {
     w.g = group_find(t.unit0, p.groups, u);
-    const int first = t.start[w.g], rows = t.start[w.g + 1] - first;
-    grouped_tile(u - t.unit0[w.g], (rows + kGroupTile - 1) / kGroupTile,
+    const int first = t.start[w.g], rows = t.start[w.g + 1] - first, tile = t.tile[w.g];
+    grouped_tile(u - t.unit0[w.g], (rows + kRows - 1) / kRows,
                  (p.N + kGroupTile - 1) / kGroupTile, 16, tm, tn);
-    w.row = first + tm * t.tile[w.g];
-    w.row_end = min(w.row + t.tile[w.g], first + rows);
+    w.row = first + tm * tile;
+    w.row_end = min(w.row + tile, first + rows);
     w.k0 = 0;
     w.k_end = p.K;
     w.nk = group_k_tiles(p.K);
@@ -135,7 +134,7 @@ __device__ __forceinline__ GroupUnit group_unit(int u, const GroupParams& p,
 
 // Drains a pair's units (both CTAs, kGroupEpiWarps warps each): warp `ew` takes TMEM
 // lanes 32 (ew % 4) .. + 31 (columns of C) and every other 32 rows.
-template <typename TC, int kKind, typename Bars>
+template <typename TC, int kKind, int kRows, typename Bars>
 __device__ __forceinline__ void group_epilogue(const GroupParams& p, const GroupTables& t,
                                                Bars* bars, uint32_t tmem_base, uint32_t rank,
                                                int ew, int pair, int npairs) {
@@ -147,11 +146,12 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
   uint32_t seg = 0;
   bool ok = true;
   for (int u = pair; u < t.units; u += npairs) {
-    const GroupUnit w = group_unit<kKind>(u, p, t);
+    const GroupUnit w = group_unit<kKind, kRows>(u, p, t);
     const int chunks = w.mma_rows / 32;
-    float acc[128];
+    constexpr int kChunks = kRows / 64;                    // of 32 rows, this warp's
+    float acc[32 * kChunks];
 #pragma unroll
-    for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+    for (int j = 0; j < 32 * kChunks; ++j) acc[j] = 0.f;
     for (int k0 = 0; k0 < w.nk; k0 += p.seg, ++seg) {
       const uint32_t b = seg & 1;
       ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
@@ -160,7 +160,7 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
       tc_fence_after();
       const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + b * 256;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 2 * kChunks; ++c) {
         const int chunk = 2 * (c >> 1) + half;
         if (chunk < chunks) {
           uint32_t r[16];
@@ -177,7 +177,7 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
     const int col = w.col + (int)rank * 128 + q * 32 + lane;
     TC* c_out = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kChunks; ++c) {
       const int chunk = 2 * c + half;
       if (chunk < chunks)
         store_piece<TC>(acc + c * 32, c_out, p.ldc, w.row_end, p.N, w.row + chunk * 32, col, pairs,

@@ -111,6 +111,7 @@ gemm_status_t run_values(const Q4Call& c, dgemm::StreamWorkspaces& workspaces,
   if (st != GEMM_OK) return st;
   dgemm::GroupParams p;
   p.kind = dgemm::kGroupForward;
+  p.tile_rows = dgemm::kGroupTile;
   p.rows = c.rows, p.M = 0, p.K = c.K, p.per_group = 0;
   p.zmul = 1;
   p.seg = segment(c.dtype);
@@ -135,8 +136,7 @@ gemm_status_t run_values(const Q4Call& c, dgemm::StreamWorkspaces& workspaces,
       if (!encode_matrices(&tmM, c.dtype, w)) return GEMM_ERR_LAUNCH;
       p.groups = n, p.first_group = e, p.N = cols, p.offsets = c.offsets;
       p.C = static_cast<char*>(c.Y) + (long long)n0 * 2;
-      const long long most = ((long long)c.rows / dgemm::kGroupTile + (n < c.rows ? n : c.rows)) *
-                             ceil_div(cols, dgemm::kGroupTile);
+      const long long most = dgemm::group_units(c.rows, n, cols, p.tile_rows);
       st = status_of(dgemm::launch_group(c.dtype, c.dtype, p, &tmM, &tmN, &tmN16,
                                          (int)(most < c.pairs ? most : c.pairs), stream));
       if (st != GEMM_OK) return st;
