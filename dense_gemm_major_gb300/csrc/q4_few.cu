@@ -105,9 +105,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// kEach: a scale for each step of 32 terms; else for each warp's slice of a stage
-// (groups of a multiple of 128).
-template <typename T, int kTiles, bool kEach>
+// kRun: steps of 32 terms that have one scale (1, 2, or 4: a warp's slice of a stage, where
+// groups are a multiple of 128).
+template <typename T, int kTiles, int kRun>
 __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     q4_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                   const Q4FewParams p) {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     const uint16_t* const scales = static_cast<const uint16_t*>(p.scales) + first;
     const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + first : nullptr;
     const bool real = row < p.N;
-    constexpr int kSteps = kSliceK / 32;
+    constexpr int kSteps = kSliceK / 32, kRuns = kSteps / kRun;
     float acc[2][kTiles][4];
 #pragma unroll
     for (int i = 0; i < 2 * kTiles * 4; ++i) (&acc[0][0][0])[i] = 0.f;
@@ -190,19 +190,20 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     // The scales and zeros of a stage's slice, read a stage ahead and left as they
     // come: a conversion would wait for them at once.  `at`, `pos`: group of a
     // slice's first step, and its place in it.
-    uint16_t sc[kEach ? kSteps : 1];
-    unsigned char zr[kEach ? kSteps : 1];
+    uint16_t sc[kRuns];
+    unsigned char zr[kRuns];
     const int far_at = kQ4BK / p.group, far_pos = kQ4BK % p.group;
     int at = (kb * kQ4BK + wk * kSliceK) / p.group;
     int pos = (kb * kQ4BK + wk * kSliceK) % p.group;
     auto read_scales = [&](int kt, int at, int pos) {
 #pragma unroll
-      for (int i = 0; i < (kEach ? kSteps : 1); ++i) {
-        const bool ok = real && kt < ke && kt * kQ4BK + wk * kSliceK + i * 32 < p.K;
+      for (int i = 0; i < kRuns; ++i) {
+        const bool ok =
+            real && kt < ke && kt * kQ4BK + wk * kSliceK + i * kRun * 32 < p.K;
         const long long to = (long long)at * p.N;
         sc[i] = ok ? scales[to] : (uint16_t)0;
         zr[i] = ok && zeros != nullptr ? zeros[to] : (unsigned char)8;
-        if ((pos += 32) == p.group) pos = 0, ++at;
+        if ((pos += kRun * 32) == p.group) pos = 0, ++at;
       }
     };
     read_scales(kb, at, pos);
@@ -221,10 +222,10 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     RingPos<S> ring;
     bool ok = true;
     for (int kt = kb; kt < ke; ++kt, ring.next()) {
-      float s[kEach ? kSteps : 1];
-      uint32_t z[kEach ? kSteps : 1];
+      float s[kRuns];
+      uint32_t z[kRuns];
 #pragma unroll
-      for (int i = 0; i < (kEach ? kSteps : 1); ++i) {
+      for (int i = 0; i < kRuns; ++i) {
         s[i] = elem_to_f32<T>(__builtin_bit_cast(T, sc[i]));
         z[i] = zr[i] & 15u;
       }
@@ -246,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
       Zero<T> zero[4] = {Zero<T>(0), Zero<T>(0), Zero<T>(0), Zero<T>(0)};
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        if (kEach || i == 0) {
+        if (i % kRun == 0) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            zero[r] = Zero<T>(__shfl_sync(0xffffffffu, z[i], r * 8 + g));
+            zero[r] = Zero<T>(__shfl_sync(0xffffffffu, z[i / kRun], r * 8 + g));
 #pragma unroll
           for (int e = 0; e < 2 * kTiles * 4; ++e) (&part[0][0][0])[e] = 0.f;
         }
@@ -269,11 +270,11 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
             mma_16816<T>(part[h][m], a1, b2, b3);
           }
         }
-        if (kEach || i == kSteps - 1) {
+        if (i % kRun == kRun - 1) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float lo = __shfl_sync(0xffffffffu, s[kEach ? i : 0], h * 16 + g);
-            const float hi = __shfl_sync(0xffffffffu, s[kEach ? i : 0], h * 16 + 8 + g);
+            const float lo = __shfl_sync(0xffffffffu, s[i / kRun], h * 16 + g);
+            const float hi = __shfl_sync(0xffffffffu, s[i / kRun], h * 16 + 8 + g);
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
@@ -341,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
   }
 }
 
-template <typename T, int kTiles, bool kEach>
+template <typename T, int kTiles, int kRun>
 cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
                          cudaStream_t stream) {
-  auto kernel = q4_few_kernel<T, kTiles, kEach>;
+  auto kernel = q4_few_kernel<T, kTiles, kRun>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(kernel, Layout<kTiles>::kSmem, &done);
   if (e != cudaSuccess) return e;
@@ -354,11 +355,19 @@ cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUt
                                      dim3(kThreads), Layout<kTiles>::kSmem, stream, *tmQ, *tmX, p);
 }
 
-template <typename T, bool kEach>
+template <typename T, int kTiles>
+cudaError_t launch_run(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
+                       cudaStream_t stream) {
+  if (p.group % 128 == 0) return launch_tiles<T, kTiles, 4>(p, q, x, stream);
+  return p.group % 64 == 0 ? launch_tiles<T, kTiles, 2>(p, q, x, stream)
+                           : launch_tiles<T, kTiles, 1>(p, q, x, stream);
+}
+
+template <typename T>
 cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                          cudaStream_t stream) {
-  return p.tile_rows == 8 ? launch_tiles<T, 1, kEach>(p, q, x, stream)
-                          : launch_tiles<T, 2, kEach>(p, q, x, stream);
+  return p.tile_rows == 8 ? launch_run<T, 1>(p, q, x, stream)
+                          : launch_run<T, 2>(p, q, x, stream);
 }
 
 // ------------------------------------------------------------ weights in 16 bits
@@ -406,11 +415,8 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream) {
-  if (p.group % kSliceK == 0)
-    return dtype == 1 ? launch_typed<__half, false>(p, tmQ, tmX, stream)
-                      : launch_typed<__nv_bfloat16, false>(p, tmQ, tmX, stream);
-  return dtype == 1 ? launch_typed<__half, true>(p, tmQ, tmX, stream)
-                    : launch_typed<__nv_bfloat16, true>(p, tmQ, tmX, stream);
+  return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)
+                    : launch_typed<__nv_bfloat16>(p, tmQ, tmX, stream);
 }
 
 cudaError_t launch_q4_values(int dtype, int group, int experts, int N, int K, int scale_n,

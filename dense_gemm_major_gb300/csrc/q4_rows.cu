@@ -96,9 +96,8 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-// kEach: a scale for each run of 32 columns; else for each stage (groups of a multiple of
-// 128).
-template <typename T, int MT, bool kEach>
+// kRun: columns that have one scale (32, 64, or a stage's 128).
+template <typename T, int MT, int kRun>
 __global__ void __launch_bounds__(kThreads, 1)
     q4_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                    const Q4FewParams p) {
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------ conversion
     // A thread of its group has a row.  (A warp reaches the lanes 32 (warp % 4) .. + 31.)
-    constexpr int kRuns = kEach ? BK / 32 : 1;
+    constexpr int kRuns = BK / kRun;
     const int group = (warp - kConvWarp) / kGroupWarps;
     const int row = (warp & 3) * 32 + lane;
     const int n = n0 + row;
@@ -234,11 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int a = at, q = pos_in;
 #pragma unroll
       for (int i = 0; i < kRuns; ++i) {
-        const bool ok = real && kt < ke && kt * BK + i * 32 < p.K;
+        const bool ok = real && kt < ke && kt * BK + i * kRun < p.K;
         const long long to = (long long)a * p.N;
         sc[i] = ok ? scales[to] : (uint16_t)0;
         zr[i] = ok && zeros != nullptr ? zeros[to] : (unsigned char)8;
-        if ((q += 32) == p.group) q = 0, ++a;
+        if ((q += kRun) == p.group) q = 0, ++a;
       }
     };
     // 16-byte chunks in 128-byte rows are swizzled by the row; a stage has four.
@@ -282,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint4 x = q[2 * h + i];
-          const uint32_t sr = sv[kEach ? 2 * h + i : 0], zz = zv[kEach ? 2 * h + i : 0];
+          const int run = (2 * h + i) * 32 / kRun;
+          const uint32_t sr = sv[run], zz = zv[run];
           weights8<T>(x.x, zz, sr, a + 16 * i);
           weights8<T>(x.y, zz, sr, a + 16 * i + 4);
           weights8<T>(x.z, zz, sr, a + 16 * i + 8);
@@ -386,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, int MT, bool kEach>
+template <typename T, int MT, int kRun>
 cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
                         cudaStream_t stream) {
-  auto kernel = q4_rows_kernel<T, MT, kEach>;
+  auto kernel = q4_rows_kernel<T, MT, kRun>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(kernel, Layout<MT>::kSmem, &done);
   if (e != cudaSuccess) return e;
@@ -399,27 +399,32 @@ cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* tmQ, const CUte
                                      dim3(kThreads), Layout<MT>::kSmem, stream, *tmQ, *tmX, p);
 }
 
-template <typename T, bool kEach>
+template <typename T, int kRun>
 cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                          cudaStream_t stream) {
   switch (p.tile_rows) {
-    case 16: return launch_rows<T, 16, kEach>(p, q, x, stream);
-    case 32: return launch_rows<T, 32, kEach>(p, q, x, stream);
-    case 64: return launch_rows<T, 64, kEach>(p, q, x, stream);
-    case 128: return launch_rows<T, 128, kEach>(p, q, x, stream);
+    case 16: return launch_rows<T, 16, kRun>(p, q, x, stream);
+    case 32: return launch_rows<T, 32, kRun>(p, q, x, stream);
+    case 64: return launch_rows<T, 64, kRun>(p, q, x, stream);
+    case 128: return launch_rows<T, 128, kRun>(p, q, x, stream);
   }
   return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t launch_run(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
+                       cudaStream_t stream) {
+  if (p.group % 128 == 0) return launch_typed<T, 128>(p, q, x, stream);
+  return p.group % 64 == 0 ? launch_typed<T, 64>(p, q, x, stream)
+                           : launch_typed<T, 32>(p, q, x, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                            const CUtensorMap* tmX, cudaStream_t stream) {
-  if (p.group % BK == 0)
-    return dtype == 1 ? launch_typed<__half, false>(p, tmQ, tmX, stream)
-                      : launch_typed<__nv_bfloat16, false>(p, tmQ, tmX, stream);
-  return dtype == 1 ? launch_typed<__half, true>(p, tmQ, tmX, stream)
-                    : launch_typed<__nv_bfloat16, true>(p, tmQ, tmX, stream);
+  return dtype == 1 ? launch_run<__half>(p, tmQ, tmX, stream)
+                    : launch_run<__nv_bfloat16>(p, tmQ, tmX, stream);
 }
 
 }  // namespace dgemm
