@@ -25,6 +25,40 @@ struct GroupUnit {
   int mma_rows;             // rows rounded up to the MMA's steps of 32
 };
 
+// The groups' ends in order, 32 at a time, by a warp: offsets that decrease or leave 0 ..
+// rows are moved to the nearest that do not.  (No offsets: one group has all rows.)
+struct GroupEnds {
+  const int* offsets;
+  int rows;
+  __device__ __forceinline__ int clamp(int v) const { return min(max(v, 0), rows); }
+  __device__ __forceinline__ int first() const {
+    return offsets == nullptr ? 0 : clamp(offsets[0]);
+  }
+  __device__ __forceinline__ bool first_is_bad() const {
+    return offsets != nullptr && offsets[0] != clamp(offsets[0]);
+  }
+  // End of group i (of `groups`; lanes past them: the last one's), and where it begins;
+  // *last: where the lanes' first group begins, then where their last ends.
+  __device__ __forceinline__ int next(int i, int groups, int* last, int* before,
+                                      bool* bad) const {
+    const int lane = threadIdx.x & 31;
+    const int raw = i >= groups ? 0 : (offsets == nullptr ? rows : offsets[i + 1]);
+    int v = i >= groups ? *last : clamp(raw);
+    const int own = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, *last);
+    *bad |= i < groups && (own != raw || v != own);
+    const int o = __shfl_up_sync(0xffffffffu, v, 1);
+    *before = lane == 0 ? *last : o;
+    *last = __shfl_sync(0xffffffffu, v, 31);
+    return v;
+  }
+};
+
 struct GroupTables {
   int start[kGroupMaxGroups + 1];        // first rows of the groups, in order
   int unit0[kGroupMaxGroups + 1];        // their first units
@@ -59,44 +93,36 @@ template <int kKind, int kRows>
 __device__ __forceinline__ void group_tables(const GroupParams& p, GroupTables& t) {
   const int lane = threadIdx.x & 31;
   const int tiles_n = (p.N + kGroupTile - 1) / kGroupTile;
-  int last = 0, units = 0;
-  bool bad = false;
-  const int end = p.first_group + p.groups;
-  for (int base = 0; base <= end; base += 32) {
-    const int i = base + lane;
-    const int raw = p.offsets == nullptr ? (i == 0 ? 0 : p.rows)
-                                         : (i <= end ? p.offsets[i] : p.rows);
-    const int own = min(max(raw, 0), p.rows);
-    int v = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v = max(v, o);
-    }
-    v = max(v, last);
-    bad |= own != raw || v != own;
-    int before = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) before = last;
-    // Group i - 1, whose end this lane has.
-    const int m = v - before;
-    const bool is = i > p.first_group && i <= end;
+  const GroupEnds ends{p.offsets, p.rows};
+  int units = 0;
+  int last = ends.first();
+  bool bad = ends.first_is_bad();
+  for (int base = 0; base < p.first_group + p.groups; base += 32) {
+    const int i = base + lane, g = i - p.first_group;
+    int before;
+    const int end = ends.next(i, p.first_group + p.groups, &last, &before, &bad);
+    const bool is = g >= 0 && g < p.groups;
+    if (is) t.start[g] = before;
     if (kKind != kGroupWeights) {
-      int n = is ? (m + kRows - 1) / kRows * tiles_n : 0;
+      const int m = end - before, mine = is ? (m + kRows - 1) / kRows * tiles_n : 0;
+      int n = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, n, d);
         if (lane >= d) n += o;
       }
-      if (is && m > 0) t.tile[i - 1 - p.first_group] = (short)group_tile_rows<kRows>(m);
-      if (i >= p.first_group && i <= end) t.unit0[i - p.first_group] = units + n;
+      if (is) t.unit0[g] = units + n - mine;
+      if (is && m > 0) t.tile[g] = (short)group_tile_rows<kRows>(m);
       units += __shfl_sync(0xffffffffu, n, 31);
     }
-    if (i >= p.first_group && i <= end) t.start[i - p.first_group] = v;
-    last = __shfl_sync(0xffffffffu, v, 31);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
     raise_fault(p.fault, kFaultGroupOffsets);
-  if (lane == 0) t.units = kKind == kGroupWeights ? p.groups * p.per_group : units;
+  if (lane == 0) {
+    t.start[p.groups] = last;
+    t.unit0[p.groups] = units;
+    t.units = kKind == kGroupWeights ? p.groups * p.per_group : units;
+  }
 }
 
 template <int kKind, int kRows>

@@ -2,7 +2,7 @@
 // integers.
 #pragma once
 
-#include "mx.cuh"
+#include "group_sched.cuh"
 #include "q4.h"
 
 namespace dgemm {
@@ -57,7 +57,7 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 
 // Tile `slot` of the rows, tile_rows each: its expert (-1: there is no such tile) and
-// rows [lo, hi).  By one warp; offsets are put in order as group_sched.cuh does.
+// rows [lo, hi).  By one warp.
 struct Q4Rows {
   int expert, lo, hi;
 };
@@ -71,41 +71,29 @@ __device__ __forceinline__ Q4Rows q4_rows_of_slot(int slot, const Q4FewParams& p
   }
   r.expert = -1, r.lo = r.hi = 0;
   const int lane = threadIdx.x & 31;
-  int last = 0, tiles = 0;
-  bool bad = false;
-  for (int base = 0; base <= p.experts; base += 32) {
-    const int i = base + lane;
-    const int raw = i <= p.experts ? p.offsets[i] : p.rows;
-    const int own = min(max(raw, 0), p.rows);
-    int v = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v = max(v, o);
-    }
-    v = max(v, last);
-    bad |= own != raw || v != own;
-    int before = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) before = last;
-    const int mine = i >= 1 && i <= p.experts ? (v - before + p.tile_rows - 1) / p.tile_rows : 0;
+  const GroupEnds ends{p.offsets, p.rows};
+  int last = ends.first(), tiles = 0;
+  bool bad = ends.first_is_bad();
+  for (int base = 0; base < p.experts; base += 32) {
+    int before;
+    const int end = ends.next(base + lane, p.experts, &last, &before, &bad);
+    const int mine = (end - before + p.tile_rows - 1) / p.tile_rows;
     int n = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, n, d);
       if (lane >= d) n += o;
     }
-    // (Lane i has the end of expert i - 1, whose tiles end at tiles + n.)
     const unsigned here =
         __ballot_sync(0xffffffffu, slot < tiles + n && slot >= tiles + n - mine);
-    if (here != 0 && r.expert < 0) {
+    if (here != 0) {
       const int src = __ffs(here) - 1;
-      r.expert = base + src - 1;
+      r.expert = base + src;
       const int first = __shfl_sync(0xffffffffu, tiles + n - mine, src);
       r.lo = __shfl_sync(0xffffffffu, before, src) + (slot - first) * p.tile_rows;
-      r.hi = min(r.lo + p.tile_rows, __shfl_sync(0xffffffffu, v, src));
+      r.hi = min(r.lo + p.tile_rows, __shfl_sync(0xffffffffu, end, src));
     }
     tiles += __shfl_sync(0xffffffffu, n, 31);
-    last = __shfl_sync(0xffffffffu, v, 31);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0 && slot == 0)
     raise_fault(p.fault, kFaultGroupOffsets);
