@@ -421,6 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                  p.timeout_ns, &bars->abort, kFaultTcProducerWait, freed);
           if (!ok) break;
           if (half == kHalves - 1) {
+            // The proxy fence keeps TMA's refill behind the loads above, which may still
+            // be on their way (2 % of the time; with the arrival after the stores'
+            // fence below it was 10 to 15 %).
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[r]));
           }
