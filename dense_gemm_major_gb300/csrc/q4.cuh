@@ -41,6 +41,10 @@ __device__ __forceinline__ uint32_t mul_x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Codes less their zeros are made as multiples of 1 / kQ4Unit; results are multiplied by it.
+template <typename T>
+constexpr float kQ4Unit = __is_same(T, __half) ? 1.f : 64.f;
+
 // Volatile, so that no load moves past the arrival that gives its stage back.
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;

@@ -64,8 +64,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A zero as what is added to codes: -(128 + z) in BF16; in FP16 -(1024 + z) and
-// -(64 + z).
+// A zero as what is added to codes: in FP16 -(1024 + z) and -(64 + z), in BF16 -z / 64.
 template <typename T>
 struct Zero {
   uint32_t a, b;
@@ -74,28 +73,30 @@ struct Zero {
       a = 0xE400E400u + z * 0x00010001u;
       b = 0xD400D400u + z * 0x00100010u;
     } else {
-      a = 0xC300C300u + z * 0x00010001u;
+      const float v = (float)z * -0x1p-6f;
+      a = pack2<T>(v, v);
       b = 0;
     }
   }
 };
 
-// The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes, less their zero.  A code
-// in the low mantissa bits of 128 (BF16) or 1024 (FP16) is that plus the code; FP16 has
-// room for one four bits further up, 1024 + 16 q.
+// The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes, less their zero, over
+// kQ4Unit.  FP16: a code in the low mantissa bits of 1024 is that plus the code, and four
+// bits further up 1024 + 16 q.  BF16 has no room for the latter; but the integer n in the
+// low eight bits of a BF16 number is n 2^-133, whether it is subnormal (n < 128) or not, and
+// the multiplication with 2^127, or 2^123 for a code four bits further up, is exact.
 template <typename T>
 __device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, uint32_t (&v)[4]) {
-  if constexpr (__is_same(T, __half)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t x = w >> (8 * i);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = w >> (8 * i);
+    if constexpr (__is_same(T, __half)) {
       v[2 * i] = fma_x2<T>(and_or(x, 0x000F000Fu, 0x64006400u), 0x3C003C00u, z.a);
       v[2 * i + 1] = fma_x2<T>(and_or(x, 0x00F000F0u, 0x64006400u), 0x2C002C00u, z.b);   // 1/16
+    } else {
+      v[2 * i] = fma_x2<T>(x & 0x000F000Fu, 0x7F007F00u, z.a);          // 2^127
+      v[2 * i + 1] = fma_x2<T>(x & 0x00F000F0u, 0x7D007D00u, z.a);      // 2^123
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = fma_x2<T>(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), 0x3F803F80u, z.a);
   }
 }
 
@@ -321,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
 #pragma unroll
       for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
       const int n = n0 + i % kQ4TileN;
-      if (n < p.N) Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v);
+      if (n < p.N)
+        Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
     }
   } else {
     for (int i = threadIdx.x; i < values; i += kThreads) {
@@ -336,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
       float v = 0.f;
       for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
       const int n = n0 + i % kQ4TileN;
-      if (n < p.N) Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v);
+      if (n < p.N)
+        Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
     }
     cluster_sync_all();   // nobody leaves while its sums may still be read
   }

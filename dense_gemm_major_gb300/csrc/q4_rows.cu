@@ -2,7 +2,7 @@
 // Y = X . W^T, the weights rounded to X's type on the way.
 //
 // Bound by reading the codes and by the instructions that make 16-bit values of them
-// (for eight codes 9 of the integer and 8 of the FMA pipe, each at half rate), which
+// (for eight codes 8 or 9 of the integer and 8 of the FMA pipe, each at half rate), which
 // do not depend on the number of rows; so W is the MMA's M side (128 rows per CTA), X
 // its N side (16 to 128).  The values go to tensor memory, from where the MMA reads its
 // A: through shared memory they would be written and read at four times the codes'
@@ -73,19 +73,31 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-// Eight codes as four pairs of weights, in the order of their columns: z -(128 + zero)
-// in BF16, -(1024 + zero) in FP16, twice; s the scale, twice.
+// Eight codes as four pairs of weights over kQ4Unit, in the order of their columns; z:
+// the zero, s: the scale, twice (see zero_term()).  FP16: a code in the low mantissa bits of
+// 1024 is that plus the code.  BF16: the integer n in a number's low eight bits is n
+// 2^-133, so that 2^127 and, four bits further up, 2^123 make both codes of a byte q / 64.
 template <typename T>
 __device__ __forceinline__ void weights8(uint32_t w, uint32_t z, uint32_t s, uint32_t* v) {
-  constexpr uint32_t kOne = __is_same(T, __half) ? 0x3C003C00u : 0x3F803F80u;
-  constexpr uint32_t kBase = __is_same(T, __half) ? 0x64006400u : 0x43004300u;
   const uint32_t h = w >> 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    // Byte j of the low and of the high halves; the other bytes are masked away.
-    const uint32_t x = __byte_perm(w, h, (j + 4) * 0x1100 + j * 0x11);
-    v[j] = mul_x2<T>(fma_x2<T>(and_or(x, 0x000F000Fu, kBase), kOne, z), s);
+    if constexpr (__is_same(T, __half)) {
+      // Byte j of the low and of the high halves; the other bytes are masked away.
+      const uint32_t x = __byte_perm(w, h, (j + 4) * 0x1100 + j * 0x11);
+      v[j] = mul_x2<T>(fma_x2<T>(and_or(x, 0x000F000Fu, 0x64006400u), 0x3C003C00u, z), s);
+    } else {
+      const uint32_t x = __byte_perm(w, w, j * 0x1111) & 0x00F0000Fu;
+      v[j] = mul_x2<T>(fma_x2<T>(x, 0x7D007F00u, z), s);
+    }
   }
+}
+// -(1024 + zero) in FP16, -zero / 64 in BF16, twice.
+template <typename T>
+__device__ __forceinline__ uint32_t zero_term(uint32_t zero) {
+  if constexpr (__is_same(T, __half)) return 0xE400E400u + zero * 0x00010001u;
+  const float v = (float)zero * -0x1p-6f;
+  return pack2<T>(v, v);
 }
 
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
@@ -259,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kRuns; ++i) {
         sv[i] = sc[i] * 0x00010001u;
-        zv[i] = (__is_same(T, __half) ? 0xE400E400u : 0xC300C300u) + (zr[i] & 15u) * 0x00010001u;
+        zv[i] = zero_term<T>(zr[i] & 15u);
       }
       at += far_at;
       if ((pos_in += far_pos) >= p.group) pos_in -= p.group, ++at;
@@ -321,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           T* const y = static_cast<T*>(p.Y) + (long long)(rows.lo + c * 16) * p.ldy + n0 + col;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (c * 16 + j < m_end) y[j * p.ldy] = from_f32_any<T>(__uint_as_float(r[j]));
+            if (c * 16 + j < m_end)
+              y[j * p.ldy] = from_f32_any<T>(__uint_as_float(r[j]) * kQ4Unit<T>);
         }
       }
     }
@@ -353,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       T* const y = static_cast<T*>(p.Y) + (long long)(rows.lo + m) * p.ldy + n0 + col;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (n0 + col + j < p.N) y[j] = from_f32_any<T>(sum[j]);
+        if (n0 + col + j < p.N) y[j] = from_f32_any<T>(sum[j] * kQ4Unit<T>);
     }
     cluster_sync_all();   // no CTA leaves while others read its partial tile
   }
