@@ -97,7 +97,8 @@ PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!one_device(x.device.p, b.device.p) || !same_inner(x.cols, b.rows)) return nullptr;
   gemm_op_t op = GEMM_OP_N;
   int ldb, outer = b.rows, inner = b.cols;
-  if (b.s2 == 1 || b.cols <= 1) {
+  // (A single column with unit stride is a single row stored transposed.)
+  if ((b.s2 == 1 || b.cols <= 1) && !(b.cols == 1 && b.rows > 1 && b.s1 == 1)) {
     ldb = b.s1;
   } else if (b.s1 == 1 || b.rows <= 1) {
     op = GEMM_OP_T;

@@ -1,19 +1,23 @@
 // Products of a few rows with 4-bit weights and group scales: Y = X . W^T,
 // W[n][k] = s[n][k / group] (q[n][k] - z[n][k / group]).
 //
-// Bound by reading the codes, half a byte a weight.  A CTA takes 64 rows of W and a
-// share of K; its 8 warps are 2 groups of 32 rows x 4 ranges of a stage's K, and
-// multiply with mma.sync.m16n8k16: W's rows on the 16-wide side, X's on the 8-wide
-// one.  The integers q - z are exact in 16 bits; each group's sum is kept apart in
-// FP32 and scaled once, so that no product is rounded.  (The tensor cores of
-// tcgen05 would want the 16-bit values in shared memory, four times the bytes that
-// came in, for rows that fill 1/16 of their tile.)
+// A CTA takes 64 rows of W and a share of K; its 8 warps are 2 groups of 32 rows x 4
+// ranges of a stage's K, and multiply with mma.sync.m16n8k16: W's rows on the 16-wide
+// side, X's on the 8-wide one.  The integers q - z are exact in 16 bits; each group's sum
+// is kept apart in FP32 and scaled once, so that no product is rounded.  (On tcgen05, as
+// in q4_rows.cu, a call takes 1 to 2 us longer up to 8 rows: tensor memory and its
+// hand-overs, and a multiplication by the scale for every two weights.)
 //
 // Codes and X come by TMA into a ring.  The sum's order is free as long as both
 // operands have it: a thread's word of eight codes is taken apart as the pairs (0,
-// 4), (1, 5), (2, 6), (3, 7), one mask and shift each, and X's eight values are
-// permuted the same way.  The four ranges of K and then the CTAs of the cluster are
-// added in their order.
+// 4), (1, 5), (2, 6), (3, 7), a mask and a multiply-add each and one shift, and X's eight
+// values are permuted the same way.  The four ranges of K and then the CTAs of the
+// cluster are added in their order.
+//
+// Measured in a graph on changing weights, BF16, groups of 128: 1 x 4096 x 4096 5.5 us, 1 x
+// 8192 x 8192 11.8 (2.9 TB/s of codes and scales; of 64: 12.8, of 32: 14.8).  Without the
+// products the latter takes 9; they are bound by their instructions, of which the integer
+// pipe, at half rate, takes a third.
 #include "q4.cuh"
 
 namespace dgemm {
@@ -373,71 +377,12 @@ cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUten
                           : launch_run<T, 2>(p, q, x, stream);
 }
 
-// ------------------------------------------------------------ weights in 16 bits
-
-// Each thread: the 32 codes of 16 bytes, which share a scale.  A block takes 32 rows x
-// 8 such chunks, a warp's lanes 8 rows x 4 chunks.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    q4_values_kernel(int group, long long tiles_n, int N, int K, int scale_n,
-                     const unsigned char* codes, int ldq, long long stride_q, const T* scales,
-                     const unsigned char* zeros, const int* offsets, T* D, long long ldd) {
-  wait_prior_grids();
-  allow_dependent_grids();
-  const int chunks = (K + 31) / 32, groups = (K + group - 1) / group;
-  const int e = (int)(blockIdx.x / tiles_n);
-  if (offsets != nullptr && offsets[e + 1] <= offsets[e]) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = (int)(blockIdx.x - e * tiles_n) * 32 + (warp & 3) * 8 + (lane >> 2);
-  if (n >= N) return;
-  const unsigned char* const q_row = codes + e * stride_q + (long long)n * ldq;
-  const long long s_row = (long long)e * groups * scale_n + n;
-  T* const d_row = D + ((long long)e * N + n) * ldd;
-  for (int c = (int)blockIdx.y * 8 + (warp >> 2) * 4 + (lane & 3); c < chunks;
-       c += (int)gridDim.y * 8) {
-    const uint4 w = *reinterpret_cast<const uint4*>(q_row + (long long)c * 16);
-    const long long at = s_row + (long long)(c * 32ll / group) * scale_n;
-    const float s = elem_to_f32<T>(scales[at]);
-    const float z = zeros != nullptr ? (float)(zeros[at] & 15) : 8.f;
-    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-    T* const to = d_row + (long long)c * 32;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (c * 32ll + j * 8 >= K) break;     // (ldd has room for whole groups of 8)
-      uint32_t v[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        v[h] = pack2<T>(((float)((q[j] >> (8 * h)) & 15u) - z) * s,
-                        ((float)((q[j] >> (8 * h + 4)) & 15u) - z) * s);
-      *reinterpret_cast<uint4*>(to + j * 8) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream) {
   return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)
                     : launch_typed<__nv_bfloat16>(p, tmQ, tmX, stream);
-}
-
-cudaError_t launch_q4_values(int dtype, int group, int experts, int N, int K, int scale_n,
-                             const unsigned char* codes, int ldq, long long stride_q,
-                             const void* scales, const unsigned char* zeros, const int* offsets,
-                             void* D, long long ldd, cudaStream_t stream) {
-  const long long tiles_n = (N + 31ll) / 32;
-  const int parts = (K + 255) / 256;
-  const dim3 grid((unsigned)(experts * tiles_n), (unsigned)(parts < 65535 ? parts : 65535));
-  if (dtype == 1)
-    return launch_gemm_kernel(q4_values_kernel<__half>, grid, dim3(256), 0, stream, group, tiles_n,
-                              N, K, scale_n, codes, ldq, stride_q,
-                              static_cast<const __half*>(scales), zeros, offsets,
-                              static_cast<__half*>(D), ldd);
-  return launch_gemm_kernel(q4_values_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, group,
-                            tiles_n, N, K, scale_n, codes, ldq, stride_q,
-                            static_cast<const __nv_bfloat16*>(scales), zeros, offsets,
-                            static_cast<__nv_bfloat16*>(D), ldd);
 }
 
 }  // namespace dgemm

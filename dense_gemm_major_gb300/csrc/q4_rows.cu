@@ -12,6 +12,12 @@
 // tiles through distributed shared memory in rank order, so results are reproducible and
 // there is no workspace.
 //
+// Measured in a graph on changing weights, BF16, groups of 128: 40 x 8192 x 8192 14.9 us
+// (2.3 TB/s of codes and scales), 33 x 4096 x 4096 8.1, 128 x 4096 x 4096 10.8.  Without
+// the conversions the former takes 12, without MMAs and loads too 10: the turns of the
+// converting warps, some 5 us before and after them, and 24 of the 152 SMs, which the powers
+// of two leave idle.
+//
 // Roles (640 threads): warp 0 loads the codes (TMA) into a ring of their own, warp 1
 // issues the MMAs, warp 2 loads X, warps 4-19 convert: four groups of 4 warps take turns
 // at 128-deep stages, so that one's waits pass while the others convert.  Warps 4-7
@@ -24,8 +30,9 @@ namespace {
 constexpr int BN = kQ4RowsTileN, BK = kQ4RowsBK;
 constexpr int kThreads = 640;
 constexpr int kConvWarp = 4, kGroups = 4, kGroupWarps = 4;
-// A slot of codes is two stages deep: 128 bytes of each row.  (With one stage, 64
-// bytes, the loads were what took longest: 16.9 against ... us.)
+// A slot of codes is two stages deep: TMA then copies 128 bytes of each row.  (With that
+// and four groups of converting warps, for two groups of 8 and slots of one stage, 17.3 ->
+// 15.8 us at 8192 x 8192, 16 rows.)
 constexpr uint32_t kRawBytes = BN * BK;                     // 16 KB
 constexpr uint32_t kACols = BK / 2;                         // of tensor memory, a stage of W
 

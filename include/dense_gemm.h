@@ -274,7 +274,8 @@ const char *gemm_status_string(gemm_status_t status);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's fault
- * word, which a kernel sets when one of its bounded waits gives up.
+ * word, which a kernel sets when one of its bounded waits gives up (and, bit 9, a
+ * grouped product that was given offsets out of order).
  * Returns GEMM_ERR_DEVICE_TIMEOUT if it was set, GEMM_ERR_LAUNCH if the
  * stream reports an error, else GEMM_OK.  *fault_bits (may be NULL)
  * receives the raw fault bits.

@@ -7,7 +7,7 @@
  * are grouped by expert):
  *   codes   N rows of ldq bytes (a multiple of 16, at least (K + 1) / 2), 16-byte
  *           aligned: columns 2j and 2j + 1 in the low and high half of byte j.
- *           Nothing past a row's last code counts.
+ *           Nothing past a row's last code is read, so the last row may end there.
  *   scales  ceil(K / group) rows of N values of X's type, contiguous
  *   zeros   ceil(K / group) rows of N bytes, contiguous, of which the low four bits
  *           count; or NULL: 8 for all
@@ -45,9 +45,10 @@ extern "C" {
  * expert g, W its matrix, as gemm_grouped does.  X is 16-byte aligned and ldx a
  * multiple of 8, or X is packed (ldx == K) at any alignment of its type, which takes
  * a copy with aligned rows in a workspace first; else GEMM_ERR_MISALIGNED.  Y has any
- * alignment of its type.  FP32 accumulation; one rounding.  (Up to 8 rows, or 16 of a
- * small matrix: the integers code - zero, exact in 16 bits, are multiplied and each
- * group's FP32 sum scaled.  More: the weights are rounded to dtype first.)  K == 0: zeros.
+ * alignment of its type.  FP32 accumulation; one rounding.  (Up to 8 rows, 16 of a
+ * small matrix, or 4 for each expert: the integers code - zero, exact in 16 bits, are
+ * multiplied and each group's FP32 sum scaled.  More: the weights are rounded to dtype
+ * first.)  K == 0: zeros.
  */
 gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, int K, int experts,
                              const void *X, int ldx, const void *codes, int ldq,
