@@ -71,7 +71,8 @@ gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int
   p.C = C, p.ldc = ldc, p.stride_c = 0;
   p.timeout_ns = dgemm::wait_bound_ns();
   const long long most = dgemm::group_units(rows, groups, N, p.tile_rows);
-  const int pairs = (int)(most < max_pairs ? most : max_pairs);
+  p.parts = dgemm::group_parts(most, p.K, p.tile_rows, max_pairs);
+  const int pairs = (int)(most * p.parts < max_pairs ? most * p.parts : max_pairs);
   return status_of(dgemm::launch_group(dtype, dtype_c, p, &tmM, &tmN, &tmN16, pairs, stream));
 }
 

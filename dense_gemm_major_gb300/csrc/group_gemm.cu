@@ -15,6 +15,9 @@
 // (even CTA), warp 2 clears the rows past a group's end (weights' gradient),
 // warps 4-11 drain the accumulators and store.
 //
+// Few units of few rows would leave most SMs idle: up to four pairs of a cluster then
+// share a unit's K and add their sums through distributed shared memory, in their order.
+//
 // Measured (8 experts of 4096 x 4096, 8192 rows, in a graph): forward 161 us (1.70
 // PFLOP/s); weights' gradient in FP32 206, in BF16 171.  What bounds them is what moves
 // between L2 and the SMs, 128 KB for each k-tile of a unit and the results: forward without
@@ -76,7 +79,7 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 }
 
 template <typename T, typename TC, int kKind, int kRows>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     group_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN,
                  const __grid_constant__ CUtensorMap tmN16, const GroupParams p) {
   using L = Layout<kRows>;
@@ -89,8 +92,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   static_assert(sizeof(Barriers<S>) <= 512, "barrier block must fit its reserved space");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
-  const int npairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  // A cluster is a pair, or (kParts) up to four, which share a unit's K.
+  constexpr bool kParts = kRows == 64;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1u;          // 0: issues the pair's MMAs
+  const uint32_t leader = crank & ~1u;
+  const uint16_t both = (uint16_t)(0x3u << leader);
+  const int parts = kParts ? p.parts : 1, part = (int)(crank >> 1);
+  const int clusters = (int)gridDim.x / (2 * parts), cluster = (int)blockIdx.x / (2 * parts);
   constexpr bool kWeights = kKind == kGroupWeights;
   constexpr bool kMK = kKind == kGroupForward;   // the M side is K-major
   constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
@@ -133,20 +142,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       RingPos<S> pos;
       uint32_t it = 0;
       bool ok = true;
-      for (int u = pair; u < units && ok; u += npairs) {
+      for (int u = cluster; u < units && ok; u += clusters) {
         const GroupUnit w = group_unit<kKind, kRows>(u, p, tables);
         const int half = w.mma_rows / 2;                 // rows of C that this CTA loads
         const int row = w.row + (int)rank * half;
         const int col = w.col + (int)rank * 128;
         const int z = w.g * p.zmul;
-        for (int kt = 0; kt < w.nk; ++kt, ++it, pos.next()) {
+        const int k_first = kParts ? group_part_first(w.nk, part, parts) : 0;
+        const int k_last = kParts ? group_part_first(w.nk, part + 1, parts) : w.nk;
+        for (int kt = k_first; kt < k_last; ++kt, ++it, pos.next()) {
           const uint32_t s = pos.slot;
           ok = role_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
                          &bars->abort, kFaultTcProducerWait, true);
           if (!ok) break;
           const uint32_t sm = smem_u32(base + s * kStage), sn = sm + kSide;
           const uint32_t full = smem_u32(&bars->full[s]);
-          const uint32_t fb = mapa_shared(full, 0);
+          const uint32_t fb = mapa_shared(full, leader);
           if constexpr (kWeights) {
             const int k = w.k0 + kt * BK;
             const int valid = w.k_end - k;               // rows of the group from k on
@@ -207,12 +218,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ready = false;
       uint32_t seg = 0;
       bool ok = true;
-      for (int u = pair; u < units && ok; u += npairs) {
+      for (int u = cluster; u < units && ok; u += clusters) {
         const GroupUnit w = group_unit<kKind, kRows>(u, p, tables);
         const uint32_t idesc = instr_desc(kAb, 256, (uint32_t)w.mma_rows, kMK ? 0u : 1u,
                                           kWeights ? 1u : 0u);
-        for (int k0 = 0; k0 < w.nk && ok; k0 += p.seg, ++seg) {
-          const int k1 = min(k0 + p.seg, w.nk);
+        const int k_first = kParts ? group_part_first(w.nk, part, parts) : 0;
+        const int k_last = kParts ? group_part_first(w.nk, part + 1, parts) : w.nk;
+        for (int k0 = k_first; k0 < k_last && ok; k0 += p.seg, ++seg) {
+          const int k1 = min(k0 + p.seg, k_last);
           const uint32_t b = seg & 1;
           ok = role_wait(smem_u32(&bars->acc_empty[b]), ((seg >> 1) & 1u) ^ 1u, p.fault,
                          p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
@@ -243,10 +256,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mlo + ((kMK ? (k >> 2) * kBlock + (k & 3) * 32 : k * 2048) >> 4),
                     nlo + ((kWeights ? k * 2048 : (k >> 2) * L::kNBlock + (k & 3) * 32) >> 4), idesc,
                     (kt > k0 || k > 0) ? 1u : 0u);
-            mma_commit_pair_multicast(freed, 0x3);
+            mma_commit_pair_multicast(freed, both);
           }
           if (!ok) break;
-          mma_commit_pair_multicast(smem_u32(&bars->acc_full[b]), 0x3);
+          mma_commit_pair_multicast(smem_u32(&bars->acc_full[b]), both);
         }
       }
     }
@@ -258,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // operands (zero times a NaN is not zero).
       uint32_t it = 0, uses = 0;   // a bit per slot: the parity of its next use
       bool ok = true;
-      for (int u = pair; u < units && ok; u += npairs) {
+      for (int u = cluster; u < units && ok; u += clusters) {
         const GroupUnit w = group_unit<kKind, kRows>(u, p, tables);
         it += (uint32_t)w.nk;
         const int valid = w.k_end - w.k0 - (w.nk - 1) * BK;
@@ -277,18 +290,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), 0));
+        if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->full[s]), leader));
       }
       __syncwarp();
     }
   } else if (warp >= kEpiWarp) {
-    group_epilogue<TC, kKind, kRows>(p, tables, bars, tmem_base, rank, warp - kEpiWarp, pair, npairs);
+    group_epilogue<TC, kKind, kRows>(p, tables, bars, tmem_base, crank, warp - kEpiWarp, cluster,
+                                     clusters, reinterpret_cast<float*>(base));
+  }
+
+  if constexpr (kParts) {
+    if (parts > 1) {
+      // The parts' sums in their order, each CTA for some rows of its columns.
+      cluster_sync_all();
+      if (cluster < units) {
+        const GroupUnit w = group_unit<kKind, kRows>(cluster, p, tables);
+        // Four columns of a row per thread, all parts' values on their way at once.
+        const int pieces = (w.row_end - w.row) * 32;
+        for (int i = part * kThreads + (int)threadIdx.x; i < pieces; i += parts * kThreads) {
+          const uint32_t at = smem_u32(base) + (uint32_t)i * 16u;
+          float4 v[kGroupMaxParts];
+#pragma unroll
+          for (int j = 0; j < kGroupMaxParts; ++j)
+            v[j] = j < parts ? ld_cluster_v4(mapa_shared(at, 2u * j + rank))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+          float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+          for (int j = 1; j < kGroupMaxParts; ++j)
+            sum[0] += v[j].x, sum[1] += v[j].y, sum[2] += v[j].z, sum[3] += v[j].w;
+          const int col = w.col + (int)rank * 128 + (i & 31) * 4;
+          TC* const c = static_cast<TC*>(p.C) + (long long)(w.row + (i >> 5)) * p.ldc + col;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < p.N) {
+              const float x = p.alpha * sum[e];
+              c[e] = from_f32_any<TC>(p.beta == 0.f ? x : fmaf(p.beta, to_f32_any<TC>(c[e]), x));
+            }
+        }
+      }
+    }
   }
 
   // ------------------------------------------------ teardown
   if (warp == 1 && rank == 0 && elect_one()) {
     // Every MMA of the pair has completed before TMEM is freed.
-    mma_commit_pair_multicast(smem_u32(&bars->drain), 0x1);
+    mma_commit_pair_multicast(smem_u32(&bars->drain), (uint16_t)(1u << leader));
     if (!mbar_wait_bounded(smem_u32(&bars->drain), 0, p.timeout_ns, nullptr))
       raise_fault(p.fault, kFaultDrainWait);
   }
@@ -307,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // neither CTA leaves while the pair may still touch its memory
+  cluster_sync_all();   // no CTA leaves while others may still touch its memory
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
@@ -321,8 +367,9 @@ cudaError_t launch_typed(const GroupParams& p, const CUtensorMap* tmM, const CUt
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(kernel, Layout<kRows>::kSmem, &done);
   if (e != cudaSuccess) return e;
-  return launch_gemm_kernel(kernel, dim3(2 * pairs), dim3(kThreads), Layout<kRows>::kSmem, stream,
-                            *tmM, *tmN, *tmN16, p);
+  return launch_gemm_kernel_clusters(2 * (unsigned)p.parts, kernel, dim3(2 * pairs),
+                                     dim3(kThreads), Layout<kRows>::kSmem, stream, *tmM, *tmN,
+                                     *tmN16, p);
 }
 
 template <typename T, typename TC>

@@ -156,29 +156,54 @@ __device__ __forceinline__ GroupUnit group_unit(int u, const GroupParams& p,
   return w;
 }
 
+// First k-tile of a part of a unit's nk.
+__device__ __forceinline__ int group_part_first(int nk, int part, int parts) {
+  return (int)((long long)nk * part / parts);
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------ draining
 
-// Drains a pair's units (both CTAs, kGroupEpiWarps warps each): warp `ew` takes TMEM
-// lanes 32 (ew % 4) .. + 31 (columns of C) and every other 32 rows.
+// Drains a cluster's units (each CTA, kGroupEpiWarps warps): warp `ew` takes TMEM lanes
+// 32 (ew % 4) .. + 31 (columns of C) and every other 32 rows.  Where pairs share a unit
+// (p.parts > 1: no more than one for the cluster), their sums go to shared memory, `sums`,
+// row by row of the CTA's 128 columns.
 template <typename TC, int kKind, int kRows, typename Bars>
 __device__ __forceinline__ void group_epilogue(const GroupParams& p, const GroupTables& t,
-                                               Bars* bars, uint32_t tmem_base, uint32_t rank,
-                                               int ew, int pair, int npairs) {
+                                               Bars* bars, uint32_t tmem_base, uint32_t crank,
+                                               int ew, int cluster, int clusters, float* sums) {
   const int lane = threadIdx.x & 31;
   const int q = ew & 3, half = ew >> 2;
-  constexpr bool kWeights = kKind == kGroupWeights;
+  constexpr bool kWeights = kKind == kGroupWeights, kParts = kRows == 64;
+  const uint32_t rank = crank & 1u, leader = crank & ~1u;
+  const int parts = kParts ? p.parts : 1, part = (int)(crank >> 1);
   const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 && ((p.ldc | p.N) & 1) == 0 &&
                      (p.stride_c & 1) == 0;
   uint32_t seg = 0;
   bool ok = true;
-  for (int u = pair; u < t.units; u += npairs) {
+  for (int u = cluster; u < t.units; u += clusters) {
     const GroupUnit w = group_unit<kKind, kRows>(u, p, t);
     const int chunks = w.mma_rows / 32;
     constexpr int kChunks = kRows / 64;                    // of 32 rows, this warp's
     float acc[32 * kChunks];
 #pragma unroll
     for (int j = 0; j < 32 * kChunks; ++j) acc[j] = 0.f;
-    for (int k0 = 0; k0 < w.nk; k0 += p.seg, ++seg) {
+    const int k_first = kParts ? group_part_first(w.nk, part, parts) : 0;
+    const int k_last = kParts ? group_part_first(w.nk, part + 1, parts) : w.nk;
+    for (int k0 = k_first; k0 < k_last; k0 += p.seg, ++seg) {
       const uint32_t b = seg & 1;
       ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
                            &bars->abort, kFaultTcEpilogueWait, false, false);
@@ -197,9 +222,17 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), 0));
+      if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), leader));
     }
     if (!ok) break;
+    if (kParts && parts > 1) {
+      if (half < chunks) {
+        float* const to = sums + half * 32 * 128 + q * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) to[j * 128] = acc[j];
+      }
+      break;
+    }
     const int col = w.col + (int)rank * 128 + q * 32 + lane;
     TC* c_out = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0);
 #pragma unroll

@@ -104,12 +104,6 @@ __device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, ui
   }
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // kRun: steps of 32 terms that have one scale (1, 2, or 4: a warp's slice of a stage, where
 // groups are a multiple of 128).
 template <typename T, int kTiles, int kRun>

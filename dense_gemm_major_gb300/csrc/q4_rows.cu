@@ -107,14 +107,6 @@ __device__ __forceinline__ uint32_t zero_term(uint32_t zero) {
   return pack2<T>(v, v);
 }
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 // kRun: columns that have one scale (32, 64, or a stage's 128).
 template <typename T, int MT, int kRun>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -131,6 +131,39 @@ def _like(v):
     return buf[:, :v.shape[1]]
 
 
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32")])
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("case", [([1], 100, 4096), ([64], 256, 1040), ([5, 0, 60, 1], 513, 3000),
+                                  ([33], 130, 8200), ([0, 0, 2], 1030, 2056), ([64, 64, 64], 600, 1100)],
+                         ids=lambda c: f"{len(c[0])}x{sum(c[0])}-{c[1]}-{c[2]}")
+def test_pairs_that_share_long_sums(dg, dtype, out, op, case):
+    """Few units of few rows: two or four pairs share K, scaled results too."""
+    sizes, N, K = case
+    gen = torch.Generator("cuda").manual_seed(N)
+    rows = sum(sizes)
+    off = _offsets(sizes, 2)
+    a = _padded((rows + 5, K), dtype, gen, pad=8)
+    a[:2], a[rows + 2:] = NAN, NAN
+    b = _padded((len(sizes), K, N) if op == "N" else (len(sizes), N, K), dtype, gen)
+    bm = b if op == "N" else b.transpose(1, 2)
+    old = torch.randn((rows + 5, N), generator=gen, device="cuda").to(TYPES[out])
+    for alpha, beta in ((1.0, 0.0), (0.5, -2.0)):
+        c = old.clone()
+        dg.grouped_matmul(a, bm, off, out=c, alpha=alpha, beta=beta)
+        check_device(dg)
+        assert torch.equal(c[:2], old[:2]) and torch.equal(c[rows + 2:], old[rows + 2:])
+        lo = 2
+        for g, n in enumerate(sizes):
+            x, w, o = a[lo:lo + n].double(), bm[g].double(), old[lo:lo + n].double()
+            if n:
+                _check(c[lo:lo + n], alpha * (x @ w) + beta * o,
+                       abs(alpha) * (x.abs() @ w.abs()) + abs(beta) * o.abs(), K + 1, out)
+            lo += n
+        again = old.clone()
+        dg.grouped_matmul(a, bm, off, out=again, alpha=alpha, beta=beta)
+        assert torch.equal(again, c)
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_scaled_and_accumulated(dg, out):
     gen = torch.Generator("cuda").manual_seed(3)
