@@ -71,8 +71,9 @@ gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int
   p.C = C, p.ldc = ldc, p.stride_c = 0;
   p.timeout_ns = dgemm::wait_bound_ns();
   const long long most = dgemm::group_units(rows, groups, N, p.tile_rows);
-  p.parts = dgemm::group_parts(most, p.K, p.tile_rows, max_pairs);
-  const int pairs = (int)(most * p.parts < max_pairs ? most * p.parts : max_pairs);
+  p.log_parts = dgemm::group_log_parts(most, p.K, max_pairs);
+  const long long want = most << p.log_parts;
+  const int pairs = (int)(want < max_pairs ? want : max_pairs);
   return status_of(dgemm::launch_group(dtype, dtype_c, p, &tmM, &tmN, &tmN16, pairs, stream));
 }
 
@@ -123,7 +124,9 @@ gemm_status_t gemm_grouped_grad(int dtype, int dtype_c, int rows, int M, int N, 
   p.C = C, p.ldc = ldc, p.stride_c = groups > 1 ? stride_c : 0;
   p.timeout_ns = dgemm::wait_bound_ns();
   const long long units = (long long)groups * p.per_group;
-  const int pairs = (int)(units < max_pairs ? units : max_pairs);
+  p.log_parts = dgemm::group_log_parts(units, empty ? 0 : rows / groups, max_pairs);
+  const long long want = units << p.log_parts;
+  const int pairs = (int)(want < max_pairs ? want : max_pairs);
   return status_of(dgemm::launch_group(dtype, dtype_c, p, &tmM, &tmN, &tmN, pairs, stream));
 }
 

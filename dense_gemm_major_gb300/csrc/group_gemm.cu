@@ -15,8 +15,7 @@
 // (even CTA), warp 2 clears the rows past a group's end (weights' gradient),
 // warps 4-11 drain the accumulators and store.
 //
-// Few units of few rows would leave most SMs idle: up to four pairs of a cluster then
-// share a unit's K and add their sums through distributed shared memory, in their order.
+// Few units would leave most SMs idle: up to four pairs of a cluster then share a unit's K and add their sums through distributed shared memory, in their order.
 //
 // Measured (8 experts of 4096 x 4096, 8192 rows, in a graph): forward 161 us (1.70
 // PFLOP/s); weights' gradient in FP32 206, in BF16 171.  What bounds them is what moves
@@ -92,14 +91,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(sizeof(Barriers<S>) <= 512, "barrier block must fit its reserved space");
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // A cluster is a pair, or (kParts) up to four, which share a unit's K.
-  constexpr bool kParts = kRows == 64;
+  // A cluster is a pair, or up to four, which share a unit's K.
   const uint32_t crank = cluster_ctarank();
   const uint32_t rank = crank & 1u;          // 0: issues the pair's MMAs
   const uint32_t leader = crank & ~1u;
   const uint16_t both = (uint16_t)(0x3u << leader);
-  const int parts = kParts ? p.parts : 1, part = (int)(crank >> 1);
-  const int clusters = (int)gridDim.x / (2 * parts), cluster = (int)blockIdx.x / (2 * parts);
+  const int parts = 1 << p.log_parts, part = (int)(crank >> 1);
+  const int clusters = (int)gridDim.x >> (1 + p.log_parts);
+  const int cluster = (int)blockIdx.x >> (1 + p.log_parts);
   constexpr bool kWeights = kKind == kGroupWeights;
   constexpr bool kMK = kKind == kGroupForward;   // the M side is K-major
   constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
@@ -148,8 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = w.row + (int)rank * half;
         const int col = w.col + (int)rank * 128;
         const int z = w.g * p.zmul;
-        const int k_first = kParts ? group_part_first(w.nk, part, parts) : 0;
-        const int k_last = kParts ? group_part_first(w.nk, part + 1, parts) : w.nk;
+        const int k_first = group_part_first(w.nk, part, p);
+        const int k_last = group_part_first(w.nk, part + 1, p);
         for (int kt = k_first; kt < k_last; ++kt, ++it, pos.next()) {
           const uint32_t s = pos.slot;
           ok = role_wait(smem_u32(&bars->empty[s]), pos.parity ^ 1u, p.fault, p.timeout_ns,
@@ -222,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const GroupUnit w = group_unit<kKind, kRows>(u, p, tables);
         const uint32_t idesc = instr_desc(kAb, 256, (uint32_t)w.mma_rows, kMK ? 0u : 1u,
                                           kWeights ? 1u : 0u);
-        const int k_first = kParts ? group_part_first(w.nk, part, parts) : 0;
-        const int k_last = kParts ? group_part_first(w.nk, part + 1, parts) : w.nk;
+        const int k_first = group_part_first(w.nk, part, p);
+        const int k_last = group_part_first(w.nk, part + 1, p);
         for (int k0 = k_first; k0 < k_last && ok; k0 += p.seg, ++seg) {
           const int k1 = min(k0 + p.seg, k_last);
           const uint32_t b = seg & 1;
@@ -273,9 +272,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = cluster; u < units && ok; u += clusters) {
         const GroupUnit w = group_unit<kKind, kRows>(u, p, tables);
-        it += (uint32_t)w.nk;
+        const int k_first = group_part_first(w.nk, part, p);
+        const int k_last = group_part_first(w.nk, part + 1, p);
+        it += (uint32_t)(k_last - k_first);
         const int valid = w.k_end - w.k0 - (w.nk - 1) * BK;
-        if (w.nk == 0 || (valid & 15) == 0) continue;
+        if (k_last == k_first || k_last != w.nk || (valid & 15) == 0) continue;
         const uint32_t s = (it - 1) % S;
         ok = role_wait_lanes(smem_u32(&bars->tail[s]), (uses >> s) & 1u, p.fault, p.timeout_ns,
                              &bars->abort, kFaultTcProducerWait);
@@ -299,34 +300,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      clusters, reinterpret_cast<float*>(base));
   }
 
-  if constexpr (kParts) {
-    if (parts > 1) {
-      // The parts' sums in their order, each CTA for some rows of its columns.
-      cluster_sync_all();
-      if (cluster < units) {
-        const GroupUnit w = group_unit<kKind, kRows>(cluster, p, tables);
-        // Four columns of a row per thread, all parts' values on their way at once.
-        const int pieces = (w.row_end - w.row) * 32;
-        for (int i = part * kThreads + (int)threadIdx.x; i < pieces; i += parts * kThreads) {
-          const uint32_t at = smem_u32(base) + (uint32_t)i * 16u;
-          float4 v[kGroupMaxParts];
+  if (parts > 1) {
+    // The parts' sums in their order, each CTA for some rows of its columns.
+    cluster_sync_all();
+    if (cluster < units) {
+      const GroupUnit w = group_unit<kKind, kRows>(cluster, p, tables);
+      // Four columns of a row per thread, all parts' values on their way at once.
+      const int pieces = (w.row_end - w.row) * 32;
+      for (int i = part * kThreads + (int)threadIdx.x; i < pieces; i += parts * kThreads) {
+        const uint32_t at = smem_u32(base) + (uint32_t)i * 16u;
+        float4 v[kGroupMaxParts];
 #pragma unroll
-          for (int j = 0; j < kGroupMaxParts; ++j)
-            v[j] = j < parts ? ld_cluster_v4(mapa_shared(at, 2u * j + rank))
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        for (int j = 0; j < kGroupMaxParts; ++j)
+          v[j] = j < parts ? ld_cluster_v4(mapa_shared(at, 2u * j + rank))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-          for (int j = 1; j < kGroupMaxParts; ++j)
-            sum[0] += v[j].x, sum[1] += v[j].y, sum[2] += v[j].z, sum[3] += v[j].w;
-          const int col = w.col + (int)rank * 128 + (i & 31) * 4;
-          TC* const c = static_cast<TC*>(p.C) + (long long)(w.row + (i >> 5)) * p.ldc + col;
+        for (int j = 1; j < kGroupMaxParts; ++j)
+          sum[0] += v[j].x, sum[1] += v[j].y, sum[2] += v[j].z, sum[3] += v[j].w;
+        const int col = w.col + (int)rank * 128 + (i & 31) * 4;
+        TC* const c = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0) +
+                      (long long)(w.row + (i >> 5)) * p.ldc + col;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < p.N) {
-              const float x = p.alpha * sum[e];
-              c[e] = from_f32_any<TC>(p.beta == 0.f ? x : fmaf(p.beta, to_f32_any<TC>(c[e]), x));
-            }
-        }
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.N) {
+            const float x = p.alpha * sum[e];
+            c[e] = from_f32_any<TC>(p.beta == 0.f ? x : fmaf(p.beta, to_f32_any<TC>(c[e]), x));
+          }
       }
     }
   }
@@ -367,7 +367,7 @@ cudaError_t launch_typed(const GroupParams& p, const CUtensorMap* tmM, const CUt
   static std::atomic<uint64_t> done{0};
   cudaError_t e = mx_allow_smem(kernel, Layout<kRows>::kSmem, &done);
   if (e != cudaSuccess) return e;
-  return launch_gemm_kernel_clusters(2 * (unsigned)p.parts, kernel, dim3(2 * pairs),
+  return launch_gemm_kernel_clusters(2u << p.log_parts, kernel, dim3(2 * pairs),
                                      dim3(kThreads), Layout<kRows>::kSmem, stream, *tmM, *tmN,
                                      *tmN16, p);
 }

@@ -156,9 +156,9 @@ __device__ __forceinline__ GroupUnit group_unit(int u, const GroupParams& p,
   return w;
 }
 
-// First k-tile of a part of a unit's nk.
-__device__ __forceinline__ int group_part_first(int nk, int part, int parts) {
-  return (int)((long long)nk * part / parts);
+// First k-tile of a part of a unit's nk (at most 2^24).
+__device__ __forceinline__ int group_part_first(int nk, int part, const GroupParams& p) {
+  return nk * part >> p.log_parts;
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -179,7 +179,7 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 
 // Drains a cluster's units (each CTA, kGroupEpiWarps warps): warp `ew` takes TMEM lanes
 // 32 (ew % 4) .. + 31 (columns of C) and every other 32 rows.  Where pairs share a unit
-// (p.parts > 1: no more than one for the cluster), their sums go to shared memory, `sums`,
+// (p.log_parts > 0: no more than one for the cluster), their sums go to shared memory, `sums`,
 // row by row of the CTA's 128 columns.
 template <typename TC, int kKind, int kRows, typename Bars>
 __device__ __forceinline__ void group_epilogue(const GroupParams& p, const GroupTables& t,
@@ -187,9 +187,9 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
                                                int ew, int cluster, int clusters, float* sums) {
   const int lane = threadIdx.x & 31;
   const int q = ew & 3, half = ew >> 2;
-  constexpr bool kWeights = kKind == kGroupWeights, kParts = kRows == 64;
+  constexpr bool kWeights = kKind == kGroupWeights;
   const uint32_t rank = crank & 1u, leader = crank & ~1u;
-  const int parts = kParts ? p.parts : 1, part = (int)(crank >> 1);
+  const int part = (int)(crank >> 1);
   const bool pairs = (reinterpret_cast<uintptr_t>(p.C) & 3u) == 0 && ((p.ldc | p.N) & 1) == 0 &&
                      (p.stride_c & 1) == 0;
   uint32_t seg = 0;
@@ -201,8 +201,8 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
     float acc[32 * kChunks];
 #pragma unroll
     for (int j = 0; j < 32 * kChunks; ++j) acc[j] = 0.f;
-    const int k_first = kParts ? group_part_first(w.nk, part, parts) : 0;
-    const int k_last = kParts ? group_part_first(w.nk, part + 1, parts) : w.nk;
+    const int k_first = group_part_first(w.nk, part, p);
+    const int k_last = group_part_first(w.nk, part + 1, p);
     for (int k0 = k_first; k0 < k_last; k0 += p.seg, ++seg) {
       const uint32_t b = seg & 1;
       ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (seg >> 1) & 1u, p.fault, p.timeout_ns,
@@ -225,11 +225,15 @@ __device__ __forceinline__ void group_epilogue(const GroupParams& p, const Group
       if (lane == 0) mbar_arrive_any_cta(mapa_shared(smem_u32(&bars->acc_empty[b]), leader));
     }
     if (!ok) break;
-    if (kParts && parts > 1) {
-      if (half < chunks) {
-        float* const to = sums + half * 32 * 128 + q * 32 + lane;
+    if (p.log_parts > 0) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) to[j * 128] = acc[j];
+      for (int c = 0; c < kChunks; ++c) {
+        const int chunk = 2 * c + half;
+        if (chunk < chunks) {
+          float* const to = sums + chunk * 32 * 128 + q * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) to[j * 128] = acc[c * 32 + j];
+        }
       }
       break;
     }

@@ -164,6 +164,45 @@ def test_pairs_that_share_long_sums(dg, dtype, out, op, case):
         assert torch.equal(again, c)
 
 
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("case", [([1100], 100, 130), ([1500], 300, 500), ([4000, 0, 1111], 256, 256),
+                                  ([1, 5000], 65, 513), ([3001, 3000], 520, 256)],
+                         ids=lambda c: f"{len(c[0])}x{sum(c[0])}-{c[1]}-{c[2]}")
+def test_pairs_that_share_a_gradient(dg, dtype, out, case):
+    """Few units over many rows, with NaN around the groups; and large products of one
+    group, whose tiles have more than 64 rows."""
+    sizes, M, N = case
+    gen = torch.Generator("cuda").manual_seed(M)
+    rows = sum(sizes)
+    off = _offsets(sizes, 2)
+    a, x = _padded((rows + 5, M), dtype, gen, pad=8), _padded((rows + 5, N), dtype, gen)
+    a[:2], a[rows + 2:], x[:2], x[rows + 2:] = NAN, NAN, NAN, NAN
+    old = torch.randn((len(sizes), M, N), generator=gen, device="cuda").to(TYPES[out])
+    for alpha, beta in ((1.0, 0.0), (0.5, 1.0)):
+        c = old.clone()
+        dg.grouped_grad(a, x, off, out=c, alpha=alpha, beta=beta)
+        check_device(dg)
+        lo = 2
+        for g, n in enumerate(sizes):
+            p, q, o = a[lo:lo + n].double(), x[lo:lo + n].double(), old[g].double()
+            _check(c[g], alpha * (p.t() @ q) + beta * o,
+                   abs(alpha) * (p.abs().t() @ q.abs()) + abs(beta) * o.abs(), n + 1, out)
+            lo += n
+        again = old.clone()
+        dg.grouped_grad(a, x, off, out=again, alpha=alpha, beta=beta)
+        assert torch.equal(again, c)
+    wide = _padded((rows + 5, 3000), dtype, gen)
+    few = _offsets([200, rows - 200] if len(sizes) > 1 else [rows])
+    w = _padded((few.numel() - 1, 3000, N), dtype, gen)
+    y = dg.grouped_matmul(wide, w, few, dtype=TYPES[out])
+    check_device(dg)
+    lo = 0
+    for g, n in enumerate(few.diff().tolist()):
+        p, q = wide[lo:lo + n].double(), w[g].double()
+        _check(y[lo:lo + n], p @ q, p.abs() @ q.abs(), 3000, out)
+        lo += n
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_scaled_and_accumulated(dg, out):
     gen = torch.Generator("cuda").manual_seed(3)
