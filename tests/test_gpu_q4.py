@@ -177,6 +177,31 @@ def test_special_values_stay_in_their_row_and_column(dg, rows):
     check_device(dg)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,K", [(1, 100), (20, 1), (20, 100), (40, 1031), (100, 157), (800, 100)])
+def test_scales_whose_codes_past_the_end_would_overflow(dg, dtype, rows, K):
+    """Codes 7 to 9 of scales of 9000: the weights are finite, 8 times the scale is not in
+    FP16.  Nothing past a row's last code counts, whatever it stands for."""
+    gen = torch.Generator("cuda").manual_seed(rows + K)
+    x = (_x(gen, rows, K, "bf16") * 0.01).to(TYPES[dtype])
+    buf = torch.full((rows, -(-K // 8) * 8 + 8), NAN, dtype=TYPES[dtype], device="cuda")
+    buf[:, :K] = x
+    n = -(-K // 128)
+    codes = torch.randint(0, 256, (130, -(-K // 32) * 16), generator=gen, device="cuda",
+                          dtype=torch.uint8)
+    k = torch.arange(K, device="cuda")
+    q = torch.randint(7, 10, (130, K), generator=gen, device="cuda")
+    for half in (0, 1):
+        at = k[k % 2 == half]
+        keep = 0xF0 if half == 0 else 0x0F
+        codes[:, at // 2] = (codes[:, at // 2] & keep) | (q[:, at] << (4 * half)).to(torch.uint8)
+    scales = torch.full((130, n), 9000.0, device="cuda").to(TYPES[dtype])
+    w = dg.Q4Tensor(codes, scales, cols=K, group=128)
+    values = scales[:, k // 128].double() * (q - 8).double()
+    _check(dg.q4_linear(buf[:, :K], w), buf[:, :K], values, K, dtype, rows > 8)
+    check_device(dg)
+
+
 @pytest.mark.parametrize("rows", [1, 5, 70, 300])
 def test_contiguous_x_of_any_width(dg, rows):
     gen = torch.Generator("cuda").manual_seed(5)
