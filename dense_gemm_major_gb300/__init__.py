@@ -700,8 +700,8 @@ class Q4Tensor:
             raise ValueError("1 to 1024 experts")
         rows = lead[-1]
         ld = codes.stride(-2) if rows > 1 else -(-width // 16) * 16
-        if codes.dim() == 3 and lead[0] > 1:
-            if rows <= 1:
+        if codes.dim() == 3 and lead[0] > 1 and rows > 0:
+            if rows == 1:
                 ld = codes.stride(0)
             if codes.stride(0) != rows * ld:
                 raise ValueError("experts' codes must follow one another")

@@ -231,6 +231,20 @@ def test_empty_calls(dg):
     check_device(dg)
 
 
+def test_weights_without_rows(dg):
+    """Experts of no outputs, and of one, whose codes' rows are the experts' distance."""
+    gen = torch.Generator("cuda").manual_seed(16)
+    x = _x(gen, 5, 64, "bf16")
+    none = dg.Q4Tensor(torch.zeros((3, 0, 32), dtype=torch.uint8, device="cuda"),
+                       torch.zeros((3, 0, 1), dtype=torch.bfloat16, device="cuda"))
+    assert dg.q4_linear(x, none, offsets=_offsets([1, 2, 2])).shape == (5, 0)
+    w, values = _weights(dg, gen, (3, 1), 64, "bf16", 32, True, pad=16)
+    y = dg.q4_linear(x, w, offsets=_offsets([1, 2, 2]))
+    for g, (lo, hi) in enumerate(((0, 1), (1, 3), (3, 5))):
+        _check(y[lo:hi], x[lo:hi], values[g], 64, "bf16")
+    check_device(dg)
+
+
 @pytest.mark.parametrize("rows", [10, 700])
 @pytest.mark.parametrize("raw,meant", [([0, 5, 3, 9], [0, 5, 5, 9]), ([-4, 2, 6, 9], [0, 2, 6, 9]),
                                        ([0, 5000, 6, 9], [0, -1, -1, -1])])
