@@ -47,8 +47,10 @@ struct Layout {
   // waited for kGroups stages ago, so that there need to be that many.
   static constexpr int S = MT <= 64 ? 6 : 4, R = 6;
   static_assert(S >= kGroups && R % 2 == 0, "phases");
-  static constexpr uint32_t kSmem = S * kStage + R * kRawBytes + 512 + 1024;
-  static_assert(kSmem <= 232448, "shared memory");
+  // All of an SM's (s_rows is beside it), so that no CTA of another cluster with tensor
+  // memory is: two clusters could each hold on one SM what the other waits for on another.
+  static constexpr uint32_t kSmem = 232448 - 1024;
+  static_assert(S * kStage + R * kRawBytes + 512 + 1024 <= kSmem, "shared memory");
   static_assert(MT * BN * 4 <= S * kStage + R * kRawBytes, "partial tiles reuse the rings");
   // Tensor memory: the accumulator, then W's stages.
   static constexpr uint32_t kACol = MT < 32 ? 32 : MT;

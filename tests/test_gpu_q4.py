@@ -317,6 +317,42 @@ def test_stream_argument_and_the_allocator(dg):
     check_device(dg)
 
 
+def test_two_streams_at_once(dg):
+    """Products with 4-bit weights of every kernel on one stream, others that use tensor
+    memory on another."""
+    gen = torch.Generator("cuda").manual_seed(17)
+    w, _ = _weights(dg, gen, (1024,), 4096, "bf16", 128, True)
+    e, _ = _weights(dg, gen, (4, 512), 1024, "bf16", 32, True)
+    m = dg.mx_quantize(torch.randn((1024, 4096), generator=gen, device="cuda").bfloat16())
+    g = torch.randn((4, 1024, 512), generator=gen, device="cuda").bfloat16()
+    xs = [_x(gen, rows, 4096, "bf16") for rows in (5, 16, 33, 100, 900)]
+    r = _x(gen, 70, 1024, "bf16")
+    packed = torch.randn((33, 4095), generator=gen, device="cuda").bfloat16()
+    wp, _ = _weights(dg, gen, (200,), 4095, "bf16", 128, True)
+    off = _offsets([30, 0, 15, 25])
+
+    def one():
+        return [dg.q4_linear(x, w) for x in xs] + [dg.q4_linear(r, e, offsets=off),
+                                                   dg.q4_linear(packed, wp)]
+
+    def two():
+        return ([dg.mx_linear(x.contiguous(), m) for x in xs[:4]] + [dg.grouped_matmul(r, g, off)]
+                + [dg.q4_linear(x, w) for x in xs])
+    want = one(), two()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s, f in zip(streams, (one, two)):
+            with torch.cuda.stream(s):
+                got.append(f())
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for a, b in zip(outs, want[i % 2]):
+            assert torch.equal(a, b)
+    check_device(dg)
+
+
 def test_arrays_past_32_bit_offsets(dg):
     """Codes past 2^32 bytes, more weights than the workspace holds at a time."""
     gen = torch.Generator("cuda").manual_seed(14)
