@@ -33,12 +33,20 @@ inline long long group_units(int rows, int groups, int N, int tile_rows) {
          ((N + kGroupTile - 1ll) / kGroupTile);
 }
 // Pairs that share a unit's K (weights: the rows of a group to expect), where there are few
-// units.  One / two / four, us (rows, groups, N, K): 8 rows of 1 group, 1024 x 8192 21.0 /
-// 13.7 / 9.7, 60 1024 x 4096 12.9 / 10.3 / 8.5, 2 of 2 1024 x 4096 13.1 / 9.8 / 8.1, 1 4096 x
-// 4096 13.5 / 10.6 / 16.7 (clusters of eight CTAs that do not fit all at once), 64 2048 x
-// 2048 8.9 / 8.4; 512 1024 x 8192 41.5 / 26.9; gradients of 8192 rows of 1 group, 256 x
-// 256 43.7 / 27.7 / 18.5, 1024 x 1024 42.2 / 27.6, 4 512 x 512 16.7 / 14.8; but 60 1024 x 1024 5.7 / 6.2, 2 of 2 4096 x 1024 7.6 / 8.0 and 1024 x 1024
-// 6.9 / 6.5.
+// units.  One / two / four, us:
+//   products   8 rows of 1 group, N x K of 1024 x 8192      21.0 / 13.7 / 9.7
+//              60 rows of 1, 1024 x 4096                    12.9 / 10.3 / 8.5
+//              2 rows of 2, 1024 x 4096                     13.1 / 9.8 / 8.1
+//              1 row of 1, 4096 x 4096                      13.5 / 10.6 / 16.7 (clusters of
+//                                        eight CTAs, which do not all fit at once)
+//              64 rows of 1, 2048 x 2048                    8.9 / 8.4
+//              512 rows of 1, 1024 x 8192                   41.5 / 26.9
+//   gradients  8192 rows of 1, 256 x 256                    43.7 / 27.7 / 18.5
+//              8192 rows of 1, 1024 x 1024                  42.2 / 27.6
+//              8192 rows of 4, 512 x 512                    16.7 / 14.8
+//   but        60 rows of 1, 1024 x 1024                    5.7 / 6.2
+//              2 rows of 2, 4096 x 1024                     7.6 / 8.0
+//              2 rows of 2, 1024 x 1024                     6.9 / 6.5
 constexpr int kGroupMaxParts = 4;
 inline int group_log_parts(long long units, long long K, int max_pairs) {
   if (K <= 8 * kGroupBK || 2 * units > max_pairs) return 0;
@@ -53,8 +61,8 @@ struct GroupParams {
   // columns x X's), the sums run over the group's rows (K == 0: without terms).
   int M, N, K;
   int tile_rows;            // most rows of a unit: 256, or 64 (products)
-  int log_parts = 0;        // pairs that share a unit's K: 1, or 2 or 4 (no more units than
-                            // clusters)
+  int log_parts = 0;        // log2 of the pairs that share a unit's K: 1, or 2 or 4 where there
+                            // are no more units than clusters
   int per_group;            // weights: tiles of a C[g]
   const int* offsets;       // null (groups 1): all rows are one group's
   int zmul;                 // 0: one B for all groups

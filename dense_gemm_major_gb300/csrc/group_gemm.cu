@@ -15,7 +15,8 @@
 // (even CTA), warp 2 clears the rows past a group's end (weights' gradient),
 // warps 4-11 drain the accumulators and store.
 //
-// Few units would leave most SMs idle: up to four pairs of a cluster then share a unit's K and add their sums through distributed shared memory, in their order.
+// Few units would leave most SMs idle: up to four pairs of a cluster then share a unit's K
+// and add their sums through distributed shared memory, in their order.
 //
 // Measured (8 experts of 4096 x 4096, 8192 rows, in a graph): forward 161 us (1.70
 // PFLOP/s); weights' gradient in FP32 206, in BF16 171.  What bounds them is what moves

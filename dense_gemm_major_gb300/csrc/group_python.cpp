@@ -1,6 +1,6 @@
 // The torch wrappers of the grouped products and of those with 4-bit weights as a
-// CPython extension around the C ABI (see py_call.h).  dense_gemm_major_gb300/__init__.py documents the
-// functions and gives their defaults.
+// CPython extension around the C ABI (see py_call.h).  dense_gemm_major_gb300/__init__.py
+// documents the functions and gives their defaults.
 #include "py_call.h"
 
 #include "dense_gemm_group.h"

@@ -4,9 +4,10 @@
 // A group's rows are cut into equal tiles of at most 256 (few rows: 64), a multiple of 32
 // (1342 rows: six of 224 rather than five of 256 and one of 62), so that the units of a
 // round end together: 8192 rows of 8 experts, 4096 x 4096, 167 -> 161 us.  (Groups taken in
-// the order of their units' cost changed nothing.  Ranges of units cut along K, one for
-// each pair, whose pieces meet through a workspace, were slower in every case: storing
-// and adding the pieces took 8 to 10 us at the end, the last round that is not full 4 to 8.)
+// the order of their units' cost changed nothing.  Where there are more units than pairs,
+// ranges of units cut along K, one for each pair, whose pieces meet through a workspace, were
+// slower in every case: storing and adding the pieces took 8 to 10 us at the end, the last
+// round that is not full 4 to 8.)
 #pragma once
 
 #include "group.h"

@@ -301,8 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           weights8<T>(x.z, zz, sr, a + 16 * i + 8);
           weights8<T>(x.w, zz, sr, a + 16 * i + 12);
         }
-        tmem_st32(to + s * kACols + h * 32, a);
-      }
         // Past K, where X is zeros, the codes may stand for infinities.
         const int left = p.K - kt * BK - h * 64;
         if (left < 64) {
@@ -310,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j)
             if (2 * j + 1 >= left) a[j] = 2 * j < left ? a[j] & 0xFFFFu : 0u;
         }
+        tmem_st32(to + s * kACols + h * 32, a);
+      }
       // (The proxy fence waits for the loads, before TMA refills the slot.)
       fence_proxy_async_smem();
       tmem_st_wait();

@@ -67,9 +67,10 @@ gemm_status_t gemm_grouped(int dtype, gemm_op_t op_b, int dtype_c, int rows, int
 
 /*
  * C[g] := alpha * A[rows of g]^T . X[rows of g] + beta * C[g] for every group g: A
- * is rows x M, X rows x N, C[g] (M x N, ldc >= N) at C + g * stride_c.  The
- * gradient of a layer's weights (out x in): A = dY, X the layer's input.  An empty
- * group's C[g] becomes beta * C[g]; beta == 0: C is not read.
+ * is rows x M, X rows x N, C[g] (M x N, ldc >= N) at C + g * stride_c, where none
+ * reaches into the next (stride_c >= (M - 1) * ldc + N).  The gradient of a layer's
+ * weights (out x in): A = dY, X the layer's input.  An empty group's C[g] becomes
+ * beta * C[g]; beta == 0: C is not read.
  */
 gemm_status_t gemm_grouped_grad(int dtype, int dtype_c, int rows, int M, int N, int groups,
                                 float alpha, const void *A, int lda, const void *X, int ldx,

@@ -1,5 +1,7 @@
 """GPU tests of the products grouped by expert against plain 64-bit products of
 each group, within a bound derived from FP32 accumulation and one rounding."""
+import threading
+
 import pytest
 import torch
 
@@ -452,6 +454,40 @@ def test_stream_argument_and_the_allocator(dg):
         assert [float(t) for t in sums] == [float(n) for n in sizes]
         for a, b in zip(copies, want):
             assert torch.equal(a, b)
+    check_device(dg)
+
+
+@pytest.mark.parametrize("shared", [False, True], ids=["own streams", "one stream"])
+def test_threads_at_once(dg, shared):
+    """Calls from several threads whose operands take copies in a workspace, each on its
+    own stream and all on one: every thread has its own sizes and results."""
+    gen = torch.Generator("cuda").manual_seed(18)
+    cases = []
+    for i in range(4):
+        K, N, off = 501 + 66 * i, 333 - 50 * i, _offsets([40 + i, 0, 300, 7 * i])
+        rows = 340 + 8 * i
+        x, dy, w = (torch.randn(shape, generator=gen, device="cuda").half()
+                    for shape in ((rows, K), (rows, N), (4, N, K)))
+        cases.append((x, dy, w, off, _step(dg, x, dy, w, off)))
+    one = torch.cuda.Stream()
+    streams = [one if shared else torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(case, stream):
+        x, dy, w, off, want = case
+        with torch.cuda.stream(stream):
+            for _ in range(25):
+                got = _step(dg, x, dy, w, off)
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    wrong.append(x.shape)
+    threads = [threading.Thread(target=run, args=a) for a in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
     check_device(dg)
 
 
