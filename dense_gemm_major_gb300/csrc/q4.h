@@ -22,6 +22,7 @@ struct Q4FewParams {
   int tile_rows;            // rows of Y per CTA
   int slots;                // upper bound of tiles of rows
   int split;                // CTAs (a cluster) that share a tile's K
+  int max_ctas;             // few rows: as many as run at once
   const void* scales;
   const unsigned char* zeros;
   void* Y;

@@ -74,6 +74,7 @@ bool run_codes(const Q4Call& c, int expect, cudaStream_t stream, gemm_status_t* 
   const long long tiles = (long long)ceil_div(c.N, tile_n) * p.slots;
   const int nk = ceil_div(c.K, few ? dgemm::kQ4BK : 2 * dgemm::kQ4RowsBK);
   const int room = 2 * c.pairs * (few ? 2 : 1);
+  p.max_ctas = room;
   p.split = 1;
   while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= room) p.split *= 2;
   if (!few && (c.K - 1) / p.split >= segment(c.dtype) * dgemm::kGroupBK * (c.dtype == 2 ? 8 : 1))

@@ -30,18 +30,29 @@ constexpr uint32_t kCodeBox = 128 * kQ4TileN;              // 256 codes of each 
 constexpr int kCodeBoxes = kQ4BK / 256, kXBoxes = kQ4BK / 64;
 static_assert(kWarpsN * 32 == kQ4TileN, "32 rows of W per warp");
 
-// kTiles: 8-row tiles of X.
-template <int kTiles>
+// The experts' tiles of 8 rows.
+struct Tables {
+  int start[kGroupMaxGroups + 1];    // first rows of the experts, in order
+  short slot0[kGroupMaxGroups];      // their first tiles
+  int slots;
+};
+
+// kTiles: 8-row tiles of X.  kExperts: a CTA goes from unit to unit, so that the next one's
+// first loads are under way at the end of each; else it has only one.
+template <int kTiles, bool kExperts>
 struct Layout {
+  static_assert(kTiles == 1 || !kExperts, "tiles of 8 rows of an expert");
   static constexpr uint32_t kXBox = kTiles * 8 * 128;      // 64 values of each row
   static constexpr uint32_t kStage = kCodeBoxes * kCodeBox + kXBoxes * kXBox;
-  // Two CTAs per SM, with as many stages as there is room for.
+  static constexpr uint32_t kSums = kWarpsK * kQ4TileN * kTiles * 8 * 4;
+  static constexpr uint32_t kTable = (sizeof(Tables) + 15) / 16 * 16;
+  // Two CTAs per SM, with as many stages as there is room for.  (A single unit's sums take
+  // the ring's place.)
   static constexpr int kCtas = 2;
-  static constexpr int S = (232448 / kCtas - 2560) / kStage;
-  static constexpr uint32_t kSmem = S * kStage + 256 + 1024;
-  // The sums take the ring's place.
-  static_assert(kWarpsK * kQ4TileN * kTiles * 8 * 4 <= S * kStage, "shared memory");
-  static_assert(S >= 2 && kSmem <= 232448, "shared memory");
+  static constexpr uint32_t kRest = (kExperts ? kSums + kTable : 0) + 256 + 1024;
+  static constexpr int S = (233472 / kCtas - 1024 - kRest) / kStage;
+  static constexpr uint32_t kSmem = S * kStage + kRest;
+  static_assert(kSums <= S * kStage && S >= 2 && kSmem <= 232448, "shared memory");
 };
 
 template <int S>
@@ -104,23 +115,80 @@ __device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, ui
   }
 }
 
+// The tables, by one warp.
+__device__ __forceinline__ void q4_tables(const Q4FewParams& p, Tables& t) {
+  const int lane = threadIdx.x & 31, experts = p.experts;
+  const GroupEnds ends{p.offsets, p.rows};
+  int last = ends.first(), slots = 0;
+  bool bad = ends.first_is_bad();
+  for (int base = 0; base < experts; base += 32) {
+    const int e = base + lane;
+    int before;
+    const int end = ends.next(e, experts, &last, &before, &bad);
+    const int mine = (end - before + p.tile_rows - 1) / p.tile_rows;
+    int n = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
+    }
+    if (e < experts) {
+      t.start[e] = before;
+      t.slot0[e] = (short)(slots + n - mine);
+    }
+    slots += __shfl_sync(0xffffffffu, n, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
+    raise_fault(p.fault, kFaultGroupOffsets);
+  if (lane == 0) {
+    t.start[experts] = last;
+    t.slots = slots;
+  }
+}
+
+// Unit u: 64 columns for a tile of rows (without experts there is one tile), a tile's units one
+// behind the other.
+struct Unit {
+  int expert, lo, hi;     // its rows [lo, hi)
+  int n0;
+  bool real;              // there is such a unit
+};
+template <bool kExperts>
+__device__ __forceinline__ Unit unit_of(unsigned u, const Q4FewParams& p, const Tables& t) {
+  Unit w;
+  if constexpr (kExperts) {
+    const unsigned tiles_n = ((unsigned)p.N + kQ4TileN - 1) / kQ4TileN;
+    const int slot = (int)(u / tiles_n);
+    w.real = slot < t.slots;
+    w.expert = group_find(t.slot0, p.experts, (short)min(slot, t.slots));
+    w.lo = t.start[w.expert] + (slot - t.slot0[w.expert]) * p.tile_rows;
+    w.hi = min(w.lo + p.tile_rows, t.start[w.expert + 1]);
+    w.n0 = (int)(u - slot * tiles_n) * kQ4TileN;
+  } else {
+    w.real = true;
+    w.expert = 0, w.lo = 0, w.hi = p.rows;
+    w.n0 = (int)u * kQ4TileN;
+  }
+  return w;
+}
+
 // kRun: steps of 32 terms that have one scale (1, 2, or 4: a warp's slice of a stage, where
 // groups are a multiple of 128).
-template <typename T, int kTiles, int kRun>
-__global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
+template <typename T, int kTiles, int kRun, bool kExperts>
+__global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
     q4_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                   const Q4FewParams p) {
-  using L = Layout<kTiles>;
+  using L = Layout<kTiles, kExperts>;
   constexpr int S = L::S;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
-  float* const sums = reinterpret_cast<float*>(base);
-  auto* bars = reinterpret_cast<Barriers<S>*>(base + S * L::kStage);
+  float* const sums = reinterpret_cast<float*>(base + (kExperts ? S * L::kStage : 0));
+  Tables& tables = *reinterpret_cast<Tables*>(base + S * L::kStage + L::kSums);
+  auto* bars = reinterpret_cast<Barriers<S>*>(base + L::kSmem - 256 - 1024);
   static_assert(sizeof(Barriers<S>) <= 256, "barrier block must fit its reserved space");
-  __shared__ Q4Rows s_rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
-  const int n0 = (int)(blockIdx.x / (unsigned)p.split) * kQ4TileN;
+  const unsigned first = blockIdx.x / (unsigned)p.split, step = gridDim.x / (unsigned)p.split;
   const int nk = (p.K + kQ4BK - 1) / kQ4BK;
   const int kb = (int)((long long)rank * nk / p.split);
   const int ke = (int)((long long)(rank + 1) * nk / p.split);
@@ -137,34 +205,41 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
   }
   wait_prior_grids();
   allow_dependent_grids();
-  if (warp == 0) {
-    const Q4Rows r = q4_rows_of_slot((int)blockIdx.y, p);
-    if (lane == 0) s_rows = r;
-  }
+  if (kExperts && warp == 0) q4_tables(p, tables);
   __syncthreads();
-  const Q4Rows rows = s_rows;
-  if (rows.expert < 0) return;   // (the same in all of a cluster)
+  auto unit_at = [&](unsigned u) { return unit_of<kExperts>(u, p, tables); };
+  if (!unit_at(first).real) return;   // (the same in all of a cluster)
+  const bool loop = kExperts && p.split == 1;
 
+  constexpr int kPlane = kQ4TileN * kTiles * 8;
+  T* const Y = static_cast<T*>(p.Y);
   uint32_t issued = 0;
   if (warp == kWarps) {
     if (elect_one()) {
       // ---------------------------------------------- loads
       RingPos<S> pos;
-      for (int kt = kb; kt < ke; ++kt, pos.next()) {
-        if (!role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
-                       &bars->abort, kFaultTcProducerWait, true))
-          break;
-        const uint32_t st = smem_u32(base + pos.slot * L::kStage);
-        const uint32_t full = smem_u32(&bars->full[pos.slot]);
-        mbar_arrive_expect_tx(full, L::kStage);
+      bool ok = true;
+      for (unsigned u = first; ok; u += step) {
+        const Unit unit = unit_at(u);
+        if (!unit.real) break;
+        for (int kt = kb; kt < ke; ++kt, pos.next()) {
+          ok = role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                         &bars->abort, kFaultTcProducerWait, true);
+          if (!ok) break;
+          const uint32_t st = smem_u32(base + pos.slot * L::kStage);
+          const uint32_t full = smem_u32(&bars->full[pos.slot]);
+          mbar_arrive_expect_tx(full, L::kStage);
 #pragma unroll
-        for (int j = 0; j < kCodeBoxes; ++j)
-          tma_load_3d(st + j * kCodeBox, &tmQ, full, (kt * kQ4BK + j * 256) / 2, n0, rows.expert);
+          for (int j = 0; j < kCodeBoxes; ++j)
+            tma_load_3d(st + j * kCodeBox, &tmQ, full, (kt * kQ4BK + j * 256) / 2, unit.n0,
+                        unit.expert);
 #pragma unroll
-        for (int j = 0; j < kXBoxes; ++j)
-          tma_load_2d(st + kCodeBoxes * kCodeBox + j * L::kXBox, &tmX, full, kt * kQ4BK + j * 64,
-                      rows.lo);
-        ++issued;
+          for (int j = 0; j < kXBoxes; ++j)
+            tma_load_2d(st + kCodeBoxes * kCodeBox + j * L::kXBox, &tmX, full, kt * kQ4BK + j * 64,
+                        unit.lo);
+          ++issued;
+        }
+        if (!loop) break;
       }
     }
     __syncwarp();
@@ -173,27 +248,29 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
     const int wn = warp / kWarpsK, wk = warp % kWarpsK;
     const int g = lane >> 2, t = lane & 3;
     const int groups = (p.K + p.group - 1) / p.group;
+    constexpr int kSteps = kSliceK / 32, kRuns = kSteps / kRun;
     // This lane's row of W, whose scales and zeros it reads for the warp: a group's
     // are stored together (with a row's stored together each lane read a line of its
     // own: 13.3 us at 8192 x 8192 with groups of 128, 28.8 with 32).
-    const int row = n0 + wn * 32 + lane;
-    const long long first = (long long)rows.expert * groups * p.N + row;
-    const uint16_t* const scales = static_cast<const uint16_t*>(p.scales) + first;
-    const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + first : nullptr;
-    const bool real = row < p.N;
-    constexpr int kSteps = kSliceK / 32, kRuns = kSteps / kRun;
-    float acc[2][kTiles][4];
-#pragma unroll
-    for (int i = 0; i < 2 * kTiles * 4; ++i) (&acc[0][0][0])[i] = 0.f;
-
+    const uint16_t* scales;
+    const unsigned char* zeros;
+    bool real;
+    auto row_of = [&](const Unit& w) {
+      const int row = w.n0 + wn * 32 + lane;
+      const long long at = (long long)w.expert * groups * p.N + row;
+      scales = static_cast<const uint16_t*>(p.scales) + at;
+      zeros = p.zeros != nullptr ? p.zeros + at : nullptr;
+      real = row < p.N;
+    };
     // The scales and zeros of a stage's slice, read a stage ahead and left as they
     // come: a conversion would wait for them at once.  `at`, `pos`: group of a
     // slice's first step, and its place in it.
     uint16_t sc[kRuns];
     unsigned char zr[kRuns];
     const int far_at = kQ4BK / p.group, far_pos = kQ4BK % p.group;
-    int at = (kb * kQ4BK + wk * kSliceK) / p.group;
-    int pos = (kb * kQ4BK + wk * kSliceK) % p.group;
+    const int first_at = (kb * kQ4BK + wk * kSliceK) / p.group;
+    const int first_pos = (kb * kQ4BK + wk * kSliceK) % p.group;
+    int at = first_at, pos = first_pos;
     auto read_scales = [&](int kt, int at, int pos) {
 #pragma unroll
       for (int i = 0; i < kRuns; ++i) {
@@ -205,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
         if ((pos += kRun * 32) == p.group) pos = 0, ++at;
       }
     };
+    row_of(unit_at(first));
     read_scales(kb, at, pos);
     // Chunks of 16 bytes in 128-byte rows are swizzled by the row.  (An 8-row tile of
     // X has its rows in the order 0, 4, 1, 5, 2, 6, 3, 7: eight lanes with two rows'
@@ -220,84 +298,114 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
       x_at[i] = kCodeBoxes * kCodeBox + wk * 2 * L::kXBox + xr * 128 + (((i * 4 + t) ^ xr) << 4);
     RingPos<S> ring;
     bool ok = true;
-    for (int kt = kb; kt < ke; ++kt, ring.next()) {
-      float s[kRuns];
-      uint32_t z[kRuns];
+    bool more = true;
+    for (unsigned u = first; more; u += step) {
+      float acc[2][kTiles][4];
 #pragma unroll
-      for (int i = 0; i < kRuns; ++i) {
-        s[i] = elem_to_f32<T>(__builtin_bit_cast(T, sc[i]));
-        z[i] = zr[i] & 15u;
-      }
-      at += far_at;
-      if ((pos += far_pos) >= p.group) pos -= p.group, ++at;
-      read_scales(kt + 1, at, pos);
-      ok = role_wait_lanes(smem_u32(&bars->full[ring.slot]), ring.parity, p.fault, p.timeout_ns,
-                           &bars->abort, kFaultTcMmaWait);
-      if (!ok) break;
-      const uint32_t st = smem_u32(base) + ring.slot * L::kStage;
-      // (Past K, X is zeros and the codes stand for finite values.)
-      uint32_t w[kSteps][4];
+      for (int i = 0; i < 2 * kTiles * 4; ++i) (&acc[0][0][0])[i] = 0.f;
+      more = false;
+      for (int kt = kb; kt < ke; ++kt, ring.next()) {
+        float s[kRuns];
+        uint32_t z[kRuns];
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < kRuns; ++i) {
+          s[i] = elem_to_f32<T>(__builtin_bit_cast(T, sc[i]));
+          z[i] = zr[i] & 15u;
+        }
+        at += far_at;
+        if ((pos += far_pos) >= p.group) pos -= p.group, ++at;
+        int k_far = kt + 1;
+        if (loop && k_far == ke) {
+          const Unit next = unit_at(u + step);
+          if (next.real) {
+            row_of(next);
+            more = true, k_far = kb, at = first_at, pos = first_pos;
+          }
+        }
+        read_scales(k_far, at, pos);
+        ok = role_wait_lanes(smem_u32(&bars->full[ring.slot]), ring.parity, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcMmaWait);
+        if (!ok) break;
+        const uint32_t st = smem_u32(base) + ring.slot * L::kStage;
+        // (Past K, X is zeros and the codes stand for finite values.)
+        uint32_t w[kSteps][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          w[i][r] = ld_shared_u32(st + q_at[i] + r * 8 * 128);
-      float part[2][kTiles][4];
-      Zero<T> zero[4] = {Zero<T>(0), Zero<T>(0), Zero<T>(0), Zero<T>(0)};
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        if (i % kRun == 0) {
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            zero[r] = Zero<T>(__shfl_sync(0xffffffffu, z[i / kRun], r * 8 + g));
+            w[i][r] = ld_shared_u32(st + q_at[i] + r * 8 * 128);
+        float part[2][kTiles][4];
+        Zero<T> zero[4] = {Zero<T>(0), Zero<T>(0), Zero<T>(0), Zero<T>(0)};
 #pragma unroll
-          for (int e = 0; e < 2 * kTiles * 4; ++e) (&part[0][0][0])[e] = 0.f;
-        }
-        uint32_t v[4][4];
+        for (int i = 0; i < kSteps; ++i) {
+          if (i % kRun == 0) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) codes_less_zero<T>(w[i][r], zero[r], v[r]);
+            for (int r = 0; r < 4; ++r)
+              zero[r] = Zero<T>(__shfl_sync(0xffffffffu, z[i / kRun], r * 8 + g));
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          const uint4 x = ld_shared_v4(st + x_at[i & 1] + (i >> 1) * L::kXBox + m * 1024);
-          const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
-          const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
+            for (int e = 0; e < 2 * kTiles * 4; ++e) (&part[0][0][0])[e] = 0.f;
+          }
+          uint32_t v[4][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0[4] = {v[2 * h][0], v[2 * h + 1][0], v[2 * h][1], v[2 * h + 1][1]};
-            const uint32_t a1[4] = {v[2 * h][2], v[2 * h + 1][2], v[2 * h][3], v[2 * h + 1][3]};
-            mma_16816<T>(part[h][m], a0, b0, b1);
-            mma_16816<T>(part[h][m], a1, b2, b3);
+          for (int r = 0; r < 4; ++r) codes_less_zero<T>(w[i][r], zero[r], v[r]);
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) {
+            const uint4 x = ld_shared_v4(st + x_at[i & 1] + (i >> 1) * L::kXBox + m * 1024);
+            const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
+            const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0[4] = {v[2 * h][0], v[2 * h + 1][0], v[2 * h][1], v[2 * h + 1][1]};
+              const uint32_t a1[4] = {v[2 * h][2], v[2 * h + 1][2], v[2 * h][3], v[2 * h + 1][3]};
+              mma_16816<T>(part[h][m], a0, b0, b1);
+              mma_16816<T>(part[h][m], a1, b2, b3);
+            }
+          }
+          if (i % kRun == kRun - 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float lo = __shfl_sync(0xffffffffu, s[i / kRun], h * 16 + g);
+              const float hi = __shfl_sync(0xffffffffu, s[i / kRun], h * 16 + 8 + g);
+#pragma unroll
+              for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  acc[h][m][e] = fmaf(e < 2 ? lo : hi, part[h][m][e], acc[h][m][e]);
+            }
           }
         }
-        if (i % kRun == kRun - 1) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float lo = __shfl_sync(0xffffffffu, s[i / kRun], h * 16 + g);
-            const float hi = __shfl_sync(0xffffffffu, s[i / kRun], h * 16 + 8 + g);
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[h][m][e] = fmaf(e < 2 ? lo : hi, part[h][m][e], acc[h][m][e]);
-          }
-        }
+        // The proxy fence waits for the loads above: without it TMA has been seen to
+        // refill the stage before the last of them had read it.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->empty[ring.slot]));
       }
-      // The proxy fence waits for the loads above: without it TMA has been seen to
-      // refill the stage before the last of them had read it.
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->empty[ring.slot]));
+      // sums[wk][row of X][row of W]: where the stages were, or once the last unit's have
+      // been read.
+      if (!kExperts || u != first) asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      float* const to = sums + wk * kPlane + wn * 32;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            to[(m * 8 + t + 4 * (e & 1)) * kQ4TileN + h * 16 + (e >> 1) * 8 + g] = acc[h][m][e];
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      // The ranges of K in order (a cluster's: into the first).
+      const Unit unit = unit_at(u);
+      for (int i = threadIdx.x; i < (unit.hi - unit.lo) * kQ4TileN; i += 32 * kWarps) {
+        float v = sums[i];
+#pragma unroll
+        for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
+        const int n = unit.n0 + i % kQ4TileN;
+        if (p.split > 1)
+          sums[i] = v;
+        else if (n < p.N)
+          Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
+      }
+      if (!ok) break;
     }
-    // sums[wk][row of X][row of W], where the stages were.
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-    float* const to = sums + wk * (kQ4TileN * kTiles * 8) + wn * 32;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          to[(m * 8 + t + 4 * (e & 1)) * kQ4TileN + h * 16 + (e >> 1) * 8 + g] = acc[h][m][e];
   }
   __syncthreads();
   if (warp == kWarps && elect_one() && bars->abort) {
@@ -309,66 +417,51 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles>::kCtas)
         break;
       }
   }
-  // The ranges of K in order, into the first; then this CTA's part of the tile over
-  // the cluster.
-  const int values = (rows.hi - rows.lo) * kQ4TileN;
-  constexpr int kPlane = kQ4TileN * kTiles * 8;
-  T* const Y = static_cast<T*>(p.Y);
-  if (p.split == 1) {
-    for (int i = threadIdx.x; i < values; i += kThreads) {
-      float v = sums[i];
-#pragma unroll
-      for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
-      const int n = n0 + i % kQ4TileN;
-      if (n < p.N)
-        Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
-    }
-  } else {
-    for (int i = threadIdx.x; i < values; i += kThreads) {
-      float v = sums[i];
-#pragma unroll
-      for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
-      sums[i] = v;
-    }
+  if (p.split > 1) {
+    // This CTA's part of the tile over the cluster.
     cluster_sync_all();
+    const Unit unit = unit_at(first);
+    const int values = (unit.hi - unit.lo) * kQ4TileN;
     for (int i = rank * kThreads + threadIdx.x; i < values; i += p.split * kThreads) {
       const uint32_t at = smem_u32(sums + i);
       float v = 0.f;
       for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
-      const int n = n0 + i % kQ4TileN;
+      const int n = unit.n0 + i % kQ4TileN;
       if (n < p.N)
-        Y[(long long)(rows.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
+        Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
     }
     cluster_sync_all();   // nobody leaves while its sums may still be read
   }
 }
 
-template <typename T, int kTiles, int kRun>
+template <typename T, int kTiles, int kRun, bool kExperts>
 cudaError_t launch_tiles(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
                          cudaStream_t stream) {
-  auto kernel = q4_few_kernel<T, kTiles, kRun>;
+  using L = Layout<kTiles, kExperts>;
+  auto kernel = q4_few_kernel<T, kTiles, kRun, kExperts>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = mx_allow_smem(kernel, Layout<kTiles>::kSmem, &done);
+  cudaError_t e = mx_allow_smem(kernel, L::kSmem, &done);
   if (e != cudaSuccess) return e;
-  const long long tiles = ((long long)p.N + kQ4TileN - 1) / kQ4TileN;
-  return launch_gemm_kernel_clusters((unsigned)p.split, kernel,
-                                     dim3((unsigned)(tiles * p.split), (unsigned)p.slots),
-                                     dim3(kThreads), Layout<kTiles>::kSmem, stream, *tmQ, *tmX, p);
+  const long long units = ((long long)p.N + kQ4TileN - 1) / kQ4TileN * p.slots;
+  const long long ctas = kExperts && units > p.max_ctas ? p.max_ctas : units;
+  return launch_gemm_kernel_clusters((unsigned)p.split, kernel, dim3((unsigned)(ctas * p.split)),
+                                     dim3(kThreads), L::kSmem, stream, *tmQ, *tmX, p);
 }
 
-template <typename T, int kTiles>
+template <typename T, int kTiles, bool kExperts>
 cudaError_t launch_run(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                        cudaStream_t stream) {
-  if (p.group % 128 == 0) return launch_tiles<T, kTiles, 4>(p, q, x, stream);
-  return p.group % 64 == 0 ? launch_tiles<T, kTiles, 2>(p, q, x, stream)
-                           : launch_tiles<T, kTiles, 1>(p, q, x, stream);
+  if (p.group % 128 == 0) return launch_tiles<T, kTiles, 4, kExperts>(p, q, x, stream);
+  return p.group % 64 == 0 ? launch_tiles<T, kTiles, 2, kExperts>(p, q, x, stream)
+                           : launch_tiles<T, kTiles, 1, kExperts>(p, q, x, stream);
 }
 
 template <typename T>
 cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
                          cudaStream_t stream) {
-  return p.tile_rows == 8 ? launch_run<T, 1>(p, q, x, stream)
-                          : launch_run<T, 2>(p, q, x, stream);
+  if (p.experts != 0) return launch_run<T, 1, true>(p, q, x, stream);
+  return p.tile_rows == 8 ? launch_run<T, 1, false>(p, q, x, stream)
+                          : launch_run<T, 2, false>(p, q, x, stream);
 }
 
 }  // namespace

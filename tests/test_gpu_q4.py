@@ -145,6 +145,31 @@ def test_experts(dg, dtype, zeros, case):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group,K", [(32, 1600), (64, 130), (128, 2000)])
+@pytest.mark.parametrize("experts,N", [(64, 1100), (1024, 200)])
+def test_more_tiles_of_experts_than_run_at_once(dg, dtype, group, K, experts, N):
+    """Experts of 0 to 3 rows and one of 70, in several rounds."""
+    gen = torch.Generator("cuda").manual_seed(experts + K)
+    sizes = torch.randint(0, 4, (experts,), generator=gen, device="cuda").tolist()
+    sizes[5] = 70
+    x = _x(gen, sum(sizes), K, dtype)
+    w, values = _weights(dg, gen, (experts, N), K, dtype, group, True)
+    y = dg.q4_linear(x, w, offsets=_offsets(sizes))
+    for _ in range(3):
+        assert torch.equal(dg.q4_linear(x, w, offsets=_offsets(sizes)), y)
+    check_device(dg)
+    ends = torch.tensor([0] + sizes).cumsum(0).tolist()
+    for g in [0, 1, 2, 3, 4, 5, 6, experts // 2, experts - 3, experts - 2, experts - 1]:
+        lo, hi = ends[g], ends[g + 1]
+        if hi > lo:
+            _check(y[lo:hi], x[lo:hi], values[g], K, dtype, True)
+    every = torch.arange(experts, device="cuda").repeat_interleave(
+        torch.tensor(sizes, device="cuda"))
+    want = torch.stack([values[g] @ r for g, r in zip(every.tolist(), x.double())])
+    assert float((y.double() - want).norm() / want.norm()) <= 2 * ref.UNIT[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("rows", [1, 7, 12, 40, 64, 200])
 def test_exact_on_integers(dg, dtype, rows):
     """Integer activations and power-of-two scales: FP32 holds every sum exactly, so
