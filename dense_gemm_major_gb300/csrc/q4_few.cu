@@ -30,13 +30,6 @@ constexpr uint32_t kCodeBox = 128 * kQ4TileN;              // 256 codes of each 
 constexpr int kCodeBoxes = kQ4BK / 256, kXBoxes = kQ4BK / 64;
 static_assert(kWarpsN * 32 == kQ4TileN, "32 rows of W per warp");
 
-// The experts' tiles of 8 rows.
-struct Tables {
-  int start[kGroupMaxGroups + 1];    // first rows of the experts, in order
-  short slot0[kGroupMaxGroups];      // their first tiles
-  int slots;
-};
-
 // kTiles: 8-row tiles of X.  kExperts: a CTA goes from unit to unit, so that the next one's
 // first loads are under way at the end of each; else it has only one.
 template <int kTiles, bool kExperts>
@@ -45,7 +38,7 @@ struct Layout {
   static constexpr uint32_t kXBox = kTiles * 8 * 128;      // 64 values of each row
   static constexpr uint32_t kStage = kCodeBoxes * kCodeBox + kXBoxes * kXBox;
   static constexpr uint32_t kSums = kWarpsK * kQ4TileN * kTiles * 8 * 4;
-  static constexpr uint32_t kTable = (sizeof(Tables) + 15) / 16 * 16;
+  static constexpr uint32_t kTable = (sizeof(Q4Tables) + 15) / 16 * 16 + kWarps * 2 * 16;
   // Two CTAs per SM, with as many stages as there is room for.  (A single unit's sums take
   // the ring's place.)
   static constexpr int kCtas = 2;
@@ -96,7 +89,7 @@ struct Zero {
 };
 
 // The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes, less their zero, over
-// kQ4Unit.  FP16: a code in the low mantissa bits of 1024 is that plus the code, and four
+// kQ4Value.  FP16: a code in the low mantissa bits of 1024 is that plus the code, and four
 // bits further up 1024 + 16 q.  BF16 has no room for the latter; but the integer n in the
 // low eight bits of a BF16 number is n 2^-133, whether it is subnormal (n < 128) or not, and
 // the multiplication with 2^127, or 2^123 for a code four bits further up, is exact.
@@ -115,61 +108,16 @@ __device__ __forceinline__ void codes_less_zero(uint32_t w, const Zero<T>& z, ui
   }
 }
 
-// The tables, by one warp.
-__device__ __forceinline__ void q4_tables(const Q4FewParams& p, Tables& t) {
-  const int lane = threadIdx.x & 31, experts = p.experts;
-  const GroupEnds ends{p.offsets, p.rows};
-  int last = ends.first(), slots = 0;
-  bool bad = ends.first_is_bad();
-  for (int base = 0; base < experts; base += 32) {
-    const int e = base + lane;
-    int before;
-    const int end = ends.next(e, experts, &last, &before, &bad);
-    const int mine = (end - before + p.tile_rows - 1) / p.tile_rows;
-    int n = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, n, d);
-      if (lane >= d) n += o;
-    }
-    if (e < experts) {
-      t.start[e] = before;
-      t.slot0[e] = (short)(slots + n - mine);
-    }
-    slots += __shfl_sync(0xffffffffu, n, 31);
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
-    raise_fault(p.fault, kFaultGroupOffsets);
-  if (lane == 0) {
-    t.start[experts] = last;
-    t.slots = slots;
-  }
-}
-
-// Unit u: 64 columns for a tile of rows (without experts there is one tile), a tile's units one
-// behind the other.
-struct Unit {
-  int expert, lo, hi;     // its rows [lo, hi)
-  int n0;
-  bool real;              // there is such a unit
-};
-template <bool kExperts>
-__device__ __forceinline__ Unit unit_of(unsigned u, const Q4FewParams& p, const Tables& t) {
-  Unit w;
-  if constexpr (kExperts) {
-    const unsigned tiles_n = ((unsigned)p.N + kQ4TileN - 1) / kQ4TileN;
-    const int slot = (int)(u / tiles_n);
-    w.real = slot < t.slots;
-    w.expert = group_find(t.slot0, p.experts, (short)min(slot, t.slots));
-    w.lo = t.start[w.expert] + (slot - t.slot0[w.expert]) * p.tile_rows;
-    w.hi = min(w.lo + p.tile_rows, t.start[w.expert + 1]);
-    w.n0 = (int)(u - slot * tiles_n) * kQ4TileN;
-  } else {
-    w.real = true;
-    w.expert = 0, w.lo = 0, w.hi = p.rows;
-    w.n0 = (int)u * kQ4TileN;
-  }
-  return w;
+// A barrier of the warps that multiply: whether `b` holds in any thread.
+__device__ __forceinline__ bool products_any(bool b) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 1, %2, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"((int)b), "n"(32 * kWarps)
+      : "memory");
+  return any != 0;
 }
 
 // kRun: steps of 32 terms that have one scale (1, 2, or 4: a warp's slice of a stage, where
@@ -183,12 +131,16 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
   float* const sums = reinterpret_cast<float*>(base + (kExperts ? S * L::kStage : 0));
-  Tables& tables = *reinterpret_cast<Tables*>(base + S * L::kStage + L::kSums);
+  // (kExperts:) each warp's unit and the next, the tables.
+  int4* const entered = reinterpret_cast<int4*>(base + S * L::kStage + L::kSums);
+  Q4Tables& tables = *reinterpret_cast<Q4Tables*>(entered + 2 * kWarps);
+  __shared__ Q4Unit s_unit;
   auto* bars = reinterpret_cast<Barriers<S>*>(base + L::kSmem - 256 - 1024);
   static_assert(sizeof(Barriers<S>) <= 256, "barrier block must fit its reserved space");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
   const unsigned first = blockIdx.x / (unsigned)p.split, step = gridDim.x / (unsigned)p.split;
+  const Q4Walk walk0(kExperts ? p.N : 1, kQ4TileN, first, step);     // (kExperts)
   const int nk = (p.K + kQ4BK - 1) / kQ4BK;
   const int kb = (int)((long long)rank * nk / p.split);
   const int ke = (int)((long long)(rank + 1) * nk / p.split);
@@ -205,23 +157,44 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
   }
   wait_prior_grids();
   allow_dependent_grids();
-  if (kExperts && warp == 0) q4_tables(p, tables);
+  Q4Unit unit0{0, 0, p.rows, (int)first * kQ4TileN, true};
+  if constexpr (kExperts) {
+    if (warp == 0) {
+      Q4Unit w = q4_tables(p, tables, walk0.slot);
+      w.n0 = walk0.n * kQ4TileN;
+      if (lane == 0) s_unit = w;
+    }
+  }
   __syncthreads();
-  auto unit_at = [&](unsigned u) { return unit_of<kExperts>(u, p, tables); };
-  if (!unit_at(first).real) return;   // (the same in all of a cluster)
+  if constexpr (kExperts) unit0 = s_unit;
+  if (!unit0.real) return;   // (the same in all of a cluster)
   const bool loop = kExperts && p.split == 1;
 
   constexpr int kPlane = kQ4TileN * kTiles * 8;
   T* const Y = static_cast<T*>(p.Y);
+  // The ranges of K in order: to Y, or into the first where a cluster adds on.  (Experts: by
+  // the warps that multiply.)
+  auto add_ranges = [&](int lo, int hi, int n0) {
+    const int values = (hi - lo) * kQ4TileN;
+    for (int i = threadIdx.x; i < values; i += kExperts ? 32 * kWarps : kThreads) {
+      float v = sums[i];
+#pragma unroll
+      for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
+      const int n = n0 + i % kQ4TileN;
+      if (p.split > 1)
+        sums[i] = v;
+      else if (n < p.N)
+        Y[(long long)(lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Value<T>);
+    }
+  };
   uint32_t issued = 0;
   if (warp == kWarps) {
     if (elect_one()) {
       // ---------------------------------------------- loads
       RingPos<S> pos;
       bool ok = true;
-      for (unsigned u = first; ok; u += step) {
-        const Unit unit = unit_at(u);
-        if (!unit.real) break;
+      Q4Unit unit = unit0;
+      for (Q4Walk walk = walk0; ok && unit.real;) {
         for (int kt = kb; kt < ke; ++kt, pos.next()) {
           ok = role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
                          &bars->abort, kFaultTcProducerWait, true);
@@ -240,6 +213,8 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
           ++issued;
         }
         if (!loop) break;
+        walk.next();
+        unit = q4_unit(p, tables, walk, kQ4TileN);
       }
     }
     __syncwarp();
@@ -255,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
     const uint16_t* scales;
     const unsigned char* zeros;
     bool real;
-    auto row_of = [&](const Unit& w) {
+    auto row_of = [&](const Q4Unit& w) {
       const int row = w.n0 + wn * 32 + lane;
       const long long at = (long long)w.expert * groups * p.N + row;
       scales = static_cast<const uint16_t*>(p.scales) + at;
@@ -282,8 +257,16 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
         if ((pos += kRun * 32) == p.group) pos = 0, ++at;
       }
     };
-    row_of(unit_at(first));
+    row_of(unit0);
     read_scales(kb, at, pos);
+    Q4Walk walk = walk0;
+    int expert = unit0.expert;
+    uint32_t turn = 0;        // (of a unit)
+    auto enter = [&](const Q4Unit& w, uint32_t turn) {
+      if (kExperts && lane == 0)
+        entered[warp * 2 + (turn & 1)] = make_int4(w.lo, w.hi, w.n0, 0);
+    };
+    enter(unit0, 0);
     // Chunks of 16 bytes in 128-byte rows are swizzled by the row.  (An 8-row tile of
     // X has its rows in the order 0, 4, 1, 5, 2, 6, 3, 7: eight lanes with two rows'
     // four chunks then read 128 different bytes.)
@@ -299,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
     RingPos<S> ring;
     bool ok = true;
     bool more = true;
-    for (unsigned u = first; more; u += step) {
+    for (; more; ++turn) {
       float acc[2][kTiles][4];
 #pragma unroll
       for (int i = 0; i < 2 * kTiles * 4; ++i) (&acc[0][0][0])[i] = 0.f;
@@ -316,9 +299,12 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
         if ((pos += far_pos) >= p.group) pos -= p.group, ++at;
         int k_far = kt + 1;
         if (loop && k_far == ke) {
-          const Unit next = unit_at(u + step);
+          walk.next();
+          const Q4Unit next = q4_unit_by_warp(p, tables, walk, kQ4TileN, expert);
           if (next.real) {
             row_of(next);
+            enter(next, turn + 1);
+            expert = next.expert;
             more = true, k_far = kb, at = first_at, pos = first_pos;
           }
         }
@@ -382,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
       }
       // sums[wk][row of X][row of W]: where the stages were, or once the last unit's have
       // been read.
-      if (!kExperts || u != first) asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      if (!kExperts || turn != 0) asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
       float* const to = sums + wk * kPlane + wn * 32;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -391,20 +377,11 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             to[(m * 8 + t + 4 * (e & 1)) * kQ4TileN + h * 16 + (e >> 1) * 8 + g] = acc[h][m][e];
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-      // The ranges of K in order (a cluster's: into the first).
-      const Unit unit = unit_at(u);
-      for (int i = threadIdx.x; i < (unit.hi - unit.lo) * kQ4TileN; i += 32 * kWarps) {
-        float v = sums[i];
-#pragma unroll
-        for (int j = 1; j < kWarpsK; ++j) v += sums[j * kPlane + i];
-        const int n = unit.n0 + i % kQ4TileN;
-        if (p.split > 1)
-          sums[i] = v;
-        else if (n < p.N)
-          Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
-      }
-      if (!ok) break;
+      if constexpr (!kExperts) break;
+      // (All of them go on or none.)
+      if (products_any(!ok)) break;
+      const int4 unit = entered[warp * 2 + (turn & 1)];
+      add_ranges(unit.x, unit.y, unit.z);
     }
   }
   __syncthreads();
@@ -417,10 +394,11 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
         break;
       }
   }
+  if constexpr (!kExperts) add_ranges(unit0.lo, unit0.hi, unit0.n0);
   if (p.split > 1) {
     // This CTA's part of the tile over the cluster.
     cluster_sync_all();
-    const Unit unit = unit_at(first);
+    const Q4Unit unit = unit0;
     const int values = (unit.hi - unit.lo) * kQ4TileN;
     for (int i = rank * kThreads + threadIdx.x; i < values; i += p.split * kThreads) {
       const uint32_t at = smem_u32(sums + i);
@@ -428,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
       for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
       const int n = unit.n0 + i % kQ4TileN;
       if (n < p.N)
-        Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Unit<T>);
+        Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Value<T>);
     }
     cluster_sync_all();   // nobody leaves while its sums may still be read
   }

@@ -35,9 +35,13 @@ constexpr int kConvWarp = 4, kGroups = 4, kGroupWarps = 4;
 // 15.8 us at 8192 x 8192, 16 rows.)
 constexpr uint32_t kRawBytes = BN * BK;                     // 16 KB
 constexpr uint32_t kACols = BK / 2;                         // of tensor memory, a stage of W
+// Units from the one that a warp drains next to the one of its next stage: of two stages or
+// more, so that a turn is two units ahead of the last, and the next one four.
+constexpr uint32_t kEntered = 8;
 
-// MT: rows of X that the MMA computes.
-template <int MT>
+// MT: rows of X that the MMA computes.  kLoop: a CTA goes from unit to unit; else it has a
+// share of K of only one.
+template <int MT, bool kLoop>
 struct Layout {
   static constexpr uint32_t kXBlock = MT * 128;             // 64 k of X
   static constexpr uint32_t kStage = 2 * kXBlock;
@@ -45,16 +49,21 @@ struct Layout {
   // codes: their number is even, so that each is read by the same two groups every time.
   // Stages: the MMAs free them in order, and a group has seen the one freed that it
   // waited for kGroups stages ago, so that there need to be that many.
-  static constexpr int S = MT <= 64 ? 6 : 4, R = 6;
+  static constexpr int S = MT <= 64 ? 6 : 4, R = kLoop && MT > 64 ? 4 : 6;
   static_assert(S >= kGroups && R % 2 == 0, "phases");
+  static constexpr uint32_t kTable =
+      kLoop ? (sizeof(Q4Tables) + 15) / 16 * 16 + kGroups * kGroupWarps * kEntered * 16 : 0;
   // All of an SM's (s_rows is beside it), so that no CTA of another cluster with tensor
   // memory is: two clusters could each hold on one SM what the other waits for on another.
   static constexpr uint32_t kSmem = 232448 - 1024;
-  static_assert(S * kStage + R * kRawBytes + 512 + 1024 <= kSmem, "shared memory");
+  static_assert(S * kStage + R * kRawBytes + kTable + 512 + 1024 <= kSmem, "shared memory");
   static_assert(MT * BN * 4 <= S * kStage + R * kRawBytes, "partial tiles reuse the rings");
-  // Tensor memory: the accumulator, then W's stages.
-  static constexpr uint32_t kACol = MT < 32 ? 32 : MT;
+  // Tensor memory: the accumulator (two, in turn), then W's stages.
+  static constexpr uint32_t kAccCols = MT < 32 ? 32 : MT;
+  static constexpr uint32_t kACol = kLoop ? 2 * kAccCols : kAccCols;
   static_assert(kACol + S * kACols <= 512, "tensor memory");
+  // Warps that drain an accumulator: each group takes every fourth 16 rows of X.
+  static constexpr int kDrainWarps = kGroupWarps * (MT / 16 < kGroups ? MT / 16 : kGroups);
 };
 
 template <int S, int R>
@@ -63,7 +72,8 @@ struct alignas(8) Barriers {
   uint64_t empty[S];
   uint64_t raw_full[R];
   uint64_t raw_empty[R];
-  uint64_t acc_full;
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -82,7 +92,7 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-// Eight codes as four pairs of weights over kQ4Unit, in the order of their columns; z:
+// Eight codes as four pairs of weights over kQ4Value, in the order of their columns; z:
 // the zero, s: the scale, twice (see zero_term()).  FP16: a code in the low mantissa bits of
 // 1024 is that plus the code.  BF16: the integer n in a number's low eight bits is n
 // 2^-133, so that 2^127 and, four bits further up, 2^123 make both codes of a byte q / 64.
@@ -110,25 +120,31 @@ __device__ __forceinline__ uint32_t zero_term(uint32_t zero) {
 }
 
 // kRun: columns that have one scale (32, 64, or a stage's 128).
-template <typename T, int MT, int kRun>
+template <typename T, int MT, int kRun, bool kLoop>
 __global__ void __launch_bounds__(kThreads, 1)
     q4_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                    const Q4FewParams p) {
-  using L = Layout<MT>;
+  using L = Layout<MT, kLoop>;
   constexpr int S = L::S, R = L::R;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const base = align_smem_1024(smem_raw);
   unsigned char* const raw_base = base + S * L::kStage;
   auto* bars = reinterpret_cast<Barriers<S, R>*>(raw_base + R * kRawBytes);
   static_assert(sizeof(Barriers<S, R>) <= 512, "barrier block must fit its reserved space");
-  __shared__ Q4Rows s_rows;
+  // (kLoop:) each converting warp's units since the one it drains next, the tables.
+  int4* const entered = reinterpret_cast<int4*>(raw_base + R * kRawBytes + 512);
+  Q4Tables& tables = *reinterpret_cast<Q4Tables*>(entered + kGroups * kGroupWarps * kEntered);
+  __shared__ Q4Unit s_unit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
-  const int n0 = (int)(blockIdx.x / (unsigned)p.split) * BN;
-  // k-tiles [kb, ke), from an even one on.
+  const int rank = !kLoop && p.split > 1 ? (int)cluster_ctarank() : 0;
+  // This CTA's k-tiles of a unit: from kb on (even), of which there are `stages`.  (In a loop
+  // they are even too, the last one all zeros if need be: every unit begins with a slot.)
   const int nk = (p.K + BK - 1) / BK, nk2 = (nk + 1) / 2;
-  const int kb = 2 * (int)((long long)rank * nk2 / p.split);
-  const int ke = min(2 * (int)((long long)(rank + 1) * nk2 / p.split), nk);
+  const int kb = kLoop ? 0 : 2 * (int)((long long)rank * nk2 / p.split);
+  const int stages =
+      kLoop ? 2 * nk2 : min(2 * (int)((long long)(rank + 1) * nk2 / p.split), nk) - kb;
+  // (kLoop: from unit to unit; else the one that the grid gives.)
+  const Q4Walk walk0(p.N, BN, blockIdx.x / (unsigned)p.split, gridDim.x);
   constexpr uint32_t kAb = __is_same(T, __half) ? 0u : 1u;
 
   if (threadIdx.x == 0) {
@@ -140,7 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->raw_full[r]), 1);
       mbar_init(smem_u32(&bars->raw_empty[r]), 2 * kGroupWarps);
     }
-    mbar_init(smem_u32(&bars->acc_full), 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&bars->acc_full[b]), 1);
+      mbar_init(smem_u32(&bars->acc_empty[b]), L::kDrainWarps);
+    }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -151,15 +170,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_prior_grids();
   allow_dependent_grids();
   if (warp == 2) {
-    const Q4Rows r = q4_rows_of_slot((int)blockIdx.y, p);
-    if (lane == 0) s_rows = r;
+    Q4Unit w;
+    if constexpr (kLoop) {
+      w = q4_tables(p, tables, walk0.slot);
+    } else {
+      const Q4Rows r = q4_rows_of_slot((int)blockIdx.y, p);
+      w = Q4Unit{r.expert, r.lo, r.hi, 0, r.expert >= 0};
+    }
+    w.n0 = walk0.n * BN;
+    if (lane == 0) s_unit = w;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = bars->tmem_base;
-  const Q4Rows rows = s_rows;
-  if (rows.expert < 0) {   // (the same in all of a cluster)
+  const Q4Unit unit0 = s_unit;
+  if (!unit0.real) {   // (the same in all of a cluster)
     if (warp == 1) tmem_dealloc(tmem_base, 512);
     return;
   }
@@ -169,15 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       // ---------------------------------------------- codes
       RingPos<R> pos;
-      for (int kt = kb; kt < ke; kt += 2, pos.next()) {
-        if (!role_wait(smem_u32(&bars->raw_empty[pos.slot]), pos.parity ^ 1u, p.fault,
-                       p.timeout_ns, &bars->abort, kFaultTcProducerWait, true))
-          break;
-        const uint32_t full = smem_u32(&bars->raw_full[pos.slot]);
-        mbar_arrive_expect_tx(full, kRawBytes);
-        tma_load_3d(smem_u32(raw_base + pos.slot * kRawBytes), &tmQ, full, kt * (BK / 2), n0,
-                    rows.expert);
-        ++issued;
+      bool ok = true;
+      Q4Unit unit = unit0;
+      for (Q4Walk walk = walk0; ok && unit.real;) {
+        for (int kt = kb; kt < kb + stages; kt += 2, pos.next()) {
+          ok = role_wait(smem_u32(&bars->raw_empty[pos.slot]), pos.parity ^ 1u, p.fault,
+                         p.timeout_ns, &bars->abort, kFaultTcProducerWait, true);
+          if (!ok) break;
+          const uint32_t full = smem_u32(&bars->raw_full[pos.slot]);
+          mbar_arrive_expect_tx(full, kRawBytes);
+          tma_load_3d(smem_u32(raw_base + pos.slot * kRawBytes), &tmQ, full, kt * (BK / 2),
+                      unit.n0, unit.expert);
+          ++issued;
+        }
+        if (!kLoop) break;
+        walk.next();
+        unit = q4_unit(p, tables, walk, BN);
       }
     }
     __syncwarp();
@@ -185,16 +218,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       // ---------------------------------------------- X
       RingPos<S> pos;
-      for (int kt = kb; kt < ke; ++kt, pos.next()) {
-        if (!role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
-                       &bars->abort, kFaultTcProducerWait, true))
-          break;
-        const uint32_t full = smem_u32(&bars->full[pos.slot]);
-        const uint32_t to = smem_u32(base + pos.slot * L::kStage);
-        mbar_arrive_expect_tx(full, 2 * L::kXBlock);
-        tma_load_2d(to, &tmX, full, kt * BK, rows.lo);
-        tma_load_2d(to + L::kXBlock, &tmX, full, kt * BK + 64, rows.lo);
-        ++issued;
+      bool ok = true;
+      Q4Unit unit = unit0;
+      for (Q4Walk walk = walk0; ok && unit.real;) {
+        for (int kt = kb; kt < kb + stages; ++kt, pos.next()) {
+          ok = role_wait(smem_u32(&bars->empty[pos.slot]), pos.parity ^ 1u, p.fault, p.timeout_ns,
+                         &bars->abort, kFaultTcProducerWait, true);
+          if (!ok) break;
+          const uint32_t full = smem_u32(&bars->full[pos.slot]);
+          const uint32_t to = smem_u32(base + pos.slot * L::kStage);
+          mbar_arrive_expect_tx(full, 2 * L::kXBlock);
+          tma_load_2d(to, &tmX, full, kt * BK, unit.lo);
+          tma_load_2d(to + L::kXBlock, &tmX, full, kt * BK + 64, unit.lo);
+          ++issued;
+        }
+        if (!kLoop) break;
+        walk.next();
+        unit = q4_unit(p, tables, walk, BN);
       }
     }
     __syncwarp();
@@ -205,23 +245,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // try takes over 100 cycles to answer.)
       RingPos<S> pos;
       bool ok = true, ready = false;
-      for (int kt = kb; kt < ke; ++kt) {
-        const uint32_t slot = pos.slot;
-        ok = ready || role_wait(smem_u32(&bars->full[slot]), pos.parity, p.fault, p.timeout_ns,
-                                &bars->abort, kFaultTcMmaWait, true);
-        if (!ok) break;
-        tc_fence_after();
-        pos.next();
-        ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
-        const uint32_t blo = desc_lo(smem_u32(base + slot * L::kStage), 16);
-        const uint32_t a = tmem_base + L::kACol + slot * kACols;
+      uint32_t n = 0;           // units
+      Q4Walk walk = walk0;
+      for (bool real = true; ok && real; ++n) {
+        const uint32_t b = n & 1;
+        if (kLoop) {
+          ok = role_wait(smem_u32(&bars->acc_empty[b]), ((n >> 1) & 1u) ^ 1u, p.fault,
+                         p.timeout_ns, &bars->abort, kFaultTcMmaWait, true);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        for (int i = 0; i < stages; ++i) {
+          const uint32_t slot = pos.slot;
+          ok = ready || role_wait(smem_u32(&bars->full[slot]), pos.parity, p.fault, p.timeout_ns,
+                                  &bars->abort, kFaultTcMmaWait, true);
+          if (!ok) break;
+          tc_fence_after();
+          pos.next();
+          ready = mbar_try_wait(smem_u32(&bars->full[pos.slot]), pos.parity);
+          const uint32_t blo = desc_lo(smem_u32(base + slot * L::kStage), 16);
+          const uint32_t a = tmem_base + L::kACol + slot * kACols;
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k)
-          mma_f16_ta(tmem_base, a + k * 8, blo + (((k >> 2) * L::kXBlock + (k & 3) * 32) >> 4),
-                     instr_desc(kAb, BN, MT, 0, 0), (kt > kb || k > 0) ? 1u : 0u);
-        mma_commit(smem_u32(&bars->empty[slot]));
+          for (int k = 0; k < BK / 16; ++k)
+            mma_f16_ta(tmem_base + b * L::kAccCols, a + k * 8,
+                       blo + (((k >> 2) * L::kXBlock + (k & 3) * 32) >> 4),
+                       instr_desc(kAb, BN, MT, 0, 0), (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit(smem_u32(&bars->empty[slot]));
+        }
+        if (ok) mma_commit(smem_u32(&bars->acc_full[b]));
+        walk.next();
+        real = kLoop && walk.slot < tables.slots;
       }
-      if (ok) mma_commit(smem_u32(&bars->acc_full));
     }
     __syncwarp();
   } else if (warp >= kConvWarp) {
@@ -230,23 +284,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kRuns = BK / kRun;
     const int group = (warp - kConvWarp) / kGroupWarps;
     const int row = (warp & 3) * 32 + lane;
-    const int n = n0 + row;
-    const bool real = n < p.N;
-    const long long first =
-        (long long)rows.expert * ((p.K + p.group - 1) / p.group) * p.N + n;
-    const uint16_t* const scales = static_cast<const uint16_t*>(p.scales) + first;
-    const unsigned char* const zeros = p.zeros != nullptr ? p.zeros + first : nullptr;
     // The scales and zeros of its runs, read a turn ahead and left as they come.
+    const uint16_t* scales;
+    const unsigned char* zeros;
+    bool real;
     uint16_t sc[kRuns];
     unsigned char zr[kRuns];
     const int far_at = kGroups * BK / p.group, far_pos = kGroups * BK % p.group;
-    int at = (kb + group) * BK / p.group;
-    int pos_in = (kb + group) * BK % p.group;
-    auto read_scales = [&](int kt) {
+    int at, pos_in;
+    // Its next stage: kt of the n-th unit (none beyond the last).
+    Q4Walk walk = walk0;
+    uint32_t n = 0;
+    int kt = group, expert = 0;
+    bool more;
+    auto enter = [&](Q4Unit unit) {
+      for (;;) {
+        if constexpr (kLoop) {
+          if (lane == 0 && unit.real)
+            entered[(warp - kConvWarp) * kEntered + n % kEntered] = make_int4(unit.lo, unit.hi, unit.n0, 0);
+        }
+        expert = unit.expert;
+        more = unit.real;
+        if (!more || kt < stages) break;
+        kt -= stages, ++n;
+        if constexpr (kLoop) {
+          walk.next();
+          unit = q4_unit_by_warp(p, tables, walk, BN, expert);
+        } else {
+          unit.real = false;
+        }
+      }
+      if (!more) return;
+      const long long first_of_row =
+          (long long)expert * ((p.K + p.group - 1) / p.group) * p.N + unit.n0 + row;
+      scales = static_cast<const uint16_t*>(p.scales) + first_of_row;
+      zeros = p.zeros != nullptr ? p.zeros + first_of_row : nullptr;
+      real = unit.n0 + row < p.N;
+      at = (kb + kt) * BK / p.group;
+      pos_in = (kb + kt) * BK % p.group;
+    };
+    auto read_scales = [&] {
       int a = at, q = pos_in;
 #pragma unroll
       for (int i = 0; i < kRuns; ++i) {
-        const bool ok = real && kt < ke && kt * BK + i * kRun < p.K;
+        const bool ok = real && more && (kb + kt) * BK + i * kRun < p.K;
         const long long to = (long long)a * p.N;
         sc[i] = ok ? scales[to] : (uint16_t)0;
         zr[i] = ok && zeros != nullptr ? zeros[to] : (unsigned char)8;
@@ -258,98 +339,137 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       from[i] = row * 128 + ((((group & 1) * 4 + i) ^ (row & 7)) << 4);
-    const uint32_t to = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + L::kACol;
-    read_scales(kb + group);
-    uint32_t it = (uint32_t)group;
+    const uint32_t lanes = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = true;
-    for (int kt = kb + group; kt < ke; kt += kGroups, it += kGroups) {
-      const uint32_t r = (it / 2) % R, s = it % S;
-      const uint32_t raw_parity = (it / 2 / R) & 1u, parity = ((it / S) & 1u) ^ 1u;
-      // (Both tries are on their way at once.)
-      const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), raw_parity);
-      const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), parity);
-      uint32_t sv[kRuns], zv[kRuns];
-#pragma unroll
-      for (int i = 0; i < kRuns; ++i) {
-        sv[i] = sc[i] * 0x00010001u;
-        zv[i] = zero_term<T>(zr[i] & 15u);
-      }
-      at += far_at;
-      if ((pos_in += far_pos) >= p.group) pos_in -= p.group, ++at;
-      read_scales(kt + kGroups);
-      ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), raw_parity, p.fault, p.timeout_ns,
-                           &bars->abort, kFaultTcProducerWait, loaded);
-      if (!ok) break;
-      const uint32_t raw = smem_u32(raw_base) + r * kRawBytes;
-      uint4 q[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = ld_shared_v4(raw + from[i]);
-      ok = role_wait_lanes(smem_u32(&bars->empty[s]), parity, p.fault, p.timeout_ns,
-                           &bars->abort, kFaultTcProducerWait, freed);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a[32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 x = q[2 * h + i];
-          const int run = (2 * h + i) * 32 / kRun;
-          const uint32_t sr = sv[run], zz = zv[run];
-          weights8<T>(x.x, zz, sr, a + 16 * i);
-          weights8<T>(x.y, zz, sr, a + 16 * i + 4);
-          weights8<T>(x.z, zz, sr, a + 16 * i + 8);
-          weights8<T>(x.w, zz, sr, a + 16 * i + 12);
-        }
-        // Past K, where X is zeros, the codes may stand for infinities.
-        const int left = p.K - kt * BK - h * 64;
-        if (left < 64) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (2 * j + 1 >= left) a[j] = 2 * j < left ? a[j] & 0xFFFFu : 0u;
-        }
-        tmem_st32(to + s * kACols + h * 32, a);
-      }
-      // (The proxy fence waits for the loads, before TMA refills the slot.)
-      fence_proxy_async_smem();
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&bars->full[s]));
-        mbar_arrive(smem_u32(&bars->raw_empty[r]));
-      }
-    }
     // ------------------------------------------------ draining
-    if (warp < kConvWarp + 4) {
-      ok = ok && role_wait_lanes(smem_u32(&bars->acc_full), 0u, p.fault, p.timeout_ns,
-                                 &bars->abort, kFaultTcEpilogueWait);
+    // Of the n-th unit, each group some rows.
+    auto drain = [&](uint32_t n) {
+      if (group * 16 >= MT) return;
+      const uint32_t b = n & 1;
+      const int4 unit = kLoop ? entered[(warp - kConvWarp) * kEntered + n % kEntered]
+                              : make_int4(unit0.lo, unit0.hi, unit0.n0, 0);
+      const int m_end = unit.y - unit.x;
+      ok = role_wait_lanes(smem_u32(&bars->acc_full[b]), (n >> 1) & 1u, p.fault, p.timeout_ns,
+                           &bars->abort, kFaultTcEpilogueWait);
+      if (!ok) return;
       tc_fence_after();
-      const int col = (warp & 3) * 32 + lane;
-      const uint32_t lanes = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
-      const int m_end = rows.hi - rows.lo;
 #pragma unroll 1
-      for (int c = 0; c < MT / 16 && c * 16 < m_end; ++c) {
+      for (int c = group; c < MT / 16 && c * 16 < m_end; c += kGroups) {
         uint32_t r[16];
-        tmem_ld16(lanes + c * 16, r);
-        if (p.split > 1) {
+        tmem_ld16(lanes + b * L::kAccCols + c * 16, r);
+        if constexpr (!kLoop) {
           // The partial tile, row-major, where the ring was.
-          float* const part = reinterpret_cast<float*>(base) + c * 16 * BN + col;
+          float* const part = reinterpret_cast<float*>(base) + c * 16 * BN + row;
 #pragma unroll
           for (int j = 0; j < 16; ++j) part[j * BN] = __uint_as_float(r[j]);
-        } else if (n0 + col < p.N) {
-          T* const y = static_cast<T*>(p.Y) + (long long)(rows.lo + c * 16) * p.ldy + n0 + col;
+        } else if (unit.z + row < p.N) {
+          T* const y = static_cast<T*>(p.Y) + (long long)(unit.x + c * 16) * p.ldy + unit.z + row;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (c * 16 + j < m_end)
-              y[j * p.ldy] = from_f32_any<T>(__uint_as_float(r[j]) * kQ4Unit<T>);
+              y[j * p.ldy] = from_f32_any<T>(__uint_as_float(r[j]) * kQ4Value<T>);
         }
       }
+      if constexpr (kLoop) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty[b]));
+      }
+    };
+    uint32_t drained = 0;
+    enter(unit0);
+    read_scales();
+    for (uint32_t it = (uint32_t)group;; it += kGroups) {
+      const bool now = more;
+      uint32_t over = n;        // units before this stage's
+      if (now) {
+        const uint32_t r = (it / 2) % R, s = it % S;
+        const uint32_t raw_parity = (it / 2 / R) & 1u, parity = ((it / S) & 1u) ^ 1u;
+        // (Both tries are on their way at once.)
+        const bool loaded = mbar_try_wait(smem_u32(&bars->raw_full[r]), raw_parity);
+        const bool freed = mbar_try_wait(smem_u32(&bars->empty[s]), parity);
+        uint32_t sv[kRuns], zv[kRuns];
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+          sv[i] = sc[i] * 0x00010001u;
+          zv[i] = zero_term<T>(zr[i] & 15u);
+        }
+        const int terms = p.K - (kb + kt) * BK;     // from this stage on
+        kt += kGroups;
+        at += far_at;
+        if ((pos_in += far_pos) >= p.group) pos_in -= p.group, ++at;
+        if constexpr (kLoop) {
+          if (kt >= stages) {
+            kt -= stages, ++n;
+            walk.next();
+            enter(q4_unit_by_warp(p, tables, walk, BN, expert));
+          }
+        } else {
+          more = kt < stages;
+          n = more ? 0u : 1u;
+        }
+        read_scales();
+        ok = role_wait_lanes(smem_u32(&bars->raw_full[r]), raw_parity, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait, loaded);
+        if (!ok) break;
+        const uint32_t raw = smem_u32(raw_base) + r * kRawBytes;
+        uint4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = ld_shared_v4(raw + from[i]);
+        if constexpr (__is_same(T, __half)) {
+          // Past K, where X is zeros, codes less their zeros may overflow: there they
+          // become their zeros.  (In BF16 they are below 1 before the scale.)
+          if (terms < BK) {
+            uint32_t* const words = reinterpret_cast<uint32_t*>(q);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t none = (zv[i * 8 / kRun] & 15u) * 0x11111111u;
+              const int left = terms - 8 * i;
+              const uint32_t mask = left >= 8 ? 0xFFFFFFFFu : (left > 0 ? (1u << 4 * left) - 1 : 0u);
+              words[i] = (words[i] & mask) | (none & ~mask);
+            }
+          }
+        }
+        ok = role_wait_lanes(smem_u32(&bars->empty[s]), parity, p.fault, p.timeout_ns,
+                             &bars->abort, kFaultTcProducerWait, freed);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 x = q[2 * h + i];
+            const int run = (2 * h + i) * 32 / kRun;
+            const uint32_t sr = sv[run], zz = zv[run];
+            weights8<T>(x.x, zz, sr, a + 16 * i);
+            weights8<T>(x.y, zz, sr, a + 16 * i + 4);
+            weights8<T>(x.z, zz, sr, a + 16 * i + 8);
+            weights8<T>(x.w, zz, sr, a + 16 * i + 12);
+          }
+          tmem_st32(lanes + L::kACol + s * kACols + h * 32, a);
+        }
+        // (The proxy fence waits for the loads, before TMA refills the slot.)
+        fence_proxy_async_smem();
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->full[s]));
+          mbar_arrive(smem_u32(&bars->raw_empty[r]));
+        }
+      }
+      // Units that are over are drained once the next one has a stage of this group: its
+      // MMAs then do not wait for it.
+      while (ok && drained < over) drain(drained++);
+      if (!ok || !now) break;
     }
   }
-  if (p.split > 1) {
+  if constexpr (!kLoop) {
     // ------------------------------------------------ sum of the cluster's partial tiles
     cluster_sync_all();
+    const Q4Unit rows = unit0;
+    const int n0 = rows.n0;
     // This CTA adds up BN / split of the columns, four of a row per thread, all partial
     // tiles' values on their way at once.
     constexpr int kMaxSplit = 8;
@@ -374,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       T* const y = static_cast<T*>(p.Y) + (long long)(rows.lo + m) * p.ldy + n0 + col;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (n0 + col + j < p.N) y[j] = from_f32_any<T>(sum[j] * kQ4Unit<T>);
+        if (n0 + col + j < p.N) y[j] = from_f32_any<T>(sum[j] * kQ4Value<T>);
     }
     cluster_sync_all();   // no CTA leaves while others read its partial tile
   }
@@ -407,17 +527,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, int MT, int kRun>
-cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
-                        cudaStream_t stream) {
-  auto kernel = q4_rows_kernel<T, MT, kRun>;
+template <typename T, int MT, int kRun, bool kLoop>
+cudaError_t launch_kernel(const Q4FewParams& p, const CUtensorMap* tmQ, const CUtensorMap* tmX,
+                          cudaStream_t stream) {
+  using L = Layout<MT, kLoop>;
+  auto kernel = q4_rows_kernel<T, MT, kRun, kLoop>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = mx_allow_smem(kernel, Layout<MT>::kSmem, &done);
+  cudaError_t e = mx_allow_smem(kernel, L::kSmem, &done);
   if (e != cudaSuccess) return e;
-  const long long tiles = ((long long)p.N + BN - 1) / BN;
+  const long long tiles = ((long long)p.N + BN - 1) / BN, units = tiles * p.slots;
+  if (kLoop)
+    return launch_gemm_kernel(kernel, dim3((unsigned)(units < p.max_ctas ? units : p.max_ctas)),
+                              dim3(kThreads), L::kSmem, stream, *tmQ, *tmX, p);
   return launch_gemm_kernel_clusters((unsigned)p.split, kernel,
                                      dim3((unsigned)(tiles * p.split), (unsigned)p.slots),
-                                     dim3(kThreads), Layout<MT>::kSmem, stream, *tmQ, *tmX, p);
+                                     dim3(kThreads), L::kSmem, stream, *tmQ, *tmX, p);
+}
+
+template <typename T, int MT, int kRun>
+cudaError_t launch_rows(const Q4FewParams& p, const CUtensorMap* q, const CUtensorMap* x,
+                        cudaStream_t stream) {
+  return p.split > 1 ? launch_kernel<T, MT, kRun, false>(p, q, x, stream)
+                     : launch_kernel<T, MT, kRun, true>(p, q, x, stream);
 }
 
 template <typename T, int kRun>
