@@ -38,21 +38,25 @@ struct Q4Call {
 // FP16 and groups of 64: 8 rows 4096 x 4096 6.2 / 6.7 and 7.5 / 7.8, 8192 x 8192 12.8 /
 // 15.1 and 15.0 / 16.4; 16 rows 1024 x 1024 3.6 / 3.9 and 4.4 / 4.7, 4096 x 4096 7.2 / 8.4
 // and 7.8 / 8.1, but 8192 x 8192 15.5 / 19.4 and 15.2 / 16.7, 14336 x 4096 14.5 / 17.8
-// and 13.8 / 15.1; 24 rows 4096 x 4096 8.1 / 8.7 and 8.1 / 8.4.  Of experts, whose groups
-// are uneven: 16 rows to 32 experts, 2048 x 2048, 15.9 and 20.6, 64 25.0 and 26.2, but 64 to
-// 8 14.3 and 11.0.
-constexpr int kFewRows = 8, kFewRowsSmall = 16, kFewRowsExperts = 4;
+// and 13.8 / 15.1; 24 rows 4096 x 4096 8.1 / 8.7 and 8.1 / 8.4.  Of experts (2048 x 2048,
+// groups of 128): 8 rows each of 8 8.6 / 10.3, of 32 23.6 / 26.1, of 64 39.6 / 42.7, 5 of 8
+// 8.5 / 10.2; but 16 each of 32 36.2 / 26.8.
+constexpr int kFewRows = 8, kFewRowsSmall = 16;
 constexpr long long kFewSmall = 1ll << 24;         // weights
 bool few_rows(const Q4Call& c, int expect) {
-  if (c.experts != 0) return expect <= kFewRowsExperts;
-  return expect <= ((long long)c.N * c.K <= kFewSmall ? kFewRowsSmall : kFewRows);
+  return expect <= (c.experts == 0 && (long long)c.N * c.K <= kFewSmall ? kFewRowsSmall
+                                                                        : kFewRows);
 }
-// Rows: tcgen05, each 128 rows' CTAs converting the weights for themselves.  Against the
-// product with the weights in 16 bits, us: 512 rows 4096 x 4096 19.1 and 34.1, 8192 x 8192
-// 57 and 96; 768 36.5 and 34.6, 85 and 128; 14336 x 4096 93 and 104; but 1024 37.3 and
-// 35.1, 113 and 129, 14336 x 4096 113 and 103.  8 experts of 2048 x 2048: 256 rows each 37
-// and 46, 512 58 and 56.
-constexpr int kCodeRows = 768;
+// Rows: tcgen05, each 128 rows' units converting the weights for themselves.  Against the
+// product with the weights in 16 bits, us, groups of 128 (of 32): 1024 rows 4096 x 4096
+// 29.7 / 37.3 (32.3 / 37.5), 8192 x 8192 94 / 136, 2048 rows 52.3 / 56.2 (58.7 / 56.5) and
+// 162 / 213 (185 / 216), 4096 rows 90.4 / 95.4 (102 / 95.5) and 319 / 347 (361 / 350), 14336 x
+// 4096 305 / 289; but 8192 rows 4096 x 4096 176 / 162.  8 experts: 1024 rows each 2048 x 2048
+// 59 / 74, 2048 each 108 / 105 and 4096 x 4096 344 / 392; but 4096 each 207 / 181 and 680 /
+// 668.
+bool code_rows(const Q4Call& c, int expect) {
+  return expect <= (c.experts == 0 && c.group % 128 == 0 ? 4096 : 2048);
+}
 
 // The product by one of the kernels that read the codes.  (Not done: terms beyond what a
 // sum in tensor memory, which truncates at each step, should have; see segment().  BF16
@@ -189,6 +193,6 @@ extern "C" gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, i
   Operand none{nullptr, 0, 0, 0, 1, 0, false};
   if ((st = align_operands(c.x, none, workspaces, stream)) != GEMM_OK) return st;
   const int expect = experts == 0 ? rows : ceil_div(rows, experts);
-  if (expect <= kCodeRows && run_codes(c, expect, stream, &st)) return st;
+  if (code_rows(c, expect) && run_codes(c, expect, stream, &st)) return st;
   return run_values(c, workspaces, stream);
 }

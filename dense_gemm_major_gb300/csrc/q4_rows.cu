@@ -376,12 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty[b]));
       }
     };
-    uint32_t drained = 0;
+    uint32_t drained = 0, last = 0;      // (last: unit of the last turn's stage)
     enter(unit0);
     read_scales();
     for (uint32_t it = (uint32_t)group;; it += kGroups) {
       const bool now = more;
-      uint32_t over = n;        // units before this stage's
+      const uint32_t turn = n;  // this stage's unit
       if (now) {
         const uint32_t r = (it / 2) % R, s = it % S;
         const uint32_t raw_parity = (it / 2 / R) & 1u, parity = ((it / S) & 1u) ^ 1u;
@@ -459,8 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_u32(&bars->raw_empty[r]));
         }
       }
-      // Units that are over are drained once the next one has a stage of this group: its
-      // MMAs then do not wait for it.
+      // A unit is drained a turn after the next one's first, when its MMAs are done; but all
+      // units before the last one are, whose accumulator the MMAs ahead may wait for: the
+      // stage that this group's next turn waits for is of this turn's unit or before.
+      const uint32_t over = !now ? n : max(last, turn == 0 ? 0u : turn - 1);
+      last = turn;
       while (ok && drained < over) drain(drained++);
       if (!ok || !now) break;
     }

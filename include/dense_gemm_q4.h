@@ -46,7 +46,7 @@ extern "C" {
  * multiple of 8, or X is packed (ldx == K) at any alignment of its type, which takes
  * a copy with aligned rows in a workspace first; else GEMM_ERR_MISALIGNED.  Y has any
  * alignment of its type.  FP32 accumulation; one rounding.  (Up to 8 rows, 16 of a
- * small matrix, or 4 for each expert: the integers code - zero, exact in 16 bits, are
+ * small matrix, or 8 for each expert: the integers code - zero, exact in 16 bits, are
  * multiplied and each group's FP32 sum scaled.  More: the weights are rounded to dtype
  * first.)  K == 0: zeros.
  */

@@ -114,7 +114,8 @@ def test_long_rows(dg, dtype, group, rows):
 
 EXPERTS = [([1], 64, 64, 32), ([0, 1, 0, 2], 130, 520, 64), ([0, 0], 64, 64, 32),
            ([3, 0, 9, 1, 40], 65, 777, 32), ([1] * 33, 64, 300, 128), ([70, 0, 1, 200], 100, 512, 64),
-           ([300, 0, 500, 7], 129, 777, 96), ([0, 1500], 64, 96, 32)]
+           ([300, 0, 500, 7], 129, 777, 96), ([0, 1500], 64, 96, 32),
+           ([5000, 0, 2500, 700], 100, 333, 64)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -170,7 +171,18 @@ def test_more_tiles_of_experts_than_run_at_once(dg, dtype, group, K, experts, N)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("rows", [1, 7, 12, 40, 64, 200])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("rows,N,K,group", [(2050, 130, 257, 32), (4100, 65, 300, 128)])
+def test_many_rows(dg, dtype, zeros, rows, N, K, group):
+    gen = torch.Generator("cuda").manual_seed(rows + N + K)
+    x = _x(gen, rows, K, dtype)
+    w, values = _weights(dg, gen, (N,), K, dtype, group, zeros, pad=16)
+    _check(dg.q4_linear(x, w), x, values, K, dtype)
+    check_device(dg)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [1, 7, 12, 40, 64, 200, 2100])
 def test_exact_on_integers(dg, dtype, rows):
     """Integer activations and power-of-two scales: FP32 holds every sum exactly, so
     the result is the exact one, rounded once."""
@@ -186,7 +198,7 @@ def test_exact_on_integers(dg, dtype, rows):
     check_device(dg)
 
 
-@pytest.mark.parametrize("rows", [2, 40, 200])
+@pytest.mark.parametrize("rows", [2, 40, 200, 2100])
 def test_special_values_stay_in_their_row_and_column(dg, rows):
     """An infinity or a NaN in a row of x, and a NaN scale of a row of W."""
     gen = torch.Generator("cuda").manual_seed(4)
@@ -227,7 +239,7 @@ def test_scales_whose_codes_past_the_end_would_overflow(dg, dtype, rows, K):
     check_device(dg)
 
 
-@pytest.mark.parametrize("rows", [1, 5, 70, 300])
+@pytest.mark.parametrize("rows", [1, 5, 70, 300, 2100])
 def test_contiguous_x_of_any_width(dg, rows):
     gen = torch.Generator("cuda").manual_seed(5)
     x = torch.randn((rows, 333), generator=gen, device="cuda").half()
@@ -270,14 +282,15 @@ def test_weights_without_rows(dg):
     check_device(dg)
 
 
-@pytest.mark.parametrize("rows", [10, 700])
+@pytest.mark.parametrize("rows", [10, 700, 7000])
 @pytest.mark.parametrize("raw,meant", [([0, 5, 3, 9], [0, 5, 5, 9]), ([-4, 2, 6, 9], [0, 2, 6, 9]),
                                        ([0, 5000, 6, 9], [0, -1, -1, -1])])
 def test_bad_offsets_stay_inside_and_are_reported(dg, rows, raw, meant):
     gen = torch.Generator("cuda").manual_seed(9)
     x = _x(gen, rows, 64, "bf16")
     w, _ = _weights(dg, gen, (3, 64), 64, "bf16", 32, True)
-    meant = [rows if v < 0 else v for v in meant]
+    # (5000 becomes the number of rows, or stays where there are more: then it is in range.)
+    meant = [min(rows, 5000) if v < 0 else v for v in meant]
     outs = []
     for offsets in (raw, meant):
         y = torch.full((rows, 64), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -292,11 +305,11 @@ def test_bad_offsets_stay_inside_and_are_reported(dg, rows, raw, meant):
 def test_graph_replay_with_other_groups(dg):
     gen = torch.Generator("cuda").manual_seed(12)
     cases = []
-    for rows, experts in ((30, 6), (900, 3)):
+    for rows, experts in ((30, 6), (900, 3), (6400, 3)):
         w, _ = _weights(dg, gen, (experts, 200), 544, "bf16", 32, True)
         cases.append((_x(gen, rows, 544, "bf16"), w, _offsets([rows // experts] * experts)))
     dense = [(_x(gen, rows, 544, "bf16"), _weights(dg, gen, (200,), 544, "bf16", 32, True)[0], None)
-             for rows in (3, 300)]
+             for rows in (3, 300, 2100)]
 
     def step():
         return [dg.q4_linear(x, w, offsets=o) for x, w, o in cases + dense]
@@ -322,7 +335,7 @@ def test_graph_replay_with_other_groups(dg):
 
 def test_stream_argument_and_the_allocator(dg):
     gen = torch.Generator("cuda").manual_seed(13)
-    xs = [_x(gen, rows, 1024, "bf16") for rows in (4, 400)]
+    xs = [_x(gen, rows, 1024, "bf16") for rows in (4, 400, 4100)]
     w, _ = _weights(dg, gen, (4096,), 1024, "bf16", 128, True)
     want = [dg.q4_linear(x, w) for x in xs]
     side = torch.cuda.Stream()
@@ -350,7 +363,7 @@ def test_two_streams_at_once(dg):
     e, _ = _weights(dg, gen, (4, 512), 1024, "bf16", 32, True)
     m = dg.mx_quantize(torch.randn((1024, 4096), generator=gen, device="cuda").bfloat16())
     g = torch.randn((4, 1024, 512), generator=gen, device="cuda").bfloat16()
-    xs = [_x(gen, rows, 4096, "bf16") for rows in (5, 16, 33, 100, 900)]
+    xs = [_x(gen, rows, 4096, "bf16") for rows in (5, 16, 33, 100, 900, 4100)]
     r = _x(gen, 70, 1024, "bf16")
     packed = torch.randn((33, 4095), generator=gen, device="cuda").bfloat16()
     wp, _ = _weights(dg, gen, (200,), 4095, "bf16", 128, True)
