@@ -408,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
       if (n < p.N)
         Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Value<T>);
     }
-    cluster_sync_all();   // nobody leaves while its sums may still be read
+    // Nobody leaves while its sums may still be read.
+    cluster_arrive_relaxed();
+    cluster_wait();
   }
 }
 

@@ -499,7 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j)
         if (n0 + col + j < p.N) y[j] = from_f32_any<T>(sum[j] * kQ4Value<T>);
     }
-    cluster_sync_all();   // no CTA leaves while others read its partial tile
+    // Nobody leaves while its sums may still be read.
+    cluster_arrive_relaxed();
+    cluster_wait();
   }
 
   // ------------------------------------------------ teardown
