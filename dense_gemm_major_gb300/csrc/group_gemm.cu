@@ -262,6 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_pair_multicast(smem_u32(&bars->acc_full[b]), both);
         }
       }
+      // The other CTA's last arrivals have come before this one may leave.
+      for (uint32_t i = seg > 2 ? seg - 2 : 0; ok && i < seg; ++i)
+        ok = role_wait(smem_u32(&bars->acc_empty[i & 1]), (i >> 1) & 1u, p.fault, p.timeout_ns,
+                       &bars->abort, kFaultTcMmaWait, true);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -354,7 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // no CTA leaves while others may still touch its memory
+  // No CTA leaves, nor is TMEM freed, while others may still touch its memory.
+  if (bars->abort)
+    cluster_arrive_release();
+  else
+    cluster_arrive_relaxed();
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
