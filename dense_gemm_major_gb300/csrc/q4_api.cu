@@ -48,15 +48,12 @@ bool few_rows(const Q4Call& c, int expect) {
                                                                         : kFewRows);
 }
 // Rows: tcgen05, each 128 rows' units converting the weights for themselves.  Against the
-// product with the weights in 16 bits, us, groups of 128 (of 32): 1024 rows 4096 x 4096
-// 29.7 / 37.3 (32.3 / 37.5), 8192 x 8192 94 / 136, 2048 rows 52.3 / 56.2 (58.7 / 56.5) and
-// 162 / 213 (185 / 216), 4096 rows 90.4 / 95.4 (102 / 95.5) and 319 / 347 (361 / 350), 14336 x
-// 4096 305 / 289; but 8192 rows 4096 x 4096 176 / 162.  8 experts: 1024 rows each 2048 x 2048
-// 59 / 74, 2048 each 108 / 105 and 4096 x 4096 344 / 392; but 4096 each 207 / 181 and 680 /
-// 668.
-bool code_rows(const Q4Call& c, int expect) {
-  return expect <= (c.experts == 0 && c.group % 128 == 0 ? 4096 : 2048);
-}
+// product with the weights in 16 bits, us, one after the other under the power limit, groups
+// of 128: 1024 rows 4096 x 4096 29.7 / 37.1, 2048 55.7 / 57.6 (of 32: 61.3 / 57.9) and 8192 x
+// 8192 189 / 220, 8 experts of 1024 rows each, 2048 x 2048, 61 / 75, of 2048, 4096 x 4096, 399 /
+// 418; but 4096 rows 4096 x 4096 102.2 / 100.7, 8192 x 8192 372 / 381; singly 8192 rows 4096 x
+// 4096 176 / 162, 8 experts of 4096, 2048 x 2048, 207 / 181.
+constexpr int kCodeRows = 2048;
 
 // The product by one of the kernels that read the codes.  (Not done: terms beyond what a
 // sum in tensor memory, which truncates at each step, should have; see segment().  BF16
@@ -193,6 +190,6 @@ extern "C" gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, i
   Operand none{nullptr, 0, 0, 0, 1, 0, false};
   if ((st = align_operands(c.x, none, workspaces, stream)) != GEMM_OK) return st;
   const int expect = experts == 0 ? rows : ceil_div(rows, experts);
-  if (code_rows(c, expect) && run_codes(c, expect, stream, &st)) return st;
+  if (expect <= kCodeRows && run_codes(c, expect, stream, &st)) return st;
   return run_values(c, workspaces, stream);
 }

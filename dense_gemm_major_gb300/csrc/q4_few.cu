@@ -14,10 +14,13 @@
 // values are permuted the same way.  The four ranges of K and then the CTAs of the
 // cluster are added in their order.
 //
-// Measured in a graph on changing weights, BF16, groups of 128: 1 x 4096 x 4096 5.5 us, 1 x
-// 8192 x 8192 11.8 (2.9 TB/s of codes and scales; of 64: 12.8, of 32: 14.8).  Without the
-// products the latter takes 9; they are bound by their instructions, of which the integer
-// pipe, at half rate, takes a third.
+// Units of experts: a CTA goes from one to the next, whose first loads are under way at the
+// end of each (a CTA for each unit: 64 rows of 64 experts, 2048 x 2048, 49.2 -> 37.6 us).
+//
+// Measured in a graph on changing weights, BF16, groups of 128: 1 x 4096 x 4096 5.2 us, 1 x
+// 8192 x 8192 11.5 (3.0 TB/s of codes and scales; of 64: 12.4, of 32: 14.3), 32768 x 8192 35
+// (4.0 TB/s).  Without the products 1 x 8192 x 8192 takes 9; they are bound by their
+// instructions, of which the integer pipe, at half rate, takes a third.
 #include "q4.cuh"
 
 namespace dgemm {

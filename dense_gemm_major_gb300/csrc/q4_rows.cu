@@ -1,4 +1,4 @@
-// Products of up to 128 rows with 4-bit weights and group scales on tcgen05:
+// Products with 4-bit weights and group scales on tcgen05, of tiles of up to 128 rows:
 // Y = X . W^T, the weights rounded to X's type on the way.
 //
 // Bound by reading the codes and by the instructions that make 16-bit values of them
@@ -7,21 +7,26 @@
 // its N side (16 to 128).  The values go to tensor memory, from where the MMA reads its
 // A: through shared memory they would be written and read at four times the codes'
 // bytes, which is what bounded a first version (8192 x 8192, 16 rows: 19.8 us).  A
-// thread has a row of W, as a lane of tensor memory has.  So that W's bytes travel to all
-// SMs at once, the CTAs of a cluster share a tile's K; they add their FP32 partial
-// tiles through distributed shared memory in rank order, so results are reproducible and
-// there is no workspace.
+// thread has a row of W, as a lane of tensor memory has.
 //
-// Measured in a graph on changing weights, BF16, groups of 128: 40 x 8192 x 8192 14.9 us
-// (2.3 TB/s of codes and scales), 33 x 4096 x 4096 8.1, 128 x 4096 x 4096 10.8.  Without
-// the conversions the former takes 12, without MMAs and loads too 10: the turns of the
-// converting warps, some 5 us before and after them, and 24 of the 152 SMs, which the powers
-// of two leave idle.
+// Few units: so that W's bytes travel to all SMs at once, the CTAs of a cluster share a
+// tile's K; they add their FP32 partial tiles through distributed shared memory in rank order,
+// so results are reproducible and there is no workspace.  Many (kLoop): a CTA goes from unit
+// to unit, with two accumulators in turn, so that loads and conversions do not stop between
+// them (a unit for each CTA of a larger grid: 512 rows of 64 experts, 2048 x 2048, 66.9 -> 42.6
+// us, 2048 of 32 49.8 -> 31.2, 512 x 8192 x 8192 57.1 -> 48.7).
+//
+// Measured in a graph on changing weights, BF16, groups of 128: 40 x 8192 x 8192 14.2 us
+// (2.5 TB/s of codes and scales), 33 x 4096 x 4096 7.5, 128 x 4096 x 4096 9.8; 1024 x 4096 x
+// 4096 29.1, 2048 x 8192 x 8192 166 (1.66 PFLOP/s).  What bounds 40 rows: the turns of the
+// converting warps, some 4 us before and after them (without the conversions 12 us), and 24 of
+// the 152 SMs, which the powers of two leave idle.  768 x 8192 x 8192: 72.9, without the
+// conversions 63, with one MMA of eight 62.
 //
 // Roles (640 threads): warp 0 loads the codes (TMA) into a ring of their own, warp 1
 // issues the MMAs, warp 2 loads X, warps 4-19 convert: four groups of 4 warps take turns
-// at 128-deep stages, so that one's waits pass while the others convert.  Warps 4-7
-// then drain the accumulator.
+// at 128-deep stages, so that one's waits pass while the others convert.  Each group drains
+// some rows of the accumulators.
 #include "q4.cuh"
 
 namespace dgemm {
