@@ -11,8 +11,8 @@
 
 namespace dgemm {
 
-// Few rows: a CTA computes 64 columns of Y (rows of W) for 8 or 16 rows of one expert,
-// over its share of K.
+// Few rows: a CTA computes 64 columns of Y (rows of W) for 8 or 16 rows of one expert, over
+// its share of K or one after the other.
 constexpr int kQ4TileN = 64;
 constexpr int kQ4BK = 512;
 struct Q4FewParams {
@@ -22,7 +22,7 @@ struct Q4FewParams {
   int tile_rows;            // rows of Y per CTA
   int slots;                // upper bound of tiles of rows
   int split;                // CTAs (a cluster) that share a tile's K
-  int max_ctas;             // few rows: as many as run at once
+  int max_ctas;             // as many as run at once
   const void* scales;
   const unsigned char* zeros;
   void* Y;
@@ -35,7 +35,8 @@ struct Q4FewParams {
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream);
 
-// More rows: 128 columns of Y for up to 128 rows of one expert, over a share of K.
+// More rows: 128 columns of Y for up to 128 rows of one expert, over a share of K or one after
+// the other.
 constexpr int kQ4RowsTileN = 128;
 constexpr int kQ4RowsBK = 128;
 inline int q4_rows_tile(int rows) {

@@ -58,7 +58,7 @@ struct Layout {
   static_assert(S >= kGroups && R % 2 == 0, "phases");
   static constexpr uint32_t kTable =
       kLoop ? (sizeof(Q4Tables) + 15) / 16 * 16 + kGroups * kGroupWarps * kEntered * 16 : 0;
-  // All of an SM's (s_rows is beside it), so that no CTA of another cluster with tensor
+  // All of an SM's (s_unit is beside it), so that no CTA of another cluster with tensor
   // memory is: two clusters could each hold on one SM what the other waits for on another.
   static constexpr uint32_t kSmem = 232448 - 1024;
   static_assert(S * kStage + R * kRawBytes + kTable + 512 + 1024 <= kSmem, "shared memory");
@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;;) {
         if constexpr (kLoop) {
           if (lane == 0 && unit.real)
-            entered[(warp - kConvWarp) * kEntered + n % kEntered] = make_int4(unit.lo, unit.hi, unit.n0, 0);
+            entered[(warp - kConvWarp) * kEntered + n % kEntered] =
+                make_int4(unit.lo, unit.hi, unit.n0, 0);
         }
         expert = unit.expert;
         more = unit.real;
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) {
               const uint32_t none = (zv[i * 8 / kRun] & 15u) * 0x11111111u;
               const int left = terms - 8 * i;
-              const uint32_t mask = left >= 8 ? 0xFFFFFFFFu : (left > 0 ? (1u << 4 * left) - 1 : 0u);
+              const uint32_t mask =
+                  left >= 8 ? 0xFFFFFFFFu : (left > 0 ? (1u << 4 * left) - 1 : 0u);
               words[i] = (words[i] & mask) | (none & ~mask);
             }
           }

@@ -171,6 +171,52 @@ def test_more_tiles_of_experts_than_run_at_once(dg, dtype, group, K, experts, N)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,N,K,group", [
+    (12, 70000, 256, 64), (16, 40001, 424, 32), (30, 40000, 200, 128), (25, 50000, 700, 32),
+    (60, 40000, 130, 32), (40, 30000, 1100, 128), (100, 33000, 40, 32), (2000, 4100, 100, 32),
+    (1000, 8200, 256, 128), (300, 16400, 520, 64), (1500, 3000, 1290, 128)])
+def test_more_tiles_than_run_at_once(dg, dtype, rows, N, K, group):
+    """Several units for each CTA, from two k-tiles each on: the same bits every time."""
+    gen = torch.Generator("cuda").manual_seed(rows + N + K)
+    x = _x(gen, rows, K, dtype)
+    w, values = _weights(dg, gen, (N,), K, dtype, group, True)
+    y = dg.q4_linear(x, w)
+    for _ in range(3):
+        assert torch.equal(dg.q4_linear(x, w), y)
+    check_device(dg)
+    for at in (slice(0, 300), slice(N // 2, N // 2 + 300), slice(N - 300, N)):
+        _check(y[:, at], x, values[at], K, dtype)
+    want = x.double() @ values.t()
+    # (Each weight and each result is off by half a unit at most.)
+    assert float((y.double() - want).norm() / want.norm()) <= 2 * ref.UNIT[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group,K", [(32, 96), (64, 300), (128, 1000)])
+def test_more_tiles_of_experts_than_run_at_once_on_tcgen05(dg, dtype, group, K):
+    """Experts of 0 to 60 rows, several units for each CTA, and rows of none around them."""
+    gen = torch.Generator("cuda").manual_seed(K)
+    sizes = torch.randint(0, 61, (70,), generator=gen, device="cuda").tolist()
+    sizes[3] = 0
+    sizes[69] = 0
+    x = _x(gen, sum(sizes) + 11, K, dtype)
+    w, values = _weights(dg, gen, (70, 1300), K, dtype, group, True)
+    y = torch.full((sum(sizes) + 11, 1300), 7.0, dtype=TYPES[dtype], device="cuda")
+    off = _offsets(sizes, 4)
+    for i in range(3):
+        got = dg.q4_linear(x, w, offsets=off, out=y.clone())
+        assert i == 0 or torch.equal(got, last)
+        last = got
+    check_device(dg)
+    assert (got[:4] == 7.0).all() and (got[4 + sum(sizes):] == 7.0).all()
+    lo = 4
+    for g, n in enumerate(sizes):
+        if n and g % 6 == 0:
+            _check(got[lo:lo + n], x[lo:lo + n], values[g], K, dtype)
+        lo += n
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("rows,N,K,group", [(2050, 130, 257, 32), (4100, 65, 300, 128)])
 def test_many_rows(dg, dtype, zeros, rows, N, K, group):
