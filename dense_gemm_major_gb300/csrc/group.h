@@ -2,6 +2,8 @@
 // group_api.cu.  Callers use include/dense_gemm_group.h.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -47,10 +49,41 @@ inline long long group_units(int rows, int groups, int N, int tile_rows) {
 //   but        60 rows of 1, 1024 x 1024                    5.7 / 6.2
 //              2 rows of 2, 4096 x 1024                     7.6 / 8.0
 //              2 rows of 2, 1024 x 1024                     6.9 / 6.5
+// No more units than clusters that run at once.
 constexpr int kGroupMaxParts = 4;
+int group_clusters(int log_parts);    // that the current device holds
 inline int group_log_parts(long long units, long long K, int max_pairs) {
   if (K <= 8 * kGroupBK || 2 * units > max_pairs) return 0;
-  return 8 * units <= max_pairs ? 2 : 1;
+  if (8 * units <= max_pairs && units <= group_clusters(2)) return 2;
+  return units <= group_clusters(1) ? 1 : 0;
+}
+
+// Clusters of `size` CTAs that the current device holds at once (152 SMs, one CTA on each: 36
+// of 4, 15 of 8, since a cluster's CTAs share a GPC); asked once per device and kept in
+// `known`.  0: not known.
+template <typename... P>
+int clusters_at_once(void (*kernel)(P...), unsigned size, int threads, int smem,
+                     std::atomic<int> (&known)[64]) {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {size, 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 struct GroupParams {

@@ -396,6 +396,13 @@ cudaError_t launch_kind(const GroupParams& p, const CUtensorMap* a, const CUtens
 
 }  // namespace
 
+int group_clusters(int log_parts) {
+  static std::atomic<int> known[2][64];
+  // (Of one instance: all have the same threads, and nearly the same shared memory.)
+  return clusters_at_once(group_kernel<__half, float, kGroupForward, 64>, 2u << log_parts,
+                          kThreads, Layout<64>::kSmem, known[log_parts - 1]);
+}
+
 cudaError_t launch_group(int dtype, int dtype_c, const GroupParams& p, const CUtensorMap* tmM,
                          const CUtensorMap* tmN, const CUtensorMap* tmN16, int pairs,
                          cudaStream_t stream) {

@@ -449,6 +449,12 @@ cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUten
 
 }  // namespace
 
+int q4_few_clusters(int split) {
+  static std::atomic<int> known[3][64];
+  return clusters_at_once(q4_few_kernel<__half, 1, 4, false>, (unsigned)split, kThreads,
+                          Layout<1, false>::kSmem, known[split == 2 ? 0 : (split == 4 ? 1 : 2)]);
+}
+
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream) {
   return dtype == 1 ? launch_typed<__half>(p, tmQ, tmX, stream)

@@ -585,6 +585,12 @@ cudaError_t launch_run(const Q4FewParams& p, const CUtensorMap* q, const CUtenso
 
 }  // namespace
 
+int q4_rows_clusters(int split) {
+  static std::atomic<int> known[3][64];
+  return clusters_at_once(q4_rows_kernel<__half, 64, 128, false>, (unsigned)split, kThreads,
+                          Layout<64, false>::kSmem, known[split == 2 ? 0 : (split == 4 ? 1 : 2)]);
+}
+
 cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                            const CUtensorMap* tmX, cudaStream_t stream) {
   return dtype == 1 ? launch_run<__half>(p, tmQ, tmX, stream)
