@@ -35,7 +35,7 @@ struct Q4FewParams {
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,
                           const CUtensorMap* tmX, cudaStream_t stream);
 
-// Clusters of `split` (2, 4, 8) CTAs that the current device holds at once.
+// Clusters of `split` (up to 8) CTAs that the current device holds at once.
 int q4_few_clusters(int split);
 int q4_rows_clusters(int split);
 

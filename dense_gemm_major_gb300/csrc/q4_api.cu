@@ -39,8 +39,9 @@ struct Q4Call {
 // 4096 5.6 / 5.7 / 6.5 and 6.9 / 7.3 / 7.4, 8192 x 8192 11.9 / 12.6 / 14.8 and 13.6 / 14.9 / 15.3,
 // 14336 x 4096 10.8 / 11.6 / 13.8 and 13.8 / 16.2 / 16.1; 16 rows 1024 x 1024 3.4 / 3.6 / 3.8 and
 // 4.0 / 4.2 / 4.4, 2048 x 8192 6.7 and 8.5, 4096 x 4096 6.9 / 7.4 / 8.2 and 7.1 / 7.4 / 7.5; but
-// 8192 x 8192 14.9 / 16.8 / 19.2 and 13.6 / 14.9 / 15.4.  Of experts (2048 x 2048, groups of 128): 8 rows each of 8 8.6 /
-// 10.3, of 32 23.6 / 26.1, of 64 39.6 / 42.7, 5 of 8 8.5 / 10.2; but 16 each of 32 36.2 / 26.8.
+// 8192 x 8192 14.9 / 16.8 / 19.2 and 13.6 / 14.9 / 15.4.  Of experts (2048 x 2048, groups of
+// 128): 8 rows each of 8 8.6 / 10.3, of 32 23.6 / 26.1, of 64 39.6 / 42.7, 5 of 8 8.5 / 10.2;
+// but 16 each of 32 36.2 / 26.8.
 constexpr int kFewRows = 8, kFewRowsSmall = 16;
 constexpr long long kFewSmall = 1ll << 24;         // weights
 bool few_rows(const Q4Call& c, int expect) {
@@ -69,19 +70,21 @@ bool run_codes(const Q4Call& c, int expect, cudaStream_t stream, gemm_status_t* 
     p.tile_rows = dgemm::q4_rows_tile(c.experts == 0 ? expect : 2 * expect);
   p.slots = c.experts == 0 ? ceil_div(c.rows, p.tile_rows)
                            : c.rows / p.tile_rows + (c.experts < c.rows ? c.experts : c.rows);
-  // CTAs that share a tile's K: as many (a cluster of at most 8) as keep one wave,
-  // each with a slot of codes at least.  (Of 16 clusters of 8 on 152 SMs one has to wait:
-  // 33 x 2048 x 4096 11.4 us, in clusters of 4 6.9.)
+  // CTAs that share a tile's K: as many (a cluster of at most 8) as keep one wave, each with a
+  // slot of codes at least, and no more than shorten the longest share.  (Of 16 clusters of 8
+  // on 152 SMs one has to wait: 33 x 2048 x 4096 11.4 us, in clusters of 4 6.9.  Not only powers
+  // of two: 2 x 5120 x 13824 16.8 -> 12.7 us, 40 rows 19.7 -> 15.6, 2 x 2560 x 2560 4.2 -> 3.7.)
   const int tile_n = few ? dgemm::kQ4TileN : dgemm::kQ4RowsTileN;
   const long long tiles = (long long)ceil_div(c.N, tile_n) * p.slots;
   const int nk = ceil_div(c.K, few ? dgemm::kQ4BK : 2 * dgemm::kQ4RowsBK);
   const int room = 2 * c.pairs * (few ? 2 : 1);
   p.max_ctas = room;
-  p.split = 1;
-  while (p.split < 8 && 2 * p.split <= nk && 2 * p.split * tiles <= room &&
-         tiles <= (few ? dgemm::q4_few_clusters(2 * p.split) : dgemm::q4_rows_clusters(2 * p.split)))
-    p.split *= 2;
-  if (!few && (c.K - 1) / p.split >= segment(c.dtype) * dgemm::kGroupBK * (c.dtype == 2 ? 8 : 1))
+  for (p.split = nk < 8 ? nk : 8; p.split > 1; --p.split) {
+    if (p.split * tiles > room || ceil_div(nk, p.split) == ceil_div(nk, p.split - 1)) continue;
+    if (tiles <= (few ? dgemm::q4_few_clusters(p.split) : dgemm::q4_rows_clusters(p.split))) break;
+  }
+  const long long terms = ceil_div(nk, p.split) * 2ll * dgemm::kQ4RowsBK;
+  if (!few && terms > (long long)segment(c.dtype) * dgemm::kGroupBK * (c.dtype == 2 ? 8 : 1))
     return false;
   p.scales = c.scales, p.zeros = c.zeros;
   p.Y = c.Y, p.ldy = c.ldy;

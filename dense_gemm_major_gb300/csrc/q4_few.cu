@@ -450,9 +450,9 @@ cudaError_t launch_typed(const Q4FewParams& p, const CUtensorMap* q, const CUten
 }  // namespace
 
 int q4_few_clusters(int split) {
-  static std::atomic<int> known[3][64];
+  static std::atomic<int> known[9][64];
   return clusters_at_once(q4_few_kernel<__half, 1, 4, false>, (unsigned)split, kThreads,
-                          Layout<1, false>::kSmem, known[split == 2 ? 0 : (split == 4 ? 1 : 2)]);
+                          Layout<1, false>::kSmem, known[split]);
 }
 
 cudaError_t launch_q4_few(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,

@@ -20,7 +20,7 @@
 // (2.5 TB/s of codes and scales), 33 x 4096 x 4096 7.5, 128 x 4096 x 4096 9.8; 1024 x 4096 x
 // 4096 29.1, 2048 x 8192 x 8192 166 (1.66 PFLOP/s).  What bounds 40 rows: the turns of the
 // converting warps, some 4 us before and after them (without the conversions 12 us), and 24 of
-// the 152 SMs, which the powers of two leave idle.  768 x 8192 x 8192: 72.9, without the
+// the 152 SMs, which 64 tiles leave idle.  768 x 8192 x 8192: 72.9, without the
 // conversions 63, with one MMA of eight 62.
 //
 // Roles (640 threads): warp 0 loads the codes (TMA) into a ring of their own, warp 1
@@ -480,13 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     const Q4Unit rows = unit0;
     const int n0 = rows.n0;
-    // This CTA adds up BN / split of the columns, four of a row per thread, all partial
-    // tiles' values on their way at once.
+    // This CTA adds up its part of the columns, four of a row per thread, all partial tiles'
+    // values on their way at once.
     constexpr int kMaxSplit = 8;
-    const int share = BN / p.split / 4;
+    const int share = (BN / 4 + p.split - 1) / p.split;
     for (int i = threadIdx.x; i < share * (rows.hi - rows.lo); i += kThreads) {
       const int m = i / share;
       const int col = (rank * share + (i - m * share)) * 4;
+      if (col >= BN) continue;
       const uint32_t from = smem_u32(base) + (uint32_t)(m * BN + col) * 4u;
       float4 v[kMaxSplit];
 #pragma unroll
@@ -586,9 +587,9 @@ cudaError_t launch_run(const Q4FewParams& p, const CUtensorMap* q, const CUtenso
 }  // namespace
 
 int q4_rows_clusters(int split) {
-  static std::atomic<int> known[3][64];
+  static std::atomic<int> known[9][64];
   return clusters_at_once(q4_rows_kernel<__half, 64, 128, false>, (unsigned)split, kThreads,
-                          Layout<64, false>::kSmem, known[split == 2 ? 0 : (split == 4 ? 1 : 2)]);
+                          Layout<64, false>::kSmem, known[split]);
 }
 
 cudaError_t launch_q4_rows(int dtype, const Q4FewParams& p, const CUtensorMap* tmQ,

@@ -112,6 +112,22 @@ def test_long_rows(dg, dtype, group, rows):
     check_device(dg)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,N,K", [
+    (5, 6400, 1600), (3, 3800, 2600), (7, 2700, 3600), (8, 200, 4096), (1, 2400, 3100),
+    (16, 5000, 2000), (11, 3300, 2300), (40, 5120, 2100), (20, 3200, 1541), (100, 2500, 1800),
+    (65, 2000, 1900), (33, 2048, 4096), (17, 200, 8000)])
+def test_shares_of_long_rows(dg, dtype, rows, N, K):
+    """Rows of W shared by clusters of every number of CTAs that occurs."""
+    gen = torch.Generator("cuda").manual_seed(rows + N + K)
+    x = _x(gen, rows, K, dtype)
+    w, values = _weights(dg, gen, (N,), K, dtype, 64, True)
+    y = dg.q4_linear(x, w)
+    check_device(dg)
+    _check(y, x, values, K, dtype)
+    assert torch.equal(dg.q4_linear(x, w), y)
+
+
 EXPERTS = [([1], 64, 64, 32), ([0, 1, 0, 2], 130, 520, 64), ([0, 0], 64, 64, 32),
            ([3, 0, 9, 1, 40], 65, 777, 32), ([1] * 33, 64, 300, 128), ([70, 0, 1, 200], 100, 512, 64),
            ([300, 0, 500, 7], 129, 777, 96), ([0, 1500], 64, 96, 32),
