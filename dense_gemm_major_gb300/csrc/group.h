@@ -39,13 +39,17 @@ inline long long group_units(int rows, int groups, int N, int tile_rows) {
 //   products   8 rows of 1 group, N x K of 1024 x 8192      21.0 / 13.7 / 9.7
 //              60 rows of 1, 1024 x 4096                    12.9 / 10.3 / 8.5
 //              2 rows of 2, 1024 x 4096                     13.1 / 9.8 / 8.1
-//              1 row of 1, 4096 x 4096                      13.5 / 10.6 / 16.7 (clusters of
-//                                        eight CTAs, which do not all fit at once)
+//              8 rows of 1, 2560 x 4096                     two 9.6, four 8.2
+//              8 rows of 1, 3840 x 4096                     two 10.6, four 9.9
+//              500 rows of 1, 1280 x 4096                   two 18.0, four 14.2
+//              1 row of 1, 4096 x 4096                      13.5 / 10.6 / 16.7 (a cluster of
+//                                        eight CTAs more than run at once)
 //              64 rows of 1, 2048 x 2048                    8.9 / 8.4
 //              512 rows of 1, 1024 x 8192                   41.5 / 26.9
 //   gradients  8192 rows of 1, 256 x 256                    43.7 / 27.7 / 18.5
 //              8192 rows of 1, 1024 x 1024                  42.2 / 27.6
 //              8192 rows of 4, 512 x 512                    16.7 / 14.8
+//              8192 rows of 1, 1024 x 768                   two 27.9, four 19.7
 //   but        60 rows of 1, 1024 x 1024                    5.7 / 6.2
 //              2 rows of 2, 4096 x 1024                     7.6 / 8.0
 //              2 rows of 2, 1024 x 1024                     6.9 / 6.5
@@ -54,7 +58,7 @@ constexpr int kGroupMaxParts = 4;
 int group_clusters(int log_parts);    // that the current device holds
 inline int group_log_parts(long long units, long long K, int max_pairs) {
   if (K <= 8 * kGroupBK || 2 * units > max_pairs) return 0;
-  if (8 * units <= max_pairs && units <= group_clusters(2)) return 2;
+  if (4 * units <= max_pairs && units <= group_clusters(2)) return 2;
   return units <= group_clusters(1) ? 1 : 0;
 }
 

@@ -205,6 +205,26 @@ def test_pairs_that_share_a_gradient(dg, dtype, out, case):
         lo += n
 
 
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("rows,N,K", [(8, 2500, 1100), (64, 3800, 2100), (300, 1200, 1040),
+                                      (8, 9216, 1100), (8, 9700, 1100)])
+def test_units_up_to_as_many_as_clusters_run_at_once(dg, op, rows, N, K):
+    """10 to 15 units, for clusters of eight CTAs, and around 37, for clusters of four."""
+    gen = torch.Generator("cuda").manual_seed(N)
+    a = _padded((rows, K), "bf16", gen)
+    b = _padded((1, K, N) if op == "N" else (1, N, K), "bf16", gen)
+    bm = b if op == "N" else b.transpose(1, 2)
+    c = dg.grouped_matmul(a, bm, _offsets([rows]), dtype=torch.float32)
+    check_device(dg)
+    x, w = a.double(), bm[0].double()
+    _check(c, x @ w, x.abs() @ w.abs(), K, "f32")
+    assert torch.equal(dg.grouped_matmul(a, bm, _offsets([rows]), dtype=torch.float32), c)
+    d = dg.grouped_grad(_padded((1500, 700), "bf16", gen), _padded((1500, N // 3), "bf16", gen),
+                        _offsets([1500]))
+    check_device(dg)
+    assert d.isfinite().all()
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_scaled_and_accumulated(dg, out):
     gen = torch.Generator("cuda").manual_seed(3)
