@@ -15,6 +15,10 @@ namespace dgemm {
 // its share of K or one after the other.
 constexpr int kQ4TileN = 64;
 constexpr int kQ4BK = 512;
+// Groups of columns of a row (K > 0).  (Not from K + group - 1, which for a large group is
+// past what an int holds.)
+__host__ __device__ inline int q4_groups(int K, int group) { return (K - 1) / group + 1; }
+
 struct Q4FewParams {
   int rows, N, K, group;
   int experts;              // 0: one matrix for all rows

@@ -107,7 +107,7 @@ bool run_codes(const Q4Call& c, int expect, cudaStream_t stream, gemm_status_t* 
 // some experts, or some columns of Y.
 gemm_status_t run_values(const Q4Call& c, dgemm::StreamWorkspaces& workspaces,
                          cudaStream_t stream) {
-  const long long ldd = ((long long)c.K + 7) / 8 * 8, groups = ceil_div(c.K, c.group);
+  const long long ldd = ((long long)c.K + 7) / 8 * 8, groups = dgemm::q4_groups(c.K, c.group);
   long long fit = GEMM_Q4_WORKSPACE / (ldd * 2);       // rows of W
   if (fit < 1) fit = 1;
   const bool whole = fit >= c.N;                        // matrices at a time, or parts of one
@@ -178,7 +178,7 @@ extern "C" gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, i
     if (codes == nullptr || scales == nullptr || ldq < (K + 1ll) / 2) return GEMM_ERR_INVALID_ARG;
     if (!aligned(codes, 16) || ldq % 16 != 0 || !aligned(scales, 2)) return GEMM_ERR_MISALIGNED;
     if ((st = c.x.check()) != GEMM_OK) return st;
-    const long long all = (long long)c.matrices() * N, g = ceil_div(K, group);
+    const long long all = (long long)c.matrices() * N, g = dgemm::q4_groups(K, group);
     if (overlap(Y, ys, X, c.x.bytes()) ||
         overlap(Y, ys, codes, span(all, (K + 1ll) / 2, ldq)) ||
         overlap(Y, ys, scales, (uint64_t)(all * g * 2)) ||

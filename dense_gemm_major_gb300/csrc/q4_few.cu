@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
     // ------------------------------------------------ products
     const int wn = warp / kWarpsK, wk = warp % kWarpsK;
     const int g = lane >> 2, t = lane & 3;
-    const int groups = (p.K + p.group - 1) / p.group;
+    const int groups = q4_groups(p.K, p.group);
     constexpr int kSteps = kSliceK / 32, kRuns = kSteps / kRun;
     // This lane's row of W, whose scales and zeros it reads for the warp: a group's
     // are stored together (with a row's stored together each lane read a line of its

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) return;
       const long long first_of_row =
-          (long long)expert * ((p.K + p.group - 1) / p.group) * p.N + unit.n0 + row;
+          (long long)expert * q4_groups(p.K, p.group) * p.N + unit.n0 + row;
       scales = static_cast<const uint16_t*>(p.scales) + first_of_row;
       zeros = p.zeros != nullptr ? p.zeros + first_of_row : nullptr;
       real = unit.n0 + row < p.N;

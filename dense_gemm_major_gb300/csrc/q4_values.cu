@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(256)
                      const unsigned char* zeros, const int* offsets, T* D, long long ldd) {
   wait_prior_grids();
   allow_dependent_grids();
-  const int chunks = (K + 31) / 32, groups = (K + group - 1) / group;
+  const int chunks = (K + 31) / 32, groups = q4_groups(K, group);
   const int e = (int)(blockIdx.x / tiles_n);
   if (offsets != nullptr && offsets[e + 1] <= offsets[e]) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

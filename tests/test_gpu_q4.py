@@ -161,6 +161,25 @@ def test_experts(dg, dtype, zeros, case):
         lo += n
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("K", [64, 256, 4096])
+@pytest.mark.parametrize("sizes", [[2, 0, 3, 1], [30, 0, 9, 61], [3000, 0, 2500, 2900]],
+                         ids=lambda s: str(sum(s)))
+def test_experts_with_the_largest_group(dg, zeros, K, sizes):
+    """A scale for each row, by a group that K is far below: K + group - 1 is past what an
+    int holds.  Rows for each of the kernels."""
+    gen = torch.Generator("cuda").manual_seed(sum(sizes) + K)
+    x = _x(gen, sum(sizes), K, "bf16")
+    w, values = _weights(dg, gen, (len(sizes), 70), K, "bf16", 2 ** 31 - 32, zeros)
+    y = dg.q4_linear(x, w, offsets=_offsets(sizes))
+    check_device(dg)
+    lo = 0
+    for g, n in enumerate(sizes):
+        if n:
+            _check(y[lo:lo + n], x[lo:lo + n], values[g], K, "bf16", sum(sizes) > 8)
+        lo += n
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("group,K", [(32, 1600), (64, 130), (128, 2000)])
 @pytest.mark.parametrize("experts,N", [(64, 1100), (1024, 200)])

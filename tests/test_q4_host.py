@@ -45,6 +45,14 @@ def test_refusals(kw, status):
     assert _call(**kw) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(Y=S + 48 * 2 - 2), dict(Y=Z + 46), dict(K=64, ldx=64, Y=S + 48 * 2 - 2),
+    dict(experts=3, off=OFF, Y=S + 3 * 48 * 2 - 2), dict(experts=3, off=OFF, Y=Z + 3 * 48 - 2)])
+def test_overlaps_with_scales_of_the_largest_group(kw):
+    """K + group - 1 is past 2^31 - 1: there is still one group to a row."""
+    assert _call(group=2 ** 31 - 32, **kw) == INVALID
+
+
 def test_empty_calls_need_no_device():
     assert _call(rows=0, X=0, Y=0) == dg.GEMM_OK
     assert _call(N=0, q=0, s=0, Y=0) == dg.GEMM_OK
