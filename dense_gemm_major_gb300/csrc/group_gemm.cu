@@ -310,9 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     if (cluster < units) {
       const GroupUnit w = group_unit<kKind, kRows>(cluster, p, tables);
-      // Four columns of a row per thread, all parts' values on their way at once.
+      // Four columns of a row per thread, all parts' values on their way at once.  (Only those
+      // that are stored are read: see cluster_arrive_relaxed().)
       const int pieces = (w.row_end - w.row) * 32;
       for (int i = part * kThreads + (int)threadIdx.x; i < pieces; i += parts * kThreads) {
+        const int col = w.col + (int)rank * 128 + (i & 31) * 4;
+        if (col >= p.N) continue;
         const uint32_t at = smem_u32(base) + (uint32_t)i * 16u;
         float4 v[kGroupMaxParts];
 #pragma unroll
@@ -323,7 +326,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 1; j < kGroupMaxParts; ++j)
           sum[0] += v[j].x, sum[1] += v[j].y, sum[2] += v[j].z, sum[3] += v[j].w;
-        const int col = w.col + (int)rank * 128 + (i & 31) * 4;
         TC* const c = static_cast<TC*>(p.C) + (kWeights ? w.g * p.stride_c : 0) +
                       (long long)(w.row + (i >> 5)) * p.ldc + col;
 #pragma unroll

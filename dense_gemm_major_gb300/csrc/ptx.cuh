@@ -162,8 +162,9 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 // The two halves.  A relaxed arrival orders nothing and so does not wait for stores to
-// memory that are under way, which takes up to a microsecond: enough where what a thread read
-// of the others' shared memory has come.
+// memory that are under way, which takes up to a microsecond: enough where each value that a
+// thread read of the others' shared memory went into a store before, which cannot be issued
+// until the value has come.  (A read that nothing uses may still be under way: there is none.)
 __device__ __forceinline__ void cluster_arrive_release() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }

@@ -399,17 +399,18 @@ __global__ void __launch_bounds__(kThreads, Layout<kTiles, kExperts>::kCtas)
   }
   if constexpr (!kExperts) add_ranges(unit0.lo, unit0.hi, unit0.n0);
   if (p.split > 1) {
-    // This CTA's part of the tile over the cluster.
+    // This CTA's part of the tile over the cluster.  (Only what is stored is read: see
+    // cluster_arrive_relaxed().)
     cluster_sync_all();
     const Q4Unit unit = unit0;
     const int values = (unit.hi - unit.lo) * kQ4TileN;
     for (int i = rank * kThreads + threadIdx.x; i < values; i += p.split * kThreads) {
+      const int n = unit.n0 + i % kQ4TileN;
+      if (n >= p.N) continue;
       const uint32_t at = smem_u32(sums + i);
       float v = 0.f;
       for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(mapa_shared(at, (uint32_t)r));
-      const int n = unit.n0 + i % kQ4TileN;
-      if (n < p.N)
-        Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Value<T>);
+      Y[(long long)(unit.lo + i / kQ4TileN) * p.ldy + n] = from_f32_any<T>(v * kQ4Value<T>);
     }
     // Nobody leaves while its sums may still be read.
     cluster_arrive_relaxed();

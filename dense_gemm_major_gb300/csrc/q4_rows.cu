@@ -481,13 +481,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Q4Unit rows = unit0;
     const int n0 = rows.n0;
     // This CTA adds up its part of the columns, four of a row per thread, all partial tiles'
-    // values on their way at once.
+    // values on their way at once.  (Only those that are stored are read: see
+    // cluster_arrive_relaxed().)
     constexpr int kMaxSplit = 8;
     const int share = (BN / 4 + p.split - 1) / p.split;
     for (int i = threadIdx.x; i < share * (rows.hi - rows.lo); i += kThreads) {
       const int m = i / share;
       const int col = (rank * share + (i - m * share)) * 4;
-      if (col >= BN) continue;
+      if (col >= BN || n0 + col >= p.N) continue;
       const uint32_t from = smem_u32(base) + (uint32_t)(m * BN + col) * 4u;
       float4 v[kMaxSplit];
 #pragma unroll

@@ -591,3 +591,28 @@ def test_refusals_of_the_wrappers(dg):
             f()
         assert e.value.status == status
     check_device(dg)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["N", "T"])
+@pytest.mark.parametrize("N", [1, 3, 127, 130, 257, 259, 390])
+@pytest.mark.parametrize("rows,K", [(3, 1100), (200, 2050)])
+def test_last_columns_of_shared_units(dg, out, op, rows, K, N):
+    """Units of few columns whose K pairs of a cluster share, most of which nobody stores or
+    reads, one call close behind another: each has the same bits, within the bound.  The
+    gradient has the sum over K rows."""
+    gen = torch.Generator("cuda").manual_seed(rows + N)
+    a = _padded((rows, K), "bf16", gen)
+    b = _padded((1, K, N) if op == "N" else (1, N, K), "bf16", gen)
+    bm = b if op == "N" else b.transpose(1, 2)
+    cs = [dg.grouped_matmul(a, bm, _offsets([rows]), dtype=TYPES[out]) for _ in range(20)]
+    check_device(dg)
+    x, w = a.double(), bm[0].double()
+    _check(cs[0], x @ w, x.abs() @ w.abs(), K, out)
+    assert all(torch.equal(c, cs[0]) for c in cs)
+    p, q = _padded((K, rows), "bf16", gen), _padded((K, N), "bf16", gen)
+    cs = [dg.grouped_grad(p, q, _offsets([K]), dtype=TYPES[out]) for _ in range(20)]
+    check_device(dg)
+    x, w = p.double(), q.double()
+    _check(cs[0][0], x.t() @ w, x.abs().t() @ w.abs(), K, out)
+    assert all(torch.equal(c, cs[0]) for c in cs)

@@ -567,3 +567,18 @@ def test_long_sums_of_like_terms_keep_their_size(dg, dtype, rows):
     want = torch.stack([x.double() @ (((w.codes[n, k // 2].int() >> (4 * (k % 2)).int()) & 15)
                                       .double() * 2.0 ** -10) for n in range(N)], dim=1)
     assert abs(float(((got - want) / want).mean())) <= {"f16": 2.0 ** -13, "bf16": 2.0 ** -10}[dtype]
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("N", [1, 3, 66, 129, 131, 257])
+@pytest.mark.parametrize("rows,K", [(5, 1100), (16, 4096), (40, 800), (100, 4100)])
+def test_last_columns_of_shared_tiles(dg, zeros, rows, K, N):
+    """Tiles of few columns whose K a cluster shares, most of which nobody stores or reads,
+    one call close behind another: each has the same bits, within the bound."""
+    gen = torch.Generator("cuda").manual_seed(rows + N)
+    x = _x(gen, rows, K, "bf16")
+    w, values = _weights(dg, gen, (N,), K, "bf16", 64, zeros)
+    ys = [dg.q4_linear(x, w) for _ in range(20)]
+    check_device(dg)
+    _check(ys[0], x, values, K, "bf16", rows > 8)
+    assert all(torch.equal(y, ys[0]) for y in ys)
