@@ -33,8 +33,16 @@ StreamEntry* entry_of(int dev, cudaStream_t stream) {
   return &(*entries)[Key(dev, stream, stream == cudaStreamPerThread ? thread : 0)];
 }
 
+// Size of the workspace that replaces one of `old` bytes.  (See StreamWorkspaces::get().)
+size_t grown(WorkspaceUse use, size_t old, size_t bytes) {
+  if (use != kWsValues) return bytes > 2 * old ? bytes : 2 * old;
+  size_t size = 256;
+  while (size < bytes) size *= 2;
+  return size;
+}
+
 gemm_status_t grow(Workspace& w, WorkspaceUse use, size_t bytes, cudaStream_t stream) {
-  size_t size = bytes > 2 * w.bytes ? bytes : 2 * w.bytes;
+  size_t size = grown(use, w.bytes, bytes);
   void* p = nullptr;
   if (cudaMalloc(&p, size) != cudaSuccess) {
     cudaGetLastError();

@@ -41,7 +41,10 @@ class StreamWorkspaces {
   // too small is replaced by one at least twice its size, and its memory
   // stays allocated until the process exits: work that is queued, and graphs
   // that were captured on this stream, hold its address.  (Doubling bounds
-  // what is left behind by the size in use.)
+  // what is left behind by the size in use.)  kWsValues has a stated bound, which
+  // doubling would pass (200 MB, then 400 for a call that needs 250): its sizes are
+  // powers of two, as the bound is, and what is left behind is less than the size in
+  // use as well.
   gemm_status_t get(WorkspaceUse use, size_t bytes, void** out) noexcept;
 
   // The next epoch of the flags, never 0; after get(kWsFlags).

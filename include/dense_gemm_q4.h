@@ -21,11 +21,12 @@
  * Inputs must not overlap outputs.  Sizes are at most GEMM_GROUP_MAX_SIZE.
  *
  * Device memory: calls with many rows take a workspace for the weights in 16 bits,
- * at most GEMM_Q4_WORKSPACE bytes (more only where one expert's single row of codes
- * needs more): one per (device, stream), under the rules of dense_gemm.h (replaced
- * by a larger one when a call needs more, never freed, shared by the graphs captured
- * on the stream, whose replays must not overlap).  Before a stream capture, make one
- * call of the same sizes on that stream.
+ * a power of two of bytes, at most GEMM_Q4_WORKSPACE (more only where a single row of an
+ * expert's weights needs more): one per (device, stream), under the rules of dense_gemm.h
+ * (replaced by a larger one when a call needs more, never freed, shared by the graphs
+ * captured on the stream, whose replays must not overlap).  Those replaced take less
+ * than the last one together.  Before a stream capture, make one call of the same sizes
+ * on that stream.
  */
 #ifndef DENSE_GEMM_Q4_H_
 #define DENSE_GEMM_Q4_H_

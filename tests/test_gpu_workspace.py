@@ -67,6 +67,36 @@ def test_mx_graph_replays_after_a_larger_call(dg):
                         [lambda: None, lambda: (x.normal_(generator=gen), dy.normal_(generator=gen))])
 
 
+def test_q4_graph_replays_after_larger_calls(dg):
+    """A product whose 4-bit weights go through the workspace in 16 bits, captured; then
+    calls that need 150 and 250 MB of it, which a workspace of 256 serves."""
+    gen = torch.Generator("cuda").manual_seed(4)
+
+    def weights(N, K):
+        return dg.Q4Tensor(torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda",
+                                         dtype=torch.uint8),
+                           torch.full((N, K // 128), 0.01, device="cuda").bfloat16())
+    x = torch.randn((2500, 256), generator=gen, device="cuda").bfloat16()
+    w = weights(300, 256)
+    big = [weights(N, 4096) for N in (150 * 128, 250 * 128)]
+    wide = torch.randn((2100, 4096), generator=gen, device="cuda").bfloat16()
+    outs = [torch.empty((2100, q.rows), dtype=torch.bfloat16, device="cuda") for q in big]
+
+    def step():
+        return (dg.q4_linear(x, w),)
+    s = torch.cuda.Stream()
+    g, got = _capture(step, s)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    with torch.cuda.stream(s):
+        for q, out in zip(big, outs):
+            dg.q4_linear(wide, q, out=out)
+        s.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] < 320 << 20
+    _replays_like_eager(dg, g, got, step, [
+        lambda: x.copy_(torch.randn((2500, 256), generator=gen, device="cuda").bfloat16())] * 3)
+
+
 @pytest.mark.parametrize("shape,larger", [((256, 256, 256), (512, 512, 1024)),    # slices of K
                                           ((2048, 2048, 512), (2048, 4096, 512)),  # cut tiles
                                           ((1000, 1030, 777), (2000, 2062, 1555))])  # re-pitched

@@ -94,6 +94,28 @@ def test_growth_keeps_the_outgrown_memory(ws):
     assert ws.t_freed() == 0 and ws.t_allocations() <= 7
 
 
+VALUES = 4
+
+
+@pytest.mark.parametrize("needs", [(200, 250), (1, 200, 250, 256), (130, 131, 255), (256, 3),
+                                   tuple(range(1, 257)), (100, 300)])
+def test_the_weights_workspace_keeps_its_bound(ws, needs):
+    """MB that calls need one after the other: no workspace for 4-bit weights in 16 bits is
+    above 256 MB as long as no call needs more, and those that were outgrown are together
+    smaller than the one in use."""
+    for n in needs:
+        assert ws.t_get(16, VALUES, n << 20) is not None
+    sizes = [ws.t_size(i) for i in range(ws.t_allocations())]
+    assert max(needs) << 20 <= sizes[-1] <= (256 << 20 if max(needs) <= 256 else 512 << 20)
+    assert sum(sizes[:-1]) < sizes[-1] and ws.t_freed() == 0
+
+
+def test_little_memory_for_the_weights_workspace(ws):
+    """The power of two does not fit: what the call needs."""
+    ws.t_limit(200 << 20)
+    assert ws.t_get(16, VALUES, 190 << 20) is not None and ws.t_size(0) == 190 << 20
+
+
 def test_streams_and_uses_do_not_share(ws):
     got = {ws.t_get(s, use, 4096) for s in (0, 16, 32) for use in (PARTIALS, PACK, FLAGS, QUANTIZED)}
     assert len(got) == 12 and None not in got
