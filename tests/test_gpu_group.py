@@ -226,6 +226,20 @@ def test_units_up_to_as_many_as_clusters_run_at_once(dg, op, rows, N, K):
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [400, 833, 1266, 1300, 3000, 3233])
+def test_values_of_gradients_up_to_as_many_units_as_clusters_run_at_once(dg, out, N):
+    """6 to 15 units, which clusters of eight CTAs share, 18 to 36, of four, and 39, which none
+    do."""
+    gen = torch.Generator("cuda").manual_seed(N)
+    a, x = _padded((1500, 700), "bf16", gen), _padded((1500, N), "bf16", gen)
+    d = dg.grouped_grad(a, x, _offsets([1500]), dtype=TYPES[out])
+    check_device(dg)
+    p, q = a.double(), x.double()
+    _check(d[0], p.t() @ q, p.abs().t() @ q.abs(), 1500, out)
+    assert torch.equal(dg.grouped_grad(a, x, _offsets([1500]), dtype=TYPES[out]), d)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_scaled_and_accumulated(dg, out):
     gen = torch.Generator("cuda").manual_seed(3)
     sizes = [70, 0, 300, 1]
