@@ -642,7 +642,8 @@ def grouped_matmul(A, B, offsets, out=None, dtype=None, alpha=1.0, beta=0.0, str
     """out[i] = alpha * (A[i] @ B[g]) + beta * out[i] for the rows i of each
     group g.  A (rows x K) and B (groups x K x N) are float16 or bfloat16, A
     row-major, B's matrices row-major or transposed views, which are read in
-    place: with weights W stored groups x out x in, ``grouped_matmul(x,
+    place, one behind the other (or one for all groups: B.expand): with weights W
+    stored groups x out x in, ``grouped_matmul(x,
     W.transpose(1, 2), offsets)`` is a layer's forward product and
     ``grouped_matmul(dy, W, offsets)`` the gradient of its input.  The result is
     of the operands' dtype or float32 (``dtype``, or that of ``out``).  Rows of no
@@ -750,7 +751,10 @@ def q4_linear(x, W, offsets=None, out=None, stream=None):
     whose scales have x's dtype, which the result has too.  Weights of experts
     take ``offsets``, as grouped_matmul does: the rows of expert g are multiplied
     with its matrix, and rows of no expert are not written.  x has rows of a
-    multiple of 16 bytes, or is contiguous (copied to aligned rows first)."""
+    multiple of 16 bytes, or is contiguous (copied to aligned rows first).  For more
+    than 8 to 16 rows (8 for each expert) the weights are rounded to x's dtype first:
+    a row's result depends that much on how many rows there are, and float16 weights
+    beyond 65504 become infinite."""
     if stream is not None and out is None:
         return _on_stream(stream, lambda: q4_linear(x, W, offsets))
     return (_group or _load_group()).q4_linear(x, W, offsets, out, stream)

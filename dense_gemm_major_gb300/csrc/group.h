@@ -52,8 +52,8 @@ inline long long group_units(int rows, int groups, int N, int tile_rows) {
 //              8192 rows of 1, 1024 x 768                   two 27.9, four 19.7
 //   but        60 rows of 1, 1024 x 1024                    5.7 / 6.2
 //              2 rows of 2, 4096 x 1024                     7.6 / 8.0
-//              2 rows of 2, 1024 x 1024                     6.9 / 6.5
-// No more units than clusters that run at once.
+// No more units than clusters that run at once.  (K alone says when it is short, which is not
+// best everywhere: 2 rows of 2, 1024 x 1024, would gain by two, 6.9 / 6.5.)
 constexpr int kGroupMaxParts = 4;
 int group_clusters(int log_parts);    // that the current device holds
 inline int group_log_parts(long long units, long long K, int max_pairs) {

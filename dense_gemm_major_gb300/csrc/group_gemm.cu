@@ -18,11 +18,12 @@
 // Few units would leave most SMs idle: up to four pairs of a cluster then share a unit's K
 // and add their sums through distributed shared memory, in their order.
 //
-// Measured (8 experts of 4096 x 4096, 8192 rows, in a graph): forward 161 us (1.70
-// PFLOP/s); weights' gradient in FP32 206, in BF16 171.  What bounds them is what moves
+// Measured (8 experts of 4096 x 4096, 8192 rows, in a graph of twelve): forward 162 us (1.70
+// PFLOP/s; back to back for longer, under the power limit, 184); weights' gradient in FP32
+// 206, in BF16 171.  What bounds them is what moves
 // between L2 and the SMs, 128 KB for each k-tile of a unit and the results: forward without
 // loads 134 us, the gradients without stores 148 and 138, with one MMA of eight 180 and 142.
-// Small groups read each weight once: 64 rows of 32 experts, 2048 x 2048, 38 us (5.8 TB/s).
+// Small groups read each weight once: 64 rows of 32 experts, 2048 x 2048, 35 us (6.2 TB/s).
 //
 // FP32 sums.  The MMA truncates the running sum at every 16-deep step, so a unit
 // is summed in segments (GroupParams::seg), which the draining warps add in

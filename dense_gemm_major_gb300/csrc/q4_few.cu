@@ -19,8 +19,10 @@
 //
 // Measured in a graph on changing weights, BF16, groups of 128: 1 x 4096 x 4096 5.2 us, 1 x
 // 8192 x 8192 11.5 (3.0 TB/s of codes and scales; of 64: 12.4, of 32: 14.3), 32768 x 8192 35
-// (4.0 TB/s).  Without the products 1 x 8192 x 8192 takes 9; they are bound by their
-// instructions, of which the integer pipe, at half rate, takes a third.
+// (4.0 TB/s).  Without the products 1 x 8192 x 8192 takes 9.  No unit is near its limit there
+// (of the time: integer pipe 27 %, issue 31 %, DRAM 30 %).  What bounds it is latency: a warp
+// waits for a stage, reads, converts and multiplies one after the other, with 16 such warps on
+// an SM; and shares are uneven, 256 CTAs for 304 places leave 48 SMs with one.
 #include "q4.cuh"
 
 namespace dgemm {
@@ -93,7 +95,9 @@ struct Zero {
 
 // The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes, less their zero, over
 // kQ4Value.  FP16: a code in the low mantissa bits of 1024 is that plus the code, and four
-// bits further up 1024 + 16 q.  BF16 has no room for the latter; but the integer n in the
+// bits further up 1024 + 16 q (the known conversion of small integers by a magic number, for
+// 4-bit weights in Kim, Henry, Fahim and Hassan Awadalla, "Who Says Elephants Can't Run",
+// 2022).  BF16 has no room for the latter; but the integer n in the
 // low eight bits of a BF16 number is n 2^-133, whether it is subnormal (n < 128) or not, and
 // the multiplication with 2^127, or 2^123 for a code four bits further up, is exact.
 template <typename T>

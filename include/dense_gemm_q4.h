@@ -20,8 +20,9 @@
  * is queued, work is queued on `stream`, and every device-side wait is bounded.
  * Inputs must not overlap outputs.  Sizes are at most GEMM_GROUP_MAX_SIZE.
  *
- * Device memory: calls with many rows take a workspace for the weights in 16 bits,
- * a power of two of bytes, at most GEMM_Q4_WORKSPACE (more only where a single row of an
+ * Device memory: calls with more than 2048 rows (of an expert, were all alike), or with sums
+ * too long for the tensor cores (see below), take a workspace for the weights in 16 bits, a
+ * power of two of bytes, at most GEMM_Q4_WORKSPACE (more only where a single row of an
  * expert's weights needs more): one per (device, stream), under the rules of dense_gemm.h
  * (replaced by a larger one when a call needs more, never freed, shared by the graphs
  * captured on the stream, whose replays must not overlap).  Those replaced take less
@@ -46,10 +47,16 @@ extern "C" {
  * expert g, W its matrix, as gemm_grouped does.  X is 16-byte aligned and ldx a
  * multiple of 8, or X is packed (ldx == K) at any alignment of its type, which takes
  * a copy with aligned rows in a workspace first; else GEMM_ERR_MISALIGNED.  Y has any
- * alignment of its type.  FP32 accumulation; one rounding.  (Up to 8 rows, 16 of a
- * small matrix, or 8 for each expert: the integers code - zero, exact in 16 bits, are
- * multiplied and each group's FP32 sum scaled.  More: the weights are rounded to dtype
- * first.)  K == 0: zeros.
+ * alignment of its type.  FP32 accumulation; one rounding of the result.  K == 0: zeros.
+ *
+ * Up to 8 rows, 16 of a matrix of at most 2^24 weights, or 8 for each expert, the integers
+ * code - zero, exact in 16 bits, are multiplied and each group's FP32 sum is scaled.  For
+ * more rows the weights are rounded to dtype first: a row's result then differs by their
+ * rounding from what it is among few rows, and an FP16 weight that rounds beyond 65504 is an
+ * infinity, where among few rows only the result has to fit.  (There the tensor cores also
+ * truncate the running sum at each step of 16 terms.  It is cut into parts that are added in
+ * FP32, of at most 16384 terms; up to 2048 rows in BF16, which rounds eight times as coarsely
+ * as FP16, of 131072.)
  */
 gemm_status_t gemm_q4_linear(int dtype, int group, int rows, int N, int K, int experts,
                              const void *X, int ldx, const void *codes, int ldq,

@@ -582,3 +582,19 @@ def test_last_columns_of_shared_tiles(dg, zeros, rows, K, N):
     check_device(dg)
     _check(ys[0], x, values, K, "bf16", rows > 8)
     assert all(torch.equal(y, ys[0]) for y in ys)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("rows,N,K", [(1, 130, 300), (8, 8192, 2560), (16, 200, 1000)])
+def test_few_rows_take_weights_that_fp16_does_not_hold(dg, zeros, rows, N, K):
+    """Scales of 20000: integers are multiplied, and only the result has to fit FP16."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    w, values = _weights(dg, gen, (N,), K, "f16", 64, zeros)
+    values = values / w.scales.double().repeat_interleave(64, dim=1)[:, :K] * 20000
+    w.scales.fill_(20000.0)
+    x = _x(gen, rows, K, "f16")
+    x.mul_(2.0 ** -12)
+    y = dg.q4_linear(x, w)
+    check_device(dg)
+    assert values.abs().max() > 65504 and y.isfinite().all()
+    _check(y, x, values, K, "f16", False)
